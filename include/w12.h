@@ -347,6 +347,165 @@ int w12_q8_gemm_group(const uint16_t *x_dev, int count, const void *const *blobs
                       uint16_t *const *y_devs, int M, void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * ------------------------------------------------- paged key-value cache
+ * What lies between a layer's q/k/v products and its output product: page
+ * tables, the cache write, and the attention of the new tokens over the cached
+ * ones.  (No passage of the pages has a counterpart; the W12 products of a
+ * decoder layer need it to make a layer.)
+ *
+ * A cache holds the keys and the values of num_pages pages of page_size tokens
+ * and kv_heads heads of head_dim elements: element d of head h of the token in
+ * slot s lies at (s / page_size) * page_stride + h * head_stride +
+ * (s % page_size) * row_stride + d (strides in elements, the same for k_dev and
+ * v_dev; multiples of 16 bytes).  dtype:
+ *   W12_KV_BF16  BF16 elements, scales_dev NULL
+ *   W12_KV_Q8    int8 elements, symmetric per token and head as in the Q8
+ *                weight copy: s = max |x| / 127 in fp32, q = rint(x / s); a zero
+ *                row has s = 0.  scales_dev: fp32 [num_pages][kv_heads]
+ *                [page_size][2], contiguous, [0] of the key and [1] of the value.
+ *                A row with a NaN or an infinity gets that as its scale and
+ *                reads back as NaN.
+ * page_size: a multiple of 16.  head_dim: 64, 128 or 256.  k_dev, v_dev and
+ * scales_dev 16-byte aligned.
+ *
+ * A request's tokens lie in the pages its row of `tables` lists (int32 page
+ * numbers, token t in entry t / page_size); an entry outside 0..num_pages-1 is
+ * an absent page.  A slot is page * page_size + offset, or -1 for none.
+ * Lengths, tables, positions and slots are device memory: no call here reads
+ * them on the host, so a step's calls can be captured in a CUDA graph.
+ */
+#define W12_KV_BF16 0
+#define W12_KV_Q8 1
+
+typedef struct w12_kv_cache {
+    void *k_dev, *v_dev;
+    float *scales_dev;
+    int64_t num_pages;
+    int64_t page_stride, head_stride, row_stride;
+    int32_t page_size, kv_heads, head_dim, dtype;
+} w12_kv_cache;
+
+/*
+ * One step's pages, positions and slots.  Request b holds owned_in[b] pages
+ * (table entries 0..owned_in[b]-1) with lens[b] tokens in them and gets
+ * new_lens[b] more (clamped to what max_blocks pages hold; a negative value
+ * counts as 0).  need = ceil((lens + new_lens) / page_size) pages:
+ *   - the need - owned_in missing pages come from the ring of free pages, in
+ *     request order: ring[(head + a) % ring_size], a = 0, 1, ...
+ *   - with trim, the owned_in - need pages too many go back behind its tail, in
+ *     request and table order (their table entries stay as they are).
+ * ring_state_in = {head, tail}: ring[i % ring_size] is free for head <= i < tail.
+ * Pages given back in a step can be taken in the next one.
+ * Out: owned_out, ring_state_out (either may be its own input: in place),
+ * tables and ring (in place); cu_new[requests + 1], the prefix sum of new_lens;
+ * for token t = cu_new[b] + i of `tokens`: positions[t] = lens[b] + i and its
+ * slot.  Tokens behind the last one get position 0 and slot -1.
+ * Where the ring runs out, the pages that are missing are absent (-1) in the
+ * table, their tokens get slot -1 and w12_check_status returns
+ * BUFFER_TOO_SMALL; where the new tokens are more than `tokens`, the ones behind
+ * are left out, and where a length had to be clamped, SHAPE.
+ * All arrays 4-byte aligned (the 64-bit ones 8-byte).  tables: row b at
+ * tables + b * table_stride.  max_blocks * page_size < 2^31.
+ */
+typedef struct w12_kv_plan_args {
+    const int32_t *lens, *new_lens;
+    const int32_t *owned_in;
+    int32_t *owned_out;
+    int32_t *tables;
+    int64_t table_stride;
+    int32_t *ring;
+    const int64_t *ring_state_in;
+    int64_t *ring_state_out;
+    int32_t *cu_new;
+    int32_t *positions;
+    int64_t *slots;
+    int32_t requests, max_blocks, page_size, ring_size, tokens, trim;
+} w12_kv_plan_args;
+
+int w12_kv_plan(const w12_kv_plan_args *args, void *stream);
+
+/*
+ * Per token t and head: RMS norm of q and k over the head (x * rsqrt(mean(x^2) +
+ * eps) * weight; NULL weights: no norm), rotation of the first `rot` elements by
+ * row positions[t] of rope (fp32 [rope_rows][rot]: rot/2 cosines, then rot/2
+ * sines; rot 0: none) with partners rot/2 apart (interleaved 0) or next to each
+ * other (1), all in fp32; q_out = BF16_rne, k and v into the cache at slots[t]
+ * (-1: not stored).  q, k, v: BF16, token t at t * stride (elements), heads of
+ * head_dim one after the other, as the q/k/v products write them.  heads 0: no
+ * q.  q_out may be q.  Two tokens with one slot: either may stay.  rot: a
+ * multiple of 16 (interleaved: of 2), at most head_dim.  q, k, v, q_out, the
+ * weights and rope 16-byte aligned, strides multiples of 8.  A slot outside the
+ * cache is not stored and a position outside the table uses its nearest row;
+ * w12_check_status then returns INVALID_ARG.
+ */
+typedef struct w12_kv_store_args {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    const uint16_t *q_norm, *k_norm;
+    const float *rope;
+    const int32_t *positions;
+    const int64_t *slots;
+    int64_t rope_rows;
+    int32_t tokens, heads, rot, interleaved;
+    float eps;
+} w12_kv_store_args;
+
+int w12_kv_store(const w12_kv_cache *cache, const w12_kv_store_args *args, void *stream);
+
+/*
+ * Cached rows back as BF16: k_out and v_out [tokens][kv_heads][head_dim]
+ * contiguous, 16-byte aligned; row t from slots[t], zeros for -1.  A BF16 cache gives its
+ * bits back; a Q8 row is q * s in fp32, rounded once.  A slot outside the cache
+ * reads as zeros and w12_check_status returns INVALID_ARG.
+ */
+int w12_kv_read(const w12_kv_cache *cache, const int64_t *slots, int32_t tokens, uint16_t *k_out, uint16_t *v_out,
+                void *stream);
+
+/*
+ * Attention of the new tokens over their requests' cached tokens (their own
+ * among them: store first).  Tokens cu_new[b] .. cu_new[b+1]-1 of q belong to
+ * request b, which had lens[b] tokens before them; new token i has index
+ * lens[b] + i.  It sees key j of its request where j < lens[b] + new tokens,
+ * the page of j is present, and
+ *   - without tree: j <= lens[b] + i;
+ *   - with tree (uint32 per token): j < lens[b], or bit j - lens[b] of tree[t] is
+ *     set (new tokens from the 33rd on are then seen by none);
+ *   - with window > 0: also j > lens[b] + i - window.
+ * out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j over the keys seen, of
+ * key head h / (heads / kv_heads); lse[t][h] (NULL: not written) = ln sum_j
+ * exp(scale * q . k_j).  A token that sees nothing gets out 0 and lse
+ * -infinity; rows of q behind cu_new[requests] get nothing.  What unseen slots
+ * hold, NaN among it, has no effect.  fp32 scores,
+ * softmax statistics and sums; the softmax weights are rounded to BF16 for the
+ * tensor cores.  Results are reproducible run to run for the same lengths.
+ * q, out: BF16, token t at t * stride, stride a multiple of 8, 16-byte aligned.
+ * heads: a multiple of kv_heads.  max_new: the most new tokens a request has,
+ * as far as the caller knows; it picks the row tile and any value is correct.
+ * workspace: at least w12_kv_attend_workspace_size bytes, 256-byte aligned,
+ * ZERO-FILLED BEFORE ITS FIRST USE; every successful call leaves its counters
+ * zero again (after a TIMEOUT, zero it again).  Calls of any shape may share a
+ * workspace that is large enough for each, if they are ordered on the GPU.
+ */
+typedef struct w12_kv_attend_args {
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    int64_t q_stride, out_stride;
+    const int32_t *tables;
+    int64_t table_stride;
+    const int32_t *lens, *cu_new;
+    const uint32_t *tree;
+    int32_t requests, max_blocks, tokens, heads, max_new, window;
+    float scale;
+} w12_kv_attend_args;
+
+int w12_kv_attend_workspace_size(const w12_kv_cache *cache, const w12_kv_attend_args *args, size_t *bytes);
+
+int w12_kv_attend(const w12_kv_cache *cache, const w12_kv_attend_args *args, void *workspace, size_t ws_bytes,
+                  void *stream);
+
+/*
  * Measurement helper with no counterpart on the pages: reads `bytes` (a
  * multiple of 16) of device memory at buf_dev (16-byte aligned) once, with
  * 16-byte streaming loads spread over every SM, and writes the 4-byte word at
@@ -360,9 +519,9 @@ int w12_read_stream(const void *buf_dev, size_t bytes, void *sink_dev, uint32_t 
 
 /*
  * Synchronise `stream`, then read and clear the current device's status word,
- * which kernels set when a bounded wait gives up (TIMEOUT) or the device
- * encoder finds its output buffer too short (BUFFER_TOO_SMALL) or too many
- * escapes (SHAPE).  Returns that status, CUDA on a CUDA error, else OK.
+ * which kernels set when a bounded wait gives up (TIMEOUT), the device encoder
+ * finds its output buffer too short (BUFFER_TOO_SMALL) or too many escapes
+ * (SHAPE), or a paged-cache call meets what its comment lists.  Returns that status, CUDA on a CUDA error, else OK.
  */
 int w12_check_status(void *stream);
 

@@ -2,7 +2,9 @@
 
 ``w12`` is the ctypes binding of libw12.so (C ABI in include/w12.h);
 ``W12Weight`` is a small convenience holder built on it (torch provides the
-device memory and the stream).  ``workloads`` draws the seeded synthetic inputs.
+device memory and the stream).  ``KVCache``, ``KVPages`` and ``KVStep`` (kv.py)
+are the attention side of a layer: a paged key-value cache, its page tables and
+one step of its requests.  ``workloads`` draws the seeded synthetic inputs.
 """
 from __future__ import annotations
 
@@ -11,7 +13,16 @@ import numpy as np
 from . import w12
 from .w12 import W12Error
 
-__all__ = ["w12", "W12Error", "W12Weight", "W12Group", "Q8Weight", "Q8Group"]
+__all__ = ["w12", "W12Error", "W12Weight", "W12Group", "Q8Weight", "Q8Group", "KVCache", "KVPages", "KVStep"]
+
+
+def __getattr__(name):
+    # kv.py needs torch at import; the host encoder does not
+    if name in ("KVCache", "KVPages", "KVStep"):
+        from . import kv
+
+        return getattr(kv, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class W12Weight:

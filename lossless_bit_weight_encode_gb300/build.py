@@ -16,7 +16,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
-CUDA_SOURCES = ["kernels.cu"]
+CUDA_SOURCES = ["kernels.cu", "kv.cu", "kv_attend_d64.cu", "kv_attend_d128.cu", "kv_attend_d256.cu"]
 CXX_SOURCES = ["encoder.cpp", "q8_host.cpp", "capi.cpp"]
 
 

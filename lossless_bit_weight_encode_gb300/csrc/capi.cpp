@@ -507,6 +507,206 @@ int w12_q8_gemm_group(const uint16_t *x_dev, int count, const void *const *blobs
     });
 }
 
+namespace {
+int check_kv_cache(const w12_kv_cache *c, std::string &err) {
+    if (!c || !c->k_dev || !c->v_dev) {
+        err = "the cache or one of its pointers is null";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (c->dtype != W12_KV_BF16 && c->dtype != W12_KV_Q8) {
+        err = "cache dtype must be W12_KV_BF16 or W12_KV_Q8";
+        return W12_ERR_INVALID_ARG;
+    }
+    if ((c->dtype == W12_KV_Q8) != (c->scales_dev != nullptr)) {
+        err = "a Q8 cache needs scales_dev, a BF16 cache has none";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) {
+        err = "head_dim must be 64, 128 or 256";
+        return W12_ERR_SHAPE;
+    }
+    if (c->num_pages < 1 || c->num_pages > 0x7FFFFFFF || c->kv_heads < 1 || c->kv_heads > 65536 ||
+        c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > (1 << 20)) {
+        err = "num_pages and kv_heads must be at least 1 (kv_heads at most 65536) and page_size a multiple of 16 up "
+              "to 2^20";
+        return W12_ERR_SHAPE;
+    }
+    const int64_t unit = c->dtype == W12_KV_BF16 ? 8 : 16;
+    for (const int64_t s : {c->page_stride, c->head_stride, c->row_stride}) {
+        if (s < c->head_dim || s >= (int64_t(1) << 37)) {
+            err = "cache strides must be at least head_dim and below 2^37";
+            return W12_ERR_SHAPE;
+        }
+        if (s % unit != 0) {
+            err = "cache strides must be multiples of 16 bytes";
+            return W12_ERR_ALIGNMENT;
+        }
+    }
+    if (!aligned(c->k_dev, 16) || !aligned(c->v_dev, 16) || !aligned(c->scales_dev, 16)) {
+        err = "k_dev, v_dev and scales_dev must be 16-byte aligned";
+        return W12_ERR_ALIGNMENT;
+    }
+    return W12_OK;
+}
+
+int check_kv_attend(const w12_kv_cache *c, const w12_kv_attend_args *a, std::string &err) {
+    const int rc = check_kv_cache(c, err);
+    if (rc != W12_OK) return rc;
+    if (!a) {
+        err = "args is null";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (a->requests < 1 || a->tokens < 1 || a->max_blocks < 1 || a->window < 0 || a->max_new < 0) {
+        err = "requests, tokens and max_blocks must be at least 1, window and max_new at least 0";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (a->heads < 1 || a->heads % c->kv_heads != 0 || a->heads > 65536) {
+        err = "heads must be a multiple of kv_heads, at most 65536";
+        return W12_ERR_SHAPE;
+    }
+    if ((int64_t)a->max_blocks * c->page_size >= (int64_t(1) << 31) || a->table_stride < a->max_blocks) {
+        err = "max_blocks * page_size must be below 2^31 and table_stride at least max_blocks";
+        return W12_ERR_SHAPE;
+    }
+    return W12_OK;
+}
+}  // namespace
+
+int w12_kv_plan(const w12_kv_plan_args *args, void *stream) {
+    return guarded([&](std::string &err) {
+        if (!args || !args->lens || !args->new_lens || !args->owned_in || !args->owned_out || !args->tables ||
+            !args->ring || !args->ring_state_in || !args->ring_state_out || !args->cu_new ||
+            (args->tokens > 0 && (!args->positions || !args->slots))) {
+            err = "null pointer";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        if (args->requests < 1 || args->max_blocks < 1 || args->ring_size < 1 || args->tokens < 0) {
+            err = "requests, max_blocks and ring_size must be at least 1 and tokens at least 0";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        if (args->page_size < 16 || args->page_size % 16 != 0 ||
+            (int64_t)args->max_blocks * args->page_size >= (int64_t(1) << 31) ||
+            args->table_stride < args->max_blocks) {
+            err = "page_size must be a multiple of 16, max_blocks * page_size below 2^31 and table_stride at least "
+                  "max_blocks";
+            return (int)W12_ERR_SHAPE;
+        }
+        for (const void *p : {(const void *)args->lens, (const void *)args->new_lens, (const void *)args->owned_in,
+                              (const void *)args->owned_out, (const void *)args->tables, (const void *)args->ring,
+                              (const void *)args->cu_new, (const void *)args->positions})
+            if (!aligned(p, 4)) {
+                err = "32-bit arrays must be 4-byte aligned";
+                return (int)W12_ERR_ALIGNMENT;
+            }
+        if (!aligned(args->ring_state_in, 8) || !aligned(args->ring_state_out, 8) || !aligned(args->slots, 8)) {
+            err = "64-bit arrays must be 8-byte aligned";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        return w12::launch::kv_plan(*args, stream, &err);
+    });
+}
+
+int w12_kv_store(const w12_kv_cache *cache, const w12_kv_store_args *args, void *stream) {
+    return guarded([&](std::string &err) {
+        const int rc = check_kv_cache(cache, err);
+        if (rc != W12_OK) return rc;
+        if (!args || !args->k || !args->v || !args->slots || args->heads < 0 ||
+            (args->heads > 0 && (!args->q || !args->q_out)) || args->tokens < 0) {
+            err = "null pointer or a negative count";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        if (args->heads > 65536) {
+            err = "heads must be at most 65536";
+            return (int)W12_ERR_SHAPE;
+        }
+        if (args->rot < 0 || args->rot > cache->head_dim || args->rot % (args->interleaved ? 2 : 16) != 0) {
+            err = "rot must be a multiple of 16 (of 2 when interleaved) and at most head_dim";
+            return (int)W12_ERR_SHAPE;
+        }
+        if (args->rot > 0 && (!args->rope || !args->positions || args->rope_rows < 1)) {
+            err = "rotation needs rope, rope_rows and positions";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        const int64_t kv = (int64_t)cache->kv_heads * cache->head_dim, qd = (int64_t)args->heads * cache->head_dim;
+        if (args->k_stride < kv || args->v_stride < kv ||
+            (args->heads > 0 && (args->q_stride < qd || args->q_out_stride < qd))) {
+            err = "a token stride is shorter than its heads";
+            return (int)W12_ERR_SHAPE;
+        }
+        if ((args->k_stride | args->v_stride) % 8 != 0 ||
+            (args->heads > 0 && (args->q_stride | args->q_out_stride) % 8 != 0)) {
+            err = "token strides must be multiples of 8 elements";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        for (const void *p : {(const void *)args->q, (const void *)args->k, (const void *)args->v,
+                              (const void *)args->q_out, (const void *)args->q_norm, (const void *)args->k_norm,
+                              (const void *)args->rope})
+            if (!aligned(p, 16)) {
+                err = "q, k, v, q_out, the norm weights and rope must be 16-byte aligned";
+                return (int)W12_ERR_ALIGNMENT;
+            }
+        if (!aligned(args->positions, 4) || !aligned(args->slots, 8)) {
+            err = "positions must be 4-byte and slots 8-byte aligned";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        return w12::launch::kv_store(*cache, *args, stream, &err);
+    });
+}
+
+int w12_kv_read(const w12_kv_cache *cache, const int64_t *slots, int32_t tokens, uint16_t *k_out, uint16_t *v_out,
+                void *stream) {
+    return guarded([&](std::string &err) {
+        const int rc = check_kv_cache(cache, err);
+        if (rc != W12_OK) return rc;
+        if (!slots || !k_out || !v_out || tokens < 0) {
+            err = "null pointer or a negative count";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        if (!aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16)) {
+            err = "slots must be 8-byte and the outputs 16-byte aligned";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        return w12::launch::kv_read(*cache, slots, tokens, k_out, v_out, stream, &err);
+    });
+}
+
+int w12_kv_attend_workspace_size(const w12_kv_cache *cache, const w12_kv_attend_args *args, size_t *bytes) {
+    return guarded([&](std::string &err) {
+        const int rc = check_kv_attend(cache, args, err);
+        if (rc != W12_OK) return rc;
+        if (!bytes) {
+            err = "bytes is null";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        return w12::launch::kv_attend_workspace_size(*cache, *args, bytes, &err);
+    });
+}
+
+int w12_kv_attend(const w12_kv_cache *cache, const w12_kv_attend_args *args, void *workspace, size_t ws_bytes,
+                  void *stream) {
+    return guarded([&](std::string &err) {
+        const int rc = check_kv_attend(cache, args, err);
+        if (rc != W12_OK) return rc;
+        if (!args->q || !args->out || !args->tables || !args->lens || !args->cu_new || !workspace) {
+            err = "null device pointer";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        const int64_t row = (int64_t)args->heads * cache->head_dim;
+        if (args->q_stride < row || args->out_stride < row) {
+            err = "a token stride is shorter than its heads";
+            return (int)W12_ERR_SHAPE;
+        }
+        if (args->q_stride % 8 != 0 || args->out_stride % 8 != 0 || !aligned(args->q, 16) || !aligned(args->out, 16) ||
+            !aligned(workspace, 256) || !aligned(args->lse, 4) || !aligned(args->tables, 4) ||
+            !aligned(args->lens, 4) || !aligned(args->cu_new, 4) || !aligned(args->tree, 4)) {
+            err = "q and out must be 16-byte aligned with strides of a multiple of 8, workspace 256-byte, the 32-bit "
+                  "arrays 4-byte aligned";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        return w12::launch::kv_attend(*cache, *args, workspace, ws_bytes, stream, &err);
+    });
+}
+
 int w12_read_stream(const void *buf_dev, size_t bytes, void *sink_dev, uint32_t never, void *stream) {
     return guarded([&](std::string &err) {
         if (!buf_dev || !sink_dev) {

@@ -1,7 +1,8 @@
 // Host launchers of the W12 kernels and the per-device status word.
 //
-// One translation unit holds every kernel so that the status word
-// (g_w12_status, static device memory: no allocation) is one symbol per device.
+// This translation unit holds the weight kernels and the status word
+// (g_w12_status, static device memory: no allocation), one symbol per device;
+// the paged-cache kernels (kv.cu, kv_attend_*.cu) get its address.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -17,6 +18,7 @@
 #include "gemm_tc_sm.cuh"
 #include "gemv.cuh"
 #include "gemv_sm.cuh"
+#include "kv_common.cuh"
 #include "w12_host.hpp"
 #include "w12_launch.hpp"
 
@@ -376,6 +378,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder(std::string *err) {
 }
 
 }  // namespace
+
+int device_view(DeviceView *out, std::string *err) {
+    DeviceState *s = nullptr;
+    const int rc = device_state(&s, err);
+    if (rc != W12_OK) return rc;
+    out->device = s->device;
+    out->sm_count = s->sm_count;
+    out->status = s->status;
+    out->pdl = opt(kOptPdl) != 0;
+    out->timeout_ns = (uint64_t)opt(kOptTimeout) * 1000000ull;
+    return W12_OK;
+}
+
+void *tensor_map_encode(std::string *err) { return reinterpret_cast<void *>(tensor_map_encoder(err)); }
 
 int plan_gemm(const w12_info &info, int M, GemmPlan *plan, std::string *err, bool q8) {
     if (M < 1 || M > 32) {
@@ -805,6 +821,18 @@ int check_status(void *stream, std::string *err) {
         if (v & dev::kStatusEncodeOverflow) {
             *err = "w12_encode_device: the blob buffer is shorter than the encoding" + word;
             return W12_ERR_BUFFER_TOO_SMALL;
+        }
+        if (v & dev::kStatusKvPages) {
+            *err = "w12_kv_plan: the ring of free pages ran out" + word;
+            return W12_ERR_BUFFER_TOO_SMALL;
+        }
+        if (v & dev::kStatusKvIndex) {
+            *err = "w12_kv_store or w12_kv_read: a slot or a position outside its table" + word;
+            return W12_ERR_INVALID_ARG;
+        }
+        if (v & dev::kStatusKvSizes) {
+            *err = "a paged-cache call met lengths that do not fit its tables or its token count" + word;
+            return W12_ERR_SHAPE;
         }
         *err = "w12_encode_device: more than 2^32-1 escapes, split the matrix" + word;
         return W12_ERR_SHAPE;

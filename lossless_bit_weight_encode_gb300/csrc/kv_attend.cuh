@@ -1,0 +1,730 @@
+// Attention of a step's new tokens over the paged cache (w12_kv_attend in
+// include/w12.h).
+//
+// Mathematics.  Per request, key head and row (a row is one new token and one
+// query head of the key head's group): x_j = scale * log2(e) * q . k_j, one pass
+// over the keys with the running maximum m, sum l = sum 2^(x_j - m) and output
+// o = sum 2^(x_j - m) v_j.  Two partial results join as
+//   m = max(m1, m2), l = l1 2^(m1-m) + l2 2^(m2-m), o likewise,
+// and out = o / l, lse = m ln 2 + ln l.  The running maximum is only raised when
+// a score passes it by more than 8 (2^8 is harmless in fp32), so that most tiles
+// need neither the cross-lane maximum nor a rescaling of o.
+//
+// What bounds it: the keys and values are read once, from HBM; per byte of a
+// BF16 cache there are 2 * rows flops.  Layout for that: a producer warp keeps a
+// ring of 64-key tiles full by TMA (one 5-D box of 16 tokens x head_dim per k and
+// v: 16 tokens are the page granularity, so any page size that is a multiple of
+// 16 works and a box never crosses a page), and four consumer warps multiply on
+// the tensor cores straight from shared memory.  The rows are few, so they are
+// the 8-wide N of mma.m16n8k16 and the keys (for k q^T) or the head's columns
+// (for v^T p^T) its M: nothing is padded from 6 rows to 128.  The probabilities
+// go from accumulator to operand layout with one movmatrix per 8 x 8.  Warps
+// split a tile's keys (WK) and, where the rows are many, the rows (WR).
+//
+// Work split.  The unit is one 64-key tile of one (request, key head, row block);
+// all units form one line that the CTAs cut into equal ranges, whatever the
+// lengths.  A range that covers a row block's keys only in part leaves its
+// partial result in the workspace, and the CTA that arrives last at the block's
+// counter joins the parts in range order (the same result in every run).
+//
+// Q8 cache: int8 elements become BF16 exactly in registers; a key's scale
+// multiplies its score, a value's scale its probability.
+#pragma once
+
+#include <cuda.h>
+
+#include "kv_common.cuh"
+#include "w12_device.cuh"
+
+namespace w12 {
+namespace dev {
+
+constexpr int kAttendTile = 64;       // keys of a pipeline stage
+constexpr int kAttendSlice = 16;      // keys of one TMA box and of one mma
+constexpr int kAttendThreads = 160;   // four consumer warps and the producer
+constexpr float kAttendLazy = 8.0f;   // how far a score may pass the running maximum (log2)
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D, bool Q8, int WK, int WR, int NT>
+struct AttendCfg {
+    static_assert(WK * WR == 4, "four consumer warps");
+    static constexpr int kRows = WR * NT * 8;
+    static constexpr int kElem = Q8 ? 1 : 2;
+    static constexpr int kRowBytes = D * kElem < 128 ? D * kElem : 128;  // swizzled box rows
+    static constexpr int kHalves = D * kElem / kRowBytes;
+    static constexpr int kSliceBytes = kAttendSlice * D * kElem;
+    static constexpr int kTileBytes = 4 * kSliceBytes;  // k (or v) of a stage
+    static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kStages = kStageBytes >= 65536 ? 3 : 98304 / kStageBytes > 8 ? 8 : 98304 / kStageBytes;
+    static constexpr int kScaleBytes = Q8 ? 512 : 0;  // per stage: 64 keys x (k, v)
+    static constexpr int kMergeStride = 68;           // floats: 64 columns and 4 of skew
+    static constexpr int kOffScales = kStages * kStageBytes;
+    static constexpr int kOffMerge = kOffScales + kStages * kScaleBytes;
+    static constexpr int kOffMl = kOffMerge + WK * kRows * kMergeStride * 4;
+    static constexpr int kOffBars = kOffMl + WK * kRows * 8;
+    static constexpr int kSmemBytes = kOffBars + 2 * 8 * kStages + 4 * kStages + 16 + 1024;  // 1024: alignment
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// c += a (16 x 16) * b (16 x 8), BF16 operands, fp32 sums.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four int8 to BF16, exactly: bytes 0 and 2 to lo, bytes 1 and 3 to hi.  With
+// b = byte: 128 + (b & 127) is BF16 0x4300 | (b & 127); adding -128 (b >= 0) or
+// -256 (b < 0), which is BF16 0xC300 | (b & 128), gives b, which BF16 holds.
+__device__ __forceinline__ void q8_to_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t h = w >> 8;
+    const uint32_t a0 = (w & 0x007F007Fu) | 0x43004300u, b0 = (w & 0x00800080u) | 0xC300C300u;
+    const uint32_t a1 = (h & 0x007F007Fu) | 0x43004300u, b1 = (h & 0x00800080u) | 0xC300C300u;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a0), "r"(b0));
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(a1), "r"(b1));
+}
+
+// 5-D tiled copy global -> shared.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int32_t c1, int32_t c3, int32_t c4,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5, %6}], [%7];" ::"r"(dst),
+        "l"(tmap), "r"(0), "r"(c1), "r"(0), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// One request as the kernel sees it.
+struct KvRequest {
+    int32_t past, q0, qlen, kv, first, tile0, ntiles, rblocks;
+    int64_t units;
+};
+
+template <int ROWS>
+__device__ __forceinline__ KvRequest kv_request(const KvAttendParams &p, int b) {
+    KvRequest r;
+    r.q0 = min(max(p.cu_new[b], 0), p.tokens);
+    r.qlen = min(max(p.cu_new[b + 1], r.q0), p.tokens) - r.q0;
+    r.past = min(max(p.lens[b], 0), p.max_keys);
+    r.kv = (int32_t)min((int64_t)r.past + r.qlen, (int64_t)p.max_keys);
+    // first key that any of the request's new tokens sees
+    r.first = p.window > 0 ? (int32_t)max((int64_t)r.past + 1 - p.window, (int64_t)0) : 0;
+    r.tile0 = min(r.first, r.kv) / kAttendTile;
+    r.ntiles = max((r.kv + kAttendTile - 1) / kAttendTile - r.tile0, 1);
+    r.rblocks = (int32_t)(((int64_t)r.qlen * p.group + ROWS - 1) / ROWS);
+    r.units = (int64_t)p.kv_heads * r.rblocks * r.ntiles;
+    return r;
+}
+
+__device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    return v;
+}
+
+// A CTA's range of units and its place in it; every warp keeps its own copy.
+struct KvWalk {
+    int64_t total, u, end;  // all units, the next one, the range's end
+    int64_t start;          // first unit of request b
+    int32_t b, ctas;
+};
+
+template <int ROWS>
+__device__ __forceinline__ bool kv_walk_init(const KvAttendParams &p, KvWalk &w, KvRequest &r) {
+    const int lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int b = lane; b < p.requests; b += 32) sum += kv_request<ROWS>(p, b).units;
+    w.total = warp_sum_i64(sum);
+    w.ctas = (int32_t)min((int64_t)gridDim.x, w.total);
+    if ((int)blockIdx.x >= w.ctas) return false;
+    w.u = w.total * blockIdx.x / w.ctas;
+    w.end = w.total * (blockIdx.x + 1) / w.ctas;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.requests; b0 += 32) {
+        const int64_t own = b0 + lane < p.requests ? kv_request<ROWS>(p, b0 + lane).units : 0;
+        int64_t inc = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, inc, d);
+            if (lane >= d) inc += x;
+        }
+        const uint32_t hit = __ballot_sync(~0u, before + inc > w.u);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            w.b = b0 + src;
+            w.start = __shfl_sync(~0u, before + inc - own, src);
+            r = kv_request<ROWS>(p, w.b);
+            return true;
+        }
+        before += __shfl_sync(~0u, inc, 31);
+    }
+    return false;  // not reached: u < total
+}
+
+// The piece at w.u: its (key head, row block) and its tiles [ja, jb).
+struct KvPiece {
+    int32_t head, rb, ja, jb;
+};
+
+__device__ __forceinline__ KvPiece kv_piece(const KvWalk &w, const KvRequest &r) {
+    const int64_t off = w.u - w.start;
+    const int32_t item = (int32_t)(off / r.ntiles);
+    KvPiece c;
+    c.head = item / r.rblocks;
+    c.rb = item - c.head * r.rblocks;
+    c.ja = (int32_t)(off - (int64_t)item * r.ntiles);
+    c.jb = (int32_t)min((int64_t)r.ntiles, w.end - w.u + c.ja);
+    return c;
+}
+
+// Moves on by n units within the request, to the next request where it ends.
+template <int ROWS>
+__device__ __forceinline__ void kv_advance(const KvAttendParams &p, KvWalk &w, KvRequest &r, int32_t n) {
+    w.u += n;
+    while (w.u < w.end && w.u >= w.start + r.units) {
+        w.start += r.units;
+        r = kv_request<ROWS>(p, ++w.b);
+    }
+}
+
+// Which keys of a slice one row sees.
+struct KvRowView {
+    int32_t index;  // of the row's token in the request: past + i
+    uint32_t tree;
+};
+
+__device__ __forceinline__ bool kv_sees(const KvAttendParams &p, const KvRequest &r, const KvRowView &v, int32_t key) {
+    bool s = key < r.kv;
+    if (p.tree) {
+        const int32_t j = key - r.past;
+        s = s && (j < 0 || (j < 32 && ((v.tree >> j) & 1u)));
+    } else {
+        s = s && key <= v.index;
+    }
+    return s && (p.window <= 0 || key > v.index - p.window);
+}
+
+template <int D, bool Q8, int WK, int WR, int NT>
+__global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvAttendParams p,
+                                                                       const __grid_constant__ CUtensorMap tm_k,
+                                                                       const __grid_constant__ CUtensorMap tm_v) {
+    using C = AttendCfg<D, Q8, WK, WR, NT>;
+    constexpr int ROWS = C::kRows, KS = D / 16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    float *merge = reinterpret_cast<float *>(smem + C::kOffMerge);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::kOffMl);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
+    uint64_t *empty = full + C::kStages;
+    uint32_t *present = reinterpret_cast<uint32_t *>(empty + C::kStages);
+    volatile uint32_t *last_flag = present + C::kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 4);
+        }
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 128) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
+
+    KvWalk w;
+    KvRequest r;
+    if (!kv_walk_init<ROWS>(p, w, r)) return;  // the same for the whole CTA
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ producer
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && w.u < w.end) {
+            const KvPiece c = kv_piece(w, r);
+            const int32_t *row = p.tables + (int64_t)w.b * p.table_stride;
+            for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
+                const uint32_t stage = it % C::kStages, round = it / C::kStages;
+                // lane s < 4 deals with slice s
+                const int32_t kb = (r.tile0 + j) * kAttendTile + lane * kAttendSlice;
+                const bool want = lane < 4 && kb < r.kv && kb + kAttendSlice > r.first;
+                int32_t page = -1, off = 0;
+                if (want) {
+                    const int32_t e = kb / p.page_size;
+                    off = kb - e * p.page_size;
+                    page = row[e];
+                }
+                if (round > 0) ok = mbar_wait(&empty[stage], (round - 1) & 1, deadline);
+                ok = __shfl_sync(~0u, ok, 0);
+                if (!ok) break;
+                const bool here = page >= 0 && page < p.num_pages;
+                const uint32_t mask = __ballot_sync(~0u, here) & 15u;
+                if (lane == 0) {
+                    present[stage] = mask;
+                    mbar_arrive_expect_tx(&full[stage],
+                                          (uint32_t)__popc(mask) * (2 * C::kSliceBytes + (Q8 ? 128 : 0)));
+                }
+                __syncwarp();
+                if (here) {
+                    const uint32_t dst = smem_u32(smem + stage * C::kStageBytes + lane * C::kSliceBytes);
+                    const uint32_t bar = smem_u32(&full[stage]);
+                    tma_load_5d(dst, &tm_k, off, c.head, page, bar);
+                    tma_load_5d(dst + C::kTileBytes, &tm_v, off, c.head, page, bar);
+                    if (Q8)
+                        bulk_g2s(smem + C::kOffScales + stage * C::kScaleBytes + lane * 128,
+                                 p.scales + (((int64_t)page * p.kv_heads + c.head) * p.page_size + off) * 2, 128,
+                                 &full[stage]);
+                }
+            }
+            if (ok) kv_advance<ROWS>(p, w, r, c.jb - c.ja);
+        }
+        if (!ok) {
+            // no copy may still be in flight when the CTA ends
+            if (lane == 0) {
+                atomicOr(p.status, 8u);
+                const uint64_t late = globaltimer_ns() + p.timeout_ns;
+                for (uint32_t k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
+                    if (!mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1, late)) break;
+            }
+            __syncwarp();
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int wk = warp % WK, wr = warp / WK;
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t it = 0;
+    bool ok = true;
+    while (w.u < w.end) {
+        const KvPiece c = kv_piece(w, r);
+        const int32_t nrows = min((int64_t)ROWS, (int64_t)r.qlen * p.group - (int64_t)c.rb * ROWS);
+        const int32_t row0 = c.rb * ROWS;
+
+        // q as the mma's B operand: row (n) g of each 8-row tile, columns (k) of
+        // step ks in the order the A operand's layout wants
+        uint32_t qf[NT][KS][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int lr = (wr * NT + nt) * 8 + g;
+            const int32_t rr = row0 + lr;
+            const int32_t i = rr / p.group;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                p.q + (int64_t)(r.q0 + (lr < nrows ? i : 0)) * p.q_stride +
+                (int64_t)(c.head * p.group + (lr < nrows ? rr - i * p.group : 0)) * D);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t a = 0, b = 0;
+                if (lr < nrows) {
+                    if (Q8) {
+                        // columns 4t..4t+3 of the step; pairs (0, 2) and (1, 3), as q8_to_bf16 gives them
+                        const uint32_t x = src[ks * 8 + 2 * t], y = src[ks * 8 + 2 * t + 1];
+                        a = prmt(x, y, 0x5410u);
+                        b = prmt(x, y, 0x7632u);
+                    } else {
+                        a = src[ks * 8 + t];
+                        b = src[ks * 8 + 4 + t];
+                    }
+                }
+                qf[nt][ks][0] = a;
+                qf[nt][ks][1] = b;
+            }
+        }
+        float o[KS][NT][4] = {};
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.0f;
+
+        for (int j = c.ja; j < c.jb; ++j, ++it) {
+            const uint32_t stage = it % C::kStages, round = it / C::kStages;
+            // after a timeout the walk goes on without waiting (its reads stay
+            // inside shared memory) so that every barrier below is reached
+            if (ok && !mbar_wait(&full[stage], round & 1, deadline)) {
+                ok = false;
+                if (lane == 0) atomicOr(p.status, 8u);
+            }
+            __syncwarp();
+            const uint32_t mask = present[stage];
+            const uint32_t kbase = smem_u32(smem + stage * C::kStageBytes), vbase = kbase + C::kTileBytes;
+            for (int s = wk; s < 4; s += WK) {
+                if (!((mask >> s) & 1u)) continue;
+                const int32_t kb = (r.tile0 + j) * kAttendTile + s * kAttendSlice;
+                const uint32_t ks_base = kbase + s * C::kSliceBytes, vs_base = vbase + s * C::kSliceBytes;
+                // scores of 16 keys (rows g, g + 8) and NT * 8 rows (columns 2t, 2t + 1)
+                float x[NT][4] = {};
+                if (!Q8) {
+                    const int krow = ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const int chunk = 2 * ks + (lane >> 4);
+                        uint32_t a[4];
+                        ldsm4(ks_base + (chunk / 8) * (16 * 128) + krow * 128 + (((chunk % 8) ^ (krow & 7)) << 4), a);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_bf16(x[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                    }
+                } else {
+                    constexpr int CH = C::kRowBytes / 16;  // 16-byte chunks of a box row
+                    const int krow = ((lane >> 3) & 1) * 8 + (lane & 7);
+                    const int sw = CH == 8 ? krow & 7 : (krow >> 1) & 3;
+#pragma unroll
+                    for (int k2 = 0; k2 < KS / 2; ++k2) {
+                        const int chunk = 2 * k2 + (lane >> 4);
+                        uint32_t w4[4];
+                        ldsm4(ks_base + (chunk / CH) * (16 * C::kRowBytes) + krow * C::kRowBytes +
+                                  (((chunk % CH) ^ sw) << 4),
+                              w4);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t a[4];
+                            q8_to_bf16(w4[2 * e], a[0], a[2]);
+                            q8_to_bf16(w4[2 * e + 1], a[1], a[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_bf16(x[nt], a, qf[nt][2 * k2 + e][0], qf[nt][2 * k2 + e][1]);
+                        }
+                    }
+                }
+                float vs0 = 1.0f, vs1 = 1.0f, sc0 = p.scale_log2, sc1 = p.scale_log2;
+                if (Q8) {
+                    const float2 *sc =
+                        reinterpret_cast<const float2 *>(smem + C::kOffScales + stage * C::kScaleBytes) + s * 16;
+                    const float2 a = sc[g], b = sc[g + 8];
+                    sc0 *= a.x, sc1 *= b.x, vs0 = a.y, vs1 = b.y;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) x[nt][0] *= sc0, x[nt][1] *= sc0, x[nt][2] *= sc1, x[nt][3] *= sc1;
+
+                // keys that some row does not see
+                const bool edge = kb + kAttendSlice > (p.tree ? r.past : r.past + 1) || kb + kAttendSlice > r.kv ||
+                                  (p.window > 0 && kb <= r.past + r.qlen - 1 - p.window);
+                uint32_t seen = ~0u;  // bit 4 nt + c: score c of tile nt
+                if (edge) {
+                    seen = 0;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int32_t lr = (wr * NT + nt) * 8 + 2 * t + e;
+                            const int32_t i = min(row0 + lr, row0 + nrows - 1) / p.group;
+                            KvRowView v;
+                            v.index = r.past + i;
+                            v.tree = p.tree ? p.tree[r.q0 + i] : 0u;
+                            if (kv_sees(p, r, v, kb + g)) seen |= 1u << (4 * nt + e);
+                            if (kv_sees(p, r, v, kb + g + 8)) seen |= 1u << (4 * nt + e + 2);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!((seen >> (4 * nt + e)) & 1u)) x[nt][e] = -INFINITY;
+                }
+
+                // running maximum
+                bool raise = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        raise |= fmaxf(x[nt][e], x[nt][e + 2]) > m[nt][e] + kAttendLazy;
+                if (__any_sync(~0u, raise)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float al[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = fmaxf(x[nt][e], x[nt][e + 2]);
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                            v = fmaxf(v, m[nt][e]);
+                            al[e] = v == -INFINITY ? 1.0f : ex2(m[nt][e] - v);
+                            m[nt][e] = v;
+                            l[nt][e] *= al[e];
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < KS; ++mt)
+                            o[mt][nt][0] *= al[0], o[mt][nt][1] *= al[1], o[mt][nt][2] *= al[0], o[mt][nt][3] *= al[1];
+                    }
+                }
+                // probabilities; l sums them in fp32, the tensor cores get them (with
+                // Q8 times the value's scale) rounded to BF16: at most 2^-8 of each
+                // weight, as the rounding of the output
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
+                    const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+                    float p0 = ex2(x[nt][0] - m0), p1 = ex2(x[nt][1] - m1);
+                    float p2 = ex2(x[nt][2] - m0), p3 = ex2(x[nt][3] - m1);
+                    l[nt][0] += p0 + p2;
+                    l[nt][1] += p1 + p3;
+                    if (Q8) {
+                        p0 *= vs0, p1 *= vs0, p2 *= vs1, p3 *= vs1;
+                        if (edge) {  // an unseen key's scale may be anything
+                            const uint32_t sn = seen >> (4 * nt);
+                            p0 = sn & 1u ? p0 : 0.0f, p1 = sn & 2u ? p1 : 0.0f;
+                            p2 = sn & 4u ? p2 : 0.0f, p3 = sn & 8u ? p3 : 0.0f;
+                        }
+                    }
+                    const uint32_t a = pack_bf16x2(p0, p1), b = pack_bf16x2(p2, p3);
+                    pb[nt][0] = movmatrix(a);
+                    pb[nt][1] = movmatrix(b);
+                }
+
+                // o (columns of the head x rows) += v^T p^T
+                if (!Q8) {
+                    const int vrow = (lane >> 4) * 8 + (lane & 7);
+                    bool odd = false;  // a value that is not finite behind a key that some row does not see
+                    uint32_t k0 = ~0u, k1 = ~0u;
+                    if (edge) {
+                        // keys behind the request's last one hold anything: zero
+                        const int32_t nv = r.kv - kb;
+                        k0 = (2 * t < nv ? 0xFFFFu : 0u) | (2 * t + 1 < nv ? 0xFFFF0000u : 0u);
+                        k1 = (2 * t + 8 < nv ? 0xFFFFu : 0u) | (2 * t + 9 < nv ? 0xFFFF0000u : 0u);
+#pragma unroll 4
+                        for (int mt = 0; mt < KS; ++mt) {
+                            const int chunk = 2 * mt + ((lane >> 3) & 1);
+                            uint32_t a[4];
+                            ldsm4_trans(
+                                vs_base + (chunk / 8) * (16 * 128) + vrow * 128 + (((chunk % 8) ^ (vrow & 7)) << 4), a);
+                            a[0] &= k0, a[1] &= k0, a[2] &= k1, a[3] &= k1;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                odd |= (a[e] & 0x7F80u) == 0x7F80u || (a[e] & 0x7F800000u) == 0x7F800000u;
+                        }
+                        odd = __any_sync(~0u, odd);
+                    }
+                    if (!odd) {
+#pragma unroll
+                        for (int mt = 0; mt < KS; ++mt) {
+                            const int chunk = 2 * mt + ((lane >> 3) & 1);
+                            uint32_t a[4];
+                            ldsm4_trans(
+                                vs_base + (chunk / 8) * (16 * 128) + vrow * 128 + (((chunk % 8) ^ (vrow & 7)) << 4), a);
+                            a[0] &= k0, a[1] &= k0, a[2] &= k1, a[3] &= k1;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_bf16(o[mt][nt], a, pb[nt][0], pb[nt][1]);
+                        }
+                    } else {
+                        // 0 * NaN must not reach a row that does not see the key: one
+                        // row at a time, with the values of its unseen keys zeroed
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint32_t bal[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) bal[e] = __ballot_sync(~0u, (seen >> (4 * nt + e)) & 1u);
+                            for (int n = 0; n < 8; ++n) {
+                                // ballot bit 4 g + t holds key g (or g + 8) of row 2t + e
+                                const uint32_t lo = (n & 1 ? bal[1] : bal[0]) >> (n >> 1);
+                                const uint32_t hi = (n & 1 ? bal[3] : bal[2]) >> (n >> 1);
+                                uint32_t z0 = 0, z1 = 0;
+                                if ((lo >> (8 * t)) & 1u) z0 |= 0xFFFFu;
+                                if ((lo >> (8 * t + 4)) & 1u) z0 |= 0xFFFF0000u;
+                                if ((hi >> (8 * t)) & 1u) z1 |= 0xFFFFu;
+                                if ((hi >> (8 * t + 4)) & 1u) z1 |= 0xFFFF0000u;
+                                const uint32_t b0 = g == n ? pb[nt][0] : 0u, b1 = g == n ? pb[nt][1] : 0u;
+#pragma unroll
+                                for (int mt = 0; mt < KS; ++mt) {
+                                    const int chunk = 2 * mt + ((lane >> 3) & 1);
+                                    uint32_t a[4];
+                                    ldsm4_trans(vs_base + (chunk / 8) * (16 * 128) + vrow * 128 +
+                                                    (((chunk % 8) ^ (vrow & 7)) << 4),
+                                                a);
+                                    a[0] &= z0, a[1] &= z0, a[2] &= z1, a[3] &= z1;
+                                    float y[4] = {};
+                                    mma_bf16(y, a, b0, b1);
+                                    // the other rows' sums are 0 * value here: only row n's count
+                                    if (2 * t == (n & ~1)) {
+                                        if (n & 1) o[mt][nt][1] += y[1], o[mt][nt][3] += y[3];
+                                        else o[mt][nt][0] += y[0], o[mt][nt][2] += y[2];
+                                    }
+                                }
+                            }
+                        }
+                    }
+                } else {
+                    constexpr int CH = C::kRowBytes / 16;
+                    const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7);
+                    const int sw = CH == 8 ? vrow & 7 : (vrow >> 1) & 3;
+#pragma unroll
+                    for (int m2 = 0; m2 < KS / 2; ++m2) {
+                        const int chunk = 2 * m2 + (lane >> 4);
+                        uint32_t w4[4];
+                        ldsm4_trans(vs_base + (chunk / CH) * (16 * C::kRowBytes) + vrow * C::kRowBytes +
+                                        (((chunk % CH) ^ sw) << 4),
+                                    w4);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // rows g of the tile are the even columns 2g, rows g + 8 the odd ones
+                            uint32_t a[4];
+                            q8_to_bf16(w4[2 * e], a[0], a[1]);
+                            q8_to_bf16(w4[2 * e + 1], a[2], a[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_bf16(o[2 * m2 + e][nt], a, pb[nt][0], pb[nt][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+        }
+
+        // ------------------------------------------------------------ join the warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = l[nt][e];
+                v += __shfl_xor_sync(~0u, v, 4);
+                v += __shfl_xor_sync(~0u, v, 8);
+                v += __shfl_xor_sync(~0u, v, 16);
+                if (g == 0) ml[wk * ROWS + (wr * NT + nt) * 8 + 2 * t + e] = make_float2(m[nt][e], v);
+            }
+        const bool whole = c.ja == 0 && c.jb == r.ntiles;
+        const int32_t slot = 2 * (int32_t)blockIdx.x + (c.ja > 0 ? 0 : 1);
+#pragma unroll
+        for (int dc = 0; dc < D / 64; ++dc) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float *dst = merge + (wk * ROWS + (wr * NT + nt) * 8 + 2 * t) * C::kMergeStride + mt * 16;
+                    const int d0 = Q8 ? 2 * g : g, d1 = Q8 ? 2 * g + 1 : g + 8;
+                    dst[d0] = o[dc * 4 + mt][nt][0];
+                    dst[d0 + C::kMergeStride] = o[dc * 4 + mt][nt][1];
+                    dst[d1] = o[dc * 4 + mt][nt][2];
+                    dst[d1 + C::kMergeStride] = o[dc * 4 + mt][nt][3];
+                }
+            }
+            consumers_sync();
+            for (int i = threadIdx.x; i < nrows * 16; i += 128) {
+                const int lr = i >> 4, v4 = i & 15;
+                float mm = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < WK; ++k) mm = fmaxf(mm, ml[k * ROWS + lr].x);
+                float sum = 0.0f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    const float2 s = ml[k * ROWS + lr];
+                    const float f = s.x == -INFINITY ? 0.0f : ex2(s.x - mm);
+                    const float4 y =
+                        *reinterpret_cast<const float4 *>(merge + (k * ROWS + lr) * C::kMergeStride + v4 * 4);
+                    sum += f * s.y;
+                    acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+                }
+                if (whole) {
+                    const int32_t rr = row0 + lr, tok = r.q0 + rr / p.group, h = c.head * p.group + rr % p.group;
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    uint2 b;
+                    b.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+                    b.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+                    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (int64_t)h * D + dc * 64 + v4 * 4) = b;
+                    if (p.lse && dc == 0 && v4 == 0)
+                        p.lse[(int64_t)tok * (p.group * p.kv_heads) + h] =
+                            sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4 *>(p.part + ((int64_t)slot * ROWS + lr) * D + dc * 64 + v4 * 4) = acc;
+                    if (dc == 0 && v4 == 0) p.part_ml[(int64_t)slot * ROWS + lr] = make_float2(mm, sum);
+                }
+            }
+            consumers_sync();
+        }
+
+        // ------------------------------------------------------------ join the CTAs
+        if (!whole) {
+            const int64_t s0 = w.u - c.ja;  // the row block's first unit
+            const int32_t c0 = (int32_t)(((s0 + 1) * w.ctas - 1) / w.total);
+            const int32_t c1 = (int32_t)(((s0 + r.ntiles) * w.ctas - 1) / w.total);
+            const int64_t ci = c.head + (int64_t)p.kv_heads *
+                                            (w.b + (int64_t)r.q0 * p.group / ROWS + c.rb);
+            const bool counted = ci < p.n_counters;  // false only for a cu_new that is not a prefix sum
+            __threadfence();
+            consumers_sync();
+            if (threadIdx.x == 0) {
+                uint32_t is_last = 0;
+                if (counted) is_last = atomicAdd(&p.counters[ci], 1u) == (uint32_t)(c1 - c0);
+                else atomicOr(p.status, kStatusKvSizes);
+                *last_flag = is_last;
+            }
+            consumers_sync();
+            if (*last_flag) {
+                __threadfence();
+                for (int i = threadIdx.x; i < nrows * (D / 4); i += 128) {
+                    const int lr = i / (D / 4), v4 = i % (D / 4);
+                    float mm = -INFINITY, sum = 0.0f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int32_t k = c0; k <= c1; ++k) {
+                        const int64_t at = (int64_t)(2 * k + (k == c0 ? 1 : 0)) * ROWS + lr;
+                        const float2 s = __ldcg(p.part_ml + at);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D) + v4);
+                        const float mn = fmaxf(mm, s.x);
+                        const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
+                        const float f1 = s.x == -INFINITY ? 0.0f : ex2(s.x - mn);
+                        sum = sum * f0 + s.y * f1;
+                        acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
+                        acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
+                        mm = mn;
+                    }
+                    const int32_t rr = row0 + lr, tok = r.q0 + rr / p.group, h = c.head * p.group + rr % p.group;
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    uint2 b;
+                    b.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+                    b.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+                    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (int64_t)h * D + v4 * 4) = b;
+                    if (p.lse && v4 == 0)
+                        p.lse[(int64_t)tok * (p.group * p.kv_heads) + h] =
+                            sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+                }
+                if (threadIdx.x == 0) p.counters[ci] = 0;
+            }
+        }
+        kv_advance<ROWS>(p, w, r, c.jb - c.ja);
+    }
+    if (!ok && warp == 0 && lane == 0) {
+        // a wait ran out: no copy may still be in flight when the CTA ends
+        const uint64_t late = globaltimer_ns() + p.timeout_ns;
+        for (uint32_t k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
+            if (!mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1, late)) break;
+    }
+}
+
+}  // namespace dev
+}  // namespace w12

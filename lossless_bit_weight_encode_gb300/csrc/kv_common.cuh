@@ -1,0 +1,84 @@
+// Pieces shared by the paged key-value cache kernels.
+#pragma once
+
+#include <cstdint>
+
+namespace w12 {
+namespace dev {
+
+// Status word bits of the paged-cache calls (w12_check_status).
+constexpr uint32_t kStatusKvPages = 64u;   // the ring of free pages ran out
+constexpr uint32_t kStatusKvSizes = 128u;  // a length or the token count had to be clamped
+constexpr uint32_t kStatusKvIndex = 256u;  // a slot or position outside its table
+
+// Cache geometry as the kernels take it (w12_kv_cache in include/w12.h).
+struct KvGeom {
+    uint8_t *k, *v;
+    float *scales;
+    int64_t num_pages;
+    int64_t page_stride, head_stride, row_stride;  // elements
+    int32_t page_size, kv_heads;
+};
+
+struct KvPlanParams {
+    const int32_t *lens, *new_lens;
+    const int32_t *owned_in;
+    int32_t *owned_out;
+    int32_t *tables;
+    int64_t table_stride;
+    int32_t *ring;
+    const int64_t *state_in;
+    int64_t *state_out;
+    int32_t *cu_new;
+    int32_t *positions;
+    int64_t *slots;
+    int32_t requests, max_blocks, page_size, ring_size, tokens, trim;
+    uint32_t *status;
+};
+
+struct KvStoreParams {
+    KvGeom c;
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    const uint16_t *q_norm, *k_norm;
+    const float *rope;
+    const int32_t *positions;
+    const int64_t *slots;
+    int64_t rope_rows;
+    int32_t tokens, heads, rot;
+    float eps;
+    uint32_t *status;
+};
+
+struct KvReadParams {
+    KvGeom c;
+    const int64_t *slots;
+    uint16_t *k_out, *v_out;
+    int32_t tokens;
+    uint32_t *status;
+};
+
+struct KvAttendParams {
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    int64_t q_stride, out_stride;
+    const int32_t *tables;
+    int64_t table_stride;
+    const int32_t *lens, *cu_new;
+    const uint32_t *tree;
+    const float *scales;
+    int64_t num_pages;
+    int32_t requests, max_keys, tokens, kv_heads, group, window, page_size;
+    float scale_log2;  // softmax scale times log2(e)
+    float *part;       // partial outputs [2 * CTAs][rows][head_dim]
+    float2 *part_ml;   // their maxima and sums [2 * CTAs][rows]
+    uint32_t *counters;
+    uint32_t n_counters;
+    uint32_t *status;
+    uint64_t timeout_ns;
+};
+
+}  // namespace dev
+}  // namespace w12

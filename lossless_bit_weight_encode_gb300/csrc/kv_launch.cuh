@@ -1,0 +1,137 @@
+// Launch helpers of the paged-cache kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+#include <string>
+#include <utility>
+
+#include "kv_attend.cuh"
+#include "w12.h"
+#include "w12_launch.hpp"
+
+namespace w12 {
+namespace launch {
+
+inline int kv_cuda_fail(cudaError_t e, const char *what, std::string *err) {
+    *err = std::string(what) + ": " + cudaGetErrorString(e);
+    return W12_ERR_CUDA;
+}
+
+// Launch that may start while the kernel before it finishes (the kernels wait
+// with griddepcontrol.wait before they touch memory); cluster > 1: a cluster of
+// that many CTAs.
+template <class... KArgs, class... Args>
+cudaError_t kv_launch(const DeviceView &d, void (*kernel)(KArgs...), dim3 grid, int threads, int smem, int cluster,
+                      void *stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (d.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+constexpr int kKvMaxDevices = 64;
+
+// Rows of the tile a launch uses: new tokens times query heads per key head,
+// 8 to 64; more rows take several row blocks.
+inline int attend_rows(int max_new, int group) {
+    const int64_t rows = (int64_t)(max_new < 1 ? 1 : max_new) * group;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+// Workspace: the partial outputs, their maxima and sums, the counters.  The
+// first two have the same size in every plan of a device (kPartElems bounds rows x
+// head_dim x CTAs per SM), so that the counters lie at one place and calls of
+// different shapes can share a workspace: what one leaves zero is what another
+// finds.
+constexpr int kPartElems = 64 * 256;
+struct AttendPlan {
+    int rows = 8, ctas = 1;
+    size_t off_ml = 0, off_counters = 0, bytes = 0;
+    uint32_t n_counters = 0;
+};
+
+// One head_dim's kernels (kv_attend_*.cu): CTAs resident on the whole device
+// (with `p` null), or the launch.
+template <int D>
+int attend_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvAttendParams *p,
+               const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
+
+template <int D, bool Q8, int WK, int WR, int NT>
+int attend_variant(const DeviceView &d, int *resident, const dev::KvAttendParams *p, const CUtensorMap *tm_k,
+                   const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+    using C = dev::AttendCfg<D, Q8, WK, WR, NT>;
+    auto kernel = &dev::w12_kv_attend_kernel<D, Q8, WK, WR, NT>;
+    static std::mutex mu;
+    static int per_sm[kKvMaxDevices] = {};
+    if (d.device < 0 || d.device >= kKvMaxDevices) {
+        *err = "device ordinal out of range";
+        return W12_ERR_CUDA;
+    }
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (per_sm[d.device] == 0) {
+            void *k = reinterpret_cast<void *>(kernel);
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            int occ = 0;
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, dev::kAttendThreads, C::kSmemBytes);
+            if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend set-up", err);
+            if (occ < 1) {
+                *err = "w12_kv_attend cannot be resident on this device";
+                return W12_ERR_CUDA;
+            }
+            constexpr int kMost = kPartElems / (C::kRows * D);
+            per_sm[d.device] = occ < kMost ? occ : kMost;
+        }
+        *resident = per_sm[d.device] * d.sm_count;
+    }
+    if (!p) return W12_OK;
+    const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)ctas), dev::kAttendThreads, C::kSmemBytes, 1, stream,
+                                    *p, *tm_k, *tm_v);
+    if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend launch", err);
+    return W12_OK;
+}
+
+// The variants of one head_dim.  Rows up to 16 (BF16 operands of q and the sums
+// of 8 or 16 rows in registers): the warps split a tile's keys.  More rows: they
+// split the rows too, because the sums of 32 rows x head_dim do not fit a warp.
+// 256 columns take twice the registers per row, so the rows are split earlier.
+template <int D, bool Q8>
+int attend_rows_variant(const DeviceView &d, int rows, int *resident, const dev::KvAttendParams *p,
+                        const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+    switch (rows) {
+    case 8: return attend_variant<D, Q8, 4, 1, 1>(d, resident, p, tm_k, tm_v, ctas, stream, err);
+    case 16:
+        return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(d, resident, p, tm_k, tm_v,
+                                                                                          ctas, stream, err);
+    case 32:
+        return attend_variant<D, Q8, D == 256 ? 1 : 2, D == 256 ? 4 : 2, D == 256 ? 1 : 2>(d, resident, p, tm_k, tm_v,
+                                                                                          ctas, stream, err);
+    default: return attend_variant<D, Q8, 1, 4, 2>(d, resident, p, tm_k, tm_v, ctas, stream, err);
+    }
+}
+
+}  // namespace launch
+}  // namespace w12

@@ -1,0 +1,169 @@
+// Page tables, positions and slots of one step (w12_kv_plan in include/w12.h).
+//
+// Per request: need = ceil((len + new) / page), grow = max(need - owned, 0),
+// drop = max(owned - need, 0) with trim.  Three prefix sums over the requests
+// (new tokens, grow, drop) place every token, every page taken and every page
+// given back; each of the three lists is then walked flat, one element per
+// thread, its request found by a binary search in the prefix sums, so that one
+// long prompt among short ones costs no more than the same tokens spread out.
+//
+// The call is latency: it moves 20 bytes per request and 12 per token.  One
+// cluster of CTAs computes the sums redundantly and shares the lists; its
+// barrier is what allows owned and the ring state to be updated in place.  No
+// CTA reads what another writes: a taken page is read from the ring, never from
+// the table entry it goes to, and the ring positions given back are not those
+// taken (at most ring_size pages are free).
+#pragma once
+
+#include "kv_common.cuh"
+#include "w12_device.cuh"
+
+namespace w12 {
+namespace dev {
+
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ int32_t clamp_i32(int64_t v, int64_t lo, int64_t hi) {
+    return (int32_t)(v < lo ? lo : v > hi ? hi : v);
+}
+
+// Largest i in [0, n) with start[i] <= v (start[0] <= v holds).  Requests with
+// nothing share their successor's start, so the largest one is the owner.
+__device__ __forceinline__ int find_start(const int64_t *start, int n, int64_t v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanParams p) {
+    __shared__ int64_t s_tok[kPlanThreads], s_grow[kPlanThreads], s_drop[kPlanThreads];
+    __shared__ int32_t s_len[kPlanThreads], s_owned[kPlanThreads], s_need[kPlanThreads];
+    __shared__ int64_t s_warp[3][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const int64_t first = (int64_t)rank * kPlanThreads + tid, step = (int64_t)ranks * kPlanThreads;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t head = p.state_in[0], tail = p.state_in[1];
+    const int64_t avail = tail > head ? tail - head : 0;
+    const int64_t cap = (int64_t)p.max_blocks * p.page_size;
+    int64_t tok0 = 0, grow0 = 0, drop0 = 0;  // totals of the chunks before
+    uint32_t flags = 0;
+    for (int base = 0; base < p.requests; base += kPlanThreads) {
+        const int n = min(kPlanThreads, p.requests - base);
+        int32_t len = 0, add = 0, owned = 0, need = 0;
+        if (tid < n) {
+            const int32_t l = p.lens[base + tid], a = p.new_lens[base + tid], o = p.owned_in[base + tid];
+            len = clamp_i32(l, 0, cap);
+            add = clamp_i32(a, 0, cap - len);
+            owned = clamp_i32(o, 0, p.max_blocks);
+            if (len != l || add != (a < 0 ? 0 : a) || owned != o) flags |= kStatusKvSizes;
+            need = (int32_t)(((int64_t)len + add + p.page_size - 1) / p.page_size);
+        }
+        const int64_t grow = need > owned ? need - owned : 0;
+        const int64_t drop = p.trim && owned > need ? owned - need : 0;
+        int64_t a = add, b = grow, c = drop;  // inclusive sums
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, a, d), y = __shfl_up_sync(~0u, b, d), z = __shfl_up_sync(~0u, c, d);
+            if (lane >= d) a += x, b += y, c += z;
+        }
+        if (lane == 31) s_warp[0][warp] = a, s_warp[1][warp] = b, s_warp[2][warp] = c;
+        __syncthreads();
+        if (warp < 3) {
+            int64_t v = s_warp[warp][lane];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t x = __shfl_up_sync(~0u, v, d);
+                if (lane >= d) v += x;
+            }
+            s_warp[warp][lane] = v;
+        }
+        __syncthreads();
+        if (warp > 0) a += s_warp[0][warp - 1], b += s_warp[1][warp - 1], c += s_warp[2][warp - 1];
+        const int64_t tok_n = s_warp[0][31], grow_n = s_warp[1][31], drop_n = s_warp[2][31];
+        s_tok[tid] = tok0 + a - add;
+        s_grow[tid] = grow0 + b - grow;
+        s_drop[tid] = drop0 + c - drop;
+        s_len[tid] = len;
+        s_owned[tid] = owned;
+        s_need[tid] = need;
+        const int64_t left = avail - s_grow[tid];
+        const int32_t given = (int32_t)(grow < left ? grow : left > 0 ? left : 0);
+        if (given < grow) flags |= kStatusKvPages;
+        // every CTA has read its inputs of this chunk before any output of it
+        // is written (owned_out may be owned_in)
+        if (ranks > 1) cluster_sync();
+        else __syncthreads();
+        if (rank == 0 && tid < n) {
+            p.owned_out[base + tid] = owned + given - (int32_t)drop;
+            if (base + tid == 0) p.cu_new[0] = 0;
+            p.cu_new[base + tid + 1] = clamp_i32(s_tok[tid] + add, 0, 0x7FFFFFFF);
+        }
+        // tokens
+        const int64_t tok_end = min(tok0 + tok_n, (int64_t)p.tokens);
+        for (int64_t t = tok0 + first; t < tok_end; t += step) {
+            const int r = find_start(s_tok, n, t);
+            const int32_t pos = s_len[r] + (int32_t)(t - s_tok[r]);
+            const int32_t j = pos / p.page_size;
+            int32_t page = -1;
+            if (j < s_owned[r]) {
+                page = p.tables[(int64_t)(base + r) * p.table_stride + j];
+            } else {
+                const int64_t at = s_grow[r] + j - s_owned[r];
+                if (at < avail) page = p.ring[(uint64_t)(head + at) % (uint32_t)p.ring_size];
+            }
+            p.positions[t] = pos;
+            p.slots[t] = page < 0 ? -1 : (int64_t)page * p.page_size + (pos - j * p.page_size);
+        }
+        // pages taken (or missing) and pages given back
+        for (int64_t g = grow0 + first; g < grow0 + grow_n; g += step) {
+            const int r = find_start(s_grow, n, g);
+            const int64_t j = s_owned[r] + (g - s_grow[r]);
+            p.tables[(int64_t)(base + r) * p.table_stride + j] =
+                g < avail ? p.ring[(uint64_t)(head + g) % (uint32_t)p.ring_size] : -1;
+        }
+        for (int64_t g = drop0 + first; g < drop0 + drop_n; g += step) {
+            const int r = find_start(s_drop, n, g);
+            const int64_t j = s_need[r] + (g - s_drop[r]);
+            p.ring[(uint64_t)(tail + g) % (uint32_t)p.ring_size] = p.tables[(int64_t)(base + r) * p.table_stride + j];
+        }
+        tok0 += tok_n;
+        grow0 += grow_n;
+        drop0 += drop_n;
+        __syncthreads();  // the shared arrays are free for the next chunk
+    }
+    for (int64_t t = tok0 + first; t < p.tokens; t += step) {
+        p.positions[t] = 0;
+        p.slots[t] = -1;
+    }
+    if (tok0 > p.tokens) flags |= kStatusKvSizes;
+    if (rank == 0 && tid == 0) {
+        // (at least one request:) every CTA has passed a chunk's cluster barrier,
+        // so it has read the state
+        p.state_out[0] = head + (grow0 < avail ? grow0 : avail);
+        p.state_out[1] = tail + drop0;
+    }
+    if (flags && rank == 0) atomicOr(p.status, flags);
+}
+
+}  // namespace dev
+}  // namespace w12

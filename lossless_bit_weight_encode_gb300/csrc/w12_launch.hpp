@@ -71,6 +71,26 @@ int encoded_size_device(const uint16_t *w_dev, int64_t N, int64_t K, void *works
 int encode_device(const uint16_t *w_dev, int64_t N, int64_t K, void *blob_dev, size_t cap, void *workspace,
                   size_t ws_bytes, void *stream, std::string *err);
 
+// What the paged-cache launchers need of the current device and the options.
+struct DeviceView {
+    int device = 0, sm_count = 0;
+    uint32_t *status = nullptr;
+    bool pdl = true;
+    uint64_t timeout_ns = 0;
+};
+int device_view(DeviceView *out, std::string *err);
+
+// The driver's cuTensorMapEncodeTiled (null and *err where it is missing).
+void *tensor_map_encode(std::string *err);
+
+int kv_plan(const w12_kv_plan_args &a, void *stream, std::string *err);
+int kv_store(const w12_kv_cache &c, const w12_kv_store_args &a, void *stream, std::string *err);
+int kv_read(const w12_kv_cache &c, const int64_t *slots, int32_t tokens, uint16_t *k_out, uint16_t *v_out,
+            void *stream, std::string *err);
+int kv_attend_workspace_size(const w12_kv_cache &c, const w12_kv_attend_args &a, size_t *bytes, std::string *err);
+int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspace, size_t ws_bytes, void *stream,
+              std::string *err);
+
 int selftest_timeout(uint32_t timeout_us, void *stream, std::string *err);
 
 int set_option(const char *name, int64_t value, std::string *err);

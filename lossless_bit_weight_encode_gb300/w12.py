@@ -28,6 +28,7 @@ EXPORTED = (
     "w12_gemm", "w12_gemm_group_workspace_size", "w12_gemm_group", "w12_gemm_group_launch_info", "w12_gemm_argmax_workspace_size", "w12_gemm_argmax", "w12_gemm_noalloc", "w12_encode_workspace_size", "w12_encoded_size_device", "w12_encode_device",
     "w12_q8_encoded_size", "w12_q8_encode_host", "w12_q8_blob_info", "w12_q8_gemm_workspace_size", "w12_q8_gemm",
     "w12_q8_gemm_group_workspace_size", "w12_q8_gemm_group_launch_info", "w12_q8_gemm_group",
+    "w12_kv_plan", "w12_kv_store", "w12_kv_read", "w12_kv_attend_workspace_size", "w12_kv_attend",
     "w12_read_stream", "w12_check_status", "w12_selftest_timeout", "w12_set_option", "w12_get_option",
 )
 
@@ -63,6 +64,51 @@ class w12_q8_info(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+KV_BF16, KV_Q8 = 0, 1  # W12_KV_* in include/w12.h
+
+
+class w12_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p), ("scales_dev", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+    ]
+
+
+class w12_kv_plan_args(ctypes.Structure):
+    _fields_ = [
+        ("lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("owned_in", ctypes.c_void_p),
+        ("owned_out", ctypes.c_void_p), ("tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("ring", ctypes.c_void_p), ("ring_state_in", ctypes.c_void_p), ("ring_state_out", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("requests", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("ring_size", ctypes.c_int32), ("tokens", ctypes.c_int32), ("trim", ctypes.c_int32),
+    ]
+
+
+class w12_kv_store_args(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+        ("rope", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("rope_rows", ctypes.c_int64), ("tokens", ctypes.c_int32), ("heads", ctypes.c_int32), ("rot", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+    ]
+
+
+class w12_kv_attend_args(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64), ("tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("lens", ctypes.c_void_p), ("cu_new", ctypes.c_void_p), ("tree", ctypes.c_void_p),
+        ("requests", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("tokens", ctypes.c_int32),
+        ("heads", ctypes.c_int32), ("max_new", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
 
 
 _lib = None
@@ -111,6 +157,12 @@ def lib() -> ctypes.CDLL:
                                                 ctypes.POINTER(ctypes.c_int32)]
     L.w12_q8_gemm_group.argtypes = [vp, i32, ctypes.POINTER(vp), ctypes.POINTER(w12_q8_info), ctypes.POINTER(vp),
                                     i32, vp, sz, vp]
+    cache_p = ctypes.POINTER(w12_kv_cache)
+    L.w12_kv_plan.argtypes = [ctypes.POINTER(w12_kv_plan_args), vp]
+    L.w12_kv_store.argtypes = [cache_p, ctypes.POINTER(w12_kv_store_args), vp]
+    L.w12_kv_read.argtypes = [cache_p, vp, ctypes.c_int32, vp, vp, vp]
+    L.w12_kv_attend_workspace_size.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), ctypes.POINTER(sz)]
+    L.w12_kv_attend.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), vp, sz, vp]
     L.w12_read_stream.argtypes = [vp, sz, vp, ctypes.c_uint32, vp]
     L.w12_check_status.argtypes = [vp]
     L.w12_selftest_timeout.argtypes = [ctypes.c_uint32, vp]
@@ -379,6 +431,33 @@ def w12_q8_gemm_group(x_dev, blobs_dev, infos, ys_dev, M: int, workspace, stream
     _check(w12_q8_gemm_group_ptr(x_dev.data_ptr(), [b.data_ptr() for b in blobs_dev], infos,
                                  [y.data_ptr() for y in ys_dev], M, workspace.data_ptr(),
                                  workspace.numel() * workspace.element_size(), _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------- paged key-value cache
+# The argument structs hold raw pointers (include/w12.h); kv.py fills them from
+# tensors and keeps those alive.
+def w12_kv_plan(args: w12_kv_plan_args, stream=None) -> None:
+    _check(lib().w12_kv_plan(args, _stream_handle(stream)))
+
+
+def w12_kv_store(cache: w12_kv_cache, args: w12_kv_store_args, stream=None) -> None:
+    _check(lib().w12_kv_store(cache, args, _stream_handle(stream)))
+
+
+def w12_kv_read(cache: w12_kv_cache, slots_ptr: int, tokens: int, k_out_ptr: int, v_out_ptr: int,
+                stream=None) -> None:
+    _check(lib().w12_kv_read(cache, slots_ptr, tokens, k_out_ptr, v_out_ptr, _stream_handle(stream)))
+
+
+def w12_kv_attend_workspace_size(cache: w12_kv_cache, args: w12_kv_attend_args) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().w12_kv_attend_workspace_size(cache, args, ctypes.byref(out)))
+    return out.value
+
+
+def w12_kv_attend(cache: w12_kv_cache, args: w12_kv_attend_args, workspace_ptr: int, workspace_bytes: int,
+                  stream=None) -> None:
+    _check(lib().w12_kv_attend(cache, args, workspace_ptr, workspace_bytes, _stream_handle(stream)))
 
 
 def w12_read_stream_ptr(buf_ptr: int, nbytes: int, sink_ptr: int, never: int, stream_handle: int | None) -> int:
