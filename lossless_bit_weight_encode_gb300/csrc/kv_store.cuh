@@ -84,116 +84,131 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], bool any, bool norm, 
     }
 }
 
+// Cosines and sines of the lane's columns (pairs, when interleaved: four of each).
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rope_row(const float *row, int rot, int sub, float (&cs)[8], float (&sn)[8]) {
+    const int h2 = rot / 2;
+    if (INTERLEAVED) {
+        const int c = 4 * sub;
+        if (h2 % 4 == 0) {  // 16-byte aligned rows
+            if (c < h2) {
+                const float4 a = *reinterpret_cast<const float4 *>(row + c);
+                const float4 b = *reinterpret_cast<const float4 *>(row + h2 + c);
+                cs[0] = a.x, cs[1] = a.y, cs[2] = a.z, cs[3] = a.w;
+                sn[0] = b.x, sn[1] = b.y, sn[2] = b.z, sn[3] = b.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (c + i < h2) cs[i] = row[c + i], sn[i] = row[h2 + c + i];
+            }
+        }
+    } else if (8 * sub < rot) {
+        const int c = 8 * sub >= h2 ? 8 * sub - h2 : 8 * sub;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(row + c + i);
+            const float4 b = *reinterpret_cast<const float4 *>(row + h2 + c + i);
+            cs[i] = a.x, cs[i + 1] = a.y, cs[i + 2] = a.z, cs[i + 3] = a.w;
+            sn[i] = b.x, sn[i + 1] = b.y, sn[i + 2] = b.z, sn[i + 3] = b.w;
+        }
+    }
+}
+
 // One CTA handles the heads (q, then k, then v) of one token, or a share of
-// them where the tokens are few: lane groups take heads in turn and keep the
-// token's cosines and sines, so that the table is read once per group and not
-// once per head.
+// them where the tokens are few.  A lane group takes every GROUPS-th head, four
+// at a time: their loads are all in flight before the first is used, and the
+// token's cosines and sines are read once per group and not once per head.
 template <int D, bool Q8, bool INTERLEAVED>
-__global__ void __launch_bounds__(kStoreThreads) w12_kv_store_kernel(KvStoreParams p) {
-    constexpr int LANES = D / 8, GROUPS = kStoreThreads / LANES;
+__global__ void __launch_bounds__(kStoreThreads, 3) w12_kv_store_kernel(KvStoreParams p) {
+    constexpr int LANES = D / 8, GROUPS = kStoreThreads / LANES, U = 4;
     const int sub = threadIdx.x % LANES, group = blockIdx.x * GROUPS + threadIdx.x / LANES;
     const int stride = gridDim.x * GROUPS;
     const int heads = p.heads, hk = p.c.kv_heads, all = heads + 2 * hk;
     pdl_launch_dependents();
     pdl_wait();
-    float wq[8] = {}, wk[8] = {};
     const bool norm_q = p.q_norm != nullptr, norm_k = p.k_norm != nullptr;
-    if (norm_q) unpack8(reinterpret_cast<const uint4 *>(p.q_norm)[sub], wq);
-    if (norm_k) unpack8(reinterpret_cast<const uint4 *>(p.k_norm)[sub], wk);
     uint32_t flags = 0;
     for (int64_t t = blockIdx.y; t < p.tokens; t += gridDim.y) {
-        float cs[8], sn[8];
-        if (p.rot > 0) {
-            int64_t pos = p.positions[t];
-            if (pos < 0 || pos >= p.rope_rows) {
-                flags |= kStatusKvIndex;
-                pos = pos < 0 ? 0 : p.rope_rows - 1;
-            }
-            const float *row = p.rope + pos * p.rot;
-            const int h2 = p.rot / 2;
-            if (INTERLEAVED) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 4 * sub + i;
-                    cs[i] = c < h2 ? row[c] : 1.0f;
-                    sn[i] = c < h2 ? row[h2 + c] : 0.0f;
-                }
-            } else {
-                const int c = 8 * sub >= h2 ? 8 * sub - h2 : 8 * sub;
-                if (8 * sub < p.rot) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(row + c + i);
-                        const float4 b = *reinterpret_cast<const float4 *>(row + h2 + c + i);
-                        cs[i] = a.x, cs[i + 1] = a.y, cs[i + 2] = a.z, cs[i + 3] = a.w;
-                        sn[i] = b.x, sn[i + 1] = b.y, sn[i + 2] = b.z, sn[i + 3] = b.w;
-                    }
-                }
-            }
-        }
         const int64_t slot = p.slots[t];
-        const int64_t page = slot / p.c.page_size, off = slot - page * p.c.page_size;
-        const bool kept = slot >= 0 && page < p.c.num_pages;
-        if (slot >= 0 && !kept) flags |= kStatusKvIndex;
-        // the shuffles want whole warps: every group runs the same rounds
-        for (int j0 = 0; j0 < all; j0 += stride) {
-            if (j0 + (int)(blockIdx.x * GROUPS) >= all) break;  // uniform: no group of this CTA has a head left
-            const int j = j0 + group;
-            const bool live = j < all;
-            const bool is_q = j < heads, is_k = !is_q && j < heads + hk;
-            const int h = is_q ? j : is_k ? j - heads : j - heads - hk;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (live) {
-                const uint16_t *src = is_q   ? p.q + t * p.q_stride
-                                      : is_k ? p.k + t * p.k_stride
-                                             : p.v + t * p.v_stride;
-                u = reinterpret_cast<const uint4 *>(src + (int64_t)h * D)[sub];
-            }
-            float x[8];
-            unpack8(u, x);
-            {
-                float y[8];
+        int64_t pos = p.rot > 0 ? p.positions[t] : 0;
+        float cs[8] = {}, sn[8] = {};
+        // the shuffles want whole warps: every group of the CTA runs the same rounds
+        for (int j0 = blockIdx.x * GROUPS; j0 < all; j0 += U * stride) {
+            const int jg = j0 - blockIdx.x * GROUPS + group;
+            uint4 u[U];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = x[i];
-                float w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = is_q ? wq[i] : wk[i];
-                norm_rotate<D, INTERLEAVED>(y, norm_q || norm_k, is_q ? norm_q : norm_k, w, p.eps, p.rot, cs, sn,
-                                            sub);
-                if (is_q || is_k) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = y[i];
+            for (int r = 0; r < U; ++r) {
+                const int j = jg + r * stride;
+                u[r] = make_uint4(0, 0, 0, 0);
+                if (j < all) {
+                    const uint16_t *src = j < heads        ? p.q + t * p.q_stride + (int64_t)j * D
+                                          : j < heads + hk ? p.k + t * p.k_stride + (int64_t)(j - heads) * D
+                                                           : p.v + t * p.v_stride + (int64_t)(j - heads - hk) * D;
+                    u[r] = reinterpret_cast<const uint4 *>(src)[sub];
                 }
             }
-            if (is_q) {
-                reinterpret_cast<uint4 *>(p.q_out + t * p.q_out_stride + (int64_t)h * D)[sub] = pack8(x);
-            }
-            if (!Q8) {
-                if (live && !is_q && kept) {
-                    const int64_t e = page * p.c.page_stride + h * p.c.head_stride + off * p.c.row_stride + 8 * sub;
-                    reinterpret_cast<uint4 *>(is_k ? p.c.k : p.c.v)[e / 8] = is_k ? pack8(x) : u;
+            if (j0 == blockIdx.x * GROUPS && p.rot > 0) {
+                if (pos < 0 || pos >= p.rope_rows) {
+                    flags |= kStatusKvIndex;
+                    pos = pos < 0 ? 0 : p.rope_rows - 1;
                 }
-            } else {
-                float a = 0.0f;
+                rope_row<INTERLEAVED>(p.rope + pos * p.rot, p.rot, sub, cs, sn);
+            }
+            const int64_t page = slot / p.c.page_size, off = slot - page * p.c.page_size;
+            const bool kept = slot >= 0 && page < p.c.num_pages;
+            if (slot >= 0 && !kept) flags |= kStatusKvIndex;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(x[i]));
+            for (int r = 0; r < U; ++r) {
+                const int j = jg + r * stride;
+                if (j0 + r * stride >= all) break;  // the same for the whole CTA
+                const bool is_q = j < heads, is_v = j >= heads + hk;
+                const bool is_k = !is_q && !is_v;
+                const int h = is_q ? j : is_k ? j - heads : j - heads - hk;
+                float x[8];
+                unpack8(u[r], x);
+                // a warp of values alone has nothing to norm or rotate
+                if (__any_sync(~0u, !is_v)) {
+                    float y[8], w[8] = {};
+                    if (is_q ? norm_q : norm_k && is_k)
+                        unpack8(reinterpret_cast<const uint4 *>(is_q ? p.q_norm : p.k_norm)[sub], w);
 #pragma unroll
-                for (int d = LANES / 2; d > 0; d >>= 1) a = max_nan(a, __shfl_xor_sync(~0u, a, d));
-                const float s = a / 127.0f;
-                if (live && !is_q && kept) {
-                    // a scale that is NaN or infinite keeps q = 0: the row reads back
-                    // as NaN
-                    const bool usual = s > 0.0f && s < INFINITY;
-                    uint32_t b[2] = {0, 0};
+                    for (int i = 0; i < 8; ++i) y[i] = x[i];
+                    norm_rotate<D, INTERLEAVED>(y, norm_q || norm_k, is_q ? norm_q : norm_k, w, p.eps, p.rot, cs, sn,
+                                                sub);
+                    if (!is_v) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float r = usual ? fminf(fmaxf(rintf(x[i] / s), -127.0f), 127.0f) : 0.0f;
-                        b[i / 4] |= ((uint32_t)(int)r & 0xFFu) << (8 * (i % 4));
+                        for (int i = 0; i < 8; ++i) x[i] = y[i];
                     }
-                    const int64_t e = page * p.c.page_stride + h * p.c.head_stride + off * p.c.row_stride + 8 * sub;
-                    reinterpret_cast<uint2 *>(is_k ? p.c.k : p.c.v)[e / 8] = make_uint2(b[0], b[1]);
-                    if (sub == 0)
-                        p.c.scales[((page * hk + h) * p.c.page_size + off) * 2 + (is_k ? 0 : 1)] = s;
+                }
+                if (is_q) {
+                    reinterpret_cast<uint4 *>(p.q_out + t * p.q_out_stride + (int64_t)h * D)[sub] = pack8(x);
+                }
+                const bool write = j < all && !is_q && kept;
+                const int64_t e = page * p.c.page_stride + h * p.c.head_stride + off * p.c.row_stride + 8 * sub;
+                if (!Q8) {
+                    if (write) reinterpret_cast<uint4 *>(is_k ? p.c.k : p.c.v)[e / 8] = is_k ? pack8(x) : u[r];
+                } else if (__any_sync(~0u, !is_q)) {
+                    float a = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(x[i]));
+#pragma unroll
+                    for (int d = LANES / 2; d > 0; d >>= 1) a = max_nan(a, __shfl_xor_sync(~0u, a, d));
+                    const float s = a / 127.0f;
+                    if (write) {
+                        // a scale that is NaN or infinite keeps q = 0: the row
+                        // reads back as NaN
+                        const bool usual = s > 0.0f && s < INFINITY;
+                        uint32_t b[2] = {0, 0};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float r8 = usual ? fminf(fmaxf(rintf(x[i] / s), -127.0f), 127.0f) : 0.0f;
+                            b[i / 4] |= ((uint32_t)(int)r8 & 0xFFu) << (8 * (i % 4));
+                        }
+                        reinterpret_cast<uint2 *>(is_k ? p.c.k : p.c.v)[e / 8] = make_uint2(b[0], b[1]);
+                        if (sub == 0)
+                            p.c.scales[((page * hk + h) * p.c.page_size + off) * 2 + (is_k ? 0 : 1)] = s;
+                    }
                 }
             }
         }

@@ -23,27 +23,29 @@ _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float3
 _workspaces = {}  # (device, stream handle) -> zeroed workspace of the attend calls on that stream
 
 
-class _on:
-    """The device and stream a call runs on: outputs are allocated for that
-    stream.  ``stream`` as in w12.py: None (the current one), a torch stream or
-    a handle."""
+_current_device = torch.cuda.current_device
+# handle of a device's current stream, without the stream object around it
+_current_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, tensor, stream):
-        self.device = tensor.device.index
-        self.stream = stream
-        self.guards = ()
+
+class _on:
+    """The device and stream of a call that is not for the current ones: outputs
+    are allocated for that stream.  ``stream`` as in w12.py: None (the current
+    one), a torch stream or a handle."""
+
+    def __init__(self, index, stream):
+        self.index, self.stream, self.guards = index, stream, ()
 
     def __enter__(self):
-        if self.device != torch.cuda.current_device():
-            self.guards = (torch.cuda.device(self.device),)
-        if self.stream is not None:
-            s = self.stream
+        self.guards = (torch.cuda.device(self.index),)
+        s = self.stream
+        if s is not None:
             if isinstance(s, int):
-                s = torch.cuda.ExternalStream(s, device=self.device) if s else torch.cuda.default_stream(self.device)
+                s = torch.cuda.ExternalStream(s, device=self.index) if s else torch.cuda.default_stream(self.index)
             self.guards += (torch.cuda.stream(s),)
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return _current_stream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -56,26 +58,28 @@ def _need(ok, text):
         raise ValueError(text)
 
 
-def _ints(t, dtype, name, device):
-    """Pointer of a contiguous 1-D integer tensor."""
-    if t.dtype != dtype or t.dim() != 1 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor on {device}")
+def _ints(t, dtype, name, index):
+    """Pointer of a contiguous 1-D integer tensor on CUDA device `index`."""
+    if t.dtype is not dtype or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor on CUDA device {index}")
     return t.data_ptr()
 
 
-def _rows(t, dim, name, device, heads=None):
-    """(pointer, token stride, heads) of [T, heads * dim] or [T, heads, dim]
-    BF16 rows whose heads lie one after the other."""
+def _rows(t, dim, name, index, heads=None):
+    """(pointer, token stride, tokens, heads) of [T, heads * dim] or
+    [T, heads, dim] BF16 rows whose heads lie one after the other."""
     shape, stride = t.shape, t.stride()
+    n = 0
     if len(shape) == 2:
-        ok, n = stride[1] == 1 and shape[1] % dim == 0, shape[1] // dim
-    else:
-        ok = len(shape) == 3 and shape[2] == dim and stride[2] == 1 and (stride[1] == dim or shape[1] == 1)
-        n = shape[1] if ok else 0
-    if not ok or t.dtype != _BF16 or t.device != device or n < 1 or (heads is not None and n != heads):
-        raise ValueError(f"{name} must be BF16 [tokens, {heads or 'heads'} * {dim}] on {device} with contiguous heads")
+        if stride[1] == 1 and shape[1] % dim == 0:
+            n = shape[1] // dim
+    elif len(shape) == 3 and shape[2] == dim and stride[2] == 1 and (stride[1] == dim or shape[1] == 1):
+        n = shape[1]
+    if n < 1 or t.dtype is not _BF16 or t.get_device() != index or (heads is not None and n != heads):
+        raise ValueError(f"{name} must be BF16 [tokens, {heads or 'heads'} * {dim}] on CUDA device {index} with "
+                         "contiguous heads")
     # one row has no stride that matters
-    return t.data_ptr(), stride[0] if shape[0] > 1 else n * dim, n
+    return t.data_ptr(), stride[0] if shape[0] > 1 else n * dim, shape[0], n
 
 
 class KVStep:
@@ -87,10 +91,31 @@ class KVStep:
     ``max_new``: the most new tokens of a request, as far as is known.  What a
     call does not use may be None."""
 
+    _kinds = {"lens": _I32, "cu_new": _I32, "positions": _I32, "slots": _I64, "tree": _I32}
+
     def __init__(self, tables=None, lens=None, cu_new=None, positions=None, slots=None, max_new=1, tree=None):
         self.tables, self.lens, self.cu_new = tables, lens, cu_new
         self.positions, self.slots = positions, slots
         self.max_new, self.tree = int(max_new), tree
+
+    def __setattr__(self, name, value):
+        # checked here, once, and not in every call of every layer
+        if value is not None and name in self._kinds:
+            _ints(value, self._kinds[name], name, value.get_device() if value.is_cuda else "of its own")
+        elif value is not None and name == "tables":
+            _need(value.dtype is _I32 and value.dim() == 2 and value.stride(1) == 1 and value.is_cuda,
+                  "tables must be an int32 CUDA tensor [requests, max_blocks] with contiguous rows")
+        object.__setattr__(self, name, value)
+
+    def _on(self, index, *names):
+        """Pointers of the named arrays, all on CUDA device `index`."""
+        out = []
+        for name in names:
+            t = getattr(self, name)
+            if t is None or t.get_device() != index:
+                raise ValueError(f"step.{name} is missing or not on CUDA device {index}")
+            out.append(t.data_ptr())
+        return out
 
 
 class KVPages:
@@ -102,12 +127,12 @@ class KVPages:
     {head, tail}.  ``KVPages.create`` starts with every page free."""
 
     def __init__(self, tables, owned, ring, ring_state, page_size):
-        dev = tables.device
-        _need(tables.dtype == _I32 and tables.dim() == 2 and tables.stride(1) == 1 and tables.is_cuda,
+        _need(tables.dtype is _I32 and tables.dim() == 2 and tables.stride(1) == 1 and tables.is_cuda,
               "tables must be an int32 CUDA tensor [requests, max_blocks] with contiguous rows")
-        _ints(owned, _I32, "owned", dev)
-        _ints(ring, _I32, "ring", dev)
-        _ints(ring_state, _I64, "ring_state", dev)
+        self._index = tables.get_device()
+        _ints(owned, _I32, "owned", self._index)
+        _ints(ring, _I32, "ring", self._index)
+        _ints(ring_state, _I64, "ring_state", self._index)
         _need(owned.numel() == tables.shape[0] and ring.numel() >= 1 and ring_state.numel() == 2,
               "owned must have an entry per request, ring at least one and ring_state two")
         self.tables, self.owned, self.ring, self.ring_state = tables, owned, ring, ring_state
@@ -135,24 +160,35 @@ class KVPages:
         unless outputs are given.  ``step`` refers to ``lens``, which must stay as
         it is until the step's attend calls have run.  A ring that runs out is
         reported by w12_check_status."""
-        tables, dev = self.tables, self.tables.device
-        n = tables.shape[0]
+        if stream is None and _current_device() == self._index:
+            return self._plan(lens, new_lens, step, trim, owned_out, ring_state_out, _current_stream(self._index))
+        with _on(self._index, stream) as st:
+            return self._plan(lens, new_lens, step, trim, owned_out, ring_state_out, st)
+
+    def _plan(self, lens, new_lens, step, trim, owned_out, ring_state_out, st):
+        tables, index = self.tables, self._index
+        n, blocks = tables.shape
+        if step.lens is not lens:
+            step.lens = lens
+        if step.tables is not tables:
+            step.tables = tables
+        lens_p, cu_p, pos_p, slots_p = step._on(index, "lens", "cu_new", "positions", "slots")
+        tokens = step.slots.numel()
         _need(lens.numel() == n and new_lens.numel() == n, "lens and new_lens must have an entry per request")
-        owned_out = self.owned if owned_out is None else owned_out
-        ring_state_out = self.ring_state if ring_state_out is None else ring_state_out
-        _need(owned_out.numel() == n and ring_state_out.numel() == 2, "owned_out or ring_state_out has another size")
-        _need(step.cu_new.numel() == n + 1 and step.positions.numel() == step.slots.numel(),
+        _need(step.cu_new.numel() == n + 1 and step.positions.numel() == tokens,
               "step belongs to another number of requests")
-        args = w12.w12_kv_plan_args(
-            _ints(lens, _I32, "lens", dev), _ints(new_lens, _I32, "new_lens", dev), self.owned.data_ptr(),
-            _ints(owned_out, _I32, "owned_out", dev), tables.data_ptr(), tables.stride(0) if n > 1 else tables.shape[1], self.ring.data_ptr(),
-            self.ring_state.data_ptr(), _ints(ring_state_out, _I64, "ring_state_out", dev),
-            _ints(step.cu_new, _I32, "cu_new", dev), _ints(step.positions, _I32, "positions", dev),
-            _ints(step.slots, _I64, "slots", dev), n, tables.shape[1], self.page_size, self.ring.numel(),
-            step.slots.numel(), 1 if trim else 0)
-        with _on(tables, stream) as st:
-            w12.w12_kv_plan(args, st)
-        step.tables, step.lens = tables, lens
+        owned_p, state_p = self.owned.data_ptr(), self.ring_state.data_ptr()
+        owned_o, state_o = owned_p, state_p
+        if owned_out is not None:
+            owned_o = _ints(owned_out, _I32, "owned_out", index)
+            _need(owned_out.numel() == n, "owned_out must have an entry per request")
+        if ring_state_out is not None:
+            state_o = _ints(ring_state_out, _I64, "ring_state_out", index)
+            _need(ring_state_out.numel() == 2, "ring_state_out must have two entries")
+        w12.w12_kv_plan(w12.w12_kv_plan_args(
+            lens_p, _ints(new_lens, _I32, "new_lens", index), owned_p, owned_o, tables.data_ptr(),
+            tables.stride(0) if n > 1 else blocks, self.ring.data_ptr(), state_p, state_o, cu_p, pos_p, slots_p, n,
+            blocks, self.page_size, self.ring.numel(), tokens, 1 if trim else 0), st)
         return step
 
 
@@ -173,6 +209,7 @@ class KVCache:
             _need(scales.shape == (pages, heads, page, 2) and scales.dtype == _F32 and scales.is_contiguous()
                   and scales.device == k.device, "scales must be contiguous fp32 [num_pages, kv_heads, page_size, 2]")
         self.k, self.v, self.scales, self.device = k, v, scales, k.device
+        self._index = k.get_device()
         self.kv_heads, self.page_size, self.head_dim = heads, page, dim
         # a dimension of one element has no stride that matters
         stride = [s if n > 1 else dim for n, s in zip(k.shape, k.stride())]
@@ -195,55 +232,70 @@ class KVCache:
               stream=None):
         """Norm (``q_norm``, ``k_norm``: BF16 [head_dim]) and rotation (``rope``:
         fp32 [positions, rot], cosines then sines) of q and k, k and v into the
-        cache at step.slots.  Returns the new q (``out``, which may be q); q None:
-        only k and v."""
-        dim, dev = self.head_dim, self.device
-        kp, ks, _ = _rows(k, dim, "k", dev, self.kv_heads)
-        vp, vs, _ = _rows(v, dim, "v", dev, self.kv_heads)
-        tokens = k.shape[0]
-        _need(v.shape[0] == tokens and step.slots.numel() == tokens, "k, v and step.slots must have as many tokens")
-        qp = qs = op = os_ = heads = 0
-        rot = rows = rp = pp = 0
+        cache at step.slots.  Returns the new q, [tokens, heads, head_dim] (of
+        ``out``, which may be q); q None: only k and v."""
+        if stream is None and _current_device() == self._index:
+            return self._store(q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out, _current_stream(self._index))
+        with _on(self._index, stream) as st:
+            return self._store(q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out, st)
+
+    def _store(self, q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out, st):
+        dim, index = self.head_dim, self._index
+        kp, ks, tokens, _ = _rows(k, dim, "k", index, self.kv_heads)
+        vp, vs, nv, _ = _rows(v, dim, "v", index, self.kv_heads)
+        slots_p, = step._on(index, "slots")
+        _need(nv == tokens and step.slots.numel() == tokens, "k, v and step.slots must have as many tokens")
+        qp = qs = op = os_ = heads = rot = rows = rp = pp = 0
         if rope is not None:
-            _need(rope.dtype == _F32 and rope.dim() == 2 and rope.is_contiguous() and rope.device == dev,
+            _need(rope.dtype is _F32 and rope.dim() == 2 and rope.is_contiguous() and rope.get_device() == index,
                   "rope must be a contiguous fp32 tensor [positions, rot]")
-            _need(step.positions is not None and step.positions.numel() == tokens, "step.positions must have as many tokens")
+            pp, = step._on(index, "positions")
+            _need(step.positions.numel() == tokens, "step.positions must have as many tokens")
             rows, rot = rope.shape
-            rp, pp = rope.data_ptr(), _ints(step.positions, _I32, "step.positions", dev)
-        for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if t is not None:
-                _need(t.dtype == _BF16 and t.shape == (dim,) and t.is_contiguous() and t.device == dev,
-                      f"{name} must be BF16 [{dim}]")
-        sp = _ints(step.slots, _I64, "step.slots", dev)
-        with _on(k, stream) as st:
-            if q is not None:
-                qp, qs, heads = _rows(q, dim, "q", dev)
-                _need(q.shape[0] == tokens, "q and k must have as many tokens")
-                if out is None:
-                    out = torch.empty(q.shape, dtype=_BF16, device=dev)
-                op, os_, n = _rows(out, dim, "out", dev, heads)
-                _need(out.shape[0] == tokens, "out and q must have as many tokens")
-            w12.w12_kv_store(self._c, w12.w12_kv_store_args(
-                qp, kp, vp, op, qs, ks, vs, os_, None if q_norm is None else q_norm.data_ptr(),
-                None if k_norm is None else k_norm.data_ptr(), rp, pp, sp, rows, tokens, heads, rot,
-                1 if interleaved else 0, eps), st)
-        return out if q is not None else None
+            rp = rope.data_ptr()
+        wq = wk = 0
+        if q_norm is not None:
+            wq = self._weight(q_norm, "q_norm")
+        if k_norm is not None:
+            wk = self._weight(k_norm, "k_norm")
+        if q is not None:
+            qp, qs, nq, heads = _rows(q, dim, "q", index)
+            if out is None:
+                out = torch.empty(q.shape, dtype=_BF16, device=self.device)
+            op, os_, no, _ = _rows(out, dim, "out", index, heads)
+            _need(nq == tokens and no == tokens, "q, out and k must have as many tokens")
+        w12.w12_kv_store(self._c, w12.w12_kv_store_args(qp, kp, vp, op, qs, ks, vs, os_, wq, wk, rp, pp, slots_p, rows,
+                                                        tokens, heads, rot, 1 if interleaved else 0, eps), st)
+        return out.view(tokens, heads, dim) if q is not None else None
+
+    def _weight(self, w, name):
+        if w.dtype is not _BF16 or w.dim() != 1 or w.numel() != self.head_dim or not w.is_contiguous() \
+                or w.get_device() != self._index:
+            raise ValueError(f"{name} must be contiguous BF16 [{self.head_dim}] on CUDA device {self._index}")
+        return w.data_ptr()
 
     def read(self, slots, out=None, stream=None):
         """(k, v) BF16 [tokens, kv_heads, head_dim] of the cached rows at ``slots``
         (int64; zeros for -1).  ``out``: a pair to write to."""
-        shape = (slots.numel(), self.kv_heads, self.head_dim)
-        sp = _ints(slots, _I64, "slots", self.device)
-        with _on(slots, stream) as st:
-            if out is None:
-                out = (torch.empty(shape, dtype=_BF16, device=self.device),
-                       torch.empty(shape, dtype=_BF16, device=self.device))
+        if stream is None and _current_device() == self._index:
+            return self._read(slots, out, _current_stream(self._index))
+        with _on(self._index, stream) as st:
+            return self._read(slots, out, st)
+
+    def _read(self, slots, out, st):
+        sp, tokens = _ints(slots, _I64, "slots", self._index), slots.numel()
+        shape = (tokens, self.kv_heads, self.head_dim)
+        if out is None:
+            k = torch.empty(shape, dtype=_BF16, device=self.device)
+            v = torch.empty(shape, dtype=_BF16, device=self.device)
+        else:
+            k, v = out
             for t in out:
-                _need(t.shape == shape and t.dtype == _BF16 and t.is_contiguous() and t.device == self.device,
+                _need(t.shape == shape and t.dtype is _BF16 and t.is_contiguous() and t.get_device() == self._index,
                       "out must be two contiguous BF16 tensors [tokens, kv_heads, head_dim]")
-            if shape[0]:
-                w12.w12_kv_read(self._c, sp, shape[0], out[0].data_ptr(), out[1].data_ptr(), st)
-        return out
+        if tokens:
+            w12.w12_kv_read(self._c, sp, tokens, k.data_ptr(), v.data_ptr(), st)
+        return k, v
 
     def workspace(self, args, st):
         """The zeroed workspace of the attend calls on stream ``st`` (shared by
@@ -252,13 +304,13 @@ class KVCache:
         size = self._ws_bytes.get(key)
         if size is None:
             size = self._ws_bytes[key] = w12.w12_kv_attend_workspace_size(self._c, args)
-        ws = _workspaces.get((self.device.index, st))
+        ws = _workspaces.get((self._index, st))
         if ws is None or ws.numel() < size:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("the workspace of this stream is not large enough yet: make one ordinary call of "
                                    "this size on the stream before capturing, or pass workspace=")
             ws = torch.zeros((size + (1 << 20) - 1) >> 20 << 20, dtype=torch.uint8, device=self.device)
-            _workspaces[(self.device.index, st)] = ws
+            _workspaces[(self._index, st)] = ws
         return ws
 
     def attend(self, q, step, scale=None, window=0, out=None, lse=None, workspace=None, stream=None):
@@ -269,32 +321,35 @@ class KVCache:
         stream share a workspace; ``workspace`` (uint8, zero-filled before its
         first use) takes its place, as a captured graph needs that is replayed
         beside other calls."""
-        dim, dev = self.head_dim, self.device
-        qp, qs, heads = _rows(q, dim, "q", dev)
-        tables, lens, tokens = step.tables, step.lens, q.shape[0]
-        _need(tables.dtype == _I32 and tables.dim() == 2 and tables.stride(1) == 1 and tables.device == dev,
-              "step.tables must be int32 [requests, max_blocks] with contiguous rows")
-        n = lens.numel()
-        _need(tables.shape[0] == n and step.cu_new.numel() == n + 1, "step.tables, lens and cu_new do not agree")
-        tp = lp = 0
+        if stream is None and _current_device() == self._index:
+            return self._attend(q, step, scale, window, out, lse, workspace, _current_stream(self._index))
+        with _on(self._index, stream) as st:
+            return self._attend(q, step, scale, window, out, lse, workspace, st)
+
+    def _attend(self, q, step, scale, window, out, lse, workspace, st):
+        dim, index = self.head_dim, self._index
+        qp, qs, tokens, heads = _rows(q, dim, "q", index)
+        tables_p, lens_p, cu_p = step._on(index, "tables", "lens", "cu_new")
+        rows, blocks = step.tables.shape
+        n = step.lens.numel()
+        _need(rows == n and step.cu_new.numel() == n + 1, "step.tables, lens and cu_new do not agree")
+        tree_p = lse_p = 0
         if step.tree is not None:
-            tp = _ints(step.tree, _I32, "step.tree", dev)
+            tree_p, = step._on(index, "tree")
             _need(step.tree.numel() >= tokens, "step.tree must have a mask per token")
         if lse is not None:
-            _need(lse.dtype == _F32 and lse.shape == (tokens, heads) and lse.is_contiguous() and lse.device == dev,
-                  "lse must be contiguous fp32 [tokens, heads]")
-            lp = lse.data_ptr()
-        with _on(q, stream) as st:
-            if out is None:
-                out = torch.empty(q.shape, dtype=_BF16, device=dev)
-            op, os_, _ = _rows(out, dim, "out", dev, heads)
-            _need(out.shape[0] == tokens, "out and q must have as many tokens")
-            if tokens == 0:
-                return out
-            args = w12.w12_kv_attend_args(
-                qp, op, lp, qs, os_, tables.data_ptr(), tables.stride(0) if n > 1 else tables.shape[1],
-                _ints(lens, _I32, "step.lens", dev), _ints(step.cu_new, _I32, "step.cu_new", dev), tp, n,
-                tables.shape[1], tokens, heads, step.max_new, window, dim ** -0.5 if scale is None else scale)
-            ws = self.workspace(args, st) if workspace is None else workspace
-            w12.w12_kv_attend(self._c, args, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+            _need(lse.dtype is _F32 and lse.shape == (tokens, heads) and lse.is_contiguous() and
+                  lse.get_device() == index, "lse must be contiguous fp32 [tokens, heads]")
+            lse_p = lse.data_ptr()
+        if out is None:
+            out = torch.empty(q.shape, dtype=_BF16, device=self.device)
+        op, os_, no, _ = _rows(out, dim, "out", index, heads)
+        _need(no == tokens, "out and q must have as many tokens")
+        if tokens == 0:
+            return out
+        args = w12.w12_kv_attend_args(
+            qp, op, lse_p, qs, os_, tables_p, step.tables.stride(0) if n > 1 else blocks, lens_p, cu_p, tree_p, n,
+            blocks, tokens, heads, step.max_new, window, dim ** -0.5 if scale is None else scale)
+        ws = self.workspace(args, st) if workspace is None else workspace
+        w12.w12_kv_attend(self._c, args, ws.data_ptr(), ws.numel() * ws.element_size(), st)
         return out

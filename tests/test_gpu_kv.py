@@ -266,7 +266,7 @@ def test_store_in_place_and_without_q():
     want = cache.store(q, k, v, step, q_norm=w, rope=rope)  # a norm of q alone
     kept = cache.k.clone()
     got = cache.store(q, k, v, step, q_norm=w, rope=rope, out=q)
-    assert got is q and torch.equal(got, want)
+    assert got.data_ptr() == q.data_ptr() and got.shape == (3, 4, 64) and torch.equal(got, want)
     cache.k.zero_()
     assert cache.store(None, k, v, step, rope=rope) is None
     assert torch.equal(cache.k, kept)
