@@ -32,6 +32,7 @@ dev::KvGeom geometry(const w12_kv_cache &c) {
     g.page_stride = c.page_stride;
     g.head_stride = c.head_stride;
     g.row_stride = c.row_stride;
+    g.page_inv = ~uint64_t(0) / (uint64_t)c.page_size;
     g.page_size = c.page_size;
     g.kv_heads = c.kv_heads;
     return g;
@@ -171,8 +172,9 @@ int kv_store(const w12_kv_cache &c, const w12_kv_store_args &a, void *stream, st
     p.rot = a.rot;
     p.eps = a.eps;
     p.status = d.status;
-    const int all = a.heads + 2 * c.kv_heads, groups = dev::kStoreThreads / (c.head_dim / 8);
-    // few tokens: a lane group per head; many: as few CTAs per token as fill the device
+    const int per = 256 / c.head_dim, groups = dev::kStoreThreads / 32;  // heads of a warp's round, warps
+    const int all = (a.heads + per - 1) / per + 2 * ((c.kv_heads + per - 1) / per);
+    // few tokens: a warp per round; many: as few CTAs per token as fill the device
     const int want = (all + groups - 1) / groups;
     const int64_t fill = (int64_t)d.sm_count * 8;
     const int gx = (int)std::max<int64_t>(1, std::min<int64_t>(want, fill / a.tokens));
@@ -198,9 +200,10 @@ int kv_read(const w12_kv_cache &c, const int64_t *slots, int32_t tokens, uint16_
     p.v_out = v_out;
     p.tokens = tokens;
     p.status = d.status;
-    const int64_t threads = (int64_t)tokens * c.kv_heads * (c.head_dim / 8);
-    const int grid = (int)std::min<int64_t>((threads + dev::kStoreThreads - 1) / dev::kStoreThreads,
-                                            (int64_t)d.sm_count * 16);
+    const int per = 256 / c.head_dim, rounds = (c.kv_heads + per - 1) / per, warps = dev::kStoreThreads / 32;
+    p.rounds_inv = ~uint64_t(0) / (uint64_t)rounds;
+    const int64_t items = (int64_t)tokens * rounds;
+    const int grid = (int)std::min<int64_t>((items + warps - 1) / warps, (int64_t)d.sm_count * 32);
     const bool q8 = c.dtype == W12_KV_Q8;
     const cudaError_t e = c.head_dim == 64    ? read_dim<64>(d, q8, grid, p, stream)
                           : c.head_dim == 128 ? read_dim<128>(d, q8, grid, p, stream)

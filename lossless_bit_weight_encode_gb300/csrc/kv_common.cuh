@@ -17,6 +17,7 @@ struct KvGeom {
     float *scales;
     int64_t num_pages;
     int64_t page_stride, head_stride, row_stride;  // elements
+    uint64_t page_inv;                             // floor((2^64 - 1) / page_size)
     int32_t page_size, kv_heads;
 };
 
@@ -55,6 +56,7 @@ struct KvReadParams {
     KvGeom c;
     const int64_t *slots;
     uint16_t *k_out, *v_out;
+    uint64_t rounds_inv;  // floor((2^64 - 1) / warp rounds per token)
     int32_t tokens;
     uint32_t *status;
 };
