@@ -90,11 +90,29 @@ int attend_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_
 // [pages][kv_heads][page_size][head_dim] as (16-byte-chunked row, token, 128-byte
 // block of the row, head, page): a box is 16 tokens of one head, its 128-byte
 // blocks one after the other, each swizzled for ldmatrix.
-int cache_map(const w12_kv_cache &c, const void *base, CUtensorMap *tm, std::string *err) {
+// The tcgen05 kernel (`tc`) takes its boxes as [pages][kv_heads][page_size][head_dim]:
+// 16 tokens x 64 BF16 columns, swizzled as its operands are, or 16 tokens x all
+// columns in bytes.
+int cache_map(const w12_kv_cache &c, bool tc, const void *base, CUtensorMap *tm, std::string *err) {
     auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode(err));
     if (!encode) return W12_ERR_CUDA;
     const bool q8 = c.dtype == W12_KV_Q8;
     const cuuint64_t elem = q8 ? 1 : 2;
+    if (tc) {
+        const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
+                                    (cuuint64_t)c.num_pages};
+        const cuuint64_t strides[3] = {(cuuint64_t)c.row_stride * elem, (cuuint64_t)c.head_stride * elem,
+                                       (cuuint64_t)c.page_stride * elem};
+        const cuuint32_t box[4] = {q8 ? (cuuint32_t)c.head_dim : 64u, (cuuint32_t)dev::kAttendSlice, 1, 1};
+        const cuuint32_t unit[4] = {1, 1, 1, 1};
+        const CUresult r = encode(tm, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                                  const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r == CUDA_SUCCESS) return W12_OK;
+        *err = "cuTensorMapEncodeTiled failed for the cache (code " + std::to_string((int)r) + ")";
+        return W12_ERR_CUDA;
+    }
     const cuuint64_t row = std::min<cuuint64_t>(128, c.head_dim * elem);
     const cuuint64_t dims[5] = {row / elem, (cuuint64_t)c.page_size, (cuuint64_t)c.head_dim * elem / row,
                                 (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
@@ -235,8 +253,9 @@ int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspac
         return W12_ERR_BUFFER_TOO_SMALL;
     }
     CUtensorMap tm_k, tm_v;
-    rc = cache_map(c, c.k_dev, &tm_k, err);
-    if (rc == W12_OK) rc = cache_map(c, c.v_dev, &tm_v, err);
+    const bool tc = plan.rows == dev::kTcRows;
+    rc = cache_map(c, tc, c.k_dev, &tm_k, err);
+    if (rc == W12_OK) rc = cache_map(c, tc, c.v_dev, &tm_v, err);
     if (rc != W12_OK) return rc;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     dev::KvAttendParams p;
@@ -250,6 +269,10 @@ int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspac
     p.lens = a.lens;
     p.cu_new = a.cu_new;
     p.tree = a.tree;
+    p.v = static_cast<const uint16_t *>(c.v_dev);
+    p.v_page_stride = c.page_stride;
+    p.v_head_stride = c.head_stride;
+    p.v_row_stride = c.row_stride;
     p.scales = c.scales_dev;
     p.num_pages = c.num_pages;
     p.requests = a.requests;

@@ -71,12 +71,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -224,6 +218,10 @@ struct KvRowView {
     uint32_t tree;
 };
 
+__device__ __forceinline__ int32_t kv_index(const KvRequest &r, int32_t i) {
+    return (int32_t)min((int64_t)r.past + i, (int64_t)0x7FFFFFFF);
+}
+
 __device__ __forceinline__ bool kv_sees(const KvAttendParams &p, const KvRequest &r, const KvRowView &v, int32_t key) {
     bool s = key < r.kv;
     if (p.tree) {
@@ -233,6 +231,65 @@ __device__ __forceinline__ bool kv_sees(const KvAttendParams &p, const KvRequest
         s = s && key <= v.index;
     }
     return s && (p.window <= 0 || key > v.index - p.window);
+}
+
+// Row lr of a piece: out = acc / sum (four columns from col on) and, with the
+// first of them, lse.
+template <int ROWS, int D>
+__device__ __forceinline__ void kv_emit(const KvAttendParams &p, const KvRequest &r, const KvPiece &c, int lr, int col,
+                                        float mm, float sum, const float4 &acc) {
+    const int32_t rr = c.rb * ROWS + lr, i = rr / p.group, tok = r.q0 + i, h = c.head * p.group + rr - i * p.group;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint2 b;
+    b.x = pack_bf16(acc.x * inv, acc.y * inv);
+    b.y = pack_bf16(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (int64_t)h * D + col) = b;
+    if (p.lse && col == 0)
+        p.lse[(int64_t)tok * (p.group * p.kv_heads) + h] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+}
+
+// The row block's parts come together: called by the 128 consumer threads when
+// they have written the CTA's part to its slot.  The last CTA to arrive joins the
+// parts in range order.
+template <int ROWS, int D>
+__device__ __forceinline__ void kv_join(const KvAttendParams &p, const KvWalk &w, const KvRequest &r, const KvPiece &c,
+                                        int32_t nrows, volatile uint32_t *last_flag) {
+    const int64_t s0 = w.u - c.ja;  // the row block's first unit
+    const int32_t c0 = (int32_t)(((s0 + 1) * w.ctas - 1) / w.total);
+    const int32_t c1 = (int32_t)(((s0 + r.ntiles) * w.ctas - 1) / w.total);
+    const int64_t ci = c.head + (int64_t)p.kv_heads * (w.b + (int64_t)r.q0 * p.group / ROWS + c.rb);
+    const bool counted = ci < p.n_counters;  // false only for a cu_new that is not a prefix sum
+    __threadfence();
+    consumers_sync();
+    if (threadIdx.x == 0) {
+        uint32_t is_last = 0;
+        if (counted) is_last = atomicAdd(&p.counters[ci], 1u) == (uint32_t)(c1 - c0);
+        else atomicOr(p.status, kStatusKvSizes);
+        *last_flag = is_last;
+    }
+    consumers_sync();
+    if (!*last_flag) return;
+    __threadfence();
+    for (int i = threadIdx.x; i < nrows * (D / 4); i += 128) {
+        const int lr = i / (D / 4), v4 = i % (D / 4);
+        float mm = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int32_t k = c0; k <= c1; ++k) {
+            const int64_t at = (int64_t)(2 * k + (k == c0 ? 1 : 0)) * ROWS + lr;
+            const float2 s = __ldcg(p.part_ml + at);
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D) + v4);
+            const float mn = fmaxf(mm, s.x);
+            const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
+            const float f1 = s.x == -INFINITY ? 0.0f : ex2(s.x - mn);
+            sum = sum * f0 + s.y * f1;
+            acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
+            acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
+            mm = mn;
+        }
+        kv_emit<ROWS, D>(p, r, c, lr, v4 * 4, mm, sum, acc);
+    }
+    if (threadIdx.x == 0) p.counters[ci] = 0;
 }
 
 template <int D, bool Q8, int WK, int WR, int NT>
@@ -431,7 +488,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
 
                 // keys that some row does not see
                 const bool edge = kb + kAttendSlice > (p.tree ? r.past : r.past + 1) || kb + kAttendSlice > r.kv ||
-                                  (p.window > 0 && kb <= r.past + r.qlen - 1 - p.window);
+                                  (p.window > 0 && kb <= (int64_t)r.past + r.qlen - 1 - p.window);
                 uint32_t seen = ~0u;  // bit 4 nt + c: score c of tile nt
                 if (edge) {
                     seen = 0;
@@ -442,7 +499,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
                             const int32_t lr = (wr * NT + nt) * 8 + 2 * t + e;
                             const int32_t i = min(row0 + lr, row0 + nrows - 1) / p.group;
                             KvRowView v;
-                            v.index = r.past + i;
+                            v.index = kv_index(r, i);
                             v.tree = p.tree ? p.tree[r.q0 + i] : 0u;
                             if (kv_sees(p, r, v, kb + g)) seen |= 1u << (4 * nt + e);
                             if (kv_sees(p, r, v, kb + g + 8)) seen |= 1u << (4 * nt + e + 2);
@@ -502,7 +559,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
                             p2 = sn & 4u ? p2 : 0.0f, p3 = sn & 8u ? p3 : 0.0f;
                         }
                     }
-                    const uint32_t a = pack_bf16x2(p0, p1), b = pack_bf16x2(p2, p3);
+                    const uint32_t a = pack_bf16(p0, p1), b = pack_bf16(p2, p3);
                     pb[nt][0] = movmatrix(a);
                     pb[nt][1] = movmatrix(b);
                 }
@@ -650,15 +707,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
                     acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
                 }
                 if (whole) {
-                    const int32_t rr = row0 + lr, tok = r.q0 + rr / p.group, h = c.head * p.group + rr % p.group;
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    uint2 b;
-                    b.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-                    b.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-                    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (int64_t)h * D + dc * 64 + v4 * 4) = b;
-                    if (p.lse && dc == 0 && v4 == 0)
-                        p.lse[(int64_t)tok * (p.group * p.kv_heads) + h] =
-                            sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+                    kv_emit<ROWS, D>(p, r, c, lr, dc * 64 + v4 * 4, mm, sum, acc);
                 } else {
                     *reinterpret_cast<float4 *>(p.part + ((int64_t)slot * ROWS + lr) * D + dc * 64 + v4 * 4) = acc;
                     if (dc == 0 && v4 == 0) p.part_ml[(int64_t)slot * ROWS + lr] = make_float2(mm, sum);
@@ -667,55 +716,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
             consumers_sync();
         }
 
-        // ------------------------------------------------------------ join the CTAs
-        if (!whole) {
-            const int64_t s0 = w.u - c.ja;  // the row block's first unit
-            const int32_t c0 = (int32_t)(((s0 + 1) * w.ctas - 1) / w.total);
-            const int32_t c1 = (int32_t)(((s0 + r.ntiles) * w.ctas - 1) / w.total);
-            const int64_t ci = c.head + (int64_t)p.kv_heads *
-                                            (w.b + (int64_t)r.q0 * p.group / ROWS + c.rb);
-            const bool counted = ci < p.n_counters;  // false only for a cu_new that is not a prefix sum
-            __threadfence();
-            consumers_sync();
-            if (threadIdx.x == 0) {
-                uint32_t is_last = 0;
-                if (counted) is_last = atomicAdd(&p.counters[ci], 1u) == (uint32_t)(c1 - c0);
-                else atomicOr(p.status, kStatusKvSizes);
-                *last_flag = is_last;
-            }
-            consumers_sync();
-            if (*last_flag) {
-                __threadfence();
-                for (int i = threadIdx.x; i < nrows * (D / 4); i += 128) {
-                    const int lr = i / (D / 4), v4 = i % (D / 4);
-                    float mm = -INFINITY, sum = 0.0f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int32_t k = c0; k <= c1; ++k) {
-                        const int64_t at = (int64_t)(2 * k + (k == c0 ? 1 : 0)) * ROWS + lr;
-                        const float2 s = __ldcg(p.part_ml + at);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D) + v4);
-                        const float mn = fmaxf(mm, s.x);
-                        const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
-                        const float f1 = s.x == -INFINITY ? 0.0f : ex2(s.x - mn);
-                        sum = sum * f0 + s.y * f1;
-                        acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
-                        acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
-                        mm = mn;
-                    }
-                    const int32_t rr = row0 + lr, tok = r.q0 + rr / p.group, h = c.head * p.group + rr % p.group;
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    uint2 b;
-                    b.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-                    b.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-                    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (int64_t)h * D + v4 * 4) = b;
-                    if (p.lse && v4 == 0)
-                        p.lse[(int64_t)tok * (p.group * p.kv_heads) + h] =
-                            sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
-                }
-                if (threadIdx.x == 0) p.counters[ci] = 0;
-            }
-        }
+        if (!whole) kv_join<ROWS, D>(p, w, r, c, nrows, last_flag);
         kv_advance<ROWS>(p, w, r, c.jb - c.ja);
     }
     if (!ok && warp == 0 && lane == 0) {

@@ -1,0 +1,673 @@
+// Paged-cache attention for many rows per key head, on tcgen05 (the mathematics,
+// the work split and the joining are those of kv_attend.cuh).
+//
+// Where several drafted tokens meet a wide group (rows = new tokens x query heads
+// per key head), the warp-level products of kv_attend.cuh become the bound: every
+// warp reads (and, of an 8-bit cache, converts) the same keys for its own few rows.
+// Here 128 rows are the M of one tcgen05.mma: a tile's keys are read from shared
+// memory once for all rows.  Per 64-key tile
+//   S [128 x 64]  = Q (shared, K-major)  x K^T (shared, K-major)
+//   P             = 2^(S - m), one row per thread of four warps, BF16, over S
+//   O [128 x D] += P (TMEM)              x V (shared, MN-major)
+// S is double-buffered, so the tensor cores make the next tile's scores while the
+// softmax warps work on this one's.  O stays in TMEM for a whole piece; it is
+// rescaled only when a row's maximum rises by more than 2^8.
+//
+// A producer warp fills the K and V rings by TMA.  A Q8 cache's rows arrive as
+// bytes in rings of their own and four more warps turn them into BF16 operands;
+// the order of the columns within every four (0, 2, 1, 3) is what comes out of the
+// byte pairs cheapest, and Q's columns and O's follow it.
+//
+// For head_dim 64 and 128 a CTA takes half of TMEM and less than half of the
+// shared memory, so two share an SM and fill each other's waits.
+#pragma once
+
+#include "kv_attend.cuh"
+
+namespace w12 {
+namespace dev {
+
+constexpr int kTcRows = 128;
+constexpr int kTcInfo = 16;  // ring of per-tile facts (present slices, scales)
+
+template <int D, bool Q8>
+struct AttendTcCfg {
+    static constexpr int kBlocks = D / 64;                 // 128-byte column blocks of an operand row
+    static constexpr int kQBytes = kTcRows * D * 2;
+    static constexpr int kTileBytes = kAttendTile * D * 2;  // K or V of a tile as BF16 operand
+    static constexpr int kRawBytes = kAttendTile * D;       // K or V of a tile as bytes (Q8)
+    // operand rings (filled by TMA, or by the converting warps) and byte rings
+    static constexpr int kOps = Q8 ? 1 : D == 64 ? 4 : 2;
+    static constexpr int kRaws = Q8 ? (D == 64 ? 4 : 2) : 0;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + kQBytes;
+    static constexpr int kOffV = kOffK + kOps * kTileBytes;
+    static constexpr int kOffRaw = kOffV + kOps * kTileBytes;  // K, V of stage 0, K, V of stage 1, ...
+    static constexpr int kOffRawScale = kOffRaw + kRaws * 2 * kRawBytes;
+    static constexpr int kOffScale = kOffRawScale + kRaws * 512;  // [kTcInfo][2][64] fp32 (Q8)
+    static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * 512 : 0);
+    static constexpr int kBars = 4 * kOps + 2 * kRaws + 2 + 2 + 2 + 3;
+    static constexpr int kOffInfo = kOffBars + 8 * kBars;
+    static constexpr int kSmemBytes = kOffInfo + 4 * kTcInfo + 32 + 1024;  // 1024: alignment
+    static constexpr int kThreads = Q8 ? 320 : 192;
+    static constexpr int kTmemCols = D == 256 ? 512 : 256;
+    static constexpr int kSCol = D == 256 ? 256 : 128;  // two S buffers of 64 columns; O from column 0
+};
+
+// Warp-collective 32-column TMEM load and store (lane i <-> TMEM lane base + i).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+        "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+        "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// 4-D tiled copy global -> shared: column, token in page, head, page.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// A tile whose keys not all rows see, or of which a slice is missing.
+__device__ __forceinline__ bool kv_edge_tile(const KvAttendParams &p, const KvRequest &r, int32_t kb, uint32_t present) {
+    return present != 15u || (int64_t)kb + kAttendTile > (p.tree ? r.past : r.past + 1) ||
+           kb + kAttendTile > r.kv || (p.window > 0 && kb <= (int64_t)r.past + r.qlen - 1 - p.window);
+}
+
+__device__ __forceinline__ uint64_t low_bits(int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// Bit k: the row sees key kb + k of the tile (kv_sees and the present slices).
+__device__ __forceinline__ uint64_t kv_seen64(const KvAttendParams &p, const KvRequest &r, const KvRowView &v, int32_t kb,
+                                              uint32_t present) {
+    uint64_t m = low_bits((int64_t)r.kv - kb);
+    if (p.tree) {
+        const int64_t sh = (int64_t)r.past - kb;
+        const uint64_t drawn = sh >= 64 ? 0 : sh >= 0 ? (uint64_t)v.tree << sh : sh > -32 ? (uint64_t)(v.tree >> -sh) : 0;
+        m &= low_bits(sh) | drawn;
+    } else {
+        m &= low_bits((int64_t)v.index + 1 - kb);
+    }
+    if (p.window > 0) m &= ~low_bits((int64_t)v.index - p.window + 1 - kb);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        if (!((present >> s) & 1u)) m &= ~(0xFFFFull << (16 * s));
+    return m;
+}
+
+// One pipeline barrier's phase by use count.  The parity tells a phase only from
+// its neighbours: who waits for use n knows that use n - 1 is over, and use n + 1
+// cannot be over.  So what is waited for every tile (scores, probabilities,
+// products) has two barriers, one for even and one for odd tiles: the scores of
+// tile g are made after the product of tile g - 2.
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t use, uint64_t deadline) {
+    return mbar_wait(bar, use & 1u, deadline);
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
+    w12_kv_attend_tc_kernel(const KvAttendParams p, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v) {
+    using C = AttendTcCfg<D, Q8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + C::kOffBars), *kempty = kfull + C::kOps;
+    uint64_t *vfull = kempty + C::kOps, *vempty = vfull + C::kOps;
+    uint64_t *rfull = vempty + C::kOps, *rempty = rfull + C::kRaws;
+    uint64_t *sfull = rempty + C::kRaws, *pfull = sfull + 2;
+    uint64_t *pvdone = pfull + 2, *qfull = pvdone + 2, *ofree = qfull + 1, *drain = ofree + 1;
+    uint32_t *present = reinterpret_cast<uint32_t *>(smem + C::kOffInfo);
+    volatile uint32_t *last_flag = present + kTcInfo;
+    volatile uint32_t *poison = last_flag + 1;
+    uint32_t *tmem_slot = const_cast<uint32_t *>(last_flag) + 2;
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kOps; ++i) {
+            mbar_init(&kfull[i], Q8 ? 4 : 1);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vfull[i], Q8 ? 4 : 1);
+            mbar_init(&vempty[i], 1);
+        }
+        for (int i = 0; i < C::kRaws; ++i) {
+            mbar_init(&rfull[i], 1);
+            mbar_init(&rempty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&pvdone[i], 1);
+        }
+        mbar_init(qfull, 4);
+        mbar_init(ofree, 4);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        *poison = 0;
+    }
+    if (threadIdx.x == 128) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    pdl_wait();
+    const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
+    KvWalk w;
+    KvRequest r;
+    if (!kv_walk_init<kTcRows>(p, w, r)) return;  // the same for the whole CTA
+    // TMEM only after the kernel before has finished, and the kernel behind only
+    // when every CTA here has its TMEM: neither can then hold columns that the
+    // other waits for
+    if (warp == 5) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ TMA producer
+        uint32_t it = 0;
+        while (ok && w.u < w.end) {
+            const KvPiece c = kv_piece(w, r);
+            const int32_t *row = p.tables + (int64_t)w.b * p.table_stride;
+            for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
+                // lane 4 b + s deals with slice s (and with column block b)
+                const int s = lane & 3, blk = lane >> 2;
+                const int32_t kb = (r.tile0 + j) * kAttendTile + s * kAttendSlice;
+                const bool mine = Q8 ? lane < 4 : lane < 4 * C::kBlocks;
+                int32_t page = -1, off = 0;
+                if (mine && kb < r.kv && kb + kAttendSlice > r.first) {
+                    const int32_t e = kb / p.page_size;
+                    off = kb - e * p.page_size;
+                    page = row[e];
+                }
+                const bool here = page >= 0 && page < p.num_pages;
+                const uint32_t mask = __ballot_sync(~0u, here) & 15u;
+                const uint32_t n = (uint32_t)__popc(mask);
+                if (Q8) {
+                    const uint32_t stage = it % (C::kRaws + !Q8), use = it / (C::kRaws + !Q8);
+                    if (use > 0) ok = tc_wait(&rempty[stage], use - 1, deadline);
+                    ok = __shfl_sync(~0u, ok, 0);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        present[it % kTcInfo] = mask;
+                        mbar_arrive_expect_tx(&rfull[stage], n * (2 * kAttendSlice * D + 128));
+                    }
+                    __syncwarp();
+                    if (here) {
+                        const uint32_t dst = smem_u32(smem + C::kOffRaw + stage * 2 * C::kRawBytes + s * kAttendSlice * D);
+                        const uint32_t bar = smem_u32(&rfull[stage]);
+                        tma_load_4d(dst, &tm_k, 0, off, c.head, page, bar);
+                        tma_load_4d(dst + C::kRawBytes, &tm_v, 0, off, c.head, page, bar);
+                        bulk_g2s(smem + C::kOffRawScale + stage * 512 + s * 128,
+                                 p.scales + (((int64_t)page * p.kv_heads + c.head) * p.page_size + off) * 2, 128,
+                                 &rfull[stage]);
+                    }
+                } else {
+                    const uint32_t stage = it % C::kOps, use = it / C::kOps;
+                    const uint32_t at = stage * C::kTileBytes + blk * (kAttendTile * 128) + s * (kAttendSlice * 128);
+                    if (use > 0) ok = tc_wait(&kempty[stage], use - 1, deadline);
+                    ok = __shfl_sync(~0u, ok, 0);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        present[it % kTcInfo] = mask;
+                        mbar_arrive_expect_tx(&kfull[stage], n * (kAttendSlice * D * 2));
+                    }
+                    __syncwarp();
+                    if (here)
+                        tma_load_4d(smem_u32(smem + C::kOffK + at), &tm_k, 64 * blk, off, c.head, page,
+                                    smem_u32(&kfull[stage]));
+                    if (use > 0) ok = tc_wait(&vempty[stage], use - 1, deadline);
+                    ok = __shfl_sync(~0u, ok, 0);
+                    if (!ok) {
+                        // its keys are on their way: wait for them below
+                        ++it;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&vfull[stage], n * (kAttendSlice * D * 2));
+                    __syncwarp();
+                    if (here)
+                        tma_load_4d(smem_u32(smem + C::kOffV + at), &tm_v, 64 * blk, off, c.head, page,
+                                    smem_u32(&vfull[stage]));
+                }
+            }
+            if (ok) kv_advance<kTcRows>(p, w, r, c.jb - c.ja);
+        }
+        // no copy may still be in flight when the CTA ends (only after a timeout
+        // is that not so already)
+        if (!ok && lane == 0) {
+            atomicOr(p.status, 8u);
+            const uint64_t late = globaltimer_ns() + p.timeout_ns;
+            constexpr uint32_t N = Q8 ? C::kRaws + !Q8 : C::kOps;
+            for (uint32_t k = it > N ? it - N : 0; k < it; ++k) {
+                if (!tc_wait(Q8 ? &rfull[k % N] : &kfull[k % N], k / N, late)) break;
+                if (!Q8 && !tc_wait(&vfull[k % N], k / N, late)) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kAttendTile);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
+        uint32_t it = 0, piece = 0;  // tiles whose scores have been issued; pieces
+        // scores of tile `it` into S[it & 1]
+        auto scores = [&](uint32_t issued) -> bool {
+            const uint32_t stage = it % C::kOps;
+            // the buffer's last probabilities (tile it - 2) have been multiplied:
+            // wait for the last product issued so far
+            if (issued > 0 && !tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline)) return false;
+            if (!tc_wait(&kfull[stage], it / C::kOps, deadline)) return false;
+            tc_fence_after();
+            const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
+            const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
+            const uint32_t d = tmem + C::kSCol + 64 * (it & 1);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
+                           b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
+            mma_commit(&kempty[stage]);
+            mma_commit(&sfull[it & 1]);
+            ++it;
+            return true;
+        };
+        if (lane == 0) {
+            while (ok && w.u < w.end) {
+                const KvPiece c = kv_piece(w, r);
+                const int n = c.jb - c.ja;
+                ok = tc_wait(qfull, piece, deadline) && scores(it);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j + 1 < n && !(ok = scores(it - 1))) break;
+                    const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
+                    ok = tc_wait(&pfull[g & 1], g >> 1, deadline) && tc_wait(&vfull[stage], g / C::kOps, deadline);
+                    if (ok && j == 0 && piece > 0) ok = tc_wait(ofree, piece - 1, deadline);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = tmem + C::kSCol + 64 * (g & 1);
+                    const uint64_t b = smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128,
+                                                 1024u, 2u);
+#pragma unroll
+                    for (int k = 0; k < kAttendTile / 16; ++k)
+                        mma_tmem_a(tmem, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
+                    mma_commit(&vempty[stage]);
+                    mma_commit(&pvdone[g & 1]);
+                }
+                ++piece;
+                if (ok) {
+                    // kv_advance is one lane's here: it has no warp operations
+                    kv_advance<kTcRows>(p, w, r, n);
+                }
+            }
+            if (!ok) atomicOr(p.status, 8u);
+            mma_commit(drain);  // nothing issued may still run when TMEM is given back
+            tc_wait(drain, 0, globaltimer_ns() + p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp >= 6) {
+        // ------------------------------------------------------------ converters (Q8)
+        const int ct = (warp - 6) * 32 + lane;
+        uint32_t it = 0;
+        constexpr uint32_t N = C::kRaws + !Q8;
+        constexpr int CH = D / 16;  // 16-byte chunks of a row
+        while (ok && w.u < w.end) {
+            const KvPiece c = kv_piece(w, r);
+            for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
+                const uint32_t stage = it % N;
+                ok = tc_wait(&rfull[stage], it / N, deadline);
+                if (ok && it > 0) ok = tc_wait(&kempty[0], it - 1, deadline);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                // scales of the tile's keys, the softmax scale in the keys' ones
+                {
+                    const float *src = reinterpret_cast<const float *>(smem + C::kOffRawScale + stage * 512);
+                    float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (it % kTcInfo) * 512);
+                    dst[ct] = src[2 * (ct & 63) + (ct >> 6)] * (ct < 64 ? p.scale_log2 : 1.0f);
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (kv == 1) {
+                        if (it > 0) ok = tc_wait(&vempty[0], it - 1, deadline);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                    }
+                    const uint32_t src = smem_u32(smem + C::kOffRaw + (stage * 2 + kv) * C::kRawBytes);
+                    const uint32_t dst = smem_u32(smem + (kv ? C::kOffV : C::kOffK));
+#pragma unroll
+                    for (int i = 0; i < kAttendTile * CH / 128; ++i) {
+                        const int ch = i * 128 + ct, key = ch / CH, cc = ch % CH;
+                        const uint4 u = lds128(src + ch * 16);
+                        uint4 a, b;
+                        q8_to_bf16(u.x, a.x, a.y);
+                        q8_to_bf16(u.y, a.z, a.w);
+                        q8_to_bf16(u.z, b.x, b.y);
+                        q8_to_bf16(u.w, b.z, b.w);
+                        const uint32_t at = dst + (cc / 4) * (kAttendTile * 128) + key * 128;
+                        const uint32_t a0 = at + (((2 * (cc % 4)) ^ (key & 7)) << 4);
+                        const uint32_t a1 = at + (((2 * (cc % 4) + 1) ^ (key & 7)) << 4);
+                        // odd column blocks the other way round: eight lanes then
+                        // write eight different 16-byte bank groups
+                        const bool turn = (cc / 4) & 1;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(turn ? a1 : a0),
+                                     "r"(turn ? b.x : a.x), "r"(turn ? b.y : a.y), "r"(turn ? b.z : a.z),
+                                     "r"(turn ? b.w : a.w)
+                                     : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(turn ? a0 : a1),
+                                     "r"(turn ? a.x : b.x), "r"(turn ? a.y : b.y), "r"(turn ? a.z : b.z),
+                                     "r"(turn ? a.w : b.w)
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv ? &vfull[0] : &kfull[0]);
+                }
+                if (ok && lane == 0) mbar_arrive(&rempty[stage]);
+            }
+            if (ok) kv_advance<kTcRows>(p, w, r, c.jb - c.ja);
+        }
+        if (!ok && lane == 0) atomicOr(p.status, 8u);
+    } else {
+        // ------------------------------------------------------------ softmax and output, one row per thread
+        const int lr = threadIdx.x;  // 0..127, TMEM lane
+        const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+        // a negative softmax scale is put into Q, so that the largest score is the
+        // largest product
+        const float scale = fabsf(p.scale_log2);
+        uint32_t it = 0;
+        KvPiece c = kv_piece(w, r);
+        // Q rows of a piece to shared memory, rows behind the last one zero
+        auto load_q = [&](const KvRequest &rq, const KvPiece &pc) {
+            const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
+            constexpr int CH = D / 8;  // 16-byte chunks of a row
+#pragma unroll 8
+            for (int i = lane; i < 32 * CH; i += 32) {
+                const int row = warp * 32 + i / CH, ch = i % CH;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (row < rows) {
+                    const int32_t rr = pc.rb * kTcRows + row, tok = rr / p.group;
+                    u = *reinterpret_cast<const uint4 *>(p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
+                                                         (int64_t)(pc.head * p.group + rr - tok * p.group) * D + 8 * ch);
+                }
+                if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
+                    u.x ^= 0x80008000u, u.y ^= 0x80008000u, u.z ^= 0x80008000u, u.w ^= 0x80008000u;
+                if (Q8)  // the column order of the converted keys
+                    u = make_uint4(prmt(u.x, u.y, 0x5410u), prmt(u.x, u.y, 0x7632u), prmt(u.z, u.w, 0x5410u),
+                                   prmt(u.z, u.w, 0x7632u));
+                *reinterpret_cast<uint4 *>(smem + C::kOffQ + (ch / 8) * (kTcRows * 128) + row * 128 +
+                                           (((ch % 8) ^ (row & 7)) << 4)) = u;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull);
+        };
+        load_q(r, c);
+        while (true) {
+            const int32_t nrows = (int32_t)min((int64_t)kTcRows, (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows);
+            const bool busy = 32 * warp < nrows;  // a warp without rows only keeps step
+            const int32_t i = min(c.rb * kTcRows + lr, c.rb * kTcRows + nrows - 1) / p.group;
+            KvRowView view;
+            view.index = kv_index(r, i);
+            view.tree = p.tree ? p.tree[r.q0 + i] : 0u;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = c.ja; j < c.jb; ++j, ++it) {
+                // after a timeout the walk goes on without waiting, so that every
+                // barrier below is reached
+                if (ok) ok = tc_wait(&sfull[it & 1], it >> 1, deadline);
+                ok = __all_sync(~0u, ok);
+                tc_fence_after();
+                const int32_t kb = (r.tile0 + j) * kAttendTile;
+                const uint32_t here = present[it % kTcInfo];
+                const bool edge = kv_edge_tile(p, r, kb, here);
+                const uint32_t ts = tl + C::kSCol + 64 * (it & 1);
+                if (busy) {
+                    // Two passes over the scores in TMEM, 32 at a time: the maximum,
+                    // then the probabilities.  Reading them twice costs less than
+                    // the registers of all 64.
+                    const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * 512);
+                    uint64_t seen = ~0ull;
+                    if (edge) seen = kv_seen64(p, r, view, kb, here);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 64; h += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(ts + h, x);
+                        tmem_wait_ld();
+                        if (Q8) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 s = *reinterpret_cast<const float2 *>(sc + h + k);
+                                const f2 y = make_f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])) *
+                                             make_f2(s.x, s.y);
+                                x[k] = __float_as_uint(f2_lo(y));
+                                x[k + 1] = __float_as_uint(f2_hi(y));
+                            }
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((seen >> (h + k)) & 1ull)) x[k] = __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            top = fmaxf(fmaxf(top, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+                    }
+                    if (!Q8) top *= scale;
+                    if (__any_sync(~0u, top > m + kAttendLazy)) {
+                        const float mn = fmaxf(m, top);
+                        const float al = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                        m = mn;
+                        l *= al;
+                        if (j > c.ja) {
+                            if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
+                            ok = __all_sync(~0u, ok);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int d0 = 0; d0 < D; d0 += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tl + d0, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                                tmem_st32(tl + d0, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float m0 = m == -INFINITY ? 0.0f : m;
+                    const f2 minus = make_f2(-m0, -m0), scale2 = make_f2(scale, scale);
+                    f2 l2 = make_f2(0.0f, 0.0f);
+#pragma unroll
+                    for (int h = 0; h < 64; h += 32) {
+                        uint32_t x[32], pk[16];
+                        tmem_ld32(ts + h, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            f2 y = make_f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                            if (Q8) {
+                                const float2 s = *reinterpret_cast<const float2 *>(sc + h + k);
+                                y = y * make_f2(s.x, s.y) + minus;
+                            } else {
+                                y = fma2(y, scale2, minus);
+                            }
+                            float a = ex2(f2_lo(y)), b = ex2(f2_hi(y));
+                            if (edge) {
+                                if (!((seen >> (h + k)) & 1ull)) a = 0.0f;
+                                if (!((seen >> (h + k + 1)) & 1ull)) b = 0.0f;
+                            }
+                            f2 e = make_f2(a, b);
+                            l2 = l2 + e;
+                            if (Q8) {
+                                const float2 s = *reinterpret_cast<const float2 *>(sc + 64 + h + k);
+                                e = e * make_f2(s.x, s.y);
+                                // an unseen key's scale may be anything
+                                if (edge) {
+                                    if (!((seen >> (h + k)) & 1ull)) e = make_f2(0.0f, f2_hi(e));
+                                    if (!((seen >> (h + k + 1)) & 1ull)) e = make_f2(f2_lo(e), 0.0f);
+                                }
+                            }
+                            pk[k / 2] = pack_bf16(f2_lo(e), f2_hi(e));
+                        }
+                        // over scores that both passes have read
+                        tmem_st16(ts + h / 2, pk);
+                    }
+                    l += f2_lo(l2) + f2_hi(l2);
+                    tmem_wait_st();
+                }
+                if (!Q8 && edge) {
+                    // values behind the request's last token or of missing slices
+                    // become zero, and so do (noted, for the rows that see them)
+                    // values that are not finite: the product must not meet 0 * NaN
+                    const uint32_t stage = it % C::kOps;
+                    if (ok) ok = tc_wait(&vfull[stage], it / C::kOps, deadline);
+                    ok = __all_sync(~0u, ok);
+                    constexpr int CH = D / 8;
+                    for (int q = lr; q < kAttendTile * CH; q += 128) {
+                        const int key = q / CH, ch = q % CH;
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + C::kOffV + stage * C::kTileBytes +
+                                                              (ch / 8) * (kAttendTile * 128) + key * 128 +
+                                                              (((ch % 8) ^ (key & 7)) << 4));
+                        uint4 u = *at;
+                        if (kb + key >= r.kv || !((here >> (key / 16)) & 1u)) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else {
+                            uint32_t e[4] = {u.x, u.y, u.z, u.w};
+                            bool hit = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u, hit = true;
+                                if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0xFFFFu, hit = true;
+                            }
+                            if (hit) {
+                                *at = make_uint4(e[0], e[1], e[2], e[3]);
+                                *poison = 1;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[it & 1]);
+            }
+            // the next piece's Q while the last products of this one run (all
+            // scores of this piece are there, so nothing reads Q any more)
+            KvWalk w2 = w;
+            KvRequest r2 = r;
+            kv_advance<kTcRows>(p, w2, r2, c.jb - c.ja);
+            const bool more = w2.u < w2.end;
+            KvPiece c2 = c;
+            if (more) {
+                c2 = kv_piece(w2, r2);
+                load_q(r2, c2);
+            }
+            if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
+            ok = __all_sync(~0u, ok);
+            tc_fence_after();
+            const bool whole = c.ja == 0 && c.jb == r.ntiles;
+            bool bad = false;
+            if (!Q8) {
+                consumers_sync();  // every thread's note is in
+                bad = *poison != 0;
+                if (bad) {  // the same for all four warps
+                    consumers_sync();
+                    *poison = 0;
+                    consumers_sync();
+                }
+            }
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (c.ja > 0 ? 0 : 1);
+            if (busy) {
+                const int32_t head = c.head * p.group + c.rb * kTcRows + lr - i * p.group;
+                uint16_t *dst = p.out + (r.q0 + i) * p.out_stride + (int64_t)head * D;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+                for (int d0 = 0; d0 < D; d0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tl + d0, o);
+                    tmem_wait_ld();
+                    if (bad && lr < nrows) {
+                        // values that are not finite count, as they are, for the
+                        // rows that see their keys (a weight is positive; what went
+                        // through the product already stays what it is)
+                        for (int j = c.ja; j < c.jb; ++j) {
+                            const int32_t kb = (r.tile0 + j) * kAttendTile;
+                            uint64_t seen = kv_seen64(p, r, view, kb, 15u);
+                            for (; seen; seen &= seen - 1) {
+                                const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
+                                const int32_t page = p.tables[(int64_t)w.b * p.table_stride + e];
+                                if (page < 0 || page >= p.num_pages) continue;
+                                const uint16_t *v = p.v + page * p.v_page_stride + c.head * p.v_head_stride +
+                                                    (int64_t)(key - e * p.page_size) * p.v_row_stride + d0;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if ((v[k] & 0x7F80u) == 0x7F80u)
+                                        o[k] = __float_as_uint(__uint_as_float(o[k]) +
+                                                               __uint_as_float((uint32_t)v[k] << 16));
+                            }
+                        }
+                    }
+                    if (lr < nrows) {
+                        float y[32];  // Q8: columns (0, 2, 1, 3) of every four
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            y[k] = __uint_as_float(o[!Q8 || k % 4 == 0 || k % 4 == 3 ? k : k % 4 == 1 ? k + 1 : k - 1]);
+                        if (whole) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 8)
+                                *reinterpret_cast<uint4 *>(dst + d0 + k) = make_uint4(
+                                    pack_bf16(y[k] * inv, y[k + 1] * inv), pack_bf16(y[k + 2] * inv, y[k + 3] * inv),
+                                    pack_bf16(y[k + 4] * inv, y[k + 5] * inv),
+                                    pack_bf16(y[k + 6] * inv, y[k + 7] * inv));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4)
+                                *reinterpret_cast<float4 *>(p.part + (slot * kTcRows + lr) * D + d0 + k) =
+                                    make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                        }
+                    }
+                }
+                if (lr < nrows) {
+                    if (!whole) p.part_ml[slot * kTcRows + lr] = make_float2(m, l);
+                    else if (p.lse)
+                        p.lse[(int64_t)(r.q0 + i) * (p.group * p.kv_heads) + head] =
+                            l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ofree);
+            if (!whole) kv_join<kTcRows, D>(p, w, r, c, nrows, last_flag);
+            if (!more) break;
+            w = w2;
+            r = r2;
+            c = c2;
+        }
+        if (!ok && lane == 0) atomicOr(p.status, 8u);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+}  // namespace dev
+}  // namespace w12

@@ -70,6 +70,8 @@ struct KvAttendParams {
     int64_t table_stride;
     const int32_t *lens, *cu_new;
     const uint32_t *tree;
+    const uint16_t *v;  // a BF16 cache's values, and their strides in elements
+    int64_t v_page_stride, v_head_stride, v_row_stride;
     const float *scales;
     int64_t num_pages;
     int32_t requests, max_keys, tokens, kv_heads, group, window, page_size;
@@ -81,6 +83,41 @@ struct KvAttendParams {
     uint32_t *status;
     uint64_t timeout_ns;
 };
+
+// Two fp32 to packed BF16, round to nearest even, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Pairs of fp32 in one 64-bit register and the packed arithmetic on them (each
+// half rounds as the scalar operation does).
+struct f2 {
+    uint64_t v;
+};
+__device__ __forceinline__ f2 make_f2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_lo(f2 a) { return __uint_as_float((uint32_t)a.v); }
+__device__ __forceinline__ float f2_hi(f2 a) { return __uint_as_float((uint32_t)(a.v >> 32)); }
+__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
 
 }  // namespace dev
 }  // namespace w12

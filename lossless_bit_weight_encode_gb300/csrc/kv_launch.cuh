@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "kv_attend.cuh"
+#include "kv_attend_tc.cuh"
 #include "w12.h"
 #include "w12_launch.hpp"
 
@@ -52,11 +53,12 @@ cudaError_t kv_launch(const DeviceView &d, void (*kernel)(KArgs...), dim3 grid, 
 
 constexpr int kKvMaxDevices = 64;
 
-// Rows of the tile a launch uses: new tokens times query heads per key head,
-// 8 to 64; more rows take several row blocks.
+// Rows of the tile a launch uses: new tokens times query heads per key head.  Up
+// to 32 the warp-level kernel with 8, 16 or 32 rows, above the tcgen05 kernel with
+// 128; more rows take several row blocks.
 inline int attend_rows(int max_new, int group) {
     const int64_t rows = (int64_t)(max_new < 1 ? 1 : max_new) * group;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : dev::kTcRows;
 }
 
 // Workspace: the partial outputs, their maxima and sums, the counters.  The
@@ -64,7 +66,7 @@ inline int attend_rows(int max_new, int group) {
 // head_dim x CTAs per SM), so that the counters lie at one place and calls of
 // different shapes can share a workspace: what one leaves zero is what another
 // finds.
-constexpr int kPartElems = 64 * 256;
+constexpr int kPartElems = 128 * 256;
 struct AttendPlan {
     int rows = 8, ctas = 1;
     size_t off_ml = 0, off_counters = 0, bytes = 0;
@@ -77,13 +79,10 @@ template <int D>
 int attend_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvAttendParams *p,
                const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
 
-template <int D, bool Q8, int WK, int WR, int NT>
-int attend_variant(const DeviceView &d, int *resident, const dev::KvAttendParams *p, const CUtensorMap *tm_k,
-                   const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
-    using C = dev::AttendCfg<D, Q8, WK, WR, NT>;
-    auto kernel = &dev::w12_kv_attend_kernel<D, Q8, WK, WR, NT>;
-    static std::mutex mu;
-    static int per_sm[kKvMaxDevices] = {};
+// Occupancy of one kernel on first use, then (with `p`) its launch.
+inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams, CUtensorMap, CUtensorMap), int rows_dim,
+                         int threads, int smem, std::mutex &mu, int *per_sm, int *resident, const dev::KvAttendParams *p,
+                         const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     if (d.device < 0 || d.device >= kKvMaxDevices) {
         *err = "device ordinal out of range";
         return W12_ERR_CUDA;
@@ -92,26 +91,45 @@ int attend_variant(const DeviceView &d, int *resident, const dev::KvAttendParams
         std::lock_guard<std::mutex> lock(mu);
         if (per_sm[d.device] == 0) {
             void *k = reinterpret_cast<void *>(kernel);
-            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             int occ = 0;
-            if (e == cudaSuccess)
-                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, dev::kAttendThreads, C::kSmemBytes);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, threads, (size_t)smem);
             if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend set-up", err);
             if (occ < 1) {
                 *err = "w12_kv_attend cannot be resident on this device";
                 return W12_ERR_CUDA;
             }
-            constexpr int kMost = kPartElems / (C::kRows * D);
-            per_sm[d.device] = occ < kMost ? occ : kMost;
+            const int most = kPartElems / rows_dim;
+            per_sm[d.device] = occ < most ? occ : most;
         }
         *resident = per_sm[d.device] * d.sm_count;
     }
     if (!p) return W12_OK;
-    const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)ctas), dev::kAttendThreads, C::kSmemBytes, 1, stream,
-                                    *p, *tm_k, *tm_v);
+    const cudaError_t e =
+        kv_launch(d, kernel, dim3((unsigned)ctas), threads, smem, 1, stream, *p, *tm_k, *tm_v);
     if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend launch", err);
     return W12_OK;
+}
+
+template <int D, bool Q8, int WK, int WR, int NT>
+int attend_variant(const DeviceView &d, int *resident, const dev::KvAttendParams *p, const CUtensorMap *tm_k,
+                   const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+    using C = dev::AttendCfg<D, Q8, WK, WR, NT>;
+    static std::mutex mu;
+    static int per_sm[kKvMaxDevices] = {};
+    return attend_kernel(d, &dev::w12_kv_attend_kernel<D, Q8, WK, WR, NT>, C::kRows * D, dev::kAttendThreads,
+                         C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
+}
+
+template <int D, bool Q8>
+int attend_tc_variant(const DeviceView &d, int *resident, const dev::KvAttendParams *p, const CUtensorMap *tm_k,
+                      const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+    using C = dev::AttendTcCfg<D, Q8>;
+    static std::mutex mu;
+    static int per_sm[kKvMaxDevices] = {};
+    return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8>, dev::kTcRows * D, C::kThreads, C::kSmemBytes, mu,
+                         per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
 // The variants of one head_dim.  Rows up to 16 (BF16 operands of q and the sums
@@ -129,7 +147,7 @@ int attend_rows_variant(const DeviceView &d, int rows, int *resident, const dev:
     case 32:
         return attend_variant<D, Q8, D == 256 ? 1 : 2, D == 256 ? 4 : 2, D == 256 ? 1 : 2>(d, resident, p, tm_k, tm_v,
                                                                                           ctas, stream, err);
-    default: return attend_variant<D, Q8, 1, 4, 2>(d, resident, p, tm_k, tm_v, ctas, stream, err);
+    default: return attend_tc_variant<D, Q8>(d, resident, p, tm_k, tm_v, ctas, stream, err);
     }
 }
 

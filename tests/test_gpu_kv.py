@@ -429,11 +429,12 @@ def test_attend(dim, heads, kv_heads, q8, lens, new, page):
 
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("window", [1, 16, 63, 64, 100, 5000])
-def test_attend_window(q8, window):
+@pytest.mark.parametrize("group,dim", [(3, 128), (11, 128), (17, 64), (9, 256)])
+def test_attend_window(q8, window, group, dim):
     lens, new = [0, 300, 64, 127], [2, 5, 1, 1]
-    cache, tables, cu, q, step = attend_case(lens, new, 6, 2, 128, 16, q8, seed=window)
+    cache, tables, cu, q, step = attend_case(lens, new, 2 * group, 2, dim, 16, q8, seed=window)
     out, lse = run_attend(cache, q, step, window=window, scale=0.2)
-    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, window, 0.2, 3))
+    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, window, 0.2, group))
 
 
 @pytest.mark.parametrize("q8", [False, True])
@@ -477,9 +478,10 @@ def test_attend_layouts_and_strided_q(layout, q8, dim):
 
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("dim", [64, 128, 256])
-def test_attend_long_split_over_ctas(q8, dim):
+@pytest.mark.parametrize("new", [[1, 2, 1], [16, 7, 25]])
+def test_attend_long_split_over_ctas(q8, dim, new):
     """One request over many CTAs, beside short ones; the same bits every time."""
-    lens, new = [9000, 3, 700], [1, 2, 1]
+    lens = [9000, 3, 700]
     cache, tables, cu, q, step = attend_case(lens, new, 6, 1, dim, 16, q8, seed=dim)
     out, lse = run_attend(cache, q, step)
     check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, dim ** -0.5, 6))
@@ -488,27 +490,31 @@ def test_attend_long_split_over_ctas(q8, dim):
         assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
-def test_attend_absent_pages():
-    lens, new = [100, 40], [1, 1]
-    cache, tables, cu, q, step = attend_case(lens, new, 4, 2, 128, 16, False, seed=8)
-    tables[0, 2], tables[0, 4], tables[1, :] = -1, 1 << 20, -5
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [2, 40])
+@pytest.mark.parametrize("q8", [False, True])
+def test_attend_absent_pages(group, q8, dim):
+    lens, new = [200, 40], [1, 1]
+    cache, tables, cu, q, step = attend_case(lens, new, 2 * group, 2, dim, 16, q8, seed=8)
+    tables[0, 2], tables[0, 4], tables[0, 8:12], tables[1, :] = -1, 1 << 20, -1, -5
     step.tables.copy_(torch.from_numpy(tables))
     out, lse = run_attend(cache, q, step)
-    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, 128 ** -0.5, 2))
+    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, dim ** -0.5, group))
     assert (out[1] == 0).all() and torch.isinf(lse[1]).all()
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("q8", [False, True])
-def test_attend_unseen_values_have_no_effect(dim, bad, q8):
+@pytest.mark.parametrize("group", [3, 12])  # the warp-level and the tcgen05 kernel
+def test_attend_unseen_values_have_no_effect(dim, bad, q8, group):
     """Drafted tokens whose keys and values are not finite: the tokens that do
     not see them are as if they were not there; those that do are not finite."""
     lens, new = [37], [5]
-    cache, tables, cu, q, step = attend_case(lens, new, 6, 2, dim, 16, q8, seed=1)
+    cache, tables, cu, q, step = attend_case(lens, new, 2 * group, 2, dim, 16, q8, seed=1)
     tree = np.array([1, 2, 5, 10, 0b10001], np.int32)  # token 1 is seen by 1 and 3 alone
     step.tree = torch.from_numpy(tree).cuda()
-    ref = attend_ref(q, cache, tables, lens, cu, tree, 0, dim ** -0.5, 3)
+    ref = attend_ref(q, cache, tables, lens, cu, tree, 0, dim ** -0.5, group)
     page, off = int(tables[0, 38 // 16]), 38 % 16
     if q8:
         cache.scales[page, 1, off] = bad
@@ -518,18 +524,24 @@ def test_attend_unseen_values_have_no_effect(dim, bad, q8):
     out, lse = run_attend(cache, q, step)
     clean = [0, 2, 4]
     check_attend(out[clean], lse[clean], tuple(x[clean] for x in ref))
-    check_attend(out.view(5, 6, dim)[:, :3], lse[:, :3], tuple(x[:, :3] for x in ref))
+    out = out.view(5, 2 * group, dim)
+    check_attend(out[:, :group], lse[:, :group], tuple(x[:, :group] for x in ref))
     if bad != bad:
-        assert torch.isnan(out.view(5, 6, dim)[1, 3:, 3:9]).all() and torch.isnan(out.view(5, 6, dim)[3, 3:, 3:9]).all()
+        assert torch.isnan(out[1, group:, 3:9]).all() and torch.isnan(out[3, group:, 3:9]).all()
+    # a request behind it is not touched by what this one met
+    again, lse2 = run_attend(cache, q, step)
+    assert torch.equal(again.view(out.shape)[clean], out[clean]) and torch.equal(lse2[clean], lse[clean])
 
 
-def test_attend_large_scores():
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 64), (40, 2, 64), (40, 2, 128), (20, 1, 256)])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+def test_attend_large_scores(heads, kv_heads, dim, scale):
     """Scores far apart and far from zero: the running maximum is raised again and again."""
     lens, new = [400], [2]
-    cache, tables, cu, q, step = attend_case(lens, new, 8, 2, 64, 16, False, seed=4)
+    cache, tables, cu, q, step = attend_case(lens, new, heads, kv_heads, dim, 16, False, seed=4)
     cache.k.mul_(torch.linspace(-30, 60, cache.k.shape[0], device="cuda")[:, None, None, None])
-    out, lse = run_attend(cache, q, step, scale=1.0)
-    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, 1.0, 4))
+    out, lse = run_attend(cache, q, step, scale=scale)
+    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, scale, heads // kv_heads))
 
 
 def test_attend_rows_without_tokens_and_more_rows_than_max_new_says():
@@ -545,13 +557,15 @@ def test_attend_rows_without_tokens_and_more_rows_than_max_new_says():
     assert (out[13:] == 3).all() and (lse[13:] == 3).all()
 
 
-def test_attend_many_requests():
+@pytest.mark.parametrize("most,heads,kv_heads", [(2, 4, 2), (30, 8, 2)])
+@pytest.mark.parametrize("q8", [False, True])
+def test_attend_many_requests(most, heads, kv_heads, q8):
     rng = random.Random(0)
     lens = [rng.randint(0, 90) for _ in range(300)]
-    new = [rng.choice([0, 1, 1, 2]) for _ in range(300)]
-    cache, tables, cu, q, step = attend_case(lens, new, 4, 2, 64, 16, False, seed=6)
+    new = [rng.choice([0, 1, 1, most]) for _ in range(300)]
+    cache, tables, cu, q, step = attend_case(lens, new, heads, kv_heads, 64, 16, q8, seed=6)
     out, lse = run_attend(cache, q, step)
-    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, 0.125, 2))
+    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, 0.125, heads // kv_heads))
 
 
 def test_attend_offsets_past_32_bits():
