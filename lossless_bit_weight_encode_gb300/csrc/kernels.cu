@@ -86,6 +86,35 @@ __global__ void w12_selftest_timeout_kernel(uint32_t *status, uint64_t timeout_n
 }  // namespace dev
 
 namespace launch {
+
+static int launch_fail(cudaError_t e, const char *what, std::string *err) {
+    *err = std::string(what) + ": " + cudaGetErrorString(e);
+    return W12_ERR_CUDA;
+}
+
+// Resident CTAs per SM from the kernel's own limits: registers (allocated per
+// warp in units of 256), dynamic shared memory (+1 KB reserved per CTA) and
+// threads.  The runtime's occupancy query is taken when it reports more.
+int resident_ctas(const void *kernel, int threads, int smem_bytes, int device, std::string *err, int *out) {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return launch_fail(e, "cudaFuncGetAttributes", err);
+    int regs_sm = 0, smem_sm = 0, threads_sm = 0;
+    cudaDeviceGetAttribute(&regs_sm, cudaDevAttrMaxRegistersPerMultiprocessor, device);
+    cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, device);
+    cudaDeviceGetAttribute(&threads_sm, cudaDevAttrMaxThreadsPerMultiProcessor, device);
+    const int warps = (threads + 31) / 32;
+    const int regs_warp = ((fa.numRegs * 32 + 255) / 256) * 256;
+    int occ = regs_warp > 0 ? regs_sm / (warps * regs_warp) : 1;
+    occ = std::min(occ, smem_sm / (smem_bytes + 1024));
+    occ = std::min(occ, threads_sm / threads);
+    int api = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&api, kernel, threads, (size_t)smem_bytes);
+    if (e != cudaSuccess) return launch_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor", err);
+    *out = std::max(std::max(occ, api), 1);
+    return W12_OK;
+}
+
 namespace {
 
 constexpr int kStages = 4;
@@ -117,33 +146,7 @@ int gemm_smem_bytes() {
     return dev::GemmCfg<NTOK, kStages, ASMEM, Q8>::kSmemBytes;
 }
 
-int cuda_fail(cudaError_t e, const char *what, std::string *err) {
-    *err = std::string(what) + ": " + cudaGetErrorString(e);
-    return W12_ERR_CUDA;
-}
-
-// Resident CTAs per SM from the kernel's own limits: registers (allocated per
-// warp in units of 256), dynamic shared memory (+1 KB reserved per CTA) and
-// threads.  The runtime's occupancy query is taken when it reports more.
-int resident_ctas(const void *kernel, int threads, int smem_bytes, int device, std::string *err, int *out) {
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes", err);
-    int regs_sm = 0, smem_sm = 0, threads_sm = 0;
-    cudaDeviceGetAttribute(&regs_sm, cudaDevAttrMaxRegistersPerMultiprocessor, device);
-    cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, device);
-    cudaDeviceGetAttribute(&threads_sm, cudaDevAttrMaxThreadsPerMultiProcessor, device);
-    const int warps = (threads + 31) / 32;
-    const int regs_warp = ((fa.numRegs * 32 + 255) / 256) * 256;
-    int occ = regs_warp > 0 ? regs_sm / (warps * regs_warp) : 1;
-    occ = std::min(occ, smem_sm / (smem_bytes + 1024));
-    occ = std::min(occ, threads_sm / threads);
-    int api = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&api, kernel, threads, (size_t)smem_bytes);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor", err);
-    *out = std::max(std::max(occ, api), 1);
-    return W12_OK;
-}
+int cuda_fail(cudaError_t e, const char *what, std::string *err) { return launch_fail(e, what, err); }
 
 template <int NTOK, bool ASMEM, bool Q8 = false>
 int prepare_gemm(DeviceState &s, std::string *err) {

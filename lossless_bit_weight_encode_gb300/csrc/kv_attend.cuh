@@ -248,48 +248,100 @@ __device__ __forceinline__ void kv_emit(const KvAttendParams &p, const KvRequest
         p.lse[(int64_t)tok * (p.group * p.kv_heads) + h] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
 }
 
-// The row block's parts come together: called by the 128 consumer threads when
-// they have written the CTA's part to its slot.  The last CTA to arrive joins the
-// parts in range order.
-template <int ROWS, int D>
-__device__ __forceinline__ void kv_join(const KvAttendParams &p, const KvWalk &w, const KvRequest &r, const KvPiece &c,
-                                        int32_t nrows, volatile uint32_t *last_flag) {
+// A row block whose keys several CTAs shared: where its parts are and its counter.
+struct KvParts {
+    int64_t first;  // row of the first CTA's first slot
+    int64_t counter;
+    int32_t n;  // parts, one per CTA in range order
+};
+
+template <int ROWS>
+__device__ __forceinline__ KvParts kv_parts(const KvAttendParams &p, const KvWalk &w, const KvRequest &r,
+                                            const KvPiece &c) {
     const int64_t s0 = w.u - c.ja;  // the row block's first unit
     const int32_t c0 = (int32_t)(((s0 + 1) * w.ctas - 1) / w.total);
     const int32_t c1 = (int32_t)(((s0 + r.ntiles) * w.ctas - 1) / w.total);
-    const int64_t ci = c.head + (int64_t)p.kv_heads * (w.b + (int64_t)r.q0 * p.group / ROWS + c.rb);
-    const bool counted = ci < p.n_counters;  // false only for a cu_new that is not a prefix sum
+    KvParts q;
+    q.first = 2 * (int64_t)c0 * ROWS;
+    q.counter = c.head + (int64_t)p.kv_heads * (w.b + (int64_t)r.q0 * p.group / ROWS + c.rb);
+    q.n = c1 - c0 + 1;
+    return q;
+}
+
+// Called by the 128 consumer threads when they have written the CTA's part to its
+// slot: true (for all of them) in the CTA that arrives last.
+__device__ __forceinline__ bool kv_arrive(const KvAttendParams &p, const KvParts &q, volatile uint32_t *last_flag) {
+    const bool counted = q.counter < p.n_counters;  // false only for a cu_new that is not a prefix sum
     __threadfence();
     consumers_sync();
     if (threadIdx.x == 0) {
         uint32_t is_last = 0;
-        if (counted) is_last = atomicAdd(&p.counters[ci], 1u) == (uint32_t)(c1 - c0);
+        if (counted) is_last = atomicAdd(&p.counters[q.counter], 1u) == (uint32_t)(q.n - 1);
         else atomicOr(p.status, kStatusKvSizes);
+        if (is_last) p.counters[q.counter] = 0;
         *last_flag = is_last;
     }
     consumers_sync();
-    if (!*last_flag) return;
+    if (!*last_flag) return false;
     __threadfence();
-    for (int i = threadIdx.x; i < nrows * (D / 4); i += 128) {
-        const int lr = i / (D / 4), v4 = i % (D / 4);
-        float mm = -INFINITY, sum = 0.0f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int32_t k = c0; k <= c1; ++k) {
-            const int64_t at = (int64_t)(2 * k + (k == c0 ? 1 : 0)) * ROWS + lr;
-            const float2 s = __ldcg(p.part_ml + at);
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D) + v4);
-            const float mn = fmaxf(mm, s.x);
-            const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
-            const float f1 = s.x == -INFINITY ? 0.0f : ex2(s.x - mn);
-            sum = sum * f0 + s.y * f1;
-            acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
-            acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
-            mm = mn;
+    return true;
+}
+
+// The parts' joining in range order by `threads` threads, P parts at a time: a
+// thread has the loads of 2 P parts in flight (P: what the kernel has registers
+// for) and raises its maximum once per P.
+template <int ROWS, int D, int P>
+__device__ __forceinline__ void kv_join(const KvAttendParams &p, const KvParts &q, const KvRequest &r, const KvPiece &c,
+                                        int32_t nrows, int tid, int threads) {
+    constexpr int U = 2;
+    const int items = nrows * (D / 4);
+    for (int i0 = tid; i0 < items; i0 += U * threads) {
+        float4 acc[U];
+        float mm[U], sum[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f), mm[u] = -INFINITY, sum[u] = 0.0f;
+        for (int32_t k0 = 0; k0 < q.n; k0 += P) {
+            float4 y[U][P];
+            float2 s[U][P];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = min(i0 + u * threads, items - 1), lr = i / (D / 4), v4 = i % (D / 4);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    // the first CTA's part is in its second slot, every other one's
+                    // in its first
+                    const int32_t kk = min(k0 + k, q.n - 1);
+                    const int64_t at = q.first + (2 * kk + (kk == 0)) * ROWS + lr;
+                    s[u][k] = __ldcg(&p.part_ml[at]);
+                    y[u][k] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D) + v4);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float mn = mm[u];
+#pragma unroll
+                for (int k = 0; k < P; ++k) mn = fmaxf(mn, s[u][k].x);
+                const float f0 = mm[u] == -INFINITY ? 0.0f : ex2(mm[u] - mn);
+                mm[u] = mn;
+                sum[u] *= f0;
+                acc[u].x *= f0, acc[u].y *= f0, acc[u].z *= f0, acc[u].w *= f0;
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    const float g = k0 + k < q.n && s[u][k].x != -INFINITY ? ex2(s[u][k].x - mn) : 0.0f;
+                    // a part that does not count (g = 0) may hold anything
+                    const float4 v = g == 0.0f ? make_float4(0.f, 0.f, 0.f, 0.f) : y[u][k];
+                    sum[u] = g == 0.0f ? sum[u] : fmaf(g, s[u][k].y, sum[u]);
+                    acc[u].x = fmaf(g, v.x, acc[u].x), acc[u].y = fmaf(g, v.y, acc[u].y);
+                    acc[u].z = fmaf(g, v.z, acc[u].z), acc[u].w = fmaf(g, v.w, acc[u].w);
+                }
+            }
         }
-        kv_emit<ROWS, D>(p, r, c, lr, v4 * 4, mm, sum, acc);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * threads;
+            if (i < items) kv_emit<ROWS, D>(p, r, c, i / (D / 4), (i % (D / 4)) * 4, mm[u], sum[u], acc[u]);
+        }
     }
-    if (threadIdx.x == 0) p.counters[ci] = 0;
 }
 
 template <int D, bool Q8, int WK, int WR, int NT>
@@ -716,7 +768,10 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
             consumers_sync();
         }
 
-        if (!whole) kv_join<ROWS, D>(p, w, r, c, nrows, last_flag);
+        if (!whole) {
+            const KvParts q = kv_parts<ROWS>(p, w, r, c);
+            if (kv_arrive(p, q, last_flag)) kv_join<ROWS, D, 8>(p, q, r, c, nrows, (int)threadIdx.x, 128);
+        }
         kv_advance<ROWS>(p, w, r, c.jb - c.ja);
     }
     if (!ok && warp == 0 && lane == 0) {

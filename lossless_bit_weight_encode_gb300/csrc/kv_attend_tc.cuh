@@ -30,6 +30,14 @@ namespace dev {
 constexpr int kTcRows = 128;
 constexpr int kTcInfo = 16;  // ring of per-tile facts (present slices, scales)
 
+// A row block whose last part this CTA brought (at most two: its first and its
+// last one).
+struct TcJoin {
+    KvParts q;
+    KvRequest r;
+    KvPiece c;
+};
+
 template <int D, bool Q8>
 struct AttendTcCfg {
     static constexpr int kBlocks = D / 64;                 // 128-byte column blocks of an operand row
@@ -44,11 +52,13 @@ struct AttendTcCfg {
     static constexpr int kOffV = kOffK + kOps * kTileBytes;
     static constexpr int kOffRaw = kOffV + kOps * kTileBytes;  // K, V of stage 0, K, V of stage 1, ...
     static constexpr int kOffRawScale = kOffRaw + kRaws * 2 * kRawBytes;
-    static constexpr int kOffScale = kOffRawScale + kRaws * 512;  // [kTcInfo][2][64] fp32 (Q8)
-    static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * 512 : 0);
+    static constexpr int kInfoBytes = 528;  // 64 key scales, 64 value scales, the largest key scale
+    static constexpr int kOffScale = kOffRawScale + kRaws * 512;  // [kTcInfo][kInfoBytes] (Q8)
+    static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * kInfoBytes : 0);
     static constexpr int kBars = 4 * kOps + 2 * kRaws + 2 + 2 + 2 + 3;
     static constexpr int kOffInfo = kOffBars + 8 * kBars;
-    static constexpr int kSmemBytes = kOffInfo + 4 * kTcInfo + 32 + 1024;  // 1024: alignment
+    static constexpr int kOffJoins = kOffInfo + 4 * kTcInfo + 32;
+    static constexpr int kSmemBytes = kOffJoins + 2 * (int)sizeof(TcJoin) + 1024;  // 1024: alignment
     static constexpr int kThreads = Q8 ? 320 : 192;
     static constexpr int kTmemCols = D == 256 ? 512 : 256;
     static constexpr int kSCol = D == 256 ? 256 : 128;  // two S buffers of 64 columns; O from column 0
@@ -122,6 +132,99 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t use, uint64_t de
     return mbar_wait(bar, use & 1u, deadline);
 }
 
+// The softmax of one row's 64 scores, in two passes over TMEM (columns ts .. of the
+// thread's lane): the maximum, then the weights.  Reading them twice costs less
+// than the registers of all 64.  sc: the keys' 64 scales (with the softmax scale)
+// and the values' 64 (Q8).  EDGE: only the keys of `seen`.  EXACT (Q8): the largest
+// score; else the largest product before the scales, which with the tile's largest
+// scale bounds the scores and mostly shows that the running maximum can stay.
+template <bool Q8, bool EDGE, bool EXACT>
+__device__ __forceinline__ float tc_tile_max(uint32_t ts, const float *sc, uint64_t seen) {
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int h = 0; h < 64; h += 32) {
+        uint32_t x[32];
+        tmem_ld32(ts + h, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(x[k + e]);
+            if (Q8 && EXACT) {
+                const float4 s = *reinterpret_cast<const float4 *>(sc + h + k);
+                const f2 a = make_f2(y[0], y[1]) * make_f2(s.x, s.y), b = make_f2(y[2], y[3]) * make_f2(s.z, s.w);
+                y[0] = f2_lo(a), y[1] = f2_hi(a), y[2] = f2_lo(b), y[3] = f2_hi(b);
+            }
+            if (EDGE) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!((uint32_t)(seen >> h) & (1u << (k + e)))) y[e] = -INFINITY;
+            }
+            if (Q8 && !EXACT) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fabsf(y[e]);
+            }
+            top[0] = fmaxf(fmaxf(top[0], y[0]), y[1]);
+            top[1] = fmaxf(fmaxf(top[1], y[2]), y[3]);
+        }
+    }
+    return fmaxf(top[0], top[1]);
+}
+
+// Weights 2^(score - m) as BF16 over the scores (columns ts .. ts + 31); returns
+// their sum.
+template <bool Q8, bool EDGE>
+__device__ __forceinline__ float tc_tile_weights(uint32_t ts, const float *sc, float scale, float m, uint64_t seen) {
+    const f2 minus = make_f2(-m, -m), scale2 = make_f2(scale, scale);
+    f2 l0 = make_f2(0.0f, 0.0f), l1 = l0;
+#pragma unroll
+    for (int h = 0; h < 64; h += 32) {
+        uint32_t x[32], pk[16];
+        tmem_ld32(ts + h, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            f2 y0 = make_f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            f2 y1 = make_f2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+            if (Q8) {
+                const float4 s = *reinterpret_cast<const float4 *>(sc + h + k);
+                y0 = fma2(y0, make_f2(s.x, s.y), minus);
+                y1 = fma2(y1, make_f2(s.z, s.w), minus);
+            } else {
+                y0 = fma2(y0, scale2, minus);
+                y1 = fma2(y1, scale2, minus);
+            }
+            float e[4] = {ex2(f2_lo(y0)), ex2(f2_hi(y0)), ex2(f2_lo(y1)), ex2(f2_hi(y1))};
+            if (EDGE) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!((uint32_t)(seen >> h) & (1u << (k + i)))) e[i] = 0.0f;
+            }
+            f2 e0 = make_f2(e[0], e[1]), e1 = make_f2(e[2], e[3]);
+            l0 = l0 + e0;
+            l1 = l1 + e1;
+            if (Q8) {
+                float4 s = *reinterpret_cast<const float4 *>(sc + 64 + h + k);
+                if (EDGE) {  // an unseen key's scale may be anything
+                    const uint32_t b = (uint32_t)(seen >> h) >> k;
+                    s.x = b & 1u ? s.x : 0.0f, s.y = b & 2u ? s.y : 0.0f;
+                    s.z = b & 4u ? s.z : 0.0f, s.w = b & 8u ? s.w : 0.0f;
+                }
+                e0 = e0 * make_f2(s.x, s.y);
+                e1 = e1 * make_f2(s.z, s.w);
+            }
+            pk[k / 2] = pack_bf16(f2_lo(e0), f2_hi(e0));
+            pk[k / 2 + 1] = pack_bf16(f2_lo(e1), f2_hi(e1));
+        }
+        // over scores that both passes have read
+        tmem_st16(ts + h / 2, pk);
+    }
+    tmem_wait_st();
+    l0 = l0 + l1;
+    return f2_lo(l0) + f2_hi(l0);
+}
+
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     w12_kv_attend_tc_kernel(const KvAttendParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -138,6 +241,8 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     volatile uint32_t *last_flag = present + kTcInfo;
     volatile uint32_t *poison = last_flag + 1;
     uint32_t *tmem_slot = const_cast<uint32_t *>(last_flag) + 2;
+    volatile uint32_t *n_joins = last_flag + 3;
+    TcJoin *joins = reinterpret_cast<TcJoin *>(smem + C::kOffJoins);
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -161,6 +266,7 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         mbar_init(drain, 1);
         fence_mbar_init();
         *poison = 0;
+        *n_joins = 0;
     }
     if (threadIdx.x == 128) {
         prefetch_tmap(&tm_k);
@@ -329,6 +435,14 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         uint32_t it = 0;
         constexpr uint32_t N = C::kRaws + !Q8;
         constexpr int CH = D / 16;  // 16-byte chunks of a row
+        // the thread's first chunk and where its two operand chunks go; odd column
+        // blocks in the other order, so that eight lanes write eight different
+        // 16-byte bank groups
+        const int ckey = ct / CH, cc = ct % CH;
+        const bool turn = (cc / 4) & 1;
+        const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
+        const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
+        const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
         while (ok && w.u < w.end) {
             const KvPiece c = kv_piece(w, r);
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
@@ -337,11 +451,23 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                 if (ok && it > 0) ok = tc_wait(&kempty[0], it - 1, deadline);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
-                // scales of the tile's keys, the softmax scale in the keys' ones
-                {
-                    const float *src = reinterpret_cast<const float *>(smem + C::kOffRawScale + stage * 512);
-                    float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (it % kTcInfo) * 512);
-                    dst[ct] = src[2 * (ct & 63) + (ct >> 6)] * (ct < 64 ? p.scale_log2 : 1.0f);
+                // scales of the tile's keys, the softmax scale in the keys' ones,
+                // and the largest of those
+                if (warp < 8) {
+                    const float2 *src = reinterpret_cast<const float2 *>(smem + C::kOffRawScale + stage * 512);
+                    float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes);
+                    if (warp == 6) {
+                        const float a = src[lane].x * p.scale_log2, b = src[lane + 32].x * p.scale_log2;
+                        dst[lane] = a;
+                        dst[lane + 32] = b;
+                        float top = max_nan(fabsf(a), fabsf(b));
+#pragma unroll
+                        for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+                        if (lane == 0) dst[128] = top;
+                    } else {
+                        dst[64 + lane] = src[lane].y;
+                        dst[96 + lane] = src[lane + 32].y;
+                    }
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
@@ -350,31 +476,27 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                         ok = __all_sync(~0u, ok);
                         if (!ok) break;
                     }
-                    const uint32_t src = smem_u32(smem + C::kOffRaw + (stage * 2 + kv) * C::kRawBytes);
-                    const uint32_t dst = smem_u32(smem + (kv ? C::kOffV : C::kOffK));
+                    const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + kv) * C::kRawBytes) + ct;
+                    uint8_t *dst = smem + (kv ? C::kOffV : C::kOffK);
+                    constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
+                    constexpr int G = N4 < 4 ? N4 : 4;
 #pragma unroll
-                    for (int i = 0; i < kAttendTile * CH / 128; ++i) {
-                        const int ch = i * 128 + ct, key = ch / CH, cc = ch % CH;
-                        const uint4 u = lds128(src + ch * 16);
-                        uint4 a, b;
-                        q8_to_bf16(u.x, a.x, a.y);
-                        q8_to_bf16(u.y, a.z, a.w);
-                        q8_to_bf16(u.z, b.x, b.y);
-                        q8_to_bf16(u.w, b.z, b.w);
-                        const uint32_t at = dst + (cc / 4) * (kAttendTile * 128) + key * 128;
-                        const uint32_t a0 = at + (((2 * (cc % 4)) ^ (key & 7)) << 4);
-                        const uint32_t a1 = at + (((2 * (cc % 4) + 1) ^ (key & 7)) << 4);
-                        // odd column blocks the other way round: eight lanes then
-                        // write eight different 16-byte bank groups
-                        const bool turn = (cc / 4) & 1;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(turn ? a1 : a0),
-                                     "r"(turn ? b.x : a.x), "r"(turn ? b.y : a.y), "r"(turn ? b.z : a.z),
-                                     "r"(turn ? b.w : a.w)
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(turn ? a0 : a1),
-                                     "r"(turn ? a.x : b.x), "r"(turn ? a.y : b.y), "r"(turn ? a.z : b.z),
-                                     "r"(turn ? a.w : b.w)
-                                     : "memory");
+                    for (int i0 = 0; i0 < N4; i0 += G) {
+                        uint4 u[G];
+#pragma unroll
+                        for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
+#pragma unroll
+                        for (int i = 0; i < G; ++i) {
+                            uint4 a, b;
+                            q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
+                            q8_to_bf16(turn ? u[i].w : u[i].y, a.z, a.w);
+                            q8_to_bf16(turn ? u[i].x : u[i].z, b.x, b.y);
+                            q8_to_bf16(turn ? u[i].y : u[i].w, b.z, b.w);
+                            // 128 / CH keys further: a multiple of 8, the same swizzle
+                            uint8_t *row = dst + (i0 + i) * (128 / CH) * 128;
+                            *reinterpret_cast<uint4 *>(row + at0) = a;
+                            *reinterpret_cast<uint4 *>(row + at1) = b;
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -439,38 +561,19 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                 const bool edge = kv_edge_tile(p, r, kb, here);
                 const uint32_t ts = tl + C::kSCol + 64 * (it & 1);
                 if (busy) {
-                    // Two passes over the scores in TMEM, 32 at a time: the maximum,
-                    // then the probabilities.  Reading them twice costs less than
-                    // the registers of all 64.
-                    const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * 512);
-                    uint64_t seen = ~0ull;
-                    if (edge) seen = kv_seen64(p, r, view, kb, here);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int h = 0; h < 64; h += 32) {
-                        uint32_t x[32];
-                        tmem_ld32(ts + h, x);
-                        tmem_wait_ld();
-                        if (Q8) {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float2 s = *reinterpret_cast<const float2 *>(sc + h + k);
-                                const f2 y = make_f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])) *
-                                             make_f2(s.x, s.y);
-                                x[k] = __float_as_uint(f2_lo(y));
-                                x[k + 1] = __float_as_uint(f2_hi(y));
-                            }
-                        }
-                        if (edge) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!((seen >> (h + k)) & 1ull)) x[k] = __float_as_uint(-INFINITY);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            top = fmaxf(fmaxf(top, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+                    const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes);
+                    const uint64_t seen = edge ? kv_seen64(p, r, view, kb, here) : ~0ull;
+                    float top;
+                    if (Q8) {
+                        top = edge ? INFINITY : tc_tile_max<Q8, false, false>(ts, sc, seen) * sc[128];
+                        // (not <=, so that a NaN scale takes this way too)
+                        if (__any_sync(~0u, !(top <= m + kAttendLazy)))
+                            top = edge ? tc_tile_max<Q8, true, true>(ts, sc, seen)
+                                       : tc_tile_max<Q8, false, true>(ts, sc, seen);
+                    } else {
+                        top = scale * (edge ? tc_tile_max<Q8, true, true>(ts, sc, seen)
+                                            : tc_tile_max<Q8, false, true>(ts, sc, seen));
                     }
-                    if (!Q8) top *= scale;
                     if (__any_sync(~0u, top > m + kAttendLazy)) {
                         const float mn = fmaxf(m, top);
                         const float al = mn == -INFINITY ? 1.0f : ex2(m - mn);
@@ -493,45 +596,8 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                         }
                     }
                     const float m0 = m == -INFINITY ? 0.0f : m;
-                    const f2 minus = make_f2(-m0, -m0), scale2 = make_f2(scale, scale);
-                    f2 l2 = make_f2(0.0f, 0.0f);
-#pragma unroll
-                    for (int h = 0; h < 64; h += 32) {
-                        uint32_t x[32], pk[16];
-                        tmem_ld32(ts + h, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            f2 y = make_f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-                            if (Q8) {
-                                const float2 s = *reinterpret_cast<const float2 *>(sc + h + k);
-                                y = y * make_f2(s.x, s.y) + minus;
-                            } else {
-                                y = fma2(y, scale2, minus);
-                            }
-                            float a = ex2(f2_lo(y)), b = ex2(f2_hi(y));
-                            if (edge) {
-                                if (!((seen >> (h + k)) & 1ull)) a = 0.0f;
-                                if (!((seen >> (h + k + 1)) & 1ull)) b = 0.0f;
-                            }
-                            f2 e = make_f2(a, b);
-                            l2 = l2 + e;
-                            if (Q8) {
-                                const float2 s = *reinterpret_cast<const float2 *>(sc + 64 + h + k);
-                                e = e * make_f2(s.x, s.y);
-                                // an unseen key's scale may be anything
-                                if (edge) {
-                                    if (!((seen >> (h + k)) & 1ull)) e = make_f2(0.0f, f2_hi(e));
-                                    if (!((seen >> (h + k + 1)) & 1ull)) e = make_f2(f2_lo(e), 0.0f);
-                                }
-                            }
-                            pk[k / 2] = pack_bf16(f2_lo(e), f2_hi(e));
-                        }
-                        // over scores that both passes have read
-                        tmem_st16(ts + h / 2, pk);
-                    }
-                    l += f2_lo(l2) + f2_hi(l2);
-                    tmem_wait_st();
+                    l += edge ? tc_tile_weights<Q8, true>(ts, sc, scale, m0, seen)
+                              : tc_tile_weights<Q8, false>(ts, sc, scale, m0, seen);
                 }
                 if (!Q8 && edge) {
                     // values behind the request's last token or of missing slices
@@ -655,7 +721,15 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(ofree);
-            if (!whole) kv_join<kTcRows, D>(p, w, r, c, nrows, last_flag);
+            if (!whole) {
+                const KvParts q = kv_parts<kTcRows>(p, w, r, c);
+                // joined by all warps at the end of the range
+                if (kv_arrive(p, q, last_flag) && threadIdx.x == 0) {
+                    TcJoin &e = joins[*n_joins];
+                    e.q = q, e.r = r, e.c = c;
+                    ++*n_joins;
+                }
+            }
             if (!more) break;
             w = w2;
             r = r2;
@@ -667,6 +741,11 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     __syncthreads();
     tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, C::kTmemCols);
+    for (uint32_t i = 0; i < *n_joins; ++i) {
+        const TcJoin e = joins[i];
+        const int32_t nrows = (int32_t)min((int64_t)kTcRows, (int64_t)e.r.qlen * p.group - (int64_t)e.c.rb * kTcRows);
+        kv_join<kTcRows, D, 4>(p, e.q, e.r, e.c, nrows, (int)threadIdx.x, C::kThreads);
+    }
 }
 
 }  // namespace dev

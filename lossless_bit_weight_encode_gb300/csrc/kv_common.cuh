@@ -91,6 +91,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// Maximum that keeps a NaN of either side.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Pairs of fp32 in one 64-bit register and the packed arithmetic on them (each
 // half rounds as the scalar operation does).
 struct f2 {

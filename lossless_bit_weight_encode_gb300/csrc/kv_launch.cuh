@@ -93,13 +93,10 @@ inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams
             void *k = reinterpret_cast<void *>(kernel);
             cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-            int occ = 0;
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, threads, (size_t)smem);
             if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend set-up", err);
-            if (occ < 1) {
-                *err = "w12_kv_attend cannot be resident on this device";
-                return W12_ERR_CUDA;
-            }
+            int occ = 0;
+            const int rc = resident_ctas(k, threads, smem, d.device, err, &occ);
+            if (rc != W12_OK) return rc;
             const int most = kPartElems / rows_dim;
             per_sm[d.device] = occ < most ? occ : most;
         }

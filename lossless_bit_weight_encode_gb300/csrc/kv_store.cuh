@@ -21,13 +21,6 @@ constexpr int kStoreThreads = 128;
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Maximum that keeps a NaN of either side.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 // Eight BF16 as four pairs, and back.
 __device__ __forceinline__ void unpack8(const uint4 &u, f2 (&x)[4]) {
     x[0] = make_f2(bf16_lo(u.x), bf16_hi(u.x)), x[1] = make_f2(bf16_lo(u.y), bf16_hi(u.y));

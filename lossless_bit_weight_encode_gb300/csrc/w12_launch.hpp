@@ -80,6 +80,9 @@ struct DeviceView {
 };
 int device_view(DeviceView *out, std::string *err);
 
+// CTAs of a kernel that fit an SM (kernels.cu).
+int resident_ctas(const void *kernel, int threads, int smem_bytes, int device, std::string *err, int *out);
+
 // The driver's cuTensorMapEncodeTiled (null and *err where it is missing).
 void *tensor_map_encode(std::string *err);
 
