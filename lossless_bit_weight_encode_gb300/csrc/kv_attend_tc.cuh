@@ -38,6 +38,14 @@ struct TcJoin {
     KvPiece c;
 };
 
+// A softmax warp's place: kept in shared memory, so that the loop over a piece's
+// tiles has the registers.
+struct TcPlace {
+    KvWalk w;
+    KvRequest r;
+    KvPiece c;
+};
+
 template <int D, bool Q8>
 struct AttendTcCfg {
     static constexpr int kBlocks = D / 64;                 // 128-byte column blocks of an operand row
@@ -55,10 +63,11 @@ struct AttendTcCfg {
     static constexpr int kInfoBytes = 528;  // 64 key scales, 64 value scales, the largest key scale
     static constexpr int kOffScale = kOffRawScale + kRaws * 512;  // [kTcInfo][kInfoBytes] (Q8)
     static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * kInfoBytes : 0);
-    static constexpr int kBars = 4 * kOps + 2 * kRaws + 2 + 2 + 2 + 3;
+    static constexpr int kBars = 4 * kOps + 4 * kRaws + 2 + 2 + 2 + 3;
     static constexpr int kOffInfo = kOffBars + 8 * kBars;
     static constexpr int kOffJoins = kOffInfo + 4 * kTcInfo + 32;
-    static constexpr int kSmemBytes = kOffJoins + 2 * (int)sizeof(TcJoin) + 1024;  // 1024: alignment
+    static constexpr int kOffPlaces = kOffJoins + 2 * (int)sizeof(TcJoin);
+    static constexpr int kSmemBytes = kOffPlaces + 4 * (int)sizeof(TcPlace) + 1024;  // 1024: alignment
     static constexpr int kThreads = Q8 ? 320 : 192;
     static constexpr int kTmemCols = D == 256 ? 512 : 256;
     static constexpr int kSCol = D == 256 ? 256 : 128;  // two S buffers of 64 columns; O from column 0
@@ -97,20 +106,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int3
         : "memory");
 }
 
-// A tile whose keys not all rows see, or of which a slice is missing.
-__device__ __forceinline__ bool kv_edge_tile(const KvAttendParams &p, const KvRequest &r, int32_t kb, uint32_t present) {
-    return present != 15u || (int64_t)kb + kAttendTile > (p.tree ? r.past : r.past + 1) ||
-           kb + kAttendTile > r.kv || (p.window > 0 && kb <= (int64_t)r.past + r.qlen - 1 - p.window);
-}
-
 __device__ __forceinline__ uint64_t low_bits(int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
 // Bit k: the row sees key kb + k of the tile (kv_sees and the present slices).
-__device__ __forceinline__ uint64_t kv_seen64(const KvAttendParams &p, const KvRequest &r, const KvRowView &v, int32_t kb,
-                                              uint32_t present) {
-    uint64_t m = low_bits((int64_t)r.kv - kb);
+__device__ __forceinline__ uint64_t kv_seen64(const KvAttendParams &p, int32_t kv, int32_t past, const KvRowView &v,
+                                              int32_t kb, uint32_t present) {
+    uint64_t m = low_bits((int64_t)kv - kb);
     if (p.tree) {
-        const int64_t sh = (int64_t)r.past - kb;
+        const int64_t sh = (int64_t)past - kb;
         const uint64_t drawn = sh >= 64 ? 0 : sh >= 0 ? (uint64_t)v.tree << sh : sh > -32 ? (uint64_t)(v.tree >> -sh) : 0;
         m &= low_bits(sh) | drawn;
     } else {
@@ -141,7 +144,7 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t use, uint64_t de
 template <bool Q8, bool EDGE, bool EXACT>
 __device__ __forceinline__ float tc_tile_max(uint32_t ts, const float *sc, uint64_t seen) {
     float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 64; h += 32) {
         uint32_t x[32];
         tmem_ld32(ts + h, x);
@@ -178,7 +181,7 @@ template <bool Q8, bool EDGE>
 __device__ __forceinline__ float tc_tile_weights(uint32_t ts, const float *sc, float scale, float m, uint64_t seen) {
     const f2 minus = make_f2(-m, -m), scale2 = make_f2(scale, scale);
     f2 l0 = make_f2(0.0f, 0.0f), l1 = l0;
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 64; h += 32) {
         uint32_t x[32], pk[16];
         tmem_ld32(ts + h, x);
@@ -234,8 +237,9 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + C::kOffBars), *kempty = kfull + C::kOps;
     uint64_t *vfull = kempty + C::kOps, *vempty = vfull + C::kOps;
-    uint64_t *rfull = vempty + C::kOps, *rempty = rfull + C::kRaws;
-    uint64_t *sfull = rempty + C::kRaws, *pfull = sfull + 2;
+    uint64_t *rkfull = vempty + C::kOps, *rkempty = rkfull + C::kRaws;
+    uint64_t *rvfull = rkempty + C::kRaws, *rvempty = rvfull + C::kRaws;
+    uint64_t *sfull = rvempty + C::kRaws, *pfull = sfull + 2;
     uint64_t *pvdone = pfull + 2, *qfull = pvdone + 2, *ofree = qfull + 1, *drain = ofree + 1;
     uint32_t *present = reinterpret_cast<uint32_t *>(smem + C::kOffInfo);
     volatile uint32_t *last_flag = present + kTcInfo;
@@ -253,8 +257,10 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
             mbar_init(&vempty[i], 1);
         }
         for (int i = 0; i < C::kRaws; ++i) {
-            mbar_init(&rfull[i], 1);
-            mbar_init(&rempty[i], 4);
+            mbar_init(&rkfull[i], 1);
+            mbar_init(&rkempty[i], 4);
+            mbar_init(&rvfull[i], 1);
+            mbar_init(&rvempty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
@@ -311,52 +317,39 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                 const bool here = page >= 0 && page < p.num_pages;
                 const uint32_t mask = __ballot_sync(~0u, here) & 15u;
                 const uint32_t n = (uint32_t)__popc(mask);
-                if (Q8) {
-                    const uint32_t stage = it % (C::kRaws + !Q8), use = it / (C::kRaws + !Q8);
-                    if (use > 0) ok = tc_wait(&rempty[stage], use - 1, deadline);
-                    ok = __shfl_sync(~0u, ok, 0);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        present[it % kTcInfo] = mask;
-                        mbar_arrive_expect_tx(&rfull[stage], n * (2 * kAttendSlice * D + 128));
-                    }
-                    __syncwarp();
-                    if (here) {
-                        const uint32_t dst = smem_u32(smem + C::kOffRaw + stage * 2 * C::kRawBytes + s * kAttendSlice * D);
-                        const uint32_t bar = smem_u32(&rfull[stage]);
-                        tma_load_4d(dst, &tm_k, 0, off, c.head, page, bar);
-                        tma_load_4d(dst + C::kRawBytes, &tm_v, 0, off, c.head, page, bar);
-                        bulk_g2s(smem + C::kOffRawScale + stage * 512 + s * 128,
-                                 p.scales + (((int64_t)page * p.kv_heads + c.head) * p.page_size + off) * 2, 128,
-                                 &rfull[stage]);
-                    }
-                } else {
-                    const uint32_t stage = it % C::kOps, use = it / C::kOps;
-                    const uint32_t at = stage * C::kTileBytes + blk * (kAttendTile * 128) + s * (kAttendSlice * 128);
-                    if (use > 0) ok = tc_wait(&kempty[stage], use - 1, deadline);
-                    ok = __shfl_sync(~0u, ok, 0);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        present[it % kTcInfo] = mask;
-                        mbar_arrive_expect_tx(&kfull[stage], n * (kAttendSlice * D * 2));
-                    }
-                    __syncwarp();
-                    if (here)
-                        tma_load_4d(smem_u32(smem + C::kOffK + at), &tm_k, 64 * blk, off, c.head, page,
-                                    smem_u32(&kfull[stage]));
-                    if (use > 0) ok = tc_wait(&vempty[stage], use - 1, deadline);
-                    ok = __shfl_sync(~0u, ok, 0);
-                    if (!ok) {
-                        // its keys are on their way: wait for them below
-                        ++it;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&vfull[stage], n * (kAttendSlice * D * 2));
-                    __syncwarp();
-                    if (here)
-                        tma_load_4d(smem_u32(smem + C::kOffV + at), &tm_v, 64 * blk, off, c.head, page,
-                                    smem_u32(&vfull[stage]));
+                constexpr uint32_t N = Q8 ? C::kRaws : C::kOps;
+                constexpr uint32_t bytes = kAttendSlice * D * (Q8 ? 1 : 2);
+                const uint32_t stage = it % N, use = it / N;
+                uint64_t *const kbar = Q8 ? &rkfull[stage] : &kfull[stage];
+                uint64_t *const vbar = Q8 ? &rvfull[stage] : &vfull[stage];
+                const uint32_t at = Q8 ? C::kOffRaw + stage * 2 * C::kRawBytes + s * bytes
+                                       : stage * C::kTileBytes + blk * (kAttendTile * 128) + s * (kAttendSlice * 128);
+                if (use > 0) ok = tc_wait(Q8 ? &rkempty[stage] : &kempty[stage], use - 1, deadline);
+                ok = __shfl_sync(~0u, ok, 0);
+                if (!ok) break;
+                if (lane == 0) {
+                    present[it % kTcInfo] = mask;
+                    mbar_arrive_expect_tx(kbar, n * (bytes + (Q8 ? 128 : 0)));
                 }
+                __syncwarp();
+                if (here) {
+                    tma_load_4d(smem_u32(smem + (Q8 ? at : C::kOffK + at)), &tm_k, Q8 ? 0 : 64 * blk, off, c.head, page,
+                                smem_u32(kbar));
+                    if (Q8)
+                        bulk_g2s(smem + C::kOffRawScale + stage * 512 + s * 128,
+                                 p.scales + (((int64_t)page * p.kv_heads + c.head) * p.page_size + off) * 2, 128, kbar);
+                }
+                if (use > 0) ok = tc_wait(Q8 ? &rvempty[stage] : &vempty[stage], use - 1, deadline);
+                ok = __shfl_sync(~0u, ok, 0);
+                if (!ok) {
+                    ++it;  // its keys are on their way: waited for below
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(vbar, n * bytes);
+                __syncwarp();
+                if (here)
+                    tma_load_4d(smem_u32(smem + (Q8 ? at + C::kRawBytes : C::kOffV + at)), &tm_v, Q8 ? 0 : 64 * blk, off,
+                                c.head, page, smem_u32(vbar));
             }
             if (ok) kv_advance<kTcRows>(p, w, r, c.jb - c.ja);
         }
@@ -365,11 +358,11 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         if (!ok && lane == 0) {
             atomicOr(p.status, 8u);
             const uint64_t late = globaltimer_ns() + p.timeout_ns;
-            constexpr uint32_t N = Q8 ? C::kRaws + !Q8 : C::kOps;
-            for (uint32_t k = it > N ? it - N : 0; k < it; ++k) {
-                if (!tc_wait(Q8 ? &rfull[k % N] : &kfull[k % N], k / N, late)) break;
-                if (!Q8 && !tc_wait(&vfull[k % N], k / N, late)) break;
-            }
+            constexpr uint32_t N = Q8 ? C::kRaws : C::kOps;
+            for (uint32_t k = it > N ? it - N : 0; k < it; ++k)
+                if (!tc_wait(Q8 ? &rkfull[k % N] : &kfull[k % N], k / N, late) ||
+                    !tc_wait(Q8 ? &rvfull[k % N] : &vfull[k % N], k / N, late))
+                    break;
         }
         __syncwarp();
     } else if (warp == 5) {
@@ -432,7 +425,6 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     } else if (warp >= 6) {
         // ------------------------------------------------------------ converters (Q8)
         const int ct = (warp - 6) * 32 + lane;
-        uint32_t it = 0;
         constexpr uint32_t N = C::kRaws + !Q8;
         constexpr int CH = D / 16;  // 16-byte chunks of a row
         // the thread's first chunk and where its two operand chunks go; odd column
@@ -443,68 +435,68 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
         const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
         const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
-        while (ok && w.u < w.end) {
-            const KvPiece c = kv_piece(w, r);
-            for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
-                const uint32_t stage = it % N;
-                ok = tc_wait(&rfull[stage], it / N, deadline);
-                if (ok && it > 0) ok = tc_wait(&kempty[0], it - 1, deadline);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
-                // scales of the tile's keys, the softmax scale in the keys' ones,
-                // and the largest of those
-                if (warp < 8) {
-                    const float2 *src = reinterpret_cast<const float2 *>(smem + C::kOffRawScale + stage * 512);
-                    float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes);
-                    if (warp == 6) {
-                        const float a = src[lane].x * p.scale_log2, b = src[lane + 32].x * p.scale_log2;
-                        dst[lane] = a;
-                        dst[lane + 32] = b;
-                        float top = max_nan(fabsf(a), fabsf(b));
+        const uint32_t total = (uint32_t)(w.end - w.u);
+        // K or V of tile x to its operand buffer, which the tile before must have left
+        auto convert = [&](bool values, uint32_t x) -> bool {
+            const uint32_t stage = x % N;
+            bool good = tc_wait(values ? &rvfull[stage] : &rkfull[stage], x / N, deadline);
+            if (good && x > 0) good = tc_wait(values ? &vempty[0] : &kempty[0], x - 1, deadline);
+            if (!__all_sync(~0u, good)) return false;
+            if (!values && warp < 8) {
+                // scales of the tile's keys, the softmax scale in the keys' ones, and
+                // the largest of those
+                const float2 *src = reinterpret_cast<const float2 *>(smem + C::kOffRawScale + stage * 512);
+                float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (x % kTcInfo) * C::kInfoBytes);
+                if (warp == 6) {
+                    const float a = src[lane].x * p.scale_log2, b = src[lane + 32].x * p.scale_log2;
+                    dst[lane] = a;
+                    dst[lane + 32] = b;
+                    float top = max_nan(fabsf(a), fabsf(b));
 #pragma unroll
-                        for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
-                        if (lane == 0) dst[128] = top;
-                    } else {
-                        dst[64 + lane] = src[lane].y;
-                        dst[96 + lane] = src[lane + 32].y;
-                    }
+                    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+                    if (lane == 0) dst[128] = top;
+                } else {
+                    dst[64 + lane] = src[lane].y;
+                    dst[96 + lane] = src[lane + 32].y;
                 }
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (kv == 1) {
-                        if (it > 0) ok = tc_wait(&vempty[0], it - 1, deadline);
-                        ok = __all_sync(~0u, ok);
-                        if (!ok) break;
-                    }
-                    const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + kv) * C::kRawBytes) + ct;
-                    uint8_t *dst = smem + (kv ? C::kOffV : C::kOffK);
-                    constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
-                    constexpr int G = N4 < 4 ? N4 : 4;
-#pragma unroll
-                    for (int i0 = 0; i0 < N4; i0 += G) {
-                        uint4 u[G];
-#pragma unroll
-                        for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
-#pragma unroll
-                        for (int i = 0; i < G; ++i) {
-                            uint4 a, b;
-                            q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
-                            q8_to_bf16(turn ? u[i].w : u[i].y, a.z, a.w);
-                            q8_to_bf16(turn ? u[i].x : u[i].z, b.x, b.y);
-                            q8_to_bf16(turn ? u[i].y : u[i].w, b.z, b.w);
-                            // 128 / CH keys further: a multiple of 8, the same swizzle
-                            uint8_t *row = dst + (i0 + i) * (128 / CH) * 128;
-                            *reinterpret_cast<uint4 *>(row + at0) = a;
-                            *reinterpret_cast<uint4 *>(row + at1) = b;
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(kv ? &vfull[0] : &kfull[0]);
-                }
-                if (ok && lane == 0) mbar_arrive(&rempty[stage]);
             }
-            if (ok) kv_advance<kTcRows>(p, w, r, c.jb - c.ja);
+            const uint4 *src =
+                reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + values) * C::kRawBytes) + ct;
+            uint8_t *dst = smem + (values ? C::kOffV : C::kOffK);
+            constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
+            constexpr int G = N4 < 4 ? N4 : 4;
+#pragma unroll
+            for (int i0 = 0; i0 < N4; i0 += G) {
+                uint4 u[G];
+#pragma unroll
+                for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    uint4 a, b;
+                    q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
+                    q8_to_bf16(turn ? u[i].w : u[i].y, a.z, a.w);
+                    q8_to_bf16(turn ? u[i].x : u[i].z, b.x, b.y);
+                    q8_to_bf16(turn ? u[i].y : u[i].w, b.z, b.w);
+                    // 128 / CH keys further: a multiple of 8, the same swizzle
+                    uint8_t *row = dst + (i0 + i) * (128 / CH) * 128;
+                    *reinterpret_cast<uint4 *>(row + at0) = a;
+                    *reinterpret_cast<uint4 *>(row + at1) = b;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(values ? &vfull[0] : &kfull[0]);
+                mbar_arrive(values ? &rvempty[stage] : &rkempty[stage]);
+            }
+            return true;
+        };
+        // the keys run one tile ahead: their buffer is free as soon as the scores
+        // are made, the values' only after the softmax
+        ok = convert(false, 0);
+        for (uint32_t x = 0; ok && x < total; ++x) {
+            if (x + 1 < total) ok = convert(false, x + 1);
+            ok = ok && convert(true, x);
         }
         if (!ok && lane == 0) atomicOr(p.status, 8u);
     } else {
@@ -515,7 +507,9 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         // largest product
         const float scale = fabsf(p.scale_log2);
         uint32_t it = 0;
-        KvPiece c = kv_piece(w, r);
+        TcPlace &place = reinterpret_cast<TcPlace *>(smem + C::kOffPlaces)[warp];
+        if (lane == 0) place = TcPlace{w, r, kv_piece(w, r)};
+        __syncwarp();
         // Q rows of a piece to shared memory, rows behind the last one zero
         auto load_q = [&](const KvRequest &rq, const KvPiece &pc) {
             const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
@@ -541,28 +535,40 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
         };
-        load_q(r, c);
+        load_q(place.r, place.c);
         while (true) {
-            const int32_t nrows = (int32_t)min((int64_t)kTcRows, (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows);
-            const bool busy = 32 * warp < nrows;  // a warp without rows only keeps step
-            const int32_t i = min(c.rb * kTcRows + lr, c.rb * kTcRows + nrows - 1) / p.group;
+            int32_t nrows, i, kb, tiles, keys, past, lim, low;
             KvRowView view;
-            view.index = kv_index(r, i);
-            view.tree = p.tree ? p.tree[r.q0 + i] : 0u;
+            {
+                const KvRequest &r = place.r;
+                const KvPiece &c = place.c;
+                nrows = (int32_t)min((int64_t)kTcRows, (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows);
+                i = min(c.rb * kTcRows + lr, c.rb * kTcRows + nrows - 1) / p.group;
+                view.index = kv_index(r, i);
+                view.tree = p.tree ? p.tree[r.q0 + i] : 0u;
+                kb = (r.tile0 + c.ja) * kAttendTile;
+                tiles = c.jb - c.ja;
+                keys = r.kv;
+                past = r.past;
+                // every row sees the keys from low on and before lim
+                lim = min(r.kv, p.tree ? r.past : r.past + 1);
+                low = p.window > 0 ? (int32_t)max((int64_t)r.past + r.qlen - p.window, (int64_t)0) : 0;
+            }
+            const bool busy = 32 * warp < nrows;  // a warp without rows only keeps step
             float m = -INFINITY, l = 0.0f;
-            for (int j = c.ja; j < c.jb; ++j, ++it) {
+            for (int j = 0; j < tiles; ++j, ++it, kb += kAttendTile) {
                 // after a timeout the walk goes on without waiting, so that every
                 // barrier below is reached
                 if (ok) ok = tc_wait(&sfull[it & 1], it >> 1, deadline);
                 ok = __all_sync(~0u, ok);
                 tc_fence_after();
-                const int32_t kb = (r.tile0 + j) * kAttendTile;
                 const uint32_t here = present[it % kTcInfo];
-                const bool edge = kv_edge_tile(p, r, kb, here);
+                // a tile whose keys not all rows see, or of which a slice is missing
+                const bool edge = here != 15u || kb > lim - kAttendTile || kb < low;
                 const uint32_t ts = tl + C::kSCol + 64 * (it & 1);
                 if (busy) {
                     const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes);
-                    const uint64_t seen = edge ? kv_seen64(p, r, view, kb, here) : ~0ull;
+                    const uint64_t seen = edge ? kv_seen64(p, keys, past, view, kb, here) : ~0ull;
                     float top;
                     if (Q8) {
                         top = edge ? INFINITY : tc_tile_max<Q8, false, false>(ts, sc, seen) * sc[128];
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                         const float al = mn == -INFINITY ? 1.0f : ex2(m - mn);
                         m = mn;
                         l *= al;
-                        if (j > c.ja) {
+                        if (j > 0) {
                             if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
                             ok = __all_sync(~0u, ok);
                             tc_fence_after();
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                                                               (ch / 8) * (kAttendTile * 128) + key * 128 +
                                                               (((ch % 8) ^ (key & 7)) << 4));
                         uint4 u = *at;
-                        if (kb + key >= r.kv || !((here >> (key / 16)) & 1u)) {
+                        if (kb + key >= keys || !((here >> (key / 16)) & 1u)) {
                             *at = make_uint4(0, 0, 0, 0);
                         } else {
                             uint32_t e[4] = {u.x, u.y, u.z, u.w};
@@ -637,19 +643,26 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
             }
             // the next piece's Q while the last products of this one run (all
             // scores of this piece are there, so nothing reads Q any more)
-            KvWalk w2 = w;
-            KvRequest r2 = r;
-            kv_advance<kTcRows>(p, w2, r2, c.jb - c.ja);
-            const bool more = w2.u < w2.end;
-            KvPiece c2 = c;
-            if (more) {
-                c2 = kv_piece(w2, r2);
-                load_q(r2, c2);
+            const KvWalk w1 = place.w;
+            const KvRequest r1 = place.r;
+            const KvPiece c1 = place.c;
+            bool more;
+            {
+                KvWalk w2 = w1;
+                KvRequest r2 = r1;
+                kv_advance<kTcRows>(p, w2, r2, tiles);
+                more = w2.u < w2.end;
+                if (more) {
+                    const KvPiece c2 = kv_piece(w2, r2);
+                    load_q(r2, c2);
+                    if (lane == 0) place = TcPlace{w2, r2, c2};
+                    __syncwarp();
+                }
             }
             if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
             ok = __all_sync(~0u, ok);
             tc_fence_after();
-            const bool whole = c.ja == 0 && c.jb == r.ntiles;
+            const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
             bool bad = false;
             if (!Q8) {
                 consumers_sync();  // every thread's note is in
@@ -660,10 +673,10 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                     consumers_sync();
                 }
             }
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (c.ja > 0 ? 0 : 1);
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (c1.ja > 0 ? 0 : 1);
             if (busy) {
-                const int32_t head = c.head * p.group + c.rb * kTcRows + lr - i * p.group;
-                uint16_t *dst = p.out + (r.q0 + i) * p.out_stride + (int64_t)head * D;
+                const int32_t head = c1.head * p.group + c1.rb * kTcRows + lr - i * p.group;
+                uint16_t *dst = p.out + (r1.q0 + i) * p.out_stride + (int64_t)head * D;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
                 for (int d0 = 0; d0 < D; d0 += 32) {
@@ -674,14 +687,14 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                         // values that are not finite count, as they are, for the
                         // rows that see their keys (a weight is positive; what went
                         // through the product already stays what it is)
-                        for (int j = c.ja; j < c.jb; ++j) {
-                            const int32_t kb = (r.tile0 + j) * kAttendTile;
-                            uint64_t seen = kv_seen64(p, r, view, kb, 15u);
+                        for (int j = c1.ja; j < c1.jb; ++j) {
+                            const int32_t kb = (r1.tile0 + j) * kAttendTile;
+                            uint64_t seen = kv_seen64(p, r1.kv, r1.past, view, kb, 15u);
                             for (; seen; seen &= seen - 1) {
                                 const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
-                                const int32_t page = p.tables[(int64_t)w.b * p.table_stride + e];
+                                const int32_t page = p.tables[(int64_t)w1.b * p.table_stride + e];
                                 if (page < 0 || page >= p.num_pages) continue;
-                                const uint16_t *v = p.v + page * p.v_page_stride + c.head * p.v_head_stride +
+                                const uint16_t *v = p.v + page * p.v_page_stride + c1.head * p.v_head_stride +
                                                     (int64_t)(key - e * p.page_size) * p.v_row_stride + d0;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
@@ -714,7 +727,7 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
                 if (lr < nrows) {
                     if (!whole) p.part_ml[slot * kTcRows + lr] = make_float2(m, l);
                     else if (p.lse)
-                        p.lse[(int64_t)(r.q0 + i) * (p.group * p.kv_heads) + head] =
+                        p.lse[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] =
                             l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
             }
@@ -722,18 +735,15 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(ofree);
             if (!whole) {
-                const KvParts q = kv_parts<kTcRows>(p, w, r, c);
+                const KvParts q = kv_parts<kTcRows>(p, w1, r1, c1);
                 // joined by all warps at the end of the range
                 if (kv_arrive(p, q, last_flag) && threadIdx.x == 0) {
                     TcJoin &e = joins[*n_joins];
-                    e.q = q, e.r = r, e.c = c;
+                    e.q = q, e.r = r1, e.c = c1;
                     ++*n_joins;
                 }
             }
             if (!more) break;
-            w = w2;
-            r = r2;
-            c = c2;
         }
         if (!ok && lane == 0) atomicOr(p.status, 8u);
     }
