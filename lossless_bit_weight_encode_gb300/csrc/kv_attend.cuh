@@ -25,7 +25,9 @@
 // all units form one line that the CTAs cut into equal ranges, whatever the
 // lengths.  A range that covers a row block's keys only in part leaves its
 // partial result in the workspace, and the CTA that arrives last at the block's
-// counter joins the parts in range order (the same result in every run).
+// counter joins the parts in range order (the same result in every run).  Where
+// that would be a long chain for one CTA (kv_launch.cuh has the rule), a second
+// kernel joins every row with a CTA of its own.
 //
 // Q8 cache: int8 elements become BF16 exactly in registers; a key's scale
 // multiplies its score, a value's scale its probability.
@@ -768,7 +770,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
             consumers_sync();
         }
 
-        if (!whole) {
+        if (!whole && !p.join_later) {
             const KvParts q = kv_parts<ROWS>(p, w, r, c);
             if (kv_arrive(p, q, last_flag)) kv_join<ROWS, D, 8>(p, q, r, c, nrows, (int)threadIdx.x, 128);
         }
@@ -780,6 +782,127 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
         for (uint32_t k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
             if (!mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1, late)) break;
     }
+}
+
+// Joins the parts of one output row (token blockIdx.x / heads, head the rest) of a
+// launch with ROWS-row blocks and `grid` CTAs; a row that one CTA had whole is
+// finished already.  Eight warps take the parts in turn, then meet in shared
+// memory, both in a fixed order.
+constexpr int kJoinThreads = 256;
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAttendParams p, int grid) {
+    constexpr int W = kJoinThreads / 32, V = D / 32;  // columns of a lane
+    __shared__ float s_acc[W][D];
+    __shared__ float2 s_ml[W];
+    __shared__ KvParts s_q;
+    __shared__ int32_t s_lr;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = p.group * p.kv_heads;
+    const int32_t tok = blockIdx.x / heads, h = blockIdx.x - tok * heads;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == 0) {
+        // the token's request, its first unit and all units
+        int64_t total = 0, start = -1;
+        int32_t mine = 0;
+        for (int b0 = 0; b0 < p.requests; b0 += 32) {
+            KvRequest r;
+            r.units = 0, r.q0 = r.qlen = 0;
+            if (b0 + lane < p.requests) r = kv_request<ROWS>(p, b0 + lane);
+            int64_t inc = r.units;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t x = __shfl_up_sync(~0u, inc, d);
+                if (lane >= d) inc += x;
+            }
+            const uint32_t hit = __ballot_sync(~0u, tok >= r.q0 && tok < r.q0 + r.qlen);
+            if (hit && start < 0) {
+                mine = b0 + __ffs(hit) - 1;
+                start = total + __shfl_sync(~0u, inc - r.units, __ffs(hit) - 1);
+            }
+            total += __shfl_sync(~0u, inc, 31);
+        }
+        if (lane == 0) {
+            s_q.n = 0;
+            if (start >= 0) {
+                KvWalk w;
+                const KvRequest r = kv_request<ROWS>(p, mine);
+                KvPiece c;
+                const int32_t rr = (tok - r.q0) * p.group + h % p.group;
+                c.head = h / p.group;
+                c.rb = rr / ROWS;
+                c.ja = 0;
+                w.total = total;
+                w.ctas = (int32_t)min((int64_t)grid, total);
+                w.b = mine;
+                w.u = start + ((int64_t)c.head * r.rblocks + c.rb) * r.ntiles;
+                s_q = kv_parts<ROWS>(p, w, r, c);
+                s_lr = rr - c.rb * ROWS;
+            }
+        }
+    }
+    __syncthreads();
+    const KvParts q = s_q;
+    if (q.n <= 1) return;
+    float acc[V] = {}, mm = -INFINITY, sum = 0.0f;
+    for (int32_t k0 = warp; k0 < q.n; k0 += 4 * W) {
+        float y[4][V];
+        float2 s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int32_t k = min(k0 + u * W, q.n - 1);
+            const int64_t at = q.first + (2 * k + (k == 0)) * ROWS + s_lr;
+            s[u] = __ldcg(&p.part_ml[at]);
+            const float *src = p.part + at * D;
+            if constexpr (V == 2) {
+                const float2 a = __ldcg(reinterpret_cast<const float2 *>(src) + lane);
+                y[u][0] = a.x, y[u][1] = a.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    const float4 a = __ldcg(reinterpret_cast<const float4 *>(src) + lane * (V / 4) + e / 4);
+                    y[u][e] = a.x, y[u][e + 1] = a.y, y[u][e + 2] = a.z, y[u][e + 3] = a.w;
+                }
+            }
+        }
+        float mn = mm;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mn = fmaxf(mn, s[u].x);
+        const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
+        mm = mn;
+        sum *= f0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] *= f0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            // a part that does not count may hold anything
+            if (k0 + u * W < q.n && s[u].x != -INFINITY) {
+                const float g = ex2(s[u].x - mn);
+                sum = fmaf(g, s[u].y, sum);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(g, y[u][e], acc[e]);
+            }
+        }
+    }
+    if (lane == 0) s_ml[warp] = make_float2(mm, sum);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    float top = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k].x);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        const float f = s_ml[k].x == -INFINITY ? 0.0f : ex2(s_ml[k].x - top);
+        l += f * s_ml[k].y;
+        o0 += f * s_acc[k][2 * threadIdx.x];
+        o1 += f * s_acc[k][2 * threadIdx.x + 1];
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    reinterpret_cast<uint32_t *>(p.out + tok * p.out_stride + (int64_t)h * D)[threadIdx.x] = pack_bf16(o0 * inv, o1 * inv);
+    if (p.lse && threadIdx.x == 0) p.lse[(int64_t)tok * heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 }  // namespace dev

@@ -7,8 +7,10 @@ namespace launch {
 template <>
 int attend_dim<128>(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvAttendParams *p,
                    const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
-    return q8 ? attend_rows_variant<128, true>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err)
-              : attend_rows_variant<128, false>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err);
+    const int rc = q8 ? attend_rows_variant<128, true>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err)
+                      : attend_rows_variant<128, false>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err);
+    if (rc != W12_OK || !p || !p->join_later) return rc;
+    return join_launch<128>(d, rows, *p, ctas, stream, err);
 }
 
 }  // namespace launch

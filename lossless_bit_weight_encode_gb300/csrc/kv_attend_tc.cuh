@@ -18,6 +18,9 @@
 // the order of the columns within every four (0, 2, 1, 3) is what comes out of the
 // byte pairs cheapest, and Q's columns and O's follow it.
 //
+// What a CTA has of a row block that others share goes to the workspace and is
+// joined by w12_kv_join_kernel: 128 rows of parts are too much for one CTA.
+//
 // For head_dim 64 and 128 a CTA takes half of TMEM and less than half of the
 // shared memory, so two share an SM and fill each other's waits.
 #pragma once
@@ -29,14 +32,6 @@ namespace dev {
 
 constexpr int kTcRows = 128;
 constexpr int kTcInfo = 16;  // ring of per-tile facts (present slices, scales)
-
-// A row block whose last part this CTA brought (at most two: its first and its
-// last one).
-struct TcJoin {
-    KvParts q;
-    KvRequest r;
-    KvPiece c;
-};
 
 // A softmax warp's place: kept in shared memory, so that the loop over a piece's
 // tiles has the registers.
@@ -65,8 +60,7 @@ struct AttendTcCfg {
     static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * kInfoBytes : 0);
     static constexpr int kBars = 4 * kOps + 4 * kRaws + 2 + 2 + 2 + 3;
     static constexpr int kOffInfo = kOffBars + 8 * kBars;
-    static constexpr int kOffJoins = kOffInfo + 4 * kTcInfo + 32;
-    static constexpr int kOffPlaces = kOffJoins + 2 * (int)sizeof(TcJoin);
+    static constexpr int kOffPlaces = kOffInfo + 4 * kTcInfo + 32;
     static constexpr int kSmemBytes = kOffPlaces + 4 * (int)sizeof(TcPlace) + 1024;  // 1024: alignment
     static constexpr int kThreads = Q8 ? 320 : 192;
     static constexpr int kTmemCols = D == 256 ? 512 : 256;
@@ -242,11 +236,8 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     uint64_t *sfull = rvempty + C::kRaws, *pfull = sfull + 2;
     uint64_t *pvdone = pfull + 2, *qfull = pvdone + 2, *ofree = qfull + 1, *drain = ofree + 1;
     uint32_t *present = reinterpret_cast<uint32_t *>(smem + C::kOffInfo);
-    volatile uint32_t *last_flag = present + kTcInfo;
-    volatile uint32_t *poison = last_flag + 1;
-    uint32_t *tmem_slot = const_cast<uint32_t *>(last_flag) + 2;
-    volatile uint32_t *n_joins = last_flag + 3;
-    TcJoin *joins = reinterpret_cast<TcJoin *>(smem + C::kOffJoins);
+    volatile uint32_t *poison = present + kTcInfo;
+    uint32_t *tmem_slot = present + kTcInfo + 1;
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -272,7 +263,6 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         mbar_init(drain, 1);
         fence_mbar_init();
         *poison = 0;
-        *n_joins = 0;
     }
     if (threadIdx.x == 128) {
         prefetch_tmap(&tm_k);
@@ -734,15 +724,6 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(ofree);
-            if (!whole) {
-                const KvParts q = kv_parts<kTcRows>(p, w1, r1, c1);
-                // joined by all warps at the end of the range
-                if (kv_arrive(p, q, last_flag) && threadIdx.x == 0) {
-                    TcJoin &e = joins[*n_joins];
-                    e.q = q, e.r = r1, e.c = c1;
-                    ++*n_joins;
-                }
-            }
             if (!more) break;
         }
         if (!ok && lane == 0) atomicOr(p.status, 8u);
@@ -751,11 +732,6 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     __syncthreads();
     tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, C::kTmemCols);
-    for (uint32_t i = 0; i < *n_joins; ++i) {
-        const TcJoin e = joins[i];
-        const int32_t nrows = (int32_t)min((int64_t)kTcRows, (int64_t)e.r.qlen * p.group - (int64_t)e.c.rb * kTcRows);
-        kv_join<kTcRows, D, 4>(p, e.q, e.r, e.c, nrows, (int)threadIdx.x, C::kThreads);
-    }
 }
 
 }  // namespace dev

@@ -73,6 +73,31 @@ struct AttendPlan {
     uint32_t n_counters = 0;
 };
 
+// Whether the parts of a row block that several CTAs share are joined by a second
+// kernel (a CTA per output row) or by the CTA that arrives last.  With two parts
+// per row block or more (few requests, as far as the host knows) the chain through
+// the last CTA is the longer way: one request of 777 tokens 7.4 against 10.4 us, two
+// of 100001 116 against 121; with fewer, most rows have one part and the second
+// kernel only costs: 128 requests of 1024 visible tokens 74 against 56 us.
+inline bool join_later(int rows, int group, int kv_heads, int max_new, int requests, int ctas) {
+    if (rows == dev::kTcRows) return true;
+    const int64_t blocks = ((int64_t)(max_new < 1 ? 1 : max_new) * group + rows - 1) / rows;
+    return ctas >= 2 * blocks * kv_heads * requests;
+}
+
+// The second kernel, for launches of `rows`-row blocks.
+template <int D>
+int join_launch(const DeviceView &d, int rows, const dev::KvAttendParams &p, int ctas, void *stream, std::string *err) {
+    const auto kernel = rows == 8    ? &dev::w12_kv_join_kernel<D, 8>
+                        : rows == 16 ? &dev::w12_kv_join_kernel<D, 16>
+                        : rows == 32 ? &dev::w12_kv_join_kernel<D, 32>
+                                     : &dev::w12_kv_join_kernel<D, dev::kTcRows>;
+    const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)(p.tokens * p.group * p.kv_heads)), dev::kJoinThreads, 0, 1,
+                                    stream, p, ctas);
+    if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend join launch", err);
+    return W12_OK;
+}
+
 // One head_dim's kernels (kv_attend_*.cu): CTAs resident on the whole device
 // (with `p` null), or the launch.
 template <int D>
