@@ -346,6 +346,36 @@ __device__ __forceinline__ void kv_join(const KvAttendParams &p, const KvParts &
     }
 }
 
+// A request's page numbers from one of its entries on, 64 of them in a warp's
+// registers (entry base + lane, base + 32 + lane): the load of a tile's pages is
+// then far behind its use.  Every lane takes part in every call.
+struct KvPageWindow {
+    const int32_t *row;
+    int32_t base, last, cur, next;
+
+    __device__ __forceinline__ int32_t load(int32_t e) const { return e <= last ? __ldg(row + e) : -1; }
+    // entries `first` to `end` - 1 will be asked for, in order
+    __device__ __forceinline__ void start(const int32_t *table_row, int32_t first, int32_t end) {
+        row = table_row;
+        base = first;
+        last = end - 1;
+        cur = load(base + (int)(threadIdx.x & 31));
+        next = load(base + 32 + (int)(threadIdx.x & 31));
+    }
+    // page of entry e (of each lane's own; all within 32 entries from `low`, the
+    // smallest, which never falls)
+    __device__ __forceinline__ int32_t get(int32_t low, int32_t e) {
+        while (low >= base + 32) {
+            base += 32;
+            cur = next;
+            next = load(base + 32 + (int)(threadIdx.x & 31));
+        }
+        const int32_t at = e - base;
+        const int32_t a = __shfl_sync(~0u, cur, at & 31), b = __shfl_sync(~0u, next, at & 31);
+        return at < 32 ? a : b;
+    }
+};
+
 template <int D, bool Q8, int WK, int WR, int NT>
 __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvAttendParams p,
                                                                        const __grid_constant__ CUtensorMap tm_k,
@@ -388,18 +418,16 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
         bool ok = true;
         while (ok && w.u < w.end) {
             const KvPiece c = kv_piece(w, r);
-            const int32_t *row = p.tables + (int64_t)w.b * p.table_stride;
+            KvPageWindow pages;
+            pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * kAttendTile / p.page_size,
+                        (r.kv + p.page_size - 1) / p.page_size);
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
                 const uint32_t stage = it % C::kStages, round = it / C::kStages;
                 // lane s < 4 deals with slice s
-                const int32_t kb = (r.tile0 + j) * kAttendTile + lane * kAttendSlice;
+                const int32_t t0 = (r.tile0 + j) * kAttendTile, kb = t0 + (lane & 3) * kAttendSlice;
                 const bool want = lane < 4 && kb < r.kv && kb + kAttendSlice > r.first;
-                int32_t page = -1, off = 0;
-                if (want) {
-                    const int32_t e = kb / p.page_size;
-                    off = kb - e * p.page_size;
-                    page = row[e];
-                }
+                const int32_t e = kb / p.page_size, off = kb - e * p.page_size;
+                const int32_t found = pages.get(t0 / p.page_size, e), page = want ? found : -1;
                 if (round > 0) ok = mbar_wait(&empty[stage], (round - 1) & 1, deadline);
                 ok = __shfl_sync(~0u, ok, 0);
                 if (!ok) break;

@@ -292,18 +292,16 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         uint32_t it = 0;
         while (ok && w.u < w.end) {
             const KvPiece c = kv_piece(w, r);
-            const int32_t *row = p.tables + (int64_t)w.b * p.table_stride;
+            KvPageWindow pages;
+            pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * kAttendTile / p.page_size,
+                        (r.kv + p.page_size - 1) / p.page_size);
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
                 // lane 4 b + s deals with slice s (and with column block b)
                 const int s = lane & 3, blk = lane >> 2;
-                const int32_t kb = (r.tile0 + j) * kAttendTile + s * kAttendSlice;
-                const bool mine = Q8 ? lane < 4 : lane < 4 * C::kBlocks;
-                int32_t page = -1, off = 0;
-                if (mine && kb < r.kv && kb + kAttendSlice > r.first) {
-                    const int32_t e = kb / p.page_size;
-                    off = kb - e * p.page_size;
-                    page = row[e];
-                }
+                const int32_t t0 = (r.tile0 + j) * kAttendTile, kb = t0 + s * kAttendSlice;
+                const bool want = lane < (Q8 ? 4 : 4 * C::kBlocks) && kb < r.kv && kb + kAttendSlice > r.first;
+                const int32_t e = kb / p.page_size, off = kb - e * p.page_size;
+                const int32_t found = pages.get(t0 / p.page_size, e), page = want ? found : -1;
                 const bool here = page >= 0 && page < p.num_pages;
                 const uint32_t mask = __ballot_sync(~0u, here) & 15u;
                 const uint32_t n = (uint32_t)__popc(mask);
