@@ -120,6 +120,17 @@ __device__ __forceinline__ uint64_t kv_seen64(const KvAttendParams &p, int32_t k
     return m;
 }
 
+// True in one lane of the warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+
 // One pipeline barrier's phase by use count.  The parity tells a phase only from
 // its neighbours: who waits for use n knows that use n - 1 is over, and use n + 1
 // cannot be over.  So what is waited for every tile (scores, probabilities,
@@ -357,54 +368,66 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         // ------------------------------------------------------------ MMA
         constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kAttendTile);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
+        // The whole warp walks; one elected lane issues.  What the products' operands
+        // are computed from comes out of shuffles and votes, so that the compiler
+        // knows it to be the same for the warp: an operand that could differ between
+        // lanes costs each product a move to a uniform register, and issuing then
+        // took longer than the products (700 cycles for a tile's eight).
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const bool leader = elect_one();
         uint32_t it = 0, piece = 0;  // tiles whose scores have been issued; pieces
         // scores of tile `it` into S[it & 1]
         auto scores = [&](uint32_t issued) -> bool {
             const uint32_t stage = it % C::kOps;
             // the buffer's last probabilities (tile it - 2) have been multiplied:
             // wait for the last product issued so far
-            if (issued > 0 && !tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline)) return false;
-            if (!tc_wait(&kfull[stage], it / C::kOps, deadline)) return false;
+            bool good = issued == 0 || tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline);
+            good = good && tc_wait(&kfull[stage], it / C::kOps, deadline);
+            if (!__all_sync(~0u, good)) return false;
             tc_fence_after();
-            const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
-            const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
-            const uint32_t d = tmem + C::kSCol + 64 * (it & 1);
+            if (leader) {
+                const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
+                const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
+                const uint32_t d = tm + C::kSCol + 64 * (it & 1);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
-                           b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
-            mma_commit(&kempty[stage]);
-            mma_commit(&sfull[it & 1]);
+                for (int k = 0; k < D / 16; ++k)
+                    mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
+                               b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
+                mma_commit(&kempty[stage]);
+                mma_commit(&sfull[it & 1]);
+            }
+            __syncwarp();
             ++it;
             return true;
         };
-        if (lane == 0) {
-            while (ok && w.u < w.end) {
-                const KvPiece c = kv_piece(w, r);
-                const int n = c.jb - c.ja;
-                ok = tc_wait(qfull, piece, deadline) && scores(it);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (j + 1 < n && !(ok = scores(it - 1))) break;
-                    const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
-                    ok = tc_wait(&pfull[g & 1], g >> 1, deadline) && tc_wait(&vfull[stage], g / C::kOps, deadline);
-                    if (ok && j == 0 && piece > 0) ok = tc_wait(ofree, piece - 1, deadline);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t a = tmem + C::kSCol + 64 * (g & 1);
-                    const uint64_t b = smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128,
-                                                 1024u, 2u);
+        while (ok) {
+            int n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
+            n = __shfl_sync(~0u, n, 0);
+            if (n == 0) break;
+            ok = __all_sync(~0u, tc_wait(qfull, piece, deadline)) && scores(it);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n && !(ok = scores(it - 1))) break;
+                const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
+                bool good = tc_wait(&pfull[g & 1], g >> 1, deadline) && tc_wait(&vfull[stage], g / C::kOps, deadline);
+                if (good && j == 0 && piece > 0) good = tc_wait(ofree, piece - 1, deadline);
+                if (!(ok = __all_sync(~0u, good))) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t a = tm + C::kSCol + 64 * (g & 1);
+                    const uint64_t b =
+                        smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128, 1024u, 2u);
 #pragma unroll
                     for (int k = 0; k < kAttendTile / 16; ++k)
-                        mma_tmem_a(tmem, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
+                        mma_tmem_a(tm, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
                     mma_commit(&vempty[stage]);
                     mma_commit(&pvdone[g & 1]);
                 }
-                ++piece;
-                if (ok) {
-                    // kv_advance is one lane's here: it has no warp operations
-                    kv_advance<kTcRows>(p, w, r, n);
-                }
+                __syncwarp();
             }
+            ++piece;
+            if (ok) kv_advance<kTcRows>(p, w, r, n);
+        }
+        if (leader) {
             if (!ok) atomicOr(p.status, 8u);
             mma_commit(drain);  // nothing issued may still run when TMEM is given back
             tc_wait(drain, 0, globaltimer_ns() + p.timeout_ns);
