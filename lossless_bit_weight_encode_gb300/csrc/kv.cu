@@ -287,7 +287,7 @@ int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspac
     p.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
     p.part = reinterpret_cast<float *>(ws);
     p.n_counters = plan.n_counters;
-    p.join_later = join_later(plan.rows, p.group, c.kv_heads, a.max_new, a.requests, plan.ctas);
+    p.join_later = join_warps(plan.rows, p.group, c.kv_heads, a.max_new, a.requests, plan.ctas);
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     int resident = 0;

@@ -812,75 +812,76 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
     }
 }
 
-// Joins the parts of one output row (token blockIdx.x / heads, head the rest) of a
-// launch with ROWS-row blocks and `grid` CTAs; a row that one CTA had whole is
-// finished already.  Eight warps take the parts in turn, then meet in shared
-// memory, both in a fixed order.
+// Joins the parts of the output rows (token and head, heads fastest) of a launch with
+// ROWS-row blocks and `grid` CTAs; a row that one CTA had whole is finished already.
+// WPR warps share a row: they take its parts in turn and meet in shared memory,
+// both in a fixed order.
 constexpr int kJoinThreads = 256;
 
-template <int D, int ROWS>
+template <int D, int ROWS, int WPR>
 __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAttendParams p, int grid) {
     constexpr int W = kJoinThreads / 32, V = D / 32;  // columns of a lane
-    __shared__ float s_acc[W][D];
+    __shared__ float s_acc[WPR > 1 ? W : 1][D];
     __shared__ float2 s_ml[W];
-    __shared__ KvParts s_q;
-    __shared__ int32_t s_lr;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int heads = p.group * p.kv_heads;
-    const int32_t tok = blockIdx.x / heads, h = blockIdx.x - tok * heads;
+    const int64_t out_row = (int64_t)blockIdx.x * (W / WPR) + warp / WPR;
+    const int32_t tok = (int32_t)(out_row / heads), h = (int32_t)(out_row - (int64_t)tok * heads);
     pdl_launch_dependents();
     pdl_wait();
-    if (warp == 0) {
-        // the token's request, its first unit and all units
-        int64_t total = 0, start = -1;
-        int32_t mine = 0;
-        for (int b0 = 0; b0 < p.requests; b0 += 32) {
-            KvRequest r;
-            r.units = 0, r.q0 = r.qlen = 0;
-            if (b0 + lane < p.requests) r = kv_request<ROWS>(p, b0 + lane);
-            int64_t inc = r.units;
+    // the token's request, its first unit and all units
+    int64_t total = 0, start = -1;
+    KvRequest r;
+    r.q0 = r.qlen = 0;
+    int32_t b = 0;
+    for (int b0 = 0; b0 < p.requests; b0 += 32) {
+        KvRequest x;
+        x.units = 0, x.q0 = x.qlen = 0;
+        if (b0 + lane < p.requests) x = kv_request<ROWS>(p, b0 + lane);
+        int64_t inc = x.units;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t x = __shfl_up_sync(~0u, inc, d);
-                if (lane >= d) inc += x;
-            }
-            const uint32_t hit = __ballot_sync(~0u, tok >= r.q0 && tok < r.q0 + r.qlen);
-            if (hit && start < 0) {
-                mine = b0 + __ffs(hit) - 1;
-                start = total + __shfl_sync(~0u, inc - r.units, __ffs(hit) - 1);
-            }
-            total += __shfl_sync(~0u, inc, 31);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, inc, d);
+            if (lane >= d) inc += y;
         }
-        if (lane == 0) {
-            s_q.n = 0;
-            if (start >= 0) {
-                KvWalk w;
-                const KvRequest r = kv_request<ROWS>(p, mine);
-                KvPiece c;
-                const int32_t rr = (tok - r.q0) * p.group + h % p.group;
-                c.head = h / p.group;
-                c.rb = rr / ROWS;
-                c.ja = 0;
-                w.total = total;
-                w.ctas = (int32_t)min((int64_t)grid, total);
-                w.b = mine;
-                w.u = start + ((int64_t)c.head * r.rblocks + c.rb) * r.ntiles;
-                s_q = kv_parts<ROWS>(p, w, r, c);
-                s_lr = rr - c.rb * ROWS;
-            }
+        const uint32_t hit = __ballot_sync(~0u, tok >= x.q0 && tok < x.q0 + x.qlen);
+        if (hit && start < 0) {
+            const int src = __ffs(hit) - 1;
+            b = b0 + src;
+            start = total + __shfl_sync(~0u, inc - x.units, src);
+            r.q0 = __shfl_sync(~0u, x.q0, src);
+            r.ntiles = __shfl_sync(~0u, x.ntiles, src);
+            r.rblocks = __shfl_sync(~0u, x.rblocks, src);
         }
+        total += __shfl_sync(~0u, inc, 31);
     }
-    __syncthreads();
-    const KvParts q = s_q;
-    if (q.n <= 1) return;
+    KvParts q;
+    q.n = 0;
+    int32_t lr = 0;
+    if (start >= 0) {  // the same for the whole warp, and for all warps of a row
+        const int32_t rr = (tok - r.q0) * p.group + h % p.group;
+        KvPiece c;
+        KvWalk w;
+        c.head = h / p.group;
+        c.rb = rr / ROWS;
+        c.ja = 0;
+        w.total = total;
+        w.ctas = (int32_t)min((int64_t)grid, total);
+        w.b = b;
+        w.u = start + ((int64_t)c.head * r.rblocks + c.rb) * r.ntiles;
+        q = kv_parts<ROWS>(p, w, r, c);
+        lr = rr - c.rb * ROWS;
+    }
+    if (WPR == 1 && q.n <= 1) return;
     float acc[V] = {}, mm = -INFINITY, sum = 0.0f;
-    for (int32_t k0 = warp; k0 < q.n; k0 += 4 * W) {
-        float y[4][V];
-        float2 s[4];
+    constexpr int U = V == 8 || WPR > 1 ? 4 : 8;  // parts whose loads are in flight
+    for (int32_t k0 = warp % WPR; q.n > 1 && k0 < q.n; k0 += U * WPR) {
+        float y[U][V];
+        float2 s[U];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int32_t k = min(k0 + u * W, q.n - 1);
-            const int64_t at = q.first + (2 * k + (k == 0)) * ROWS + s_lr;
+        for (int u = 0; u < U; ++u) {
+            const int32_t k = min(k0 + u * WPR, q.n - 1);
+            const int64_t at = q.first + (2 * k + (k == 0)) * ROWS + lr;
             s[u] = __ldcg(&p.part_ml[at]);
             const float *src = p.part + at * D;
             if constexpr (V == 2) {
@@ -896,16 +897,16 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
         }
         float mn = mm;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mn = fmaxf(mn, s[u].x);
+        for (int u = 0; u < U; ++u) mn = fmaxf(mn, s[u].x);
         const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
         mm = mn;
         sum *= f0;
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] *= f0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             // a part that does not count may hold anything
-            if (k0 + u * W < q.n && s[u].x != -INFINITY) {
+            if (k0 + u * WPR < q.n && s[u].x != -INFINITY) {
                 const float g = ex2(s[u].x - mn);
                 sum = fmaf(g, s[u].y, sum);
 #pragma unroll
@@ -913,24 +914,31 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
             }
         }
     }
-    if (lane == 0) s_ml[warp] = make_float2(mm, sum);
+    if constexpr (WPR > 1) {
+        static_assert(WPR == W, "one row per CTA");
+        if (lane == 0) s_ml[warp] = make_float2(mm, sum);
 #pragma unroll
-    for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
-    __syncthreads();
-    if (threadIdx.x >= D / 2) return;
-    float top = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+        for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
+        __syncthreads();
+        if (warp > 0 || q.n <= 1) return;
+        mm = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k].x);
+        for (int e = 0; e < V; ++e) acc[e] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        const float f = s_ml[k].x == -INFINITY ? 0.0f : ex2(s_ml[k].x - top);
-        l += f * s_ml[k].y;
-        o0 += f * s_acc[k][2 * threadIdx.x];
-        o1 += f * s_acc[k][2 * threadIdx.x + 1];
+        for (int k = 0; k < W; ++k) mm = fmaxf(mm, s_ml[k].x);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float f = s_ml[k].x == -INFINITY ? 0.0f : ex2(s_ml[k].x - mm);
+            sum += f * s_ml[k].y;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] += f * s_acc[k][lane * V + e];
+        }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    reinterpret_cast<uint32_t *>(p.out + tok * p.out_stride + (int64_t)h * D)[threadIdx.x] = pack_bf16(o0 * inv, o1 * inv);
-    if (p.lse && threadIdx.x == 0) p.lse[(int64_t)tok * heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + tok * p.out_stride + (int64_t)h * D) + lane * (V / 2);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[(int64_t)tok * heads + h] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
 }
 
 }  // namespace dev

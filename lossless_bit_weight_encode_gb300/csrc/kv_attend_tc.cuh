@@ -13,8 +13,8 @@
 // softmax warps work on this one's.  O stays in TMEM for a whole piece; it is
 // rescaled only when a row's maximum rises by more than 2^8.
 //
-// A producer warp fills the K and V rings by TMA.  A Q8 cache's rows arrive as
-// bytes in rings of their own and four more warps turn them into BF16 operands;
+// Two warps fill the K and V rings by TMA.  A Q8 cache's rows arrive as bytes in
+// rings of their own and four warps turn them into BF16 operands;
 // the order of the columns within every four (0, 2, 1, 3) is what comes out of the
 // byte pairs cheapest, and Q's columns and O's follow it.
 //
@@ -62,7 +62,7 @@ struct AttendTcCfg {
     static constexpr int kOffInfo = kOffBars + 8 * kBars;
     static constexpr int kOffPlaces = kOffInfo + 4 * kTcInfo + 32;
     static constexpr int kSmemBytes = kOffPlaces + 4 * (int)sizeof(TcPlace) + 1024;  // 1024: alignment
-    static constexpr int kThreads = Q8 ? 320 : 192;
+    static constexpr int kThreads = Q8 ? 384 : 224;
     static constexpr int kTmemCols = D == 256 ? 512 : 256;
     static constexpr int kSCol = D == 256 ? 256 : 128;  // two S buffers of 64 columns; O from column 0
 };
@@ -233,8 +233,82 @@ __device__ __forceinline__ float tc_tile_weights(uint32_t ts, const float *sc, f
     return f2_lo(l0) + f2_hi(l0);
 }
 
+// Fills a ring with the keys or the values of the CTA's tiles, one tile per step().
+// Keys and values have a loader (and a warp) each: a ring's next tile is then asked
+// for as soon as its own slot is free, two tiles ahead of its use.
 template <int D, bool Q8>
-__global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
+struct TcLoader {
+    using C = AttendTcCfg<D, Q8>;
+    static constexpr uint32_t N = Q8 ? C::kRaws : C::kOps;
+    const void *map;
+    uint8_t *ring;            // slot 0
+    uint64_t *full, *empty;   // [N] each
+    uint32_t slot_bytes;
+    uint8_t *scales;          // with Q8 keys: slot 0 of the scales
+    uint32_t *present;        // with the keys: kTcInfo tiles' slices
+    KvWalk w;
+    KvRequest r;
+    KvPiece c;
+    KvPageWindow pages;
+    int32_t j;
+    uint32_t it;
+
+    __device__ __forceinline__ void open(const KvAttendParams &p) {
+        c = kv_piece(w, r);
+        j = c.ja;
+        pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * kAttendTile / p.page_size,
+                    (r.kv + p.page_size - 1) / p.page_size);
+    }
+    __device__ __forceinline__ void start(const KvAttendParams &p, const KvWalk &walk, const KvRequest &req) {
+        w = walk;
+        r = req;
+        it = 0;
+        if (w.u < w.end) open(p);
+    }
+    // False when a wait ran out.  Nothing happens behind the last tile.
+    __device__ __forceinline__ bool step(const KvAttendParams &p, uint64_t deadline) {
+        const int lane = threadIdx.x & 31;
+        if (w.u >= w.end) return true;
+        // lane 4 b + s deals with slice s (and with column block b)
+        const int s = lane & 3, blk = lane >> 2;
+        const int32_t t0 = (r.tile0 + j) * kAttendTile, kb = t0 + s * kAttendSlice;
+        const bool want = lane < (Q8 ? 4 : 4 * C::kBlocks) && kb < r.kv && kb + kAttendSlice > r.first;
+        const int32_t e = kb / p.page_size, off = kb - e * p.page_size;
+        const int32_t found = pages.get(t0 / p.page_size, e), page = want ? found : -1;
+        const bool here = page >= 0 && page < p.num_pages;
+        const uint32_t mask = __ballot_sync(~0u, here) & 15u;
+        constexpr uint32_t bytes = kAttendSlice * D * (Q8 ? 1 : 2);  // of a slice
+        const uint32_t stage = it % N, use = it / N;
+        if (use > 0 && !__all_sync(~0u, tc_wait(&empty[stage], use - 1, deadline))) return false;
+        if (lane == 0) {
+            if (present) present[it % kTcInfo] = mask;
+            mbar_arrive_expect_tx(&full[stage], (uint32_t)__popc(mask) * (bytes + (scales ? 128u : 0u)));
+        }
+        __syncwarp();
+        if (here) {
+            const uint32_t bar = smem_u32(&full[stage]);
+            const uint32_t at = stage * slot_bytes + (Q8 ? s * bytes : blk * (kAttendTile * 128) + s * (kAttendSlice * 128));
+            tma_load_4d(smem_u32(ring) + at, map, Q8 ? 0 : 64 * blk, off, c.head, page, bar);
+            if (scales)
+                bulk_g2s(scales + stage * 512 + s * 128,
+                         p.scales + (((int64_t)page * p.kv_heads + c.head) * p.page_size + off) * 2, 128, &full[stage]);
+        }
+        ++it;
+        if (++j == c.jb) {
+            kv_advance<kTcRows>(p, w, r, c.jb - c.ja);
+            if (w.u < w.end) open(p);
+        }
+        return true;
+    }
+    // After a timeout: no copy may still be in flight when the CTA ends.
+    __device__ __forceinline__ void drain(uint64_t deadline) {
+        for (uint32_t k = it > N ? it - N : 0; k < it; ++k)
+            if (!tc_wait(&full[k % N], k / N, deadline)) break;
+    }
+};
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
     w12_kv_attend_tc_kernel(const KvAttendParams p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
     using C = AttendTcCfg<D, Q8>;
@@ -298,219 +372,8 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    if (warp == 4) {
-        // ------------------------------------------------------------ TMA producer
-        uint32_t it = 0;
-        while (ok && w.u < w.end) {
-            const KvPiece c = kv_piece(w, r);
-            KvPageWindow pages;
-            pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * kAttendTile / p.page_size,
-                        (r.kv + p.page_size - 1) / p.page_size);
-            for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
-                // lane 4 b + s deals with slice s (and with column block b)
-                const int s = lane & 3, blk = lane >> 2;
-                const int32_t t0 = (r.tile0 + j) * kAttendTile, kb = t0 + s * kAttendSlice;
-                const bool want = lane < (Q8 ? 4 : 4 * C::kBlocks) && kb < r.kv && kb + kAttendSlice > r.first;
-                const int32_t e = kb / p.page_size, off = kb - e * p.page_size;
-                const int32_t found = pages.get(t0 / p.page_size, e), page = want ? found : -1;
-                const bool here = page >= 0 && page < p.num_pages;
-                const uint32_t mask = __ballot_sync(~0u, here) & 15u;
-                const uint32_t n = (uint32_t)__popc(mask);
-                constexpr uint32_t N = Q8 ? C::kRaws : C::kOps;
-                constexpr uint32_t bytes = kAttendSlice * D * (Q8 ? 1 : 2);
-                const uint32_t stage = it % N, use = it / N;
-                uint64_t *const kbar = Q8 ? &rkfull[stage] : &kfull[stage];
-                uint64_t *const vbar = Q8 ? &rvfull[stage] : &vfull[stage];
-                const uint32_t at = Q8 ? C::kOffRaw + stage * 2 * C::kRawBytes + s * bytes
-                                       : stage * C::kTileBytes + blk * (kAttendTile * 128) + s * (kAttendSlice * 128);
-                if (use > 0) ok = tc_wait(Q8 ? &rkempty[stage] : &kempty[stage], use - 1, deadline);
-                ok = __shfl_sync(~0u, ok, 0);
-                if (!ok) break;
-                if (lane == 0) {
-                    present[it % kTcInfo] = mask;
-                    mbar_arrive_expect_tx(kbar, n * (bytes + (Q8 ? 128 : 0)));
-                }
-                __syncwarp();
-                if (here) {
-                    tma_load_4d(smem_u32(smem + (Q8 ? at : C::kOffK + at)), &tm_k, Q8 ? 0 : 64 * blk, off, c.head, page,
-                                smem_u32(kbar));
-                    if (Q8)
-                        bulk_g2s(smem + C::kOffRawScale + stage * 512 + s * 128,
-                                 p.scales + (((int64_t)page * p.kv_heads + c.head) * p.page_size + off) * 2, 128, kbar);
-                }
-                if (use > 0) ok = tc_wait(Q8 ? &rvempty[stage] : &vempty[stage], use - 1, deadline);
-                ok = __shfl_sync(~0u, ok, 0);
-                if (!ok) {
-                    ++it;  // its keys are on their way: waited for below
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(vbar, n * bytes);
-                __syncwarp();
-                if (here)
-                    tma_load_4d(smem_u32(smem + (Q8 ? at + C::kRawBytes : C::kOffV + at)), &tm_v, Q8 ? 0 : 64 * blk, off,
-                                c.head, page, smem_u32(vbar));
-            }
-            if (ok) kv_advance<kTcRows>(p, w, r, c.jb - c.ja);
-        }
-        // no copy may still be in flight when the CTA ends (only after a timeout
-        // is that not so already)
-        if (!ok && lane == 0) {
-            atomicOr(p.status, 8u);
-            const uint64_t late = globaltimer_ns() + p.timeout_ns;
-            constexpr uint32_t N = Q8 ? C::kRaws : C::kOps;
-            for (uint32_t k = it > N ? it - N : 0; k < it; ++k)
-                if (!tc_wait(Q8 ? &rkfull[k % N] : &kfull[k % N], k / N, late) ||
-                    !tc_wait(Q8 ? &rvfull[k % N] : &vfull[k % N], k / N, late))
-                    break;
-        }
-        __syncwarp();
-    } else if (warp == 5) {
-        // ------------------------------------------------------------ MMA
-        constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kAttendTile);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
-        // The whole warp walks; one elected lane issues.  What the products' operands
-        // are computed from comes out of shuffles and votes, so that the compiler
-        // knows it to be the same for the warp: an operand that could differ between
-        // lanes costs each product a move to a uniform register, and issuing then
-        // took longer than the products (700 cycles for a tile's eight).
-        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-        const bool leader = elect_one();
-        uint32_t it = 0, piece = 0;  // tiles whose scores have been issued; pieces
-        // scores of tile `it` into S[it & 1]
-        auto scores = [&](uint32_t issued) -> bool {
-            const uint32_t stage = it % C::kOps;
-            // the buffer's last probabilities (tile it - 2) have been multiplied:
-            // wait for the last product issued so far
-            bool good = issued == 0 || tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline);
-            good = good && tc_wait(&kfull[stage], it / C::kOps, deadline);
-            if (!__all_sync(~0u, good)) return false;
-            tc_fence_after();
-            if (leader) {
-                const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
-                const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
-                const uint32_t d = tm + C::kSCol + 64 * (it & 1);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
-                               b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
-                mma_commit(&kempty[stage]);
-                mma_commit(&sfull[it & 1]);
-            }
-            __syncwarp();
-            ++it;
-            return true;
-        };
-        while (ok) {
-            int n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
-            n = __shfl_sync(~0u, n, 0);
-            if (n == 0) break;
-            ok = __all_sync(~0u, tc_wait(qfull, piece, deadline)) && scores(it);
-            for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n && !(ok = scores(it - 1))) break;
-                const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
-                bool good = tc_wait(&pfull[g & 1], g >> 1, deadline) && tc_wait(&vfull[stage], g / C::kOps, deadline);
-                if (good && j == 0 && piece > 0) good = tc_wait(ofree, piece - 1, deadline);
-                if (!(ok = __all_sync(~0u, good))) break;
-                tc_fence_after();
-                if (leader) {
-                    const uint32_t a = tm + C::kSCol + 64 * (g & 1);
-                    const uint64_t b =
-                        smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128, 1024u, 2u);
-#pragma unroll
-                    for (int k = 0; k < kAttendTile / 16; ++k)
-                        mma_tmem_a(tm, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
-                    mma_commit(&vempty[stage]);
-                    mma_commit(&pvdone[g & 1]);
-                }
-                __syncwarp();
-            }
-            ++piece;
-            if (ok) kv_advance<kTcRows>(p, w, r, n);
-        }
-        if (leader) {
-            if (!ok) atomicOr(p.status, 8u);
-            mma_commit(drain);  // nothing issued may still run when TMEM is given back
-            tc_wait(drain, 0, globaltimer_ns() + p.timeout_ns);
-        }
-        __syncwarp();
-    } else if (warp >= 6) {
-        // ------------------------------------------------------------ converters (Q8)
-        const int ct = (warp - 6) * 32 + lane;
-        constexpr uint32_t N = C::kRaws + !Q8;
-        constexpr int CH = D / 16;  // 16-byte chunks of a row
-        // the thread's first chunk and where its two operand chunks go; odd column
-        // blocks in the other order, so that eight lanes write eight different
-        // 16-byte bank groups
-        const int ckey = ct / CH, cc = ct % CH;
-        const bool turn = (cc / 4) & 1;
-        const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
-        const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
-        const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
-        const uint32_t total = (uint32_t)(w.end - w.u);
-        // K or V of tile x to its operand buffer, which the tile before must have left
-        auto convert = [&](bool values, uint32_t x) -> bool {
-            const uint32_t stage = x % N;
-            bool good = tc_wait(values ? &rvfull[stage] : &rkfull[stage], x / N, deadline);
-            if (good && x > 0) good = tc_wait(values ? &vempty[0] : &kempty[0], x - 1, deadline);
-            if (!__all_sync(~0u, good)) return false;
-            if (!values && warp < 8) {
-                // scales of the tile's keys, the softmax scale in the keys' ones, and
-                // the largest of those
-                const float2 *src = reinterpret_cast<const float2 *>(smem + C::kOffRawScale + stage * 512);
-                float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (x % kTcInfo) * C::kInfoBytes);
-                if (warp == 6) {
-                    const float a = src[lane].x * p.scale_log2, b = src[lane + 32].x * p.scale_log2;
-                    dst[lane] = a;
-                    dst[lane + 32] = b;
-                    float top = max_nan(fabsf(a), fabsf(b));
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
-                    if (lane == 0) dst[128] = top;
-                } else {
-                    dst[64 + lane] = src[lane].y;
-                    dst[96 + lane] = src[lane + 32].y;
-                }
-            }
-            const uint4 *src =
-                reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + values) * C::kRawBytes) + ct;
-            uint8_t *dst = smem + (values ? C::kOffV : C::kOffK);
-            constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
-            constexpr int G = N4 < 4 ? N4 : 4;
-#pragma unroll
-            for (int i0 = 0; i0 < N4; i0 += G) {
-                uint4 u[G];
-#pragma unroll
-                for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    uint4 a, b;
-                    q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
-                    q8_to_bf16(turn ? u[i].w : u[i].y, a.z, a.w);
-                    q8_to_bf16(turn ? u[i].x : u[i].z, b.x, b.y);
-                    q8_to_bf16(turn ? u[i].y : u[i].w, b.z, b.w);
-                    // 128 / CH keys further: a multiple of 8, the same swizzle
-                    uint8_t *row = dst + (i0 + i) * (128 / CH) * 128;
-                    *reinterpret_cast<uint4 *>(row + at0) = a;
-                    *reinterpret_cast<uint4 *>(row + at1) = b;
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(values ? &vfull[0] : &kfull[0]);
-                mbar_arrive(values ? &rvempty[stage] : &rkempty[stage]);
-            }
-            return true;
-        };
-        // the keys run one tile ahead: their buffer is free as soon as the scores
-        // are made, the values' only after the softmax
-        ok = convert(false, 0);
-        for (uint32_t x = 0; ok && x < total; ++x) {
-            if (x + 1 < total) ok = convert(false, x + 1);
-            ok = ok && convert(true, x);
-        }
-        if (!ok && lane == 0) atomicOr(p.status, 8u);
-    } else {
+    if (warp < 4) {
+        if (Q8 && D < 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         // ------------------------------------------------------------ softmax and output, one row per thread
         const int lr = threadIdx.x;  // 0..127, TMEM lane
         const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
@@ -523,24 +386,35 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
         __syncwarp();
         // Q rows of a piece to shared memory, rows behind the last one zero
         auto load_q = [&](const KvRequest &rq, const KvPiece &pc) {
+            constexpr int CH = D / 8, STEPS = CH, G = 8;  // 16-byte chunks of a row; 32 chunks a step
+            // where this lane's row is; the steps then ask the lanes
             const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
-            constexpr int CH = D / 8;  // 16-byte chunks of a row
-#pragma unroll 8
-            for (int i = lane; i < 32 * CH; i += 32) {
-                const int row = warp * 32 + i / CH, ch = i % CH;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (row < rows) {
-                    const int32_t rr = pc.rb * kTcRows + row, tok = rr / p.group;
-                    u = *reinterpret_cast<const uint4 *>(p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
-                                                         (int64_t)(pc.head * p.group + rr - tok * p.group) * D + 8 * ch);
+            const int32_t rr = pc.rb * kTcRows + lr, tok = rr / p.group;
+            const int64_t src = lr < rows ? (int64_t)(rq.q0 + tok) * p.q_stride +
+                                                (int64_t)(pc.head * p.group + rr - tok * p.group) * D
+                                          : -1;
+#pragma unroll
+            for (int s0 = 0; s0 < STEPS; s0 += G) {
+                uint4 u[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const int i = (s0 + g) * 32 + lane;
+                    const int64_t at = __shfl_sync(~0u, src, i / CH);
+                    u[g] = make_uint4(0, 0, 0, 0);
+                    if (at >= 0) u[g] = __ldg(reinterpret_cast<const uint4 *>(p.q + at) + i % CH);
                 }
-                if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
-                    u.x ^= 0x80008000u, u.y ^= 0x80008000u, u.z ^= 0x80008000u, u.w ^= 0x80008000u;
-                if (Q8)  // the column order of the converted keys
-                    u = make_uint4(prmt(u.x, u.y, 0x5410u), prmt(u.x, u.y, 0x7632u), prmt(u.z, u.w, 0x5410u),
-                                   prmt(u.z, u.w, 0x7632u));
-                *reinterpret_cast<uint4 *>(smem + C::kOffQ + (ch / 8) * (kTcRows * 128) + row * 128 +
-                                           (((ch % 8) ^ (row & 7)) << 4)) = u;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const int i = (s0 + g) * 32 + lane, row = warp * 32 + i / CH, ch = i % CH;
+                    uint4 v = u[g];
+                    if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
+                        v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+                    if (Q8)  // the column order of the converted keys
+                        v = make_uint4(prmt(v.x, v.y, 0x5410u), prmt(v.x, v.y, 0x7632u), prmt(v.z, v.w, 0x5410u),
+                                       prmt(v.z, v.w, 0x7632u));
+                    *reinterpret_cast<uint4 *>(smem + C::kOffQ + (ch / 8) * (kTcRows * 128) + row * 128 +
+                                               (((ch % 8) ^ (row & 7)) << 4)) = v;
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -748,6 +622,173 @@ __global__ void __launch_bounds__(Q8 ? 320 : 192, D == 256 ? 1 : 2)
             if (!more) break;
         }
         if (!ok && lane == 0) atomicOr(p.status, 8u);
+        } else {
+        if (Q8 && D < 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 4 || warp == 6) {
+        // ------------------------------------------------------------ loaders
+        TcLoader<D, Q8> load;
+        const bool keys = warp == 4;
+        load.map = keys ? &tm_k : &tm_v;
+        load.ring = smem + (Q8 ? C::kOffRaw + (keys ? 0 : C::kRawBytes) : keys ? C::kOffK : C::kOffV);
+        load.full = Q8 ? (keys ? rkfull : rvfull) : keys ? kfull : vfull;
+        load.empty = Q8 ? (keys ? rkempty : rvempty) : keys ? kempty : vempty;
+        load.slot_bytes = Q8 ? 2 * C::kRawBytes : C::kTileBytes;
+        load.scales = Q8 && keys ? smem + C::kOffRawScale : nullptr;
+        load.present = keys ? present : nullptr;
+        load.start(p, w, r);
+        while (ok && load.w.u < load.w.end) ok = load.step(p, deadline);
+        if (!ok && lane == 0) {
+            atomicOr(p.status, 8u);
+            load.drain(globaltimer_ns() + p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kAttendTile);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
+        // The whole warp walks; one elected lane issues.  What the products' operands
+        // are computed from comes out of shuffles and votes, so that the compiler
+        // knows it to be the same for the warp: an operand that could differ between
+        // lanes costs each product a move to a uniform register, and issuing then
+        // took longer than the products (700 cycles for a tile's eight).
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const bool leader = elect_one();
+        uint32_t it = 0, piece = 0;  // tiles whose scores have been issued; pieces
+        // scores of tile `it` into S[it & 1]
+        auto scores = [&](uint32_t issued) -> bool {
+            const uint32_t stage = it % C::kOps;
+            // the buffer's last probabilities (tile it - 2) have been multiplied:
+            // wait for the last product issued so far
+            bool good = issued == 0 || tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline);
+            good = good && tc_wait(&kfull[stage], it / C::kOps, deadline);
+            if (!__all_sync(~0u, good)) return false;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
+                const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
+                const uint32_t d = tm + C::kSCol + 64 * (it & 1);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
+                               b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
+                mma_commit(&kempty[stage]);
+                mma_commit(&sfull[it & 1]);
+            }
+            __syncwarp();
+            ++it;
+            return true;
+        };
+        while (ok) {
+            int n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
+            n = __shfl_sync(~0u, n, 0);
+            if (n == 0) break;
+            ok = __all_sync(~0u, tc_wait(qfull, piece, deadline)) && scores(it);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n && !(ok = scores(it - 1))) break;
+                const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
+                bool good = tc_wait(&pfull[g & 1], g >> 1, deadline) && tc_wait(&vfull[stage], g / C::kOps, deadline);
+                if (good && j == 0 && piece > 0) good = tc_wait(ofree, piece - 1, deadline);
+                if (!(ok = __all_sync(~0u, good))) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t a = tm + C::kSCol + 64 * (g & 1);
+                    const uint64_t b =
+                        smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128, 1024u, 2u);
+#pragma unroll
+                    for (int k = 0; k < kAttendTile / 16; ++k)
+                        mma_tmem_a(tm, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
+                    mma_commit(&vempty[stage]);
+                    mma_commit(&pvdone[g & 1]);
+                }
+                __syncwarp();
+            }
+            ++piece;
+            if (ok) kv_advance<kTcRows>(p, w, r, n);
+        }
+        if (leader) {
+            if (!ok) atomicOr(p.status, 8u);
+            mma_commit(drain);  // nothing issued may still run when TMEM is given back
+            tc_wait(drain, 0, globaltimer_ns() + p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (Q8 && warp >= 8) {
+        // ------------------------------------------------------------ converters of a Q8 cache
+        const int cw = warp - 8, ct = cw * 32 + lane;
+        constexpr uint32_t N = C::kRaws + !Q8;
+        constexpr int CH = D / 16;  // 16-byte chunks of a row
+        // the thread's first chunk and where its two operand chunks go; odd column
+        // blocks in the other order, so that eight lanes write eight different
+        // 16-byte bank groups
+        const int ckey = ct / CH, cc = ct % CH;
+        const bool turn = (cc / 4) & 1;
+        const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
+        const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
+        const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
+        const uint32_t total = (uint32_t)(w.end - w.u);
+        // K or V of tile x to its operand buffer, which the tile before must have left
+        auto convert = [&](bool values, uint32_t x) -> bool {
+            const uint32_t stage = x % N;
+            bool good = tc_wait(values ? &rvfull[stage] : &rkfull[stage], x / N, deadline);
+            if (good && x > 0) good = tc_wait(values ? &vempty[0] : &kempty[0], x - 1, deadline);
+            if (!__all_sync(~0u, good)) return false;
+            if (!values && cw < 2) {
+                // scales of the tile's keys, the softmax scale in the keys' ones, and
+                // the largest of those
+                const float2 *src = reinterpret_cast<const float2 *>(smem + C::kOffRawScale + stage * 512);
+                float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (x % kTcInfo) * C::kInfoBytes);
+                if (cw == 0) {
+                    const float a = src[lane].x * p.scale_log2, b = src[lane + 32].x * p.scale_log2;
+                    dst[lane] = a;
+                    dst[lane + 32] = b;
+                    float top = max_nan(fabsf(a), fabsf(b));
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+                    if (lane == 0) dst[128] = top;
+                } else {
+                    dst[64 + lane] = src[lane].y;
+                    dst[96 + lane] = src[lane + 32].y;
+                }
+            }
+            const uint4 *src =
+                reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + values) * C::kRawBytes) + ct;
+            uint8_t *dst = smem + (values ? C::kOffV : C::kOffK);
+            constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
+            constexpr int G = N4 < 4 ? N4 : 4;
+#pragma unroll
+            for (int i0 = 0; i0 < N4; i0 += G) {
+                uint4 u[G];
+#pragma unroll
+                for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    uint4 a, b;
+                    q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
+                    q8_to_bf16(turn ? u[i].w : u[i].y, a.z, a.w);
+                    q8_to_bf16(turn ? u[i].x : u[i].z, b.x, b.y);
+                    q8_to_bf16(turn ? u[i].y : u[i].w, b.z, b.w);
+                    // 128 / CH keys further: a multiple of 8, the same swizzle
+                    uint8_t *row = dst + (i0 + i) * (128 / CH) * 128;
+                    *reinterpret_cast<uint4 *>(row + at0) = a;
+                    *reinterpret_cast<uint4 *>(row + at1) = b;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(values ? &vfull[0] : &kfull[0]);
+                mbar_arrive(values ? &rvempty[stage] : &rkempty[stage]);
+            }
+            return true;
+        };
+        // the keys run one tile ahead: their buffer is free as soon as the scores
+        // are made, the values' only after the softmax
+        ok = convert(false, 0);
+        for (uint32_t x = 0; ok && x < total; ++x) {
+            if (x + 1 < total) ok = convert(false, x + 1);
+            ok = ok && convert(true, x);
+        }
+        if (!ok && lane == 0) atomicOr(p.status, 8u);
+    }
     }
     tc_fence_before();
     __syncthreads();

@@ -80,7 +80,7 @@ struct KvAttendParams {
     float2 *part_ml;   // their maxima and sums [2 * CTAs][rows]
     uint32_t *counters;
     uint32_t n_counters;
-    int32_t join_later;  // parts are joined by w12_kv_join_kernel
+    int32_t join_later;  // warps per row of w12_kv_join_kernel, which joins the parts; 0: no such launch
     uint32_t *status;
     uint64_t timeout_ns;
 };

@@ -79,20 +79,23 @@ struct AttendPlan {
 // the last CTA is the longer way: one request of 777 tokens 7.4 against 10.4 us, two
 // of 100001 116 against 121; with fewer, most rows have one part and the second
 // kernel only costs: 128 requests of 1024 visible tokens 74 against 56 us.
-inline bool join_later(int rows, int group, int kv_heads, int max_new, int requests, int ctas) {
-    if (rows == dev::kTcRows) return true;
-    const int64_t blocks = ((int64_t)(max_new < 1 ? 1 : max_new) * group + rows - 1) / rows;
-    return ctas >= 2 * blocks * kv_heads * requests;
+// Returns the warps per row of the second kernel, 0: none.
+inline int join_warps(int rows, int group, int kv_heads, int max_new, int requests, int ctas) {
+    const int64_t blocks = ((int64_t)(max_new < 1 ? 1 : max_new) * group + rows - 1) / rows * kv_heads * requests;
+    return ctas >= 16 * blocks ? 8 : ctas >= 2 * blocks || rows == dev::kTcRows ? 1 : 0;
 }
 
-// The second kernel, for launches of `rows`-row blocks.
-template <int D>
+// The second kernel, for launches of `rows`-row blocks.  A warp per row where a row
+// has up to 16 parts or so (16-token trees, 5 parts: 5 us against 19 with eight
+// warps, a CTA per row); eight where it has more.
+template <int D, int WPR>
 int join_launch(const DeviceView &d, int rows, const dev::KvAttendParams &p, int ctas, void *stream, std::string *err) {
-    const auto kernel = rows == 8    ? &dev::w12_kv_join_kernel<D, 8>
-                        : rows == 16 ? &dev::w12_kv_join_kernel<D, 16>
-                        : rows == 32 ? &dev::w12_kv_join_kernel<D, 32>
-                                     : &dev::w12_kv_join_kernel<D, dev::kTcRows>;
-    const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)(p.tokens * p.group * p.kv_heads)), dev::kJoinThreads, 0, 1,
+    const auto kernel = rows == 8    ? &dev::w12_kv_join_kernel<D, 8, WPR>
+                        : rows == 16 ? &dev::w12_kv_join_kernel<D, 16, WPR>
+                        : rows == 32 ? &dev::w12_kv_join_kernel<D, 32, WPR>
+                                     : &dev::w12_kv_join_kernel<D, dev::kTcRows, WPR>;
+    const int64_t out_rows = (int64_t)p.tokens * p.group * p.kv_heads, per = dev::kJoinThreads / 32 / WPR;
+    const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)((out_rows + per - 1) / per)), dev::kJoinThreads, 0, 1,
                                     stream, p, ctas);
     if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend join launch", err);
     return W12_OK;
