@@ -41,11 +41,24 @@
 namespace w12 {
 namespace dev {
 
-constexpr int kAttendTile = 64;       // keys of a pipeline stage
+constexpr int kAttendTile = 64;       // keys of a pipeline stage of the tcgen05 kernel
 constexpr int kAttendSlice = 16;      // keys of one TMA box and of one mma
 constexpr int kAttendThreads = 160;   // four consumer warps and the producer
 constexpr float kAttendLazy = 8.0f;   // how far a score may pass the running maximum (log2)
 constexpr float kLn2 = 0.69314718055994530942f;
+
+// CTAs per SM that a variant is made for, by bytes of a stage and registers.
+template <int D, bool Q8, int NT>
+constexpr int attend_ctas() {
+    return D == 256 && !Q8 ? 1 : D == 64 && Q8 && NT == 1 ? 3 : 2;
+}
+
+// Keys of a pipeline stage: 128 where they fit 32 KB, so that a warp has two slices
+// for each wait and works on both at once; else 64.
+template <int D, bool Q8>
+struct AttendTile {
+    static constexpr int kKeys = D * (Q8 ? 1 : 2) <= 128 ? 128 : 64;
+};
 
 template <int D, bool Q8, int WK, int WR, int NT>
 struct AttendCfg {
@@ -55,10 +68,16 @@ struct AttendCfg {
     static constexpr int kRowBytes = D * kElem < 128 ? D * kElem : 128;  // swizzled box rows
     static constexpr int kHalves = D * kElem / kRowBytes;
     static constexpr int kSliceBytes = kAttendSlice * D * kElem;
-    static constexpr int kTileBytes = 4 * kSliceBytes;  // k (or v) of a stage
+    static constexpr int kTile = AttendTile<D, Q8>::kKeys;
+    static constexpr int kSlices = kTile / kAttendSlice;
+    static constexpr int kPair = kSlices / WK >= 2 ? 2 : 1;  // slices a warp works on at once
+    static constexpr int kTileBytes = kSlices * kSliceBytes;  // k (or v) of a stage
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kStages = kStageBytes >= 65536 ? 3 : 98304 / kStageBytes > 8 ? 8 : 98304 / kStageBytes;
-    static constexpr int kScaleBytes = Q8 ? 512 : 0;  // per stage: 64 keys x (k, v)
+    static constexpr int kCtas = attend_ctas<D, Q8, NT>();
+    static constexpr int kRing = (kCtas == 1 ? 192 : kCtas == 2 ? 96 : kCtas == 3 ? 60 : 48) * 1024;
+    static constexpr int kStages = kRing / kStageBytes > 8 ? 8 : kRing / kStageBytes;
+    static_assert(kStages >= 2, "a ring");
+    static constexpr int kScaleBytes = Q8 ? kTile * 8 : 0;  // per stage: (k, v) of each key
     static constexpr int kMergeStride = 68;           // floats: 64 columns and 4 of skew
     static constexpr int kOffScales = kStages * kStageBytes;
     static constexpr int kOffMerge = kOffScales + kStages * kScaleBytes;
@@ -98,13 +117,21 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// (a & mask) ^ bits as one instruction (left to itself the compiler makes two, each
+// with a constant of its own).
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+    return d;
+}
+
 // Four int8 to BF16, exactly: bytes 0 and 2 to lo, bytes 1 and 3 to hi.  With
 // b = byte: 128 + (b & 127) is BF16 0x4300 | (b & 127); adding -128 (b >= 0) or
 // -256 (b < 0), which is BF16 0xC300 | (b & 128), gives b, which BF16 holds.
 __device__ __forceinline__ void q8_to_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     const uint32_t h = w >> 8;
-    const uint32_t a0 = (w & 0x007F007Fu) | 0x43004300u, b0 = (w & 0x00800080u) | 0xC300C300u;
-    const uint32_t a1 = (h & 0x007F007Fu) | 0x43004300u, b1 = (h & 0x00800080u) | 0xC300C300u;
+    const uint32_t a0 = and_xor(w, 0x007F007Fu, 0x43004300u), b0 = and_xor(w, 0x00800080u, 0xC300C300u);
+    const uint32_t a1 = and_xor(h, 0x007F007Fu, 0x43004300u), b1 = and_xor(h, 0x00800080u, 0xC300C300u);
     asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a0), "r"(b0));
     asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(a1), "r"(b1));
 }
@@ -127,7 +154,7 @@ struct KvRequest {
     int64_t units;
 };
 
-template <int ROWS>
+template <int ROWS, int TILE>
 __device__ __forceinline__ KvRequest kv_request(const KvAttendParams &p, int b) {
     KvRequest r;
     r.q0 = min(max(p.cu_new[b], 0), p.tokens);
@@ -136,8 +163,8 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttendParams &p, int b) 
     r.kv = (int32_t)min((int64_t)r.past + r.qlen, (int64_t)p.max_keys);
     // first key that any of the request's new tokens sees
     r.first = p.window > 0 ? (int32_t)max((int64_t)r.past + 1 - p.window, (int64_t)0) : 0;
-    r.tile0 = min(r.first, r.kv) / kAttendTile;
-    r.ntiles = max((r.kv + kAttendTile - 1) / kAttendTile - r.tile0, 1);
+    r.tile0 = min(r.first, r.kv) / TILE;
+    r.ntiles = max((r.kv + TILE - 1) / TILE - r.tile0, 1);
     r.rblocks = (int32_t)(((int64_t)r.qlen * p.group + ROWS - 1) / ROWS);
     r.units = (int64_t)p.kv_heads * r.rblocks * r.ntiles;
     return r;
@@ -156,11 +183,11 @@ struct KvWalk {
     int32_t b, ctas;
 };
 
-template <int ROWS>
+template <int ROWS, int TILE>
 __device__ __forceinline__ bool kv_walk_init(const KvAttendParams &p, KvWalk &w, KvRequest &r) {
     const int lane = threadIdx.x & 31;
     int64_t sum = 0;
-    for (int b = lane; b < p.requests; b += 32) sum += kv_request<ROWS>(p, b).units;
+    for (int b = lane; b < p.requests; b += 32) sum += kv_request<ROWS, TILE>(p, b).units;
     w.total = warp_sum_i64(sum);
     w.ctas = (int32_t)min((int64_t)gridDim.x, w.total);
     if ((int)blockIdx.x >= w.ctas) return false;
@@ -168,7 +195,7 @@ __device__ __forceinline__ bool kv_walk_init(const KvAttendParams &p, KvWalk &w,
     w.end = w.total * (blockIdx.x + 1) / w.ctas;
     int64_t before = 0;
     for (int b0 = 0; b0 < p.requests; b0 += 32) {
-        const int64_t own = b0 + lane < p.requests ? kv_request<ROWS>(p, b0 + lane).units : 0;
+        const int64_t own = b0 + lane < p.requests ? kv_request<ROWS, TILE>(p, b0 + lane).units : 0;
         int64_t inc = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -180,7 +207,7 @@ __device__ __forceinline__ bool kv_walk_init(const KvAttendParams &p, KvWalk &w,
             const int src = __ffs(hit) - 1;
             w.b = b0 + src;
             w.start = __shfl_sync(~0u, before + inc - own, src);
-            r = kv_request<ROWS>(p, w.b);
+            r = kv_request<ROWS, TILE>(p, w.b);
             return true;
         }
         before += __shfl_sync(~0u, inc, 31);
@@ -205,12 +232,12 @@ __device__ __forceinline__ KvPiece kv_piece(const KvWalk &w, const KvRequest &r)
 }
 
 // Moves on by n units within the request, to the next request where it ends.
-template <int ROWS>
+template <int ROWS, int TILE>
 __device__ __forceinline__ void kv_advance(const KvAttendParams &p, KvWalk &w, KvRequest &r, int32_t n) {
     w.u += n;
     while (w.u < w.end && w.u >= w.start + r.units) {
         w.start += r.units;
-        r = kv_request<ROWS>(p, ++w.b);
+        r = kv_request<ROWS, TILE>(p, ++w.b);
     }
 }
 
@@ -377,11 +404,11 @@ struct KvPageWindow {
 };
 
 template <int D, bool Q8, int WK, int WR, int NT>
-__global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvAttendParams p,
+__global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_kv_attend_kernel(const KvAttendParams p,
                                                                        const __grid_constant__ CUtensorMap tm_k,
                                                                        const __grid_constant__ CUtensorMap tm_v) {
     using C = AttendCfg<D, Q8, WK, WR, NT>;
-    constexpr int ROWS = C::kRows, KS = D / 16;
+    constexpr int ROWS = C::kRows, KS = D / 16, TILE = C::kTile, PAIR = C::kPair;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     float *merge = reinterpret_cast<float *>(smem + C::kOffMerge);
@@ -410,7 +437,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
 
     KvWalk w;
     KvRequest r;
-    if (!kv_walk_init<ROWS>(p, w, r)) return;  // the same for the whole CTA
+    if (!kv_walk_init<ROWS, TILE>(p, w, r)) return;  // the same for the whole CTA
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
@@ -419,20 +446,20 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
         while (ok && w.u < w.end) {
             const KvPiece c = kv_piece(w, r);
             KvPageWindow pages;
-            pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * kAttendTile / p.page_size,
+            pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * TILE / p.page_size,
                         (r.kv + p.page_size - 1) / p.page_size);
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
                 const uint32_t stage = it % C::kStages, round = it / C::kStages;
-                // lane s < 4 deals with slice s
-                const int32_t t0 = (r.tile0 + j) * kAttendTile, kb = t0 + (lane & 3) * kAttendSlice;
-                const bool want = lane < 4 && kb < r.kv && kb + kAttendSlice > r.first;
+                // lane s deals with slice s
+                const int32_t t0 = (r.tile0 + j) * TILE, kb = t0 + (lane % C::kSlices) * kAttendSlice;
+                const bool want = lane < C::kSlices && kb < r.kv && kb + kAttendSlice > r.first;
                 const int32_t e = kb / p.page_size, off = kb - e * p.page_size;
                 const int32_t found = pages.get(t0 / p.page_size, e), page = want ? found : -1;
                 if (round > 0) ok = mbar_wait(&empty[stage], (round - 1) & 1, deadline);
                 ok = __shfl_sync(~0u, ok, 0);
                 if (!ok) break;
                 const bool here = page >= 0 && page < p.num_pages;
-                const uint32_t mask = __ballot_sync(~0u, here) & 15u;
+                const uint32_t mask = __ballot_sync(~0u, here);
                 if (lane == 0) {
                     present[stage] = mask;
                     mbar_arrive_expect_tx(&full[stage],
@@ -450,7 +477,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
                                  &full[stage]);
                 }
             }
-            if (ok) kv_advance<ROWS>(p, w, r, c.jb - c.ja);
+            if (ok) kv_advance<ROWS, TILE>(p, w, r, c.jb - c.ja);
         }
         if (!ok) {
             // no copy may still be in flight when the CTA ends
@@ -474,6 +501,9 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
         const KvPiece c = kv_piece(w, r);
         const int32_t nrows = min((int64_t)ROWS, (int64_t)r.qlen * p.group - (int64_t)c.rb * ROWS);
         const int32_t row0 = c.rb * ROWS;
+        // every row sees the keys from low on and before lim
+        const int32_t lim = min(r.kv, p.tree ? r.past : r.past + 1);
+        const int32_t low = p.window > 0 ? (int32_t)max((int64_t)r.past + r.qlen - p.window, (int64_t)0) : 0;
 
         // q as the mma's B operand: row (n) g of each 8-row tile, columns (k) of
         // step ks in the order the A operand's layout wants
@@ -519,59 +549,68 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
             }
             __syncwarp();
             const uint32_t mask = present[stage];
+            const int32_t tb = (r.tile0 + j) * TILE;
             const uint32_t kbase = smem_u32(smem + stage * C::kStageBytes), vbase = kbase + C::kTileBytes;
-            for (int s = wk; s < 4; s += WK) {
-                if (!((mask >> s) & 1u)) continue;
-                const int32_t kb = (r.tile0 + j) * kAttendTile + s * kAttendSlice;
-                const uint32_t ks_base = kbase + s * C::kSliceBytes, vs_base = vbase + s * C::kSliceBytes;
+#pragma unroll 1
+            for (int s0 = wk; s0 < C::kSlices; s0 += PAIR * WK) {
+                // slices s0 (and s0 + WK)
+                const uint32_t both = PAIR == 2 ? (mask >> s0 & 1u) | (mask >> (s0 + WK) & 1u) << 1 : mask >> s0 & 1u;
+                if (both == 0) continue;
                 // scores of 16 keys (rows g, g + 8) and NT * 8 rows (columns 2t, 2t + 1)
-                float x[NT][4] = {};
-                if (!Q8) {
+                float x[PAIR][NT][4] = {};
+                float vs[PAIR][2];
+                {
                     const int krow = ((lane >> 3) & 1) * 8 + (lane & 7);
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const int chunk = 2 * ks + (lane >> 4);
-                        uint32_t a[4];
-                        ldsm4(ks_base + (chunk / 8) * (16 * 128) + krow * 128 + (((chunk % 8) ^ (krow & 7)) << 4), a);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_bf16(x[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-                    }
-                } else {
                     constexpr int CH = C::kRowBytes / 16;  // 16-byte chunks of a box row
-                    const int krow = ((lane >> 3) & 1) * 8 + (lane & 7);
                     const int sw = CH == 8 ? krow & 7 : (krow >> 1) & 3;
+                    const uint32_t row = kbase + s0 * C::kSliceBytes + krow * C::kRowBytes;
+                    constexpr int STEP = Q8 ? 2 : 1;
 #pragma unroll
-                    for (int k2 = 0; k2 < KS / 2; ++k2) {
-                        const int chunk = 2 * k2 + (lane >> 4);
-                        uint32_t w4[4];
-                        ldsm4(ks_base + (chunk / CH) * (16 * C::kRowBytes) + krow * C::kRowBytes +
-                                  (((chunk % CH) ^ sw) << 4),
-                              w4);
+                    for (int ks = 0; ks < KS; ks += STEP) {
+                        const int chunk = Q8 ? ks + (lane >> 4) : 2 * ks + (lane >> 4);
+                        const uint32_t at = (chunk / CH) * (16 * C::kRowBytes) + (((chunk % CH) ^ sw) << 4);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint32_t a[4];
-                            q8_to_bf16(w4[2 * e], a[0], a[2]);
-                            q8_to_bf16(w4[2 * e + 1], a[1], a[3]);
+                        for (int u = 0; u < PAIR; ++u) {
+                            uint32_t w4[4];
+                            ldsm4(row + u * WK * C::kSliceBytes + at, w4);
+                            if (!Q8) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_bf16(x[nt], a, qf[nt][2 * k2 + e][0], qf[nt][2 * k2 + e][1]);
+                                for (int nt = 0; nt < NT; ++nt) mma_bf16(x[u][nt], w4, qf[nt][ks][0], qf[nt][ks][1]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    uint32_t a[4];
+                                    q8_to_bf16(w4[2 * e], a[0], a[2]);
+                                    q8_to_bf16(w4[2 * e + 1], a[1], a[3]);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        mma_bf16(x[u][nt], a, qf[nt][ks + e][0], qf[nt][ks + e][1]);
+                                }
+                            }
                         }
                     }
                 }
-                float vs0 = 1.0f, vs1 = 1.0f, sc0 = p.scale_log2, sc1 = p.scale_log2;
-                if (Q8) {
-                    const float2 *sc =
-                        reinterpret_cast<const float2 *>(smem + C::kOffScales + stage * C::kScaleBytes) + s * 16;
-                    const float2 a = sc[g], b = sc[g + 8];
-                    sc0 *= a.x, sc1 *= b.x, vs0 = a.y, vs1 = b.y;
-                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) x[nt][0] *= sc0, x[nt][1] *= sc0, x[nt][2] *= sc1, x[nt][3] *= sc1;
+                for (int u = 0; u < PAIR; ++u) {
+                    float sc0 = p.scale_log2, sc1 = p.scale_log2;
+                    vs[u][0] = vs[u][1] = 1.0f;
+                    if (Q8) {
+                        const float2 *sc =
+                            reinterpret_cast<const float2 *>(smem + C::kOffScales + stage * C::kScaleBytes) +
+                            (s0 + u * WK) * 16;
+                        const float2 a = sc[g], b = sc[g + 8];
+                        sc0 *= a.x, sc1 *= b.x, vs[u][0] = a.y, vs[u][1] = b.y;
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        x[u][nt][0] *= sc0, x[u][nt][1] *= sc0, x[u][nt][2] *= sc1, x[u][nt][3] *= sc1;
+                }
 
-                // keys that some row does not see
-                const bool edge = kb + kAttendSlice > (p.tree ? r.past : r.past + 1) || kb + kAttendSlice > r.kv ||
-                                  (p.window > 0 && kb <= (int64_t)r.past + r.qlen - 1 - p.window);
-                uint32_t seen = ~0u;  // bit 4 nt + c: score c of tile nt
+                // keys that some row does not see, or that are not there
+                const int32_t kb = tb + s0 * kAttendSlice;
+                constexpr int SPAN = ((PAIR - 1) * WK + 1) * kAttendSlice;
+                const bool edge = kb > lim - SPAN || kb < low || both != (1u << PAIR) - 1u;
+                uint32_t seen = ~0u;  // bit 4 (u NT + nt) + c: score c of tile nt of slice u
                 if (edge) {
                     seen = 0;
 #pragma unroll
@@ -583,31 +622,42 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
                             KvRowView v;
                             v.index = kv_index(r, i);
                             v.tree = p.tree ? p.tree[r.q0 + i] : 0u;
-                            if (kv_sees(p, r, v, kb + g)) seen |= 1u << (4 * nt + e);
-                            if (kv_sees(p, r, v, kb + g + 8)) seen |= 1u << (4 * nt + e + 2);
+#pragma unroll
+                            for (int u = 0; u < PAIR; ++u) {
+                                const int32_t key = kb + u * WK * kAttendSlice + g;
+                                if (!((both >> u) & 1u)) continue;
+                                if (kv_sees(p, r, v, key)) seen |= 1u << (4 * (u * NT + nt) + e);
+                                if (kv_sees(p, r, v, key + 8)) seen |= 1u << (4 * (u * NT + nt) + e + 2);
+                            }
                         }
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int u = 0; u < PAIR; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!((seen >> (4 * nt + e)) & 1u)) x[nt][e] = -INFINITY;
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!((seen >> (4 * (u * NT + nt) + e)) & 1u)) x[u][nt][e] = -INFINITY;
                 }
 
                 // running maximum
                 bool raise = false;
+                float top[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        raise |= fmaxf(x[nt][e], x[nt][e + 2]) > m[nt][e] + kAttendLazy;
+                    for (int e = 0; e < 2; ++e) {
+                        top[nt][e] = fmaxf(x[0][nt][e], x[0][nt][e + 2]);
+                        if (PAIR == 2) top[nt][e] = fmaxf(fmaxf(top[nt][e], x[PAIR - 1][nt][e]), x[PAIR - 1][nt][e + 2]);
+                        raise |= top[nt][e] > m[nt][e] + kAttendLazy;
+                    }
                 if (__any_sync(~0u, raise)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float al[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float v = fmaxf(x[nt][e], x[nt][e + 2]);
+                            float v = top[nt][e];
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
@@ -624,94 +674,112 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
                 // probabilities; l sums them in fp32, the tensor cores get them (with
                 // Q8 times the value's scale) rounded to BF16: at most 2^-8 of each
                 // weight, as the rounding of the output
-                uint32_t pb[NT][2];
+                uint32_t pb[PAIR][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
                     const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
-                    float p0 = ex2(x[nt][0] - m0), p1 = ex2(x[nt][1] - m1);
-                    float p2 = ex2(x[nt][2] - m0), p3 = ex2(x[nt][3] - m1);
-                    l[nt][0] += p0 + p2;
-                    l[nt][1] += p1 + p3;
-                    if (Q8) {
-                        p0 *= vs0, p1 *= vs0, p2 *= vs1, p3 *= vs1;
-                        if (edge) {  // an unseen key's scale may be anything
-                            const uint32_t sn = seen >> (4 * nt);
-                            p0 = sn & 1u ? p0 : 0.0f, p1 = sn & 2u ? p1 : 0.0f;
-                            p2 = sn & 4u ? p2 : 0.0f, p3 = sn & 8u ? p3 : 0.0f;
+#pragma unroll
+                    for (int u = 0; u < PAIR; ++u) {
+                        float p0 = ex2(x[u][nt][0] - m0), p1 = ex2(x[u][nt][1] - m1);
+                        float p2 = ex2(x[u][nt][2] - m0), p3 = ex2(x[u][nt][3] - m1);
+                        l[nt][0] += p0 + p2;
+                        l[nt][1] += p1 + p3;
+                        if (Q8) {
+                            p0 *= vs[u][0], p1 *= vs[u][0], p2 *= vs[u][1], p3 *= vs[u][1];
+                            if (edge) {  // an unseen key's scale may be anything
+                                const uint32_t sn = seen >> (4 * (u * NT + nt));
+                                p0 = sn & 1u ? p0 : 0.0f, p1 = sn & 2u ? p1 : 0.0f;
+                                p2 = sn & 4u ? p2 : 0.0f, p3 = sn & 8u ? p3 : 0.0f;
+                            }
                         }
+                        pb[u][nt][0] = movmatrix(pack_bf16(p0, p1));
+                        pb[u][nt][1] = movmatrix(pack_bf16(p2, p3));
                     }
-                    const uint32_t a = pack_bf16(p0, p1), b = pack_bf16(p2, p3);
-                    pb[nt][0] = movmatrix(a);
-                    pb[nt][1] = movmatrix(b);
                 }
 
                 // o (columns of the head x rows) += v^T p^T
+                const uint32_t vs0 = vbase + s0 * C::kSliceBytes;
                 if (!Q8) {
                     const int vrow = (lane >> 4) * 8 + (lane & 7);
+                    constexpr int CH = C::kRowBytes / 16;
+                    auto v_at = [&](int u, int mt) {
+                        const int chunk = 2 * mt + ((lane >> 3) & 1);
+                        return vs0 + u * WK * C::kSliceBytes + (chunk / CH) * (16 * C::kRowBytes) +
+                               vrow * C::kRowBytes + (((chunk % CH) ^ (vrow & 7)) << 4);
+                    };
                     bool odd = false;  // a value that is not finite behind a key that some row does not see
-                    uint32_t k0 = ~0u, k1 = ~0u;
-                    if (edge) {
-                        // keys behind the request's last one hold anything: zero
-                        const int32_t nv = r.kv - kb;
-                        k0 = (2 * t < nv ? 0xFFFFu : 0u) | (2 * t + 1 < nv ? 0xFFFF0000u : 0u);
-                        k1 = (2 * t + 8 < nv ? 0xFFFFu : 0u) | (2 * t + 9 < nv ? 0xFFFF0000u : 0u);
-#pragma unroll 4
-                        for (int mt = 0; mt < KS; ++mt) {
-                            const int chunk = 2 * mt + ((lane >> 3) & 1);
-                            uint32_t a[4];
-                            ldsm4_trans(
-                                vs_base + (chunk / 8) * (16 * 128) + vrow * 128 + (((chunk % 8) ^ (vrow & 7)) << 4), a);
-                            a[0] &= k0, a[1] &= k0, a[2] &= k1, a[3] &= k1;
+                    uint32_t keep[PAIR][2];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                odd |= (a[e] & 0x7F80u) == 0x7F80u || (a[e] & 0x7F800000u) == 0x7F800000u;
+                    for (int u = 0; u < PAIR; ++u) keep[u][0] = keep[u][1] = ~0u;
+                    if (edge) {
+#pragma unroll
+                        for (int u = 0; u < PAIR; ++u) {
+                            // keys behind the request's last one, and missing slices, hold
+                            // anything: zero
+                            const int32_t nv = (both >> u) & 1u ? r.kv - (kb + u * WK * kAttendSlice) : 0;
+                            keep[u][0] = (2 * t < nv ? 0xFFFFu : 0u) | (2 * t + 1 < nv ? 0xFFFF0000u : 0u);
+                            keep[u][1] = (2 * t + 8 < nv ? 0xFFFFu : 0u) | (2 * t + 9 < nv ? 0xFFFF0000u : 0u);
+#pragma unroll 4
+                            for (int mt = 0; mt < KS; ++mt) {
+                                uint32_t a[4];
+                                ldsm4_trans(v_at(u, mt), a);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    a[e] &= keep[u][e / 2];
+                                    odd |= (a[e] & 0x7F80u) == 0x7F80u || (a[e] & 0x7F800000u) == 0x7F800000u;
+                                }
+                            }
                         }
                         odd = __any_sync(~0u, odd);
                     }
                     if (!odd) {
 #pragma unroll
                         for (int mt = 0; mt < KS; ++mt) {
-                            const int chunk = 2 * mt + ((lane >> 3) & 1);
-                            uint32_t a[4];
-                            ldsm4_trans(
-                                vs_base + (chunk / 8) * (16 * 128) + vrow * 128 + (((chunk % 8) ^ (vrow & 7)) << 4), a);
-                            a[0] &= k0, a[1] &= k0, a[2] &= k1, a[3] &= k1;
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_bf16(o[mt][nt], a, pb[nt][0], pb[nt][1]);
+                            for (int u = 0; u < PAIR; ++u) {
+                                uint32_t a[4];
+                                ldsm4_trans(v_at(u, mt), a);
+                                a[0] &= keep[u][0], a[1] &= keep[u][0], a[2] &= keep[u][1], a[3] &= keep[u][1];
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma_bf16(o[mt][nt], a, pb[u][nt][0], pb[u][nt][1]);
+                            }
                         }
                     } else {
                         // 0 * NaN must not reach a row that does not see the key: one
                         // row at a time, with the values of its unseen keys zeroed
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            uint32_t bal[4];
+                        for (int u = 0; u < PAIR; ++u) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) bal[e] = __ballot_sync(~0u, (seen >> (4 * nt + e)) & 1u);
-                            for (int n = 0; n < 8; ++n) {
-                                // ballot bit 4 g + t holds key g (or g + 8) of row 2t + e
-                                const uint32_t lo = (n & 1 ? bal[1] : bal[0]) >> (n >> 1);
-                                const uint32_t hi = (n & 1 ? bal[3] : bal[2]) >> (n >> 1);
-                                uint32_t z0 = 0, z1 = 0;
-                                if ((lo >> (8 * t)) & 1u) z0 |= 0xFFFFu;
-                                if ((lo >> (8 * t + 4)) & 1u) z0 |= 0xFFFF0000u;
-                                if ((hi >> (8 * t)) & 1u) z1 |= 0xFFFFu;
-                                if ((hi >> (8 * t + 4)) & 1u) z1 |= 0xFFFF0000u;
-                                const uint32_t b0 = g == n ? pb[nt][0] : 0u, b1 = g == n ? pb[nt][1] : 0u;
+                            for (int nt = 0; nt < NT; ++nt) {
+                                uint32_t bal[4];
 #pragma unroll
-                                for (int mt = 0; mt < KS; ++mt) {
-                                    const int chunk = 2 * mt + ((lane >> 3) & 1);
-                                    uint32_t a[4];
-                                    ldsm4_trans(vs_base + (chunk / 8) * (16 * 128) + vrow * 128 +
-                                                    (((chunk % 8) ^ (vrow & 7)) << 4),
-                                                a);
-                                    a[0] &= z0, a[1] &= z0, a[2] &= z1, a[3] &= z1;
-                                    float y[4] = {};
-                                    mma_bf16(y, a, b0, b1);
-                                    // the other rows' sums are 0 * value here: only row n's count
-                                    if (2 * t == (n & ~1)) {
-                                        if (n & 1) o[mt][nt][1] += y[1], o[mt][nt][3] += y[3];
-                                        else o[mt][nt][0] += y[0], o[mt][nt][2] += y[2];
+                                for (int e = 0; e < 4; ++e)
+                                    bal[e] = __ballot_sync(~0u, (seen >> (4 * (u * NT + nt) + e)) & 1u);
+#pragma unroll 1
+                                for (int n = 0; n < 8; ++n) {
+                                    // ballot bit 4 g + t holds key g (or g + 8) of row 2t + e
+                                    const uint32_t lo = (n & 1 ? bal[1] : bal[0]) >> (n >> 1);
+                                    const uint32_t hi = (n & 1 ? bal[3] : bal[2]) >> (n >> 1);
+                                    uint32_t z0 = 0, z1 = 0;
+                                    if ((lo >> (8 * t)) & 1u) z0 |= 0xFFFFu;
+                                    if ((lo >> (8 * t + 4)) & 1u) z0 |= 0xFFFF0000u;
+                                    if ((hi >> (8 * t)) & 1u) z1 |= 0xFFFFu;
+                                    if ((hi >> (8 * t + 4)) & 1u) z1 |= 0xFFFF0000u;
+                                    const uint32_t b0 = g == n ? pb[u][nt][0] : 0u, b1 = g == n ? pb[u][nt][1] : 0u;
+#pragma unroll
+                                    for (int mt = 0; mt < KS; ++mt) {
+                                        uint32_t a[4];
+                                        ldsm4_trans(v_at(u, mt), a);
+                                        a[0] &= z0, a[1] &= z0, a[2] &= z1, a[3] &= z1;
+                                        float y[4] = {};
+                                        mma_bf16(y, a, b0, b1);
+                                        // the other rows' sums are 0 * value here: only
+                                        // row n's count
+                                        if (2 * t == (n & ~1)) {
+                                            if (n & 1) o[mt][nt][1] += y[1], o[mt][nt][3] += y[3];
+                                            else o[mt][nt][0] += y[0], o[mt][nt][2] += y[2];
+                                        }
                                     }
                                 }
                             }
@@ -722,20 +790,23 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
                     const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7);
                     const int sw = CH == 8 ? vrow & 7 : (vrow >> 1) & 3;
 #pragma unroll
-                    for (int m2 = 0; m2 < KS / 2; ++m2) {
-                        const int chunk = 2 * m2 + (lane >> 4);
-                        uint32_t w4[4];
-                        ldsm4_trans(vs_base + (chunk / CH) * (16 * C::kRowBytes) + vrow * C::kRowBytes +
-                                        (((chunk % CH) ^ sw) << 4),
-                                    w4);
+                    for (int m2 = 0; m2 < KS; m2 += 2) {
+                        const int chunk = m2 + (lane >> 4);
+                        const uint32_t at = vs0 + (chunk / CH) * (16 * C::kRowBytes) + vrow * C::kRowBytes +
+                                            (((chunk % CH) ^ sw) << 4);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            // rows g of the tile are the even columns 2g, rows g + 8 the odd ones
-                            uint32_t a[4];
-                            q8_to_bf16(w4[2 * e], a[0], a[1]);
-                            q8_to_bf16(w4[2 * e + 1], a[2], a[3]);
+                        for (int u = 0; u < PAIR; ++u) {
+                            uint32_t w4[4];
+                            ldsm4_trans(at + u * WK * C::kSliceBytes, w4);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_bf16(o[2 * m2 + e][nt], a, pb[nt][0], pb[nt][1]);
+                            for (int e = 0; e < 2; ++e) {
+                                // rows g of the tile are the even columns 2g, rows g + 8 the odd ones
+                                uint32_t a[4];
+                                q8_to_bf16(w4[2 * e], a[0], a[1]);
+                                q8_to_bf16(w4[2 * e + 1], a[2], a[3]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma_bf16(o[m2 + e][nt], a, pb[u][nt][0], pb[u][nt][1]);
+                            }
                         }
                     }
                 }
@@ -800,9 +871,9 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
 
         if (!whole && !p.join_later) {
             const KvParts q = kv_parts<ROWS>(p, w, r, c);
-            if (kv_arrive(p, q, last_flag)) kv_join<ROWS, D, 8>(p, q, r, c, nrows, (int)threadIdx.x, 128);
+            if (kv_arrive(p, q, last_flag)) kv_join<ROWS, D, C::kCtas < 3 ? 8 : 4>(p, q, r, c, nrows, (int)threadIdx.x, 128);
         }
-        kv_advance<ROWS>(p, w, r, c.jb - c.ja);
+        kv_advance<ROWS, TILE>(p, w, r, c.jb - c.ja);
     }
     if (!ok && warp == 0 && lane == 0) {
         // a wait ran out: no copy may still be in flight when the CTA ends
@@ -818,7 +889,7 @@ __global__ void __launch_bounds__(kAttendThreads) w12_kv_attend_kernel(const KvA
 // both in a fixed order.
 constexpr int kJoinThreads = 256;
 
-template <int D, int ROWS, int WPR>
+template <int D, int ROWS, int TILE, int WPR>
 __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAttendParams p, int grid) {
     constexpr int W = kJoinThreads / 32, V = D / 32;  // columns of a lane
     __shared__ float s_acc[WPR > 1 ? W : 1][D];
@@ -837,7 +908,7 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
     for (int b0 = 0; b0 < p.requests; b0 += 32) {
         KvRequest x;
         x.units = 0, x.q0 = x.qlen = 0;
-        if (b0 + lane < p.requests) x = kv_request<ROWS>(p, b0 + lane);
+        if (b0 + lane < p.requests) x = kv_request<ROWS, TILE>(p, b0 + lane);
         int64_t inc = x.units;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {

@@ -295,7 +295,7 @@ struct TcLoader {
         }
         ++it;
         if (++j == c.jb) {
-            kv_advance<kTcRows>(p, w, r, c.jb - c.ja);
+            kv_advance<kTcRows, kAttendTile>(p, w, r, c.jb - c.ja);
             if (w.u < w.end) open(p);
         }
         return true;
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
     const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
     KvWalk w;
     KvRequest r;
-    if (!kv_walk_init<kTcRows>(p, w, r)) return;  // the same for the whole CTA
+    if (!kv_walk_init<kTcRows, kAttendTile>(p, w, r)) return;  // the same for the whole CTA
     // TMEM only after the kernel before has finished, and the kernel behind only
     // when every CTA here has its TMEM: neither can then hold columns that the
     // other waits for
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
             {
                 KvWalk w2 = w1;
                 KvRequest r2 = r1;
-                kv_advance<kTcRows>(p, w2, r2, tiles);
+                kv_advance<kTcRows, kAttendTile>(p, w2, r2, tiles);
                 more = w2.u < w2.end;
                 if (more) {
                     const KvPiece c2 = kv_piece(w2, r2);
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                 __syncwarp();
             }
             ++piece;
-            if (ok) kv_advance<kTcRows>(p, w, r, n);
+            if (ok) kv_advance<kTcRows, kAttendTile>(p, w, r, n);
         }
         if (leader) {
             if (!ok) atomicOr(p.status, 8u);

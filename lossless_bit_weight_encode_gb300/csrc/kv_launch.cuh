@@ -88,17 +88,24 @@ inline int join_warps(int rows, int group, int kv_heads, int max_new, int reques
 // The second kernel, for launches of `rows`-row blocks.  A warp per row where a row
 // has up to 16 parts or so (16-token trees, 5 parts: 5 us against 19 with eight
 // warps, a CTA per row); eight where it has more.
-template <int D, int WPR>
+template <int D, int TILE, int WPR>
 int join_launch(const DeviceView &d, int rows, const dev::KvAttendParams &p, int ctas, void *stream, std::string *err) {
-    const auto kernel = rows == 8    ? &dev::w12_kv_join_kernel<D, 8, WPR>
-                        : rows == 16 ? &dev::w12_kv_join_kernel<D, 16, WPR>
-                        : rows == 32 ? &dev::w12_kv_join_kernel<D, 32, WPR>
-                                     : &dev::w12_kv_join_kernel<D, dev::kTcRows, WPR>;
+    const auto kernel = rows == 8    ? &dev::w12_kv_join_kernel<D, 8, TILE, WPR>
+                        : rows == 16 ? &dev::w12_kv_join_kernel<D, 16, TILE, WPR>
+                        : rows == 32 ? &dev::w12_kv_join_kernel<D, 32, TILE, WPR>
+                                     : &dev::w12_kv_join_kernel<D, dev::kTcRows, dev::kAttendTile, WPR>;
     const int64_t out_rows = (int64_t)p.tokens * p.group * p.kv_heads, per = dev::kJoinThreads / 32 / WPR;
     const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)((out_rows + per - 1) / per)), dev::kJoinThreads, 0, 1,
                                     stream, p, ctas);
     if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend join launch", err);
     return W12_OK;
+}
+
+template <int D, bool Q8>
+int join_parts(const DeviceView &d, int rows, const dev::KvAttendParams &p, int ctas, void *stream, std::string *err) {
+    constexpr int TILE = dev::AttendTile<D, Q8>::kKeys;
+    return p.join_later > 1 ? join_launch<D, TILE, 8>(d, rows, p, ctas, stream, err)
+                            : join_launch<D, TILE, 1>(d, rows, p, ctas, stream, err);
 }
 
 // One head_dim's kernels (kv_attend_*.cu): CTAs resident on the whole device
