@@ -65,7 +65,7 @@ int attend_call(const DeviceView &d, const w12_kv_cache &c, int rows, int *resid
 int attend_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_args &a, AttendPlan *plan,
                 std::string *err) {
     const int group = a.heads / c.kv_heads;
-    plan->rows = attend_rows(a.max_new, group);
+    plan->rows = attend_rows(a.max_new, group, c.kv_heads, a.requests, c.dtype == W12_KV_Q8, d.sm_count);
     int resident = 0;
     const int rc = attend_call(d, c, plan->rows, &resident, nullptr, nullptr, nullptr, 0, nullptr, err);
     if (rc != W12_OK) return rc;

@@ -19,7 +19,8 @@
 // the 8-wide N of mma.m16n8k16 and the keys (for k q^T) or the head's columns
 // (for v^T p^T) its M: nothing is padded from 6 rows to 128.  The probabilities
 // go from accumulator to operand layout with one movmatrix per 8 x 8.  Warps
-// split a tile's keys (WK) and, where the rows are many, the rows (WR).
+// split a tile's keys (WK) and, where a warp's registers do not hold the sums of all
+// rows, the rows (WR).
 //
 // Work split.  The unit is one 64-key tile of one (request, key head, row block);
 // all units form one line that the CTAs cut into equal ranges, whatever the

@@ -53,12 +53,20 @@ cudaError_t kv_launch(const DeviceView &d, void (*kernel)(KArgs...), dim3 grid, 
 
 constexpr int kKvMaxDevices = 64;
 
-// Rows of the tile a launch uses: new tokens times query heads per key head.  Up
-// to 32 the warp-level kernel with 8, 16 or 32 rows, above the tcgen05 kernel with
-// 128; more rows take several row blocks.
-inline int attend_rows(int max_new, int group) {
+// Rows of the tile a launch uses: new tokens times query heads per key head.  Up to
+// 8 the warp-level kernel, above 16 the tcgen05 kernel with 128 (more rows take
+// several row blocks).  30 rows measured 326 us against 532 with 32-row warp-level
+// tiles (64 requests of 8000 tokens, BF16; 8-bit 347 against 547), 128 against 133
+// for two requests of 100001.  Between 9 and 16 rows the warp-level kernel is the
+// shorter way for few row blocks (12 rows, one request of 777 tokens: 9.1 against
+// 10.6 us) and for 8-bit caches (64 x 8000: 325 against 340), the tcgen05 kernel for
+// as many blocks as SMs (64 x 8000, BF16: 315 against 343; windows of 1024: 76
+// against 81).
+inline int attend_rows(int max_new, int group, int kv_heads, int requests, bool q8, int sm_count) {
     const int64_t rows = (int64_t)(max_new < 1 ? 1 : max_new) * group;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : dev::kTcRows;
+    if (rows <= 8) return 8;
+    if (rows > 16 || (!q8 && (int64_t)kv_heads * requests >= sm_count)) return dev::kTcRows;
+    return 16;
 }
 
 // Workspace: the partial outputs, their maxima and sums, the counters.  The
@@ -92,7 +100,6 @@ template <int D, int TILE, int WPR>
 int join_launch(const DeviceView &d, int rows, const dev::KvAttendParams &p, int ctas, void *stream, std::string *err) {
     const auto kernel = rows == 8    ? &dev::w12_kv_join_kernel<D, 8, TILE, WPR>
                         : rows == 16 ? &dev::w12_kv_join_kernel<D, 16, TILE, WPR>
-                        : rows == 32 ? &dev::w12_kv_join_kernel<D, 32, TILE, WPR>
                                      : &dev::w12_kv_join_kernel<D, dev::kTcRows, dev::kAttendTile, WPR>;
     const int64_t out_rows = (int64_t)p.tokens * p.group * p.kv_heads, per = dev::kJoinThreads / 32 / WPR;
     const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)((out_rows + per - 1) / per)), dev::kJoinThreads, 0, 1,
@@ -164,10 +171,9 @@ int attend_tc_variant(const DeviceView &d, int *resident, const dev::KvAttendPar
                          per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
-// The variants of one head_dim.  Rows up to 16 (BF16 operands of q and the sums
-// of 8 or 16 rows in registers): the warps split a tile's keys.  More rows: they
-// split the rows too, because the sums of 32 rows x head_dim do not fit a warp.
-// 256 columns take twice the registers per row, so the rows are split earlier.
+// The variants of one head_dim.  With 8 rows the warps split a tile's keys; so they
+// do with 16, but for 256 columns, whose sums for 16 rows do not fit a warp: there
+// they split the rows too.
 template <int D, bool Q8>
 int attend_rows_variant(const DeviceView &d, int rows, int *resident, const dev::KvAttendParams *p,
                         const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
@@ -175,9 +181,6 @@ int attend_rows_variant(const DeviceView &d, int rows, int *resident, const dev:
     case 8: return attend_variant<D, Q8, 4, 1, 1>(d, resident, p, tm_k, tm_v, ctas, stream, err);
     case 16:
         return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(d, resident, p, tm_k, tm_v,
-                                                                                          ctas, stream, err);
-    case 32:
-        return attend_variant<D, Q8, D == 256 ? 1 : 2, D == 256 ? 4 : 2, D == 256 ? 1 : 2>(d, resident, p, tm_k, tm_v,
                                                                                           ctas, stream, err);
     default: return attend_tc_variant<D, Q8>(d, resident, p, tm_k, tm_v, ctas, stream, err);
     }
