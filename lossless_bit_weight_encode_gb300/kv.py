@@ -23,7 +23,7 @@ _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float3
 _workspaces = {}  # (device, stream handle) -> zeroed workspace of the attend calls on that stream
 
 
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
 # handle of a device's current stream, without the stream object around it
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -101,21 +101,17 @@ class KVStep:
     def __setattr__(self, name, value):
         # checked here, once, and not in every call of every layer
         if value is not None and name in self._kinds:
-            _ints(value, self._kinds[name], name, value.get_device() if value.is_cuda else "of its own")
+            _ints(value, self._kinds[name], name, self._one_device(value))
         elif value is not None and name == "tables":
-            _need(value.dtype is _I32 and value.dim() == 2 and value.stride(1) == 1 and value.is_cuda,
+            _need(value.dtype is _I32 and value.dim() == 2 and value.stride(1) == 1,
                   "tables must be an int32 CUDA tensor [requests, max_blocks] with contiguous rows")
+            self._one_device(value)
         object.__setattr__(self, name, value)
 
-    def _on(self, index, *names):
-        """Pointers of the named arrays, all on CUDA device `index`."""
-        out = []
-        for name in names:
-            t = getattr(self, name)
-            if t is None or t.get_device() != index:
-                raise ValueError(f"step.{name} is missing or not on CUDA device {index}")
-            out.append(t.data_ptr())
-        return out
+    def _one_device(self, t):
+        _need(t.is_cuda and t.get_device() == self.__dict__.setdefault("device", t.get_device()),
+              "a step's arrays must be on one CUDA device")
+        return t.get_device()
 
 
 class KVPages:
@@ -172,12 +168,12 @@ class KVPages:
             step.lens = lens
         if step.tables is not tables:
             step.tables = tables
-        lens_p, cu_p, pos_p, slots_p = step._on(index, "lens", "cu_new", "positions", "slots")
-        tokens = step.slots.numel()
-        _need(lens.numel() == n and new_lens.numel() == n, "lens and new_lens must have an entry per request")
-        _need(step.cu_new.numel() == n + 1 and step.positions.numel() == tokens,
-              "step belongs to another number of requests")
-        owned_p, state_p = self.owned.data_ptr(), self.ring_state.data_ptr()
+        cu, positions, slots, owned, state = step.cu_new, step.positions, step.slots, self.owned, self.ring_state
+        tokens = slots.numel()
+        if (step.device != index or lens.numel() != n or new_lens.numel() != n or cu.numel() != n + 1
+                or positions.numel() != tokens):
+            raise ValueError("lens, new_lens and step must be on the tables' device, with an entry per request")
+        owned_p, state_p = owned.data_ptr(), state.data_ptr()
         owned_o, state_o = owned_p, state_p
         if owned_out is not None:
             owned_o = _ints(owned_out, _I32, "owned_out", index)
@@ -186,9 +182,10 @@ class KVPages:
             state_o = _ints(ring_state_out, _I64, "ring_state_out", index)
             _need(ring_state_out.numel() == 2, "ring_state_out must have two entries")
         w12.w12_kv_plan(w12.w12_kv_plan_args(
-            lens_p, _ints(new_lens, _I32, "new_lens", index), owned_p, owned_o, tables.data_ptr(),
-            tables.stride(0) if n > 1 else blocks, self.ring.data_ptr(), state_p, state_o, cu_p, pos_p, slots_p, n,
-            blocks, self.page_size, self.ring.numel(), tokens, 1 if trim else 0), st)
+            lens.data_ptr(), _ints(new_lens, _I32, "new_lens", index), owned_p, owned_o, tables.data_ptr(),
+            tables.stride(0) if n > 1 else blocks, self.ring.data_ptr(), state_p, state_o, cu.data_ptr(),
+            positions.data_ptr(), slots.data_ptr(), n, blocks, self.page_size, self.ring.numel(), tokens,
+            1 if trim else 0), st)
         return step
 
 
@@ -216,6 +213,7 @@ class KVCache:
         self._c = w12.w12_kv_cache(k.data_ptr(), v.data_ptr(), None if scales is None else scales.data_ptr(), pages,
                                    stride[0], stride[1], stride[2], page, heads, dim,
                                    w12.KV_BF16 if scales is None else w12.KV_Q8)
+        self._scale = dim ** -0.5
         self._ws_bytes = {}
 
     @classmethod
@@ -243,30 +241,31 @@ class KVCache:
         dim, index = self.head_dim, self._index
         kp, ks, tokens, _ = _rows(k, dim, "k", index, self.kv_heads)
         vp, vs, nv, _ = _rows(v, dim, "v", index, self.kv_heads)
-        slots_p, = step._on(index, "slots")
-        _need(nv == tokens and step.slots.numel() == tokens, "k, v and step.slots must have as many tokens")
+        slots = step.slots
+        if slots is None or step.device != index or nv != tokens or slots.numel() != tokens:
+            raise ValueError("k, v and step.slots must have as many tokens, on the cache's device")
         qp = qs = op = os_ = heads = rot = rows = rp = pp = 0
         if rope is not None:
-            _need(rope.dtype is _F32 and rope.dim() == 2 and rope.is_contiguous() and rope.get_device() == index,
-                  "rope must be a contiguous fp32 tensor [positions, rot]")
-            pp, = step._on(index, "positions")
-            _need(step.positions.numel() == tokens, "step.positions must have as many tokens")
+            positions = step.positions
+            if (rope.dtype is not _F32 or rope.dim() != 2 or not rope.is_contiguous() or rope.get_device() != index
+                    or positions is None or positions.numel() != tokens):
+                raise ValueError("rope must be a contiguous fp32 tensor [positions, rot] on the cache's device and "
+                                 "step.positions have as many tokens as k")
             rows, rot = rope.shape
-            rp = rope.data_ptr()
-        wq = wk = 0
-        if q_norm is not None:
-            wq = self._weight(q_norm, "q_norm")
-        if k_norm is not None:
-            wk = self._weight(k_norm, "k_norm")
+            rp, pp = rope.data_ptr(), positions.data_ptr()
+        wq = self._weight(q_norm, "q_norm") if q_norm is not None else 0
+        wk = self._weight(k_norm, "k_norm") if k_norm is not None else 0
         if q is not None:
             qp, qs, nq, heads = _rows(q, dim, "q", index)
             if out is None:
                 out = torch.empty(q.shape, dtype=_BF16, device=self.device)
             op, os_, no, _ = _rows(out, dim, "out", index, heads)
-            _need(nq == tokens and no == tokens, "q, out and k must have as many tokens")
-        w12.w12_kv_store(self._c, w12.w12_kv_store_args(qp, kp, vp, op, qs, ks, vs, os_, wq, wk, rp, pp, slots_p, rows,
-                                                        tokens, heads, rot, 1 if interleaved else 0, eps), st)
-        return out.view(tokens, heads, dim) if q is not None else None
+            if nq != tokens or no != tokens:
+                raise ValueError("q, out and k must have as many tokens")
+        w12.w12_kv_store(self._c, w12.w12_kv_store_args(qp, kp, vp, op, qs, ks, vs, os_, wq, wk, rp, pp,
+                                                        slots.data_ptr(), rows, tokens, heads, rot,
+                                                        1 if interleaved else 0, eps), st)
+        return None if q is None else out if out.dim() == 3 else out.view(tokens, heads, dim)
 
     def _weight(self, w, name):
         if w.dtype is not _BF16 or w.dim() != 1 or w.numel() != self.head_dim or not w.is_contiguous() \
@@ -297,10 +296,9 @@ class KVCache:
             w12.w12_kv_read(self._c, sp, tokens, k.data_ptr(), v.data_ptr(), st)
         return k, v
 
-    def workspace(self, args, st):
+    def workspace(self, args, key, st):
         """The zeroed workspace of the attend calls on stream ``st`` (shared by
-        all caches), large enough for ``args``."""
-        key = (args.requests, args.tokens, args.heads, args.max_new, args.max_blocks)
+        all caches), large enough for ``args``; ``key``: what its size depends on."""
         size = self._ws_bytes.get(key)
         if size is None:
             size = self._ws_bytes[key] = w12.w12_kv_attend_workspace_size(self._c, args)
@@ -329,27 +327,30 @@ class KVCache:
     def _attend(self, q, step, scale, window, out, lse, workspace, st):
         dim, index = self.head_dim, self._index
         qp, qs, tokens, heads = _rows(q, dim, "q", index)
-        tables_p, lens_p, cu_p = step._on(index, "tables", "lens", "cu_new")
-        rows, blocks = step.tables.shape
-        n = step.lens.numel()
-        _need(rows == n and step.cu_new.numel() == n + 1, "step.tables, lens and cu_new do not agree")
+        tables, lens, cu, tree = step.tables, step.lens, step.cu_new, step.tree
+        rows, blocks = tables.shape
+        n = lens.numel()
+        if step.device != index or rows != n or cu.numel() != n + 1:
+            raise ValueError("step.tables, lens and cu_new must agree and be on the cache's device")
         tree_p = lse_p = 0
-        if step.tree is not None:
-            tree_p, = step._on(index, "tree")
-            _need(step.tree.numel() >= tokens, "step.tree must have a mask per token")
+        if tree is not None:
+            tree_p = tree.data_ptr()
+            _need(tree.numel() >= tokens, "step.tree must have a mask per token")
         if lse is not None:
-            _need(lse.dtype is _F32 and lse.shape == (tokens, heads) and lse.is_contiguous() and
-                  lse.get_device() == index, "lse must be contiguous fp32 [tokens, heads]")
+            if (lse.dtype is not _F32 or lse.shape != (tokens, heads) or not lse.is_contiguous()
+                    or lse.get_device() != index):
+                raise ValueError("lse must be contiguous fp32 [tokens, heads] on the cache's device")
             lse_p = lse.data_ptr()
         if out is None:
             out = torch.empty(q.shape, dtype=_BF16, device=self.device)
         op, os_, no, _ = _rows(out, dim, "out", index, heads)
-        _need(no == tokens, "out and q must have as many tokens")
+        if no != tokens:
+            raise ValueError("out and q must have as many tokens")
         if tokens == 0:
             return out
         args = w12.w12_kv_attend_args(
-            qp, op, lse_p, qs, os_, tables_p, step.tables.stride(0) if n > 1 else blocks, lens_p, cu_p, tree_p, n,
-            blocks, tokens, heads, step.max_new, window, dim ** -0.5 if scale is None else scale)
-        ws = self.workspace(args, st) if workspace is None else workspace
+            qp, op, lse_p, qs, os_, tables.data_ptr(), tables.stride(0) if n > 1 else blocks, lens.data_ptr(),
+            cu.data_ptr(), tree_p, n, blocks, tokens, heads, step.max_new, window, self._scale if scale is None else scale)
+        ws = self.workspace(args, (n, tokens, heads, step.max_new, blocks), st) if workspace is None else workspace
         w12.w12_kv_attend(self._c, args, ws.data_ptr(), ws.numel() * ws.element_size(), st)
         return out
