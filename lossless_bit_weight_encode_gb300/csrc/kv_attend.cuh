@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
         prefetch_tmap(&tm_v);
     }
     __syncthreads();
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // after the wait: w12_kv_join_kernel relies on it
     const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
 
     KvWalk w;
@@ -899,9 +899,9 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
     const int heads = p.group * p.kv_heads;
     const int64_t out_row = (int64_t)blockIdx.x * (W / WPR) + warp / WPR;
     const int32_t tok = (int32_t)(out_row / heads), h = (int32_t)(out_row - (int64_t)tok * heads);
-    pdl_launch_dependents();
-    pdl_wait();
-    // the token's request, its first unit and all units
+    // Lengths and offsets come from before the attention kernel, which lets this one
+    // start only when it has itself seen all that is before it.
+    // The token's request, its first unit and all units:
     int64_t total = 0, start = -1;
     KvRequest r;
     r.q0 = r.qlen = 0;
@@ -944,6 +944,8 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
         q = kv_parts<ROWS>(p, w, r, c);
         lr = rr - c.rb * ROWS;
     }
+    pdl_launch_dependents();
+    pdl_wait();
     if (WPR == 1 && q.n <= 1) return;
     float acc[V] = {}, mm = -INFINITY, sum = 0.0f;
     constexpr int U = V == 8 || WPR > 1 ? 4 : 8;  // parts whose loads are in flight
