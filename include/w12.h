@@ -405,7 +405,8 @@ typedef struct w12_kv_cache {
  * BUFFER_TOO_SMALL; where the new tokens are more than `tokens`, the ones behind
  * are left out, and where a length had to be clamped, SHAPE.
  * All arrays 4-byte aligned (the 64-bit ones 8-byte).  tables: row b at
- * tables + b * table_stride.  max_blocks * page_size < 2^31.
+ * tables + b * table_stride.  max_blocks * page_size and max_blocks * requests
+ * below 2^31.
  */
 typedef struct w12_kv_plan_args {
     const int32_t *lens, *new_lens;

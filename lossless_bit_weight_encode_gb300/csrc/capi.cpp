@@ -586,9 +586,10 @@ int w12_kv_plan(const w12_kv_plan_args *args, void *stream) {
         }
         if (args->page_size < 16 || args->page_size % 16 != 0 ||
             (int64_t)args->max_blocks * args->page_size >= (int64_t(1) << 31) ||
+            (int64_t)args->max_blocks * args->requests >= (int64_t(1) << 31) ||
             args->table_stride < args->max_blocks) {
-            err = "page_size must be a multiple of 16, max_blocks * page_size below 2^31 and table_stride at least "
-                  "max_blocks";
+            err = "page_size must be a multiple of 16, max_blocks * page_size and max_blocks * requests below 2^31 and "
+                  "table_stride at least max_blocks";
             return (int)W12_ERR_SHAPE;
         }
         for (const void *p : {(const void *)args->lens, (const void *)args->new_lens, (const void *)args->owned_in,

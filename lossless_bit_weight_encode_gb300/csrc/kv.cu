@@ -154,6 +154,7 @@ int kv_plan(const w12_kv_plan_args &a, void *stream, std::string *err) {
     p.max_blocks = a.max_blocks;
     p.page_size = a.page_size;
     p.ring_size = a.ring_size;
+    p.ring_inv = ~uint64_t(0) / (uint64_t)a.ring_size;
     p.tokens = a.tokens;
     p.trim = a.trim != 0;
     p.status = d.status;

@@ -33,6 +33,7 @@ struct KvPlanParams {
     int32_t *cu_new;
     int32_t *positions;
     int64_t *slots;
+    uint64_t ring_inv;  // floor((2^64 - 1) / ring_size)
     int32_t requests, max_blocks, page_size, ring_size, tokens, trim;
     uint32_t *status;
 };

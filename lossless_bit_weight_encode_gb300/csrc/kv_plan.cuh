@@ -29,7 +29,7 @@ __device__ __forceinline__ int32_t clamp_i32(int64_t v, int64_t lo, int64_t hi) 
 
 // Largest i in [0, n) with start[i] <= v (start[0] <= v holds).  Requests with
 // nothing share their successor's start, so the largest one is the owner.
-__device__ __forceinline__ int find_start(const int64_t *start, int n, int64_t v) {
+__device__ __forceinline__ int find_start(const int32_t *start, int n, int32_t v) {
     int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -37,6 +37,23 @@ __device__ __forceinline__ int find_start(const int64_t *start, int n, int64_t v
         else hi = mid;
     }
     return lo;
+}
+
+// Entry (base + i) of the ring, base < size (more than size entries on: only for an
+// inconsistent ring state).
+__device__ __forceinline__ int32_t ring_at(int32_t base, int32_t i, int32_t size) {
+    uint32_t x = (uint32_t)base + (uint32_t)i;
+    if (x >= (uint32_t)size) x -= (uint32_t)size;
+    if (x >= (uint32_t)size) x %= (uint32_t)size;
+    return (int32_t)x;
+}
+
+// v mod size for v >= 0, with inv = floor((2^64 - 1) / size): the high product is the
+// quotient or one less.
+__device__ __forceinline__ int32_t ring_base(int64_t v, int32_t size, uint64_t inv) {
+    const uint64_t u = v < 0 ? 0 : (uint64_t)v;
+    const int64_t r = (int64_t)(u - __umul64hi(u, inv) * (uint64_t)size);
+    return (int32_t)(r >= size ? r - size : r);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -54,97 +71,106 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanParams p) {
-    __shared__ int64_t s_tok[kPlanThreads], s_grow[kPlanThreads], s_drop[kPlanThreads];
+    // prefix sums of the chunk's requests: all fit 32 bits (the tables have fewer than
+    // 2^31 entries), but for the tokens, which are cut there
+    __shared__ int32_t s_tok[kPlanThreads], s_grow[kPlanThreads], s_drop[kPlanThreads];
     __shared__ int32_t s_len[kPlanThreads], s_owned[kPlanThreads], s_need[kPlanThreads];
-    __shared__ int64_t s_warp[3][32];
+    __shared__ int64_t s_wtok[32];
+    __shared__ int32_t s_wgrow[32], s_wdrop[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
-    const int64_t first = (int64_t)rank * kPlanThreads + tid, step = (int64_t)ranks * kPlanThreads;
+    const int32_t first = (int32_t)rank * kPlanThreads + tid, step = (int32_t)ranks * kPlanThreads;
     pdl_launch_dependents();
     pdl_wait();
     const int64_t head = p.state_in[0], tail = p.state_in[1];
-    const int64_t avail = tail > head ? tail - head : 0;
-    const int64_t cap = (int64_t)p.max_blocks * p.page_size;
-    int64_t tok0 = 0, grow0 = 0, drop0 = 0;  // totals of the chunks before
+    const int32_t avail = clamp_i32(tail - head, 0, p.ring_size);
+    const int32_t head_at = ring_base(head, p.ring_size, p.ring_inv), tail_at = ring_base(tail, p.ring_size, p.ring_inv);
+    const int32_t cap = p.max_blocks * p.page_size;
+    int64_t tok0 = 0;
+    int32_t grow0 = 0, drop0 = 0;  // totals of the chunks before
     uint32_t flags = 0;
     for (int base = 0; base < p.requests; base += kPlanThreads) {
         const int n = min(kPlanThreads, p.requests - base);
         int32_t len = 0, add = 0, owned = 0, need = 0;
         if (tid < n) {
             const int32_t l = p.lens[base + tid], a = p.new_lens[base + tid], o = p.owned_in[base + tid];
-            len = clamp_i32(l, 0, cap);
-            add = clamp_i32(a, 0, cap - len);
-            owned = clamp_i32(o, 0, p.max_blocks);
-            if (len != l || add != (a < 0 ? 0 : a) || owned != o) flags |= kStatusKvSizes;
+            len = min(max(l, 0), cap);
+            add = min(max(a, 0), cap - len);
+            owned = min(max(o, 0), p.max_blocks);
+            if (len != l || add != max(a, 0) || owned != o) flags |= kStatusKvSizes;
             need = (int32_t)(((int64_t)len + add + p.page_size - 1) / p.page_size);
         }
-        const int64_t grow = need > owned ? need - owned : 0;
-        const int64_t drop = p.trim && owned > need ? owned - need : 0;
-        int64_t a = add, b = grow, c = drop;  // inclusive sums
+        const int32_t grow = max(need - owned, 0), drop = p.trim ? max(owned - need, 0) : 0;
+        int64_t a = add;  // inclusive sums
+        int32_t b = grow, c = drop;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t x = __shfl_up_sync(~0u, a, d), y = __shfl_up_sync(~0u, b, d), z = __shfl_up_sync(~0u, c, d);
+            const int64_t x = __shfl_up_sync(~0u, a, d);
+            const int32_t y = __shfl_up_sync(~0u, b, d), z = __shfl_up_sync(~0u, c, d);
             if (lane >= d) a += x, b += y, c += z;
         }
-        if (lane == 31) s_warp[0][warp] = a, s_warp[1][warp] = b, s_warp[2][warp] = c;
+        if (lane == 31) s_wtok[warp] = a, s_wgrow[warp] = b, s_wdrop[warp] = c;
         __syncthreads();
-        if (warp < 3) {
-            int64_t v = s_warp[warp][lane];
+        if (warp == 0) {
+            int64_t x = s_wtok[lane];
+            int32_t y = s_wgrow[lane], z = s_wdrop[lane];
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int64_t x = __shfl_up_sync(~0u, v, d);
-                if (lane >= d) v += x;
+                const int64_t u = __shfl_up_sync(~0u, x, d);
+                const int32_t v = __shfl_up_sync(~0u, y, d), w = __shfl_up_sync(~0u, z, d);
+                if (lane >= d) x += u, y += v, z += w;
             }
-            s_warp[warp][lane] = v;
+            s_wtok[lane] = x, s_wgrow[lane] = y, s_wdrop[lane] = z;
         }
         __syncthreads();
-        if (warp > 0) a += s_warp[0][warp - 1], b += s_warp[1][warp - 1], c += s_warp[2][warp - 1];
-        const int64_t tok_n = s_warp[0][31], grow_n = s_warp[1][31], drop_n = s_warp[2][31];
-        s_tok[tid] = tok0 + a - add;
+        if (warp > 0) a += s_wtok[warp - 1], b += s_wgrow[warp - 1], c += s_wdrop[warp - 1];
+        const int64_t tok_n = s_wtok[31];
+        const int32_t grow_n = s_wgrow[31], drop_n = s_wdrop[31];
+        s_tok[tid] = (int32_t)min(tok0 + a - add, (int64_t)0x7FFFFFFF);
         s_grow[tid] = grow0 + b - grow;
         s_drop[tid] = drop0 + c - drop;
         s_len[tid] = len;
         s_owned[tid] = owned;
         s_need[tid] = need;
-        const int64_t left = avail - s_grow[tid];
-        const int32_t given = (int32_t)(grow < left ? grow : left > 0 ? left : 0);
+        const int32_t given = min(grow, max(avail - (grow0 + b - grow), 0));
         if (given < grow) flags |= kStatusKvPages;
         // every CTA has read its inputs of this chunk before any output of it
         // is written (owned_out may be owned_in)
         if (ranks > 1) cluster_sync();
         else __syncthreads();
         if (rank == 0 && tid < n) {
-            p.owned_out[base + tid] = owned + given - (int32_t)drop;
+            p.owned_out[base + tid] = owned + given - drop;
             if (base + tid == 0) p.cu_new[0] = 0;
-            p.cu_new[base + tid + 1] = clamp_i32(s_tok[tid] + add, 0, 0x7FFFFFFF);
+            p.cu_new[base + tid + 1] = (int32_t)min(tok0 + a, (int64_t)0x7FFFFFFF);
         }
         // tokens
-        const int64_t tok_end = min(tok0 + tok_n, (int64_t)p.tokens);
+        const int32_t tok_end = (int32_t)min(tok0 + tok_n, (int64_t)p.tokens);
         for (int64_t t = tok0 + first; t < tok_end; t += step) {
-            const int r = find_start(s_tok, n, t);
-            const int32_t pos = s_len[r] + (int32_t)(t - s_tok[r]);
-            const int32_t j = pos / p.page_size;
+            const int r = find_start(s_tok, n, (int32_t)t);
+            const int32_t pos = s_len[r] + (int32_t)t - s_tok[r], j = pos / p.page_size;
             int32_t page = -1;
             if (j < s_owned[r]) {
                 page = p.tables[(int64_t)(base + r) * p.table_stride + j];
             } else {
-                const int64_t at = s_grow[r] + j - s_owned[r];
-                if (at < avail) page = p.ring[(uint64_t)(head + at) % (uint32_t)p.ring_size];
+                const int32_t at = s_grow[r] + j - s_owned[r];
+                if (at < avail) page = p.ring[ring_at(head_at, at, p.ring_size)];
             }
             p.positions[t] = pos;
             p.slots[t] = page < 0 ? -1 : (int64_t)page * p.page_size + (pos - j * p.page_size);
         }
         // pages taken (or missing) and pages given back
-        for (int64_t g = grow0 + first; g < grow0 + grow_n; g += step) {
+        for (int32_t i = first; i < grow_n; i += step) {
+            const int32_t g = grow0 + i;
             const int r = find_start(s_grow, n, g);
-            const int64_t j = s_owned[r] + (g - s_grow[r]);
+            const int32_t j = s_owned[r] + g - s_grow[r];
             p.tables[(int64_t)(base + r) * p.table_stride + j] =
-                g < avail ? p.ring[(uint64_t)(head + g) % (uint32_t)p.ring_size] : -1;
+                g < avail ? p.ring[ring_at(head_at, g, p.ring_size)] : -1;
         }
-        for (int64_t g = drop0 + first; g < drop0 + drop_n; g += step) {
+        for (int32_t i = first; i < drop_n; i += step) {
+            const int32_t g = drop0 + i;
             const int r = find_start(s_drop, n, g);
-            const int64_t j = s_need[r] + (g - s_drop[r]);
-            p.ring[(uint64_t)(tail + g) % (uint32_t)p.ring_size] = p.tables[(int64_t)(base + r) * p.table_stride + j];
+            const int32_t j = s_need[r] + g - s_drop[r];
+            p.ring[ring_at(tail_at, g, p.ring_size)] = p.tables[(int64_t)(base + r) * p.table_stride + j];
         }
         tok0 += tok_n;
         grow0 += grow_n;
@@ -159,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
     if (rank == 0 && tid == 0) {
         // (at least one request:) every CTA has passed a chunk's cluster barrier,
         // so it has read the state
-        p.state_out[0] = head + (grow0 < avail ? grow0 : avail);
+        p.state_out[0] = head + min(grow0, avail);
         p.state_out[1] = tail + drop0;
     }
     if (flags && rank == 0) atomicOr(p.status, flags);

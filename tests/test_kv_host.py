@@ -97,7 +97,8 @@ def test_store_refused(kw, status):
 @pytest.mark.parametrize("kw,status", [(dict(requests=0), INVALID), (dict(max_blocks=0), INVALID),
                                        (dict(ring_size=0), INVALID), (dict(tokens=-1), INVALID),
                                        (dict(page_size=20), SHAPE), (dict(page_size=0), SHAPE),
-                                       (dict(table_stride=7), SHAPE), (dict(lens=A + 2), ALIGN),
+                                       (dict(table_stride=7), SHAPE), (dict(requests=1 << 28), SHAPE),
+                                       (dict(lens=A + 2), ALIGN),
                                        (dict(slots=A + 4), ALIGN), (dict(ring_state_in=A + 4), ALIGN)] +
                          [(dict([(n, None)]), INVALID) for n in ("lens", "new_lens", "owned_in", "owned_out", "tables",
                                                                  "ring", "ring_state_in", "ring_state_out", "cu_new",
