@@ -63,11 +63,12 @@ struct AttendTcCfg {
     static constexpr int kOffPlaces = kOffInfo + 4 * kTcInfo + 32;
     static constexpr int kSmemBytes = kOffPlaces + 4 * (int)sizeof(TcPlace) + 1024;  // 1024: alignment
     static constexpr int kThreads = Q8 ? 384 : 224;
+    static constexpr int kRegs = !Q8 ? 0 : D == 256 ? 168 : 80;  // at launch, where warps exchange registers
     static constexpr int kTmemCols = D == 256 ? 512 : 256;
     static constexpr int kSCol = D == 256 ? 256 : 128;  // two S buffers of 64 columns; O from column 0
 };
 
-// Warp-collective 32-column TMEM load and store (lane i <-> TMEM lane base + i).
+// Warp-collective 32-column TMEM load (lane i <- TMEM lane base + i).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -79,17 +80,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
-        "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
-        "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
-
 // 4-D tiled copy global -> shared: column, token in page, head, page.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int32_t c0, int32_t c1, int32_t c2,
                                             int32_t c3, uint32_t bar) {
@@ -140,97 +130,147 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t use, uint64_t de
     return mbar_wait(bar, use & 1u, deadline);
 }
 
-// The softmax of one row's 64 scores, in two passes over TMEM (columns ts .. of the
-// thread's lane): the maximum, then the weights.  Reading them twice costs less
-// than the registers of all 64.  sc: the keys' 64 scales (with the softmax scale)
-// and the values' 64 (Q8).  EDGE: only the keys of `seen`.  EXACT (Q8): the largest
-// score; else the largest product before the scales, which with the tile's largest
-// scale bounds the scores and mostly shows that the running maximum can stay.
-template <bool Q8, bool EDGE, bool EXACT>
-__device__ __forceinline__ float tc_tile_max(uint32_t ts, const float *sc, uint64_t seen) {
-    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-    for (int h = 0; h < 64; h += 32) {
-        uint32_t x[32];
-        tmem_ld32(ts + h, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(x[k + e]);
-            if (Q8 && EXACT) {
-                const float4 s = *reinterpret_cast<const float4 *>(sc + h + k);
-                const f2 a = make_f2(y[0], y[1]) * make_f2(s.x, s.y), b = make_f2(y[2], y[3]) * make_f2(s.z, s.w);
-                y[0] = f2_lo(a), y[1] = f2_hi(a), y[2] = f2_lo(b), y[3] = f2_hi(b);
-            }
-            if (EDGE) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!((uint32_t)(seen >> h) & (1u << (k + e)))) y[e] = -INFINITY;
-            }
-            if (Q8 && !EXACT) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = fabsf(y[e]);
-            }
-            top[0] = fmaxf(fmaxf(top[0], y[0]), y[1]);
-            top[1] = fmaxf(fmaxf(top[1], y[2]), y[3]);
-        }
-    }
-    return fmaxf(top[0], top[1]);
+// 16 TMEM lanes (rows) at a time, spread as a product's accumulator is: lane 4 g + t
+// has rows g and g + 8, of every eight 32-bit columns 2 t and 2 t + 1 (of row g first).
+__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+                 "}, [%32];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+                   "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+                   "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+                   "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+                 "}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+                   "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16x32(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {"
+                 "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+                 "};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+// The same rows, of every four columns t (of row g first): pairs of BF16 columns.
+__device__ __forceinline__ void tmem_st16x32p(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {"
+                 "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+                 "};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
 }
 
-// Weights 2^(score - m) as BF16 over the scores (columns ts .. ts + 31); returns
-// their sum.
-template <bool Q8, bool EDGE>
-__device__ __forceinline__ float tc_tile_weights(uint32_t ts, const float *sc, float scale, float m, uint64_t seen) {
-    const f2 minus = make_f2(-m, -m), scale2 = make_f2(scale, scale);
-    f2 l0 = make_f2(0.0f, 0.0f), l1 = l0;
-#pragma unroll 1
-    for (int h = 0; h < 64; h += 32) {
-        uint32_t x[32], pk[16];
-        tmem_ld32(ts + h, x);
-        tmem_wait_ld();
+// The softmax of 16 rows' 64 scores x, which become BF16 weights at ts, over them.
+// A thread has 16 keys of two rows (see tmem_ld16x64), so it needs the scales of 16
+// keys and not of 64: with a row per thread their broadcast reads from shared memory
+// alone took a fifth of its bandwidth.  sc (Q8): the tile's 64 key scales with the
+// softmax scale in them, its 64 value scales and the largest key scale, from the
+// thread's first key on; scale: the softmax scale, not negative (BF16).  m, l: the rows' running maximum (the
+// same in the four threads of a row) and the thread's share of their sum.  EDGE: only
+// the keys of `seen`, shifted so that bit 8 j + e is the thread's key 2 j + e.
+// rescale(a0, a1) multiplies the rows' output so far.
+template <bool Q8, bool EDGE, class Rescale>
+__device__ __forceinline__ void tc_softmax(uint32_t ts, const uint32_t (&x)[32], const float *sc, float scale,
+                                           float (&m)[2], float (&l)[2], uint64_t seen0, uint64_t seen1,
+                                           Rescale rescale) {
+    const auto pair = [&](int j, int row) {
+        return make_f2(__uint_as_float(x[4 * j + 2 * row]), __uint_as_float(x[4 * j + 2 * row + 1]));
+    };
+    const auto scale_of = [&](int j) {  // of the thread's keys 2 j and 2 j + 1, the softmax scale in it
+        if (!Q8) return make_f2(scale, scale);
+        const float2 s = *reinterpret_cast<const float2 *>(sc + 8 * j);
+        return make_f2(s.x, s.y);
+    };
+    const auto sees = [&](int j, int row, int e) { return (((row ? seen1 : seen0) >> (8 * j + e)) & 1ull) != 0; };
+    float top[2] = {-INFINITY, -INFINITY};
+    bool exact = EDGE || !Q8;
+    if (!exact) {
+        // the largest product times the tile's largest scale bounds the scores and
+        // mostly shows that the running maximum can stay
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            f2 y0 = make_f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-            f2 y1 = make_f2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
-            if (Q8) {
-                const float4 s = *reinterpret_cast<const float4 *>(sc + h + k);
-                y0 = fma2(y0, make_f2(s.x, s.y), minus);
-                y1 = fma2(y1, make_f2(s.z, s.w), minus);
-            } else {
-                y0 = fma2(y0, scale2, minus);
-                y1 = fma2(y1, scale2, minus);
-            }
-            float e[4] = {ex2(f2_lo(y0)), ex2(f2_hi(y0)), ex2(f2_lo(y1)), ex2(f2_hi(y1))};
-            if (EDGE) {
+        for (int j = 0; j < 8; ++j) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (!((uint32_t)(seen >> h) & (1u << (k + i)))) e[i] = 0.0f;
-            }
-            f2 e0 = make_f2(e[0], e[1]), e1 = make_f2(e[2], e[3]);
-            l0 = l0 + e0;
-            l1 = l1 + e1;
-            if (Q8) {
-                float4 s = *reinterpret_cast<const float4 *>(sc + 64 + h + k);
-                if (EDGE) {  // an unseen key's scale may be anything
-                    const uint32_t b = (uint32_t)(seen >> h) >> k;
-                    s.x = b & 1u ? s.x : 0.0f, s.y = b & 2u ? s.y : 0.0f;
-                    s.z = b & 4u ? s.z : 0.0f, s.w = b & 8u ? s.w : 0.0f;
-                }
-                e0 = e0 * make_f2(s.x, s.y);
-                e1 = e1 * make_f2(s.z, s.w);
-            }
-            pk[k / 2] = pack_bf16(f2_lo(e0), f2_hi(e0));
-            pk[k / 2 + 1] = pack_bf16(f2_lo(e1), f2_hi(e1));
+            for (int r = 0; r < 2; ++r)
+                top[r] = fmaxf(fmaxf(top[r], fabsf(__uint_as_float(x[4 * j + 2 * r]))),
+                               fabsf(__uint_as_float(x[4 * j + 2 * r + 1])));
         }
-        // over scores that both passes have read
-        tmem_st16(ts + h / 2, pk);
+        // (not <=, so that a NaN scale takes the exact way too)
+        const float largest = sc[128 - 2 * (int)(threadIdx.x & 3)];
+        exact = __any_sync(~0u, !(top[0] * largest <= m[0] + kAttendLazy) || !(top[1] * largest <= m[1] + kAttendLazy));
     }
-    tmem_wait_st();
-    l0 = l0 + l1;
-    return f2_lo(l0) + f2_hi(l0);
+    if (exact) {
+        top[0] = top[1] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const f2 ks = scale_of(j);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const f2 y = Q8 ? pair(j, r) * ks : pair(j, r);
+                const float y0 = !EDGE || sees(j, r, 0) ? f2_lo(y) : -INFINITY;
+                const float y1 = !EDGE || sees(j, r, 1) ? f2_hi(y) : -INFINITY;
+                top[r] = fmaxf(fmaxf(top[r], y0), y1);
+            }
+        }
+        if (!Q8) top[0] *= scale, top[1] *= scale;
+        if (__any_sync(~0u, top[0] > m[0] + kAttendLazy || top[1] > m[1] + kAttendLazy)) {
+            float al[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float v = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+                v = fmaxf(fmaxf(v, __shfl_xor_sync(~0u, v, 2)), m[r]);
+                al[r] = v == -INFINITY ? 1.0f : ex2(m[r] - v);
+                m[r] = v;
+                l[r] *= al[r];
+            }
+            rescale(al[0], al[1]);
+        }
+    }
+    uint32_t pk[16];
+    f2 minus[2], sum[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const float m0 = m[r] == -INFINITY ? 0.0f : -m[r];
+        minus[r] = make_f2(m0, m0);
+        sum[r] = make_f2(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const f2 ks = scale_of(j);
+        float2 vs = make_float2(1.0f, 1.0f);
+        if (Q8) vs = *reinterpret_cast<const float2 *>(sc + 64 + 8 * j);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const f2 y = fma2(pair(j, r), ks, minus[r]);
+            float a = ex2(f2_lo(y)), b = ex2(f2_hi(y));
+            if (EDGE) {
+                if (!sees(j, r, 0)) a = 0.0f;
+                if (!sees(j, r, 1)) b = 0.0f;
+            }
+            f2 e = make_f2(a, b);
+            sum[r] = sum[r] + e;
+            if (Q8) {
+                e = e * make_f2(vs.x, vs.y);
+                if (EDGE)  // an unseen key's scale may be anything
+                    e = make_f2(sees(j, r, 0) ? f2_lo(e) : 0.0f, sees(j, r, 1) ? f2_hi(e) : 0.0f);
+            }
+            pk[2 * j + r] = pack_bf16(f2_lo(e), f2_hi(e));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) l[r] += f2_lo(sum[r]) + f2_hi(sum[r]);
+    tmem_st16x32p(ts, pk);
 }
 
 // Fills a ring with the keys or the values of the CTA's tiles, one tile per step().
@@ -373,12 +413,16 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
     bool ok = true;
 
     if (warp < 4) {
+        // 128 threads x 128 + 256 x 56 = 384 x 80 registers (232, 136, 168 for D = 256):
+        // what one side takes on the other gives up
         if (Q8 && D < 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        if (Q8 && D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // ------------------------------------------------------------ softmax and output, one row per thread
         const int lr = threadIdx.x;  // 0..127, TMEM lane
         const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
-        // a negative softmax scale is put into Q, so that the largest score is the
-        // largest product
+        const int g8 = lane >> 2, t4 = lane & 3;
+        // of a BF16 cache the softmax scale's sign is in Q, so that the largest product
+        // is the largest score
         const float scale = fabsf(p.scale_log2);
         uint32_t it = 0;
         TcPlace &place = reinterpret_cast<TcPlace *>(smem + C::kOffPlaces)[warp];
@@ -422,15 +466,13 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
         };
         load_q(place.r, place.c);
         while (true) {
-            int32_t nrows, i, kb, tiles, keys, past, lim, low;
-            KvRowView view;
+            int32_t nrows, i, row0, kb, tiles, keys, past, lim, low;
             {
                 const KvRequest &r = place.r;
                 const KvPiece &c = place.c;
                 nrows = (int32_t)min((int64_t)kTcRows, (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows);
-                i = min(c.rb * kTcRows + lr, c.rb * kTcRows + nrows - 1) / p.group;
-                view.index = kv_index(r, i);
-                view.tree = p.tree ? p.tree[r.q0 + i] : 0u;
+                row0 = c.rb * kTcRows;
+                i = min(row0 + lr, row0 + nrows - 1) / p.group;  // new token of TMEM lane lr's row
                 kb = (r.tile0 + c.ja) * kAttendTile;
                 tiles = c.jb - c.ja;
                 keys = r.kv;
@@ -439,8 +481,19 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                 lim = min(r.kv, p.tree ? r.past : r.past + 1);
                 low = p.window > 0 ? (int32_t)max((int64_t)r.past + r.qlen - p.window, (int64_t)0) : 0;
             }
+            // the keys of the tile at kb that row `row` of the block sees
+            const auto seen_by = [&](int row, uint32_t here) -> uint64_t {
+                const int32_t tok = min(row0 + row, row0 + nrows - 1) / p.group;
+                KvRowView v;
+                v.index = kv_index(place.r, tok);
+                v.tree = p.tree ? p.tree[place.r.q0 + tok] : 0u;
+                return kv_seen64(p, keys, past, v, kb, here) >> (2 * t4);
+            };
             const bool busy = 32 * warp < nrows;  // a warp without rows only keeps step
-            float m = -INFINITY, l = 0.0f;
+            // rows g, g + 8 | g + 16, g + 24 of the warp's 32, as tc_softmax has them
+            float mr[2][2], sr[2][2];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) mr[h / 2][h % 2] = -INFINITY, sr[h / 2][h % 2] = 0.0f;
             for (int j = 0; j < tiles; ++j, ++it, kb += kAttendTile) {
                 // after a timeout the walk goes on without waiting, so that every
                 // barrier below is reached
@@ -452,43 +505,50 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                 const bool edge = here != 15u || kb > lim - kAttendTile || kb < low;
                 const uint32_t ts = tl + C::kSCol + 64 * (it & 1);
                 if (busy) {
-                    const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes);
-                    const uint64_t seen = edge ? kv_seen64(p, keys, past, view, kb, here) : ~0ull;
-                    float top;
-                    if (Q8) {
-                        top = edge ? INFINITY : tc_tile_max<Q8, false, false>(ts, sc, seen) * sc[128];
-                        // (not <=, so that a NaN scale takes this way too)
-                        if (__any_sync(~0u, !(top <= m + kAttendLazy)))
-                            top = edge ? tc_tile_max<Q8, true, true>(ts, sc, seen)
-                                       : tc_tile_max<Q8, false, true>(ts, sc, seen);
-                    } else {
-                        top = scale * (edge ? tc_tile_max<Q8, true, true>(ts, sc, seen)
-                                            : tc_tile_max<Q8, false, true>(ts, sc, seen));
-                    }
-                    if (__any_sync(~0u, top > m + kAttendLazy)) {
-                        const float mn = fmaxf(m, top);
-                        const float al = mn == -INFINITY ? 1.0f : ex2(m - mn);
-                        m = mn;
-                        l *= al;
-                        if (j > 0) {
+                    const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes) +
+                                      2 * t4;
+                    // the second 16 rows' scores are on their way while the first are
+                    // worked on, where there are registers for both
+                    constexpr bool kAhead = D == 256;
+                    uint32_t x[2][32];
+                    tmem_ld16x64(ts, x[0]);
+                    tmem_wait_ld();
+                    if (kAhead) tmem_ld16x64(ts + (16u << 16), x[1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (32 * warp + 16 * h >= nrows) break;  // the same for the warp
+                        if (h == 1) {
+                            if (!kAhead) tmem_ld16x64(ts + (16u << 16), x[1]);
+                            tmem_wait_ld();
+                        }
+                        const uint32_t to = tl + ((uint32_t)(16 * h) << 16);
+                        const auto rescale = [&](float a0, float a1) {
+                            if (j == 0) return;  // nothing there yet
                             if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
                             ok = __all_sync(~0u, ok);
                             tc_fence_after();
 #pragma unroll 1
                             for (int d0 = 0; d0 < D; d0 += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(tl + d0, o);
+                                uint32_t o[16];
+                                tmem_ld16x32(to + d0, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                                tmem_st32(tl + d0, o);
+                                for (int k = 0; k < 16; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * ((k & 2) ? a1 : a0));
+                                tmem_st16x32(to + d0, o);
                             }
                             tmem_wait_st();
+                        };
+                        const uint32_t tsh = ts + ((uint32_t)(16 * h) << 16);
+                        if (edge) {
+                            const int row = 32 * warp + 16 * h + g8;
+                            tc_softmax<Q8, true>(tsh, x[h], sc, scale, mr[h], sr[h], seen_by(row, here),
+                                                 seen_by(row + 8, here), rescale);
+                        } else {
+                            tc_softmax<Q8, false>(tsh, x[h], sc, scale, mr[h], sr[h], 0, 0, rescale);
                         }
                     }
-                    const float m0 = m == -INFINITY ? 0.0f : m;
-                    l += edge ? tc_tile_weights<Q8, true>(ts, sc, scale, m0, seen)
-                              : tc_tile_weights<Q8, false>(ts, sc, scale, m0, seen);
+                    tmem_wait_st();
                 }
                 if (!Q8 && edge) {
                     // values behind the request's last token or of missing slices
@@ -547,6 +607,18 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
             if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
             ok = __all_sync(~0u, ok);
             tc_fence_after();
+            // the rows' statistics: summed over a row's four threads, then to the lane
+            // that has the row in the output's layout (row 8 k + g from lane 4 g)
+            float m = 0.0f, l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float s = sr[k / 2][k % 2];
+                s += __shfl_xor_sync(~0u, s, 1);
+                s += __shfl_xor_sync(~0u, s, 2);
+                const float a = __shfl_sync(~0u, mr[k / 2][k % 2], (lane & 7) * 4);
+                const float b = __shfl_sync(~0u, s, (lane & 7) * 4);
+                if (lane >> 3 == k) m = a, l = b;
+            }
             const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
             bool bad = false;
             if (!Q8) {
@@ -574,6 +646,9 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                         // through the product already stays what it is)
                         for (int j = c1.ja; j < c1.jb; ++j) {
                             const int32_t kb = (r1.tile0 + j) * kAttendTile;
+                            KvRowView view;
+                            view.index = kv_index(r1, i);
+                            view.tree = p.tree ? p.tree[r1.q0 + i] : 0u;
                             uint64_t seen = kv_seen64(p, r1.kv, r1.past, view, kb, 15u);
                             for (; seen; seen &= seen - 1) {
                                 const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
@@ -624,6 +699,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
         if (!ok && lane == 0) atomicOr(p.status, 8u);
         } else {
         if (Q8 && D < 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (Q8 && D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
     if (warp == 4 || warp == 6) {
         // ------------------------------------------------------------ loaders
         TcLoader<D, Q8> load;

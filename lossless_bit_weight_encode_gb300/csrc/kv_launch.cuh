@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 #include <string>
 #include <utility>
@@ -121,10 +122,11 @@ template <int D>
 int attend_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvAttendParams *p,
                const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
 
-// Occupancy of one kernel on first use, then (with `p`) its launch.
-inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams, CUtensorMap, CUtensorMap), int rows_dim,
-                         int threads, int smem, std::mutex &mu, int *per_sm, int *resident, const dev::KvAttendParams *p,
-                         const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+// Occupancy of one kernel on first use (at most `most` CTAs per SM), then (with `p`)
+// its launch.  regs > 0: the registers per thread it has to have been compiled to.
+inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams, CUtensorMap, CUtensorMap), int most,
+                         int threads, int regs, int smem, std::mutex &mu, int *per_sm, int *resident,
+                         const dev::KvAttendParams *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     if (d.device < 0 || d.device >= kKvMaxDevices) {
         *err = "device ordinal out of range";
         return W12_ERR_CUDA;
@@ -139,7 +141,15 @@ inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams
             int occ = 0;
             const int rc = resident_ctas(k, threads, smem, d.device, err, &occ);
             if (rc != W12_OK) return rc;
-            const int most = kPartElems / rows_dim;
+            // a kernel whose warps exchange registers was made for so many of them; with
+            // fewer, who takes some on would wait for ever
+            cudaFuncAttributes fa;
+            e = cudaFuncGetAttributes(&fa, k);
+            if (e != cudaSuccess) return kv_cuda_fail(e, "cudaFuncGetAttributes", err);
+            if (regs > 0 && fa.numRegs != regs) {
+                *err = "w12_kv_attend was compiled to another register count than it is made for";
+                return W12_ERR_CUDA;
+            }
             per_sm[d.device] = occ < most ? occ : most;
         }
         *resident = per_sm[d.device] * d.sm_count;
@@ -157,8 +167,8 @@ int attend_variant(const DeviceView &d, int *resident, const dev::KvAttendParams
     using C = dev::AttendCfg<D, Q8, WK, WR, NT>;
     static std::mutex mu;
     static int per_sm[kKvMaxDevices] = {};
-    return attend_kernel(d, &dev::w12_kv_attend_kernel<D, Q8, WK, WR, NT>, C::kRows * D, dev::kAttendThreads,
-                         C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
+    return attend_kernel(d, &dev::w12_kv_attend_kernel<D, Q8, WK, WR, NT>, kPartElems / (C::kRows * D),
+                         dev::kAttendThreads, 0, C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
 template <int D, bool Q8>
@@ -167,7 +177,8 @@ int attend_tc_variant(const DeviceView &d, int *resident, const dev::KvAttendPar
     using C = dev::AttendTcCfg<D, Q8>;
     static std::mutex mu;
     static int per_sm[kKvMaxDevices] = {};
-    return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8>, dev::kTcRows * D, C::kThreads, C::kSmemBytes, mu,
+    return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8>,
+                         std::min(kPartElems / (dev::kTcRows * D), 512 / C::kTmemCols), C::kThreads, C::kRegs, C::kSmemBytes, mu,
                          per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
