@@ -171,12 +171,6 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttendParams &p, int b) 
     return r;
 }
 
-__device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-    return v;
-}
-
 // A CTA's range of units and its place in it; every warp keeps its own copy.
 struct KvWalk {
     int64_t total, u, end;  // all units, the next one, the range's end
@@ -184,36 +178,53 @@ struct KvWalk {
     int32_t b, ctas;
 };
 
+// Units of all requests, and of those before each lane's: a lane sums a block of
+// consecutive requests (their loads overlap), one warp scan joins the blocks.
+struct KvSums {
+    int64_t total, before;  // all units; those before the lane's block
+    int32_t per;            // requests of a block
+};
+
+template <int ROWS, int TILE>
+__device__ __forceinline__ KvSums kv_sum_units(const KvAttendParams &p) {
+    const int lane = threadIdx.x & 31;
+    KvSums s;
+    s.per = (p.requests + 31) / 32;
+    int64_t sum = 0;
+#pragma unroll 4
+    for (int i = 0; i < s.per; ++i) {
+        const int b = lane * s.per + i;
+        if (b < p.requests) sum += kv_request<ROWS, TILE>(p, b).units;
+    }
+    int64_t inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, inc, d);
+        if (lane >= d) inc += x;
+    }
+    s.total = __shfl_sync(~0u, inc, 31);
+    s.before = inc - sum;
+    return s;
+}
+
 template <int ROWS, int TILE>
 __device__ __forceinline__ bool kv_walk_init(const KvAttendParams &p, KvWalk &w, KvRequest &r) {
-    const int lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    for (int b = lane; b < p.requests; b += 32) sum += kv_request<ROWS, TILE>(p, b).units;
-    w.total = warp_sum_i64(sum);
+    const KvSums s = kv_sum_units<ROWS, TILE>(p);
+    w.total = s.total;
     w.ctas = (int32_t)min((int64_t)gridDim.x, w.total);
     if ((int)blockIdx.x >= w.ctas) return false;
     w.u = w.total * blockIdx.x / w.ctas;
     w.end = w.total * (blockIdx.x + 1) / w.ctas;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < p.requests; b0 += 32) {
-        const int64_t own = b0 + lane < p.requests ? kv_request<ROWS, TILE>(p, b0 + lane).units : 0;
-        int64_t inc = own;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t x = __shfl_up_sync(~0u, inc, d);
-            if (lane >= d) inc += x;
-        }
-        const uint32_t hit = __ballot_sync(~0u, before + inc > w.u);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            w.b = b0 + src;
-            w.start = __shfl_sync(~0u, before + inc - own, src);
-            r = kv_request<ROWS, TILE>(p, w.b);
-            return true;
-        }
-        before += __shfl_sync(~0u, inc, 31);
+    // the last block that starts at or before u, then the request in it
+    const int src = 31 - __clz(__ballot_sync(~0u, s.before <= w.u));
+    w.start = __shfl_sync(~0u, s.before, src);
+    w.b = src * s.per;
+    r = kv_request<ROWS, TILE>(p, w.b);
+    while (w.u >= w.start + r.units) {
+        w.start += r.units;
+        r = kv_request<ROWS, TILE>(p, ++w.b);
     }
-    return false;  // not reached: u < total
+    return true;
 }
 
 // The piece at w.u: its (key head, row block) and its tiles [ja, jb).
@@ -901,31 +912,29 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
     const int32_t tok = (int32_t)(out_row / heads), h = (int32_t)(out_row - (int64_t)tok * heads);
     // Lengths and offsets come from before the attention kernel, which lets this one
     // start only when it has itself seen all that is before it.
-    // The token's request, its first unit and all units:
-    int64_t total = 0, start = -1;
+    const KvSums sums = kv_sum_units<ROWS, TILE>(p);
+    const int64_t total = sums.total;
+    // the token's request: the block that has it, then the request in it
+    int64_t start = -1;
     KvRequest r;
-    r.q0 = r.qlen = 0;
     int32_t b = 0;
-    for (int b0 = 0; b0 < p.requests; b0 += 32) {
-        KvRequest x;
-        x.units = 0, x.q0 = x.qlen = 0;
-        if (b0 + lane < p.requests) x = kv_request<ROWS, TILE>(p, b0 + lane);
-        int64_t inc = x.units;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(~0u, inc, d);
-            if (lane >= d) inc += y;
-        }
-        const uint32_t hit = __ballot_sync(~0u, tok >= x.q0 && tok < x.q0 + x.qlen);
-        if (hit && start < 0) {
+    {
+        const int first = lane * sums.per, end = min(first + sums.per, p.requests);
+        const bool mine = first < p.requests && tok >= min(max(p.cu_new[first], 0), p.tokens) &&
+                          tok < min(max(p.cu_new[end], 0), p.tokens);
+        const uint32_t hit = __ballot_sync(~0u, mine);
+        if (hit) {
             const int src = __ffs(hit) - 1;
-            b = b0 + src;
-            start = total + __shfl_sync(~0u, inc - x.units, src);
-            r.q0 = __shfl_sync(~0u, x.q0, src);
-            r.ntiles = __shfl_sync(~0u, x.ntiles, src);
-            r.rblocks = __shfl_sync(~0u, x.rblocks, src);
+            int64_t at = __shfl_sync(~0u, sums.before, src);
+            for (b = src * sums.per; b < min((src + 1) * sums.per, p.requests); ++b) {
+                r = kv_request<ROWS, TILE>(p, b);
+                if (tok >= r.q0 && tok < r.q0 + r.qlen) {
+                    start = at;
+                    break;
+                }
+                at += r.units;
+            }
         }
-        total += __shfl_sync(~0u, inc, 31);
     }
     KvParts q;
     q.n = 0;
