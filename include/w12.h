@@ -481,7 +481,7 @@ int w12_kv_read(const w12_kv_cache *cache, const int64_t *slots, int32_t tokens,
  * softmax statistics and sums; the softmax weights are rounded to BF16 for the
  * tensor cores.  Results are reproducible run to run for the same lengths.
  * q, out: BF16, token t at t * stride, stride a multiple of 8, 16-byte aligned.
- * heads: a multiple of kv_heads.  max_new: the most new tokens a request has,
+ * heads: a multiple of kv_heads; heads * tokens below 2^31.  max_new: the most new tokens a request has,
  * as far as the caller knows; it picks the row tile and any value is correct.
  * workspace: at least w12_kv_attend_workspace_size bytes, 256-byte aligned,
  * ZERO-FILLED BEFORE ITS FIRST USE; every successful call leaves its counters

@@ -560,8 +560,9 @@ int check_kv_attend(const w12_kv_cache *c, const w12_kv_attend_args *a, std::str
         err = "requests, tokens and max_blocks must be at least 1, window and max_new at least 0";
         return W12_ERR_INVALID_ARG;
     }
-    if (a->heads < 1 || a->heads % c->kv_heads != 0 || a->heads > 65536) {
-        err = "heads must be a multiple of kv_heads, at most 65536";
+    if (a->heads < 1 || a->heads % c->kv_heads != 0 || a->heads > 65536 ||
+        (int64_t)a->heads * a->tokens >= (int64_t(1) << 31)) {
+        err = "heads must be a multiple of kv_heads, at most 65536, and heads * tokens below 2^31";
         return W12_ERR_SHAPE;
     }
     if ((int64_t)a->max_blocks * c->page_size >= (int64_t(1) << 31) || a->table_stride < a->max_blocks) {

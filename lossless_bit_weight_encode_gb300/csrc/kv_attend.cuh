@@ -165,7 +165,7 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttendParams &p, int b) 
     // first key that any of the request's new tokens sees
     r.first = p.window > 0 ? (int32_t)max((int64_t)r.past + 1 - p.window, (int64_t)0) : 0;
     r.tile0 = min(r.first, r.kv) / TILE;
-    r.ntiles = max((r.kv + TILE - 1) / TILE - r.tile0, 1);
+    r.ntiles = r.kv > 0 ? max((r.kv - 1) / TILE + 1 - r.tile0, 1) : 1;
     r.rblocks = (int32_t)(((int64_t)r.qlen * p.group + ROWS - 1) / ROWS);
     r.units = (int64_t)p.kv_heads * r.rblocks * r.ntiles;
     return r;
@@ -225,6 +225,11 @@ __device__ __forceinline__ bool kv_walk_init(const KvAttendParams &p, KvWalk &w,
         r = kv_request<ROWS, TILE>(p, ++w.b);
     }
     return true;
+}
+
+// Table entries that the request's keys take.
+__device__ __forceinline__ int32_t kv_entries(const KvAttendParams &p, const KvRequest &r) {
+    return r.kv > 0 ? (r.kv - 1) / p.page_size + 1 : 0;
 }
 
 // The piece at w.u: its (key head, row block) and its tiles [ja, jb).
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
             const KvPiece c = kv_piece(w, r);
             KvPageWindow pages;
             pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * TILE / p.page_size,
-                        (r.kv + p.page_size - 1) / p.page_size);
+                        kv_entries(p, r));
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
                 const uint32_t stage = it % C::kStages, round = it / C::kStages;
                 // lane s deals with slice s

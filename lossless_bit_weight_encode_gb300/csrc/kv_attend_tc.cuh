@@ -297,7 +297,7 @@ struct TcLoader {
         c = kv_piece(w, r);
         j = c.ja;
         pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * kAttendTile / p.page_size,
-                    (r.kv + p.page_size - 1) / p.page_size);
+                    kv_entries(p, r));
     }
     __device__ __forceinline__ void start(const KvAttendParams &p, const KvWalk &walk, const KvRequest &req) {
         w = walk;

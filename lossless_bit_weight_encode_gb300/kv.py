@@ -23,6 +23,14 @@ _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float3
 _workspaces = {}  # (device, stream handle) -> zeroed workspace of the attend calls on that stream
 
 
+
+
+def clear_workspaces():
+    """Drop the attend calls' workspaces (after a TIMEOUT, which can leave their
+    counters set; the next call makes a zeroed one)."""
+    _workspaces.clear()
+
+
 _current_device = torch._C._cuda_getDevice
 # handle of a device's current stream, without the stream object around it
 _current_stream = torch._C._cuda_getCurrentRawStream
@@ -262,9 +270,10 @@ class KVCache:
             op, os_, no, _ = _rows(out, dim, "out", index, heads)
             if nq != tokens or no != tokens:
                 raise ValueError("q, out and k must have as many tokens")
-        w12.w12_kv_store(self._c, w12.w12_kv_store_args(qp, kp, vp, op, qs, ks, vs, os_, wq, wk, rp, pp,
-                                                        slots.data_ptr(), rows, tokens, heads, rot,
-                                                        1 if interleaved else 0, eps), st)
+        if tokens:
+            w12.w12_kv_store(self._c, w12.w12_kv_store_args(qp, kp, vp, op, qs, ks, vs, os_, wq, wk, rp, pp,
+                                                            slots.data_ptr(), rows, tokens, heads, rot,
+                                                            1 if interleaved else 0, eps), st)
         return None if q is None else out if out.dim() == 3 else out.view(tokens, heads, dim)
 
     def _weight(self, w, name):

@@ -273,6 +273,20 @@ def test_store_in_place_and_without_q():
     status()
 
 
+def test_nothing_to_do():
+    cache = make_cache(1, 2, 16, 64, False)
+    none = torch.empty(0, 128, device="cuda", dtype=torch.bfloat16)
+    step = KVStep(positions=dev([], torch.int32), slots=dev([], torch.int64))
+    assert cache.store(none, none, none, step).shape == (0, 2, 64)
+    a, b = cache.read(step.slots)
+    assert a.shape == (0, 2, 64) and b.shape == (0, 2, 64)
+    pages = KVPages.create(4, 16, requests=2, max_blocks=2)
+    empty = pages.step(0)
+    pages.plan(dev([0, 0], torch.int32), dev([0, 0], torch.int32), empty)
+    assert empty.cu_new.tolist() == [0, 0, 0]
+    status()
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_store_zero_rows_and_values_that_are_not_finite(q8):
     cache = make_cache(1, 3, 16, 64, q8)
@@ -566,6 +580,26 @@ def test_attend_many_requests(most, heads, kv_heads, q8):
     cache, tables, cu, q, step = attend_case(lens, new, heads, kv_heads, 64, 16, q8, seed=6)
     out, lse = run_attend(cache, q, step)
     check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, None, 0, 0.125, heads // kv_heads))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_attend_random_shapes(seed):
+    rng = random.Random(seed)
+    dim, kv_heads, group = rng.choice([64, 128, 256]), rng.choice([1, 2, 3]), rng.choice([1, 2, 5, 6, 16, 33])
+    n, page, q8 = rng.randint(1, 40), rng.choice([16, 32, 48, 80, 128]), rng.random() < 0.5
+    most = rng.choice([1, 1, 2, 3, 7, 20])
+    lens = [rng.choice([0, rng.randint(0, 40), rng.randint(0, 700), rng.randint(60, 70)]) for _ in range(n)]
+    new = [rng.choice([most, most, rng.randint(0, most)]) for _ in range(n)]
+    if not sum(new):
+        new[0] = 1
+    window = rng.choice([0, 0, rng.randint(1, 200)])
+    cache, tables, cu, q, step = attend_case(lens, new, kv_heads * group, kv_heads, dim, page, q8, seed)
+    tree = None
+    if most > 1 and rng.random() < 0.5:
+        tree = np.array([rng.getrandbits(32) for _ in range(cu[-1])], np.uint32).view(np.int32)
+        step.tree = torch.from_numpy(tree).cuda()
+    out, lse = run_attend(cache, q, step, window=window)
+    check_attend(out, lse, attend_ref(q, cache, tables, lens, cu, tree, window, dim ** -0.5, group))
 
 
 def test_attend_offsets_past_32_bits():

@@ -68,6 +68,7 @@ def test_cache_refused(kw, status):
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(tables=None), INVALID), (dict(lens=None), INVALID),
     (dict(cu_new=None), INVALID), (dict(requests=0), INVALID), (dict(tokens=0), INVALID), (dict(max_blocks=0), INVALID),
     (dict(window=-1), INVALID), (dict(max_new=-1), INVALID), (dict(heads=3), SHAPE), (dict(heads=0), SHAPE),
+    (dict(heads=1 << 16, tokens=1 << 15, q_stride=1 << 22, out_stride=1 << 22), SHAPE),
     (dict(max_blocks=1 << 27, table_stride=1 << 27), SHAPE), (dict(table_stride=7), SHAPE), (dict(q_stride=248), SHAPE),
     (dict(out_stride=128), SHAPE), (dict(q_stride=260), ALIGN), (dict(q=A + 8), ALIGN), (dict(out=A + 2), ALIGN),
     (dict(lse=A + 2), ALIGN), (dict(tree=A + 1), ALIGN), (dict(tables=A + 2), ALIGN)])
