@@ -49,7 +49,7 @@ cudaError_t store_dim(const DeviceView &d, bool q8, bool inter, dim3 grid, const
 template <int D>
 cudaError_t read_dim(const DeviceView &d, bool q8, int grid, const dev::KvReadParams &p, void *st) {
     const auto kernel = q8 ? &dev::w12_kv_read_kernel<D, true> : &dev::w12_kv_read_kernel<D, false>;
-    return kv_launch(d, kernel, dim3((unsigned)grid), dev::kStoreThreads, 0, 1, st, p);
+    return kv_launch(d, kernel, dim3((unsigned)grid), dev::kReadThreads, 0, 1, st, p);
 }
 
 int attend_call(const DeviceView &d, const w12_kv_cache &c, int rows, int *resident, const dev::KvAttendParams *p,
@@ -209,7 +209,7 @@ int kv_store(const w12_kv_cache &c, const w12_kv_store_args &a, void *stream, st
     const int all = (a.heads + per - 1) / per + 2 * ((c.kv_heads + per - 1) / per);
     // few tokens: a warp per round; many: as few CTAs per token as fill the device
     const int want = (all + groups - 1) / groups;
-    const int64_t fill = (int64_t)d.sm_count * 8;
+    const int64_t fill = (int64_t)d.sm_count * 16;
     const int gx = (int)std::max<int64_t>(1, std::min<int64_t>(want, fill / a.tokens));
     const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>(a.tokens, 65535));
     const bool q8 = c.dtype == W12_KV_Q8, inter = a.interleaved != 0;
@@ -233,7 +233,7 @@ int kv_read(const w12_kv_cache &c, const int64_t *slots, int32_t tokens, uint16_
     p.v_out = v_out;
     p.tokens = tokens;
     p.status = d.status;
-    const int per = 256 / c.head_dim, rounds = (c.kv_heads + per - 1) / per, warps = dev::kStoreThreads / 32;
+    const int per = 256 / c.head_dim, rounds = (c.kv_heads + per - 1) / per, warps = dev::kReadThreads / 32;
     p.rounds_inv = ~uint64_t(0) / (uint64_t)rounds;
     const int64_t items = (int64_t)tokens * rounds;
     const int grid = (int)std::min<int64_t>((items + warps - 1) / warps, (int64_t)d.sm_count * 32);

@@ -16,7 +16,7 @@
 namespace w12 {
 namespace dev {
 
-constexpr int kStoreThreads = 128;
+constexpr int kStoreThreads = 64, kReadThreads = 128;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -127,7 +127,7 @@ __device__ __forceinline__ void norm_rotate(f2 (&x)[4], bool norm, const uint4 &
 // the large calls is HBM and, close behind it, the instructions per element:
 // hence the packed arithmetic and the warp-uniform kinds.
 template <int D, bool Q8, bool INTERLEAVED>
-__global__ void __launch_bounds__(kStoreThreads, 8) w12_kv_store_kernel(KvStoreParams p) {
+__global__ void __launch_bounds__(kStoreThreads, 16) w12_kv_store_kernel(KvStoreParams p) {
     constexpr int LANES = D / 8, HEADS = 32 / LANES, WARPS = kStoreThreads / 32, U = 4;
     const int lane = threadIdx.x & 31, sub = lane % LANES, mine = lane / LANES;
     const int hk = p.c.kv_heads;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kStoreThreads, 8) w12_kv_store_kernel(KvStoreP
                 const int h = (j < nq ? j : j < nq + nk ? j - nq : j - nq - nk) * HEADS;  // of lane group 0
                 const uint16_t *src = j < nq ? qt : j < nq + nk ? kt : vt;
                 if (j < all && h + mine < (j < nq ? p.heads : hk))
-                    u[r] = __ldcs(reinterpret_cast<const uint4 *>(src + h * D + col));
+                    u[r] = *reinterpret_cast<const uint4 *>(src + h * D + col);
             }
             if (j0 == first && p.rot > 0 && first < nq + nk) {
                 if (pos < 0 || pos >= p.rope_rows) {
@@ -223,16 +223,16 @@ __global__ void __launch_bounds__(kStoreThreads, 8) w12_kv_store_kernel(KvStoreP
 // v, for four (token, heads) items at a time, so that eight loads per lane are in
 // flight.
 template <int D, bool Q8>
-__global__ void __launch_bounds__(kStoreThreads) w12_kv_read_kernel(KvReadParams p) {
+__global__ void __launch_bounds__(kReadThreads) w12_kv_read_kernel(KvReadParams p) {
     constexpr int LANES = D / 8, HEADS = 32 / LANES, U = 4;
     const int lane = threadIdx.x & 31, sub = lane % LANES, mine = lane / LANES;
     const int hk = p.c.kv_heads, rounds = (hk + HEADS - 1) / HEADS;
     const int64_t items = (int64_t)p.tokens * rounds;
-    const int64_t stride = (int64_t)gridDim.x * (kStoreThreads / 32);
+    const int64_t stride = (int64_t)gridDim.x * (kReadThreads / 32);
     pdl_launch_dependents();
     pdl_wait();
     uint32_t flags = 0;
-    for (int64_t i0 = (int64_t)blockIdx.x * (kStoreThreads / 32) + threadIdx.x / 32; i0 < items; i0 += U * stride) {
+    for (int64_t i0 = (int64_t)blockIdx.x * (kReadThreads / 32) + threadIdx.x / 32; i0 < items; i0 += U * stride) {
         int64_t slot[U], to[U];
         int h[U];
 #pragma unroll
