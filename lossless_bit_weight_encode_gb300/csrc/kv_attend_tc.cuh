@@ -7,7 +7,7 @@
 // Here 128 rows are the M of one tcgen05.mma: a tile's keys are read from shared
 // memory once for all rows.  Per 64-key tile
 //   S [128 x 64]  = Q (shared, K-major)  x K^T (shared, K-major)
-//   P             = 2^(S - m), one row per thread of four warps, BF16, over S
+//   P             = 2^(S - m), 16 rows per warp, BF16, over S
 //   O [128 x D] += P (TMEM)              x V (shared, MN-major)
 // S is double-buffered, so the tensor cores make the next tile's scores while the
 // softmax warps work on this one's.  O stays in TMEM for a whole piece; it is
@@ -43,6 +43,21 @@ struct TcPlace {
 
 template <int D, bool Q8>
 struct AttendTcCfg {
+    // Softmax warps, then two loaders, the MMA warp (and one that idles), four
+    // converters.  Where one CTA has the SM, eight softmax warps (16 rows each) shorten
+    // the way from scores to weights; where two share it, four (32 rows each, 16 at a
+    // time) fill it as well and leave the registers.  72 rows of head_dim 256, two
+    // requests of 100001: 127 us with eight, 133 with four (8-bit 140 and 152); 96 rows
+    // of 128, eight of 16000: 108 and 101 (8-bit 122 and 116).
+    static constexpr int kSoft = D == 256 ? 8 : 4;
+    static constexpr int kThreads = 32 * (kSoft + (Q8 ? 8 : kSoft == 8 ? 4 : 3));
+    // Registers per thread at launch, then of the softmax warps and of the others: the
+    // softmax warps take what the others give up (0: no exchange).
+    static constexpr int kRegs = !Q8 ? 0 : D == 256 ? 128 : 80;
+    static constexpr int kSoftRegs = D == 256 ? 168 : 128;
+    static constexpr int kRestRegs = D == 256 ? 88 : 56;
+    static_assert(kRegs == 0 || 32 * kSoft * kSoftRegs + (kThreads - 32 * kSoft) * kRestRegs == kThreads * kRegs,
+                  "a split with more than the launch has would wait for ever");
     static constexpr int kBlocks = D / 64;                 // 128-byte column blocks of an operand row
     static constexpr int kQBytes = kTcRows * D * 2;
     static constexpr int kTileBytes = kAttendTile * D * 2;  // K or V of a tile as BF16 operand
@@ -60,10 +75,9 @@ struct AttendTcCfg {
     static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * kInfoBytes : 0);
     static constexpr int kBars = 4 * kOps + 4 * kRaws + 2 + 2 + 2 + 3;
     static constexpr int kOffInfo = kOffBars + 8 * kBars;
-    static constexpr int kOffPlaces = kOffInfo + 4 * kTcInfo + 32;
-    static constexpr int kSmemBytes = kOffPlaces + 4 * (int)sizeof(TcPlace) + 1024;  // 1024: alignment
-    static constexpr int kThreads = Q8 ? 384 : 224;
-    static constexpr int kRegs = !Q8 ? 0 : D == 256 ? 168 : 80;  // at launch, where warps exchange registers
+    static constexpr int kOffStats = kOffInfo + 4 * kTcInfo + 32;  // (max, sum) of the 128 rows
+    static constexpr int kOffPlaces = kOffStats + 8 * kTcRows;
+    static constexpr int kSmemBytes = kOffPlaces + kSoft * (int)sizeof(TcPlace) + 1024;  // 1024: alignment
     static constexpr int kTmemCols = D == 256 ? 512 : 256;
     static constexpr int kSCol = D == 256 ? 256 : 128;  // two S buffers of 64 columns; O from column 0
 };
@@ -98,7 +112,8 @@ __device__ __forceinline__ uint64_t kv_seen64(const KvAttendParams &p, int32_t k
     uint64_t m = low_bits((int64_t)kv - kb);
     if (p.tree) {
         const int64_t sh = (int64_t)past - kb;
-        const uint64_t drawn = sh >= 64 ? 0 : sh >= 0 ? (uint64_t)v.tree << sh : sh > -32 ? (uint64_t)(v.tree >> -sh) : 0;
+        const uint64_t drawn =
+            sh >= 64 ? 0 : sh >= 0 ? (uint64_t)v.tree << sh : sh > -32 ? (uint64_t)(v.tree >> -sh) : 0;
         m &= low_bits(sh) | drawn;
     } else {
         m &= low_bits((int64_t)v.index + 1 - kb);
@@ -134,7 +149,8 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t use, uint64_t de
 // has rows g and g + 8, of every eight 32-bit columns 2 t and 2 t + 1 (of row g first).
 __device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
-                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
                  "}, [%32];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                    "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
@@ -177,10 +193,10 @@ __device__ __forceinline__ void tmem_st16x32p(uint32_t taddr, const uint32_t (&v
 // keys and not of 64: with a row per thread their broadcast reads from shared memory
 // alone took a fifth of its bandwidth.  sc (Q8): the tile's 64 key scales with the
 // softmax scale in them, its 64 value scales and the largest key scale, from the
-// thread's first key on; scale: the softmax scale, not negative (BF16).  m, l: the rows' running maximum (the
-// same in the four threads of a row) and the thread's share of their sum.  EDGE: only
-// the keys of `seen`, shifted so that bit 8 j + e is the thread's key 2 j + e.
-// rescale(a0, a1) multiplies the rows' output so far.
+// thread's first key on; scale: the softmax scale, not negative (BF16).  m, l: the
+// rows' running maximum (the same in the four threads of a row) and the thread's share
+// of their sum.  EDGE: only the keys of `seen`, shifted so that bit 8 j + e is the
+// thread's key 2 j + e.  rescale(a0, a1) multiplies the rows' output so far.
 template <bool Q8, bool EDGE, class Rescale>
 __device__ __forceinline__ void tc_softmax(uint32_t ts, const uint32_t (&x)[32], const float *sc, float scale,
                                            float (&m)[2], float (&l)[2], uint64_t seen0, uint64_t seen1,
@@ -327,7 +343,8 @@ struct TcLoader {
         __syncwarp();
         if (here) {
             const uint32_t bar = smem_u32(&full[stage]);
-            const uint32_t at = stage * slot_bytes + (Q8 ? s * bytes : blk * (kAttendTile * 128) + s * (kAttendSlice * 128));
+            const uint32_t at = stage * slot_bytes +
+                                (Q8 ? s * bytes : blk * (kAttendTile * 128) + s * (kAttendSlice * 128));
             tma_load_4d(smem_u32(ring) + at, map, Q8 ? 0 : 64 * blk, off, c.head, page, bar);
             if (scales)
                 bulk_g2s(scales + stage * 512 + s * 128,
@@ -348,7 +365,7 @@ struct TcLoader {
 };
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2)
     w12_kv_attend_tc_kernel(const KvAttendParams p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
     using C = AttendTcCfg<D, Q8>;
@@ -362,8 +379,9 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
     uint64_t *pvdone = pfull + 2, *qfull = pvdone + 2, *ofree = qfull + 1, *drain = ofree + 1;
     uint32_t *present = reinterpret_cast<uint32_t *>(smem + C::kOffInfo);
     volatile uint32_t *poison = present + kTcInfo;
-    uint32_t *tmem_slot = present + kTcInfo + 1;
+    uint32_t *tmem_slot = present + kTcInfo + 3;
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
+    constexpr int kLoadK = C::kSoft, kMma = kLoadK + 1, kLoadV = kLoadK + 2, kConvert = kLoadK + 4;  // warps
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kOps; ++i) {
@@ -380,16 +398,16 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
+            mbar_init(&pfull[i], C::kSoft);
             mbar_init(&pvdone[i], 1);
         }
-        mbar_init(qfull, 4);
-        mbar_init(ofree, 4);
+        mbar_init(qfull, C::kSoft);
+        mbar_init(ofree, C::kSoft);
         mbar_init(drain, 1);
         fence_mbar_init();
-        *poison = 0;
+        poison[0] = poison[1] = poison[2] = 0;
     }
-    if (threadIdx.x == 128) {
+    if (threadIdx.x == 32 * kMma) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
@@ -401,7 +419,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
     // TMEM only after the kernel before has finished, and the kernel behind only
     // when every CTA here has its TMEM: neither can then hold columns that the
     // other waits for
-    if (warp == 5) {
+    if (warp == kMma) {
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
@@ -412,31 +430,37 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    if (warp < 4) {
-        // 128 threads x 128 + 256 x 56 = 384 x 80 registers (232, 136, 168 for D = 256):
-        // what one side takes on the other gives up
-        if (Q8 && D < 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-        if (Q8 && D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        // ------------------------------------------------------------ softmax and output, one row per thread
-        const int lr = threadIdx.x;  // 0..127, TMEM lane
-        const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+    if (warp < C::kSoft) {
+        if constexpr (C::kRegs > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+        // ------------------------------------------------------------ softmax and output
+        // Warps w and w + 4 can reach the TMEM lanes 32 w ..: with eight warps each makes
+        // the softmax of 16 of those rows and puts out half of the columns of all 32.
+        // (What is written for HALVES == 2 is the same numbers in the form that the
+        // compiler makes the shortest loop of: 116 us against 123 for an 8-bit tree.)
+        constexpr int HALVES = 8 / C::kSoft;  // 16-row halves of a warp
+        const int quarter = HALVES == 2 ? warp : warp & 3, half = HALVES == 2 ? 0 : warp >> 2;
+        const int lr = HALVES == 2 ? threadIdx.x : 32 * quarter + lane;  // output: the thread's row
+        const int base = 32 * quarter + 16 * half;                       // softmax: the warp's first row
+        const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
+        float2 *stats = reinterpret_cast<float2 *>(smem + C::kOffStats);
         const int g8 = lane >> 2, t4 = lane & 3;
         // of a BF16 cache the softmax scale's sign is in Q, so that the largest product
         // is the largest score
         const float scale = fabsf(p.scale_log2);
-        uint32_t it = 0;
+        uint32_t it = 0, piece = 0;
         TcPlace &place = reinterpret_cast<TcPlace *>(smem + C::kOffPlaces)[warp];
         if (lane == 0) place = TcPlace{w, r, kv_piece(w, r)};
         __syncwarp();
         // Q rows of a piece to shared memory, rows behind the last one zero
         auto load_q = [&](const KvRequest &rq, const KvPiece &pc) {
-            constexpr int CH = D / 8, STEPS = CH, G = 8;  // 16-byte chunks of a row; 32 chunks a step
-            // where this lane's row is; the steps then ask the lanes
+            constexpr int CH = D / 8, STEPS = HALVES * CH / 2, G = STEPS < 8 ? STEPS : 8;  // 16-byte chunks; 32 a step
+            // where each lane's row is (of 16 or 32); the steps then ask the lanes
             const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
-            const int32_t rr = pc.rb * kTcRows + lr, tok = rr / p.group;
-            const int64_t src = lr < rows ? (int64_t)(rq.q0 + tok) * p.q_stride +
-                                                (int64_t)(pc.head * p.group + rr - tok * p.group) * D
-                                          : -1;
+            const int mine = HALVES == 2 ? lr : base + lane % 16;
+            const int32_t rr = pc.rb * kTcRows + mine, tok = rr / p.group;
+            const int64_t src = mine < rows ? (int64_t)(rq.q0 + tok) * p.q_stride +
+                                                  (int64_t)(pc.head * p.group + rr - tok * p.group) * D
+                                            : -1;
 #pragma unroll
             for (int s0 = 0; s0 < STEPS; s0 += G) {
                 uint4 u[G];
@@ -449,7 +473,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                 }
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const int i = (s0 + g) * 32 + lane, row = warp * 32 + i / CH, ch = i % CH;
+                    const int i = (s0 + g) * 32 + lane, row = base + i / CH, ch = i % CH;
                     uint4 v = u[g];
                     if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
                         v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
@@ -489,11 +513,11 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                 v.tree = p.tree ? p.tree[place.r.q0 + tok] : 0u;
                 return kv_seen64(p, keys, past, v, kb, here) >> (2 * t4);
             };
-            const bool busy = 32 * warp < nrows;  // a warp without rows only keeps step
-            // rows g, g + 8 | g + 16, g + 24 of the warp's 32, as tc_softmax has them
-            float mr[2][2], sr[2][2];
+            const bool busy = base < nrows;  // a warp without rows only keeps step
+            // rows g and g + 8 of each half, as tc_softmax has them
+            float mr[HALVES][2], sr[HALVES][2];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) mr[h / 2][h % 2] = -INFINITY, sr[h / 2][h % 2] = 0.0f;
+            for (int h = 0; h < HALVES; ++h) mr[h][0] = mr[h][1] = -INFINITY, sr[h][0] = sr[h][1] = 0.0f;
             for (int j = 0; j < tiles; ++j, ++it, kb += kAttendTile) {
                 // after a timeout the walk goes on without waiting, so that every
                 // barrier below is reached
@@ -503,25 +527,18 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                 const uint32_t here = present[it % kTcInfo];
                 // a tile whose keys not all rows see, or of which a slice is missing
                 const bool edge = here != 15u || kb > lim - kAttendTile || kb < low;
-                const uint32_t ts = tl + C::kSCol + 64 * (it & 1);
                 if (busy) {
-                    const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes) +
-                                      2 * t4;
-                    // the second 16 rows' scores are on their way while the first are
-                    // worked on, where there are registers for both
-                    constexpr bool kAhead = D == 256;
-                    uint32_t x[2][32];
-                    tmem_ld16x64(ts, x[0]);
-                    tmem_wait_ld();
-                    if (kAhead) tmem_ld16x64(ts + (16u << 16), x[1]);
+                    const float *sc =
+                        reinterpret_cast<const float *>(smem + C::kOffScale + (it % kTcInfo) * C::kInfoBytes) + 2 * t4;
+                    uint32_t x[HALVES][32];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (32 * warp + 16 * h >= nrows) break;  // the same for the warp
-                        if (h == 1) {
-                            if (!kAhead) tmem_ld16x64(ts + (16u << 16), x[1]);
-                            tmem_wait_ld();
-                        }
-                        const uint32_t to = tl + ((uint32_t)(16 * h) << 16);
+                    for (int h = 0; h < HALVES; ++h) {
+                        const int row = base + 16 * h;
+                        if (row >= nrows) break;  // the same for the warp
+                        const uint32_t to = tl + ((uint32_t)(16 * (h + half)) << 16);
+                        const uint32_t ts = to + C::kSCol + 64 * (it & 1);
+                        tmem_ld16x64(ts, x[h]);
+                        tmem_wait_ld();
                         const auto rescale = [&](float a0, float a1) {
                             if (j == 0) return;  // nothing there yet
                             if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
@@ -539,14 +556,11 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                             }
                             tmem_wait_st();
                         };
-                        const uint32_t tsh = ts + ((uint32_t)(16 * h) << 16);
-                        if (edge) {
-                            const int row = 32 * warp + 16 * h + g8;
-                            tc_softmax<Q8, true>(tsh, x[h], sc, scale, mr[h], sr[h], seen_by(row, here),
-                                                 seen_by(row + 8, here), rescale);
-                        } else {
-                            tc_softmax<Q8, false>(tsh, x[h], sc, scale, mr[h], sr[h], 0, 0, rescale);
-                        }
+                        if (edge)
+                            tc_softmax<Q8, true>(ts, x[h], sc, scale, mr[h], sr[h], seen_by(row + g8, here),
+                                                 seen_by(row + g8 + 8, here), rescale);
+                        else
+                            tc_softmax<Q8, false>(ts, x[h], sc, scale, mr[h], sr[h], 0, 0, rescale);
                     }
                     tmem_wait_st();
                 }
@@ -558,7 +572,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                     if (ok) ok = tc_wait(&vfull[stage], it / C::kOps, deadline);
                     ok = __all_sync(~0u, ok);
                     constexpr int CH = D / 8;
-                    for (int q = lr; q < kAttendTile * CH; q += 128) {
+                    for (int q = threadIdx.x; q < kAttendTile * CH; q += 32 * C::kSoft) {
                         const int key = q / CH, ch = q % CH;
                         uint4 *at = reinterpret_cast<uint4 *>(smem + C::kOffV + stage * C::kTileBytes +
                                                               (ch / 8) * (kAttendTile * 128) + key * 128 +
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                             }
                             if (hit) {
                                 *at = make_uint4(e[0], e[1], e[2], e[3]);
-                                *poison = 1;
+                                poison[piece % 3] = 1;
                             }
                         }
                     }
@@ -607,36 +621,40 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
             if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
             ok = __all_sync(~0u, ok);
             tc_fence_after();
-            // the rows' statistics: summed over a row's four threads, then to the lane
-            // that has the row in the output's layout (row 8 k + g from lane 4 g)
+            // the rows' statistics, summed over a row's four threads, for who puts the
+            // rows out; and every thread's note of values that are not finite.  One sync
+            // covers both: the notes take turns, and the next piece's is cleared while
+            // no thread can be reading or setting it
             float m = 0.0f, l = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2 * HALVES; ++k) {
                 float s = sr[k / 2][k % 2];
                 s += __shfl_xor_sync(~0u, s, 1);
                 s += __shfl_xor_sync(~0u, s, 2);
-                const float a = __shfl_sync(~0u, mr[k / 2][k % 2], (lane & 7) * 4);
-                const float b = __shfl_sync(~0u, s, (lane & 7) * 4);
-                if (lane >> 3 == k) m = a, l = b;
-            }
-            const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
-            bool bad = false;
-            if (!Q8) {
-                consumers_sync();  // every thread's note is in
-                bad = *poison != 0;
-                if (bad) {  // the same for all four warps
-                    consumers_sync();
-                    *poison = 0;
-                    consumers_sync();
+                if constexpr (HALVES == 1) {
+                    if (t4 == 0) stats[base + 8 * k + g8] = make_float2(mr[0][k], s);
+                } else {  // the warp has all of its rows: row 8 k + g from lane 4 g
+                    const float a = __shfl_sync(~0u, mr[k / 2][k % 2], (lane & 7) * 4);
+                    const float b = __shfl_sync(~0u, s, (lane & 7) * 4);
+                    if (lane >> 3 == k) m = a, l = b;
                 }
             }
+            bool bad = false;
+            if constexpr (!Q8 || HALVES == 1) {
+                if (threadIdx.x == 0) poison[(piece + 1) % 3] = 0;
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoft) : "memory");
+                if (HALVES == 1) m = stats[lr].x, l = stats[lr].y;
+                bad = !Q8 && poison[piece % 3] != 0;
+            }
+            ++piece;
+            const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (c1.ja > 0 ? 0 : 1);
-            if (busy) {
+            if (32 * quarter < nrows) {
                 const int32_t head = c1.head * p.group + c1.rb * kTcRows + lr - i * p.group;
                 uint16_t *dst = p.out + (r1.q0 + i) * p.out_stride + (int64_t)head * D;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-                for (int d0 = 0; d0 < D; d0 += 32) {
+                for (int d0 = half * (D / 2); d0 < (half + HALVES) * (D / 2); d0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(tl + d0, o);
                     tmem_wait_ld();
@@ -684,7 +702,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
                         }
                     }
                 }
-                if (lr < nrows) {
+                if (half == 0 && lr < nrows) {
                     if (!whole) p.part_ml[slot * kTcRows + lr] = make_float2(m, l);
                     else if (p.lse)
                         p.lse[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] =
@@ -697,179 +715,179 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, D == 256 ? 1 : 2)
             if (!more) break;
         }
         if (!ok && lane == 0) atomicOr(p.status, 8u);
-        } else {
-        if (Q8 && D < 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (Q8 && D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
-    if (warp == 4 || warp == 6) {
-        // ------------------------------------------------------------ loaders
-        TcLoader<D, Q8> load;
-        const bool keys = warp == 4;
-        load.map = keys ? &tm_k : &tm_v;
-        load.ring = smem + (Q8 ? C::kOffRaw + (keys ? 0 : C::kRawBytes) : keys ? C::kOffK : C::kOffV);
-        load.full = Q8 ? (keys ? rkfull : rvfull) : keys ? kfull : vfull;
-        load.empty = Q8 ? (keys ? rkempty : rvempty) : keys ? kempty : vempty;
-        load.slot_bytes = Q8 ? 2 * C::kRawBytes : C::kTileBytes;
-        load.scales = Q8 && keys ? smem + C::kOffRawScale : nullptr;
-        load.present = keys ? present : nullptr;
-        load.start(p, w, r);
-        while (ok && load.w.u < load.w.end) ok = load.step(p, deadline);
-        if (!ok && lane == 0) {
-            atomicOr(p.status, 8u);
-            load.drain(globaltimer_ns() + p.timeout_ns);
-        }
-        __syncwarp();
-    } else if (warp == 5) {
-        // ------------------------------------------------------------ MMA
-        constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kAttendTile);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
-        // The whole warp walks; one elected lane issues.  What the products' operands
-        // are computed from comes out of shuffles and votes, so that the compiler
-        // knows it to be the same for the warp: an operand that could differ between
-        // lanes costs each product a move to a uniform register, and issuing then
-        // took longer than the products (700 cycles for a tile's eight).
-        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-        const bool leader = elect_one();
-        uint32_t it = 0, piece = 0;  // tiles whose scores have been issued; pieces
-        // scores of tile `it` into S[it & 1]
-        auto scores = [&](uint32_t issued) -> bool {
-            const uint32_t stage = it % C::kOps;
-            // the buffer's last probabilities (tile it - 2) have been multiplied:
-            // wait for the last product issued so far
-            bool good = issued == 0 || tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline);
-            good = good && tc_wait(&kfull[stage], it / C::kOps, deadline);
-            if (!__all_sync(~0u, good)) return false;
-            tc_fence_after();
-            if (leader) {
-                const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
-                const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
-                const uint32_t d = tm + C::kSCol + 64 * (it & 1);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
-                               b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
-                mma_commit(&kempty[stage]);
-                mma_commit(&sfull[it & 1]);
+    } else {
+        if constexpr (C::kRegs > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
+        if (warp == kLoadK || warp == kLoadV) {
+            // ------------------------------------------------------------ loaders
+            TcLoader<D, Q8> load;
+            const bool keys = warp == kLoadK;
+            load.map = keys ? &tm_k : &tm_v;
+            load.ring = smem + (Q8 ? C::kOffRaw + (keys ? 0 : C::kRawBytes) : keys ? C::kOffK : C::kOffV);
+            load.full = Q8 ? (keys ? rkfull : rvfull) : keys ? kfull : vfull;
+            load.empty = Q8 ? (keys ? rkempty : rvempty) : keys ? kempty : vempty;
+            load.slot_bytes = Q8 ? 2 * C::kRawBytes : C::kTileBytes;
+            load.scales = Q8 && keys ? smem + C::kOffRawScale : nullptr;
+            load.present = keys ? present : nullptr;
+            load.start(p, w, r);
+            while (ok && load.w.u < load.w.end) ok = load.step(p, deadline);
+            if (!ok && lane == 0) {
+                atomicOr(p.status, 8u);
+                load.drain(globaltimer_ns() + p.timeout_ns);
             }
             __syncwarp();
-            ++it;
-            return true;
-        };
-        while (ok) {
-            int n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
-            n = __shfl_sync(~0u, n, 0);
-            if (n == 0) break;
-            ok = __all_sync(~0u, tc_wait(qfull, piece, deadline)) && scores(it);
-            for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n && !(ok = scores(it - 1))) break;
-                const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
-                bool good = tc_wait(&pfull[g & 1], g >> 1, deadline) && tc_wait(&vfull[stage], g / C::kOps, deadline);
-                if (good && j == 0 && piece > 0) good = tc_wait(ofree, piece - 1, deadline);
-                if (!(ok = __all_sync(~0u, good))) break;
+        } else if (warp == kMma) {
+            // ------------------------------------------------------------ MMA
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kAttendTile);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
+            // The whole warp walks; one elected lane issues.  What the products' operands
+            // are computed from comes out of shuffles and votes, so that the compiler
+            // knows it to be the same for the warp: an operand that could differ between
+            // lanes costs each product a move to a uniform register, and issuing then
+            // took longer than the products (700 cycles for a tile's eight).
+            const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+            const bool leader = elect_one();
+            uint32_t it = 0, piece = 0;  // tiles whose scores have been issued; pieces
+            // scores of tile `it` into S[it & 1]
+            auto scores = [&](uint32_t issued) -> bool {
+                const uint32_t stage = it % C::kOps;
+                // the buffer's last probabilities (tile it - 2) have been multiplied:
+                // wait for the last product issued so far
+                bool good = issued == 0 || tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline);
+                good = good && tc_wait(&kfull[stage], it / C::kOps, deadline);
+                if (!__all_sync(~0u, good)) return false;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t a = tm + C::kSCol + 64 * (g & 1);
-                    const uint64_t b =
-                        smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128, 1024u, 2u);
-#pragma unroll
-                    for (int k = 0; k < kAttendTile / 16; ++k)
-                        mma_tmem_a(tm, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
-                    mma_commit(&vempty[stage]);
-                    mma_commit(&pvdone[g & 1]);
+                    const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
+                    const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
+                    const uint32_t d = tm + C::kSCol + 64 * (it & 1);
+    #pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
+                                   b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
+                    mma_commit(&kempty[stage]);
+                    mma_commit(&sfull[it & 1]);
                 }
                 __syncwarp();
-            }
-            ++piece;
-            if (ok) kv_advance<kTcRows, kAttendTile>(p, w, r, n);
-        }
-        if (leader) {
-            if (!ok) atomicOr(p.status, 8u);
-            mma_commit(drain);  // nothing issued may still run when TMEM is given back
-            tc_wait(drain, 0, globaltimer_ns() + p.timeout_ns);
-        }
-        __syncwarp();
-    } else if (Q8 && warp >= 8) {
-        // ------------------------------------------------------------ converters of a Q8 cache
-        const int cw = warp - 8, ct = cw * 32 + lane;
-        constexpr uint32_t N = C::kRaws + !Q8;
-        constexpr int CH = D / 16;  // 16-byte chunks of a row
-        // the thread's first chunk and where its two operand chunks go; odd column
-        // blocks in the other order, so that eight lanes write eight different
-        // 16-byte bank groups
-        const int ckey = ct / CH, cc = ct % CH;
-        const bool turn = (cc / 4) & 1;
-        const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
-        const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
-        const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
-        const uint32_t total = (uint32_t)(w.end - w.u);
-        // K or V of tile x to its operand buffer, which the tile before must have left
-        auto convert = [&](bool values, uint32_t x) -> bool {
-            const uint32_t stage = x % N;
-            bool good = tc_wait(values ? &rvfull[stage] : &rkfull[stage], x / N, deadline);
-            if (good && x > 0) good = tc_wait(values ? &vempty[0] : &kempty[0], x - 1, deadline);
-            if (!__all_sync(~0u, good)) return false;
-            if (!values && cw < 2) {
-                // scales of the tile's keys, the softmax scale in the keys' ones, and
-                // the largest of those
-                const float2 *src = reinterpret_cast<const float2 *>(smem + C::kOffRawScale + stage * 512);
-                float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (x % kTcInfo) * C::kInfoBytes);
-                if (cw == 0) {
-                    const float a = src[lane].x * p.scale_log2, b = src[lane + 32].x * p.scale_log2;
-                    dst[lane] = a;
-                    dst[lane + 32] = b;
-                    float top = max_nan(fabsf(a), fabsf(b));
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
-                    if (lane == 0) dst[128] = top;
-                } else {
-                    dst[64 + lane] = src[lane].y;
-                    dst[96 + lane] = src[lane + 32].y;
+                ++it;
+                return true;
+            };
+            while (ok) {
+                int n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
+                n = __shfl_sync(~0u, n, 0);
+                if (n == 0) break;
+                ok = __all_sync(~0u, tc_wait(qfull, piece, deadline)) && scores(it);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j + 1 < n && !(ok = scores(it - 1))) break;
+                    const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
+                    bool good = tc_wait(&pfull[g & 1], g >> 1, deadline) &&
+                                tc_wait(&vfull[stage], g / C::kOps, deadline);
+                    if (good && j == 0 && piece > 0) good = tc_wait(ofree, piece - 1, deadline);
+                    if (!(ok = __all_sync(~0u, good))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t a = tm + C::kSCol + 64 * (g & 1);
+                        const uint64_t b =
+                            smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128, 1024u, 2u);
+    #pragma unroll
+                        for (int k = 0; k < kAttendTile / 16; ++k)
+                            mma_tmem_a(tm, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
+                        mma_commit(&vempty[stage]);
+                        mma_commit(&pvdone[g & 1]);
+                    }
+                    __syncwarp();
                 }
+                ++piece;
+                if (ok) kv_advance<kTcRows, kAttendTile>(p, w, r, n);
             }
-            const uint4 *src =
-                reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + values) * C::kRawBytes) + ct;
-            uint8_t *dst = smem + (values ? C::kOffV : C::kOffK);
-            constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
-            constexpr int G = N4 < 4 ? N4 : 4;
-#pragma unroll
-            for (int i0 = 0; i0 < N4; i0 += G) {
-                uint4 u[G];
-#pragma unroll
-                for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    uint4 a, b;
-                    q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
-                    q8_to_bf16(turn ? u[i].w : u[i].y, a.z, a.w);
-                    q8_to_bf16(turn ? u[i].x : u[i].z, b.x, b.y);
-                    q8_to_bf16(turn ? u[i].y : u[i].w, b.z, b.w);
-                    // 128 / CH keys further: a multiple of 8, the same swizzle
-                    uint8_t *row = dst + (i0 + i) * (128 / CH) * 128;
-                    *reinterpret_cast<uint4 *>(row + at0) = a;
-                    *reinterpret_cast<uint4 *>(row + at1) = b;
-                }
+            if (leader) {
+                if (!ok) atomicOr(p.status, 8u);
+                mma_commit(drain);  // nothing issued may still run when TMEM is given back
+                tc_wait(drain, 0, globaltimer_ns() + p.timeout_ns);
             }
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(values ? &vfull[0] : &kfull[0]);
-                mbar_arrive(values ? &rvempty[stage] : &rkempty[stage]);
+        } else if (Q8 && warp >= kConvert) {
+            // ------------------------------------------------------------ converters of a Q8 cache
+            const int cw = warp - kConvert, ct = cw * 32 + lane;
+            constexpr uint32_t N = C::kRaws + !Q8;
+            constexpr int CH = D / 16;  // 16-byte chunks of a row
+            // the thread's first chunk and where its two operand chunks go; odd column
+            // blocks in the other order, so that eight lanes write eight different
+            // 16-byte bank groups
+            const int ckey = ct / CH, cc = ct % CH;
+            const bool turn = (cc / 4) & 1;
+            const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
+            const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
+            const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
+            const uint32_t total = (uint32_t)(w.end - w.u);
+            // K or V of tile x to its operand buffer, which the tile before must have left
+            auto convert = [&](bool values, uint32_t x) -> bool {
+                const uint32_t stage = x % N;
+                bool good = tc_wait(values ? &rvfull[stage] : &rkfull[stage], x / N, deadline);
+                if (good && x > 0) good = tc_wait(values ? &vempty[0] : &kempty[0], x - 1, deadline);
+                if (!__all_sync(~0u, good)) return false;
+                if (!values && cw < 2) {
+                    // scales of the tile's keys, the softmax scale in the keys' ones, and
+                    // the largest of those
+                    const float2 *src = reinterpret_cast<const float2 *>(smem + C::kOffRawScale + stage * 512);
+                    float *dst = reinterpret_cast<float *>(smem + C::kOffScale + (x % kTcInfo) * C::kInfoBytes);
+                    if (cw == 0) {
+                        const float a = src[lane].x * p.scale_log2, b = src[lane + 32].x * p.scale_log2;
+                        dst[lane] = a;
+                        dst[lane + 32] = b;
+                        float top = max_nan(fabsf(a), fabsf(b));
+    #pragma unroll
+                        for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+                        if (lane == 0) dst[128] = top;
+                    } else {
+                        dst[64 + lane] = src[lane].y;
+                        dst[96 + lane] = src[lane + 32].y;
+                    }
+                }
+                const uint4 *src =
+                    reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + values) * C::kRawBytes) + ct;
+                uint8_t *dst = smem + (values ? C::kOffV : C::kOffK);
+                constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
+                constexpr int G = N4 < 4 ? N4 : 4;
+    #pragma unroll
+                for (int i0 = 0; i0 < N4; i0 += G) {
+                    uint4 u[G];
+    #pragma unroll
+                    for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
+    #pragma unroll
+                    for (int i = 0; i < G; ++i) {
+                        uint4 a, b;
+                        q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
+                        q8_to_bf16(turn ? u[i].w : u[i].y, a.z, a.w);
+                        q8_to_bf16(turn ? u[i].x : u[i].z, b.x, b.y);
+                        q8_to_bf16(turn ? u[i].y : u[i].w, b.z, b.w);
+                        // 128 / CH keys further: a multiple of 8, the same swizzle
+                        uint8_t *row = dst + (i0 + i) * (128 / CH) * 128;
+                        *reinterpret_cast<uint4 *>(row + at0) = a;
+                        *reinterpret_cast<uint4 *>(row + at1) = b;
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(values ? &vfull[0] : &kfull[0]);
+                    mbar_arrive(values ? &rvempty[stage] : &rkempty[stage]);
+                }
+                return true;
+            };
+            // the keys run one tile ahead: their buffer is free as soon as the scores
+            // are made, the values' only after the softmax
+            ok = convert(false, 0);
+            for (uint32_t x = 0; ok && x < total; ++x) {
+                if (x + 1 < total) ok = convert(false, x + 1);
+                ok = ok && convert(true, x);
             }
-            return true;
-        };
-        // the keys run one tile ahead: their buffer is free as soon as the scores
-        // are made, the values' only after the softmax
-        ok = convert(false, 0);
-        for (uint32_t x = 0; ok && x < total; ++x) {
-            if (x + 1 < total) ok = convert(false, x + 1);
-            ok = ok && convert(true, x);
+            if (!ok && lane == 0) atomicOr(p.status, 8u);
         }
-        if (!ok && lane == 0) atomicOr(p.status, 8u);
-    }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_dealloc(tmem, C::kTmemCols);
+    if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 }  // namespace dev

@@ -126,7 +126,8 @@ int attend_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev:
 // its launch.  regs > 0: the registers per thread it has to have been compiled to.
 inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams, CUtensorMap, CUtensorMap), int most,
                          int threads, int regs, int smem, std::mutex &mu, int *per_sm, int *resident,
-                         const dev::KvAttendParams *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+                         const dev::KvAttendParams *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas,
+                         void *stream, std::string *err) {
     if (d.device < 0 || d.device >= kKvMaxDevices) {
         *err = "device ordinal out of range";
         return W12_ERR_CUDA;
@@ -178,8 +179,8 @@ int attend_tc_variant(const DeviceView &d, int *resident, const dev::KvAttendPar
     static std::mutex mu;
     static int per_sm[kKvMaxDevices] = {};
     return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8>,
-                         std::min(kPartElems / (dev::kTcRows * D), 512 / C::kTmemCols), C::kThreads, C::kRegs, C::kSmemBytes, mu,
-                         per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
+                         std::min(kPartElems / (dev::kTcRows * D), 512 / C::kTmemCols), C::kThreads, C::kRegs,
+                         C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
 // The variants of one head_dim.  With 8 rows the warps split a tile's keys; so they
