@@ -40,7 +40,8 @@ dev::KvGeom geometry(const w12_kv_cache &c) {
 
 template <int D>
 cudaError_t store_dim(const DeviceView &d, bool q8, bool inter, dim3 grid, const dev::KvStoreParams &p, void *st) {
-    const auto kernel = q8 ? inter ? &dev::w12_kv_store_kernel<D, true, true> : &dev::w12_kv_store_kernel<D, true, false>
+    const auto kernel = q8      ? inter ? &dev::w12_kv_store_kernel<D, true, true>
+                                        : &dev::w12_kv_store_kernel<D, true, false>
                         : inter ? &dev::w12_kv_store_kernel<D, false, true>
                                 : &dev::w12_kv_store_kernel<D, false, false>;
     return kv_launch(d, kernel, grid, dev::kStoreThreads, 0, 1, st, p);

@@ -75,7 +75,7 @@ struct AttendCfg {
     static constexpr int kTileBytes = kSlices * kSliceBytes;  // k (or v) of a stage
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kCtas = attend_ctas<D, Q8, NT>();
-    static constexpr int kRing = (kCtas == 1 ? 192 : kCtas == 2 ? 96 : kCtas == 3 ? 60 : 48) * 1024;
+    static constexpr int kRing = (kCtas == 1 ? 192 : kCtas == 2 ? 96 : 60) * 1024;
     static constexpr int kStages = kRing / kStageBytes > 8 ? 8 : kRing / kStageBytes;
     static_assert(kStages >= 2, "a ring");
     static constexpr int kScaleBytes = Q8 ? kTile * 8 : 0;  // per stage: (k, v) of each key
@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         top[nt][e] = fmaxf(x[0][nt][e], x[0][nt][e + 2]);
-                        if (PAIR == 2) top[nt][e] = fmaxf(fmaxf(top[nt][e], x[PAIR - 1][nt][e]), x[PAIR - 1][nt][e + 2]);
+                        if (PAIR == 2)
+                            top[nt][e] = fmaxf(fmaxf(top[nt][e], x[PAIR - 1][nt][e]), x[PAIR - 1][nt][e + 2]);
                         raise |= top[nt][e] > m[nt][e] + kAttendLazy;
                     }
                 if (__any_sync(~0u, raise)) {
@@ -888,7 +889,8 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
 
         if (!whole && !p.join_later) {
             const KvParts q = kv_parts<ROWS>(p, w, r, c);
-            if (kv_arrive(p, q, last_flag)) kv_join<ROWS, D, C::kCtas < 3 ? 8 : 4>(p, q, r, c, nrows, (int)threadIdx.x, 128);
+            if (kv_arrive(p, q, last_flag))
+                kv_join<ROWS, D, C::kCtas < 3 ? 8 : 4>(p, q, r, c, nrows, (int)threadIdx.x, 128);
         }
         kv_advance<ROWS, TILE>(p, w, r, c.jb - c.ja);
     }

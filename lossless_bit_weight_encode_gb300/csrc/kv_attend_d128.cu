@@ -10,7 +10,8 @@ int attend_dim<128>(const DeviceView &d, bool q8, int rows, int *resident, const
     const int rc = q8 ? attend_rows_variant<128, true>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err)
                       : attend_rows_variant<128, false>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err);
     if (rc != W12_OK || !p || !p->join_later) return rc;
-    return q8 ? join_parts<128, true>(d, rows, *p, ctas, stream, err) : join_parts<128, false>(d, rows, *p, ctas, stream, err);
+    return q8 ? join_parts<128, true>(d, rows, *p, ctas, stream, err)
+              : join_parts<128, false>(d, rows, *p, ctas, stream, err);
 }
 
 }  // namespace launch

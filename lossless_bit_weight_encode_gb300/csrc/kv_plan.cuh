@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
     pdl_wait();
     const int64_t head = p.state_in[0], tail = p.state_in[1];
     const int32_t avail = clamp_i32(tail - head, 0, p.ring_size);
-    const int32_t head_at = ring_base(head, p.ring_size, p.ring_inv), tail_at = ring_base(tail, p.ring_size, p.ring_inv);
+    const int32_t head_at = ring_base(head, p.ring_size, p.ring_inv);
+    const int32_t tail_at = ring_base(tail, p.ring_size, p.ring_inv);
     const int32_t cap = p.max_blocks * p.page_size;
     int64_t tok0 = 0;
     int32_t grow0 = 0, drop0 = 0;  // totals of the chunks before

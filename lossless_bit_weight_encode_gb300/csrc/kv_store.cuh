@@ -70,7 +70,8 @@ __device__ __forceinline__ void rope_row(const float *row, int rot, int sub, f2 
         // the first half gets x cos - partner sin, the second x cos + partner sin
         const bool low = 8 * sub < h2;
         const int c = low ? 8 * sub : 8 * sub - h2;
-        const float4 *x = reinterpret_cast<const float4 *>(row + c), *y = reinterpret_cast<const float4 *>(row + h2 + c);
+        const float4 *x = reinterpret_cast<const float4 *>(row + c);
+        const float4 *y = reinterpret_cast<const float4 *>(row + h2 + c);
         const float sg = low ? -1.0f : 1.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(kReadThreads) w12_kv_read_kernel(KvReadParams 
             k[r] = v[r] = make_uint4(0, 0, 0, 0);
             s[r] = make_float2(0.0f, 0.0f);
             if (kept && to[r] >= 0) {
-                const int64_t e = at.page * p.c.page_stride + h[r] * p.c.head_stride + at.off * p.c.row_stride + 8 * sub;
+                const int64_t e =
+                    at.page * p.c.page_stride + h[r] * p.c.head_stride + at.off * p.c.row_stride + 8 * sub;
                 if (!Q8) {
                     k[r] = reinterpret_cast<const uint4 *>(p.c.k)[e / 8];
                     v[r] = reinterpret_cast<const uint4 *>(p.c.v)[e / 8];
