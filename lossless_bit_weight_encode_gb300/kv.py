@@ -14,22 +14,57 @@ graph after one ordinary call on the same stream.
 """
 from __future__ import annotations
 
+import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
 from . import w12
+from .build import KV_HOST_PATH
 
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
 _workspaces = {}  # (device, stream handle) -> zeroed workspace of the attend calls on that stream
-
-
+_outgrown = []  # smaller ones of before: a captured graph may still use them
 
 
 def clear_workspaces():
     """Drop the attend calls' workspaces (after a TIMEOUT, which can leave their
-    counters set; the next call makes a zeroed one)."""
+    counters set; the next call makes a zeroed one).  Graphs captured with them
+    must not be replayed any more."""
     _workspaces.clear()
+    _outgrown.clear()
 
+
+def _grow(index, st, size):
+    """A zeroed workspace of at least ``size`` bytes for stream ``st``."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("the workspace of this stream is not large enough yet: make one ordinary call of "
+                           "this size on the stream before capturing, or pass workspace=")
+    if (index, st) in _workspaces:
+        _outgrown.append(_workspaces[index, st])
+    ws = torch.zeros((size + (1 << 20) - 1) >> 20 << 20, dtype=torch.uint8, device=torch.device("cuda", index))
+    _workspaces[index, st] = ws
+    return ws
+
+
+def _load_host():
+    """The module that takes the calls from tensors to the C ABI."""
+    if not os.path.exists(KV_HOST_PATH):
+        raise RuntimeError(f"the paged cache's host module is not built ({KV_HOST_PATH} missing): run "
+                           "__graft_entry__.build()")
+    loader = importlib.machinery.ExtensionFileLoader("kv_host", KV_HOST_PATH)
+    host = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kv_host", loader=loader))
+    loader.exec_module(host)
+    lib = w12.lib()
+    host.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.w12_kv_plan, lib.w12_kv_store, lib.w12_kv_read, lib.w12_kv_attend_workspace_size, lib.w12_kv_attend)),
+        w12._check)
+    return host
+
+
+_host = _load_host()
 
 _current_device = torch._C._cuda_getDevice
 # handle of a device's current stream, without the stream object around it
@@ -53,7 +88,6 @@ class _on:
             self.guards += (torch.cuda.stream(s),)
         for g in self.guards:
             g.__enter__()
-        return _current_stream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -71,23 +105,6 @@ def _ints(t, dtype, name, index):
     if t.dtype is not dtype or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor on CUDA device {index}")
     return t.data_ptr()
-
-
-def _rows(t, dim, name, index, heads=None):
-    """(pointer, token stride, tokens, heads) of [T, heads * dim] or
-    [T, heads, dim] BF16 rows whose heads lie one after the other."""
-    shape, stride = t.shape, t.stride()
-    n = 0
-    if len(shape) == 2:
-        if stride[1] == 1 and shape[1] % dim == 0:
-            n = shape[1] // dim
-    elif len(shape) == 3 and shape[2] == dim and stride[2] == 1 and (stride[1] == dim or shape[1] == 1):
-        n = shape[1]
-    if n < 1 or t.dtype is not _BF16 or t.get_device() != index or (heads is not None and n != heads):
-        raise ValueError(f"{name} must be BF16 [tokens, {heads or 'heads'} * {dim}] on CUDA device {index} with "
-                         "contiguous heads")
-    # one row has no stride that matters
-    return t.data_ptr(), stride[0] if shape[0] > 1 else n * dim, shape[0], n
 
 
 class KVStep:
@@ -164,37 +181,15 @@ class KVPages:
         unless outputs are given.  ``step`` refers to ``lens``, which must stay as
         it is until the step's attend calls have run.  A ring that runs out is
         reported by w12_check_status."""
-        if stream is None and _current_device() == self._index:
-            return self._plan(lens, new_lens, step, trim, owned_out, ring_state_out, _current_stream(self._index))
-        with _on(self._index, stream) as st:
-            return self._plan(lens, new_lens, step, trim, owned_out, ring_state_out, st)
-
-    def _plan(self, lens, new_lens, step, trim, owned_out, ring_state_out, st):
-        tables, index = self.tables, self._index
-        n, blocks = tables.shape
+        if stream is not None or _current_device() != self._index:
+            with _on(self._index, stream):
+                return self.plan(lens, new_lens, step, trim, owned_out, ring_state_out)
         if step.lens is not lens:
             step.lens = lens
-        if step.tables is not tables:
-            step.tables = tables
-        cu, positions, slots, owned, state = step.cu_new, step.positions, step.slots, self.owned, self.ring_state
-        tokens = slots.numel()
-        if (step.device != index or lens.numel() != n or new_lens.numel() != n or cu.numel() != n + 1
-                or positions.numel() != tokens):
-            raise ValueError("lens, new_lens and step must be on the tables' device, with an entry per request")
-        owned_p, state_p = owned.data_ptr(), state.data_ptr()
-        owned_o, state_o = owned_p, state_p
-        if owned_out is not None:
-            owned_o = _ints(owned_out, _I32, "owned_out", index)
-            _need(owned_out.numel() == n, "owned_out must have an entry per request")
-        if ring_state_out is not None:
-            state_o = _ints(ring_state_out, _I64, "ring_state_out", index)
-            _need(ring_state_out.numel() == 2, "ring_state_out must have two entries")
-        w12.w12_kv_plan(w12.w12_kv_plan_args(
-            lens.data_ptr(), _ints(new_lens, _I32, "new_lens", index), owned_p, owned_o, tables.data_ptr(),
-            tables.stride(0) if n > 1 else blocks, self.ring.data_ptr(), state_p, state_o, cu.data_ptr(),
-            positions.data_ptr(), slots.data_ptr(), n, blocks, self.page_size, self.ring.numel(), tokens,
-            1 if trim else 0), st)
-        return step
+        if step.tables is not self.tables:
+            step.tables = self.tables
+        return _host.plan(self, self._index, lens, new_lens, step, trim, owned_out, ring_state_out,
+                          _current_stream(self._index))
 
 
 class KVCache:
@@ -206,7 +201,8 @@ class KVCache:
     def __init__(self, k, v, scales=None):
         _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype,
               "k and v must be alike, [num_pages, kv_heads, page_size, head_dim]")
-        _need(k.is_cuda and v.device == k.device and k.stride(3) == 1, "k and v must be CUDA tensors with contiguous rows")
+        _need(k.is_cuda and v.device == k.device and k.stride(3) == 1,
+              "k and v must be CUDA tensors with contiguous rows")
         _need(k.dtype in (_BF16, torch.int8), "k and v must be BF16 or int8")
         _need((scales is None) == (k.dtype == _BF16), "an int8 cache needs scales, a BF16 cache has none")
         pages, heads, page, dim = k.shape
@@ -221,8 +217,8 @@ class KVCache:
         self._c = w12.w12_kv_cache(k.data_ptr(), v.data_ptr(), None if scales is None else scales.data_ptr(), pages,
                                    stride[0], stride[1], stride[2], page, heads, dim,
                                    w12.KV_BF16 if scales is None else w12.KV_Q8)
+        self._address = ctypes.addressof(self._c)
         self._scale = dim ** -0.5
-        self._ws_bytes = {}
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, dtype="bf16", device=None):
@@ -240,85 +236,19 @@ class KVCache:
         fp32 [positions, rot], cosines then sines) of q and k, k and v into the
         cache at step.slots.  Returns the new q, [tokens, heads, head_dim] (of
         ``out``, which may be q); q None: only k and v."""
-        if stream is None and _current_device() == self._index:
-            return self._store(q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out, _current_stream(self._index))
-        with _on(self._index, stream) as st:
-            return self._store(q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out, st)
-
-    def _store(self, q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out, st):
-        dim, index = self.head_dim, self._index
-        kp, ks, tokens, _ = _rows(k, dim, "k", index, self.kv_heads)
-        vp, vs, nv, _ = _rows(v, dim, "v", index, self.kv_heads)
-        slots = step.slots
-        if slots is None or step.device != index or nv != tokens or slots.numel() != tokens:
-            raise ValueError("k, v and step.slots must have as many tokens, on the cache's device")
-        qp = qs = op = os_ = heads = rot = rows = rp = pp = 0
-        if rope is not None:
-            positions = step.positions
-            if (rope.dtype is not _F32 or rope.dim() != 2 or not rope.is_contiguous() or rope.get_device() != index
-                    or positions is None or positions.numel() != tokens):
-                raise ValueError("rope must be a contiguous fp32 tensor [positions, rot] on the cache's device and "
-                                 "step.positions have as many tokens as k")
-            rows, rot = rope.shape
-            rp, pp = rope.data_ptr(), positions.data_ptr()
-        wq = self._weight(q_norm, "q_norm") if q_norm is not None else 0
-        wk = self._weight(k_norm, "k_norm") if k_norm is not None else 0
-        if q is not None:
-            qp, qs, nq, heads = _rows(q, dim, "q", index)
-            if out is None:
-                out = torch.empty(q.shape, dtype=_BF16, device=self.device)
-            op, os_, no, _ = _rows(out, dim, "out", index, heads)
-            if nq != tokens or no != tokens:
-                raise ValueError("q, out and k must have as many tokens")
-        if tokens:
-            w12.w12_kv_store(self._c, w12.w12_kv_store_args(qp, kp, vp, op, qs, ks, vs, os_, wq, wk, rp, pp,
-                                                            slots.data_ptr(), rows, tokens, heads, rot,
-                                                            1 if interleaved else 0, eps), st)
-        return None if q is None else out if out.dim() == 3 else out.view(tokens, heads, dim)
-
-    def _weight(self, w, name):
-        if w.dtype is not _BF16 or w.dim() != 1 or w.numel() != self.head_dim or not w.is_contiguous() \
-                or w.get_device() != self._index:
-            raise ValueError(f"{name} must be contiguous BF16 [{self.head_dim}] on CUDA device {self._index}")
-        return w.data_ptr()
+        if stream is not None or _current_device() != self._index:
+            with _on(self._index, stream):
+                return self.store(q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out)
+        return _host.store(self._address, self._index, q, k, v, step, q_norm, k_norm, eps, rope, interleaved, out,
+                           _current_stream(self._index))
 
     def read(self, slots, out=None, stream=None):
         """(k, v) BF16 [tokens, kv_heads, head_dim] of the cached rows at ``slots``
         (int64; zeros for -1).  ``out``: a pair to write to."""
-        if stream is None and _current_device() == self._index:
-            return self._read(slots, out, _current_stream(self._index))
-        with _on(self._index, stream) as st:
-            return self._read(slots, out, st)
-
-    def _read(self, slots, out, st):
-        sp, tokens = _ints(slots, _I64, "slots", self._index), slots.numel()
-        shape = (tokens, self.kv_heads, self.head_dim)
-        if out is None:
-            k = torch.empty(shape, dtype=_BF16, device=self.device)
-            v = torch.empty(shape, dtype=_BF16, device=self.device)
-        else:
-            k, v = out
-            for t in out:
-                _need(t.shape == shape and t.dtype is _BF16 and t.is_contiguous() and t.get_device() == self._index,
-                      "out must be two contiguous BF16 tensors [tokens, kv_heads, head_dim]")
-        if tokens:
-            w12.w12_kv_read(self._c, sp, tokens, k.data_ptr(), v.data_ptr(), st)
-        return k, v
-
-    def workspace(self, args, key, st):
-        """The zeroed workspace of the attend calls on stream ``st`` (shared by
-        all caches), large enough for ``args``; ``key``: what its size depends on."""
-        size = self._ws_bytes.get(key)
-        if size is None:
-            size = self._ws_bytes[key] = w12.w12_kv_attend_workspace_size(self._c, args)
-        ws = _workspaces.get((self._index, st))
-        if ws is None or ws.numel() < size:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("the workspace of this stream is not large enough yet: make one ordinary call of "
-                                   "this size on the stream before capturing, or pass workspace=")
-            ws = torch.zeros((size + (1 << 20) - 1) >> 20 << 20, dtype=torch.uint8, device=self.device)
-            _workspaces[(self._index, st)] = ws
-        return ws
+        if stream is not None or _current_device() != self._index:
+            with _on(self._index, stream):
+                return self.read(slots, out)
+        return _host.read(self._address, self._index, slots, out, _current_stream(self._index))
 
     def attend(self, q, step, scale=None, window=0, out=None, lse=None, workspace=None, stream=None):
         """Attention of the step's new tokens over their requests' cached ones
@@ -328,38 +258,10 @@ class KVCache:
         stream share a workspace; ``workspace`` (uint8, zero-filled before its
         first use) takes its place, as a captured graph needs that is replayed
         beside other calls."""
-        if stream is None and _current_device() == self._index:
-            return self._attend(q, step, scale, window, out, lse, workspace, _current_stream(self._index))
-        with _on(self._index, stream) as st:
-            return self._attend(q, step, scale, window, out, lse, workspace, st)
-
-    def _attend(self, q, step, scale, window, out, lse, workspace, st):
-        dim, index = self.head_dim, self._index
-        qp, qs, tokens, heads = _rows(q, dim, "q", index)
-        tables, lens, cu, tree = step.tables, step.lens, step.cu_new, step.tree
-        rows, blocks = tables.shape
-        n = lens.numel()
-        if step.device != index or rows != n or cu.numel() != n + 1:
-            raise ValueError("step.tables, lens and cu_new must agree and be on the cache's device")
-        tree_p = lse_p = 0
-        if tree is not None:
-            tree_p = tree.data_ptr()
-            _need(tree.numel() >= tokens, "step.tree must have a mask per token")
-        if lse is not None:
-            if (lse.dtype is not _F32 or lse.shape != (tokens, heads) or not lse.is_contiguous()
-                    or lse.get_device() != index):
-                raise ValueError("lse must be contiguous fp32 [tokens, heads] on the cache's device")
-            lse_p = lse.data_ptr()
-        if out is None:
-            out = torch.empty(q.shape, dtype=_BF16, device=self.device)
-        op, os_, no, _ = _rows(out, dim, "out", index, heads)
-        if no != tokens:
-            raise ValueError("out and q must have as many tokens")
-        if tokens == 0:
-            return out
-        args = w12.w12_kv_attend_args(
-            qp, op, lse_p, qs, os_, tables.data_ptr(), tables.stride(0) if n > 1 else blocks, lens.data_ptr(),
-            cu.data_ptr(), tree_p, n, blocks, tokens, heads, step.max_new, window, self._scale if scale is None else scale)
-        ws = self.workspace(args, (n, tokens, heads, step.max_new, blocks), st) if workspace is None else workspace
-        w12.w12_kv_attend(self._c, args, ws.data_ptr(), ws.numel() * ws.element_size(), st)
-        return out
+        if stream is not None or _current_device() != self._index:
+            with _on(self._index, stream):
+                return self.attend(q, step, scale, window, out, lse, workspace)
+        st = _current_stream(self._index)
+        own = workspace is None
+        return _host.attend(self._address, self._index, q, step, self._scale if scale is None else scale, window, out,
+                            lse, _workspaces.get((self._index, st)) if own else workspace, _grow if own else None, st)
