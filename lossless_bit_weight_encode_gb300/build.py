@@ -47,7 +47,7 @@ def _kv_host_command(out: str):
             "-isystem", os.path.join(torch, "include"),
             "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, KV_HOST_SOURCE), "-o", out,
-            "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+            "-L", libs, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
