@@ -32,6 +32,13 @@
 //
 // Q8 cache: int8 elements become BF16 exactly in registers; a key's scale
 // multiplies its score, a value's scale its probability.
+//
+// Measured: 64 requests of 8000 tokens, 48 heads over 8 of 128: BF16 310 us, 6.8 TB/s
+// (a copy of that many bytes takes as long); Q8 192 us, 5.7 TB/s, where issue (the
+// conversion) is close behind HBM.  Two of 100001, 24 heads over 4 of 256: 114 us,
+// 6.6 TB/s.  128 windows of 1024 keys: 55 us, 5.0 TB/s; calls this short spend some
+// 14 us before the ring is full and after it has run dry.  One request of 777 tokens:
+// 7.2 us, all of it latency (two launches, TMA, the join).
 #pragma once
 
 #include <cuda.h>

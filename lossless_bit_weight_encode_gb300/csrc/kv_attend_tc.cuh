@@ -23,6 +23,12 @@
 //
 // For head_dim 64 and 128 a CTA takes half of TMEM and less than half of the
 // shared memory, so two share an SM and fill each other's waits.
+//
+// Measured, 16-token trees over eight requests of 16000 tokens, 48 heads over 8 of
+// 128 (96 rows): BF16 102 us, 5.3 TB/s; Q8 116 us.  HBM would take 81 and 42 us, the
+// products 22: the Q8 kernel is bounded by what the softmax and the converters issue
+// and by shared memory, through which the bytes, the operands and the products' reads
+// of them all pass.  30 rows of 64 requests of 8000: BF16 320 us, 6.6 TB/s, Q8 336.
 #pragma once
 
 #include "kv_attend.cuh"

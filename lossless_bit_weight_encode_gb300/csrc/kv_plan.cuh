@@ -7,8 +7,12 @@
 // thread, its request found by a binary search in the prefix sums, so that one
 // long prompt among short ones costs no more than the same tokens spread out.
 //
-// The call is latency: it moves 20 bytes per request and 12 per token.  One
-// cluster of CTAs computes the sums redundantly and shares the lists; its
+// The call is latency: it moves 20 bytes per request and 12 per token (at the HBM
+// rate 0.06 us of the 6.9 us that 1024 requests with 32768 new tokens take; one request
+// with one token takes 3.3, an empty kernel 2).  What is left is the chain: lengths,
+// prefix sums, search, ring or table entry, store.  One cluster of CTAs (one CTA
+// where its threads have at most two tokens each) computes the sums redundantly and
+// shares the lists, so that there is one launch and nothing in memory between; its
 // barrier is what allows owned and the ring state to be updated in place.  No
 // CTA reads what another writes: a taken page is read from the ring, never from
 // the table entry it goes to, and the ring positions given back are not those
