@@ -719,3 +719,100 @@ def test_holders_refuse():
         KVPages(step.tables, step.lens, dev([1], torch.int64), dev([0, 1], torch.int64), 16)
     assert cache.attend(q[:0], step).shape == (0, 256)
     status()
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(24, 2, 64), (40, 2, 128), (40, 2, 256), (6, 2, 128)])
+def test_attend_infinite_values_among_many_short_requests(heads, kv_heads, dim):
+    # several short requests per CTA, every other one with infinities that its row sees
+    lens = [(37 * b) % 150 for b in range(331)]
+    cache, tables, cu, q, step = attend_case(lens, [1] * len(lens), heads, kv_heads, dim, 16, False, 21)
+    hit = torch.zeros(len(lens), kv_heads, dim, dtype=torch.bool)
+    for b in range(0, len(lens), 2):
+        for head, col in ((b % kv_heads, b % dim), (0, dim - 1)):
+            key = lens[b] - (b % 3 if lens[b] > 2 else 0)
+            cache.v[int(tables[b, key // 16]), head, key % 16, col] = math.inf
+            hit[b, head, col] = True
+    out, lse = run_attend(cache, q, step)
+    hit = hit.repeat_interleave(heads // kv_heads, 1)
+    out = out.view(hit.shape).cpu()
+    assert (out[hit] == math.inf).all() and torch.isfinite(out[~hit]).all()
+    ref = attend_ref(q, cache, tables, lens, cu, None, 0, dim ** -0.5, heads // kv_heads)
+    for x in (out, ref[0], ref[2]):
+        x.masked_fill_(hit, 0.0)
+    check_attend(out, lse, ref)
+
+
+def test_workspace_outgrown_after_a_capture():
+    # 2^18 + 64 row blocks need more counters than the first MiB of them holds
+    cache, tables, cu, q, step = attend_case([700, 20], [1, 1], 4, 1, 64, 16, False, 22)
+    ref = attend_ref(q, cache, tables, [700, 20], cu, None, 0, 0.125, 4)
+    stream = torch.cuda.Stream()
+    out, lse = torch.empty_like(q), torch.empty(2, 4, device="cuda")
+    with torch.cuda.stream(stream):
+        cache.attend(q, step, out=out, lse=lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        cache.attend(q, step, out=out, lse=lse)
+    n = (1 << 18) + 64
+    many = KVStep(step.tables[:1].expand(n, -1).contiguous(), torch.zeros(n, dtype=torch.int32, device="cuda"),
+                  torch.arange(n + 1, dtype=torch.int32, device="cuda"))
+    with torch.cuda.stream(stream):
+        big = cache.attend(q[:1].expand(n, -1, -1).contiguous(), many)
+    fill = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")  # whatever memory was given back
+    out.zero_(), lse.zero_()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attend(out, lse, ref)
+    # one visible key: its value (BF16) is the output
+    first = cache.v[int(tables[0, 0]), 0, 0]
+    assert (big.view(n, 4, 64) == first).all()
+    del fill
+    status()
+
+
+def test_calls_refuse_what_is_no_tensor_or_does_not_fit():
+    cache = make_cache(2, 2, 16, 64, False)
+    step = KVStep(dev([[0, 1]], torch.int32), dev([3], torch.int32), dev([0, 1], torch.int32),
+                  positions=dev([3], torch.int32), slots=dev([3], torch.int64))
+    q = torch.zeros(1, 4 * 64, device="cuda", dtype=torch.bfloat16)
+    kv = torch.zeros(1, 2 * 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        cache.attend([1.0], step)
+    with pytest.raises(TypeError):
+        cache.store(q, None, kv, step)
+    with pytest.raises(TypeError):
+        cache.read(3)
+    with pytest.raises(ValueError):
+        cache.attend(q, step, window=1 << 32)
+    with pytest.raises(ValueError):
+        cache.attend(q.cpu(), step)
+    with pytest.raises(ValueError):
+        cache.store(q, kv.cpu(), kv, step)
+    with pytest.raises(TypeError):
+        cache.attend(q, KVStep(step.tables, None, step.cu_new))
+    with pytest.raises(ValueError):
+        cache.read(step.slots, out=(kv.view(1, 2, 64), kv.float().view(1, 2, 64)))
+    with pytest.raises(TypeError):
+        KVPages(step.tables, step.lens, dev([1], torch.int32), dev([0, 1], torch.int64), 16).plan(
+            step.lens, [1], step)
+
+
+def test_store_returns_out_by_heads():
+    cache = make_cache(2, 2, 16, 64, False)
+    step = KVStep(slots=dev([0, 17, -1], torch.int64))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k = (torch.randn(3, n * 64, device="cuda", generator=g).to(torch.bfloat16) for n in (4, 2))
+    wide = torch.zeros(3, 304, device="cuda", dtype=torch.bfloat16)
+    out = wide[:, 24:280]
+    y = cache.store(q, k, k, step, out=out)
+    assert y.shape == (3, 4, 64) and y.data_ptr() == out.data_ptr() and y.stride() == (304, 64, 1)
+    assert torch.equal(y.reshape(3, 256), q) and torch.equal(out, q)
+    y.mul_(2)
+    assert torch.equal(out, 2 * q) and not wide[:, :24].any() and not wide[:, 280:].any()
+    three = torch.empty(3, 4, 64, device="cuda", dtype=torch.bfloat16)
+    assert cache.store(q, k, k, step, out=three) is three
+    fresh = cache.store(q, k, k, step)
+    assert fresh.shape == (3, 4, 64) and torch.equal(fresh.view(3, 256), q)
