@@ -6,29 +6,31 @@
 // warp reads (and, of an 8-bit cache, converts) the same keys for its own few rows.
 // Here 128 rows are the M of one tcgen05.mma: a tile's keys are read from shared
 // memory once for all rows.  Per 64-key tile
-//   S [128 x 64]  = Q (shared, K-major)  x K^T (shared, K-major)
+//   S [128 x 64]  = Q (TMEM or shared)   x K^T (shared, K-major)
 //   P             = 2^(S - m), 16 rows per warp, BF16, over S
 //   O [128 x D] += P (TMEM)              x V (shared, MN-major)
-// S is double-buffered, so the tensor cores make the next tile's scores while the
-// softmax warps work on this one's.  O stays in TMEM for a whole piece; it is
+// S has two or four buffers, so the tensor cores make the next tiles' scores while
+// the softmax warps work on this one's.  O stays in TMEM for a whole piece; it is
 // rescaled only when a row's maximum rises by more than 2^8.
 //
 // Two warps fill the K and V rings by TMA.  A Q8 cache's rows arrive as bytes in
-// rings of their own and four warps turn them into BF16 operands;
+// rings of their own and four or eight warps turn them into BF16 operands;
 // the order of the columns within every four (0, 2, 1, 3) is what comes out of the
 // byte pairs cheapest, and Q's columns and O's follow it.
 //
 // What a CTA has of a row block that others share goes to the workspace and is
 // joined by w12_kv_join_kernel: 128 rows of parts are too much for one CTA.
 //
-// For head_dim 64 and 128 a CTA takes half of TMEM and less than half of the
-// shared memory, so two share an SM and fill each other's waits.
+// For head_dim 64, and 128 with a Q8 cache, a CTA takes half of TMEM and less than half
+// of the shared memory, so two share an SM and fill each other's waits.
 //
 // Measured, 16-token trees over eight requests of 16000 tokens, 48 heads over 8 of
-// 128 (96 rows): BF16 102 us, 5.3 TB/s; Q8 116 us.  HBM would take 81 and 42 us, the
-// products 22: the Q8 kernel is bounded by what the softmax and the converters issue
-// and by shared memory, through which the bytes, the operands and the products' reads
-// of them all pass.  30 rows of 64 requests of 8000: BF16 320 us, 6.6 TB/s, Q8 336.
+// 128 (96 rows): BF16 96 us, 5.6 TB/s; Q8 117 us.  HBM would take 81 and 42 us, the
+// products 22.  Taking the softmax's or the conversion's instructions out shortens the
+// Q8 call by 7 % each, both by 26 %: it is bounded by the chain of bytes, operand,
+// scores, weights and product, of which two CTAs per SM overlap two.  30 rows of 64
+// requests of 8000: BF16 320 us, 6.6 TB/s, Q8 344.  72 rows of 256 columns, two of
+// 100001: BF16 128 us, Q8 107.
 #pragma once
 
 #include "kv_attend.cuh"
@@ -49,28 +51,45 @@ struct TcPlace {
 
 template <int D, bool Q8>
 struct AttendTcCfg {
-    // Softmax warps, then two loaders, the MMA warp (and one that idles), four
-    // converters.  Where one CTA has the SM, eight softmax warps (16 rows each) shorten
-    // the way from scores to weights; where two share it, four (32 rows each, 16 at a
-    // time) fill it as well and leave the registers.  72 rows of head_dim 256, two
-    // requests of 100001: 127 us with eight, 133 with four (8-bit 140 and 152); 96 rows
-    // of 128, eight of 16000: 108 and 101 (8-bit 122 and 116).
-    static constexpr int kSoft = D == 256 ? 8 : 4;
-    static constexpr int kThreads = 32 * (kSoft + (Q8 ? 8 : kSoft == 8 ? 4 : 3));
+    // Q is the scores' A operand: from TMEM, written there once per piece, where there
+    // are columns for it beside O and the scores; else from shared memory, where every
+    // tile's products read it again (128 columns, BF16: 96 us from TMEM, 102 from shared
+    // memory, for the trees above) and where it takes the room of ring slots.  Only the
+    // 8-bit cache of 128 columns has no columns left: its two CTAs per SM are worth more
+    // (117 us; one CTA with Q in TMEM 116, but 404 against 366 at 64000 tokens).
+    static constexpr bool kQTmem = !Q8 || D != 128;
+    // One CTA per SM or two (with half of TMEM each).
+    static constexpr bool kOne = D == 256 || (D == 128 && kQTmem);
+    // Score buffers, and how many tiles the scores are made ahead of the products.
+    static constexpr int kS = D == 128 && kQTmem ? 4 : 2, kAheadS = kS / 2;
+    // Softmax warps, then two loaders, the MMA warp (and one that idles), the converters
+    // in groups of four.  Where one CTA has the SM, eight softmax warps (16 rows each)
+    // shorten the way from scores to weights; where two share it, four (32 rows each, 16
+    // at a time) fill it as well and leave the registers.  72 rows of 256 columns, two
+    // requests of 100001: 127 us with eight, 133 with four; 96 rows of 128, the 8-bit
+    // trees: 122 and 116.  Keys and values have a group of converters each where there
+    // are threads for it (256 columns, 8-bit: 107 us, 140 with one group and one operand
+    // buffer; 128: 376 against 369 with one, at 64000 tokens).
+    static constexpr int kSoft = kOne ? 8 : 4;
+    static constexpr int kGroups = !Q8 ? 0 : kOne ? 2 : 1;
+    static constexpr int kThreads = 32 * (kSoft + (Q8 ? 4 + 4 * kGroups : kOne ? 4 : 3));
     // Registers per thread at launch, then of the softmax warps and of the others: the
     // softmax warps take what the others give up (0: no exchange).
-    static constexpr int kRegs = !Q8 ? 0 : D == 256 ? 128 : 80;
-    static constexpr int kSoftRegs = D == 256 ? 168 : 128;
-    static constexpr int kRestRegs = D == 256 ? 88 : 56;
+    static constexpr int kRegs = !Q8 ? 0 : kOne ? 96 : 80;
+    static constexpr int kSoftRegs = kOne ? 144 : 128;
+    static constexpr int kRestRegs = kOne ? 64 : 56;
     static_assert(kRegs == 0 || 32 * kSoft * kSoftRegs + (kThreads - 32 * kSoft) * kRestRegs == kThreads * kRegs,
                   "a split with more than the launch has would wait for ever");
-    static constexpr int kBlocks = D / 64;                 // 128-byte column blocks of an operand row
-    static constexpr int kQBytes = kTcRows * D * 2;
+    static constexpr int kQBytes = kQTmem ? 0 : kTcRows * D * 2;
     static constexpr int kTileBytes = kAttendTile * D * 2;  // K or V of a tile as BF16 operand
     static constexpr int kRawBytes = kAttendTile * D;       // K or V of a tile as bytes (Q8)
+    static constexpr int kBlocks = D / 64;                  // 128-byte column blocks of an operand row
     // operand rings (filled by TMA, or by the converting warps) and byte rings
-    static constexpr int kOps = Q8 ? 1 : D == 64 ? 4 : 2;
-    static constexpr int kRaws = Q8 ? (D == 64 ? 4 : 2) : 0;
+    static constexpr int kOps = Q8 ? (D == 256 ? 2 : 1) : D == 64 ? 5 : D == 128 ? 6 : 3;
+    static constexpr int kRaws = Q8 ? (D == 64 ? 6 : 2) : 0;
+    // A slot of the ring of facts is written again after the softmax of its tile: the
+    // loader is at most the byte ring, the operand ring and the score buffers ahead.
+    static_assert(kRaws + kOps + kS <= kTcInfo, "the ring of facts");
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + kQBytes;
     static constexpr int kOffV = kOffK + kOps * kTileBytes;
@@ -79,13 +98,14 @@ struct AttendTcCfg {
     static constexpr int kInfoBytes = 528;  // 64 key scales, 64 value scales, the largest key scale
     static constexpr int kOffScale = kOffRawScale + kRaws * 512;  // [kTcInfo][kInfoBytes] (Q8)
     static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * kInfoBytes : 0);
-    static constexpr int kBars = 4 * kOps + 4 * kRaws + 2 + 2 + 2 + 3;
+    static constexpr int kBars = 4 * kOps + 4 * kRaws + 3 * kS + 3;
     static constexpr int kOffInfo = kOffBars + 8 * kBars;
     static constexpr int kOffStats = kOffInfo + 4 * kTcInfo + 32;  // (max, sum) of the 128 rows
     static constexpr int kOffPlaces = kOffStats + 8 * kTcRows;
     static constexpr int kSmemBytes = kOffPlaces + kSoft * (int)sizeof(TcPlace) + 1024;  // 1024: alignment
-    static constexpr int kTmemCols = D == 256 ? 512 : 256;
-    static constexpr int kSCol = D == 256 ? 256 : 128;  // two S buffers of 64 columns; O from column 0
+    // O from column 0, kS score buffers of 64 columns, Q
+    static constexpr int kTmemCols = kOne ? 512 : 256, kSCol = D, kQCol = kSCol + 64 * kS;
+    static_assert(kQCol + (kQTmem ? D / 2 : 0) <= kTmemCols, "TMEM");
 };
 
 // Warp-collective 32-column TMEM load (lane i <- TMEM lane base + i).
@@ -98,6 +118,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
 // 4-D tiled copy global -> shared: column, token in page, head, page.
@@ -145,8 +175,8 @@ __device__ __forceinline__ bool elect_one() {
 // One pipeline barrier's phase by use count.  The parity tells a phase only from
 // its neighbours: who waits for use n knows that use n - 1 is over, and use n + 1
 // cannot be over.  So what is waited for every tile (scores, probabilities,
-// products) has two barriers, one for even and one for odd tiles: the scores of
-// tile g are made after the product of tile g - 2.
+// products) has a barrier per score buffer: the scores of tile g are made after the
+// product of tile g - kS.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t use, uint64_t deadline) {
     return mbar_wait(bar, use & 1u, deadline);
 }
@@ -371,7 +401,7 @@ struct TcLoader {
 };
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q8>::kOne ? 1 : 2)
     w12_kv_attend_tc_kernel(const KvAttendParams p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
     using C = AttendTcCfg<D, Q8>;
@@ -381,8 +411,8 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
     uint64_t *vfull = kempty + C::kOps, *vempty = vfull + C::kOps;
     uint64_t *rkfull = vempty + C::kOps, *rkempty = rkfull + C::kRaws;
     uint64_t *rvfull = rkempty + C::kRaws, *rvempty = rvfull + C::kRaws;
-    uint64_t *sfull = rvempty + C::kRaws, *pfull = sfull + 2;
-    uint64_t *pvdone = pfull + 2, *qfull = pvdone + 2, *ofree = qfull + 1, *drain = ofree + 1;
+    uint64_t *sfull = rvempty + C::kRaws, *pfull = sfull + C::kS;
+    uint64_t *pvdone = pfull + C::kS, *qfull = pvdone + C::kS, *ofree = qfull + 1, *drain = ofree + 1;
     uint32_t *present = reinterpret_cast<uint32_t *>(smem + C::kOffInfo);
     volatile uint32_t *poison = present + kTcInfo;
     uint32_t *tmem_slot = present + kTcInfo + 3;
@@ -402,7 +432,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
             mbar_init(&rvfull[i], 1);
             mbar_init(&rvempty[i], 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kS; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], C::kSoft);
             mbar_init(&pvdone[i], 1);
@@ -457,9 +487,39 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
         TcPlace &place = reinterpret_cast<TcPlace *>(smem + C::kOffPlaces)[warp];
         if (lane == 0) place = TcPlace{w, r, kv_piece(w, r)};
         __syncwarp();
-        // Q rows of a piece to shared memory, rows behind the last one zero
+        // Q rows of a piece to TMEM or shared memory, rows behind the last one zero; for a
+        // Q8 cache in the column order of the converted keys
         auto load_q = [&](const KvRequest &rq, const KvPiece &pc) {
             constexpr int CH = D / 8, STEPS = HALVES * CH / 2, G = STEPS < 8 ? STEPS : 8;  // 16-byte chunks; 32 a step
+            if constexpr (C::kQTmem) {
+                // the lane's row; where a quarter has two warps, half of its columns each
+                const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
+                const int32_t rr = pc.rb * kTcRows + lr, tok = rr / p.group;
+                const uint16_t *src = p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
+                                      (int64_t)(pc.head * p.group + rr - tok * p.group) * D;
+#pragma unroll
+                for (int c0 = 0; c0 < HALVES * D / 4; c0 += 32) {
+                    const int col = half * (D / 4) + c0;
+                    uint32_t x[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (lr < rows) v = __ldg(reinterpret_cast<const uint4 *>(src + 2 * col) + i);
+                        if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
+                            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+                        if (Q8)
+                            v = make_uint4(prmt(v.x, v.y, 0x5410u), prmt(v.x, v.y, 0x7632u), prmt(v.z, v.w, 0x5410u),
+                                           prmt(v.z, v.w, 0x7632u));
+                        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                    }
+                    tmem_st32(tl + C::kQCol + col, x);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfull);
+                return;
+            }
             // where each lane's row is (of 16 or 32); the steps then ask the lanes
             const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
             const int mine = HALVES == 2 ? lr : base + lane % 16;
@@ -483,7 +543,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                     uint4 v = u[g];
                     if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
                         v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-                    if (Q8)  // the column order of the converted keys
+                    if (Q8)
                         v = make_uint4(prmt(v.x, v.y, 0x5410u), prmt(v.x, v.y, 0x7632u), prmt(v.z, v.w, 0x5410u),
                                        prmt(v.z, v.w, 0x7632u));
                     *reinterpret_cast<uint4 *>(smem + C::kOffQ + (ch / 8) * (kTcRows * 128) + row * 128 +
@@ -527,7 +587,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
             for (int j = 0; j < tiles; ++j, ++it, kb += kAttendTile) {
                 // after a timeout the walk goes on without waiting, so that every
                 // barrier below is reached
-                if (ok) ok = tc_wait(&sfull[it & 1], it >> 1, deadline);
+                if (ok) ok = tc_wait(&sfull[it % C::kS], it / C::kS, deadline);
                 ok = __all_sync(~0u, ok);
                 tc_fence_after();
                 const uint32_t here = present[it % kTcInfo];
@@ -542,12 +602,12 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                         const int row = base + 16 * h;
                         if (row >= nrows) break;  // the same for the warp
                         const uint32_t to = tl + ((uint32_t)(16 * (h + half)) << 16);
-                        const uint32_t ts = to + C::kSCol + 64 * (it & 1);
+                        const uint32_t ts = to + C::kSCol + 64 * (it % C::kS);
                         tmem_ld16x64(ts, x[h]);
                         tmem_wait_ld();
                         const auto rescale = [&](float a0, float a1) {
                             if (j == 0) return;  // nothing there yet
-                            if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
+                            if (ok) ok = tc_wait(&pvdone[(it - 1) % C::kS], (it - 1) / C::kS, deadline);
                             ok = __all_sync(~0u, ok);
                             tc_fence_after();
 #pragma unroll 1
@@ -604,7 +664,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[it & 1]);
+                if (lane == 0) mbar_arrive(&pfull[it % C::kS]);
             }
             // the next piece's Q while the last products of this one run (all
             // scores of this piece are there, so nothing reads Q any more)
@@ -624,7 +684,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                     __syncwarp();
                 }
             }
-            if (ok) ok = tc_wait(&pvdone[(it - 1) & 1], (it - 1) >> 1, deadline);
+            if (ok) ok = tc_wait(&pvdone[(it - 1) % C::kS], (it - 1) / C::kS, deadline);
             ok = __all_sync(~0u, ok);
             tc_fence_after();
             // the rows' statistics, summed over a row's four threads, for who puts the
@@ -752,26 +812,34 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
             // took longer than the products (700 cycles for a tile's eight).
             const uint32_t tm = __shfl_sync(~0u, tmem, 0);
             const bool leader = elect_one();
-            uint32_t it = 0, piece = 0;  // tiles whose scores have been issued; pieces
-            // scores of tile `it` into S[it & 1]
-            auto scores = [&](uint32_t issued) -> bool {
-                const uint32_t stage = it % C::kOps;
-                // the buffer's last probabilities (tile it - 2) have been multiplied:
-                // wait for the last product issued so far
-                bool good = issued == 0 || tc_wait(&pvdone[(issued - 1) & 1], (issued - 1) >> 1, deadline);
+            uint32_t it = 0, done = 0, piece = 0;  // tiles whose scores, whose products have been issued; pieces
+            // scores of tile `it` into their buffer, when the product of the tile that had
+            // it before is over
+            auto scores = [&]() -> bool {
+                const uint32_t stage = it % C::kOps, buf = it % C::kS;
+                bool good = it < C::kS || tc_wait(&pvdone[buf], it / C::kS - 1, deadline);
                 good = good && tc_wait(&kfull[stage], it / C::kOps, deadline);
                 if (!__all_sync(~0u, good)) return false;
                 tc_fence_after();
                 if (leader) {
-                    const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
                     const uint64_t b = smem_desc(smem_u32(smem + C::kOffK + stage * C::kTileBytes), 16u, 1024u, 2u);
-                    const uint32_t d = tm + C::kSCol + 64 * (it & 1);
-    #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
-                                   b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk, k > 0);
+                    const uint32_t d = tm + C::kSCol + 64 * buf;
+                    if constexpr (C::kQTmem) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_tmem_a(d, tm + C::kQCol + 8 * k,
+                                       b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk,
+                                       k > 0);
+                    } else {
+                        const uint64_t a = smem_desc(smem_u32(smem + C::kOffQ), 16u, 1024u, 2u);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_smem_a(d, a + (uint64_t)((k >> 2) * (kTcRows * 128 / 16) + (k & 3) * 2),
+                                       b + (uint64_t)((k >> 2) * (kAttendTile * 128 / 16) + (k & 3) * 2), idesc_qk,
+                                       k > 0);
+                    }
                     mma_commit(&kempty[stage]);
-                    mma_commit(&sfull[it & 1]);
+                    mma_commit(&sfull[buf]);
                 }
                 __syncwarp();
                 ++it;
@@ -781,26 +849,29 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                 int n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
                 n = __shfl_sync(~0u, n, 0);
                 if (n == 0) break;
-                ok = __all_sync(~0u, tc_wait(qfull, piece, deadline)) && scores(it);
+                ok = __all_sync(~0u, tc_wait(qfull, piece, deadline));
+                int ahead = 0;  // tiles of the piece whose scores have been issued
                 for (int j = 0; ok && j < n; ++j) {
-                    if (j + 1 < n && !(ok = scores(it - 1))) break;
-                    const uint32_t g = it - (j + 1 < n ? 2 : 1), stage = g % C::kOps;  // the tile to multiply
-                    bool good = tc_wait(&pfull[g & 1], g >> 1, deadline) &&
+                    for (; ok && ahead < n && ahead <= j + C::kAheadS; ++ahead) ok = scores();
+                    if (!ok) break;
+                    const uint32_t g = done, stage = g % C::kOps, buf = g % C::kS;  // the tile to multiply
+                    bool good = tc_wait(&pfull[buf], g / C::kS, deadline) &&
                                 tc_wait(&vfull[stage], g / C::kOps, deadline);
                     if (good && j == 0 && piece > 0) good = tc_wait(ofree, piece - 1, deadline);
                     if (!(ok = __all_sync(~0u, good))) break;
                     tc_fence_after();
                     if (leader) {
-                        const uint32_t a = tm + C::kSCol + 64 * (g & 1);
+                        const uint32_t a = tm + C::kSCol + 64 * buf;
                         const uint64_t b =
                             smem_desc(smem_u32(smem + C::kOffV + stage * C::kTileBytes), kAttendTile * 128, 1024u, 2u);
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < kAttendTile / 16; ++k)
                             mma_tmem_a(tm, a + 8 * k, b + (uint64_t)(k * (16 * 128 / 16)), idesc_pv, j > 0 || k > 0);
                         mma_commit(&vempty[stage]);
-                        mma_commit(&pvdone[g & 1]);
+                        mma_commit(&pvdone[buf]);
                     }
                     __syncwarp();
+                    ++done;
                 }
                 ++piece;
                 if (ok) kv_advance<kTcRows, kAttendTile>(p, w, r, n);
@@ -813,7 +884,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
             __syncwarp();
         } else if (Q8 && warp >= kConvert) {
             // ------------------------------------------------------------ converters of a Q8 cache
-            const int cw = warp - kConvert, ct = cw * 32 + lane;
+            const int cw = (warp - kConvert) & 3, ct = cw * 32 + lane;
             constexpr uint32_t N = C::kRaws + !Q8;
             constexpr int CH = D / 16;  // 16-byte chunks of a row
             // the thread's first chunk and where its two operand chunks go; odd column
@@ -825,11 +896,13 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
             const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
             const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
             const uint32_t total = (uint32_t)(w.end - w.u);
-            // K or V of tile x to its operand buffer, which the tile before must have left
+            // K or V of tile x to its operand buffer, which the tile before it there must have left
             auto convert = [&](bool values, uint32_t x) -> bool {
                 const uint32_t stage = x % N;
                 bool good = tc_wait(values ? &rvfull[stage] : &rkfull[stage], x / N, deadline);
-                if (good && x > 0) good = tc_wait(values ? &vempty[0] : &kempty[0], x - 1, deadline);
+                const uint32_t op = x % C::kOps;
+                if (good && x >= C::kOps)
+                    good = tc_wait(values ? &vempty[op] : &kempty[op], x / C::kOps - 1, deadline);
                 if (!__all_sync(~0u, good)) return false;
                 if (!values && cw < 2) {
                     // scales of the tile's keys, the softmax scale in the keys' ones, and
@@ -841,7 +914,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                         dst[lane] = a;
                         dst[lane + 32] = b;
                         float top = max_nan(fabsf(a), fabsf(b));
-    #pragma unroll
+#pragma unroll
                         for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
                         if (lane == 0) dst[128] = top;
                     } else {
@@ -851,15 +924,15 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                 }
                 const uint4 *src =
                     reinterpret_cast<const uint4 *>(smem + C::kOffRaw + (stage * 2 + values) * C::kRawBytes) + ct;
-                uint8_t *dst = smem + (values ? C::kOffV : C::kOffK);
+                uint8_t *dst = smem + (values ? C::kOffV : C::kOffK) + op * C::kTileBytes;
                 constexpr int N4 = kAttendTile * CH / 128;  // 16-byte chunks of a thread, 128 / CH keys apart
                 constexpr int G = N4 < 4 ? N4 : 4;
-    #pragma unroll
+#pragma unroll
                 for (int i0 = 0; i0 < N4; i0 += G) {
                     uint4 u[G];
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < G; ++i) u[i] = src[(i0 + i) * 128];
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < G; ++i) {
                         uint4 a, b;
                         q8_to_bf16(turn ? u[i].z : u[i].x, a.x, a.y);
@@ -875,17 +948,22 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, D == 256 ? 1 : 2
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(values ? &vfull[0] : &kfull[0]);
+                    mbar_arrive(values ? &vfull[op] : &kfull[op]);
                     mbar_arrive(values ? &rvempty[stage] : &rkempty[stage]);
                 }
                 return true;
             };
-            // the keys run one tile ahead: their buffer is free as soon as the scores
-            // are made, the values' only after the softmax
-            ok = convert(false, 0);
-            for (uint32_t x = 0; ok && x < total; ++x) {
-                if (x + 1 < total) ok = convert(false, x + 1);
-                ok = ok && convert(true, x);
+            if constexpr (C::kGroups == 2) {
+                const bool values = warp >= kConvert + 4;
+                for (uint32_t x = 0; ok && x < total; ++x) ok = convert(values, x);
+            } else {
+                // the keys run one tile ahead: their buffer is free as soon as the scores
+                // are made, the values' only after the softmax
+                ok = convert(false, 0);
+                for (uint32_t x = 0; ok && x < total; ++x) {
+                    if (x + 1 < total) ok = convert(false, x + 1);
+                    ok = ok && convert(true, x);
+                }
             }
             if (!ok && lane == 0) atomicOr(p.status, 8u);
         }
