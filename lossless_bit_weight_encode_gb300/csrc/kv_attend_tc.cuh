@@ -29,7 +29,7 @@
 // products 22.  Taking the softmax's or the conversion's instructions out shortens the
 // Q8 call by 7 % each, both by 26 %: it is bounded by the chain of bytes, operand,
 // scores, weights and product, of which two CTAs per SM overlap two.  30 rows of 64
-// requests of 8000: BF16 320 us, 6.6 TB/s, Q8 344.  72 rows of 256 columns, two of
+// requests of 8000: BF16 320 us, 6.6 TB/s, Q8 337.  72 rows of 256 columns, two of
 // 100001: BF16 128 us, Q8 107.
 #pragma once
 
@@ -56,7 +56,7 @@ struct AttendTcCfg {
     // tile's products read it again (128 columns, BF16: 96 us from TMEM, 102 from shared
     // memory, for the trees above) and where it takes the room of ring slots.  Only the
     // 8-bit cache of 128 columns has no columns left: its two CTAs per SM are worth more
-    // (117 us; one CTA with Q in TMEM 116, but 404 against 366 at 64000 tokens).
+    // (117 us; one CTA with Q in TMEM 116, but 404 against 365 at 64000 tokens).
     static constexpr bool kQTmem = !Q8 || D != 128;
     // One CTA per SM or two (with half of TMEM each).
     static constexpr bool kOne = D == 256 || (D == 128 && kQTmem);
@@ -69,7 +69,7 @@ struct AttendTcCfg {
     // requests of 100001: 127 us with eight, 133 with four; 96 rows of 128, the 8-bit
     // trees: 122 and 116.  Keys and values have a group of converters each where there
     // are threads for it (256 columns, 8-bit: 107 us, 140 with one group and one operand
-    // buffer; 128: 376 against 369 with one, at 64000 tokens).
+    // buffer; 128: 376 against 365 with one, at 64000 tokens).
     static constexpr int kSoft = kOne ? 8 : 4;
     static constexpr int kGroups = !Q8 ? 0 : kOne ? 2 : 1;
     static constexpr int kThreads = 32 * (kSoft + (Q8 ? 4 + 4 * kGroups : kOne ? 4 : 3));
@@ -850,10 +850,10 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 n = __shfl_sync(~0u, n, 0);
                 if (n == 0) break;
                 ok = __all_sync(~0u, tc_wait(qfull, piece, deadline));
-                int ahead = 0;  // tiles of the piece whose scores have been issued
+                // (a loop of its own: with one that catches up at every tile 337 us became 344)
+                for (int j = 0; ok && j < min(n, C::kAheadS); ++j) ok = scores();
                 for (int j = 0; ok && j < n; ++j) {
-                    for (; ok && ahead < n && ahead <= j + C::kAheadS; ++ahead) ok = scores();
-                    if (!ok) break;
+                    if (j + C::kAheadS < n && !(ok = scores())) break;
                     const uint32_t g = done, stage = g % C::kOps, buf = g % C::kS;  // the tile to multiply
                     bool good = tc_wait(&pfull[buf], g / C::kS, deadline) &&
                                 tc_wait(&vfull[stage], g / C::kOps, deadline);

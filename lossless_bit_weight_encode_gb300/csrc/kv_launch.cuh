@@ -57,7 +57,7 @@ constexpr int kKvMaxDevices = 64;
 // Rows of the tile a launch uses: new tokens times query heads per key head.  Up to
 // 8 the warp-level kernel, above 16 the tcgen05 kernel with 128 (more rows take
 // several row blocks).  30 rows measured 326 us against 532 with 32-row warp-level
-// tiles (64 requests of 8000 tokens, BF16; 8-bit 336 against 547), 128 against 133
+// tiles (64 requests of 8000 tokens, BF16; 8-bit 337 against 547), 128 against 133
 // for two requests of 100001.  Between 9 and 16 rows the warp-level kernel is the
 // shorter way for few row blocks (12 rows, one request of 777 tokens: 9.1 against
 // 10.6 us) and for 8-bit caches (64 x 8000: 325 against 340), the tcgen05 kernel for
