@@ -434,26 +434,19 @@ def w12_q8_gemm_group(x_dev, blobs_dev, infos, ys_dev, M: int, workspace, stream
 
 
 # ---------------------------------------------------------------- paged key-value cache
-# The argument structs hold raw pointers (include/w12.h); kv.py fills them from
-# tensors and keeps those alive.
+# The argument structs hold raw pointers (include/w12.h): what they point to has to live
+# until the call's work is done.  kv.py has the calls that take tensors.
 def w12_kv_plan(args: w12_kv_plan_args, stream=None) -> None:
-    rc = (_lib or lib()).w12_kv_plan(args, stream if type(stream) is int else _stream_handle(stream))
-    if rc:
-        _check(rc)
+    _check(lib().w12_kv_plan(args, _stream_handle(stream)))
 
 
 def w12_kv_store(cache: w12_kv_cache, args: w12_kv_store_args, stream=None) -> None:
-    rc = (_lib or lib()).w12_kv_store(cache, args, stream if type(stream) is int else _stream_handle(stream))
-    if rc:
-        _check(rc)
+    _check(lib().w12_kv_store(cache, args, _stream_handle(stream)))
 
 
 def w12_kv_read(cache: w12_kv_cache, slots_ptr: int, tokens: int, k_out_ptr: int, v_out_ptr: int,
                 stream=None) -> None:
-    rc = (_lib or lib()).w12_kv_read(cache, slots_ptr, tokens, k_out_ptr, v_out_ptr,
-                                     stream if type(stream) is int else _stream_handle(stream))
-    if rc:
-        _check(rc)
+    _check(lib().w12_kv_read(cache, slots_ptr, tokens, k_out_ptr, v_out_ptr, _stream_handle(stream)))
 
 
 def w12_kv_attend_workspace_size(cache: w12_kv_cache, args: w12_kv_attend_args) -> int:
@@ -464,10 +457,7 @@ def w12_kv_attend_workspace_size(cache: w12_kv_cache, args: w12_kv_attend_args) 
 
 def w12_kv_attend(cache: w12_kv_cache, args: w12_kv_attend_args, workspace_ptr: int, workspace_bytes: int,
                   stream=None) -> None:
-    rc = (_lib or lib()).w12_kv_attend(cache, args, workspace_ptr, workspace_bytes,
-                                       stream if type(stream) is int else _stream_handle(stream))
-    if rc:
-        _check(rc)
+    _check(lib().w12_kv_attend(cache, args, workspace_ptr, workspace_bytes, _stream_handle(stream)))
 
 
 def w12_read_stream_ptr(buf_ptr: int, nbytes: int, sink_ptr: int, never: int, stream_handle: int | None) -> int:

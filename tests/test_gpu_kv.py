@@ -816,3 +816,39 @@ def test_store_returns_out_by_heads():
     assert cache.store(q, k, k, step, out=three) is three
     fresh = cache.store(q, k, k, step)
     assert fresh.shape == (3, 4, 64) and torch.equal(fresh.view(3, 256), q)
+
+
+def test_calls_by_the_c_names():
+    # pages, store, read and attention by raw pointers, as the holders make them
+    pages = KVPages.create(6, 16, 2, 4)
+    cache = make_cache(6, 2, 16, 64, False)
+    lens, new = dev([0, 0], torch.int32), dev([20, 9], torch.int32)
+    step = pages.step(29, max_new=20)
+    n, t = 2, 29
+    w12.w12_kv_plan(w12.w12_kv_plan_args(
+        lens.data_ptr(), new.data_ptr(), pages.owned.data_ptr(), pages.owned.data_ptr(), pages.tables.data_ptr(), 4,
+        pages.ring.data_ptr(), pages.ring_state.data_ptr(), pages.ring_state.data_ptr(), step.cu_new.data_ptr(),
+        step.positions.data_ptr(), step.slots.data_ptr(), n, 4, 16, 6, t, 0))
+    assert pages.owned.tolist() == [2, 1] and step.cu_new.tolist() == [0, 20, 29]
+    step.lens = lens
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v = (torch.randn(t, h * 64, device="cuda", generator=g).to(torch.bfloat16) for h in (4, 2, 2))
+    c, out = cache._c, torch.empty_like(q)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    w12.w12_kv_store(c, w12.w12_kv_store_args(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 256, 128, 128, 256, None, None, None, None,
+        step.slots.data_ptr(), 0, t, 4, 0, 0, 1e-6), stream)
+    kk, vv = (torch.empty(t, 2, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w12.w12_kv_read(c, step.slots.data_ptr(), t, kk.data_ptr(), vv.data_ptr(), stream)
+    args = w12.w12_kv_attend_args(out.data_ptr(), out.data_ptr(), None, 256, 256, step.tables.data_ptr(), 4,
+                                  lens.data_ptr(), step.cu_new.data_ptr(), None, n, 4, t, 4, 20, 0, 0.125)
+    y = torch.empty_like(q)
+    args.out = y.data_ptr()
+    ws = torch.zeros(w12.w12_kv_attend_workspace_size(c, args), dtype=torch.uint8, device="cuda")
+    stream.wait_stream(torch.cuda.current_stream())
+    w12.w12_kv_attend(c, args, ws.data_ptr(), ws.numel(), stream)
+    torch.cuda.synchronize()
+    status()
+    assert torch.equal(out, q) and torch.equal(kk.view(t, -1), k) and torch.equal(vv.view(t, -1), v)
+    assert torch.equal(y, cache.attend(out, step))
