@@ -325,8 +325,8 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     expect(n, 9);
     const int64_t index = integer(a[1]);
-    const Ref tables_o = field(a[0], names.tables), owned_o = field(a[0], names.owned), ring_o = field(a[0], names.ring),
-              state_o = field(a[0], names.ring_state), page_o = field(a[0], names.page_size),
+    const Ref tables_o = field(a[0], names.tables), owned_o = field(a[0], names.owned),
+              ring_o = field(a[0], names.ring), state_o = field(a[0], names.ring_state), page_o = field(a[0], names.page_size),
               cu_o = field(a[4], names.cu_new), positions_o = field(a[4], names.positions),
               slots_o = field(a[4], names.slots);
     const at::Tensor &tables = tensor(tables_o.get(), "tables"), &owned = tensor(owned_o.get(), "owned"),
