@@ -286,6 +286,12 @@ __device__ __forceinline__ bool kv_sees(const KvAttendParams &p, const KvRequest
     return s && (p.window <= 0 || key > v.index - p.window);
 }
 
+// What parts are scaled to when the largest of their maxima is m: a part with maximum
+// m_i counts 2^(m_i - base), 0 where m_i = -infinity.  Such a part saw nothing and has
+// sum and output 0, or its scores are all NaN and so are they (the maximum passes over
+// NaN): it is multiplied and added like any other, so that the NaN stays (0 * NaN).
+__device__ __forceinline__ float kv_part_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
 // Row lr of a piece: out = acc / sum (four columns from col on) and, with the
 // first of them, lse.
 template <int ROWS, int D>
@@ -374,16 +380,16 @@ __device__ __forceinline__ void kv_join(const KvAttendParams &p, const KvParts &
                 float mn = mm[u];
 #pragma unroll
                 for (int k = 0; k < P; ++k) mn = fmaxf(mn, s[u][k].x);
-                const float f0 = mm[u] == -INFINITY ? 0.0f : ex2(mm[u] - mn);
+                const float base = kv_part_base(mn), f0 = ex2(mm[u] - base);
                 mm[u] = mn;
                 sum[u] *= f0;
                 acc[u].x *= f0, acc[u].y *= f0, acc[u].z *= f0, acc[u].w *= f0;
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    const float g = k0 + k < q.n && s[u][k].x != -INFINITY ? ex2(s[u][k].x - mn) : 0.0f;
-                    // a part that does not count (g = 0) may hold anything
-                    const float4 v = g == 0.0f ? make_float4(0.f, 0.f, 0.f, 0.f) : y[u][k];
-                    sum[u] = g == 0.0f ? sum[u] : fmaf(g, s[u][k].y, sum[u]);
+                    if (k0 + k >= q.n) continue;
+                    const float g = ex2(s[u][k].x - base);
+                    const float4 v = y[u][k];
+                    sum[u] = fmaf(g, s[u][k].y, sum[u]);
                     acc[u].x = fmaf(g, v.x, acc[u].x), acc[u].y = fmaf(g, v.y, acc[u].y);
                     acc[u].z = fmaf(g, v.z, acc[u].z), acc[u].w = fmaf(g, v.w, acc[u].w);
                 }
@@ -873,12 +879,13 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
                 float mm = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < WK; ++k) mm = fmaxf(mm, ml[k * ROWS + lr].x);
+                const float base = kv_part_base(mm);
                 float sum = 0.0f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < WK; ++k) {
                     const float2 s = ml[k * ROWS + lr];
-                    const float f = s.x == -INFINITY ? 0.0f : ex2(s.x - mm);
+                    const float f = ex2(s.x - base);
                     const float4 y =
                         *reinterpret_cast<const float4 *>(merge + (k * ROWS + lr) * C::kMergeStride + v4 * 4);
                     sum += f * s.y;
@@ -995,16 +1002,15 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
         float mn = mm;
 #pragma unroll
         for (int u = 0; u < U; ++u) mn = fmaxf(mn, s[u].x);
-        const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
+        const float base = kv_part_base(mn), f0 = ex2(mm - base);
         mm = mn;
         sum *= f0;
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] *= f0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // a part that does not count may hold anything
-            if (k0 + u * WPR < q.n && s[u].x != -INFINITY) {
-                const float g = ex2(s[u].x - mn);
+            if (k0 + u * WPR < q.n) {
+                const float g = ex2(s[u].x - base);
                 sum = fmaf(g, s[u].y, sum);
 #pragma unroll
                 for (int e = 0; e < V; ++e) acc[e] = fmaf(g, y[u][e], acc[e]);
@@ -1023,9 +1029,10 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
         for (int e = 0; e < V; ++e) acc[e] = 0.0f;
 #pragma unroll
         for (int k = 0; k < W; ++k) mm = fmaxf(mm, s_ml[k].x);
+        const float base = kv_part_base(mm);
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-            const float f = s_ml[k].x == -INFINITY ? 0.0f : ex2(s_ml[k].x - mm);
+            const float f = ex2(s_ml[k].x - base);
             sum += f * s_ml[k].y;
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] += f * s_acc[k][lane * V + e];
