@@ -365,19 +365,36 @@ uint64_t timeout_ns() { return (uint64_t)opt(kOptTimeout) * 1000000ull; }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+template <class F>
+F driver_entry(const char *name) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool found = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess;
+    return found ? reinterpret_cast<F>(p) : nullptr;
+}
+
+// The encoder is a driver call, which takes the calling thread's context as it is.  A
+// thread whose first CUDA call this is has none yet (the runtime binds the device's on
+// its own calls, of which those before this one need none): it gets it here.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder(std::string *err) {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    if (!fn) *err = "cuTensorMapEncodeTiled is not available from the driver";
-    return fn;
+    static const auto encode = driver_entry<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled");
+    static const auto current = driver_entry<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent");
+    if (!encode || !current) {
+        *err = "cuTensorMapEncodeTiled is not available from the driver";
+        return nullptr;
+    }
+    CUcontext context = nullptr;
+    if (current(&context) != CUDA_SUCCESS || !context) {
+        int device = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e == cudaSuccess) e = cudaSetDevice(device);
+        if (e != cudaSuccess) {
+            *err = std::string("cudaSetDevice: ") + cudaGetErrorString(e);
+            return nullptr;
+        }
+    }
+    return encode;
 }
 
 }  // namespace
