@@ -486,7 +486,9 @@ int w12_kv_read(const w12_kv_cache *cache, const int64_t *slots, int32_t tokens,
  * workspace: at least w12_kv_attend_workspace_size bytes, 256-byte aligned,
  * ZERO-FILLED BEFORE ITS FIRST USE; every successful call leaves its counters
  * zero again (after a TIMEOUT, zero it again).  Calls of any shape may share a
- * workspace that is large enough for each, if they are ordered on the GPU.
+ * workspace that is large enough for each, if they are ordered on the GPU.  Host
+ * threads may make such calls at the same time on one stream: a call's launches
+ * follow one another.
  */
 typedef struct w12_kv_attend_args {
     const uint16_t *q;

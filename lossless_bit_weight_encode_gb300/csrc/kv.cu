@@ -53,6 +53,16 @@ cudaError_t read_dim(const DeviceView &d, bool q8, int grid, const dev::KvReadPa
     return kv_launch(d, kernel, dim3((unsigned)grid), dev::kReadThreads, 0, 1, st, p);
 }
 
+// Held over the launches of an attend call: the joining kernel reads what the attention
+// kernel before it left in the workspace, so nothing of another host thread's call with
+// the same workspace may come between the two.  One lock for a few workspaces (by
+// address), so that threads with workspaces of their own seldom meet.
+std::mutex &workspace_lock(const void *workspace) {
+    static std::mutex locks[64];
+    const uint64_t at = reinterpret_cast<uintptr_t>(workspace) >> 8;
+    return locks[(at ^ at >> 6 ^ at >> 12) % 64];
+}
+
 int attend_call(const DeviceView &d, const w12_kv_cache &c, int rows, int *resident, const dev::KvAttendParams *p,
                 const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     const bool q8 = c.dtype == W12_KV_Q8;
@@ -307,6 +317,7 @@ int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspac
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     int resident = 0;
+    const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
     return attend_call(d, c, plan.rows, &resident, &p, &tm_k, &tm_v, plan.ctas, stream, err);
 }
 

@@ -255,7 +255,7 @@ class KVCache:
         (their own included).  ``scale`` defaults to head_dim ** -0.5; ``window``
         > 0: a token sees only that many last tokens, itself included.  ``lse``
         (fp32 [tokens, heads]) receives the log of the softmax sums.  Calls on one
-        stream share a workspace; ``workspace`` (uint8, zero-filled before its
+        stream (of several threads too) share a workspace; ``workspace`` (uint8, zero-filled before its
         first use) takes its place, as a captured graph needs that is replayed
         beside other calls."""
         if stream is not None or _current_device() != self._index:
