@@ -410,7 +410,7 @@ struct KvPageWindow {
     const int32_t *row;
     int32_t base, last, cur, next;
 
-    __device__ __forceinline__ int32_t load(int32_t e) const { return e <= last ? __ldg(row + e) : -1; }
+    __device__ __forceinline__ int32_t load(int32_t e) const { return e <= last ? row[e] : -1; }
     // entries `first` to `end` - 1 will be asked for, in order
     __device__ __forceinline__ void start(const int32_t *table_row, int32_t first, int32_t end) {
         row = table_row;

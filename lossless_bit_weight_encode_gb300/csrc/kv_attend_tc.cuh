@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         uint4 v = make_uint4(0, 0, 0, 0);
-                        if (lr < rows) v = __ldg(reinterpret_cast<const uint4 *>(src + 2 * col) + i);
+                        if (lr < rows) v = reinterpret_cast<const uint4 *>(src + 2 * col)[i];
                         if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
                             v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
                         if (Q8)
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                     const int i = (s0 + g) * 32 + lane;
                     const int64_t at = __shfl_sync(~0u, src, i / CH);
                     u[g] = make_uint4(0, 0, 0, 0);
-                    if (at >= 0) u[g] = __ldg(reinterpret_cast<const uint4 *>(p.q + at) + i % CH);
+                    if (at >= 0) u[g] = reinterpret_cast<const uint4 *>(p.q + at)[i % CH];
                 }
 #pragma unroll
                 for (int g = 0; g < G; ++g) {

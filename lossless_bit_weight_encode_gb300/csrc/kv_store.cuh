@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kStoreThreads, 16) w12_kv_store_kernel(KvStore
                 if (!is_v) {
                     const uint16_t *wp = is_q ? p.q_norm : p.k_norm;
                     uint4 w = make_uint4(0, 0, 0, 0);
-                    if (wp) w = __ldg(reinterpret_cast<const uint4 *>(wp) + sub);
+                    if (wp) w = reinterpret_cast<const uint4 *>(wp)[sub];
                     norm_rotate<D, INTERLEAVED>(x, wp != nullptr, w, p.eps, p.rot, cs, sn, sub);
                 }
                 if (is_q) {
