@@ -162,19 +162,12 @@ struct KvRequest {
     int64_t units;
 };
 
-// A length or offset.  L2: past the L1, for w12_kv_join_kernel, which reads them before
-// it has waited for the kernels before it (see there).
-template <bool L2>
-__device__ __forceinline__ int32_t kv_length(const int32_t *at) {
-    return L2 ? __ldcg(at) : *at;
-}
-
-template <int ROWS, int TILE, bool L2 = false>
+template <int ROWS, int TILE>
 __device__ __forceinline__ KvRequest kv_request(const KvAttendParams &p, int b) {
     KvRequest r;
-    r.q0 = min(max(kv_length<L2>(p.cu_new + b), 0), p.tokens);
-    r.qlen = min(max(kv_length<L2>(p.cu_new + b + 1), r.q0), p.tokens) - r.q0;
-    r.past = min(max(kv_length<L2>(p.lens + b), 0), p.max_keys);
+    r.q0 = min(max(p.cu_new[b], 0), p.tokens);
+    r.qlen = min(max(p.cu_new[b + 1], r.q0), p.tokens) - r.q0;
+    r.past = min(max(p.lens[b], 0), p.max_keys);
     r.kv = (int32_t)min((int64_t)r.past + r.qlen, (int64_t)p.max_keys);
     // first key that any of the request's new tokens sees
     r.first = p.window > 0 ? (int32_t)max((int64_t)r.past + 1 - p.window, (int64_t)0) : 0;
@@ -199,7 +192,7 @@ struct KvSums {
     int32_t per;            // requests of a block
 };
 
-template <int ROWS, int TILE, bool L2 = false>
+template <int ROWS, int TILE>
 __device__ __forceinline__ KvSums kv_sum_units(const KvAttendParams &p) {
     const int lane = threadIdx.x & 31;
     KvSums s;
@@ -208,7 +201,7 @@ __device__ __forceinline__ KvSums kv_sum_units(const KvAttendParams &p) {
 #pragma unroll 4
     for (int i = 0; i < s.per; ++i) {
         const int b = lane * s.per + i;
-        if (b < p.requests) sum += kv_request<ROWS, TILE, L2>(p, b).units;
+        if (b < p.requests) sum += kv_request<ROWS, TILE>(p, b).units;
     }
     int64_t inc = sum;
 #pragma unroll
@@ -939,10 +932,8 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
     const int64_t out_row = (int64_t)blockIdx.x * (W / WPR) + warp / WPR;
     const int32_t tok = (int32_t)(out_row / heads), h = (int32_t)(out_row - (int64_t)tok * heads);
     // Lengths and offsets come from before the attention kernel, which lets this one
-    // start only when it has itself seen all that is before it.  They are read from L2,
-    // where they are then: this kernel has not waited yet, so a line that its SM's L1
-    // still has of older ones need not have been dropped.
-    const KvSums sums = kv_sum_units<ROWS, TILE, true>(p);
+    // start only when it has itself seen all that is before it.
+    const KvSums sums = kv_sum_units<ROWS, TILE>(p);
     const int64_t total = sums.total;
     // the token's request: the block that has it, then the request in it
     int64_t start = -1;
@@ -950,14 +941,14 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
     int32_t b = 0;
     {
         const int first = lane * sums.per, end = min(first + sums.per, p.requests);
-        const bool mine = first < p.requests && tok >= min(max(kv_length<true>(p.cu_new + first), 0), p.tokens) &&
-                          tok < min(max(kv_length<true>(p.cu_new + end), 0), p.tokens);
+        const bool mine = first < p.requests && tok >= min(max(p.cu_new[first], 0), p.tokens) &&
+                          tok < min(max(p.cu_new[end], 0), p.tokens);
         const uint32_t hit = __ballot_sync(~0u, mine);
         if (hit) {
             const int src = __ffs(hit) - 1;
             int64_t at = __shfl_sync(~0u, sums.before, src);
             for (b = src * sums.per; b < min((src + 1) * sums.per, p.requests); ++b) {
-                r = kv_request<ROWS, TILE, true>(p, b);
+                r = kv_request<ROWS, TILE>(p, b);
                 if (tok >= r.q0 && tok < r.q0 + r.qlen) {
                     start = at;
                     break;
