@@ -932,7 +932,11 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
     const int64_t out_row = (int64_t)blockIdx.x * (W / WPR) + warp / WPR;
     const int32_t tok = (int32_t)(out_row / heads), h = (int32_t)(out_row - (int64_t)tok * heads);
     // Lengths and offsets come from before the attention kernel, which lets this one
-    // start only when it has itself seen all that is before it.
+    // start only when it has itself seen all that is before it.  This kernel has not
+    // waited yet, though: the fence keeps its loads from lines that the SM's L1 has had
+    // since before they were written.  (With loads from L2 instead, the sum over 128
+    // requests in every row's warp took 117 us to 199, three tokens on windows.)
+    __threadfence();
     const KvSums sums = kv_sum_units<ROWS, TILE>(p);
     const int64_t total = sums.total;
     // the token's request: the block that has it, then the request in it

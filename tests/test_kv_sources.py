@@ -19,3 +19,15 @@ def test_no_non_coherent_loads(name):
         text = f.read()
     hits = [m.group(0) for m in re.finditer(r"__ldg\b|\.global\.nc\b|const\s+\w+\s*\*\s*__restrict__", text)]
     assert not hits, f"{name}: {hits}"
+
+
+def test_joining_kernel_fences_what_it_reads_before_it_waits():
+    """Lengths and offsets alone, and those behind a fence: nothing else orders its loads
+    with the writes of kernels that ended before it began."""
+    with open(os.path.join(CSRC, "kv_attend.cuh")) as f:
+        text = f.read()
+    start = text.index("w12_kv_join_kernel(const KvAttendParams p, int grid)")
+    ahead = text[start:text.index("pdl_wait();", start)]
+    loads = [m.start() for m in re.finditer(r"p\.(cu_new|lens)\[|kv_request<|kv_sum_units<", ahead)]
+    assert loads and "__threadfence();" in ahead[:min(loads)]
+    assert not re.search(r"p\.(tables|tree|q|part|part_ml)\s*\[", ahead)
