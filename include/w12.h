@@ -472,7 +472,13 @@ int w12_kv_read(const w12_kv_cache *cache, const int64_t *slots, int32_t tokens,
  *   - without tree: j <= lens[b] + i;
  *   - with tree (uint32 per token): j < lens[b], or bit j - lens[b] of tree[t] is
  *     set (new tokens from the 33rd on are then seen by none);
- *   - with window > 0: also j > lens[b] + i - window.
+ *   - with window > 0: also j > lens[b] + i - window.  With a tree and positions
+ *     (int32 per token; NULL: the numbers above) tokens are placed by them
+ *     instead: a drafted token's place is the cached length plus its depth, which
+ *     in a branching tree is less than its number.  Token i has place positions[t],
+ *     at least lens[b] and at most lens[b] + i (others count as the nearest); a
+ *     cached key's place is j; keys at places above the token's minus window are
+ *     seen.
  * out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j over the keys seen, of
  * key head h / (heads / kv_heads); lse[t][h] (NULL: not written) = ln sum_j
  * exp(scale * q . k_j).  A token that sees nothing gets out 0 and lse
@@ -501,6 +507,7 @@ typedef struct w12_kv_attend_args {
     const uint32_t *tree;
     int32_t requests, max_blocks, tokens, heads, max_new, window;
     float scale;
+    const int32_t *positions;
 } w12_kv_attend_args;
 
 int w12_kv_attend_workspace_size(const w12_kv_cache *cache, const w12_kv_attend_args *args, size_t *bytes);

@@ -700,7 +700,8 @@ int w12_kv_attend(const w12_kv_cache *cache, const w12_kv_attend_args *args, voi
         }
         if (args->q_stride % 8 != 0 || args->out_stride % 8 != 0 || !aligned(args->q, 16) || !aligned(args->out, 16) ||
             !aligned(workspace, 256) || !aligned(args->lse, 4) || !aligned(args->tables, 4) ||
-            !aligned(args->lens, 4) || !aligned(args->cu_new, 4) || !aligned(args->tree, 4)) {
+            !aligned(args->lens, 4) || !aligned(args->cu_new, 4) || !aligned(args->tree, 4) ||
+            !aligned(args->positions, 4)) {
             err = "q and out must be 16-byte aligned with strides of a multiple of 8, workspace 256-byte, the 32-bit "
                   "arrays 4-byte aligned";
             return (int)W12_ERR_ALIGNMENT;

@@ -295,6 +295,7 @@ int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspac
     p.lens = a.lens;
     p.cu_new = a.cu_new;
     p.tree = a.tree;
+    p.positions = a.tree && a.window > 0 ? a.positions : nullptr;
     p.v = static_cast<const uint16_t *>(c.v_dev);
     p.v_page_stride = c.page_stride;
     p.v_head_stride = c.head_stride;

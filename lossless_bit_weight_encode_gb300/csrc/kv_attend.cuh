@@ -267,12 +267,36 @@ __device__ __forceinline__ void kv_advance(const KvAttendParams &p, KvWalk &w, K
 
 // Which keys of a slice one row sees.
 struct KvRowView {
-    int32_t index;  // of the row's token in the request: past + i
+    int32_t index;  // of the row's token in the request: past + i; in a windowed tree its position
     uint32_t tree;
 };
 
 __device__ __forceinline__ int32_t kv_index(const KvRequest &r, int32_t i) {
     return (int32_t)min((int64_t)r.past + i, (int64_t)0x7FFFFFFF);
+}
+
+// The view of new token i.  PLACED: a windowed tree with positions.  There a token's
+// position lies between past and its number past + i, so that what bounds the tiles for
+// numbers bounds them too.  New tokens that the window leaves out by position are taken
+// out of the mask; those that stay have numbers at or above their positions, so they pass
+// the comparison of key numbers that the cached keys need.
+template <bool PLACED>
+__device__ __forceinline__ KvRowView kv_row_view(const KvAttendParams &p, const KvRequest &r, int32_t i) {
+    KvRowView v;
+    v.index = kv_index(r, i);
+    v.tree = p.tree ? p.tree[r.q0 + i] : 0u;
+    if (PLACED) {
+        const int32_t *at = p.positions + r.q0;
+        v.index = min(max(at[i], r.past), v.index);
+        if (v.index - r.past >= p.window) {  // deeper than the window is long
+            for (uint32_t left = v.tree; left; left &= left - 1) {
+                const int32_t j = __ffs((int)left) - 1;
+                if (j >= r.qlen) break;  // no such token: never seen
+                if (min(max(at[j], r.past), kv_index(r, j)) <= v.index - p.window) v.tree &= ~(1u << j);
+            }
+        }
+    }
+    return v;
 }
 
 __device__ __forceinline__ bool kv_sees(const KvAttendParams &p, const KvRequest &r, const KvRowView &v, int32_t key) {
@@ -649,9 +673,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
                         for (int e = 0; e < 2; ++e) {
                             const int32_t lr = (wr * NT + nt) * 8 + 2 * t + e;
                             const int32_t i = min(row0 + lr, row0 + nrows - 1) / p.group;
-                            KvRowView v;
-                            v.index = kv_index(r, i);
-                            v.tree = p.tree ? p.tree[r.q0 + i] : 0u;
+                            const KvRowView v = p.positions ? kv_row_view<true>(p, r, i) : kv_row_view<false>(p, r, i);
 #pragma unroll
                             for (int u = 0; u < PAIR; ++u) {
                                 const int32_t key = kb + u * WK * kAttendSlice + g;

@@ -400,7 +400,10 @@ struct TcLoader {
     }
 };
 
-template <int D, bool Q8>
+// PLACED (a windowed tree with positions) is a kernel of its own: with the choice at run
+// time the tile loop's registers went another way (trees over an 8-bit cache 116 us, 144
+// with the positions looked up in the loop, 118 with nothing but their load there).
+template <int D, bool Q8, bool PLACED>
 __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q8>::kOne ? 1 : 2)
     w12_kv_attend_tc_kernel(const KvAttendParams p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
@@ -574,10 +577,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             // the keys of the tile at kb that row `row` of the block sees
             const auto seen_by = [&](int row, uint32_t here) -> uint64_t {
                 const int32_t tok = min(row0 + row, row0 + nrows - 1) / p.group;
-                KvRowView v;
-                v.index = kv_index(place.r, tok);
-                v.tree = p.tree ? p.tree[place.r.q0 + tok] : 0u;
-                return kv_seen64(p, keys, past, v, kb, here) >> (2 * t4);
+                return kv_seen64(p, keys, past, kv_row_view<PLACED>(p, place.r, tok), kb, here) >> (2 * t4);
             };
             const bool busy = base < nrows;  // a warp without rows only keeps step
             // rows g and g + 8 of each half, as tc_softmax has them
@@ -730,10 +730,8 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                         // through the product already stays what it is)
                         for (int j = c1.ja; j < c1.jb; ++j) {
                             const int32_t kb = (r1.tile0 + j) * kAttendTile;
-                            KvRowView view;
-                            view.index = kv_index(r1, i);
-                            view.tree = p.tree ? p.tree[r1.q0 + i] : 0u;
-                            uint64_t seen = kv_seen64(p, r1.kv, r1.past, view, kb, 15u);
+                            uint64_t seen =
+                                kv_seen64(p, r1.kv, r1.past, kv_row_view<PLACED>(p, r1, i), kb, 15u);
                             for (; seen; seen &= seen - 1) {
                                 const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
                                 const int32_t page = p.tables[(int64_t)w1.b * p.table_stride + e];

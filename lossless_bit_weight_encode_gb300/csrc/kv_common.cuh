@@ -71,6 +71,7 @@ struct KvAttendParams {
     int64_t table_stride;
     const int32_t *lens, *cu_new;
     const uint32_t *tree;
+    const int32_t *positions;  // of a windowed tree's tokens; null: their numbers place them
     const uint16_t *v;  // a BF16 cache's values, and their strides in elements
     int64_t v_page_stride, v_head_stride, v_row_stride;
     const float *scales;

@@ -263,7 +263,8 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor &qt = tensor(a[2], "q");
     const Rows q = rows(qt, dim, "q", index, 0);
     const Ref tables_o = field(a[3], names.tables), lens_o = field(a[3], names.lens), cu_o = field(a[3], names.cu_new),
-              tree_o = field(a[3], names.tree), new_o = field(a[3], names.max_new);
+              tree_o = field(a[3], names.tree), new_o = field(a[3], names.max_new),
+              positions_o = field(a[3], names.positions);
     const at::Tensor &tables = tensor(tables_o.get(), "step.tables"), &lens = tensor(lens_o.get(), "step.lens"),
                      &cu = tensor(cu_o.get(), "step.cu_new");
     const int64_t requests = lens.numel();
@@ -287,6 +288,11 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &tree = tensor(tree_o.get(), "step.tree");
         TORCH_CHECK_VALUE(tree.numel() >= q.tokens, "step.tree must have a mask per token");
         s.tree = reinterpret_cast<const uint32_t *>(ints<int32_t>(tree, "step.tree", index));
+        if (s.window > 0 && positions_o.get() != Py_None) {
+            const at::Tensor &positions = tensor(positions_o.get(), "step.positions");
+            TORCH_CHECK_VALUE(positions.numel() >= q.tokens, "step.positions must have an entry per token");
+            s.positions = ints<int32_t>(positions, "step.positions", index);
+        }
     }
     if (a[7] != Py_None) {
         const at::Tensor &lse = tensor(a[7], "lse");

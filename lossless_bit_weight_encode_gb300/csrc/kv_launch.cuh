@@ -172,13 +172,13 @@ int attend_variant(const DeviceView &d, int *resident, const dev::KvAttendParams
                          dev::kAttendThreads, 0, C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool PLACED>
 int attend_tc_variant(const DeviceView &d, int *resident, const dev::KvAttendParams *p, const CUtensorMap *tm_k,
                       const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     using C = dev::AttendTcCfg<D, Q8>;
     static std::mutex mu;
     static int per_sm[kKvMaxDevices] = {};
-    return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8>,
+    return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8, PLACED>,
                          std::min(kPartElems / (dev::kTcRows * D), 512 / C::kTmemCols), C::kThreads, C::kRegs,
                          C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
@@ -194,7 +194,9 @@ int attend_rows_variant(const DeviceView &d, int rows, int *resident, const dev:
     case 16:
         return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(d, resident, p, tm_k, tm_v,
                                                                                           ctas, stream, err);
-    default: return attend_tc_variant<D, Q8>(d, resident, p, tm_k, tm_v, ctas, stream, err);
+    default:
+        return p && p->positions ? attend_tc_variant<D, Q8, true>(d, resident, p, tm_k, tm_v, ctas, stream, err)
+                                 : attend_tc_variant<D, Q8, false>(d, resident, p, tm_k, tm_v, ctas, stream, err);
     }
 }
 

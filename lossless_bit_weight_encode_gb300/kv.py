@@ -112,7 +112,10 @@ class KVStep:
     tokens ``cu_new[b] : cu_new[b + 1]``; for every new token its ``position``
     and cache slot (-1: none).  ``tables`` [requests, max_blocks] holds the
     requests' pages.  ``tree`` (int32, bit j of a token's mask: it attends to new
-    token j of its request) replaces the causal order among new tokens.
+    token j of its request) replaces the causal order among new tokens.  ``plan``
+    numbers a request's new tokens one after the other; for a tree, write cached
+    length + depth over ``positions`` before the store (rotation) and the attention
+    (windows).
     ``max_new``: the most new tokens of a request, as far as is known.  What a
     call does not use may be None."""
 
@@ -253,7 +256,8 @@ class KVCache:
     def attend(self, q, step, scale=None, window=0, out=None, lse=None, workspace=None, stream=None):
         """Attention of the step's new tokens over their requests' cached ones
         (their own included).  ``scale`` defaults to head_dim ** -0.5; ``window``
-        > 0: a token sees only that many last tokens, itself included.  ``lse``
+        > 0: a token sees only that many last tokens, itself included (in a tree,
+        by step.positions; where those are None, by the tokens' order).  ``lse``
         (fp32 [tokens, heads]) receives the log of the softmax sums.  Calls on one
         stream (of several threads too) share a workspace; ``workspace`` (uint8, zero-filled before its
         first use) takes its place, as a captured graph needs that is replayed

@@ -107,7 +107,7 @@ class w12_kv_attend_args(ctypes.Structure):
         ("lens", ctypes.c_void_p), ("cu_new", ctypes.c_void_p), ("tree", ctypes.c_void_p),
         ("requests", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("tokens", ctypes.c_int32),
         ("heads", ctypes.c_int32), ("max_new", ctypes.c_int32), ("window", ctypes.c_int32),
-        ("scale", ctypes.c_float),
+        ("scale", ctypes.c_float), ("positions", ctypes.c_void_p),
     ]
 
 

@@ -114,3 +114,7 @@ def test_read_refused():
     assert L.w12_kv_read(cache(), A, -1, A, A, None) == INVALID
     assert L.w12_kv_read(cache(), A, 1, A, A + 8, None) == ALIGN
     assert L.w12_kv_read(cache(), A + 4, 1, A, A, None) == ALIGN
+
+
+def test_attend_positions_refused():
+    assert w12.lib().w12_kv_attend(cache(), attend(tree=A, window=4, positions=A + 2), A, 1 << 30, None) == ALIGN
