@@ -393,8 +393,13 @@ typedef struct w12_kv_cache {
  *   - the need - owned_in missing pages come from the ring of free pages, in
  *     request order: ring[(head + a) % ring_size], a = 0, 1, ...
  *   - with trim, the owned_in - need pages too many go back behind its tail, in
- *     request and table order (their table entries stay as they are).
- * ring_state_in = {head, tail}: ring[i % ring_size] is free for head <= i < tail.
+ *     request and table order (their table entries stay as they are).  The ring
+ *     has room for ring_size - (tail - head) of them in a call; where they are
+ *     more, a request keeps the first of its pages too many (owned_out counts
+ *     them) and w12_check_status returns BUFFER_TOO_SMALL.  A ring of as many
+ *     entries as there are pages has room for all.
+ * ring_state_in = {head, tail}: ring[i % ring_size] is free for head <= i < tail,
+ * head >= 0 and 0 <= tail - head <= ring_size (else BUFFER_TOO_SMALL too).
  * Pages given back in a step can be taken in the next one.
  * Out: owned_out, ring_state_out (either may be its own input: in place),
  * tables and ring (in place); cu_new[requests + 1], the prefix sum of new_lens;

@@ -843,7 +843,7 @@ int check_status(void *stream, std::string *err) {
             return W12_ERR_BUFFER_TOO_SMALL;
         }
         if (v & dev::kStatusKvPages) {
-            *err = "w12_kv_plan: the ring of free pages ran out" + word;
+            *err = "w12_kv_plan: the ring of free pages ran out, or had no room for pages given back" + word;
             return W12_ERR_BUFFER_TOO_SMALL;
         }
         if (v & dev::kStatusKvIndex) {

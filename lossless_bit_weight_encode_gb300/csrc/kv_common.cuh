@@ -7,7 +7,7 @@ namespace w12 {
 namespace dev {
 
 // Status word bits of the paged-cache calls (w12_check_status).
-constexpr uint32_t kStatusKvPages = 64u;   // the ring of free pages ran out
+constexpr uint32_t kStatusKvPages = 64u;   // the ring of free pages ran out, or was full
 constexpr uint32_t kStatusKvSizes = 128u;  // a length or the token count had to be clamped
 constexpr uint32_t kStatusKvIndex = 256u;  // a slot or position outside its table
 

@@ -16,7 +16,8 @@
 // barrier is what allows owned and the ring state to be updated in place.  No
 // CTA reads what another writes: a taken page is read from the ring, never from
 // the table entry it goes to, and the ring positions given back are not those
-// taken (at most ring_size pages are free).
+// taken (only as many go back as entries of the ring were not free at the start; the
+// pages without room stay where they are, the last of each request going back first).
 #pragma once
 
 #include "kv_common.cuh"
@@ -87,13 +88,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
     pdl_launch_dependents();
     pdl_wait();
     const int64_t head = p.state_in[0], tail = p.state_in[1];
-    const int32_t avail = clamp_i32(tail - head, 0, p.ring_size);
+    const int32_t avail = clamp_i32(tail - head, 0, p.ring_size), room = p.ring_size - avail;
     const int32_t head_at = ring_base(head, p.ring_size, p.ring_inv);
     const int32_t tail_at = ring_base(tail, p.ring_size, p.ring_inv);
     const int32_t cap = p.max_blocks * p.page_size;
     int64_t tok0 = 0;
     int32_t grow0 = 0, drop0 = 0;  // totals of the chunks before
-    uint32_t flags = 0;
+    uint32_t flags = tail - head != avail ? kStatusKvPages : 0;
     for (int base = 0; base < p.requests; base += kPlanThreads) {
         const int n = min(kPlanThreads, p.requests - base);
         int32_t len = 0, add = 0, owned = 0, need = 0;
@@ -138,13 +139,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
         s_owned[tid] = owned;
         s_need[tid] = need;
         const int32_t given = min(grow, max(avail - (grow0 + b - grow), 0));
-        if (given < grow) flags |= kStatusKvPages;
+        const int32_t back = min(drop, max(room - (drop0 + c - drop), 0));
+        if (given < grow || back < drop) flags |= kStatusKvPages;
         // every CTA has read its inputs of this chunk before any output of it
         // is written (owned_out may be owned_in)
         if (ranks > 1) cluster_sync();
         else __syncthreads();
         if (rank == 0 && tid < n) {
-            p.owned_out[base + tid] = owned + given - drop;
+            p.owned_out[base + tid] = owned + given - back;
             if (base + tid == 0) p.cu_new[0] = 0;
             p.cu_new[base + tid + 1] = (int32_t)min(tok0 + a, (int64_t)0x7FFFFFFF);
         }
@@ -171,10 +173,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
             p.tables[(int64_t)(base + r) * p.table_stride + j] =
                 g < avail ? p.ring[ring_at(head_at, g, p.ring_size)] : -1;
         }
-        for (int32_t i = first; i < drop_n; i += step) {
+        const int32_t back_n = min(drop_n, max(room - drop0, 0));
+        for (int32_t i = first; i < back_n; i += step) {
             const int32_t g = drop0 + i;
             const int r = find_start(s_drop, n, g);
-            const int32_t j = s_need[r] + g - s_drop[r];
+            // the last min(drop, room left) of the request's pages, in table order
+            const int32_t left = room - s_drop[r], j = max(s_need[r], s_owned[r] - left) + g - s_drop[r];
             p.ring[ring_at(tail_at, g, p.ring_size)] = p.tables[(int64_t)(base + r) * p.table_stride + j];
         }
         tok0 += tok_n;
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
         // (at least one request:) every CTA has passed a chunk's cluster barrier,
         // so it has read the state
         p.state_out[0] = head + min(grow0, avail);
-        p.state_out[1] = tail + drop0;
+        p.state_out[1] = tail + min(drop0, room);
     }
     if (flags && rank == 0) atomicOr(p.status, flags);
 }

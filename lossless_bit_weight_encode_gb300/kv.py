@@ -182,8 +182,9 @@ class KVPages:
         ``lens`` (int32) cached ones and fill ``step``; ``trim`` takes back pages
         they no longer need.  ``owned`` and ``ring_state`` are updated in place
         unless outputs are given.  ``step`` refers to ``lens``, which must stay as
-        it is until the step's attend calls have run.  A ring that runs out is
-        reported by w12_check_status."""
+        it is until the step's attend calls have run.  A ring that runs out, or
+        has no room for pages that trim gives back (those stay with their
+        requests), is reported by w12_check_status."""
         if stream is not None or _current_device() != self._index:
             with _on(self._index, stream):
                 return self.plan(lens, new_lens, step, trim, owned_out, ring_state_out)
