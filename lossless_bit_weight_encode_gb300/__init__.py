@@ -8,16 +8,29 @@ one step of its requests.  ``workloads`` draws the seeded synthetic inputs.
 """
 from __future__ import annotations
 
+import importlib.util
+
 import numpy as np
 
 from . import w12
 from .w12 import W12Error
 
-__all__ = ["w12", "W12Error", "W12Weight", "W12Group", "Q8Weight", "Q8Group", "KVCache", "KVPages", "KVStep"]
+__all__ = ["w12", "W12Error", "W12Weight", "W12Group", "Q8Weight", "Q8Group"]
+
+
+def _has_torch():
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except ValueError:  # sys.modules says that it is not to be imported
+        return False
+
+
+# kv.py needs torch at import; the host encoder does not
+if _has_torch():
+    __all__ += ["KVCache", "KVPages", "KVStep"]
 
 
 def __getattr__(name):
-    # kv.py needs torch at import; the host encoder does not
     if name in ("KVCache", "KVPages", "KVStep"):
         from . import kv
 

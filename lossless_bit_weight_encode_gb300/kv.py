@@ -21,8 +21,7 @@ import os
 
 import torch
 
-from . import w12
-from .build import KV_HOST_PATH
+from . import build, w12
 
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
 _workspaces = {}  # (device, stream handle) -> zeroed workspace of the attend calls on that stream
@@ -51,10 +50,11 @@ def _grow(index, st, size):
 
 def _load_host():
     """The module that takes the calls from tensors to the C ABI."""
-    if not os.path.exists(KV_HOST_PATH):
-        raise RuntimeError(f"the paged cache's host module is not built ({KV_HOST_PATH} missing): run "
+    path = build.KV_HOST_PATH
+    if not os.path.exists(path):
+        raise RuntimeError(f"the paged cache's host module is not built ({path} missing): run "
                            "__graft_entry__.build()")
-    loader = importlib.machinery.ExtensionFileLoader("kv_host", KV_HOST_PATH)
+    loader = importlib.machinery.ExtensionFileLoader("kv_host", path)
     host = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kv_host", loader=loader))
     loader.exec_module(host)
     lib = w12.lib()
@@ -64,7 +64,16 @@ def _load_host():
     return host
 
 
-_host = _load_host()
+class _NotLoaded:
+    """Stands for the module until the first call: the package is imported before the build too."""
+
+    def __getattr__(self, name):
+        global _host
+        _host = _load_host()
+        return getattr(_host, name)
+
+
+_host = _NotLoaded()
 
 _current_device = torch._C._cuda_getDevice
 # handle of a device's current stream, without the stream object around it

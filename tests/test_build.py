@@ -2,10 +2,14 @@
 module that uses torch is built again."""
 import importlib.util
 import os
+import subprocess
+import sys
 
 import pytest
 
 from lossless_bit_weight_encode_gb300 import build as b
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class FakeCompiler:
@@ -85,3 +89,25 @@ def test_module_is_built_again_for_another_torch(fake, tmp_path, monkeypatch):
     (other / "version.py").write_text("__version__ = '99.1'\n")
     b.build()
     assert "kv_host.so" in fake.outputs()[made:]
+
+
+HIDE = "import sys; sys.modules['torch'] = None\n"
+
+
+@pytest.mark.parametrize("code", ["from lossless_bit_weight_encode_gb300 import *; print(W12Weight.__name__)",
+                                  "from lossless_bit_weight_encode_gb300 import W12Weight; print(W12Weight.__name__)"])
+def test_package_is_imported_without_torch(code):
+    r = subprocess.run([sys.executable, "-c", HIDE + code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "W12Weight", r.stderr
+
+
+def test_holders_are_imported_before_the_build(tmp_path):
+    """Only a call needs the compiled module; without it the call says what to do."""
+    code = ("from lossless_bit_weight_encode_gb300 import build\n"
+            f"build.KV_HOST_PATH = {str(tmp_path / 'kv_host.so')!r}\n"
+            "from lossless_bit_weight_encode_gb300 import *\n"
+            "from lossless_bit_weight_encode_gb300 import kv\n"
+            "print(KVCache.__name__, KVPages.__name__, KVStep.__name__)\n"
+            "try:\n    kv._host.read()\nexcept RuntimeError as e:\n    print('build()' in str(e))\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.split() == ["KVCache", "KVPages", "KVStep", "True"], r.stderr
