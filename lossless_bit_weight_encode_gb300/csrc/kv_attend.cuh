@@ -196,7 +196,7 @@ template <int ROWS, int TILE>
 __device__ __forceinline__ KvSums kv_sum_units(const KvAttendParams &p) {
     const int lane = threadIdx.x & 31;
     KvSums s;
-    s.per = (p.requests + 31) / 32;
+    s.per = (int32_t)(((uint32_t)p.requests + 31u) / 32u);
     int64_t sum = 0;
 #pragma unroll 4
     for (int i = 0; i < s.per; ++i) {
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int32_t lr = (wr * NT + nt) * 8 + 2 * t + e;
-                            const int32_t i = min(row0 + lr, row0 + nrows - 1) / p.group;
+                            const int32_t i = (row0 + min(lr, nrows - 1)) / p.group;
                             const KvRowView v = p.positions ? kv_row_view<true>(p, r, i) : kv_row_view<false>(p, r, i);
 #pragma unroll
                             for (int u = 0; u < PAIR; ++u) {
@@ -966,14 +966,15 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_kernel(const KvAtten
     KvRequest r;
     int32_t b = 0;
     {
-        const int first = lane * sums.per, end = min(first + sums.per, p.requests);
+        const int first = lane * sums.per, end = (int)min((int64_t)first + sums.per, (int64_t)p.requests);
         const bool mine = first < p.requests && tok >= min(max(p.cu_new[first], 0), p.tokens) &&
                           tok < min(max(p.cu_new[end], 0), p.tokens);
         const uint32_t hit = __ballot_sync(~0u, mine);
         if (hit) {
             const int src = __ffs(hit) - 1;
             int64_t at = __shfl_sync(~0u, sums.before, src);
-            for (b = src * sums.per; b < min((src + 1) * sums.per, p.requests); ++b) {
+            const int32_t last = (int32_t)min((int64_t)(src + 1) * sums.per, (int64_t)p.requests);
+            for (b = src * sums.per; b < last; ++b) {
                 r = kv_request<ROWS, TILE>(p, b);
                 if (tok >= r.q0 && tok < r.q0 + r.qlen) {
                     start = at;

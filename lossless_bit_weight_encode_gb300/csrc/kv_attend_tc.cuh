@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 const KvPiece &c = place.c;
                 nrows = (int32_t)min((int64_t)kTcRows, (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows);
                 row0 = c.rb * kTcRows;
-                i = min(row0 + lr, row0 + nrows - 1) / p.group;  // new token of TMEM lane lr's row
+                i = (row0 + min(lr, nrows - 1)) / p.group;  // new token of TMEM lane lr's row
                 kb = (r.tile0 + c.ja) * kAttendTile;
                 tiles = c.jb - c.ja;
                 keys = r.kv;
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             }
             // the keys of the tile at kb that row `row` of the block sees
             const auto seen_by = [&](int row, uint32_t here) -> uint64_t {
-                const int32_t tok = min(row0 + row, row0 + nrows - 1) / p.group;
+                const int32_t tok = (row0 + min(row, nrows - 1)) / p.group;
                 return kv_seen64(p, keys, past, kv_row_view<PLACED>(p, place.r, tok), kb, here) >> (2 * t4);
             };
             const bool busy = base < nrows;  // a warp without rows only keeps step

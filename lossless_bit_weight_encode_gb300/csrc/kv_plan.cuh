@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
     int64_t tok0 = 0;
     int32_t grow0 = 0, drop0 = 0;  // totals of the chunks before
     uint32_t flags = tail - head != avail ? kStatusKvPages : 0;
-    for (int base = 0; base < p.requests; base += kPlanThreads) {
-        const int n = min(kPlanThreads, p.requests - base);
+    for (int64_t base = 0; base < p.requests; base += kPlanThreads) {
+        const int n = (int)min((int64_t)kPlanThreads, p.requests - base);
         int32_t len = 0, add = 0, owned = 0, need = 0;
         if (tid < n) {
             const int32_t l = p.lens[base + tid], a = p.new_lens[base + tid], o = p.owned_in[base + tid];
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
             const int32_t pos = s_len[r] + (int32_t)t - s_tok[r], j = pos / p.page_size;
             int32_t page = -1;
             if (j < s_owned[r]) {
-                page = p.tables[(int64_t)(base + r) * p.table_stride + j];
+                page = p.tables[(base + r) * p.table_stride + j];
             } else {
                 const int32_t at = s_grow[r] + j - s_owned[r];
                 if (at < avail) page = p.ring[ring_at(head_at, at, p.ring_size)];
@@ -165,21 +165,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1) w12_kv_plan_kernel(KvPlanPara
             p.positions[t] = pos;
             p.slots[t] = page < 0 ? -1 : (int64_t)page * p.page_size + (pos - j * p.page_size);
         }
-        // pages taken (or missing) and pages given back
-        for (int32_t i = first; i < grow_n; i += step) {
-            const int32_t g = grow0 + i;
+        // pages taken (or missing) and pages given back (counted without a sign: a step
+        // past close to 2^31 of them must not wrap)
+        for (uint32_t i = first; i < (uint32_t)grow_n; i += step) {
+            const int32_t g = grow0 + (int32_t)i;
             const int r = find_start(s_grow, n, g);
             const int32_t j = s_owned[r] + g - s_grow[r];
-            p.tables[(int64_t)(base + r) * p.table_stride + j] =
+            p.tables[(base + r) * p.table_stride + j] =
                 g < avail ? p.ring[ring_at(head_at, g, p.ring_size)] : -1;
         }
         const int32_t back_n = min(drop_n, max(room - drop0, 0));
-        for (int32_t i = first; i < back_n; i += step) {
-            const int32_t g = drop0 + i;
+        for (uint32_t i = first; i < (uint32_t)back_n; i += step) {
+            const int32_t g = drop0 + (int32_t)i;
             const int r = find_start(s_drop, n, g);
             // the last min(drop, room left) of the request's pages, in table order
             const int32_t left = room - s_drop[r], j = max(s_need[r], s_owned[r] - left) + g - s_drop[r];
-            p.ring[ring_at(tail_at, g, p.ring_size)] = p.tables[(int64_t)(base + r) * p.table_stride + j];
+            p.ring[ring_at(tail_at, g, p.ring_size)] = p.tables[(base + r) * p.table_stride + j];
         }
         tok0 += tok_n;
         grow0 += grow_n;

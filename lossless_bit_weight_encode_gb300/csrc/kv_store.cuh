@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kStoreThreads, 16) w12_kv_store_kernel(KvStore
     pdl_launch_dependents();
     pdl_wait();
     uint32_t flags = 0;
-    for (int t = blockIdx.y; t < p.tokens; t += gridDim.y) {
+    for (int t = blockIdx.y; (uint32_t)t < (uint32_t)p.tokens; t = (int)((uint32_t)t + gridDim.y)) {
         const int64_t slot = p.slots[t];
         int64_t pos = p.rot > 0 ? p.positions[t] : 0;
         const uint16_t *const qt = p.q + t * p.q_stride, *const kt = p.k + t * p.k_stride,
