@@ -557,7 +557,9 @@ int w12_check_status(void *stream);
  *   splits          (0; 0..2^20) n > 0: fixed split-K with n splits where the
  *                               kernel's per-CTA limits allow it
  *   pdl             (1; 0..1)   programmatic dependent launch on GEMMs
- *   timeout_ms      (4000; 1..600000) bounded waits give up after this
+ *   timeout_ms      (4000; 1..600000) bounded waits give up this long after
+ *                               their kernel's start; w12_kv_attend adds the time
+ *                               of its operations at 4 TFLOP/s (at most 600 s)
  *   tc_sm           (1; 0..1)   tensor-core path: 1 one CTA per SM walking
  *                               stream-K ranges (A operand in TMEM), 0 several
  *                               CTAs per SM with fixed split-K

@@ -73,6 +73,17 @@ int attend_call(const DeviceView &d, const w12_kv_cache &c, int rows, int *resid
     }
 }
 
+// How long an attend kernel's waits may go on, counted from its start: the option's
+// limit, which is far above any decoding step, and the time that the call's operations
+// would take at 4 TFLOP/s (blocks of eight rows over heads of 64, among the slowest, do
+// 55), for a long prompt in one call may rightly take many seconds.  The keys are bounded by the
+// tables' width.  (A limit from each wait's own start costs the loops registers: three
+// tokens on windows of an 8-bit cache 173 us, 186.)
+uint64_t attend_timeout_ns(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_args &a) {
+    const double flops = 4.0 * a.heads * c.head_dim * a.tokens * ((double)a.max_blocks * c.page_size);
+    return d.timeout_ns + (uint64_t)std::min(flops / 4e3, 600e9);  // 4e3 per ns; ten minutes at most
+}
+
 int attend_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_args &a, AttendPlan *plan,
                 std::string *err) {
     const int group = a.heads / c.kv_heads;
@@ -316,7 +327,7 @@ int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspac
     p.n_counters = plan.n_counters;
     p.join_later = join_warps(plan.rows, p.group, c.kv_heads, a.max_new, a.requests, plan.ctas);
     p.status = d.status;
-    p.timeout_ns = d.timeout_ns;
+    p.timeout_ns = attend_timeout_ns(d, c, a);
     int resident = 0;
     const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
     return attend_call(d, c, plan.rows, &resident, &p, &tm_k, &tm_v, plan.ctas, stream, err);
