@@ -140,13 +140,16 @@ class KVStep:
         if value is not None and name in self._kinds:
             _ints(value, self._kinds[name], name, self._one_device(value))
         elif value is not None and name == "tables":
+            self._one_device(value)
             _need(value.dtype is _I32 and value.dim() == 2 and value.stride(1) == 1,
                   "tables must be an int32 CUDA tensor [requests, max_blocks] with contiguous rows")
-            self._one_device(value)
+        else:
+            return object.__setattr__(self, name, value)
+        object.__setattr__(self, "device", value.get_device())  # of its first array, and then of all
         object.__setattr__(self, name, value)
 
     def _one_device(self, t):
-        _need(t.is_cuda and t.get_device() == self.__dict__.setdefault("device", t.get_device()),
+        _need(t.is_cuda and t.get_device() == self.__dict__.get("device", t.get_device()),
               "a step's arrays must be on one CUDA device")
         return t.get_device()
 
