@@ -200,12 +200,13 @@ class KVPages:
         if stream is not None or _current_device() != self._index:
             with _on(self._index, stream):
                 return self.plan(lens, new_lens, step, trim, owned_out, ring_state_out)
+        _host.plan(self, self._index, lens, new_lens, step, trim, owned_out, ring_state_out,
+                   _current_stream(self._index))
         if step.lens is not lens:
             step.lens = lens
         if step.tables is not self.tables:
             step.tables = self.tables
-        return _host.plan(self, self._index, lens, new_lens, step, trim, owned_out, ring_state_out,
-                          _current_stream(self._index))
+        return step
 
 
 class KVCache:
