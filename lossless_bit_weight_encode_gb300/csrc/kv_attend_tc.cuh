@@ -504,10 +504,16 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 for (int c0 = 0; c0 < HALVES * D / 4; c0 += 32) {
                     const int col = half * (D / 4) + c0;
                     uint32_t x[32];
+                    uint4 u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = make_uint4(0, 0, 0, 0);
+                    if (lr < rows) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = reinterpret_cast<const uint4 *>(src + 2 * col)[i];
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (lr < rows) v = reinterpret_cast<const uint4 *>(src + 2 * col)[i];
+                        uint4 v = u[i];
                         if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
                             v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
                         if (Q8)
