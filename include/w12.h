@@ -488,12 +488,15 @@ int w12_kv_read(const w12_kv_cache *cache, const int64_t *slots, int32_t tokens,
  * key head h / (heads / kv_heads); lse[t][h] (NULL: not written) = ln sum_j
  * exp(scale * q . k_j).  A token that sees nothing gets out 0 and lse
  * -infinity; rows of q behind cu_new[requests] get nothing.  What unseen slots
- * hold, NaN among it, has no effect.  fp32 scores,
- * softmax statistics and sums; the softmax weights are rounded to BF16 for the
+ * hold, NaN among it, has no effect; a NaN in q or in a key that is seen makes
+ * the row's out and lse NaN, one in a value its column of out.  fp32 scores, softmax statistics and sums; the softmax weights are rounded to BF16 for the
  * tensor cores.  Results are reproducible run to run for the same lengths.
  * q, out: BF16, token t at t * stride, stride a multiple of 8, 16-byte aligned.
- * heads: a multiple of kv_heads; heads * tokens below 2^31.  max_new: the most new tokens a request has,
- * as far as the caller knows; it picks the row tile and any value is correct.
+ * heads: a multiple of kv_heads; heads * tokens below 2^31.  max_new: the most
+ * new tokens a request has, as far as the caller knows; it picks the row tile and
+ * any value is correct.  Made for a few new tokens per request: all of a request's
+ * rows walk the keys that any of its new tokens sees, so a prompt of T tokens
+ * costs T x T products, masked ones included, and with a window T x (T + window).
  * workspace: at least w12_kv_attend_workspace_size bytes, 256-byte aligned,
  * ZERO-FILLED BEFORE ITS FIRST USE; every successful call leaves its counters
  * zero again (after a TIMEOUT, zero it again).  Calls of any shape may share a
@@ -536,7 +539,8 @@ int w12_read_stream(const void *buf_dev, size_t bytes, void *sink_dev, uint32_t 
  * Synchronise `stream`, then read and clear the current device's status word,
  * which kernels set when a bounded wait gives up (TIMEOUT), the device encoder
  * finds its output buffer too short (BUFFER_TOO_SMALL) or too many escapes
- * (SHAPE), or a paged-cache call meets what its comment lists.  Returns that status, CUDA on a CUDA error, else OK.
+ * (SHAPE), or a paged-cache call meets what its comment lists.  Returns that
+ * status, CUDA on a CUDA error, else OK.
  */
 int w12_check_status(void *stream);
 
@@ -556,7 +560,8 @@ int w12_check_status(void *stream);
  *   stream_k        (1; 0..1)   0: fixed split-K on the CUDA-core path
  *   splits          (0; 0..2^20) n > 0: fixed split-K with n splits where the
  *                               kernel's per-CTA limits allow it
- *   pdl             (1; 0..1)   programmatic dependent launch on GEMMs
+ *   pdl             (1; 0..1)   programmatic dependent launch on GEMMs and the
+ *                               paged-cache calls
  *   timeout_ms      (4000; 1..600000) bounded waits give up this long after
  *                               their kernel's start; w12_kv_attend adds the time
  *                               of its operations at 4 TFLOP/s (at most 600 s)

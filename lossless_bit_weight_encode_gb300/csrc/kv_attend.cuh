@@ -12,7 +12,7 @@
 //
 // What bounds it: the keys and values are read once, from HBM; per byte of a
 // BF16 cache there are 2 * rows flops.  Layout for that: a producer warp keeps a
-// ring of 64-key tiles full by TMA (one 5-D box of 16 tokens x head_dim per k and
+// ring of tiles (64 or 128 keys, see AttendTile) full by TMA (one 5-D box of 16 tokens x head_dim per k and
 // v: 16 tokens are the page granularity, so any page size that is a multiple of
 // 16 works and a box never crosses a page), and four consumer warps multiply on
 // the tensor cores straight from shared memory.  The rows are few, so they are
@@ -22,9 +22,11 @@
 // split a tile's keys (WK) and, where a warp's registers do not hold the sums of all
 // rows, the rows (WR).
 //
-// Work split.  The unit is one 64-key tile of one (request, key head, row block);
+// Work split.  The unit is one tile of one (request, key head, row block);
 // all units form one line that the CTAs cut into equal ranges, whatever the
-// lengths.  A range that covers a row block's keys only in part leaves its
+// lengths.  A request's row blocks all have its tiles, from the first key that its first
+// token sees to its last key: a block of a long prompt also walks the tiles that none of
+// its own rows sees.  A range that covers a row block's keys only in part leaves its
 // partial result in the workspace, and the CTA that arrives last at the block's
 // counter joins the parts in range order (the same result in every run).  Where
 // that would be a long chain for one CTA (kv_launch.cuh has the rule), a second
@@ -33,9 +35,9 @@
 // Q8 cache: int8 elements become BF16 exactly in registers; a key's scale
 // multiplies its score, a value's scale its probability.
 //
-// Measured: 64 requests of 8000 tokens, 48 heads over 8 of 128: BF16 310 us, 6.8 TB/s
-// (a copy of that many bytes takes as long); Q8 192 us, 5.7 TB/s, where issue (the
-// conversion) is close behind HBM.  Two of 100001, 24 heads over 4 of 256: 114 us,
+// Measured: 64 requests of 8000 tokens, 48 heads over 8 of 128: BF16 311 us, 6.8 TB/s
+// (a copy of that many bytes takes as long); Q8 190 us, 5.7 TB/s, where issue (the
+// conversion) is close behind HBM.  Two of 100001, 24 heads over 4 of 256: 116 us,
 // 6.6 TB/s.  128 windows of 1024 keys: 55 us, 5.0 TB/s; calls this short spend some
 // 14 us before the ring is full and after it has run dry.  One request of 777 tokens:
 // 7.2 us, all of it latency (two launches, TMA, the join).
@@ -49,7 +51,7 @@
 namespace w12 {
 namespace dev {
 
-constexpr int kAttendTile = 64;       // keys of a pipeline stage of the tcgen05 kernel
+constexpr int kAttendTile = 64;       // keys of a tile of the tcgen05 kernel
 constexpr int kAttendSlice = 16;      // keys of one TMA box and of one mma
 constexpr int kAttendThreads = 160;   // four consumer warps and the producer
 constexpr float kAttendLazy = 8.0f;   // how far a score may pass the running maximum (log2)

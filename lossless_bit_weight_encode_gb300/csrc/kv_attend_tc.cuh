@@ -7,7 +7,7 @@
 // Here 128 rows are the M of one tcgen05.mma: a tile's keys are read from shared
 // memory once for all rows.  Per 64-key tile
 //   S [128 x 64]  = Q (TMEM or shared)   x K^T (shared, K-major)
-//   P             = 2^(S - m), 16 rows per warp, BF16, over S
+//   P             = 2^(S - m), 16 rows of a warp at a time, BF16, over S
 //   O [128 x D] += P (TMEM)              x V (shared, MN-major)
 // S has two or four buffers, so the tensor cores make the next tiles' scores while
 // the softmax warps work on this one's.  O stays in TMEM for a whole piece; it is
@@ -29,7 +29,7 @@
 // products 22.  Taking the softmax's or the conversion's instructions out shortens the
 // Q8 call by 7 % each, both by 26 %: it is bounded by the chain of bytes, operand,
 // scores, weights and product, of which two CTAs per SM overlap two.  30 rows of 64
-// requests of 8000: BF16 320 us, 6.6 TB/s, Q8 337.  72 rows of 256 columns, two of
+// requests of 8000: BF16 320 us, 6.6 TB/s, Q8 332.  72 rows of 256 columns, two of
 // 100001: BF16 128 us, Q8 107.
 #pragma once
 
@@ -327,7 +327,7 @@ __device__ __forceinline__ void tc_softmax(uint32_t ts, const uint32_t (&x)[32],
 
 // Fills a ring with the keys or the values of the CTA's tiles, one tile per step().
 // Keys and values have a loader (and a warp) each: a ring's next tile is then asked
-// for as soon as its own slot is free, two tiles ahead of its use.
+// for as soon as its own slot is free, up to a ring (kOps or kRaws tiles) ahead of its use.
 template <int D, bool Q8>
 struct TcLoader {
     using C = AttendTcCfg<D, Q8>;

@@ -8,8 +8,8 @@
 // long prompt among short ones costs no more than the same tokens spread out.
 //
 // The call is latency: it moves 20 bytes per request and 12 per token (at the HBM
-// rate 0.06 us of the 6.9 us that 1024 requests with 32768 new tokens take; one request
-// with one token takes 3.3, an empty kernel 2).  What is left is the chain: lengths,
+// rate 0.06 us of the 7.0 us that 1024 requests with 32768 new tokens take; one request
+// with one token takes 3.2, an empty kernel 2).  What is left is the chain: lengths,
 // prefix sums, search, ring or table entry, store.  One cluster of CTAs (one CTA
 // where its threads have at most two tokens each) computes the sums redundantly and
 // shares the lists, so that there is one launch and nothing in memory between; its

@@ -10,10 +10,11 @@
 // it is fp32 on the BF16 inputs with one rounding at the store.
 //
 // Every element is read and written once and nothing is shared between heads, so a
-// large call is bounded by HBM: 8192 tokens of 24 + 2 x 4 heads of 256 take 49.9 us,
-// 5.5 TB/s (the norm, rotation and address instructions keep issue 65 % busy, which is
+// large call is bounded by HBM: 8192 tokens of 24 + 2 x 4 heads of 256 take 49.6 us,
+// 5.6 TB/s (the norm, rotation and address instructions keep issue 65 % busy, which is
 // why the arithmetic is packed in pairs); 30000 cached tokens of 4 heads of 256 read
-// back take 38.2 us, 6.4 TB/s.  One token is a launch: 2.2 us.
+// back take 38.3 us, 6.4 TB/s.  One token is a launch: 2.2 us.  The same chunk stored into
+// an 8-bit cache and read back takes 77 us (46 at the HBM rate), in two launches.
 #pragma once
 
 #include "kv_common.cuh"
