@@ -489,7 +489,8 @@ int w12_kv_read(const w12_kv_cache *cache, const int64_t *slots, int32_t tokens,
  * exp(scale * q . k_j).  A token that sees nothing gets out 0 and lse
  * -infinity; rows of q behind cu_new[requests] get nothing.  What unseen slots
  * hold, NaN among it, has no effect; a NaN in q or in a key that is seen makes
- * the row's out and lse NaN, one in a value its column of out.  fp32 scores, softmax statistics and sums; the softmax weights are rounded to BF16 for the
+ * the row's out and lse NaN, one in a value its column of out.  fp32 scores,
+ * softmax statistics and sums; the softmax weights are rounded to BF16 for the
  * tensor cores.  Results are reproducible run to run for the same lengths.
  * q, out: BF16, token t at t * stride, stride a multiple of 8, 16-byte aligned.
  * heads: a multiple of kv_heads; heads * tokens below 2^31.  max_new: the most
