@@ -525,6 +525,137 @@ int w12_kv_attend(const w12_kv_cache *cache, const w12_kv_attend_args *args, voi
                   void *stream);
 
 /*
+ * Several requests that go on from one: beams, samples of one prompt, requests that are
+ * ended.  Row i of the new tables has the first ceil(k / page_size) entries of row
+ * parents[i] as it was before the call, k = lens[i] tokens (clamped to what the parent's
+ * pages hold); parents[i] = -1: none (k = 0).  In place:
+ *   - shares[P], for every page, is the number of rows (and of other holders, which the
+ *     caller counts) that hold P, less one; 0 of a free page.  Pages of which all k's
+ *     tokens use every slot are held by all rows that want them.
+ *   - the last page of a row whose k is no multiple of page_size is written to in the
+ *     next step: the row keeps it if no other row wants it and no one else holds it; of
+ *     several rows that want it so the first keeps it, and each other one gets a page from
+ *     the ring (in row order) and src[i], dst[i], rows[i]: the page to copy, the page
+ *     that it got and the tokens in it, for w12_kv_copy on every layer's cache.  All other
+ *     rows have src = dst = -1, rows = 0.
+ *   - pages that no one holds any more go behind the ring's tail, in the order of their
+ *     entries in the tables, then of the first row that held them.
+ * A page stands at the same entry of every row that holds it (so it does where rows come
+ * from one another).  parents[i] = i and a smaller lens[i] takes back what a request needs
+ * no more; in tables with shared pages it takes the place of w12_kv_plan's trim, which
+ * knows no shares.  owned[i]: the pages row i holds, lens_out[i] (NULL: not written; may be
+ * lens): k.
+ * prefix_cu, prefix_lens (NULL: none): groups of consecutive rows, prefix_cu[g] ..
+ * prefix_cu[g + 1] - 1; prefix_lens[i] = the tokens in the leading full pages that all
+ * rows of i's group with k > 0 have in common, 0 for a row with k = 0 or whose group has
+ * no other such row (what w12_kv_attend_shared takes).
+ * ring_size at least num_pages; ring and ring_state as w12_kv_plan.  requests at most 4096,
+ * max_blocks * page_size and max_blocks * requests below 2^31.  Where the ring runs out
+ * the page is absent (-1) and not copied, and w12_check_status returns BUFFER_TOO_SMALL;
+ * where a length, a parent (others than -1 count as none) or owned had to be clamped, SHAPE.
+ * All arrays 4-byte aligned, ring_state 8-byte; none overlaps another, but lens_out lens.
+ */
+typedef struct w12_kv_fork_args {
+    const int32_t *parents, *lens;
+    int32_t *lens_out;
+    int32_t *owned;
+    int32_t *tables;
+    int64_t table_stride;
+    int32_t *ring;
+    int64_t *ring_state;
+    int32_t *shares;
+    int32_t *src, *dst, *rows;
+    const int32_t *prefix_cu;
+    int32_t *prefix_lens;
+    int64_t num_pages;
+    int32_t requests, max_blocks, page_size, ring_size, groups;
+} w12_kv_fork_args;
+
+int w12_kv_fork(const w12_kv_fork_args *args, void *stream);
+
+/*
+ * Pages copied inside each of `count` caches (a model's layers) that are alike in all but
+ * their pointers: the first rows[i] tokens (NULL: all; more than page_size counts as that)
+ * of page src[i], keys, values and scales, to page dst[i], bit by bit.  A negative src or
+ * dst: none.  A page that one pair writes must not be another pair's src or dst.  A page
+ * outside the cache is not copied and w12_check_status returns INVALID_ARG.  src, dst and
+ * rows: device memory, int32[pairs].
+ */
+int w12_kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, const int32_t *dst, const int32_t *rows,
+                int32_t pairs, void *stream);
+
+/*
+ * w12_kv_attend where requests share a prefix: the keys and values of a group's prefix are
+ * read once for the new tokens of all its requests, then each request's own.  The result
+ * is that of w12_kv_attend (with other splits of the sums).  Group g has requests cu[g] ..
+ * cu[g + 1] - 1 (cu[groups + 1], cu[0] = 0, cu[groups] = requests); lens[b] (int32
+ * [requests]): the tokens that request b shares with its group, 0: none.  Within a group
+ * the lens that are not 0 are the same, a multiple of page_size (else rounded down) and at
+ * most args->lens[b] (else clamped, and w12_check_status returns SHAPE); the leading
+ * lens / page_size table entries of those requests are the same too: the first one's are
+ * read.  max_requests: the most requests of a group, as far as the caller knows; it picks
+ * the row tile and any value is correct.  args as w12_kv_attend, window 0 (INVALID_ARG
+ * otherwise; a layer with a window reads no long prefix).
+ * workspace: w12_kv_attend_shared_workspace_size bytes, 256-byte aligned, no initial
+ * contents; not one that w12_kv_attend uses, whose counters have to stay zero.  Calls that
+ * share one are ordered on the GPU; host threads may make them at the same time on one
+ * stream.
+ */
+typedef struct w12_kv_prefix {
+    const int32_t *cu, *lens;
+    int32_t groups, max_requests;
+} w12_kv_prefix;
+
+int w12_kv_attend_shared_workspace_size(const w12_kv_cache *cache, const w12_kv_attend_args *args,
+                                        const w12_kv_prefix *prefix, size_t *bytes);
+
+int w12_kv_attend_shared(const w12_kv_cache *cache, const w12_kv_attend_args *args, const w12_kv_prefix *prefix,
+                         void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One step of beam search: the best continuations of each of `requests` requests over its
+ * `beams` beams and the vocabulary.  Beam b of request r is row r * beams + b of logits
+ * (BF16 or fp32, row i at i * logits_stride elements, aligned to an element).  With
+ * M = max_v x_v over the tokens that count, token v of the row has the score
+ *   scores_in[row] + ((x_v - M) - ln sum_v exp(x_v - M)),
+ * compared in 64 bits, ties to the lower beam, then token.  Tokens that do not count:
+ * those whose bit (v % 32 of word v / 32 of the row's words at allowed + row *
+ * allowed_stride; allowed NULL: all have theirs; allowed_stride 0: one line for all rows) is 0,
+ * and logits of -infinity or NaN.  Where M is +infinity, the tokens that have it share
+ * the weight.  A beam whose score is not finite does not go on (the first step of a
+ * search has one beam with score 0 and the others at -infinity).
+ *   cand_tokens, cand_parents (the row), cand_scores [requests][take]: the best `take`,
+ *     best first;
+ *   tokens, parents, scores [requests * beams]: of these and the ones behind them the first
+ *     `beams` that do not end, token != eos (eos -1: none ends); scores may be scores_in.
+ * Where there are not that many: token -1, parent -1, score -infinity.  parents is what
+ * w12_kv_fork takes.
+ * beams 1..32, take 1..64, vocab up to 2^22, requests * beams * vocab / 3000 below 2^31.
+ * The sums are reproducible run to run.  workspace: w12_beam_workspace_size bytes,
+ * 256-byte aligned, ZERO-FILLED BEFORE ITS FIRST USE (a call leaves its counters zero);
+ * calls with the same number of requests may share one if they are ordered on the GPU.
+ */
+#define W12_BEAM_BF16 0
+#define W12_BEAM_F32 1
+
+typedef struct w12_beam_args {
+    const void *logits;
+    int64_t logits_stride;
+    const uint32_t *allowed;
+    int64_t allowed_stride;
+    const float *scores_in;
+    float *scores;
+    int32_t *tokens, *parents;
+    int32_t *cand_tokens, *cand_parents;
+    float *cand_scores;
+    int32_t requests, beams, vocab, take, eos, dtype;
+} w12_beam_args;
+
+int w12_beam_workspace_size(const w12_beam_args *args, size_t *bytes);
+
+int w12_beam_select(const w12_beam_args *args, void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Measurement helper with no counterpart on the pages: reads `bytes` (a
  * multiple of 16) of device memory at buf_dev (16-byte aligned) once, with
  * 16-byte streaming loads spread over every SM, and writes the 4-byte word at

@@ -4,7 +4,8 @@
 ``W12Weight`` is a small convenience holder built on it (torch provides the
 device memory and the stream).  ``KVCache``, ``KVPages`` and ``KVStep`` (kv.py)
 are the attention side of a layer: a paged key-value cache, its page tables and
-one step of its requests.  ``workloads`` draws the seeded synthetic inputs.
+one step of its requests; ``KVPrefix`` and ``KVCopies`` what requests share and which pages
+to copy, ``Beams`` (beam.py) the state of a beam search.  ``workloads`` draws the seeded synthetic inputs.
 """
 from __future__ import annotations
 
@@ -25,16 +26,20 @@ def _has_torch():
         return False
 
 
-# kv.py needs torch at import; the host encoder does not
+# kv.py and beam.py need torch at import; the host encoder does not
 if _has_torch():
-    __all__ += ["KVCache", "KVPages", "KVStep"]
+    __all__ += ["KVCache", "KVPages", "KVStep", "KVPrefix", "KVCopies", "Beams"]
 
 
 def __getattr__(name):
-    if name in ("KVCache", "KVPages", "KVStep"):
+    if name in ("KVCache", "KVPages", "KVStep", "KVPrefix", "KVCopies"):
         from . import kv
 
         return getattr(kv, name)
+    if name == "Beams":
+        from . import beam
+
+        return beam.Beams
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -21,7 +21,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
-CUDA_SOURCES = ["kernels.cu", "kv.cu", "kv_attend_d64.cu", "kv_attend_d128.cu", "kv_attend_d256.cu"]
+CUDA_SOURCES = ["kernels.cu", "kv.cu", "kv_attend_d64.cu", "kv_attend_d128.cu", "kv_attend_d256.cu",
+                "kv_shared_d64.cu", "kv_shared_d128.cu", "kv_shared_d256.cu", "beam.cu"]
 CXX_SOURCES = ["encoder.cpp", "q8_host.cpp", "capi.cpp"]
 KV_HOST_SOURCE = "kv_host.cpp"
 

@@ -571,6 +571,39 @@ int check_kv_attend(const w12_kv_cache *c, const w12_kv_attend_args *a, std::str
     }
     return W12_OK;
 }
+
+int check_kv_attend_buffers(const w12_kv_cache *cache, const w12_kv_attend_args *args, const void *workspace,
+                            std::string &err) {
+    if (!args->q || !args->out || !args->tables || !args->lens || !args->cu_new || !workspace) {
+        err = "null device pointer";
+        return W12_ERR_INVALID_ARG;
+    }
+    const int64_t row = (int64_t)args->heads * cache->head_dim;
+    if (args->q_stride < row || args->out_stride < row) {
+        err = "a token stride is shorter than its heads";
+        return W12_ERR_SHAPE;
+    }
+    if (args->q_stride % 8 != 0 || args->out_stride % 8 != 0 || !aligned(args->q, 16) || !aligned(args->out, 16) ||
+        !aligned(workspace, 256) || !aligned(args->lse, 4) || !aligned(args->tables, 4) || !aligned(args->lens, 4) ||
+        !aligned(args->cu_new, 4) || !aligned(args->tree, 4) || !aligned(args->positions, 4)) {
+        err = "q and out must be 16-byte aligned with strides of a multiple of 8, workspace 256-byte, the 32-bit "
+              "arrays 4-byte aligned";
+        return W12_ERR_ALIGNMENT;
+    }
+    return W12_OK;
+}
+
+int check_kv_prefix(const w12_kv_attend_args *a, const w12_kv_prefix *prefix, std::string &err) {
+    if (!prefix || prefix->groups < 1 || prefix->max_requests < 0 || a->window != 0) {
+        err = "a shared prefix needs groups and takes no window";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (prefix->groups > a->requests) {
+        err = "groups must be at most requests";
+        return W12_ERR_SHAPE;
+    }
+    return W12_OK;
+}
 }  // namespace
 
 int w12_kv_plan(const w12_kv_plan_args *args, void *stream) {
@@ -687,26 +720,177 @@ int w12_kv_attend_workspace_size(const w12_kv_cache *cache, const w12_kv_attend_
 int w12_kv_attend(const w12_kv_cache *cache, const w12_kv_attend_args *args, void *workspace, size_t ws_bytes,
                   void *stream) {
     return guarded([&](std::string &err) {
-        const int rc = check_kv_attend(cache, args, err);
+        int rc = check_kv_attend(cache, args, err);
+        if (rc == W12_OK) rc = check_kv_attend_buffers(cache, args, workspace, err);
         if (rc != W12_OK) return rc;
-        if (!args->q || !args->out || !args->tables || !args->lens || !args->cu_new || !workspace) {
+        return w12::launch::kv_attend(*cache, *args, workspace, ws_bytes, stream, &err);
+    });
+}
+
+int w12_kv_fork(const w12_kv_fork_args *args, void *stream) {
+    return guarded([&](std::string &err) {
+        if (!args || !args->parents || !args->lens || !args->owned || !args->tables || !args->ring ||
+            !args->ring_state || !args->shares || !args->src || !args->dst || !args->rows) {
+            err = "null pointer";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        if (args->requests < 1 || args->max_blocks < 1 || args->num_pages < 1 ||
+            !args->prefix_cu != !args->prefix_lens || (args->prefix_cu && args->groups < 1)) {
+            err = "requests, max_blocks and num_pages must be at least 1, and prefix_cu and prefix_lens given together, "
+                  "with groups";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        if (args->requests > 4096 || args->num_pages > 0x7FFFFFFF || args->ring_size < args->num_pages ||
+            (args->prefix_cu && args->groups > args->requests)) {
+            err = "requests must be at most 4096, ring_size at least num_pages (below 2^31) and groups at most requests";
+            return (int)W12_ERR_SHAPE;
+        }
+        if (args->page_size < 16 || args->page_size % 16 != 0 ||
+            (int64_t)args->max_blocks * args->page_size >= (int64_t(1) << 31) ||
+            (int64_t)args->max_blocks * args->requests >= (int64_t(1) << 31) ||
+            args->table_stride < args->max_blocks) {
+            err = "page_size must be a multiple of 16, max_blocks * page_size and max_blocks * requests below 2^31 and "
+                  "table_stride at least max_blocks";
+            return (int)W12_ERR_SHAPE;
+        }
+        for (const void *p : {(const void *)args->parents, (const void *)args->lens, (const void *)args->lens_out,
+                              (const void *)args->owned, (const void *)args->tables, (const void *)args->ring,
+                              (const void *)args->shares, (const void *)args->src, (const void *)args->dst,
+                              (const void *)args->rows, (const void *)args->prefix_cu,
+                              (const void *)args->prefix_lens})
+            if (!aligned(p, 4)) {
+                err = "32-bit arrays must be 4-byte aligned";
+                return (int)W12_ERR_ALIGNMENT;
+            }
+        if (!aligned(args->ring_state, 8)) {
+            err = "ring_state must be 8-byte aligned";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        return w12::launch::kv_fork(*args, stream, &err);
+    });
+}
+
+int w12_kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, const int32_t *dst, const int32_t *rows,
+                int32_t pairs, void *stream) {
+    return guarded([&](std::string &err) {
+        if (!caches || count < 1 || pairs < 0 || !src || !dst) {
+            err = "null pointer or a bad count";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        for (int32_t i = 0; i < count; ++i) {
+            const w12_kv_cache &c = caches[i], &a = caches[0];
+            const int rc = check_kv_cache(&c, err);
+            if (rc != W12_OK) return rc;
+            if (c.num_pages != a.num_pages || c.page_stride != a.page_stride || c.head_stride != a.head_stride ||
+                c.row_stride != a.row_stride || c.page_size != a.page_size || c.kv_heads != a.kv_heads ||
+                c.head_dim != a.head_dim || c.dtype != a.dtype) {
+                err = "the caches must be alike in all but their pointers";
+                return (int)W12_ERR_SHAPE;
+            }
+        }
+        if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(rows, 4)) {
+            err = "src, dst and rows must be 4-byte aligned";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        return w12::launch::kv_copy(caches, count, src, dst, rows, pairs, stream, &err);
+    });
+}
+
+int w12_kv_attend_shared_workspace_size(const w12_kv_cache *cache, const w12_kv_attend_args *args,
+                                        const w12_kv_prefix *prefix, size_t *bytes) {
+    return guarded([&](std::string &err) {
+        int rc = check_kv_attend(cache, args, err);
+        if (rc == W12_OK) rc = check_kv_prefix(args, prefix, err);
+        if (rc != W12_OK) return rc;
+        if (!bytes) {
+            err = "bytes is null";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        return w12::launch::kv_attend_shared_workspace_size(*cache, *args, *prefix, bytes, &err);
+    });
+}
+
+int w12_kv_attend_shared(const w12_kv_cache *cache, const w12_kv_attend_args *args, const w12_kv_prefix *prefix,
+                         void *workspace, size_t ws_bytes, void *stream) {
+    return guarded([&](std::string &err) {
+        int rc = check_kv_attend(cache, args, err);
+        if (rc == W12_OK) rc = check_kv_prefix(args, prefix, err);
+        if (rc == W12_OK) rc = check_kv_attend_buffers(cache, args, workspace, err);
+        if (rc != W12_OK) return rc;
+        if (!prefix->cu || !prefix->lens) {
             err = "null device pointer";
             return (int)W12_ERR_INVALID_ARG;
         }
-        const int64_t row = (int64_t)args->heads * cache->head_dim;
-        if (args->q_stride < row || args->out_stride < row) {
-            err = "a token stride is shorter than its heads";
-            return (int)W12_ERR_SHAPE;
-        }
-        if (args->q_stride % 8 != 0 || args->out_stride % 8 != 0 || !aligned(args->q, 16) || !aligned(args->out, 16) ||
-            !aligned(workspace, 256) || !aligned(args->lse, 4) || !aligned(args->tables, 4) ||
-            !aligned(args->lens, 4) || !aligned(args->cu_new, 4) || !aligned(args->tree, 4) ||
-            !aligned(args->positions, 4)) {
-            err = "q and out must be 16-byte aligned with strides of a multiple of 8, workspace 256-byte, the 32-bit "
-                  "arrays 4-byte aligned";
+        if (!aligned(prefix->cu, 4) || !aligned(prefix->lens, 4)) {
+            err = "the 32-bit arrays must be 4-byte aligned";
             return (int)W12_ERR_ALIGNMENT;
         }
-        return w12::launch::kv_attend(*cache, *args, workspace, ws_bytes, stream, &err);
+        return w12::launch::kv_attend_shared(*cache, *args, *prefix, workspace, ws_bytes, stream, &err);
+    });
+}
+
+namespace {
+int check_beam(const w12_beam_args *a, std::string &err) {
+    if (!a) {
+        err = "args is null";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (a->dtype != W12_BEAM_BF16 && a->dtype != W12_BEAM_F32) {
+        err = "dtype must be W12_BEAM_BF16 or W12_BEAM_F32";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (a->requests < 1 || a->beams < 1 || a->vocab < 1 || a->take < 1 || a->eos < -1) {
+        err = "requests, beams, vocab and take must be at least 1, eos at least -1";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (a->beams > 32 || a->take > 64 || a->vocab > (1 << 22) ||
+        (int64_t)a->requests * a->beams * (a->vocab / 3000 + 1) >= (int64_t(1) << 31)) {
+        err = "beams must be at most 32, take at most 64, vocab at most 2^22 and requests * beams * vocab / 3000 below "
+              "2^31";
+        return W12_ERR_SHAPE;
+    }
+    return W12_OK;
+}
+}  // namespace
+
+int w12_beam_workspace_size(const w12_beam_args *args, size_t *bytes) {
+    return guarded([&](std::string &err) {
+        const int rc = check_beam(args, err);
+        if (rc != W12_OK) return rc;
+        if (!bytes) {
+            err = "bytes is null";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        return w12::launch::beam_workspace_size(*args, bytes, &err);
+    });
+}
+
+int w12_beam_select(const w12_beam_args *args, void *workspace, size_t ws_bytes, void *stream) {
+    return guarded([&](std::string &err) {
+        const int rc = check_beam(args, err);
+        if (rc != W12_OK) return rc;
+        if (!args->logits || !args->scores_in || !args->scores || !args->tokens || !args->parents ||
+            !args->cand_tokens || !args->cand_parents || !args->cand_scores || !workspace) {
+            err = "null device pointer";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        if (args->logits_stride < args->vocab ||
+            (args->allowed && args->allowed_stride != 0 && args->allowed_stride < (args->vocab + 31) / 32)) {
+            err = "logits_stride must be at least vocab, allowed_stride 0 or at least ceil(vocab / 32)";
+            return (int)W12_ERR_SHAPE;
+        }
+        if (!aligned(args->logits, args->dtype == W12_BEAM_BF16 ? 2 : 4) || !aligned(workspace, 256)) {
+            err = "logits must be aligned to an element, workspace 256-byte";
+            return (int)W12_ERR_ALIGNMENT;
+        }
+        for (const void *p : {(const void *)args->allowed, (const void *)args->scores_in, (const void *)args->scores,
+                              (const void *)args->tokens, (const void *)args->parents, (const void *)args->cand_tokens,
+                              (const void *)args->cand_parents, (const void *)args->cand_scores})
+            if (!aligned(p, 4)) {
+                err = "32-bit arrays must be 4-byte aligned";
+                return (int)W12_ERR_ALIGNMENT;
+            }
+        return w12::launch::beam_select(*args, workspace, ws_bytes, stream, &err);
     });
 }
 

@@ -4,8 +4,11 @@
 #include <algorithm>
 #include <cmath>
 
+#include "kv_copy.cuh"
+#include "kv_fork.cuh"
 #include "kv_launch.cuh"
 #include "kv_plan.cuh"
+#include "kv_shared.cuh"
 #include "kv_store.cuh"
 
 namespace w12 {
@@ -20,6 +23,25 @@ int attend_dim<128>(const DeviceView &, bool, int, int *, const dev::KvAttendPar
 template <>
 int attend_dim<256>(const DeviceView &, bool, int, int *, const dev::KvAttendParams *, const CUtensorMap *,
                     const CUtensorMap *, int, void *, std::string *);
+
+template <>
+int shared_dim<64>(const DeviceView &, bool, int, int *, const dev::KvPrefixParams *, const CUtensorMap *, const CUtensorMap *,
+                   int, void *, std::string *);
+template <>
+int shared_dim<64>(const DeviceView &, bool, int, int *, const dev::KvOwnParams *, const CUtensorMap *, const CUtensorMap *,
+                   int, void *, std::string *);
+template <>
+int shared_dim<128>(const DeviceView &, bool, int, int *, const dev::KvPrefixParams *, const CUtensorMap *, const CUtensorMap *,
+                    int, void *, std::string *);
+template <>
+int shared_dim<128>(const DeviceView &, bool, int, int *, const dev::KvOwnParams *, const CUtensorMap *, const CUtensorMap *,
+                    int, void *, std::string *);
+template <>
+int shared_dim<256>(const DeviceView &, bool, int, int *, const dev::KvPrefixParams *, const CUtensorMap *, const CUtensorMap *,
+                    int, void *, std::string *);
+template <>
+int shared_dim<256>(const DeviceView &, bool, int, int *, const dev::KvOwnParams *, const CUtensorMap *, const CUtensorMap *,
+                    int, void *, std::string *);
 
 namespace {
 
@@ -106,6 +128,92 @@ int attend_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_
     plan->off_ml = (size_t)2 * d.sm_count * kPartElems * sizeof(float);
     plan->off_counters = plan->off_ml + (size_t)2 * d.sm_count * (kPartElems / 64) * sizeof(float2);
     plan->bytes = plan->off_counters + (size_t)counters * sizeof(uint32_t);
+    return W12_OK;
+}
+
+// What a launch takes from the call as it is.
+dev::KvAttendParams attend_params(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_args &a) {
+    dev::KvAttendParams p = {};
+    p.q = a.q;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.q_stride = a.q_stride;
+    p.out_stride = a.out_stride;
+    p.tables = a.tables;
+    p.table_stride = a.table_stride;
+    p.lens = a.lens;
+    p.cu_new = a.cu_new;
+    p.tree = a.tree;
+    p.positions = a.tree && a.window > 0 ? a.positions : nullptr;
+    p.v = static_cast<const uint16_t *>(c.v_dev);
+    p.v_page_stride = c.page_stride;
+    p.v_head_stride = c.head_stride;
+    p.v_row_stride = c.row_stride;
+    p.scales = c.scales_dev;
+    p.num_pages = c.num_pages;
+    p.requests = a.requests;
+    p.max_keys = a.max_blocks * c.page_size;
+    p.tokens = a.tokens;
+    p.kv_heads = c.kv_heads;
+    p.group = a.heads / c.kv_heads;
+    p.window = a.window;
+    p.page_size = c.page_size;
+    p.scale_log2 = a.scale * 1.44269504088896340736f;
+    p.status = d.status;
+    p.timeout_ns = attend_timeout_ns(d, c, a);
+    return p;
+}
+
+// The two lines of a call with shared prefixes (0: the prefixes, 1: the own tokens) and the
+// places of their buffers in the workspace.
+struct SharedPlan {
+    struct Line {
+        int rows = 8, ctas = 1;
+        size_t off_part = 0, off_ml = 0, off_row = 0, off_row_ml = 0, off_info = 0;
+    } line[2];
+    size_t bytes = 0;
+};
+
+template <class P>
+int shared_call(const DeviceView &d, const w12_kv_cache &c, int rows, int *resident, const P *p,
+                const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+    const bool q8 = c.dtype == W12_KV_Q8;
+    switch (c.head_dim) {
+    case 64: return shared_dim<64>(d, q8, rows, resident, p, tm_k, tm_v, ctas, stream, err);
+    case 128: return shared_dim<128>(d, q8, rows, resident, p, tm_k, tm_v, ctas, stream, err);
+    default: return shared_dim<256>(d, q8, rows, resident, p, tm_k, tm_v, ctas, stream, err);
+    }
+}
+
+int shared_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_args &a, const w12_kv_prefix &x,
+                SharedPlan *plan, std::string *err) {
+    const int group = a.heads / c.kv_heads, max_new = std::max(a.max_new, 1);
+    const bool q8 = c.dtype == W12_KV_Q8;
+    const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    size_t at = 0;
+    for (int i = 0; i < 2; ++i) {
+        SharedPlan::Line &l = plan->line[i];
+        const int spans = i == 0 ? x.groups : a.requests;
+        const int64_t tokens = i == 0 ? std::min<int64_t>((int64_t)std::max(x.max_requests, 1) * max_new, a.tokens) : max_new;
+        l.rows = attend_rows((int)std::min<int64_t>(tokens, 1 << 20), group, c.kv_heads, spans, q8, d.sm_count);
+        int resident = 0;
+        const int rc = i == 0 ? shared_call<dev::KvPrefixParams>(d, c, l.rows, &resident, nullptr, nullptr, nullptr, 0,
+                                                                 nullptr, err)
+                              : shared_call<dev::KvOwnParams>(d, c, l.rows, &resident, nullptr, nullptr, nullptr, 0,
+                                                              nullptr, err);
+        if (rc != W12_OK) return rc;
+        // no more CTAs than units can exist
+        const int64_t blocks = spans + (int64_t)a.tokens * group / l.rows;
+        const int64_t tiles = ((int64_t)a.max_blocks * c.page_size + dev::kAttendTile - 1) / dev::kAttendTile;
+        l.ctas = (int)std::min<int64_t>(resident, std::max<int64_t>(1, blocks * c.kv_heads * tiles));
+        const size_t slots = (size_t)2 * l.ctas * l.rows, rows = (size_t)a.tokens * a.heads;
+        l.off_part = at, at += up(slots * c.head_dim * sizeof(float));
+        l.off_ml = at, at += up(slots * sizeof(float2));
+        l.off_row = at, at += up(rows * c.head_dim * sizeof(float));
+        l.off_row_ml = at, at += up(rows * sizeof(float2));
+        l.off_info = at, at += up(rows * sizeof(int2));
+    }
+    plan->bytes = at;
     return W12_OK;
 }
 
@@ -267,6 +375,102 @@ int kv_read(const w12_kv_cache &c, const int64_t *slots, int32_t tokens, uint16_
     return W12_OK;
 }
 
+int kv_fork(const w12_kv_fork_args &a, void *stream, std::string *err) {
+    DeviceView d;
+    const int rc = device_view(&d, err);
+    if (rc != W12_OK) return rc;
+    dev::KvForkParams p;
+    p.parents = a.parents;
+    p.lens = a.lens;
+    p.lens_out = a.lens_out;
+    p.owned = a.owned;
+    p.tables = a.tables;
+    p.table_stride = a.table_stride;
+    p.ring = a.ring;
+    p.state = a.ring_state;
+    p.shares = a.shares;
+    p.src = a.src;
+    p.dst = a.dst;
+    p.rows = a.rows;
+    p.prefix_cu = a.prefix_cu;
+    p.prefix_lens = a.prefix_lens;
+    p.num_pages = a.num_pages;
+    p.ring_inv = ~uint64_t(0) / (uint64_t)a.ring_size;
+    p.requests = a.requests;
+    p.max_blocks = a.max_blocks;
+    p.page_size = a.page_size;
+    p.ring_size = a.ring_size;
+    p.groups = a.groups;
+    p.status = d.status;
+    const void *kernel = reinterpret_cast<const void *>(&dev::w12_kv_fork_kernel);
+    static std::mutex mu;
+    static bool set[kKvMaxDevices] = {};
+    cudaError_t e = cudaSuccess;
+    if (d.device >= 0 && d.device < kKvMaxDevices) {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!set[d.device]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         dev::fork_smem(dev::kForkRows));
+            if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_fork set-up", err);
+            set[d.device] = true;
+        }
+    }
+    // a CTA for every chunk of columns, as far as a cluster goes; one where that is little
+    const int chunks = (a.max_blocks + dev::kForkCols - 1) / dev::kForkCols;
+    int cluster = 1;
+    while (cluster < 16 && cluster < chunks && (int64_t)chunks * dev::kForkCols * a.requests > cluster * 1024) cluster *= 2;
+    e = kv_launch(d, &dev::w12_kv_fork_kernel, dim3((unsigned)cluster), dev::kForkThreads, dev::fork_smem(a.requests),
+                  cluster, stream, p);
+    if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_fork launch", err);
+    return W12_OK;
+}
+
+int kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, const int32_t *dst, const int32_t *rows,
+            int32_t pairs, void *stream, std::string *err) {
+    DeviceView d;
+    const int rc = device_view(&d, err);
+    if (rc != W12_OK) return rc;
+    if (pairs == 0) return W12_OK;
+    const w12_kv_cache &c = caches[0];
+    const bool q8 = c.dtype == W12_KV_Q8;
+    const int64_t elem = q8 ? 1 : 2;
+    dev::KvCopyParams p;
+    p.src = src;
+    p.dst = dst;
+    p.rows = rows;
+    p.num_pages = c.num_pages;
+    p.page_bytes = c.page_stride * elem;
+    p.head_bytes = c.head_stride * elem;
+    p.row_bytes = c.row_stride * elem;
+    p.pairs = pairs;
+    p.page_size = c.page_size;
+    p.kv_heads = c.kv_heads;
+    const int32_t slices = c.page_size / dev::kCopySlice;
+    p.slices_inv = ~uint64_t(0) / (uint64_t)slices;
+    p.heads_inv = ~uint64_t(0) / (uint64_t)c.kv_heads;
+    p.pairs_inv = ~uint64_t(0) / (uint64_t)pairs;
+    p.status = d.status;
+    const auto kernel = c.head_dim == 64    ? q8 ? &dev::w12_kv_copy_kernel<64, true> : &dev::w12_kv_copy_kernel<128, false>
+                        : c.head_dim == 128 ? q8 ? &dev::w12_kv_copy_kernel<128, true> : &dev::w12_kv_copy_kernel<256, false>
+                                            : q8 ? &dev::w12_kv_copy_kernel<256, true> : &dev::w12_kv_copy_kernel<512, false>;
+    for (int32_t i0 = 0; i0 < count; i0 += dev::kCopyCaches) {
+        const int32_t n = std::min(count - i0, dev::kCopyCaches);
+        for (int32_t i = 0; i < n; ++i) {
+            p.k[i] = static_cast<uint8_t *>(caches[i0 + i].k_dev);
+            p.v[i] = static_cast<uint8_t *>(caches[i0 + i].v_dev);
+            p.scales[i] = caches[i0 + i].scales_dev;
+        }
+        p.items = (int64_t)n * pairs * c.kv_heads * slices * 2;
+        const int64_t warps = dev::kCopyThreads / 32;
+        const int64_t grid = std::min<int64_t>((p.items + warps - 1) / warps, (int64_t)d.sm_count * 64);
+        const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)grid), dev::kCopyThreads, 0, 1, stream, p);
+        if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_copy launch", err);
+    }
+    return W12_OK;
+}
+
 int kv_attend_workspace_size(const w12_kv_cache &c, const w12_kv_attend_args &a, size_t *bytes, std::string *err) {
     DeviceView d;
     int rc = device_view(&d, err);
@@ -295,42 +499,89 @@ int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspac
     if (rc == W12_OK) rc = cache_map(c, tc, c.v_dev, &tm_v, err);
     if (rc != W12_OK) return rc;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    dev::KvAttendParams p;
-    p.q = a.q;
-    p.out = a.out;
-    p.lse = a.lse;
-    p.q_stride = a.q_stride;
-    p.out_stride = a.out_stride;
-    p.tables = a.tables;
-    p.table_stride = a.table_stride;
-    p.lens = a.lens;
-    p.cu_new = a.cu_new;
-    p.tree = a.tree;
-    p.positions = a.tree && a.window > 0 ? a.positions : nullptr;
-    p.v = static_cast<const uint16_t *>(c.v_dev);
-    p.v_page_stride = c.page_stride;
-    p.v_head_stride = c.head_stride;
-    p.v_row_stride = c.row_stride;
-    p.scales = c.scales_dev;
-    p.num_pages = c.num_pages;
-    p.requests = a.requests;
-    p.max_keys = a.max_blocks * c.page_size;
-    p.tokens = a.tokens;
-    p.kv_heads = c.kv_heads;
-    p.group = a.heads / c.kv_heads;
-    p.window = a.window;
-    p.page_size = c.page_size;
-    p.scale_log2 = a.scale * 1.44269504088896340736f;
+    dev::KvAttendParams p = attend_params(d, c, a);
     p.counters = reinterpret_cast<uint32_t *>(ws + plan.off_counters);
     p.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
     p.part = reinterpret_cast<float *>(ws);
     p.n_counters = plan.n_counters;
     p.join_later = join_warps(plan.rows, p.group, c.kv_heads, a.max_new, a.requests, plan.ctas);
-    p.status = d.status;
-    p.timeout_ns = attend_timeout_ns(d, c, a);
     int resident = 0;
     const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
     return attend_call(d, c, plan.rows, &resident, &p, &tm_k, &tm_v, plan.ctas, stream, err);
+}
+
+int kv_attend_shared_workspace_size(const w12_kv_cache &c, const w12_kv_attend_args &a, const w12_kv_prefix &prefix,
+                                    size_t *bytes, std::string *err) {
+    DeviceView d;
+    int rc = device_view(&d, err);
+    if (rc != W12_OK) return rc;
+    SharedPlan plan;
+    rc = shared_plan(d, c, a, prefix, &plan, err);
+    if (rc == W12_OK) *bytes = plan.bytes;
+    return rc;
+}
+
+int kv_attend_shared(const w12_kv_cache &c, const w12_kv_attend_args &a, const w12_kv_prefix &prefix, void *workspace,
+                     size_t ws_bytes, void *stream, std::string *err) {
+    DeviceView d;
+    int rc = device_view(&d, err);
+    if (rc != W12_OK) return rc;
+    SharedPlan plan;
+    rc = shared_plan(d, c, a, prefix, &plan, err);
+    if (rc != W12_OK) return rc;
+    if (ws_bytes < plan.bytes) {
+        *err = "workspace smaller than w12_kv_attend_shared_workspace_size";
+        return W12_ERR_BUFFER_TOO_SMALL;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    dev::KvPrefixParams head;
+    dev::KvOwnParams own;
+    CUtensorMap tm[2][2];
+    dev::KvSharedJoin join;
+    for (int i = 0; i < 2; ++i) {
+        const SharedPlan::Line &l = plan.line[i];
+        const bool tc = l.rows == dev::kTcRows, again = i == 1 && tc == (plan.line[0].rows == dev::kTcRows);
+        if (again) {
+            tm[1][0] = tm[0][0], tm[1][1] = tm[0][1];
+        } else {
+            rc = cache_map(c, tc, c.k_dev, &tm[i][0], err);
+            if (rc == W12_OK) rc = cache_map(c, tc, c.v_dev, &tm[i][1], err);
+            if (rc != W12_OK) return rc;
+        }
+        dev::KvSharedParams &p = i == 0 ? static_cast<dev::KvSharedParams &>(head) : own;
+        static_cast<dev::KvAttendParams &>(p) = attend_params(d, c, a);
+        if (i == 0) p.tree = nullptr;  // all of a prefix is seen
+        p.prefix_cu = prefix.cu;
+        p.prefix_lens = prefix.lens;
+        p.groups = prefix.groups;
+        p.part = reinterpret_cast<float *>(ws + l.off_part);
+        p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
+        p.row_part = reinterpret_cast<float *>(ws + l.off_row);
+        p.row_ml = reinterpret_cast<float2 *>(ws + l.off_row_ml);
+        p.row_info = reinterpret_cast<int2 *>(ws + l.off_info);
+        join.line[i] = {p.part, p.row_part, p.part_ml, p.row_ml, p.row_info, l.rows};
+    }
+    join.out = a.out;
+    join.lse = a.lse;
+    join.out_stride = a.out_stride;
+    join.cu_new = a.cu_new;
+    join.tokens = a.tokens;
+    join.heads = a.heads;
+    join.requests = a.requests;
+    int resident = 0;
+    const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
+    rc = shared_call(d, c, plan.line[0].rows, &resident, &head, &tm[0][0], &tm[0][1], plan.line[0].ctas, stream, err);
+    if (rc == W12_OK)
+        rc = shared_call(d, c, plan.line[1].rows, &resident, &own, &tm[1][0], &tm[1][1], plan.line[1].ctas, stream, err);
+    if (rc != W12_OK) return rc;
+    const int64_t rows = (int64_t)a.tokens * a.heads, per = dev::kJoinThreads / 32;
+    const auto kernel = c.head_dim == 64    ? &dev::w12_kv_join_shared_kernel<64>
+                        : c.head_dim == 128 ? &dev::w12_kv_join_shared_kernel<128>
+                                            : &dev::w12_kv_join_shared_kernel<256>;
+    const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)((rows + per - 1) / per)), dev::kJoinThreads, 0, 1, stream,
+                                    join);
+    if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend_shared join launch", err);
+    return W12_OK;
 }
 
 }  // namespace launch

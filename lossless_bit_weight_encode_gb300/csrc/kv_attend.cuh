@@ -45,6 +45,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kv_common.cuh"
 #include "w12_device.cuh"
 
@@ -180,6 +182,76 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttendParams &p, int b) 
     return r;
 }
 
+// Where a request's page numbers are.
+__device__ __forceinline__ const int32_t *kv_table_row(const KvAttendParams &p, int b) {
+    return p.tables + (int64_t)b * p.table_stride;
+}
+
+// With shared prefixes: the tokens that request b shares with its group, whole pages.
+__device__ __forceinline__ int32_t kv_shared_tokens(const KvSharedParams &p, int b) {
+    const int32_t n = min(max(p.prefix_lens[b], 0), min(max(p.lens[b], 0), p.max_keys));
+    return n / p.page_size * p.page_size;
+}
+
+// What a request has of its own: its table and its tokens begin behind the prefix.
+template <int ROWS, int TILE>
+__device__ __forceinline__ KvRequest kv_request(const KvOwnParams &p, int b) {
+    const int32_t shared = kv_shared_tokens(p, b);
+    KvRequest r;
+    r.q0 = min(max(p.cu_new[b], 0), p.tokens);
+    r.qlen = min(max(p.cu_new[b + 1], r.q0), p.tokens) - r.q0;
+    r.past = min(max(p.lens[b], 0), p.max_keys) - shared;
+    r.kv = (int32_t)min((int64_t)r.past + r.qlen, (int64_t)p.max_keys - shared);
+    r.first = r.tile0 = 0;
+    r.ntiles = r.kv > 0 ? (r.kv - 1) / TILE + 1 : 1;
+    r.rblocks = (int32_t)(((int64_t)r.qlen * p.group + ROWS - 1) / ROWS);
+    r.units = (int64_t)p.kv_heads * r.rblocks * r.ntiles;
+    return r;
+}
+__device__ __forceinline__ const int32_t *kv_table_row(const KvOwnParams &p, int b) {
+    return p.tables + (int64_t)b * p.table_stride + kv_shared_tokens(p, b) / p.page_size;
+}
+
+// A group's prefix, that of the first of its requests that shares one (-1: none does).
+__device__ __forceinline__ int kv_leader(const KvPrefixParams &p, int b0, int b1) {
+    for (int b = b0; b < b1; ++b)
+        if (kv_shared_tokens(p, b) > 0) return b;
+    return -1;
+}
+__device__ __forceinline__ void kv_group(const KvPrefixParams &p, int g, int &b0, int &b1) {
+    b0 = min(max(p.prefix_cu[g], 0), p.requests);
+    b1 = min(max(p.prefix_cu[g + 1], b0), p.requests);
+}
+// The group as a request: the new tokens of all its requests, which see all of the prefix.
+// (The rows of a request in it that shares nothing are not joined with what comes out.)
+template <int ROWS, int TILE>
+__device__ __forceinline__ KvRequest kv_request(const KvPrefixParams &p, int g) {
+    int b0, b1;
+    kv_group(p, g, b0, b1);
+    const int lead = kv_leader(p, b0, b1);
+    KvRequest r;
+    r.past = r.kv = lead < 0 ? 0 : kv_shared_tokens(p, lead);
+    r.q0 = min(max(p.cu_new[b0], 0), p.tokens);
+    r.qlen = lead < 0 ? 0 : min(max(p.cu_new[b1], r.q0), p.tokens) - r.q0;
+    r.first = r.tile0 = 0;
+    r.ntiles = r.kv > 0 ? (r.kv - 1) / TILE + 1 : 1;
+    r.rblocks = (int32_t)(((int64_t)r.qlen * p.group + ROWS - 1) / ROWS);
+    r.units = (int64_t)p.kv_heads * r.rblocks * r.ntiles;
+    return r;
+}
+__device__ __forceinline__ const int32_t *kv_table_row(const KvPrefixParams &p, int g) {
+    int b0, b1;
+    kv_group(p, g, b0, b1);
+    return p.tables + (int64_t)max(kv_leader(p, b0, b1), 0) * p.table_stride;
+}
+
+// What a launch's line has: requests, or groups.
+__device__ __forceinline__ int32_t kv_spans(const KvAttendParams &p) { return p.requests; }
+__device__ __forceinline__ int32_t kv_spans(const KvPrefixParams &p) { return p.groups; }
+
+template <class P>
+constexpr bool kKvShared = !std::is_same_v<P, KvAttendParams>;
+
 // A CTA's range of units and its place in it; every warp keeps its own copy.
 struct KvWalk {
     int64_t total, u, end;  // all units, the next one, the range's end
@@ -194,16 +266,17 @@ struct KvSums {
     int32_t per;            // requests of a block
 };
 
-template <int ROWS, int TILE>
-__device__ __forceinline__ KvSums kv_sum_units(const KvAttendParams &p) {
+template <int ROWS, int TILE, class P>
+__device__ __forceinline__ KvSums kv_sum_units(const P &p) {
     const int lane = threadIdx.x & 31;
     KvSums s;
-    s.per = (int32_t)(((uint32_t)p.requests + 31u) / 32u);
+    const int32_t spans = kv_spans(p);
+    s.per = (int32_t)(((uint32_t)spans + 31u) / 32u);
     int64_t sum = 0;
 #pragma unroll 4
     for (int i = 0; i < s.per; ++i) {
         const int b = lane * s.per + i;
-        if (b < p.requests) sum += kv_request<ROWS, TILE>(p, b).units;
+        if (b < spans) sum += kv_request<ROWS, TILE>(p, b).units;
     }
     int64_t inc = sum;
 #pragma unroll
@@ -216,8 +289,8 @@ __device__ __forceinline__ KvSums kv_sum_units(const KvAttendParams &p) {
     return s;
 }
 
-template <int ROWS, int TILE>
-__device__ __forceinline__ bool kv_walk_init(const KvAttendParams &p, KvWalk &w, KvRequest &r) {
+template <int ROWS, int TILE, class P>
+__device__ __forceinline__ bool kv_walk_init(const P &p, KvWalk &w, KvRequest &r) {
     const KvSums s = kv_sum_units<ROWS, TILE>(p);
     w.total = s.total;
     w.ctas = (int32_t)min((int64_t)gridDim.x, w.total);
@@ -258,8 +331,8 @@ __device__ __forceinline__ KvPiece kv_piece(const KvWalk &w, const KvRequest &r)
 }
 
 // Moves on by n units within the request, to the next request where it ends.
-template <int ROWS, int TILE>
-__device__ __forceinline__ void kv_advance(const KvAttendParams &p, KvWalk &w, KvRequest &r, int32_t n) {
+template <int ROWS, int TILE, class P>
+__device__ __forceinline__ void kv_advance(const P &p, KvWalk &w, KvRequest &r, int32_t n) {
     w.u += n;
     while (w.u < w.end && w.u >= w.start + r.units) {
         w.start += r.units;
@@ -333,6 +406,16 @@ __device__ __forceinline__ void kv_emit(const KvAttendParams &p, const KvRequest
         p.lse[(int64_t)tok * (p.group * p.kv_heads) + h] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
 }
 
+// With shared prefixes nothing is finished yet: the sums as they are.
+template <int ROWS, int D>
+__device__ __forceinline__ void kv_emit(const KvSharedParams &p, const KvRequest &r, const KvPiece &c, int lr, int col,
+                                        float mm, float sum, const float4 &acc) {
+    const int32_t rr = c.rb * ROWS + lr, i = rr / p.group, tok = r.q0 + i, h = c.head * p.group + rr - i * p.group;
+    const int64_t at = (int64_t)tok * (p.group * p.kv_heads) + h;
+    *reinterpret_cast<float4 *>(p.row_part + at * D + col) = acc;
+    if (col == 0) p.row_ml[at] = make_float2(mm, sum);
+}
+
 // A row block whose keys several CTAs shared: where its parts are and its counter.
 struct KvParts {
     int64_t first;  // row of the first CTA's first slot
@@ -351,6 +434,39 @@ __device__ __forceinline__ KvParts kv_parts(const KvAttendParams &p, const KvWal
     q.counter = c.head + (int64_t)p.kv_heads * (w.b + (int64_t)r.q0 * p.group / ROWS + c.rb);
     q.n = c1 - c0 + 1;
     return q;
+}
+
+// Where the joining kernel finds row lr of the piece's block; written by the CTA that has
+// the block's first unit.
+template <int ROWS, class P>
+__device__ __forceinline__ void kv_note(const P &p, const KvWalk &w, const KvRequest &r, const KvPiece &c, int lr,
+                                        bool whole) {
+    const int32_t rr = c.rb * ROWS + lr, i = rr / p.group;
+    const int64_t at = (int64_t)(r.q0 + i) * (p.group * p.kv_heads) + c.head * p.group + rr - i * p.group;
+    int2 info = make_int2(0, 1);
+    if (!whole) {
+        const KvParts q = kv_parts<ROWS>(p, w, r, c);
+        info = make_int2((int32_t)q.first + lr, q.n);
+    }
+    if constexpr (std::is_same_v<P, KvOwnParams>) {
+        if (kv_shared_tokens(p, w.b) > 0) info.y |= kKvSharesPrefix;
+        if (lr == 0 && kv_shared_tokens(p, w.b) != max(p.prefix_lens[w.b], 0)) atomicOr(p.status, kStatusKvSizes);
+    }
+    p.row_info[at] = info;
+}
+
+// How the launches of one call with shared prefixes follow one another: the one over the
+// prefixes is first and waits for what is before the call; the one over the own tokens
+// begins when every CTA of that has done so, with a fence for what its SM's L1 has had
+// since before, and takes the SMs as they become free; it ends when the first one has.
+template <class P>
+__device__ __forceinline__ void kv_begin() {
+    if constexpr (std::is_same_v<P, KvOwnParams>) __threadfence();
+    else pdl_wait();
+}
+template <class P>
+__device__ __forceinline__ void kv_end() {
+    if constexpr (std::is_same_v<P, KvOwnParams>) pdl_wait();
 }
 
 // Called by the 128 consumer threads when they have written the CTA's part to its
@@ -459,8 +575,8 @@ struct KvPageWindow {
     }
 };
 
-template <int D, bool Q8, int WK, int WR, int NT>
-__global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_kv_attend_kernel(const KvAttendParams p,
+template <int D, bool Q8, int WK, int WR, int NT, class P = KvAttendParams>
+__global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_kv_attend_kernel(const P p,
                                                                        const __grid_constant__ CUtensorMap tm_k,
                                                                        const __grid_constant__ CUtensorMap tm_v) {
     using C = AttendCfg<D, Q8, WK, WR, NT>;
@@ -487,13 +603,16 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
         prefetch_tmap(&tm_v);
     }
     __syncthreads();
-    pdl_wait();
+    kv_begin<P>();
     pdl_launch_dependents();  // after the wait: w12_kv_join_kernel relies on it
     const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
 
     KvWalk w;
     KvRequest r;
-    if (!kv_walk_init<ROWS, TILE>(p, w, r)) return;  // the same for the whole CTA
+    if (!kv_walk_init<ROWS, TILE>(p, w, r)) {  // the same for the whole CTA
+        kv_end<P>();
+        return;
+    }
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
@@ -502,8 +621,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
         while (ok && w.u < w.end) {
             const KvPiece c = kv_piece(w, r);
             KvPageWindow pages;
-            pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * TILE / p.page_size,
-                        kv_entries(p, r));
+            pages.start(kv_table_row(p, w.b), (r.tile0 + c.ja) * TILE / p.page_size, kv_entries(p, r));
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
                 const uint32_t stage = it % C::kStages, round = it / C::kStages;
                 // lane s deals with slice s
@@ -545,6 +663,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
             }
             __syncwarp();
         }
+        kv_end<P>();
         return;
     }
 
@@ -915,6 +1034,8 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
                     sum += f * s.y;
                     acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
                 }
+                if constexpr (kKvShared<P>)
+                    if (c.ja == 0 && dc == 0 && v4 == 0) kv_note<ROWS>(p, w, r, c, lr, whole);
                 if (whole) {
                     kv_emit<ROWS, D>(p, r, c, lr, dc * 64 + v4 * 4, mm, sum, acc);
                 } else {
@@ -925,10 +1046,12 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
             consumers_sync();
         }
 
-        if (!whole && !p.join_later) {
-            const KvParts q = kv_parts<ROWS>(p, w, r, c);
-            if (kv_arrive(p, q, last_flag))
-                kv_join<ROWS, D, C::kCtas < 3 ? 8 : 4>(p, q, r, c, nrows, (int)threadIdx.x, 128);
+        if constexpr (!kKvShared<P>) {
+            if (!whole && !p.join_later) {
+                const KvParts q = kv_parts<ROWS>(p, w, r, c);
+                if (kv_arrive(p, q, last_flag))
+                    kv_join<ROWS, D, C::kCtas < 3 ? 8 : 4>(p, q, r, c, nrows, (int)threadIdx.x, 128);
+            }
         }
         kv_advance<ROWS, TILE>(p, w, r, c.jb - c.ja);
     }
@@ -938,6 +1061,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
         for (uint32_t k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
             if (!mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1, late)) break;
     }
+    kv_end<P>();
 }
 
 // Joins the parts of the output rows (token and head, heads fastest) of a launch with

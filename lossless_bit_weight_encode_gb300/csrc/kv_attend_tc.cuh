@@ -345,20 +345,22 @@ struct TcLoader {
     int32_t j;
     uint32_t it;
 
-    __device__ __forceinline__ void open(const KvAttendParams &p) {
+    template <class P>
+    __device__ __forceinline__ void open(const P &p) {
         c = kv_piece(w, r);
         j = c.ja;
-        pages.start(p.tables + (int64_t)w.b * p.table_stride, (r.tile0 + c.ja) * kAttendTile / p.page_size,
-                    kv_entries(p, r));
+        pages.start(kv_table_row(p, w.b), (r.tile0 + c.ja) * kAttendTile / p.page_size, kv_entries(p, r));
     }
-    __device__ __forceinline__ void start(const KvAttendParams &p, const KvWalk &walk, const KvRequest &req) {
+    template <class P>
+    __device__ __forceinline__ void start(const P &p, const KvWalk &walk, const KvRequest &req) {
         w = walk;
         r = req;
         it = 0;
         if (w.u < w.end) open(p);
     }
     // False when a wait ran out.  Nothing happens behind the last tile.
-    __device__ __forceinline__ bool step(const KvAttendParams &p, uint64_t deadline) {
+    template <class P>
+    __device__ __forceinline__ bool step(const P &p, uint64_t deadline) {
         const int lane = threadIdx.x & 31;
         if (w.u >= w.end) return true;
         // lane 4 b + s deals with slice s (and with column block b)
@@ -403,9 +405,9 @@ struct TcLoader {
 // PLACED (a windowed tree with positions) is a kernel of its own: with the choice at run
 // time the tile loop's registers went another way (trees over an 8-bit cache 116 us, 144
 // with the positions looked up in the loop, 118 with nothing but their load there).
-template <int D, bool Q8, bool PLACED>
+template <int D, bool Q8, bool PLACED, class P = KvAttendParams>
 __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q8>::kOne ? 1 : 2)
-    w12_kv_attend_tc_kernel(const KvAttendParams p, const __grid_constant__ CUtensorMap tm_k,
+    w12_kv_attend_tc_kernel(const P p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
     using C = AttendTcCfg<D, Q8>;
     extern __shared__ uint8_t smem_raw[];
@@ -450,11 +452,14 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    pdl_wait();
+    kv_begin<P>();
     const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
     KvWalk w;
     KvRequest r;
-    if (!kv_walk_init<kTcRows, kAttendTile>(p, w, r)) return;  // the same for the whole CTA
+    if (!kv_walk_init<kTcRows, kAttendTile>(p, w, r)) {  // the same for the whole CTA
+        kv_end<P>();
+        return;
+    }
     // TMEM only after the kernel before has finished, and the kernel behind only
     // when every CTA here has its TMEM: neither can then hold columns that the
     // other waits for
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                                 kv_seen64(p, r1.kv, r1.past, kv_row_view<PLACED>(p, r1, i), kb, 15u);
                             for (; seen; seen &= seen - 1) {
                                 const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
-                                const int32_t page = p.tables[(int64_t)w1.b * p.table_stride + e];
+                                const int32_t page = kv_table_row(p, w1.b)[e];
                                 if (page < 0 || page >= p.num_pages) continue;
                                 const uint16_t *v = p.v + page * p.v_page_stride + c1.head * p.v_head_stride +
                                                     (int64_t)(key - e * p.page_size) * p.v_row_stride + d0;
@@ -757,7 +762,13 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             y[k] = __uint_as_float(o[!Q8 || k % 4 == 0 || k % 4 == 3 ? k : k % 4 == 1 ? k + 1 : k - 1]);
-                        if (whole) {
+                        if constexpr (kKvShared<P>) {
+                            const int64_t row = (int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head;
+                            float *to = whole ? p.row_part + row * D : p.part + (slot * kTcRows + lr) * D;
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4)
+                                *reinterpret_cast<float4 *>(to + d0 + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                        } else if (whole) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 8)
                                 *reinterpret_cast<uint4 *>(dst + d0 + k) = make_uint4(
@@ -773,8 +784,12 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                     }
                 }
                 if (half == 0 && lr < nrows) {
+                    if constexpr (kKvShared<P>) {
+                        if (c1.ja == 0) kv_note<kTcRows>(p, w1, r1, c1, lr, whole);
+                        if (whole) p.row_ml[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] = make_float2(m, l);
+                    }
                     if (!whole) p.part_ml[slot * kTcRows + lr] = make_float2(m, l);
-                    else if (p.lse)
+                    else if (!kKvShared<P> && p.lse)
                         p.lse[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] =
                             l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
@@ -976,6 +991,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
     __syncthreads();
     tc_fence_after();
     if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
+    kv_end<P>();
 }
 
 }  // namespace dev

@@ -87,6 +87,22 @@ struct KvAttendParams {
     uint64_t timeout_ns;
 };
 
+// A call with shared prefixes (w12_kv_attend_shared): one launch over the groups' prefixes
+// and one over what the requests have of their own, each a line of units of its own.  No
+// row is finished there: what a CTA has whole goes to row_part and row_ml, and row_info says
+// where a row's parts are: {row of its first part, parts (1: whole; bit 30, of the own
+// line: its request shares a prefix)}.
+struct KvSharedParams : KvAttendParams {
+    const int32_t *prefix_cu, *prefix_lens;
+    int32_t groups;
+    float *row_part;   // [tokens * heads][head_dim]
+    float2 *row_ml;    // [tokens * heads]
+    int2 *row_info;    // [tokens * heads]
+};
+struct KvPrefixParams : KvSharedParams {};
+struct KvOwnParams : KvSharedParams {};
+constexpr int32_t kKvSharesPrefix = 1 << 30;
+
 // Two fp32 to packed BF16, round to nearest even, `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;

@@ -1,4 +1,5 @@
-// Python module `kv_host`: kv.py's calls, from tensors to the C ABI's w12_kv_*.
+// Python module `kv_host`: kv.py's and beam.py's calls, from tensors to the C ABI's w12_kv_*
+// and w12_beam_select.
 //
 // A single token's store or attention runs 2 to 7 us on the GPU, and a step makes
 // two such calls per layer, so the way to the launch counts.  Looking at the tensors
@@ -13,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <limits>
+#include <vector>
 
 #include "w12.h"
 
@@ -26,11 +28,18 @@ struct Abi {
     decltype(&w12_kv_read) read;
     decltype(&w12_kv_attend_workspace_size) workspace_size;
     decltype(&w12_kv_attend) attend;
+    decltype(&w12_kv_fork) fork;
+    decltype(&w12_kv_copy) copy;
+    decltype(&w12_kv_attend_shared_workspace_size) shared_size;
+    decltype(&w12_kv_attend_shared) attend_shared;
+    decltype(&w12_beam_workspace_size) beam_size;
+    decltype(&w12_beam_select) beam_select;
     PyObject *raise;
 } abi = {};
 
 struct Names {
     PyObject *tables, *lens, *cu_new, *positions, *slots, *max_new, *tree, *owned, *ring, *ring_state, *page_size;
+    PyObject *shares, *src, *dst, *rows, *prefix, *cu, *max_requests, *address;
 } names;
 
 // An owned reference.
@@ -252,6 +261,16 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A step's prefix (None: none; so it is for a step that knows of none).
+Ref prefix_of(PyObject *step) {
+    PyObject *o = PyObject_GetAttr(step, names.prefix);
+    if (!o && PyErr_ExceptionMatches(PyExc_AttributeError)) {
+        PyErr_Clear();
+        o = Py_NewRef(Py_None);
+    }
+    return Ref(o);
+}
+
 // attend(cache, index, q, step, scale, window, out, lse, workspace, grow, stream):
 // grow(device, stream, bytes) makes a workspace where `workspace` is None or, found
 // by kv.py and not given by the caller (grow not None), too small.
@@ -305,10 +324,24 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Rows o = rows(out, dim, "out", index, q.heads);
     TORCH_CHECK_VALUE(o.tokens == q.tokens, "out and q must have as many tokens");
     s.out = o.p, s.out_stride = o.stride;
+    const Ref prefix_o = prefix_of(a[3]);
+    const bool shared = prefix_o.get() != Py_None;
+    w12_kv_prefix prefix = {};
+    if (shared) {
+        const Ref pcu_o = field(prefix_o.get(), names.cu), plens_o = field(prefix_o.get(), names.lens),
+                  most_o = field(prefix_o.get(), names.max_requests);
+        const at::Tensor &pcu = tensor(pcu_o.get(), "step.prefix.cu"), &plens = tensor(plens_o.get(), "step.prefix.lens");
+        prefix.cu = ints<int32_t>(pcu, "step.prefix.cu", index);
+        prefix.lens = ints<int32_t>(plens, "step.prefix.lens", index);
+        TORCH_CHECK_VALUE(plens.numel() == requests && pcu.numel() >= 2,
+                          "step.prefix.lens must have an entry per request and cu one more than groups");
+        prefix.groups = int32(pcu.numel() - 1, "the number of groups");
+        prefix.max_requests = int32(integer(most_o.get()), "step.prefix.max_requests");
+    }
     if (s.tokens) {
         PyObject *ws_o = a[8];
         size_t bytes = 0;
-        check(abi.workspace_size(c, &s, &bytes));
+        check(shared ? abi.shared_size(c, &s, &prefix, &bytes) : abi.workspace_size(c, &s, &bytes));
         const auto size = [](PyObject *t) { return tensor(t, "workspace").nbytes(); };
         Ref grown(a[9] != Py_None && (ws_o == Py_None || size(ws_o) < bytes)
                       ? PyObject_CallFunction(a[9], "LOn", static_cast<long long>(index), a[10],
@@ -319,7 +352,9 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
                           "workspace must be contiguous, on the cache's device");
         void *p = ws.data_ptr(), *stream = pointer<void>(a[10]);
         const size_t have = ws.nbytes();
-        call([&] { return abi.attend(c, &s, p, have, stream); });
+        call([&] {
+            return shared ? abi.attend_shared(c, &s, &prefix, p, have, stream) : abi.attend(c, &s, p, have, stream);
+        });
     }
     if (a[6] != Py_None) return Py_NewRef(a[6]);
     return THPVariable_Wrap(out);
@@ -380,25 +415,181 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(plan, store, read, workspace_size, attend, raise): the C ABI's addresses
+// fork(pages, index, parents, lens, copies, prefix, lens_out, stream)
+PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 8);
+    const int64_t index = integer(a[1]);
+    const Ref tables_o = field(a[0], names.tables), owned_o = field(a[0], names.owned), ring_o = field(a[0], names.ring),
+              state_o = field(a[0], names.ring_state), page_o = field(a[0], names.page_size),
+              shares_o = field(a[0], names.shares), src_o = field(a[4], names.src), dst_o = field(a[4], names.dst),
+              rows_o = field(a[4], names.rows);
+    TORCH_CHECK_VALUE(shares_o.get() != Py_None, "fork needs pages with shares (KVPages.create(..., shared=True))");
+    const at::Tensor &tables = tensor(tables_o.get(), "tables"), &owned = tensor(owned_o.get(), "owned"),
+                     &ring = tensor(ring_o.get(), "ring"), &state = tensor(state_o.get(), "ring_state"),
+                     &shares = tensor(shares_o.get(), "shares"), &parents = tensor(a[2], "parents"),
+                     &lens = tensor(a[3], "lens"), &src = tensor(src_o.get(), "copies.src"),
+                     &dst = tensor(dst_o.get(), "copies.dst"), &rows = tensor(rows_o.get(), "copies.rows");
+    TORCH_CHECK_VALUE(tables.dim() == 2 && tables.scalar_type() == at::kInt && tables.stride(1) == 1 &&
+                          tables.get_device() == index,
+                      "tables must be an int32 CUDA tensor [requests, max_blocks] with contiguous rows");
+    const int64_t requests = tables.size(0);
+    TORCH_CHECK_VALUE(parents.numel() == requests && lens.numel() == requests && owned.numel() == requests &&
+                          src.numel() == requests && dst.numel() == requests && rows.numel() == requests &&
+                          state.numel() == 2,
+                      "parents, lens and copies must be on the tables' device, with an entry per request");
+    w12_kv_fork_args s = {};
+    s.parents = ints<int32_t>(parents, "parents", index);
+    s.lens = ints<int32_t>(lens, "lens", index);
+    s.owned = ints<int32_t>(owned, "owned", index);
+    s.tables = static_cast<int32_t *>(tables.data_ptr());
+    s.table_stride = requests > 1 ? tables.stride(0) : tables.size(1);
+    s.ring = ints<int32_t>(ring, "ring", index);
+    s.ring_state = ints<int64_t>(state, "ring_state", index);
+    s.shares = ints<int32_t>(shares, "shares", index);
+    s.src = ints<int32_t>(src, "copies.src", index);
+    s.dst = ints<int32_t>(dst, "copies.dst", index);
+    s.rows = ints<int32_t>(rows, "copies.rows", index);
+    s.num_pages = shares.numel();
+    s.requests = int32(requests, "the number of requests");
+    s.max_blocks = int32(tables.size(1), "the tables' width");
+    s.page_size = int32(integer(page_o.get()), "page_size");
+    s.ring_size = int32(ring.numel(), "the ring's length");
+    if (a[5] != Py_None) {
+        const Ref cu_o = field(a[5], names.cu), lens_o = field(a[5], names.lens);
+        const at::Tensor &cu = tensor(cu_o.get(), "prefix.cu"), &plens = tensor(lens_o.get(), "prefix.lens");
+        s.prefix_cu = ints<int32_t>(cu, "prefix.cu", index);
+        s.prefix_lens = ints<int32_t>(plens, "prefix.lens", index);
+        TORCH_CHECK_VALUE(plens.numel() == requests && cu.numel() >= 2,
+                          "prefix.lens must have an entry per request and cu one more than groups");
+        s.groups = int32(cu.numel() - 1, "the number of groups");
+    }
+    if (a[6] != Py_None) {
+        const at::Tensor &t = tensor(a[6], "lens_out");
+        s.lens_out = ints<int32_t>(t, "lens_out", index);
+        TORCH_CHECK_VALUE(t.numel() == requests, "lens_out must have an entry per request");
+    }
+    void *stream = pointer<void>(a[7]);
+    call([&] { return abi.fork(&s, stream); });
+    return Py_NewRef(a[4]);
+    END_HANDLE_TH_ERRORS
+}
+
+// copy(cache, index, others, copies, stream)
+PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 5);
+    const int64_t index = integer(a[1]);
+    std::vector<w12_kv_cache> caches = {*pointer<const w12_kv_cache>(a[0])};
+    const Ref others(PySequence_Fast(a[2], "others must be a sequence of caches"));
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(others.get()); ++i) {
+        const Ref address = field(PySequence_Fast_GET_ITEM(others.get(), i), names.address);
+        caches.push_back(*pointer<const w12_kv_cache>(address.get()));
+    }
+    const Ref src_o = field(a[3], names.src), dst_o = field(a[3], names.dst), rows_o = field(a[3], names.rows);
+    const at::Tensor &src = tensor(src_o.get(), "copies.src"), &dst = tensor(dst_o.get(), "copies.dst");
+    const int32_t *from = ints<int32_t>(src, "copies.src", index), *to = ints<int32_t>(dst, "copies.dst", index);
+    const int32_t *rows = nullptr;
+    TORCH_CHECK_VALUE(src.numel() == dst.numel(), "copies must have as many src as dst");
+    if (rows_o.get() != Py_None) {
+        const at::Tensor &t = tensor(rows_o.get(), "copies.rows");
+        rows = ints<int32_t>(t, "copies.rows", index);
+        TORCH_CHECK_VALUE(t.numel() == src.numel(), "copies must have as many rows as src");
+    }
+    const int32_t pairs = int32(src.numel(), "the number of copies");
+    void *stream = pointer<void>(a[4]);
+    if (pairs)
+        call([&] { return abi.copy(caches.data(), (int32_t)caches.size(), from, to, rows, pairs, stream); });
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// select(args, index, logits, allowed, scores, workspace, grow, stream): args is the
+// holder's struct with its outputs; logits [requests * beams, vocab] or [requests, beams, vocab]
+PyObject *select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 8);
+    w12_beam_args s = *pointer<const w12_beam_args>(a[0]);
+    const int64_t index = integer(a[1]), rows = (int64_t)s.requests * s.beams;
+    const at::Tensor &logits = tensor(a[2], "logits");
+    bool good = logits.get_device() == index &&
+                (logits.scalar_type() == at::kBFloat16 || logits.scalar_type() == at::kFloat);
+    if (good && logits.dim() == 2) {
+        good = logits.size(0) == rows;
+        s.logits_stride = rows > 1 ? logits.stride(0) : logits.size(1);
+    } else {
+        good = good && logits.dim() == 3 && logits.size(0) == s.requests && logits.size(1) == s.beams;
+        if (good) {
+            s.logits_stride = s.beams > 1 ? logits.stride(1) : s.requests > 1 ? logits.stride(0) : logits.size(2);
+            good = s.requests == 1 || logits.stride(0) == s.beams * s.logits_stride;
+        }
+    }
+    good = good && (logits.stride(-1) == 1 || logits.size(-1) == 1);
+    TORCH_CHECK_VALUE(good, "logits must be BF16 or fp32 [", rows, ", vocab] on CUDA device ", index,
+                      " with contiguous rows");
+    s.logits = logits.data_ptr();
+    s.dtype = logits.scalar_type() == at::kBFloat16 ? W12_BEAM_BF16 : W12_BEAM_F32;
+    s.vocab = int32(logits.size(-1), "the vocabulary");
+    if (a[3] != Py_None) {
+        const at::Tensor &t = tensor(a[3], "allowed");
+        const int64_t words = (s.vocab + 31LL) / 32;
+        const bool one = t.dim() == 1;
+        TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.get_device() == index && (one || t.dim() == 2) &&
+                              t.size(-1) == words && (t.stride(-1) == 1 || words == 1) && (one || t.size(0) == rows),
+                          "allowed must be int32 [", rows, ", ", words, "] or [", words, "] on CUDA device ", index,
+                          " with contiguous rows");
+        s.allowed = static_cast<const uint32_t *>(t.data_ptr());
+        s.allowed_stride = one ? 0 : rows > 1 ? t.stride(0) : words;
+        TORCH_CHECK_VALUE(one || s.allowed_stride >= words, "allowed's rows overlap");
+    }
+    if (a[4] != Py_None) {
+        const at::Tensor &t = tensor(a[4], "scores");
+        TORCH_CHECK_VALUE(t.scalar_type() == at::kFloat && t.get_device() == index && t.numel() == rows &&
+                              t.is_contiguous(),
+                          "scores must be contiguous fp32 [requests, beams] on CUDA device ", index);
+        s.scores_in = static_cast<const float *>(t.data_ptr());
+    }
+    size_t bytes = 0;
+    check(abi.beam_size(&s, &bytes));
+    Ref grown(a[5] == Py_None || tensor(a[5], "workspace").nbytes() < bytes
+                  ? PyObject_CallFunction(a[6], "LOn", static_cast<long long>(index), a[7],
+                                          static_cast<Py_ssize_t>(bytes))
+                  : Py_NewRef(a[5]));
+    const at::Tensor &ws = tensor(grown.get(), "workspace");
+    void *p = ws.data_ptr(), *stream = pointer<void>(a[7]);
+    const size_t have = ws.nbytes();
+    call([&] { return abi.beam_select(&s, p, have, stream); });
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// bind(plan, store, read, workspace_size, attend, fork, copy, shared_size, attend_shared,
+// beam_size, beam_select, raise): the C ABI's addresses
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 6);
+    expect(n, 12);
     const auto set = [](auto &f, PyObject *o) { f = reinterpret_cast<std::decay_t<decltype(f)>>(pointer<void>(o)); };
     set(abi.plan, a[0]);
     set(abi.store, a[1]);
     set(abi.read, a[2]);
     set(abi.workspace_size, a[3]);
     set(abi.attend, a[4]);
+    set(abi.fork, a[5]);
+    set(abi.copy, a[6]);
+    set(abi.shared_size, a[7]);
+    set(abi.attend_shared, a[8]);
+    set(abi.beam_size, a[9]);
+    set(abi.beam_select, a[10]);
     Py_XDECREF(abi.raise);
-    abi.raise = Py_NewRef(a[5]);
+    abi.raise = Py_NewRef(a[11]);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
 
 #define W12_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef methods[] = {{"plan", W12_FAST(plan)},     {"store", W12_FAST(store)}, {"read", W12_FAST(read)},
-                         {"attend", W12_FAST(attend)}, {"bind", W12_FAST(bind)},   {nullptr, nullptr, 0, nullptr}};
+                         {"attend", W12_FAST(attend)}, {"fork", W12_FAST(fork)},   {"copy", W12_FAST(copy)},
+                         {"select", W12_FAST(select)}, {"bind", W12_FAST(bind)},   {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "kv_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -406,6 +597,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "kv_host", nullptr, -1, methods, nu
 PyMODINIT_FUNC PyInit_kv_host() {
     const auto name = [](const char *s) { return PyUnicode_InternFromString(s); };
     names = {name("tables"), name("lens"), name("cu_new"), name("positions"), name("slots"), name("max_new"),
-             name("tree"), name("owned"), name("ring"), name("ring_state"), name("page_size")};
+             name("tree"), name("owned"), name("ring"), name("ring_state"), name("page_size"), name("shares"),
+             name("src"), name("dst"), name("rows"), name("prefix"), name("cu"), name("max_requests"),
+             name("_address")};
     return PyModule_Create(&module);
 }

@@ -124,9 +124,9 @@ int attend_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev:
 
 // Occupancy of one kernel on first use (at most `most` CTAs per SM), then (with `p`)
 // its launch.  regs > 0: the registers per thread it has to have been compiled to.
-inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams, CUtensorMap, CUtensorMap), int most,
-                         int threads, int regs, int smem, std::mutex &mu, int *per_sm, int *resident,
-                         const dev::KvAttendParams *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas,
+template <class P>
+int attend_kernel(const DeviceView &d, void (*kernel)(P, CUtensorMap, CUtensorMap), int most, int threads, int regs,
+                  int smem, std::mutex &mu, int *per_sm, int *resident, const P *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas,
                          void *stream, std::string *err) {
     if (d.device < 0 || d.device >= kKvMaxDevices) {
         *err = "device ordinal out of range";
@@ -162,23 +162,23 @@ inline int attend_kernel(const DeviceView &d, void (*kernel)(dev::KvAttendParams
     return W12_OK;
 }
 
-template <int D, bool Q8, int WK, int WR, int NT>
-int attend_variant(const DeviceView &d, int *resident, const dev::KvAttendParams *p, const CUtensorMap *tm_k,
+template <int D, bool Q8, int WK, int WR, int NT, class P>
+int attend_variant(const DeviceView &d, int *resident, const P *p, const CUtensorMap *tm_k,
                    const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     using C = dev::AttendCfg<D, Q8, WK, WR, NT>;
     static std::mutex mu;
     static int per_sm[kKvMaxDevices] = {};
-    return attend_kernel(d, &dev::w12_kv_attend_kernel<D, Q8, WK, WR, NT>, kPartElems / (C::kRows * D),
+    return attend_kernel(d, &dev::w12_kv_attend_kernel<D, Q8, WK, WR, NT, P>, kPartElems / (C::kRows * D),
                          dev::kAttendThreads, 0, C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
-template <int D, bool Q8, bool PLACED>
-int attend_tc_variant(const DeviceView &d, int *resident, const dev::KvAttendParams *p, const CUtensorMap *tm_k,
+template <int D, bool Q8, bool PLACED, class P>
+int attend_tc_variant(const DeviceView &d, int *resident, const P *p, const CUtensorMap *tm_k,
                       const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     using C = dev::AttendTcCfg<D, Q8>;
     static std::mutex mu;
     static int per_sm[kKvMaxDevices] = {};
-    return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8, PLACED>,
+    return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8, PLACED, P>,
                          std::min(kPartElems / (dev::kTcRows * D), 512 / C::kTmemCols), C::kThreads, C::kRegs,
                          C::kSmemBytes, mu, per_sm, resident, p, tm_k, tm_v, ctas, stream, err);
 }
@@ -186,19 +186,30 @@ int attend_tc_variant(const DeviceView &d, int *resident, const dev::KvAttendPar
 // The variants of one head_dim.  With 8 rows the warps split a tile's keys; so they
 // do with 16, but for 256 columns, whose sums for 16 rows do not fit a warp: there
 // they split the rows too.
-template <int D, bool Q8>
-int attend_rows_variant(const DeviceView &d, int rows, int *resident, const dev::KvAttendParams *p,
-                        const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+template <int D, bool Q8, class P>
+int attend_rows_variant(const DeviceView &d, int rows, int *resident, const P *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     switch (rows) {
     case 8: return attend_variant<D, Q8, 4, 1, 1>(d, resident, p, tm_k, tm_v, ctas, stream, err);
     case 16:
         return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(d, resident, p, tm_k, tm_v,
                                                                                           ctas, stream, err);
     default:
-        return p && p->positions ? attend_tc_variant<D, Q8, true>(d, resident, p, tm_k, tm_v, ctas, stream, err)
-                                 : attend_tc_variant<D, Q8, false>(d, resident, p, tm_k, tm_v, ctas, stream, err);
+        if constexpr (dev::kKvShared<P>)
+            return attend_tc_variant<D, Q8, false>(d, resident, p, tm_k, tm_v, ctas, stream, err);
+        else
+            return p && p->positions
+                       ? attend_tc_variant<D, Q8, true>(d, resident, p, tm_k, tm_v, ctas, stream, err)
+                       : attend_tc_variant<D, Q8, false>(d, resident, p, tm_k, tm_v, ctas, stream, err);
     }
 }
+
+// One line of a call with shared prefixes (kv_shared_*.cu), as attend_dim.
+template <int D>
+int shared_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvPrefixParams *p,
+               const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
+template <int D>
+int shared_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvOwnParams *p,
+               const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
 
 }  // namespace launch
 }  // namespace w12

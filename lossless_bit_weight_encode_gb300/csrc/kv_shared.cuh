@@ -1,0 +1,106 @@
+// The last step of attention behind shared prefixes (w12_kv_attend_shared in
+// include/w12.h).
+//
+// Mathematics.  Softmax sums over disjoint sets of keys join as in kv_attend.cuh, whatever
+// rows were computed together: the kernels of kv_attend.cuh and kv_attend_tc.cuh run once
+// over the groups' prefixes, where the rows of all of a group's requests meet the prefix's
+// keys at once (32 beams of six query heads: 192 rows, on the tensor cores), and once over
+// what each request has of its own, and leave the sums of every row's parts; this
+// kernel joins them.
+//
+// What bounds the call: a prefix's bytes are read once per group instead of once per
+// request, so with many requests the prefix is bound by the products and the softmax of its
+// rows, and the rest by HBM.
+#pragma once
+
+#include "kv_attend.cuh"
+
+namespace w12 {
+namespace dev {
+
+// Joins the parts of the output rows (token and head, heads fastest): a warp per row, first
+// the prefix's parts in range order, then the own ones.
+struct KvSharedJoin {
+    uint16_t *out;
+    float *lse;
+    int64_t out_stride;
+    const int32_t *cu_new;
+    int32_t tokens, heads, requests;
+    struct Line {
+        const float *part, *row_part;
+        const float2 *part_ml, *row_ml;
+        const int2 *info;
+        int32_t rows;  // of a row block
+    } line[2];  // the prefixes, the own tokens
+};
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const __grid_constant__ KvSharedJoin p) {
+    constexpr int W = kJoinThreads / 32, V = D / 32;  // columns of a lane
+    constexpr int U = V == 8 ? 4 : 8;                 // parts whose loads are in flight
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * W + warp;
+    const int32_t tok = (int32_t)(row / p.heads), h = (int32_t)(row - (int64_t)tok * p.heads);
+    pdl_launch_dependents();
+    pdl_wait();
+    // rows of no request have no note
+    if (tok >= min(p.tokens, p.cu_new[p.requests]) || tok < p.cu_new[0]) return;
+    int2 info[2];
+    info[0] = __ldcg(&p.line[0].info[row]);
+    info[1] = __ldcg(&p.line[1].info[row]);
+    if (!(info[1].y & kKvSharesPrefix)) info[0].y = 0;
+    info[1].y &= ~kKvSharesPrefix;
+    const int32_t n0 = info[0].y, n = n0 + info[1].y;
+    float acc[V] = {}, mm = -INFINITY, sum = 0.0f;
+    for (int32_t k0 = 0; k0 < n; k0 += U) {
+        float y[U][V];
+        float2 s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t kk = min(k0 + u, n - 1);
+            const bool own = kk >= n0;
+            const KvSharedJoin::Line &l = p.line[own];
+            const int32_t k = own ? kk - n0 : kk;
+            const bool whole = (own ? info[1].y : info[0].y) == 1;
+            // the first CTA's part is in its second slot, every other one's in its first
+            const int64_t at = whole ? row : (own ? info[1].x : info[0].x) + (int64_t)(2 * k + (k == 0)) * l.rows;
+            s[u] = __ldcg((whole ? l.row_ml : l.part_ml) + at);
+            const float *src = (whole ? l.row_part : l.part) + at * D;
+            if constexpr (V == 2) {
+                const float2 a = __ldcg(reinterpret_cast<const float2 *>(src) + lane);
+                y[u][0] = a.x, y[u][1] = a.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    const float4 a = __ldcg(reinterpret_cast<const float4 *>(src) + lane * (V / 4) + e / 4);
+                    y[u][e] = a.x, y[u][e + 1] = a.y, y[u][e + 2] = a.z, y[u][e + 3] = a.w;
+                }
+            }
+        }
+        float mn = mm;
+#pragma unroll
+        for (int u = 0; u < U; ++u) mn = fmaxf(mn, s[u].x);
+        const float base = kv_part_base(mn), f0 = ex2(mm - base);
+        mm = mn;
+        sum *= f0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] *= f0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u < n) {
+                const float g = ex2(s[u].x - base);
+                sum = fmaf(g, s[u].y, sum);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(g, y[u][e], acc[e]);
+            }
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + tok * p.out_stride + (int64_t)h * D) + lane * (V / 2);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[row] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+}
+
+}  // namespace dev
+}  // namespace w12

@@ -24,7 +24,9 @@ import torch
 from . import build, w12
 
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
-_workspaces = {}  # (device, stream handle) -> zeroed workspace of the attend calls on that stream
+# (device, stream handle) -> zeroed workspace of the attend calls on that stream;
+# (device, stream handle, "shared") -> that of the ones with shared prefixes
+_workspaces = {}
 _outgrown = []  # smaller ones of before: a captured graph may still use them
 
 
@@ -38,13 +40,22 @@ def clear_workspaces():
 
 def _grow(index, st, size):
     """A zeroed workspace of at least ``size`` bytes for stream ``st``."""
+    return _grow_for((index, st), index, size)
+
+
+def _grow_shared(index, st, size):
+    """The same for calls with shared prefixes, which leave other things in theirs."""
+    return _grow_for((index, st, "shared"), index, size)
+
+
+def _grow_for(key, index, size):
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("the workspace of this stream is not large enough yet: make one ordinary call of "
                            "this size on the stream before capturing, or pass workspace=")
-    if (index, st) in _workspaces:
-        _outgrown.append(_workspaces[index, st])
+    if key in _workspaces:
+        _outgrown.append(_workspaces[key])
     ws = torch.zeros((size + (1 << 20) - 1) >> 20 << 20, dtype=torch.uint8, device=torch.device("cuda", index))
-    _workspaces[index, st] = ws
+    _workspaces[key] = ws
     return ws
 
 
@@ -59,8 +70,9 @@ def _load_host():
     loader.exec_module(host)
     lib = w12.lib()
     host.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.w12_kv_plan, lib.w12_kv_store, lib.w12_kv_read, lib.w12_kv_attend_workspace_size, lib.w12_kv_attend)),
-        w12._check)
+        lib.w12_kv_plan, lib.w12_kv_store, lib.w12_kv_read, lib.w12_kv_attend_workspace_size, lib.w12_kv_attend,
+        lib.w12_kv_fork, lib.w12_kv_copy, lib.w12_kv_attend_shared_workspace_size, lib.w12_kv_attend_shared,
+        lib.w12_beam_workspace_size, lib.w12_beam_select)), w12._check)
     return host
 
 
@@ -125,15 +137,17 @@ class KVStep:
     numbers a request's new tokens one after the other; for a tree, write cached
     length + depth over ``positions`` before the store (rotation) and the attention
     (windows).
-    ``max_new``: the most new tokens of a request, as far as is known.  What a
-    call does not use may be None."""
+    ``max_new``: the most new tokens of a request, as far as is known.  ``prefix``
+    (a KVPrefix): what groups of the requests share, which attend() then reads once for
+    each group.  What a call does not use may be None."""
 
     _kinds = {"lens": _I32, "cu_new": _I32, "positions": _I32, "slots": _I64, "tree": _I32}
 
-    def __init__(self, tables=None, lens=None, cu_new=None, positions=None, slots=None, max_new=1, tree=None):
+    def __init__(self, tables=None, lens=None, cu_new=None, positions=None, slots=None, max_new=1, tree=None,
+                 prefix=None):
         self.tables, self.lens, self.cu_new = tables, lens, cu_new
         self.positions, self.slots = positions, slots
-        self.max_new, self.tree = int(max_new), tree
+        self.max_new, self.tree, self.prefix = int(max_new), tree, prefix
 
     def __setattr__(self, name, value):
         # checked here, once, and not in every call of every layer
@@ -154,15 +168,59 @@ class KVStep:
         return t.get_device()
 
 
+class KVPrefix:
+    """Groups of requests with a common prefix: group g has requests ``cu[g] : cu[g + 1]``
+    (int32), request b shares its first ``lens[b]`` (int32, whole pages, 0: nothing) tokens
+    with its group; ``max_requests``: the most requests of a group, as far as is known.
+    ``KVPages.fork`` fills ``lens``; for a prompt that was put in every request's table
+    the caller does."""
+
+    def __init__(self, cu, lens, max_requests=1):
+        _need(cu.is_cuda, "cu must be on a CUDA device")
+        _ints(cu, _I32, "cu", cu.get_device())
+        _ints(lens, _I32, "lens", cu.get_device())
+        _need(cu.numel() >= 2, "cu must have an entry more than there are groups")
+        self.cu, self.lens, self.max_requests = cu, lens, int(max_requests)
+
+    @classmethod
+    def create(cls, groups, members, device=None):
+        """``groups`` groups of ``members`` requests each, which share nothing so far."""
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        return cls(torch.arange(groups + 1, dtype=_I32, device=dev) * members,
+                   torch.zeros(groups * members, dtype=_I32, device=dev), members)
+
+
+class KVCopies:
+    """Pages to copy: the first ``rows[i]`` tokens (``rows`` None: all) of page ``src[i]`` to
+    page ``dst[i]``; -1: none.  int32, as ``KVPages.fork`` writes them and ``KVCache.copy``
+    takes them."""
+
+    def __init__(self, src, dst, rows=None):
+        _need(src.is_cuda, "src must be on a CUDA device")
+        for name, t in (("src", src), ("dst", dst), ("rows", rows)):
+            if t is not None:
+                _ints(t, _I32, name, src.get_device())
+                _need(t.numel() == src.numel(), "src, dst and rows must have as many entries")
+        self.src, self.dst, self.rows = src, dst, rows
+
+    @classmethod
+    def empty(cls, requests, device=None):
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        none = lambda v: torch.full((requests,), v, dtype=_I32, device=dev)  # noqa: E731
+        return cls(none(-1), none(-1), none(0))
+
+
 class KVPages:
     """Page tables of ``requests`` requests and the ring of free pages.
 
     ``tables`` int32 [requests, max_blocks]; ``owned`` int32 [requests]: pages
     each request holds; ``ring`` int32: free page numbers, of which
     ``ring[i % len]`` for head <= i < tail are free; ``ring_state`` int64
-    {head, tail}.  ``KVPages.create`` starts with every page free."""
+    {head, tail}.  ``KVPages.create`` starts with every page free.  With ``shares`` (int32
+    [num_pages]: the holders of each page less one, 0 of free ones) requests may share
+    pages: ``fork``."""
 
-    def __init__(self, tables, owned, ring, ring_state, page_size):
+    def __init__(self, tables, owned, ring, ring_state, page_size, shares=None):
         _need(tables.dtype is _I32 and tables.dim() == 2 and tables.stride(1) == 1 and tables.is_cuda,
               "tables must be an int32 CUDA tensor [requests, max_blocks] with contiguous rows")
         self._index = tables.get_device()
@@ -171,16 +229,20 @@ class KVPages:
         _ints(ring_state, _I64, "ring_state", self._index)
         _need(owned.numel() == tables.shape[0] and ring.numel() >= 1 and ring_state.numel() == 2,
               "owned must have an entry per request, ring at least one and ring_state two")
+        if shares is not None:
+            _ints(shares, _I32, "shares", self._index)
+            _need(ring.numel() >= shares.numel() >= 1, "ring must have as many entries as shares or more")
         self.tables, self.owned, self.ring, self.ring_state = tables, owned, ring, ring_state
-        self.page_size = int(page_size)
+        self.page_size, self.shares = int(page_size), shares
 
     @classmethod
-    def create(cls, num_pages, page_size, requests, max_blocks, device=None):
+    def create(cls, num_pages, page_size, requests, max_blocks, device=None, shared=False):
         dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         return cls(torch.full((requests, max_blocks), -1, dtype=_I32, device=dev),
                    torch.zeros(requests, dtype=_I32, device=dev),
                    torch.arange(num_pages, dtype=_I32, device=dev),
-                   torch.tensor([0, num_pages], dtype=_I64, device=dev), page_size)
+                   torch.tensor([0, num_pages], dtype=_I64, device=dev), page_size,
+                   torch.zeros(num_pages, dtype=_I32, device=dev) if shared else None)
 
     def step(self, tokens, max_new=1, tree=None):
         """A KVStep with buffers for up to ``tokens`` new tokens, for plan()."""
@@ -196,7 +258,10 @@ class KVPages:
         unless outputs are given.  ``step`` refers to ``lens``, which must stay as
         it is until the step's attend calls have run.  A ring that runs out, or
         has no room for pages that trim gives back (those stay with their
-        requests), is reported by w12_check_status."""
+        requests), is reported by w12_check_status.  With ``shares`` there is no
+        ``trim``: fork() takes back, for it knows who else holds a page."""
+        if trim and self.shares is not None:
+            raise ValueError("pages that requests share are taken back by fork(), not by trim")
         if stream is not None or _current_device() != self._index:
             with _on(self._index, stream):
                 return self.plan(lens, new_lens, step, trim, owned_out, ring_state_out)
@@ -207,6 +272,23 @@ class KVPages:
         if step.tables is not self.tables:
             step.tables = self.tables
         return step
+
+
+    def fork(self, parents, lens, copies=None, prefix=None, lens_out=None, stream=None):
+        """Request i goes on from request ``parents[i]`` (int32, -1: from none, it is empty
+        then) as it was before the call, with the first ``lens[i]`` (int32) of its tokens.
+        Full pages are shared; of requests that want the same partly filled page one keeps
+        it and the others get pages of their own and an entry of ``copies`` (a KVCopies;
+        None: a new one is made), which is returned: every layer's cache has to ``copy``
+        it before the next store.  Pages that no request holds any more are free.
+        ``lens_out`` (may be ``lens``) receives the tokens kept (0 where there is no parent),
+        ``prefix.lens`` what the groups of ``prefix`` (a KVPrefix) share now."""
+        if stream is not None or _current_device() != self._index:
+            with _on(self._index, stream):
+                return self.fork(parents, lens, copies, prefix, lens_out)
+        if copies is None:
+            copies = KVCopies.empty(self.tables.shape[0], self.tables.device)
+        return _host.fork(self, self._index, parents, lens, copies, prefix, lens_out, _current_stream(self._index))
 
 
 class KVCache:
@@ -267,6 +349,17 @@ class KVCache:
                 return self.read(slots, out)
         return _host.read(self._address, self._index, slots, out, _current_stream(self._index))
 
+    def copy(self, copies, others=(), stream=None):
+        """Copy pages (``copies``: a KVCopies) inside this cache and, in the same launch,
+        inside ``others``, caches of other layers that are laid out alike.  A page that is
+        written to must not be another copy's."""
+        if stream is not None or _current_device() != self._index:
+            with _on(self._index, stream):
+                return self.copy(copies, others)
+        for c in others:
+            _need(c._index == self._index, "the caches must be on one device")
+        _host.copy(self._address, self._index, others, copies, _current_stream(self._index))
+
     def attend(self, q, step, scale=None, window=0, out=None, lse=None, workspace=None, stream=None):
         """Attention of the step's new tokens over their requests' cached ones
         (their own included).  ``scale`` defaults to head_dim ** -0.5; ``window``
@@ -275,11 +368,17 @@ class KVCache:
         (fp32 [tokens, heads]) receives the log of the softmax sums.  Calls on one
         stream (of several threads too) share a workspace; ``workspace`` (uint8, zero-filled before its
         first use) takes its place, as a captured graph needs that is replayed
-        beside other calls."""
+        beside other calls.  With ``step.prefix`` (no window then) the keys that a
+        group of requests shares are read once for all of them; such calls have a workspace of
+        their own."""
         if stream is not None or _current_device() != self._index:
             with _on(self._index, stream):
                 return self.attend(q, step, scale, window, out, lse, workspace)
         st = _current_stream(self._index)
-        own = workspace is None
+        grow = None
+        if workspace is None:
+            shared = getattr(step, "prefix", None) is not None
+            workspace = _workspaces.get((self._index, st, "shared") if shared else (self._index, st))
+            grow = _grow_shared if shared else _grow
         return _host.attend(self._address, self._index, q, step, self._scale if scale is None else scale, window, out,
-                            lse, _workspaces.get((self._index, st)) if own else workspace, _grow if own else None, st)
+                            lse, workspace, grow, st)

@@ -29,6 +29,8 @@ EXPORTED = (
     "w12_q8_encoded_size", "w12_q8_encode_host", "w12_q8_blob_info", "w12_q8_gemm_workspace_size", "w12_q8_gemm",
     "w12_q8_gemm_group_workspace_size", "w12_q8_gemm_group_launch_info", "w12_q8_gemm_group",
     "w12_kv_plan", "w12_kv_store", "w12_kv_read", "w12_kv_attend_workspace_size", "w12_kv_attend",
+    "w12_kv_fork", "w12_kv_copy", "w12_kv_attend_shared_workspace_size", "w12_kv_attend_shared",
+    "w12_beam_workspace_size", "w12_beam_select",
     "w12_read_stream", "w12_check_status", "w12_selftest_timeout", "w12_set_option", "w12_get_option",
 )
 
@@ -111,6 +113,39 @@ class w12_kv_attend_args(ctypes.Structure):
     ]
 
 
+class w12_kv_fork_args(ctypes.Structure):
+    _fields_ = [
+        ("parents", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
+        ("owned", ctypes.c_void_p), ("tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("ring", ctypes.c_void_p), ("ring_state", ctypes.c_void_p), ("shares", ctypes.c_void_p),
+        ("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+        ("prefix_cu", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+        ("requests", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("ring_size", ctypes.c_int32), ("groups", ctypes.c_int32),
+    ]
+
+
+class w12_kv_prefix(ctypes.Structure):
+    _fields_ = [
+        ("cu", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("groups", ctypes.c_int32),
+        ("max_requests", ctypes.c_int32),
+    ]
+
+
+BEAM_BF16, BEAM_F32 = 0, 1  # W12_BEAM_* in include/w12.h
+
+
+class w12_beam_args(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64), ("allowed", ctypes.c_void_p),
+        ("allowed_stride", ctypes.c_int64), ("scores_in", ctypes.c_void_p), ("scores", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p), ("parents", ctypes.c_void_p), ("cand_tokens", ctypes.c_void_p),
+        ("cand_parents", ctypes.c_void_p), ("cand_scores", ctypes.c_void_p), ("requests", ctypes.c_int32),
+        ("beams", ctypes.c_int32), ("vocab", ctypes.c_int32), ("take", ctypes.c_int32), ("eos", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -163,6 +198,14 @@ def lib() -> ctypes.CDLL:
     L.w12_kv_read.argtypes = [cache_p, vp, ctypes.c_int32, vp, vp, vp]
     L.w12_kv_attend_workspace_size.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), ctypes.POINTER(sz)]
     L.w12_kv_attend.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), vp, sz, vp]
+    prefix_p, beam_p = ctypes.POINTER(w12_kv_prefix), ctypes.POINTER(w12_beam_args)
+    L.w12_kv_fork.argtypes = [ctypes.POINTER(w12_kv_fork_args), vp]
+    L.w12_kv_copy.argtypes = [cache_p, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp]
+    L.w12_kv_attend_shared_workspace_size.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), prefix_p,
+                                                      ctypes.POINTER(sz)]
+    L.w12_kv_attend_shared.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), prefix_p, vp, sz, vp]
+    L.w12_beam_workspace_size.argtypes = [beam_p, ctypes.POINTER(sz)]
+    L.w12_beam_select.argtypes = [beam_p, vp, sz, vp]
     L.w12_read_stream.argtypes = [vp, sz, vp, ctypes.c_uint32, vp]
     L.w12_check_status.argtypes = [vp]
     L.w12_selftest_timeout.argtypes = [ctypes.c_uint32, vp]
@@ -458,6 +501,38 @@ def w12_kv_attend_workspace_size(cache: w12_kv_cache, args: w12_kv_attend_args) 
 def w12_kv_attend(cache: w12_kv_cache, args: w12_kv_attend_args, workspace_ptr: int, workspace_bytes: int,
                   stream=None) -> None:
     _check(lib().w12_kv_attend(cache, args, workspace_ptr, workspace_bytes, _stream_handle(stream)))
+
+
+def w12_kv_fork(args: w12_kv_fork_args, stream=None) -> None:
+    _check(lib().w12_kv_fork(args, _stream_handle(stream)))
+
+
+def w12_kv_copy(caches, src_ptr: int, dst_ptr: int, rows_ptr: int | None, pairs: int, stream=None) -> None:
+    """caches: a list of w12_kv_cache that are alike in all but their pointers."""
+    _check(lib().w12_kv_copy((w12_kv_cache * len(caches))(*caches), len(caches), src_ptr, dst_ptr, rows_ptr, pairs,
+                             _stream_handle(stream)))
+
+
+def w12_kv_attend_shared_workspace_size(cache: w12_kv_cache, args: w12_kv_attend_args, prefix: w12_kv_prefix) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().w12_kv_attend_shared_workspace_size(cache, args, prefix, ctypes.byref(out)))
+    return out.value
+
+
+def w12_kv_attend_shared(cache: w12_kv_cache, args: w12_kv_attend_args, prefix: w12_kv_prefix, workspace_ptr: int,
+                         workspace_bytes: int, stream=None) -> None:
+    _check(lib().w12_kv_attend_shared(cache, args, prefix, workspace_ptr, workspace_bytes, _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------- beam search
+def w12_beam_workspace_size(args: w12_beam_args) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().w12_beam_workspace_size(args, ctypes.byref(out)))
+    return out.value
+
+
+def w12_beam_select(args: w12_beam_args, workspace_ptr: int, workspace_bytes: int, stream=None) -> None:
+    _check(lib().w12_beam_select(args, workspace_ptr, workspace_bytes, _stream_handle(stream)))
 
 
 def w12_read_stream_ptr(buf_ptr: int, nbytes: int, sink_ptr: int, never: int, stream_handle: int | None) -> int:
