@@ -25,6 +25,7 @@
 
 #include <cstdint>
 
+#include "kv_common.cuh"
 #include "w12_device.cuh"
 
 namespace w12 {
@@ -227,7 +228,8 @@ __device__ __forceinline__ bool beam_before(const BeamCand &a, const BeamCand &b
 
 struct BeamShared {
     int32_t warp[kBeamThreads / 32];
-    uint32_t low[kBeamThreads / 32], high[kBeamThreads / 32];
+    alignas(16) uint32_t low[kBeamThreads / 2];
+    uint32_t high[kBeamThreads / 32], limit;
     uint64_t sum[kBeamThreads / 32];
     int32_t n, last;
     union {
@@ -255,20 +257,32 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
     x.load(static_cast<const uint8_t *>(p.logits) + row * p.stride * (BF16 ? 2 : 4), t0, t1, p.vocab,
            p.allowed ? p.allowed + row * p.allowed_stride : nullptr);
     const float own = x.top();
-    // as many groups of threads as elements are kept, or more
-    const int width = p.keep <= 8 ? 32 : p.keep <= 16 ? 16 : p.keep <= 32 ? 8 : 4;
-    uint32_t g = beam_order(own);
+    // the largest of each group of threads, 32 groups at least and twice as many as elements are kept
+    const int width = p.keep <= 16 ? 8 : p.keep <= 32 ? 4 : 2;
+    const uint32_t mine = beam_order(own);
+    uint32_t g = mine;
     for (int d = width / 2; d > 0; d >>= 1) g = max(g, __shfl_xor_sync(~0u, g, d));
-    const uint32_t lo = __reduce_min_sync(~0u, g), hi = __reduce_max_sync(~0u, g);
-    if (lane == 0) s.low[warp] = lo, s.high[warp] = hi;
+    if (tid % width == 0) s.low[tid / width] = g;
+    const uint32_t hi = __reduce_max_sync(~0u, g);
+    if (lane == 0) s.high[warp] = hi;
     if (tid == 0) s.n = 0;
     __syncthreads();
-    uint32_t low = ~0u, high = 0;
+    if (tid < kBeamThreads / width) {
+        // their keep-th largest: as many elements reach it, and in random order few more
+        const int groups = kBeamThreads / width;
+        const uint32_t v = s.low[tid];
+        int above = 0, equal = 0;
+        for (int i = 0; i < groups; i += 4) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(&s.low[i]);
+            above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+            equal += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
+        }
+        if (above < p.keep && above + equal >= p.keep) s.limit = v;  // (the same value where several do)
+    }
+    uint32_t high = 0;
 #pragma unroll
-    for (int i = 0; i < kBeamThreads / 32; ++i) low = min(low, s.low[i]), high = max(high, s.high[i]);
-    const uint32_t least = beam_order(-INFINITY) + 1;  // of a candidate
-    low = max(low, least);
-    const float top = beam_value(high), limit = beam_value(low);
+    for (int i = 0; i < kBeamThreads / 32; ++i) high = max(high, s.high[i]);
+    const float top = beam_value(high);
 
     // the part's sum
     float sum = 0.0f;
@@ -277,15 +291,17 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
         for (int e = 0; e < E; ++e) sum += x.get(e) == INFINITY ? 1.0f : 0.0f;
     } else if (beam_plain(top)) {
         const float r = -ceilf(top * kLog2E);
-        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+        const f2 ref = make_f2(r, r), big = make_f2(kLog2E, kLog2E), low = make_f2(kLog2ELow, kLog2ELow);
+        f2 s0 = make_f2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-            s0 += beam_ex2(fmaf(x.get(e), kLog2ELow, fmaf(x.get(e), kLog2E, r)));
-            s1 += beam_ex2(fmaf(x.get(e + 1), kLog2ELow, fmaf(x.get(e + 1), kLog2E, r)));
-            s2 += beam_ex2(fmaf(x.get(e + 2), kLog2ELow, fmaf(x.get(e + 2), kLog2E, r)));
-            s3 += beam_ex2(fmaf(x.get(e + 3), kLog2ELow, fmaf(x.get(e + 3), kLog2E, r)));
+            const f2 a = make_f2(x.get(e), x.get(e + 1)), b = make_f2(x.get(e + 2), x.get(e + 3));
+            const f2 c = fma2(a, low, fma2(a, big, ref)), d = fma2(b, low, fma2(b, big, ref));
+            s0 = s0 + make_f2(beam_ex2(f2_lo(c)), beam_ex2(f2_hi(c)));
+            s1 = s1 + make_f2(beam_ex2(f2_lo(d)), beam_ex2(f2_hi(d)));
         }
-        sum = (s0 + s1) + (s2 + s3);
+        s0 = s0 + s1;
+        sum = f2_lo(s0) + f2_hi(s0);
     } else if (top > -INFINITY) {
 #pragma unroll
         for (int e = 0; e < E; ++e) sum += beam_ex2((x.get(e) - top) * kLog2E);
@@ -294,6 +310,10 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) fixed += beam_shfl(fixed, d);
     if (lane == 0) s.sum[warp] = fixed;
+    __syncthreads();
+    // (no candidate is -infinity)
+    const uint32_t limit_order = max(s.limit, beam_order(-INFINITY) + 1);
+    const float limit = beam_value(limit_order);
 
     // the elements that reach the limit
     const auto push = [&](int e) {
@@ -338,17 +358,20 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
         __syncthreads();
         n = s.n;
     }
-    // sorted by counting
+    // sorted by counting, four threads for each
     BeamEntry *to = p.entries + (row * p.parts + part) * p.keep;
-    for (int i = tid; i < n; i += kBeamThreads) {
+    for (int i0 = 0; i0 < n; i0 += kBeamThreads / 4) {
+        const int i = min(i0 + tid / 4, n - 1);
         const uint32_t o = s.part.order[i];
         const int32_t at = s.part.place[i];
         int32_t rank = 0;
-        for (int j = 0; j < n; ++j) {
+        for (int j = tid % 4; j < n; j += 4) {
             const uint32_t other = s.part.order[j];
             rank += other > o || (other == o && s.part.place[j] < at);
         }
-        if (rank < p.keep) to[rank] = BeamEntry{beam_value(o), t0 + at};
+        rank += __shfl_xor_sync(~0u, rank, 1);
+        rank += __shfl_xor_sync(~0u, rank, 2);
+        if (tid % 4 == 0 && i0 + tid / 4 < n && rank < p.keep) to[rank] = BeamEntry{beam_value(o), t0 + at};
     }
     if (tid < p.keep && tid >= n) to[tid] = BeamEntry{-INFINITY, -1};
     if (tid == 0) {
@@ -453,11 +476,14 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, BeamShared &s, in
     __syncthreads();
     int32_t n = s.n;
     if (n <= kBeamJoin) {
-        for (int i = tid; i < n; i += kBeamThreads) {
+        for (int i0 = 0; i0 < n; i0 += kBeamThreads / 4) {
+            const int i = min(i0 + tid / 4, n - 1);
             const BeamCand c = s.join.pool[i];
             int32_t rank = 0;
-            for (int j = 0; j < n; ++j) rank += beam_before(s.join.pool[j], c);
-            if (rank < p.keep) s.join.best[rank] = c;
+            for (int j = tid % 4; j < n; j += 4) rank += beam_before(s.join.pool[j], c);
+            rank += __shfl_xor_sync(~0u, rank, 1);
+            rank += __shfl_xor_sync(~0u, rank, 2);
+            if (tid % 4 == 0 && i0 + tid / 4 < n && rank < p.keep) s.join.best[rank] = c;
         }
         n = min(n, p.keep);
     } else {
@@ -521,7 +547,7 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, BeamShared &s, in
 }
 
 template <bool BF16, int E>
-__global__ void __launch_bounds__(kBeamThreads) w12_beam_select_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kBeamThreads, E == 32 && !BF16 ? 4 : 6) w12_beam_select_kernel(const BeamParams p) {
     extern __shared__ uint4 beam_dyn[];
     BeamShared &s = *reinterpret_cast<BeamShared *>(beam_dyn);
     const int tid = threadIdx.x;
