@@ -10,7 +10,7 @@ namespace launch {
 namespace {
 
 struct BeamPlan {
-    int elems = 16;  // per thread
+    bool large = false;  // tiles
     int32_t parts = 1, part = 0, keep = 0;
     size_t off_stats = 0, off_entries = 0, bytes = 0;
 };
@@ -18,10 +18,15 @@ struct BeamPlan {
 BeamPlan beam_plan(const DeviceView &d, const w12_beam_args &a) {
     BeamPlan plan;
     const int64_t rows = (int64_t)a.requests * a.beams;
-    // a thread's elements: few where the rows' parts would not fill the device otherwise
-    const auto parts_of = [&](int elems) { return (a.vocab + dev::kBeamThreads * elems - 1) / (dev::kBeamThreads * elems); };
-    plan.elems = rows * parts_of(16) <= (int64_t)d.sm_count * 8 ? 16 : 32;
-    const int32_t parts = parts_of(plan.elems);
+    // A tile of half the size per CTA while that fills the device no more than once; beyond it
+    // longer parts of larger tiles, whose threshold serves all of their tiles.
+    const int64_t fill = (int64_t)d.sm_count * dev::kBeamCtas;
+    const int32_t large = a.dtype == W12_BEAM_BF16 ? 8192 : 4096;
+    const auto tiles = [&](int32_t tile) { return (a.vocab + tile - 1) / tile; };
+    plan.large = rows * tiles(large / 2) > fill;
+    const int32_t most = tiles(plan.large ? large : large / 2);
+    const int32_t parts = (int32_t)std::max<int64_t>((most + dev::kBeamTiles - 1) / dev::kBeamTiles,
+                                                     std::min<int64_t>(most, fill / rows));
     plan.part = ((a.vocab + parts - 1) / parts + 31) / 32 * 32;
     plan.parts = (a.vocab + plan.part - 1) / plan.part;
     // as many as may end, and the beams behind them
@@ -57,7 +62,9 @@ int beam_select(const w12_beam_args &a, void *workspace, size_t ws_bytes, void *
         return W12_ERR_SHAPE;
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    static constexpr dev::BeamLog logs;
     dev::BeamParams p;
+    p.logs = logs;
     p.logits = a.logits;
     p.stride = a.logits_stride;
     p.allowed = a.allowed;
@@ -80,12 +87,12 @@ int beam_select(const w12_beam_args &a, void *workspace, size_t ws_bytes, void *
     p.eos = a.eos;
     p.parts = plan.parts;
     p.part = plan.part;
+    p.per_row_inv = (uint32_t)(((uint64_t(1) << 32) + (uint64_t)plan.parts * plan.keep - 1) / ((uint64_t)plan.parts * plan.keep));
     const int smem = (int)sizeof(dev::BeamShared) + a.beams * plan.parts;
-    const bool bf16 = a.dtype == W12_BEAM_BF16;
-    const auto kernel = plan.elems == 16 ? bf16 ? &dev::w12_beam_select_kernel<true, 16>
-                                                : &dev::w12_beam_select_kernel<false, 16>
-                        : bf16           ? &dev::w12_beam_select_kernel<true, 32>
-                                         : &dev::w12_beam_select_kernel<false, 32>;
+    const auto kernel = a.dtype == W12_BEAM_BF16
+                            ? plan.large ? &dev::w12_beam_select_kernel<true, 32> : &dev::w12_beam_select_kernel<true, 16>
+                        : plan.large ? &dev::w12_beam_select_kernel<false, 16>
+                                     : &dev::w12_beam_select_kernel<false, 8>;
     const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)ctas), dev::kBeamThreads, smem, 1, stream, p);
     if (e != cudaSuccess) return kv_cuda_fail(e, "w12_beam_select launch", err);
     return W12_OK;

@@ -31,7 +31,7 @@
 namespace w12 {
 namespace dev {
 
-constexpr int kBeamThreads = 256, kBeamKeep = 64, kBeamMost = 32;
+constexpr int kBeamThreads = 256, kBeamCtas = 4, kBeamTiles = 16, kBeamKeep = 64, kBeamMost = 32;
 constexpr int kBeamPool = 512;     // elements of a part that may reach the threshold
 constexpr int kBeamJoin = 1024;    // and of a request
 constexpr int kBeamVocab = 1 << 22;
@@ -45,6 +45,25 @@ struct BeamStat {
 struct BeamEntry {
     float x;
     int32_t token;  // -1: none
+};
+
+// log2 of a positive whole number, to 1e-9.  x = 2^k f with 1 <= f < 2; of f's first six bits
+// c is about 1 / f, in eight bits, so that t = f c - 1 is small (2^-6) and exact, and
+// log2(f) = log2(1 / c) + log2(1 + t), the first from a table and the second from its series,
+// in 32 bits (2^-24 of 2^-6).
+struct BeamLog {
+    double log[64];
+    uint16_t inverse[64];  // c times 256
+    constexpr BeamLog() : log(), inverse() {
+        for (int i = 0; i < 64; ++i) {
+            inverse[i] = (uint16_t)((2 * 256 * 64 * 2 + (2 * i + 1 + 128)) / (2 * (2 * i + 1 + 128)));  // 256 / (1 + (i + 0.5) / 64)
+            // ln(256 / c) = 2 atanh(z)
+            const double x = 256.0 / inverse[i], z = (x - 1) / (x + 1);
+            double power = z, sum = 0;
+            for (int n = 1; n < 60; n += 2) sum += power / n, power *= z * z;
+            log[i] = 2 * sum * 1.4426950408889634;
+        }
+    }
 };
 
 struct BeamParams {
@@ -62,6 +81,8 @@ struct BeamParams {
     uint32_t *counters;   // [requests]
     int32_t requests, beams, vocab, take, keep, eos;
     int32_t parts, part;  // parts of a row, their tokens
+    uint32_t per_row_inv;  // ceil(2^32 / (parts keep)): divides what is below 2^32 / (parts keep)
+    BeamLog logs;         // (parameters are near; one lane's loads of a table in memory are not)
 };
 
 // Exponent that a part's sum is relative to, in powers of two.  Where the integer nearest
@@ -104,13 +125,32 @@ struct BeamElems {
         if constexpr (BF16) return __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
         return __uint_as_float(w[e]);
     }
+    // Word i (not known when compiled: chosen bit by bit of i).
+    __device__ __forceinline__ uint32_t word(int i) const {
+        constexpr int WORDS = BF16 ? E / 2 : E;
+        uint32_t y[WORDS];
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) y[k] = w[k];
+#pragma unroll
+        for (int half = WORDS / 2; half > 0; half /= 2) {
+#pragma unroll
+            for (int k = 0; k < half; ++k) y[k] = i & half ? y[k + half] : y[k];
+        }
+        return y[0];
+    }
+    __device__ __forceinline__ float element(int e) const {
+        if constexpr (BF16) {
+            const uint32_t u = word(e / 2);
+            return __uint_as_float(e & 1 ? u & 0xFFFF0000u : u << 16);
+        }
+        return __uint_as_float(word(e));
+    }
     __device__ __forceinline__ static uint32_t none() { return BF16 ? 0xFF80FF80u : 0xFF800000u; }
 
     // Tokens t0 + (j kBeamThreads + tid) VEC + e, of which those before t1 count; row: the
     // row's token 0, which may lie at any element: a thread has the same tokens of every row
     // (equal rows then have equal sums), from one 16-byte piece of memory or out of two.
-    __device__ __forceinline__ void load(const uint8_t *row, int32_t t0, int32_t t1, int32_t vocab,
-                                         const uint32_t *allowed) {
+    __device__ __forceinline__ void load(const uint8_t *row, int32_t t0, int32_t t1, int32_t vocab) {
         constexpr int ELEM = BF16 ? 2 : 4, WORDS = 4;
         const int tid = threadIdx.x;
         const int32_t mis = (int32_t)((reinterpret_cast<uintptr_t>(row + (int64_t)t0 * ELEM) & 15u) / ELEM);
@@ -155,6 +195,11 @@ struct BeamElems {
                 }
             }
         }
+    }
+    // What does not count becomes -infinity.
+    __device__ __forceinline__ void settle(int32_t t0, int32_t t1, const uint32_t *allowed) {
+        constexpr int WORDS = 4;
+        const int tid = threadIdx.x;
         if (allowed) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
@@ -206,19 +251,7 @@ __device__ __forceinline__ uint64_t beam_shfl(uint64_t v, int d) {
     return (uint64_t)hi << 32 | lo;
 }
 
-// Sum over the CTA, for all threads.
-__device__ __forceinline__ int32_t beam_count(int32_t n, int32_t *s_warp) {
-    n = __reduce_add_sync(~0u, n);
-    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = n;
-    __syncthreads();
-    int32_t all = 0;
-#pragma unroll
-    for (int i = 0; i < kBeamThreads / 32; ++i) all += s_warp[i];
-    __syncthreads();
-    return all;
-}
-
-// A candidate of a request: its score's order and its place beam * vocab + token.
+// A candidate of a request: its score's order and its place, beam and token.
 struct BeamCand {
     uint64_t order, place;
 };
@@ -226,21 +259,30 @@ __device__ __forceinline__ bool beam_before(const BeamCand &a, const BeamCand &b
     return a.order > b.order || (a.order == b.order && a.place < b.place);
 }
 
+// An element of a part: larger value, larger key; of equal ones the lower place in the part.
+__device__ __forceinline__ uint64_t beam_key(uint32_t order, int32_t place) {
+    return (uint64_t)order << 32 | (uint32_t)~place;
+}
+
 struct BeamShared {
-    int32_t warp[kBeamThreads / 32];
-    alignas(16) uint32_t low[kBeamThreads / 2];
+    alignas(16) uint32_t low[kBeamThreads];
     uint32_t high[kBeamThreads / 32], limit;
     uint64_t sum[kBeamThreads / 32];
+    int32_t bins[kBeamThreads];
     int32_t n, last;
     union {
         struct {
-            uint32_t order[kBeamPool];
-            int32_t place[kBeamPool];
-        } part;
+            float tops[kBeamTiles * kBeamThreads];  // the threads' largest logits of each tile
+            uint64_t pool[kBeamPool];               // elements that may be among the part's best
+        };
         struct {
-            BeamCand pool[kBeamJoin];
-            BeamCand best[kBeamKeep];
-            double add[kBeamMost];      // score - ln(sum of the row), relative to its largest logit
+            BeamEntry pool[kBeamJoin];
+            int32_t row[kBeamJoin];
+            uint64_t order[kBeamJoin];
+            BeamEntry best[kBeamKeep];
+            int32_t best_row[kBeamKeep];
+            uint64_t best_order[kBeamKeep];
+            double add[kBeamMost];  // score - ln(sum of the row), relative to its largest logit
             float add32[kBeamMost], top[kBeamMost];
             uint64_t sum[kBeamMost];
             BeamCand warp[kBeamThreads / 32];
@@ -249,136 +291,270 @@ struct BeamShared {
     uint8_t at[1];  // [beams * parts] behind it: how far the slow merge is in each list
 };
 
-template <bool BF16, int E>
-__device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, int64_t row, int32_t part) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    BeamElems<BF16, E> x;
-    const int32_t t0 = part * p.part, t1 = min(t0 + p.part, p.vocab);
-    x.load(static_cast<const uint8_t *>(p.logits) + row * p.stride * (BF16 ? 2 : 4), t0, t1, p.vocab,
-           p.allowed ? p.allowed + row * p.allowed_stride : nullptr);
-    const float own = x.top();
-    // the largest of each group of threads, 32 groups at least and twice as many as elements are kept
-    const int width = p.keep <= 16 ? 8 : p.keep <= 32 ? 4 : 2;
-    const uint32_t mine = beam_order(own);
-    uint32_t g = mine;
-    for (int d = width / 2; d > 0; d >>= 1) g = max(g, __shfl_xor_sync(~0u, g, d));
-    if (tid % width == 0) s.low[tid / width] = g;
-    const uint32_t hi = __reduce_max_sync(~0u, g);
-    if (lane == 0) s.high[warp] = hi;
-    if (tid == 0) s.n = 0;
-    __syncthreads();
-    if (tid < kBeamThreads / width) {
-        // their keep-th largest: as many elements reach it, and in random order few more
-        const int groups = kBeamThreads / width;
-        const uint32_t v = s.low[tid];
+// The keep-th largest of the groups' maxima in s.low, to s.limit: as many elements reach it
+// and, in random order, few more.
+__device__ __forceinline__ void beam_limit(BeamShared &s, int32_t keep, int width) {
+    const int groups = kBeamThreads / width;
+    if ((int)threadIdx.x < groups) {
+        const uint32_t v = s.low[threadIdx.x];
         int above = 0, equal = 0;
         for (int i = 0; i < groups; i += 4) {
             const uint4 o = *reinterpret_cast<const uint4 *>(&s.low[i]);
             above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
             equal += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
         }
-        if (above < p.keep && above + equal >= p.keep) s.limit = v;  // (the same value where several do)
+        if (above < keep && above + equal >= keep) s.limit = v;  // (the same value where several do)
     }
-    uint32_t high = 0;
-#pragma unroll
-    for (int i = 0; i < kBeamThreads / 32; ++i) high = max(high, s.high[i]);
-    const float top = beam_value(high);
+}
 
-    // the part's sum
-    float sum = 0.0f;
-    if (top == INFINITY) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum += x.get(e) == INFINITY ? 1.0f : 0.0f;
-    } else if (beam_plain(top)) {
-        const float r = -ceilf(top * kLog2E);
-        const f2 ref = make_f2(r, r), big = make_f2(kLog2E, kLog2E), low = make_f2(kLog2ELow, kLog2ELow);
-        f2 s0 = make_f2(0.0f, 0.0f), s1 = s0;
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-            const f2 a = make_f2(x.get(e), x.get(e + 1)), b = make_f2(x.get(e + 2), x.get(e + 3));
-            const f2 c = fma2(a, low, fma2(a, big, ref)), d = fma2(b, low, fma2(b, big, ref));
-            s0 = s0 + make_f2(beam_ex2(f2_lo(c)), beam_ex2(f2_hi(c)));
-            s1 = s1 + make_f2(beam_ex2(f2_lo(d)), beam_ex2(f2_hi(d)));
+// Adds a part's sum (largest logit t) to that of others (largest logit top).
+__device__ __forceinline__ void beam_add(float &top, uint64_t &sum, float t, uint64_t y) {
+    const float m = fmaxf(top, t);
+    const auto scaled = [&](float from, uint64_t v) -> uint64_t {
+        if (from == m) return v;
+        if (v == 0 || m == INFINITY || from == -INFINITY) return 0;
+        if (beam_plain(from) && beam_plain(m)) {  // whole powers of two apart
+            const float d = ceilf(m * kLog2E) - ceilf(from * kLog2E);
+            return d >= 64.0f ? 0 : v >> (int)d;
         }
-        s0 = s0 + s1;
-        sum = f2_lo(s0) + f2_hi(s0);
-    } else if (top > -INFINITY) {
+        const double d = beam_ref(m) - beam_ref(from);
+        return d >= 64.0 ? 0 : (uint64_t)((double)v * exp2(-d));
+    };
+    sum = scaled(top, sum) + scaled(t, y);
+    top = m;
+}
+
+// The lanes' sums together, for all of them.
+__device__ __forceinline__ void beam_total(float &top, uint64_t &sum) {
+    const float most = beam_value(__reduce_max_sync(~0u, beam_order(top)));
+    if (__all_sync(~0u, beam_plain(top) || top == -INFINITY) && most > -INFINITY) {  // whole powers of two apart
+        const int32_t r = top == -INFINITY ? -(1 << 24) : (int32_t)ceilf(top * kLog2E);
+        const int32_t d = __reduce_max_sync(~0u, r) - r;
+        sum = d >= 64 ? 0 : sum >> d;
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum += beam_ex2((x.get(e) - top) * kLog2E);
+        for (int x = 16; x > 0; x >>= 1) sum += beam_shfl(sum, x);
+        top = most;
+        return;
     }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+        const float t = __shfl_xor_sync(~0u, top, x);
+        beam_add(top, sum, t, beam_shfl(sum, x));
+    }
+}
+
+__device__ __forceinline__ double beam_log2(const BeamLog &table, uint64_t x) {
+    const int k = 63 - __clzll((long long)x);
+    const uint64_t f = x << (63 - k);                      // times 2^63
+    const int i = (int)(f >> 57) & 63;
+    // f c - 1, times 2^63: the product's bits from 2^8 up
+    const int64_t t = (int64_t)((__umul64hi(f, (uint64_t)table.inverse[i] << 48) << 8) - (1ull << 63));
+    const float y = (float)t * 1.0842021724855044e-19f;    // 2^-63
+    const float poly = y * (1.0f + y * (-0.5f + y * (0.33333333f + y * (-0.25f + y * (0.2f + y * -0.16666667f)))));
+    return (double)k + table.log[i] + (double)poly * 1.4426950408889634;
+}
+
+// The tiles of one part of a row.
+template <bool BF16, int E>
+struct BeamTiles {
+    static constexpr int32_t TILE = kBeamThreads * E;
+    const uint8_t *base;
+    const uint32_t *allowed;
+    int32_t t0, t1, vocab;
+
+    // One token's logit: the load, and what becomes of it.
+    __device__ __forceinline__ uint32_t raw(int32_t token) const {
+        const int32_t t = min(token, t1 - 1);
+        if constexpr (BF16) return reinterpret_cast<const uint16_t *>(base)[t];
+        return reinterpret_cast<const uint32_t *>(base)[t];
+    }
+    __device__ __forceinline__ float settled(uint32_t raw, int32_t token) const {
+        if (token >= t1 || (allowed && !(allowed[token >> 5] >> (token & 31) & 1u))) return -INFINITY;
+        return fmaxf(__uint_as_float(BF16 ? raw << 16 : raw) + 0.0f, -INFINITY);  // no NaN, no -0
+    }
+    // f(tile, its place in the part) for the thread's elements of each tile, the next one's
+    // loads in flight while one is worked on.
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+        BeamElems<BF16, E> next;
+        next.load(base, t0, t1, vocab);
+        for (int32_t a = t0; a < t1; a += TILE) {
+            BeamElems<BF16, E> x = next;
+            if (a + TILE < t1) next.load(base, a + TILE, t1, vocab);
+            x.settle(a, t1, allowed);
+            f(x, a - t0);
+        }
+    }
+};
+
+// Where too many elements reach the threshold (equal logits, say): the keep-th largest value
+// and the place that the last of its equals may have, a byte of both at a time from the
+// number of elements for each of its values.  All threads; the part has `keep` candidates or more.
+template <bool BF16, int E>
+__device__ __noinline__ void beam_exact(const BeamTiles<BF16, E> &tiles, BeamShared &s, int32_t keep, uint32_t least,
+                                        uint32_t &limit, int32_t &upto) {
+    const int tid = threadIdx.x;
+    int32_t left = keep;
+    limit = 0;
+    upto = 0;
+    for (int pass = 0; pass < 7; ++pass) {
+        // bytes 3 to 0 of the order, from above; then bytes 2 to 0 of the place, from below
+        const bool places = pass > 3;
+        const int shift = places ? 8 * (6 - pass) : 8 * (3 - pass);
+        s.bins[tid] = 0;
+        __syncthreads();
+        tiles.each([&](const BeamElems<BF16, E> &x, int32_t at) {
+#pragma unroll 1
+            for (int e = 0; e < E; ++e) {
+                const uint32_t o = beam_order(x.element(e)), place = (uint32_t)(at + x.place(e));
+                const bool in = places ? o == limit && (pass == 4 || place >> (shift + 8) == (uint32_t)upto >> (shift + 8))
+                                       : o >= least && (pass == 0 || o >> (shift + 8) == limit >> (shift + 8));
+                if (in) atomicAdd(&s.bins[((places ? place : o) >> shift) & 255u], 1);
+            }
+        });
+        __syncthreads();
+        int32_t seen = 0, bin = places ? 0 : 255;
+        for (; bin != (places ? 255 : 0); bin += places ? 1 : -1) {
+            if (seen + s.bins[bin] >= left) break;
+            seen += s.bins[bin];
+        }
+        left -= seen;
+        if (places) upto |= bin << shift;
+        else limit |= (uint32_t)bin << shift;
+        __syncthreads();
+    }
+}
+
+// One part of a row.
+template <bool BF16, int E>
+__device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, int64_t row, int32_t part) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t t0 = part * p.part;
+    const BeamTiles<BF16, E> tiles = {static_cast<const uint8_t *>(p.logits) + row * p.stride * (BF16 ? 2 : 4),
+                                      p.allowed ? p.allowed + row * p.allowed_stride : nullptr, t0,
+                                      min(t0 + p.part, p.vocab), p.vocab};
+    // the warp's largest logit so far, the thread's sum relative to it, the thread's largest
+    float top = -INFINITY, sum = 0.0f, mine = -INFINITY;
+    tiles.each([&](const BeamElems<BF16, E> &x, int32_t at) {
+        const float own = x.top();
+        mine = fmaxf(mine, own);
+        s.tops[at / E + tid] = own;
+        const float most = fmaxf(top, beam_value(__reduce_max_sync(~0u, beam_order(own))));
+        if (most != top) {  // the same for the warp
+            if (sum > 0.0f) {
+                if (most == INFINITY) sum = 0.0f;
+                else if (beam_plain(top) && beam_plain(most)) sum *= beam_ex2(ceilf(top * kLog2E) - ceilf(most * kLog2E));
+                else sum *= (float)exp2(beam_ref(top) - beam_ref(most));
+            }
+            top = most;
+        }
+        if (top == INFINITY) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum += x.get(e) == INFINITY ? 1.0f : 0.0f;
+        } else if (beam_plain(top)) {
+            const float r = -ceilf(top * kLog2E);
+            const f2 ref = make_f2(r, r), big = make_f2(kLog2E, kLog2E), low = make_f2(kLog2ELow, kLog2ELow);
+            f2 s0 = make_f2(0.0f, 0.0f), s1 = s0;
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const f2 u = make_f2(x.get(e), x.get(e + 1)), v = make_f2(x.get(e + 2), x.get(e + 3));
+                const f2 c = fma2(u, low, fma2(u, big, ref)), d = fma2(v, low, fma2(v, big, ref));
+                s0 = s0 + make_f2(beam_ex2(f2_lo(c)), beam_ex2(f2_hi(c)));
+                s1 = s1 + make_f2(beam_ex2(f2_lo(d)), beam_ex2(f2_hi(d)));
+            }
+            s0 = s0 + s1;
+            sum += f2_lo(s0) + f2_hi(s0);
+        } else if (top > -INFINITY) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum += beam_ex2((x.get(e) - top) * kLog2E);
+        }
+    });
+    // the selection's threshold, from the largest of groups of threads; meanwhile the part's sum
+    const int width = p.keep <= 16 ? 8 : p.keep <= 32 ? 4 : 2;
+    uint32_t g = beam_order(mine);
+    for (int d = width / 2; d > 0; d >>= 1) g = max(g, __shfl_xor_sync(~0u, g, d));
+    if (tid % width == 0) s.low[tid / width] = g;
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    beam_limit(s, p.keep, width);
     uint64_t fixed = __float2ull_rn(sum * (float)(1ull << kBeamFixed));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) fixed += beam_shfl(fixed, d);
-    if (lane == 0) s.sum[warp] = fixed;
+    if (lane == 0) s.sum[warp] = fixed, s.high[warp] = __float_as_uint(top);
     __syncthreads();
-    // (no candidate is -infinity)
-    const uint32_t limit_order = max(s.limit, beam_order(-INFINITY) + 1);
-    const float limit = beam_value(limit_order);
-
-    // the elements that reach the limit
-    const auto push = [&](int e) {
-        const int32_t at = atomicAdd(&s.n, 1);
-        if (at < kBeamPool) s.part.order[at] = beam_order(x.get(e)), s.part.place[at] = x.place(e);
-    };
-    if (own >= limit) {
+    // no candidate is -infinity
+    const uint32_t least = beam_order(__uint_as_float(BF16 ? 0xFF7F0000u : 0xFF7FFFFFu));
+    uint32_t limit = max(s.limit, least);
+    int32_t upto = 0x7FFFFFFF;
+    const int32_t all_tiles = (tiles.t1 - t0 + tiles.TILE - 1) / tiles.TILE;
+    for (int round = 0; round < 2; ++round) {
+        // The elements that reach it: of the lanes and tiles whose largest one does (hits), a
+        // lane for each element, read once more; several hits' loads are in flight.
+        const float floor = beam_value(limit);
+        constexpr int VEC = BeamElems<BF16, E>::VEC, B = 4;
+        int32_t j = -1;
+        uint32_t left = 0;
+        while (true) {
+            float v[B];
+            uint32_t raw[B];
+            int32_t place[B];
+            int n = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (x.get(e) >= limit) push(e);
-    }
-    __syncthreads();
-    int32_t n = s.n;
-    if (n > kBeamPool) {
-        // the keep-th largest value, then the places that its equals may have
-        uint32_t at = 0;
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t c = at | 1u << bit;
-            int32_t m = 0;
+            for (int k = 0; k < B; ++k) {
+                while (left == 0 && ++j < all_tiles) left = __ballot_sync(~0u, s.tops[j * kBeamThreads + tid] >= floor);
+                const int l = left ? __ffs((int)left) - 1 : 0, e = lane % E;
+                place[k] = min(j, all_tiles - 1) * tiles.TILE + (e / VEC * kBeamThreads + warp * 32 + l) * VEC + e % VEC;
+                if (left) n = k + 1;
+                left &= left - 1;
+            }
 #pragma unroll
-            for (int e = 0; e < E; ++e) m += beam_order(x.get(e)) >= c;
-            if (beam_count(m, s.warp) >= p.keep) at = c;
+            for (int k = 0; k < B; ++k) raw[k] = tiles.raw(t0 + place[k]);
+#pragma unroll
+            for (int k = 0; k < B; ++k) v[k] = k < n && lane < E ? tiles.settled(raw[k], t0 + place[k]) : -INFINITY;
+            if (n == 0) break;
+            uint32_t in[B];
+            int32_t count = 0, base = 0;
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                in[k] = __ballot_sync(~0u, v[k] > floor || (v[k] == floor && place[k] <= upto));
+                count += __popc(in[k]);
+            }
+            if (lane == 0 && count) base = atomicAdd(&s.n, count);
+            base = __shfl_sync(~0u, base, 0);
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const int32_t to = base + __popc(in[k] & ((1u << lane) - 1u));
+                if ((in[k] >> lane & 1u) && to < kBeamPool) s.pool[to] = beam_key(beam_order(v[k]), place[k]);
+                base += __popc(in[k]);
+            }
+            if (n < B) break;
         }
-        int32_t above = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) above += beam_order(x.get(e)) > at;
-        const int32_t left = p.keep - beam_count(above, s.warp);
-        int32_t upto = 0;  // fewer than `left` of them have places below it
-        for (int bit = 14; bit >= 0; --bit) {
-            int32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) m += beam_order(x.get(e)) == at && x.place(e) < upto + (1 << bit);
-            if (beam_count(m, s.warp) < left) upto += 1 << bit;
-        }
+        __syncthreads();
+        if (s.n <= kBeamPool) break;
+        beam_exact(tiles, s, p.keep, least, limit, upto);
         if (tid == 0) s.n = 0;
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t o = beam_order(x.get(e));
-            if (o > at || (o == at && x.place(e) <= upto)) push(e);
-        }
-        __syncthreads();
-        n = s.n;
     }
     // sorted by counting, four threads for each
+    const int32_t n = s.n;
     BeamEntry *to = p.entries + (row * p.parts + part) * p.keep;
     for (int i0 = 0; i0 < n; i0 += kBeamThreads / 4) {
         const int i = min(i0 + tid / 4, n - 1);
-        const uint32_t o = s.part.order[i];
-        const int32_t at = s.part.place[i];
+        const uint64_t key = s.pool[i];
         int32_t rank = 0;
-        for (int j = tid % 4; j < n; j += 4) {
-            const uint32_t other = s.part.order[j];
-            rank += other > o || (other == o && s.part.place[j] < at);
-        }
+#pragma unroll 4
+        for (int k = tid % 4; k < n; k += 4) rank += s.pool[k] > key;
         rank += __shfl_xor_sync(~0u, rank, 1);
         rank += __shfl_xor_sync(~0u, rank, 2);
-        if (tid % 4 == 0 && i0 + tid / 4 < n && rank < p.keep) to[rank] = BeamEntry{beam_value(o), t0 + at};
+        if (tid % 4 == 0 && i0 + tid / 4 < n && rank < p.keep)
+            to[rank] = BeamEntry{beam_value((uint32_t)(key >> 32)), t0 + ~(int32_t)(uint32_t)key};
     }
     if (tid < p.keep && tid >= n) to[tid] = BeamEntry{-INFINITY, -1};
-    if (tid == 0) {
-        uint64_t all = 0;
-#pragma unroll
-        for (int i = 0; i < kBeamThreads / 32; ++i) all += s.sum[i];
-        p.stats[row * p.parts + part] = BeamStat{top, 0, all};
+    if (warp == kBeamThreads / 32 - 1) {
+        float most = lane < kBeamThreads / 32 ? __uint_as_float(s.high[lane]) : -INFINITY;
+        uint64_t all = lane < kBeamThreads / 32 ? s.sum[lane] : 0;
+        beam_total(most, all);
+        if (lane == 0) p.stats[row * p.parts + part] = BeamStat{most, 0, all};
     }
 }
 
@@ -386,119 +562,143 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
 __device__ __forceinline__ void beam_join(const BeamParams &p, BeamShared &s, int32_t request) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row0 = (int64_t)request * p.beams;
-    for (int b = warp; b < p.beams; b += kBeamThreads / 32) {
-        const BeamStat *st = p.stats + (row0 + b) * p.parts;
-        float top = -INFINITY;
-        for (int c = lane; c < p.parts; c += 32) top = fmaxf(top, __ldcg(&st[c].top));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        const double ref = beam_ref(top);
-        uint64_t sum = 0;
-        for (int c = lane; c < p.parts; c += 32) {
-            const float t = __ldcg(&st[c].top);
-            uint64_t y = __ldcg(reinterpret_cast<const unsigned long long *>(&st[c].sum));
-            if (t == -INFINITY || (top == INFINITY && t < top)) continue;
-            if (t != top) {
-                const double d = ref - beam_ref(t);  // whole, but for logits beyond 2^20
-                if (d >= 64.0) y = 0;
-                else if (d == rint(d)) y >>= (int)d;
-                else y = (uint64_t)((double)y * exp2(-d));
-            }
-            sum += y;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += beam_shfl(sum, d);
-        if (lane == 0) s.join.top[b] = top, s.join.sum[b] = sum;
-    }
-    __syncthreads();
-    if (tid < p.beams) {
-        const float top = s.join.top[tid], score = p.scores_in[row0 + tid];
-        const uint64_t sum = s.join.sum[tid];
-        double add = -INFINITY;
-        if (sum > 0 && isfinite(score)) {
-            // ln of the sum relative to the largest logit
-            const double shift = beam_plain(top) ? beam_ref(top) - (double)top * 1.4426950408889634 : 0.0;
-            add = (double)score - (log2((double)sum) - kBeamFixed + shift) * 0.69314718055994530942;
-        }
-        s.join.add[tid] = add;
-        s.join.add32[tid] = (float)add;
-    }
-    if (tid == 0) s.n = 0;
-    __syncthreads();
     const int32_t lists = p.beams * p.parts;
     const BeamEntry *entries = p.entries + row0 * p.parts * p.keep;
     const auto load = [&](int32_t list, int32_t i) {
         const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(entries + (int64_t)list * p.keep + i));
         return BeamEntry{__uint_as_float(u.x), (int32_t)u.y};
     };
-    const auto relative = [&](const BeamEntry &e, int b) { return e.x == s.join.top[b] ? 0.0f : e.x - s.join.top[b]; };
-    const auto cand = [&](const BeamEntry &e, int b) {
-        const double d = e.x == s.join.top[b] ? 0.0 : (double)e.x - (double)s.join.top[b];
-        return BeamCand{beam_order(s.join.add[b] + d), (uint64_t)b * (uint64_t)p.vocab + (uint64_t)e.token};
+    // A thread has every 256th entry of all lists.  The first kAhead of them are asked for
+    // while the rows' sums are made.
+    const int64_t total = (int64_t)lists * p.keep;
+    constexpr int kAhead = 8;
+    BeamEntry ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        ahead[k] = BeamEntry{-INFINITY, -1};
+        if (tid + k * kBeamThreads < total) ahead[k] = load(0, tid + k * kBeamThreads);
+    }
+    for (int b = warp; b < p.beams; b += kBeamThreads / 32) {
+        const BeamStat *st = p.stats + (row0 + b) * p.parts;
+        float top = -INFINITY;
+        uint64_t sum = 0;  // relative to `top`
+        for (int c0 = 0; c0 < p.parts; c0 += 32) {
+            uint4 u = make_uint4(0xFF800000u, 0, 0, 0);
+            if (c0 + lane < p.parts) u = __ldcg(reinterpret_cast<const uint4 *>(st + c0 + lane));
+            if (c0 == 0) top = __uint_as_float(u.x), sum = (uint64_t)u.w << 32 | u.z;
+            else beam_add(top, sum, __uint_as_float(u.x), (uint64_t)u.w << 32 | u.z);
+        }
+        beam_total(top, sum);
+        if (lane == 0) {
+            const float score = p.scores_in[row0 + b];
+            double add = -INFINITY;
+            if (sum > 0 && isfinite(score)) {
+                // ln of the sum relative to the largest logit
+                const double shift = beam_plain(top) ? beam_ref(top) - (double)top * 1.4426950408889634 : 0.0;
+                add = (double)score - (beam_log2(p.logs, sum) + (shift - kBeamFixed)) * 0.69314718055994530942;
+            }
+            s.join.top[b] = top;
+            s.join.add[b] = add;
+            s.join.add32[b] = (float)add;
+        }
+    }
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    const auto relative = [&](float x, float top) { return x == top ? 0.0f : x - top; };
+    const auto order_of = [&](float x, int b) {
+        const float top = s.join.top[b];
+        return beam_order(s.join.add[b] + (x == top ? 0.0 : (double)x - (double)top));
     };
     // 32-bit scores differ from the true ones by less than this
-    const auto slack = [&](float v, int b) { return 9.5e-7f * (fabsf(v) + fabsf(s.join.add32[b])); };
-    const int width = p.keep <= 8 ? 32 : p.keep <= 16 ? 16 : p.keep <= 32 ? 8 : 4;
+    const auto slack = [&](float v, float add) { return 9.5e-7f * (fabsf(v) + fabsf(add)); };
+    // f(entry, its beam) for all of the thread's entries
+    const int32_t per_row = p.parts * p.keep;
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (k * kBeamThreads < total)  // (entries that are not there have no token)
+                f(ahead[k], (int)__umulhi((uint32_t)(tid + k * kBeamThreads), p.per_row_inv));
+        for (int64_t i = tid + kAhead * kBeamThreads; i < total; i += kBeamThreads) {
+            const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(entries + i));
+            f(BeamEntry{__uint_as_float(u.x), (int32_t)u.y}, (int)(i / per_row));
+        }
+    };
+    // the threshold: the keep-th largest of the best scores of groups of threads
     float best = -INFINITY;
-    // the lists go round the groups, so that few of them leave none empty
-    const int32_t l0 = tid / width + kBeamThreads / width * (tid % width);
-    for (int32_t l = l0; l < lists; l += kBeamThreads) {
-        const int b = l / p.parts;
-        if (s.join.add[b] == -INFINITY) continue;
-        const BeamEntry e = load(l, 0);
-        if (e.token < 0) continue;
-        const float v = relative(e, b) + s.join.add32[b];
-        best = fmaxf(best, v - slack(v, b));
-    }
+    each([&](const BeamEntry &e, int b) {
+        if (e.token < 0) return;
+        const float add = s.join.add32[b];
+        if (add == -INFINITY) return;
+        const float v = relative(e.x, s.join.top[b]) + add;
+        best = fmaxf(best, v - slack(v, add));
+    });
+    const int width = p.keep <= 16 ? 4 : p.keep <= 32 ? 2 : 1;
     uint32_t g = beam_order(best + 0.0f);
     for (int d = width / 2; d > 0; d >>= 1) g = max(g, __shfl_xor_sync(~0u, g, d));
-    g = __reduce_min_sync(~0u, g);
-    if (lane == 0) s.low[warp] = g;
+    if (tid % width == 0) s.low[tid / width] = g;
     __syncthreads();
-    uint32_t low = ~0u;
-#pragma unroll
-    for (int i = 0; i < kBeamThreads / 32; ++i) low = min(low, s.low[i]);
-    const float limit = beam_value(low);
-    for (int32_t l = tid; l < lists; l += kBeamThreads) {
-        const int b = l / p.parts;
-        if (s.join.add[b] == -INFINITY) continue;
-        for (int32_t i = 0; i < p.keep; ++i) {
-            const BeamEntry e = load(l, i);
-            if (e.token < 0) break;
-            const float v = relative(e, b) + s.join.add32[b];
-            if (v + slack(v, b) < limit) break;  // (not so where v is -infinity and the slack infinite)
-            const BeamCand c = cand(e, b);
-            if (c.order <= beam_order(-(double)INFINITY)) break;
-            const int32_t at = atomicAdd(&s.n, 1);
-            if (at < kBeamJoin) s.join.pool[at] = c;
-        }
-    }
+    beam_limit(s, p.keep, width);
+    __syncthreads();
+    const float limit = beam_value(s.limit);
+    each([&](const BeamEntry &e, int b) {
+        if (e.token < 0) return;
+        const float add = s.join.add32[b];
+        if (add == -INFINITY) return;
+        const float v = relative(e.x, s.join.top[b]) + add;
+        if (v + slack(v, add) < limit) return;  // (not so where v is -infinity and the slack infinite)
+        const int32_t at = atomicAdd(&s.n, 1);
+        if (at < kBeamJoin) s.join.pool[at] = e, s.join.row[at] = b;
+    });
     __syncthreads();
     int32_t n = s.n;
+    const uint64_t none = beam_order(-(double)INFINITY);
     if (n <= kBeamJoin) {
+        for (int i = tid; i < n; i += kBeamThreads) s.join.order[i] = order_of(s.join.pool[i].x, s.join.row[i]);
+        __syncthreads();
+        int32_t real = 0;
         for (int i0 = 0; i0 < n; i0 += kBeamThreads / 4) {
             const int i = min(i0 + tid / 4, n - 1);
-            const BeamCand c = s.join.pool[i];
+            const uint64_t order = s.join.order[i];
+            const BeamEntry e = s.join.pool[i];
+            const int32_t b = s.join.row[i];
             int32_t rank = 0;
-            for (int j = tid % 4; j < n; j += 4) rank += beam_before(s.join.pool[j], c);
+#pragma unroll 4
+            for (int k = tid % 4; k < n; k += 4) {
+                const uint64_t other = s.join.order[k];
+                rank += other > order;
+                if (other == order) {  // the lower beam, then token
+                    const int32_t c = s.join.row[k];
+                    rank += c < b || (c == b && s.join.pool[k].token < e.token);
+                }
+            }
             rank += __shfl_xor_sync(~0u, rank, 1);
             rank += __shfl_xor_sync(~0u, rank, 2);
-            if (tid % 4 == 0 && i0 + tid / 4 < n && rank < p.keep) s.join.best[rank] = c;
+            if (tid % 4 == 0 && i0 + tid / 4 < n && order > none) {
+                ++real;
+                if (rank < p.keep) s.join.best[rank] = e, s.join.best_row[rank] = b, s.join.best_order[rank] = order;
+            }
         }
+        real = __reduce_add_sync(~0u, real);
+        if (lane == 0) s.low[warp] = (uint32_t)real;
+        __syncthreads();
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < kBeamThreads / 32; ++i) n += (int32_t)s.low[i];
         n = min(n, p.keep);
     } else {
         // too many (equal logits, say): the lists are merged, one candidate at a time
         for (int32_t l = tid; l < lists; l += kBeamThreads) s.at[l] = 0;
         for (n = 0; n < p.keep; ++n) {
             BeamCand c = {0, ~0ull};
+            BeamEntry mine = {0.0f, -1};
             int32_t from = -1;
             for (int32_t l = tid; l < lists; l += kBeamThreads) {
                 const int b = l / p.parts, i = s.at[l];
-                if (i >= p.keep || s.join.add[b] == -INFINITY) continue;
+                if (i >= p.keep || s.join.add32[b] == -INFINITY) continue;
                 const BeamEntry e = load(l, i);
                 if (e.token < 0) continue;
-                const BeamCand other = cand(e, b);
-                if (other.order > beam_order(-(double)INFINITY) && beam_before(other, c)) c = other, from = l;
+                const BeamCand other = {order_of(e.x, b), (uint64_t)b << 32 | (uint32_t)e.token};
+                if (other.order > none && beam_before(other, c)) c = other, from = l, mine = e;
             }
             BeamCand w = c;
 #pragma unroll
@@ -513,8 +713,10 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, BeamShared &s, in
             for (int i = 1; i < kBeamThreads / 32; ++i)
                 if (beam_before(s.join.warp[i], w)) w = s.join.warp[i];
             if (w.order == 0) break;  // no more
-            if (from >= 0 && c.place == w.place) s.at[from] += 1;
-            if (tid == 0) s.join.best[n] = w;
+            if (from >= 0 && c.place == w.place) {
+                s.at[from] += 1;
+                s.join.best[n] = mine, s.join.best_row[n] = (int32_t)(w.place >> 32), s.join.best_order[n] = w.order;
+            }
             __syncthreads();
         }
     }
@@ -527,11 +729,9 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, BeamShared &s, in
             int32_t token = -1, parent = -1;
             float score = -INFINITY;
             if (i < n) {
-                const BeamCand c = s.join.best[i];
-                const int b = (int)(c.place / (uint64_t)p.vocab);
-                token = (int32_t)(c.place - (uint64_t)b * (uint64_t)p.vocab);
-                parent = (int32_t)(row0 + b);
-                score = (float)beam_value(c.order);
+                token = s.join.best[i].token;
+                parent = (int32_t)(row0 + s.join.best_row[i]);
+                score = (float)beam_value(s.join.best_order[i]);
             }
             if (i < p.take) {
                 const int64_t at = (int64_t)request * p.take + i;
@@ -547,7 +747,7 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, BeamShared &s, in
 }
 
 template <bool BF16, int E>
-__global__ void __launch_bounds__(kBeamThreads, E == 32 && !BF16 ? 4 : 6) w12_beam_select_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kBeamThreads, kBeamCtas) w12_beam_select_kernel(const __grid_constant__ BeamParams p) {
     extern __shared__ uint4 beam_dyn[];
     BeamShared &s = *reinterpret_cast<BeamShared *>(beam_dyn);
     const int tid = threadIdx.x;
