@@ -554,6 +554,9 @@ int w12_kv_attend(const w12_kv_cache *cache, const w12_kv_attend_args *args, voi
  * the page is absent (-1) and not copied, and w12_check_status returns BUFFER_TOO_SMALL;
  * where a length, a parent (others than -1 count as none) or owned had to be clamped, SHAPE.
  * All arrays 4-byte aligned, ring_state 8-byte; none overlaps another, but lens_out lens.
+ * workspace: w12_kv_fork_workspace_size bytes (the pointers in args are not looked at for
+ * that, but for whether there is a prefix_cu), 256-byte aligned, ZERO-FILLED BEFORE ITS FIRST
+ * USE; calls that share one are ordered on the GPU.
  */
 typedef struct w12_kv_fork_args {
     const int32_t *parents, *lens;
@@ -571,7 +574,9 @@ typedef struct w12_kv_fork_args {
     int32_t requests, max_blocks, page_size, ring_size, groups;
 } w12_kv_fork_args;
 
-int w12_kv_fork(const w12_kv_fork_args *args, void *stream);
+int w12_kv_fork_workspace_size(const w12_kv_fork_args *args, size_t *bytes);
+
+int w12_kv_fork(const w12_kv_fork_args *args, void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * Pages copied inside each of `count` caches (a model's layers) that are alike in all but

@@ -727,31 +727,55 @@ int w12_kv_attend(const w12_kv_cache *cache, const w12_kv_attend_args *args, voi
     });
 }
 
-int w12_kv_fork(const w12_kv_fork_args *args, void *stream) {
+namespace {
+int check_kv_fork(const w12_kv_fork_args *args, std::string &err) {
+    if (!args) {
+        err = "args is null";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (args->requests < 1 || args->max_blocks < 1 || args->num_pages < 1 ||
+        !args->prefix_cu != !args->prefix_lens || (args->prefix_cu && args->groups < 1)) {
+        err = "requests, max_blocks and num_pages must be at least 1, and prefix_cu and prefix_lens given together, "
+              "with groups";
+        return W12_ERR_INVALID_ARG;
+    }
+    if (args->requests > 4096 || args->num_pages > 0x7FFFFFFF || args->ring_size < args->num_pages ||
+        (args->prefix_cu && args->groups > args->requests)) {
+        err = "requests must be at most 4096, ring_size at least num_pages (below 2^31) and groups at most requests";
+        return W12_ERR_SHAPE;
+    }
+    if (args->page_size < 16 || args->page_size % 16 != 0 ||
+        (int64_t)args->max_blocks * args->page_size >= (int64_t(1) << 31) ||
+        (int64_t)args->max_blocks * args->requests >= (int64_t(1) << 31) ||
+        args->table_stride < args->max_blocks) {
+        err = "page_size must be a multiple of 16, max_blocks * page_size and max_blocks * requests below 2^31 and "
+              "table_stride at least max_blocks";
+        return W12_ERR_SHAPE;
+    }
+    return W12_OK;
+}
+}  // namespace
+
+int w12_kv_fork_workspace_size(const w12_kv_fork_args *args, size_t *bytes) {
     return guarded([&](std::string &err) {
-        if (!args || !args->parents || !args->lens || !args->owned || !args->tables || !args->ring ||
-            !args->ring_state || !args->shares || !args->src || !args->dst || !args->rows) {
+        const int rc = check_kv_fork(args, err);
+        if (rc != W12_OK) return rc;
+        if (!bytes) {
+            err = "bytes is null";
+            return (int)W12_ERR_INVALID_ARG;
+        }
+        return w12::launch::kv_fork_workspace_size(*args, bytes);
+    });
+}
+
+int w12_kv_fork(const w12_kv_fork_args *args, void *workspace, size_t ws_bytes, void *stream) {
+    return guarded([&](std::string &err) {
+        const int rc = check_kv_fork(args, err);
+        if (rc != W12_OK) return rc;
+        if (!args->parents || !args->lens || !args->owned || !args->tables || !args->ring || !args->ring_state ||
+            !args->shares || !args->src || !args->dst || !args->rows || !workspace) {
             err = "null pointer";
             return (int)W12_ERR_INVALID_ARG;
-        }
-        if (args->requests < 1 || args->max_blocks < 1 || args->num_pages < 1 ||
-            !args->prefix_cu != !args->prefix_lens || (args->prefix_cu && args->groups < 1)) {
-            err = "requests, max_blocks and num_pages must be at least 1, and prefix_cu and prefix_lens given together, "
-                  "with groups";
-            return (int)W12_ERR_INVALID_ARG;
-        }
-        if (args->requests > 4096 || args->num_pages > 0x7FFFFFFF || args->ring_size < args->num_pages ||
-            (args->prefix_cu && args->groups > args->requests)) {
-            err = "requests must be at most 4096, ring_size at least num_pages (below 2^31) and groups at most requests";
-            return (int)W12_ERR_SHAPE;
-        }
-        if (args->page_size < 16 || args->page_size % 16 != 0 ||
-            (int64_t)args->max_blocks * args->page_size >= (int64_t(1) << 31) ||
-            (int64_t)args->max_blocks * args->requests >= (int64_t(1) << 31) ||
-            args->table_stride < args->max_blocks) {
-            err = "page_size must be a multiple of 16, max_blocks * page_size and max_blocks * requests below 2^31 and "
-                  "table_stride at least max_blocks";
-            return (int)W12_ERR_SHAPE;
         }
         for (const void *p : {(const void *)args->parents, (const void *)args->lens, (const void *)args->lens_out,
                               (const void *)args->owned, (const void *)args->tables, (const void *)args->ring,
@@ -762,11 +786,11 @@ int w12_kv_fork(const w12_kv_fork_args *args, void *stream) {
                 err = "32-bit arrays must be 4-byte aligned";
                 return (int)W12_ERR_ALIGNMENT;
             }
-        if (!aligned(args->ring_state, 8)) {
-            err = "ring_state must be 8-byte aligned";
+        if (!aligned(args->ring_state, 8) || !aligned(workspace, 256)) {
+            err = "ring_state must be 8-byte and workspace 256-byte aligned";
             return (int)W12_ERR_ALIGNMENT;
         }
-        return w12::launch::kv_fork(*args, stream, &err);
+        return w12::launch::kv_fork(*args, workspace, ws_bytes, stream, &err);
     });
 }
 

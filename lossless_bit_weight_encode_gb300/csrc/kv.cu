@@ -25,23 +25,14 @@ int attend_dim<256>(const DeviceView &, bool, int, int *, const dev::KvAttendPar
                     const CUtensorMap *, int, void *, std::string *);
 
 template <>
-int shared_dim<64>(const DeviceView &, bool, int, int *, const dev::KvPrefixParams *, const CUtensorMap *, const CUtensorMap *,
-                   int, void *, std::string *);
+int shared_dim<64>(const DeviceView &, bool, int, dev::KvSpans, int *, const dev::KvSharedParams *, const CUtensorMap *,
+                   const CUtensorMap *, int, void *, std::string *);
 template <>
-int shared_dim<64>(const DeviceView &, bool, int, int *, const dev::KvOwnParams *, const CUtensorMap *, const CUtensorMap *,
-                   int, void *, std::string *);
+int shared_dim<128>(const DeviceView &, bool, int, dev::KvSpans, int *, const dev::KvSharedParams *, const CUtensorMap *,
+                    const CUtensorMap *, int, void *, std::string *);
 template <>
-int shared_dim<128>(const DeviceView &, bool, int, int *, const dev::KvPrefixParams *, const CUtensorMap *, const CUtensorMap *,
-                    int, void *, std::string *);
-template <>
-int shared_dim<128>(const DeviceView &, bool, int, int *, const dev::KvOwnParams *, const CUtensorMap *, const CUtensorMap *,
-                    int, void *, std::string *);
-template <>
-int shared_dim<256>(const DeviceView &, bool, int, int *, const dev::KvPrefixParams *, const CUtensorMap *, const CUtensorMap *,
-                    int, void *, std::string *);
-template <>
-int shared_dim<256>(const DeviceView &, bool, int, int *, const dev::KvOwnParams *, const CUtensorMap *, const CUtensorMap *,
-                    int, void *, std::string *);
+int shared_dim<256>(const DeviceView &, bool, int, dev::KvSpans, int *, const dev::KvSharedParams *, const CUtensorMap *,
+                    const CUtensorMap *, int, void *, std::string *);
 
 namespace {
 
@@ -83,6 +74,22 @@ std::mutex &workspace_lock(const void *workspace) {
     static std::mutex locks[64];
     const uint64_t at = reinterpret_cast<uintptr_t>(workspace) >> 8;
     return locks[(at ^ at >> 6 ^ at >> 12) % 64];
+}
+
+// A fork's columns per CTA and CTAs, and its workspace: what has to stay zero comes first and
+// has one place and size in all plans.
+struct ForkPlan {
+    int cols = dev::kForkCols, ctas = 1;
+    size_t off_state = 0, bytes = 0;
+};
+
+ForkPlan fork_plan(const w12_kv_fork_args &a) {
+    ForkPlan plan;
+    if ((int64_t)a.requests * a.max_blocks <= dev::kForkOne) plan.cols = a.max_blocks;
+    plan.ctas = (a.max_blocks + plan.cols - 1) / plan.cols;
+    plan.off_state = (size_t)dev::kForkRows * sizeof(int32_t);
+    plan.bytes = plan.off_state + 16 + ((size_t)4 * a.requests + plan.ctas) * sizeof(int32_t);
+    return plan;
 }
 
 int attend_call(const DeviceView &d, const w12_kv_cache &c, int rows, int *resident, const dev::KvAttendParams *p,
@@ -164,24 +171,26 @@ dev::KvAttendParams attend_params(const DeviceView &d, const w12_kv_cache &c, co
     return p;
 }
 
-// The two lines of a call with shared prefixes (0: the prefixes, 1: the own tokens) and the
-// places of their buffers in the workspace.
+// A call with shared prefixes: its launches (one over all spans, or one over the prefixes and
+// one over the own tokens) and the places of their buffers in the workspace.
 struct SharedPlan {
     struct Line {
         int rows = 8, ctas = 1;
-        size_t off_part = 0, off_ml = 0, off_row = 0, off_row_ml = 0, off_info = 0;
+        dev::KvSpans kind = dev::kKvAllSpans;
+        size_t off_part = 0, off_ml = 0;
     } line[2];
-    size_t bytes = 0;
+    int lines = 1;
+    size_t off_row = 0, off_row_ml = 0, off_info = 0, bytes = 0;
 };
 
-template <class P>
-int shared_call(const DeviceView &d, const w12_kv_cache &c, int rows, int *resident, const P *p,
-                const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+int shared_call(const DeviceView &d, const w12_kv_cache &c, int rows, dev::KvSpans kind, int *resident,
+                const dev::KvSharedParams *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream,
+                std::string *err) {
     const bool q8 = c.dtype == W12_KV_Q8;
     switch (c.head_dim) {
-    case 64: return shared_dim<64>(d, q8, rows, resident, p, tm_k, tm_v, ctas, stream, err);
-    case 128: return shared_dim<128>(d, q8, rows, resident, p, tm_k, tm_v, ctas, stream, err);
-    default: return shared_dim<256>(d, q8, rows, resident, p, tm_k, tm_v, ctas, stream, err);
+    case 64: return shared_dim<64>(d, q8, rows, kind, resident, p, tm_k, tm_v, ctas, stream, err);
+    case 128: return shared_dim<128>(d, q8, rows, kind, resident, p, tm_k, tm_v, ctas, stream, err);
+    default: return shared_dim<256>(d, q8, rows, kind, resident, p, tm_k, tm_v, ctas, stream, err);
     }
 }
 
@@ -189,31 +198,32 @@ int shared_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_
                 SharedPlan *plan, std::string *err) {
     const int group = a.heads / c.kv_heads, max_new = std::max(a.max_new, 1);
     const bool q8 = c.dtype == W12_KV_Q8;
+    const int64_t together = std::min<int64_t>((int64_t)std::max(x.max_requests, 1) * max_new, a.tokens);
+    plan->line[0].rows = attend_rows((int)together, group, c.kv_heads, x.groups, q8, d.sm_count);
+    plan->line[1].rows = q8 ? attend_rows(max_new, group, c.kv_heads, a.requests, q8, d.sm_count) : plan->line[0].rows;
+    plan->lines = plan->line[0].rows == plan->line[1].rows ? 1 : 2;
     const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     size_t at = 0;
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < plan->lines; ++i) {
         SharedPlan::Line &l = plan->line[i];
-        const int spans = i == 0 ? x.groups : a.requests;
-        const int64_t tokens = i == 0 ? std::min<int64_t>((int64_t)std::max(x.max_requests, 1) * max_new, a.tokens) : max_new;
-        l.rows = attend_rows((int)std::min<int64_t>(tokens, 1 << 20), group, c.kv_heads, spans, q8, d.sm_count);
         int resident = 0;
-        const int rc = i == 0 ? shared_call<dev::KvPrefixParams>(d, c, l.rows, &resident, nullptr, nullptr, nullptr, 0,
-                                                                 nullptr, err)
-                              : shared_call<dev::KvOwnParams>(d, c, l.rows, &resident, nullptr, nullptr, nullptr, 0,
-                                                              nullptr, err);
+        if (plan->lines == 2) l.kind = i == 0 ? dev::kKvPrefixes : dev::kKvOwnSpans;
+        const int rc = shared_call(d, c, l.rows, l.kind, &resident, nullptr, nullptr, nullptr, 0, nullptr, err);
         if (rc != W12_OK) return rc;
-        // no more CTAs than units can exist
-        const int64_t blocks = spans + (int64_t)a.tokens * group / l.rows;
+        // no more CTAs than tiles can exist
+        const int64_t blocks = x.groups + a.requests + 2 * ((int64_t)a.tokens * group / l.rows);
         const int64_t tiles = ((int64_t)a.max_blocks * c.page_size + dev::kAttendTile - 1) / dev::kAttendTile;
         l.ctas = (int)std::min<int64_t>(resident, std::max<int64_t>(1, blocks * c.kv_heads * tiles));
-        const size_t slots = (size_t)2 * l.ctas * l.rows, rows = (size_t)a.tokens * a.heads;
+        const size_t slots = (size_t)2 * l.ctas * l.rows;
         l.off_part = at, at += up(slots * c.head_dim * sizeof(float));
         l.off_ml = at, at += up(slots * sizeof(float2));
-        l.off_row = at, at += up(rows * c.head_dim * sizeof(float));
-        l.off_row_ml = at, at += up(rows * sizeof(float2));
-        l.off_info = at, at += up(rows * sizeof(int2));
     }
-    plan->bytes = at;
+    if (plan->lines == 1) plan->line[1] = plan->line[0];
+    const size_t rows = (size_t)2 * a.tokens * a.heads;
+    plan->off_row = at;
+    plan->off_row_ml = plan->off_row + up(rows * c.head_dim * sizeof(float));
+    plan->off_info = plan->off_row_ml + up(rows * sizeof(float2));
+    plan->bytes = plan->off_info + up(rows * sizeof(int2));
     return W12_OK;
 }
 
@@ -375,7 +385,12 @@ int kv_read(const w12_kv_cache &c, const int64_t *slots, int32_t tokens, uint16_
     return W12_OK;
 }
 
-int kv_fork(const w12_kv_fork_args &a, void *stream, std::string *err) {
+int kv_fork_workspace_size(const w12_kv_fork_args &a, size_t *bytes) {
+    *bytes = fork_plan(a).bytes;
+    return W12_OK;
+}
+
+int kv_fork(const w12_kv_fork_args &a, void *workspace, size_t ws_bytes, void *stream, std::string *err) {
     DeviceView d;
     const int rc = device_view(&d, err);
     if (rc != W12_OK) return rc;
@@ -396,33 +411,53 @@ int kv_fork(const w12_kv_fork_args &a, void *stream, std::string *err) {
     p.prefix_lens = a.prefix_lens;
     p.num_pages = a.num_pages;
     p.ring_inv = ~uint64_t(0) / (uint64_t)a.ring_size;
+    p.rows_inv = (uint32_t)(((uint64_t(1) << 32) + a.requests - 1) / a.requests);
     p.requests = a.requests;
     p.max_blocks = a.max_blocks;
     p.page_size = a.page_size;
     p.ring_size = a.ring_size;
     p.groups = a.groups;
     p.status = d.status;
-    const void *kernel = reinterpret_cast<const void *>(&dev::w12_kv_fork_kernel);
+    const ForkPlan plan = fork_plan(a);
+    if (ws_bytes < plan.bytes) {
+        *err = "workspace smaller than w12_kv_fork_workspace_size";
+        return W12_ERR_BUFFER_TOO_SMALL;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.differ = reinterpret_cast<int32_t *>(ws);
+    p.old_state = reinterpret_cast<int64_t *>(ws + plan.off_state);
+    p.need = reinterpret_cast<int32_t *>(ws + plan.off_state + 16);
+    p.held = p.need + a.requests;
+    p.parent = p.held + a.requests;
+    p.copies = p.parent + a.requests;
+    p.counts = p.copies + a.requests;
+    p.cols = plan.cols;
     static std::mutex mu;
     static bool set[kKvMaxDevices] = {};
     cudaError_t e = cudaSuccess;
     if (d.device >= 0 && d.device < kKvMaxDevices) {
         std::lock_guard<std::mutex> lock(mu);
-        if (!set[d.device]) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess)
+        for (const void *kernel : {reinterpret_cast<const void *>(&dev::w12_kv_fork_kernel<0>),
+                                   reinterpret_cast<const void *>(&dev::w12_kv_fork_kernel<1>),
+                                   reinterpret_cast<const void *>(&dev::w12_kv_fork_kernel<2>)})
+            if (!set[d.device] && e == cudaSuccess)
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         dev::fork_smem(dev::kForkRows));
-            if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_fork set-up", err);
-            set[d.device] = true;
-        }
+                                         dev::fork_smem(dev::kForkRows, dev::kForkCols));
+        if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_fork set-up", err);
+        set[d.device] = true;
     }
-    // a CTA for every chunk of columns, as far as a cluster goes; one where that is little
-    const int chunks = (a.max_blocks + dev::kForkCols - 1) / dev::kForkCols;
-    int cluster = 1;
-    while (cluster < 16 && cluster < chunks && (int64_t)chunks * dev::kForkCols * a.requests > cluster * 1024) cluster *= 2;
-    e = kv_launch(d, &dev::w12_kv_fork_kernel, dim3((unsigned)cluster), dev::kForkThreads, dev::fork_smem(a.requests),
-                  cluster, stream, p);
+    const int smem = dev::fork_smem(a.requests, plan.cols);
+    const int64_t line = (int64_t)plan.cols * a.requests;
+    const int threads = (int)std::min<int64_t>(1024, (std::max<int64_t>(line / 2, a.requests) + 127) / 128 * 128);
+    // held over both launches, as the locks of the attend calls
+    const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
+    if (plan.ctas == 1) {
+        e = kv_launch(d, &dev::w12_kv_fork_kernel<0>, dim3(1), threads, smem, 1, stream, p);
+    } else {
+        e = kv_launch(d, &dev::w12_kv_fork_kernel<1>, dim3((unsigned)plan.ctas), threads, smem, 1, stream, p);
+        if (e == cudaSuccess)
+            e = kv_launch(d, &dev::w12_kv_fork_kernel<2>, dim3((unsigned)plan.ctas), threads, smem, 1, stream, p);
+    }
     if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_fork launch", err);
     return W12_OK;
 }
@@ -534,46 +569,34 @@ int kv_attend_shared(const w12_kv_cache &c, const w12_kv_attend_args &a, const w
         return W12_ERR_BUFFER_TOO_SMALL;
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    dev::KvPrefixParams head;
-    dev::KvOwnParams own;
+    dev::KvSharedParams p = {};
+    static_cast<dev::KvAttendParams &>(p) = attend_params(d, c, a);
+    p.prefix_cu = prefix.cu;
+    p.prefix_lens = prefix.lens;
+    p.groups = prefix.groups;
+    p.row_part = reinterpret_cast<float *>(ws + plan.off_row);
+    p.row_ml = reinterpret_cast<float2 *>(ws + plan.off_row_ml);
+    p.row_info = reinterpret_cast<int2 *>(ws + plan.off_info);
+    dev::KvSharedJoin join = {a.out,      a.lse,    a.out_stride, a.cu_new, a.tokens, a.heads,
+                              a.requests, p.row_part, p.row_ml,   p.row_info, {}};
     CUtensorMap tm[2][2];
-    dev::KvSharedJoin join;
+    for (int i = 0; i < plan.lines; ++i) {
+        const bool tc = plan.line[i].rows == dev::kTcRows;
+        rc = cache_map(c, tc, c.k_dev, &tm[i][0], err);
+        if (rc == W12_OK) rc = cache_map(c, tc, c.v_dev, &tm[i][1], err);
+        if (rc != W12_OK) return rc;
+    }
+    const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
     for (int i = 0; i < 2; ++i) {
         const SharedPlan::Line &l = plan.line[i];
-        const bool tc = l.rows == dev::kTcRows, again = i == 1 && tc == (plan.line[0].rows == dev::kTcRows);
-        if (again) {
-            tm[1][0] = tm[0][0], tm[1][1] = tm[0][1];
-        } else {
-            rc = cache_map(c, tc, c.k_dev, &tm[i][0], err);
-            if (rc == W12_OK) rc = cache_map(c, tc, c.v_dev, &tm[i][1], err);
-            if (rc != W12_OK) return rc;
-        }
-        dev::KvSharedParams &p = i == 0 ? static_cast<dev::KvSharedParams &>(head) : own;
-        static_cast<dev::KvAttendParams &>(p) = attend_params(d, c, a);
-        if (i == 0) p.tree = nullptr;  // all of a prefix is seen
-        p.prefix_cu = prefix.cu;
-        p.prefix_lens = prefix.lens;
-        p.groups = prefix.groups;
         p.part = reinterpret_cast<float *>(ws + l.off_part);
         p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
-        p.row_part = reinterpret_cast<float *>(ws + l.off_row);
-        p.row_ml = reinterpret_cast<float2 *>(ws + l.off_row_ml);
-        p.row_info = reinterpret_cast<int2 *>(ws + l.off_info);
-        join.line[i] = {p.part, p.row_part, p.part_ml, p.row_ml, p.row_info, l.rows};
+        join.line[i] = {p.part, p.part_ml, l.rows};
+        if (i == plan.lines) break;
+        int resident = 0;
+        rc = shared_call(d, c, l.rows, l.kind, &resident, &p, &tm[i][0], &tm[i][1], l.ctas, stream, err);
+        if (rc != W12_OK) return rc;
     }
-    join.out = a.out;
-    join.lse = a.lse;
-    join.out_stride = a.out_stride;
-    join.cu_new = a.cu_new;
-    join.tokens = a.tokens;
-    join.heads = a.heads;
-    join.requests = a.requests;
-    int resident = 0;
-    const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
-    rc = shared_call(d, c, plan.line[0].rows, &resident, &head, &tm[0][0], &tm[0][1], plan.line[0].ctas, stream, err);
-    if (rc == W12_OK)
-        rc = shared_call(d, c, plan.line[1].rows, &resident, &own, &tm[1][0], &tm[1][1], plan.line[1].ctas, stream, err);
-    if (rc != W12_OK) return rc;
     const int64_t rows = (int64_t)a.tokens * a.heads, per = dev::kJoinThreads / 32;
     const auto kernel = c.head_dim == 64    ? &dev::w12_kv_join_shared_kernel<64>
                         : c.head_dim == 128 ? &dev::w12_kv_join_shared_kernel<128>

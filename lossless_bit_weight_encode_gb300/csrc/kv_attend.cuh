@@ -193,64 +193,86 @@ __device__ __forceinline__ int32_t kv_shared_tokens(const KvSharedParams &p, int
     return n / p.page_size * p.page_size;
 }
 
-// What a request has of its own: its table and its tokens begin behind the prefix.
-template <int ROWS, int TILE>
-__device__ __forceinline__ KvRequest kv_request(const KvOwnParams &p, int b) {
-    const int32_t shared = kv_shared_tokens(p, b);
-    KvRequest r;
-    r.q0 = min(max(p.cu_new[b], 0), p.tokens);
-    r.qlen = min(max(p.cu_new[b + 1], r.q0), p.tokens) - r.q0;
-    r.past = min(max(p.lens[b], 0), p.max_keys) - shared;
-    r.kv = (int32_t)min((int64_t)r.past + r.qlen, (int64_t)p.max_keys - shared);
-    r.first = r.tile0 = 0;
-    r.ntiles = r.kv > 0 ? (r.kv - 1) / TILE + 1 : 1;
-    r.rblocks = (int32_t)(((int64_t)r.qlen * p.group + ROWS - 1) / ROWS);
-    r.units = (int64_t)p.kv_heads * r.rblocks * r.ntiles;
-    return r;
-}
-__device__ __forceinline__ const int32_t *kv_table_row(const KvOwnParams &p, int b) {
-    return p.tables + (int64_t)b * p.table_stride + kv_shared_tokens(p, b) / p.page_size;
-}
-
-// A group's prefix, that of the first of its requests that shares one (-1: none does).
-__device__ __forceinline__ int kv_leader(const KvPrefixParams &p, int b0, int b1) {
+// The group's first request that shares a prefix (-1: none does).
+__device__ __forceinline__ int kv_leader(const KvSharedParams &p, int b0, int b1) {
     for (int b = b0; b < b1; ++b)
         if (kv_shared_tokens(p, b) > 0) return b;
     return -1;
 }
-__device__ __forceinline__ void kv_group(const KvPrefixParams &p, int g, int &b0, int &b1) {
+__device__ __forceinline__ void kv_group(const KvSharedParams &p, int g, int &b0, int &b1) {
     b0 = min(max(p.prefix_cu[g], 0), p.requests);
     b1 = min(max(p.prefix_cu[g + 1], b0), p.requests);
 }
-// The group as a request: the new tokens of all its requests, which see all of the prefix.
-// (The rows of a request in it that shares nothing are not joined with what comes out.)
-template <int ROWS, int TILE>
-__device__ __forceinline__ KvRequest kv_request(const KvPrefixParams &p, int g) {
-    int b0, b1;
-    kv_group(p, g, b0, b1);
-    const int lead = kv_leader(p, b0, b1);
+
+// Span s of the launch: a group as a request, with the new tokens of all its requests, which
+// see all of the prefix (the rows of a request in it that shares nothing are not joined with
+// what comes out); or what a request has of its own, whose table and tokens begin behind
+// the prefix.
+template <int ROWS, int TILE, KvSpans KIND>
+__device__ __forceinline__ KvRequest kv_request(const KvSpanParams<KIND> &p, int s) {
     KvRequest r;
-    r.past = r.kv = lead < 0 ? 0 : kv_shared_tokens(p, lead);
+    s += p.first_span();
+    const bool own = KIND == kKvOwnSpans || (KIND == kKvAllSpans && s >= p.groups);
+    int b0 = s - p.groups, b1 = b0 + 1, shared;
+    if (own) {
+        shared = kv_shared_tokens(p, b0);
+    } else {
+        kv_group(p, s, b0, b1);
+        const int lead = kv_leader(p, b0, b1);
+        shared = lead < 0 ? 0 : kv_shared_tokens(p, lead);
+        if (lead < 0) b1 = b0;
+    }
     r.q0 = min(max(p.cu_new[b0], 0), p.tokens);
-    r.qlen = lead < 0 ? 0 : min(max(p.cu_new[b1], r.q0), p.tokens) - r.q0;
+    r.qlen = min(max(p.cu_new[b1], r.q0), p.tokens) - r.q0;
+    r.past = own ? min(max(p.lens[b0], 0), p.max_keys) - shared : shared;
+    r.kv = own ? (int32_t)min((int64_t)r.past + r.qlen, (int64_t)p.max_keys - shared) : shared;
     r.first = r.tile0 = 0;
     r.ntiles = r.kv > 0 ? (r.kv - 1) / TILE + 1 : 1;
     r.rblocks = (int32_t)(((int64_t)r.qlen * p.group + ROWS - 1) / ROWS);
-    r.units = (int64_t)p.kv_heads * r.rblocks * r.ntiles;
+    r.units = (int64_t)p.kv_heads * r.rblocks * (r.ntiles + kKvBlockUnits);
     return r;
 }
-__device__ __forceinline__ const int32_t *kv_table_row(const KvPrefixParams &p, int g) {
-    int b0, b1;
-    kv_group(p, g, b0, b1);
-    return p.tables + (int64_t)max(kv_leader(p, b0, b1), 0) * p.table_stride;
+template <KvSpans KIND>
+__device__ __forceinline__ const int32_t *kv_table_row(const KvSpanParams<KIND> &p, int s) {
+    s += p.first_span();
+    const bool own = KIND == kKvOwnSpans || (KIND == kKvAllSpans && s >= p.groups);
+    int b0 = s - p.groups, b1;
+    if (!own) {
+        kv_group(p, s, b0, b1);
+        b0 = max(kv_leader(p, b0, b1), 0);
+    }
+    return p.tables + (int64_t)b0 * p.table_stride + (own ? kv_shared_tokens(p, b0) / p.page_size : 0);
 }
 
-// What a launch's line has: requests, or groups.
+// What a launch's line has: requests, or groups and requests.
 __device__ __forceinline__ int32_t kv_spans(const KvAttendParams &p) { return p.requests; }
-__device__ __forceinline__ int32_t kv_spans(const KvPrefixParams &p) { return p.groups; }
+template <KvSpans KIND>
+__device__ __forceinline__ int32_t kv_spans(const KvSpanParams<KIND> &p) {
+    return KIND == kKvAllSpans ? p.groups + p.requests : KIND == kKvPrefixes ? p.groups : p.requests;
+}
+
+// How the two launches of a call follow one another: the first waits for what is before the
+// call; the second begins when every CTA of that has done so, with a fence for what its SM's
+// L1 has had since before, takes the SMs as they become free and ends when the first has.
+template <class P>
+constexpr bool kKvSecond = false;
+template <>
+constexpr bool kKvSecond<KvSpanParams<kKvOwnSpans>> = true;
+template <class P>
+__device__ __forceinline__ void kv_begin() {
+    if (kKvSecond<P>) __threadfence();
+    else pdl_wait();
+}
+template <class P>
+__device__ __forceinline__ void kv_end() {
+    if (kKvSecond<P>) pdl_wait();
+}
 
 template <class P>
 constexpr bool kKvShared = !std::is_same_v<P, KvAttendParams>;
+// Units of a row block ahead of those of its tiles.
+template <class P>
+constexpr int32_t kKvAhead = kKvShared<P> ? kKvBlockUnits : 0;
 
 // A CTA's range of units and its place in it; every warp keeps its own copy.
 struct KvWalk {
@@ -289,6 +311,14 @@ __device__ __forceinline__ KvSums kv_sum_units(const P &p) {
     return s;
 }
 
+// A range that ends before the block's first tile has nothing of it.
+template <class P>
+__device__ __forceinline__ void kv_skip(KvWalk &w, const KvRequest &r) {
+    if (w.u >= w.end) return;
+    const int64_t at = (w.u - w.start) % (r.ntiles + kKvAhead<P>);
+    if (w.end - w.u + at <= kKvAhead<P>) w.u = w.end;
+}
+
 template <int ROWS, int TILE, class P>
 __device__ __forceinline__ bool kv_walk_init(const P &p, KvWalk &w, KvRequest &r) {
     const KvSums s = kv_sum_units<ROWS, TILE>(p);
@@ -306,7 +336,34 @@ __device__ __forceinline__ bool kv_walk_init(const P &p, KvWalk &w, KvRequest &r
         w.start += r.units;
         r = kv_request<ROWS, TILE>(p, ++w.b);
     }
+    if constexpr (kKvShared<P>) {
+        kv_skip<P>(w, r);
+        return w.u < w.end;
+    }
     return true;
+}
+
+// The walk's beginning for all warps.  With shared prefixes, where it is the longer way (a
+// group's prefix is that of its first request that has one), warp `by` makes it for all of them
+// (system prompt, 65 spans: 2.4 us with every warp on its own).
+template <int ROWS, int TILE, class P>
+__device__ __forceinline__ bool kv_walk_start(const P &p, KvWalk &w, KvRequest &r, int by) {
+    if constexpr (!kKvShared<P>) return kv_walk_init<ROWS, TILE>(p, w, r);
+    __shared__ KvWalk s_w;
+    __shared__ KvRequest s_r;
+    __shared__ int s_some;
+    if ((int)threadIdx.x / 32 == by) {
+        const bool some = kv_walk_init<ROWS, TILE>(p, w, r);
+        if ((threadIdx.x & 31) == 0) {
+            s_some = some;
+            s_w = w;
+            s_r = r;
+        }
+    }
+    __syncthreads();
+    w = s_w;
+    r = s_r;
+    return s_some != 0;
 }
 
 // Table entries that the request's keys take.
@@ -319,15 +376,24 @@ struct KvPiece {
     int32_t head, rb, ja, jb;
 };
 
+template <class P = KvAttendParams>
 __device__ __forceinline__ KvPiece kv_piece(const KvWalk &w, const KvRequest &r) {
+    constexpr int32_t AHEAD = kKvAhead<P>;
     const int64_t off = w.u - w.start;
-    const int32_t item = (int32_t)(off / r.ntiles);
+    const int32_t item = (int32_t)(off / (r.ntiles + AHEAD));
     KvPiece c;
     c.head = item / r.rblocks;
     c.rb = item - c.head * r.rblocks;
-    c.ja = (int32_t)(off - (int64_t)item * r.ntiles);
+    c.ja = (int32_t)(off - (int64_t)item * (r.ntiles + AHEAD)) - AHEAD;
     c.jb = (int32_t)min((int64_t)r.ntiles, w.end - w.u + c.ja);
+    if (AHEAD > 0) c.ja = max(c.ja, 0);
     return c;
+}
+// The units of a piece that begins at w.u: those of its tiles and what is ahead of them.
+template <class P>
+__device__ __forceinline__ int32_t kv_piece_units(const KvWalk &w, const KvRequest &r, const KvPiece &c) {
+    if constexpr (kKvAhead<P> == 0) return c.jb - c.ja;
+    return (int32_t)min((r.ntiles + kKvAhead<P>) - (w.u - w.start) % (r.ntiles + kKvAhead<P>), w.end - w.u);
 }
 
 // Moves on by n units within the request, to the next request where it ends.
@@ -338,6 +404,7 @@ __device__ __forceinline__ void kv_advance(const P &p, KvWalk &w, KvRequest &r, 
         w.start += r.units;
         r = kv_request<ROWS, TILE>(p, ++w.b);
     }
+    if constexpr (kKvShared<P>) kv_skip<P>(w, r);
 }
 
 // Which keys of a slice one row sees.
@@ -407,11 +474,16 @@ __device__ __forceinline__ void kv_emit(const KvAttendParams &p, const KvRequest
 }
 
 // With shared prefixes nothing is finished yet: the sums as they are.
-template <int ROWS, int D>
-__device__ __forceinline__ void kv_emit(const KvSharedParams &p, const KvRequest &r, const KvPiece &c, int lr, int col,
-                                        float mm, float sum, const float4 &acc) {
-    const int32_t rr = c.rb * ROWS + lr, i = rr / p.group, tok = r.q0 + i, h = c.head * p.group + rr - i * p.group;
-    const int64_t at = (int64_t)tok * (p.group * p.kv_heads) + h;
+// Row lr of a piece in the three arrays of rows.
+template <int ROWS, class P>
+__device__ __forceinline__ int64_t kv_row_at(const P &p, const KvWalk &w, const KvRequest &r,
+                                             const KvPiece &c, int lr) {
+    const int32_t rr = c.rb * ROWS + lr, i = rr / p.group, heads = p.group * p.kv_heads;
+    return (int64_t)(r.q0 + i + (w.b + p.first_span() >= p.groups ? p.tokens : 0)) * heads + c.head * p.group + rr - i * p.group;
+}
+template <int D>
+__device__ __forceinline__ void kv_keep(const KvSharedParams &p, int64_t at, int col, float mm, float sum,
+                                        const float4 &acc) {
     *reinterpret_cast<float4 *>(p.row_part + at * D + col) = acc;
     if (col == 0) p.row_ml[at] = make_float2(mm, sum);
 }
@@ -437,36 +509,25 @@ __device__ __forceinline__ KvParts kv_parts(const KvAttendParams &p, const KvWal
 }
 
 // Where the joining kernel finds row lr of the piece's block; written by the CTA that has
-// the block's first unit.
+// the block's first tile.
 template <int ROWS, class P>
-__device__ __forceinline__ void kv_note(const P &p, const KvWalk &w, const KvRequest &r, const KvPiece &c, int lr,
-                                        bool whole) {
-    const int32_t rr = c.rb * ROWS + lr, i = rr / p.group;
-    const int64_t at = (int64_t)(r.q0 + i) * (p.group * p.kv_heads) + c.head * p.group + rr - i * p.group;
+__device__ __forceinline__ void kv_note(const P &p, const KvWalk &w, const KvRequest &r, const KvPiece &c,
+                                        int lr, bool whole) {
     int2 info = make_int2(0, 1);
     if (!whole) {
-        const KvParts q = kv_parts<ROWS>(p, w, r, c);
-        info = make_int2((int32_t)q.first + lr, q.n);
+        // the CTAs that have the block's first and last tile
+        const int64_t span = r.ntiles + kKvBlockUnits, s0 = w.u - (w.u - w.start) % span;
+        const int32_t c0 = (int32_t)(((s0 + kKvBlockUnits + 1) * w.ctas - 1) / w.total);
+        const int32_t c1 = (int32_t)(((s0 + span) * w.ctas - 1) / w.total);
+        info = make_int2(2 * c0 * ROWS + lr, c1 - c0 + 1);
     }
-    if constexpr (std::is_same_v<P, KvOwnParams>) {
-        if (kv_shared_tokens(p, w.b) > 0) info.y |= kKvSharesPrefix;
-        if (lr == 0 && kv_shared_tokens(p, w.b) != max(p.prefix_lens[w.b], 0)) atomicOr(p.status, kStatusKvSizes);
+    const int b = w.b + p.first_span() - p.groups;
+    if (b >= 0) {
+        const int shared = kv_shared_tokens(p, b);
+        if (shared > 0) info.y |= kKvSharesPrefix;
+        if (lr == 0 && shared != max(p.prefix_lens[b], 0)) atomicOr(p.status, kStatusKvSizes);
     }
-    p.row_info[at] = info;
-}
-
-// How the launches of one call with shared prefixes follow one another: the one over the
-// prefixes is first and waits for what is before the call; the one over the own tokens
-// begins when every CTA of that has done so, with a fence for what its SM's L1 has had
-// since before, and takes the SMs as they become free; it ends when the first one has.
-template <class P>
-__device__ __forceinline__ void kv_begin() {
-    if constexpr (std::is_same_v<P, KvOwnParams>) __threadfence();
-    else pdl_wait();
-}
-template <class P>
-__device__ __forceinline__ void kv_end() {
-    if constexpr (std::is_same_v<P, KvOwnParams>) pdl_wait();
+    p.row_info[kv_row_at<ROWS>(p, w, r, c, lr)] = info;
 }
 
 // Called by the 128 consumer threads when they have written the CTA's part to its
@@ -609,7 +670,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
 
     KvWalk w;
     KvRequest r;
-    if (!kv_walk_init<ROWS, TILE>(p, w, r)) {  // the same for the whole CTA
+    if (!kv_walk_start<ROWS, TILE>(p, w, r, 0)) {  // the same for the whole CTA
         kv_end<P>();
         return;
     }
@@ -619,7 +680,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
         uint32_t it = 0;
         bool ok = true;
         while (ok && w.u < w.end) {
-            const KvPiece c = kv_piece(w, r);
+            const KvPiece c = kv_piece<P>(w, r);
             KvPageWindow pages;
             pages.start(kv_table_row(p, w.b), (r.tile0 + c.ja) * TILE / p.page_size, kv_entries(p, r));
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
@@ -651,7 +712,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
                                  &full[stage]);
                 }
             }
-            if (ok) kv_advance<ROWS, TILE>(p, w, r, c.jb - c.ja);
+            if (ok) kv_advance<ROWS, TILE>(p, w, r, kv_piece_units<P>(w, r, c));
         }
         if (!ok) {
             // no copy may still be in flight when the CTA ends
@@ -673,7 +734,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
     uint32_t it = 0;
     bool ok = true;
     while (w.u < w.end) {
-        const KvPiece c = kv_piece(w, r);
+        const KvPiece c = kv_piece<P>(w, r);
         const int32_t nrows = min((int64_t)ROWS, (int64_t)r.qlen * p.group - (int64_t)c.rb * ROWS);
         const int32_t row0 = c.rb * ROWS;
         // every row sees the keys from low on and before lim
@@ -1034,10 +1095,12 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
                     sum += f * s.y;
                     acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
                 }
-                if constexpr (kKvShared<P>)
+                if constexpr (kKvShared<P>) {
                     if (c.ja == 0 && dc == 0 && v4 == 0) kv_note<ROWS>(p, w, r, c, lr, whole);
+                    if (whole) kv_keep<D>(p, kv_row_at<ROWS>(p, w, r, c, lr), dc * 64 + v4 * 4, mm, sum, acc);
+                }
                 if (whole) {
-                    kv_emit<ROWS, D>(p, r, c, lr, dc * 64 + v4 * 4, mm, sum, acc);
+                    if constexpr (!kKvShared<P>) kv_emit<ROWS, D>(p, r, c, lr, dc * 64 + v4 * 4, mm, sum, acc);
                 } else {
                     *reinterpret_cast<float4 *>(p.part + ((int64_t)slot * ROWS + lr) * D + dc * 64 + v4 * 4) = acc;
                     if (dc == 0 && v4 == 0) p.part_ml[(int64_t)slot * ROWS + lr] = make_float2(mm, sum);
@@ -1053,7 +1116,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
                     kv_join<ROWS, D, C::kCtas < 3 ? 8 : 4>(p, q, r, c, nrows, (int)threadIdx.x, 128);
             }
         }
-        kv_advance<ROWS, TILE>(p, w, r, c.jb - c.ja);
+        kv_advance<ROWS, TILE>(p, w, r, kv_piece_units<P>(w, r, c));
     }
     if (!ok && warp == 0 && lane == 0) {
         // a wait ran out: no copy may still be in flight when the CTA ends

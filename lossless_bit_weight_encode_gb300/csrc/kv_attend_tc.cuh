@@ -161,6 +161,16 @@ __device__ __forceinline__ uint64_t kv_seen64(const KvAttendParams &p, int32_t k
     return m;
 }
 
+// Row of the block that is in TMEM lane `lane` (kTcRows: none) of `rows`.  With shared prefixes
+// the rows of a block are spread over the four quarters of TMEM, so that few rows keep all
+// softmax warps busy.
+template <class P>
+__device__ __forceinline__ int tc_row(int lane, int rows) {
+    if (!kKvShared<P>) return lane;
+    const int per = (rows + 3) / 4, row = (lane >> 5) * per + (lane & 31);
+    return (lane & 31) < per && row < rows ? row : kTcRows;
+}
+
 // True in one lane of the warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
@@ -347,7 +357,7 @@ struct TcLoader {
 
     template <class P>
     __device__ __forceinline__ void open(const P &p) {
-        c = kv_piece(w, r);
+        c = kv_piece<P>(w, r);
         j = c.ja;
         pages.start(kv_table_row(p, w.b), (r.tile0 + c.ja) * kAttendTile / p.page_size, kv_entries(p, r));
     }
@@ -390,7 +400,7 @@ struct TcLoader {
         }
         ++it;
         if (++j == c.jb) {
-            kv_advance<kTcRows, kAttendTile>(p, w, r, c.jb - c.ja);
+            kv_advance<kTcRows, kAttendTile>(p, w, r, kv_piece_units<P>(w, r, c));
             if (w.u < w.end) open(p);
         }
         return true;
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
     const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
     KvWalk w;
     KvRequest r;
-    if (!kv_walk_init<kTcRows, kAttendTile>(p, w, r)) {  // the same for the whole CTA
+    if (!kv_walk_start<kTcRows, kAttendTile>(p, w, r, 0)) {  // the same for the whole CTA
         kv_end<P>();
         return;
     }
@@ -493,7 +503,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
         const float scale = fabsf(p.scale_log2);
         uint32_t it = 0, piece = 0;
         TcPlace &place = reinterpret_cast<TcPlace *>(smem + C::kOffPlaces)[warp];
-        if (lane == 0) place = TcPlace{w, r, kv_piece(w, r)};
+        if (lane == 0) place = TcPlace{w, r, kv_piece<P>(w, r)};
         __syncwarp();
         // Q rows of a piece to TMEM or shared memory, rows behind the last one zero; for a
         // Q8 cache in the column order of the converted keys
@@ -502,7 +512,8 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             if constexpr (C::kQTmem) {
                 // the lane's row; where a quarter has two warps, half of its columns each
                 const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
-                const int32_t rr = pc.rb * kTcRows + lr, tok = rr / p.group;
+                const int row = tc_row<P>(lr, (int)rows);
+                const int32_t rr = pc.rb * kTcRows + row, tok = rr / p.group;
                 const uint16_t *src = p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
                                       (int64_t)(pc.head * p.group + rr - tok * p.group) * D;
 #pragma unroll
@@ -512,7 +523,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                     uint4 u[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[i] = make_uint4(0, 0, 0, 0);
-                    if (lr < rows) {
+                    if (row < rows) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) u[i] = reinterpret_cast<const uint4 *>(src + 2 * col)[i];
                     }
@@ -536,7 +547,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             }
             // where each lane's row is (of 16 or 32); the steps then ask the lanes
             const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
-            const int mine = HALVES == 2 ? lr : base + lane % 16;
+            const int mine = tc_row<P>(HALVES == 2 ? lr : base + lane % 16, (int)rows);
             const int32_t rr = pc.rb * kTcRows + mine, tok = rr / p.group;
             const int64_t src = mine < rows ? (int64_t)(rq.q0 + tok) * p.q_stride +
                                                   (int64_t)(pc.head * p.group + rr - tok * p.group) * D
@@ -576,7 +587,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 const KvPiece &c = place.c;
                 nrows = (int32_t)min((int64_t)kTcRows, (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows);
                 row0 = c.rb * kTcRows;
-                i = (row0 + min(lr, nrows - 1)) / p.group;  // new token of TMEM lane lr's row
+                i = (row0 + min(tc_row<P>(lr, nrows), nrows - 1)) / p.group;  // new token of TMEM lane lr's row
                 kb = (r.tile0 + c.ja) * kAttendTile;
                 tiles = c.jb - c.ja;
                 keys = r.kv;
@@ -587,10 +598,10 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             }
             // the keys of the tile at kb that row `row` of the block sees
             const auto seen_by = [&](int row, uint32_t here) -> uint64_t {
-                const int32_t tok = (row0 + min(row, nrows - 1)) / p.group;
+                const int32_t tok = (row0 + min(tc_row<P>(row, nrows), nrows - 1)) / p.group;
                 return kv_seen64(p, keys, past, kv_row_view<PLACED>(p, place.r, tok), kb, here) >> (2 * t4);
             };
-            const bool busy = base < nrows;  // a warp without rows only keeps step
+            const bool busy = tc_row<P>(base, nrows) < nrows;  // a warp without rows only keeps step
             // rows g and g + 8 of each half, as tc_softmax has them
             float mr[HALVES][2], sr[HALVES][2];
 #pragma unroll
@@ -611,7 +622,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h) {
                         const int row = base + 16 * h;
-                        if (row >= nrows) break;  // the same for the warp
+                        if (tc_row<P>(row, nrows) >= nrows) break;  // the same for the warp
                         const uint32_t to = tl + ((uint32_t)(16 * (h + half)) << 16);
                         const uint32_t ts = to + C::kSCol + 64 * (it % C::kS);
                         tmem_ld16x64(ts, x[h]);
@@ -686,10 +697,10 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             {
                 KvWalk w2 = w1;
                 KvRequest r2 = r1;
-                kv_advance<kTcRows, kAttendTile>(p, w2, r2, tiles);
+                kv_advance<kTcRows, kAttendTile>(p, w2, r2, kKvShared<P> ? kv_piece_units<P>(w2, r2, c1) : tiles);
                 more = w2.u < w2.end;
                 if (more) {
-                    const KvPiece c2 = kv_piece(w2, r2);
+                    const KvPiece c2 = kv_piece<P>(w2, r2);
                     load_q(r2, c2);
                     if (lane == 0) place = TcPlace{w2, r2, c2};
                     __syncwarp();
@@ -726,8 +737,9 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             ++piece;
             const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (c1.ja > 0 ? 0 : 1);
-            if (32 * quarter < nrows) {
-                const int32_t head = c1.head * p.group + c1.rb * kTcRows + lr - i * p.group;
+            if (tc_row<P>(32 * quarter, nrows) < nrows) {
+                const int row = tc_row<P>(lr, nrows);  // of the block, in TMEM lane lr
+                const int32_t head = c1.head * p.group + c1.rb * kTcRows + row - i * p.group;
                 uint16_t *dst = p.out + (r1.q0 + i) * p.out_stride + (int64_t)head * D;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
@@ -735,7 +747,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                     uint32_t o[32];
                     tmem_ld32(tl + d0, o);
                     tmem_wait_ld();
-                    if (bad && lr < nrows) {
+                    if (bad && row < nrows) {
                         // values that are not finite count, as they are, for the
                         // rows that see their keys (a weight is positive; what went
                         // through the product already stays what it is)
@@ -757,14 +769,13 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                             }
                         }
                     }
-                    if (lr < nrows) {
+                    if (row < nrows) {
                         float y[32];  // Q8: columns (0, 2, 1, 3) of every four
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             y[k] = __uint_as_float(o[!Q8 || k % 4 == 0 || k % 4 == 3 ? k : k % 4 == 1 ? k + 1 : k - 1]);
                         if constexpr (kKvShared<P>) {
-                            const int64_t row = (int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head;
-                            float *to = whole ? p.row_part + row * D : p.part + (slot * kTcRows + lr) * D;
+                            float *to = whole ? p.row_part + kv_row_at<kTcRows>(p, w1, r1, c1, row) * D : p.part + (slot * kTcRows + row) * D;
 #pragma unroll
                             for (int k = 0; k < 32; k += 4)
                                 *reinterpret_cast<float4 *>(to + d0 + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
@@ -778,17 +789,17 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                         } else {
 #pragma unroll
                             for (int k = 0; k < 32; k += 4)
-                                *reinterpret_cast<float4 *>(p.part + (slot * kTcRows + lr) * D + d0 + k) =
+                                *reinterpret_cast<float4 *>(p.part + (slot * kTcRows + row) * D + d0 + k) =
                                     make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
                         }
                     }
                 }
-                if (half == 0 && lr < nrows) {
+                if (half == 0 && row < nrows) {
                     if constexpr (kKvShared<P>) {
-                        if (c1.ja == 0) kv_note<kTcRows>(p, w1, r1, c1, lr, whole);
-                        if (whole) p.row_ml[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] = make_float2(m, l);
+                        if (c1.ja == 0) kv_note<kTcRows>(p, w1, r1, c1, row, whole);
+                        if (whole) p.row_ml[kv_row_at<kTcRows>(p, w1, r1, c1, row)] = make_float2(m, l);
                     }
-                    if (!whole) p.part_ml[slot * kTcRows + lr] = make_float2(m, l);
+                    if (!whole) p.part_ml[slot * kTcRows + row] = make_float2(m, l);
                     else if (!kKvShared<P> && p.lse)
                         p.lse[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] =
                             l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -865,7 +876,16 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 return true;
             };
             while (ok) {
-                int n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
+                int n = 0, units = 0;  // tiles, and the units that they are
+                if constexpr (kKvShared<P>) {
+                    if (w.u < w.end) {
+                        const KvPiece c = kv_piece<P>(w, r);
+                        n = c.jb - c.ja;
+                        units = kv_piece_units<P>(w, r, c);
+                    }
+                } else {
+                    n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
+                }
                 n = __shfl_sync(~0u, n, 0);
                 if (n == 0) break;
                 ok = __all_sync(~0u, tc_wait(qfull, piece, deadline));
@@ -893,7 +913,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                     ++done;
                 }
                 ++piece;
-                if (ok) kv_advance<kTcRows, kAttendTile>(p, w, r, n);
+                if (ok) kv_advance<kTcRows, kAttendTile>(p, w, r, kKvShared<P> ? units : n);
             }
             if (leader) {
                 if (!ok) atomicOr(p.status, 8u);
@@ -914,7 +934,17 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
             const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
             const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
-            const uint32_t total = (uint32_t)(w.end - w.u);
+            uint32_t total = (uint32_t)(w.end - w.u);  // tiles of the CTA
+            if constexpr (kKvShared<P>) {
+                KvWalk w2 = w;
+                KvRequest r2 = r;
+                total = 0;
+                while (w2.u < w2.end) {
+                    const KvPiece c = kv_piece<P>(w2, r2);
+                    total += (uint32_t)(c.jb - c.ja);
+                    kv_advance<kTcRows, kAttendTile>(p, w2, r2, kv_piece_units<P>(w2, r2, c));
+                }
+            }
             // K or V of tile x to its operand buffer, which the tile before it there must have left
             auto convert = [&](bool values, uint32_t x) -> bool {
                 const uint32_t stage = x % N;

@@ -87,21 +87,32 @@ struct KvAttendParams {
     uint64_t timeout_ns;
 };
 
-// A call with shared prefixes (w12_kv_attend_shared): one launch over the groups' prefixes
-// and one over what the requests have of their own, each a line of units of its own.  No
-// row is finished there: what a CTA has whole goes to row_part and row_ml, and row_info says
-// where a row's parts are: {row of its first part, parts (1: whole; bit 30, of the own
-// line: its request shares a prefix)}.
+// A call with shared prefixes (w12_kv_attend_shared): its spans are the groups' prefixes and
+// then what the requests have of their own.  Where one kernel suits both they are one line of
+// units and one launch, else two.  No row is finished there: what a CTA has whole goes to
+// row_part and row_ml, and row_info says where a row's parts are: {row of its first part,
+// parts (1: whole; bit 30, of the own tokens: their request shares a prefix)}.  All three
+// have the prefixes' rows first, then the own ones'.
 struct KvSharedParams : KvAttendParams {
     const int32_t *prefix_cu, *prefix_lens;
     int32_t groups;
-    float *row_part;   // [tokens * heads][head_dim]
-    float2 *row_ml;    // [tokens * heads]
-    int2 *row_info;    // [tokens * heads]
+    float *row_part;  // [2][tokens * heads][head_dim]
+    float2 *row_ml;   // [2][tokens * heads]
+    int2 *row_info;   // [2][tokens * heads]
 };
-struct KvPrefixParams : KvSharedParams {};
-struct KvOwnParams : KvSharedParams {};
+// What a launch has of the spans: all, the prefixes, or the own tokens (then it is the second).
+enum KvSpans { kKvAllSpans, kKvPrefixes, kKvOwnSpans };
+template <KvSpans KIND>
+struct KvSpanParams : KvSharedParams {
+    static constexpr KvSpans kind = KIND;
+    // the first of the launch's spans among all
+    __device__ __forceinline__ int32_t first_span() const { return KIND == kKvOwnSpans ? groups : 0; }
+};
 constexpr int32_t kKvSharesPrefix = 1 << 30;
+// What a row block costs beside its tiles (its q, the pipeline's start and end), in tiles:
+// the line counts that many units more for each, so that CTAs with many short blocks have
+// fewer of them.
+constexpr int32_t kKvBlockUnits = 3;
 
 // Two fp32 to packed BF16, round to nearest even, `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -28,6 +28,7 @@ struct Abi {
     decltype(&w12_kv_read) read;
     decltype(&w12_kv_attend_workspace_size) workspace_size;
     decltype(&w12_kv_attend) attend;
+    decltype(&w12_kv_fork_workspace_size) fork_size;
     decltype(&w12_kv_fork) fork;
     decltype(&w12_kv_copy) copy;
     decltype(&w12_kv_attend_shared_workspace_size) shared_size;
@@ -415,10 +416,10 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// fork(pages, index, parents, lens, copies, prefix, lens_out, stream)
+// fork(pages, index, parents, lens, copies, prefix, lens_out, workspace, grow, stream)
 PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 8);
+    expect(n, 10);
     const int64_t index = integer(a[1]);
     const Ref tables_o = field(a[0], names.tables), owned_o = field(a[0], names.owned), ring_o = field(a[0], names.ring),
               state_o = field(a[0], names.ring_state), page_o = field(a[0], names.page_size),
@@ -469,8 +470,16 @@ PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
         s.lens_out = ints<int32_t>(t, "lens_out", index);
         TORCH_CHECK_VALUE(t.numel() == requests, "lens_out must have an entry per request");
     }
-    void *stream = pointer<void>(a[7]);
-    call([&] { return abi.fork(&s, stream); });
+    size_t bytes = 0;
+    check(abi.fork_size(&s, &bytes));
+    Ref grown(a[7] == Py_None || tensor(a[7], "workspace").nbytes() < bytes
+                  ? PyObject_CallFunction(a[8], "LOn", static_cast<long long>(index), a[9],
+                                          static_cast<Py_ssize_t>(bytes))
+                  : Py_NewRef(a[7]));
+    const at::Tensor &ws = tensor(grown.get(), "workspace");
+    void *p = ws.data_ptr(), *stream = pointer<void>(a[9]);
+    const size_t have = ws.nbytes();
+    call([&] { return abi.fork(&s, p, have, stream); });
     return Py_NewRef(a[4]);
     END_HANDLE_TH_ERRORS
 }
@@ -563,25 +572,26 @@ PyObject *select(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(plan, store, read, workspace_size, attend, fork, copy, shared_size, attend_shared,
+// bind(plan, store, read, workspace_size, attend, fork_size, fork, copy, shared_size, attend_shared,
 // beam_size, beam_select, raise): the C ABI's addresses
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 12);
+    expect(n, 13);
     const auto set = [](auto &f, PyObject *o) { f = reinterpret_cast<std::decay_t<decltype(f)>>(pointer<void>(o)); };
     set(abi.plan, a[0]);
     set(abi.store, a[1]);
     set(abi.read, a[2]);
     set(abi.workspace_size, a[3]);
     set(abi.attend, a[4]);
-    set(abi.fork, a[5]);
-    set(abi.copy, a[6]);
-    set(abi.shared_size, a[7]);
-    set(abi.attend_shared, a[8]);
-    set(abi.beam_size, a[9]);
-    set(abi.beam_select, a[10]);
+    set(abi.fork_size, a[5]);
+    set(abi.fork, a[6]);
+    set(abi.copy, a[7]);
+    set(abi.shared_size, a[8]);
+    set(abi.attend_shared, a[9]);
+    set(abi.beam_size, a[10]);
+    set(abi.beam_select, a[11]);
     Py_XDECREF(abi.raise);
-    abi.raise = Py_NewRef(a[11]);
+    abi.raise = Py_NewRef(a[12]);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }

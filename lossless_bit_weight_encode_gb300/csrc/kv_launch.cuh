@@ -203,13 +203,19 @@ int attend_rows_variant(const DeviceView &d, int rows, int *resident, const P *p
     }
 }
 
-// One line of a call with shared prefixes (kv_shared_*.cu), as attend_dim.
+// The same for calls with shared prefixes (kv_shared_*.cu), over one kind of spans: BF16
+// caches take all in one launch.
 template <int D>
-int shared_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvPrefixParams *p,
+int shared_dim(const DeviceView &d, bool q8, int rows, dev::KvSpans kind, int *resident, const dev::KvSharedParams *p,
                const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
-template <int D>
-int shared_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvOwnParams *p,
-               const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
+
+template <int D, bool Q8, dev::KvSpans KIND>
+int shared_kind(const DeviceView &d, int rows, int *resident, const dev::KvSharedParams *p, const CUtensorMap *tm_k,
+                const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+    dev::KvSpanParams<KIND> spans;
+    if (p) static_cast<dev::KvSharedParams &>(spans) = *p;
+    return attend_rows_variant<D, Q8>(d, rows, resident, p ? &spans : nullptr, tm_k, tm_v, ctas, stream, err);
+}
 
 }  // namespace launch
 }  // namespace w12

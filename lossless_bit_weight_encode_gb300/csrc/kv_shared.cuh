@@ -1,12 +1,11 @@
-// The last step of attention behind shared prefixes (w12_kv_attend_shared in
+// The joining kernel of attention behind shared prefixes (w12_kv_attend_shared in
 // include/w12.h).
 //
 // Mathematics.  Softmax sums over disjoint sets of keys join as in kv_attend.cuh, whatever
-// rows were computed together: the kernels of kv_attend.cuh and kv_attend_tc.cuh run once
-// over the groups' prefixes, where the rows of all of a group's requests meet the prefix's
-// keys at once (32 beams of six query heads: 192 rows, on the tensor cores), and once over
-// what each request has of its own, and leave the sums of every row's parts; this
-// kernel joins them.
+// rows were computed together: the kernels of kv_attend.cuh and kv_attend_tc.cuh run over the
+// groups' prefixes, where the rows of all of a group's requests meet the prefix's keys at
+// once (32 beams of six query heads: 192 rows, on the tensor cores), and over what each
+// request has of its own, and leave the sums of every row's parts; this kernel joins them.
 //
 // What bounds the call: a prefix's bytes are read once per group instead of once per
 // request, so with many requests the prefix is bound by the products and the softmax of its
@@ -18,39 +17,39 @@
 namespace w12 {
 namespace dev {
 
-// Joins the parts of the output rows (token and head, heads fastest): a warp per row, first
-// the prefix's parts in range order, then the own ones.
 struct KvSharedJoin {
     uint16_t *out;
     float *lse;
     int64_t out_stride;
     const int32_t *cu_new;
     int32_t tokens, heads, requests;
+    const float *row_part;
+    const float2 *row_ml;
+    const int2 *row_info;
     struct Line {
-        const float *part, *row_part;
-        const float2 *part_ml, *row_ml;
-        const int2 *info;
+        const float *part;
+        const float2 *part_ml;
         int32_t rows;  // of a row block
-    } line[2];  // the prefixes, the own tokens
+    } line[2];  // of the prefixes, of the own tokens
 };
 
+// A warp per output row (token and head, heads fastest) takes its parts, first the prefix's in
+// range order, then the own ones.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const __grid_constant__ KvSharedJoin p) {
     constexpr int W = kJoinThreads / 32, V = D / 32;  // columns of a lane
     constexpr int U = V == 8 ? 4 : 8;                 // parts whose loads are in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * W + warp;
+    const int64_t row = (int64_t)blockIdx.x * W + warp, own_rows = (int64_t)p.tokens * p.heads;
     const int32_t tok = (int32_t)(row / p.heads), h = (int32_t)(row - (int64_t)tok * p.heads);
     pdl_launch_dependents();
     pdl_wait();
     // rows of no request have no note
     if (tok >= min(p.tokens, p.cu_new[p.requests]) || tok < p.cu_new[0]) return;
-    int2 info[2];
-    info[0] = __ldcg(&p.line[0].info[row]);
-    info[1] = __ldcg(&p.line[1].info[row]);
-    if (!(info[1].y & kKvSharesPrefix)) info[0].y = 0;
-    info[1].y &= ~kKvSharesPrefix;
-    const int32_t n0 = info[0].y, n = n0 + info[1].y;
+    int2 prefix = __ldcg(&p.row_info[row]), own = __ldcg(&p.row_info[own_rows + row]);
+    if (!(own.y & kKvSharesPrefix)) prefix.y = 0;
+    own.y &= ~kKvSharesPrefix;
+    const int32_t n0 = prefix.y, n = n0 + own.y;
     float acc[V] = {}, mm = -INFINITY, sum = 0.0f;
     for (int32_t k0 = 0; k0 < n; k0 += U) {
         float y[U][V];
@@ -58,14 +57,15 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int32_t kk = min(k0 + u, n - 1);
-            const bool own = kk >= n0;
-            const KvSharedJoin::Line &l = p.line[own];
-            const int32_t k = own ? kk - n0 : kk;
-            const bool whole = (own ? info[1].y : info[0].y) == 1;
+            const bool mine = kk >= n0;
+            const int32_t k = mine ? kk - n0 : kk;
+            const int2 info = mine ? own : prefix;
+            const KvSharedJoin::Line &l = p.line[mine];
+            const bool whole = info.y == 1;
             // the first CTA's part is in its second slot, every other one's in its first
-            const int64_t at = whole ? row : (own ? info[1].x : info[0].x) + (int64_t)(2 * k + (k == 0)) * l.rows;
-            s[u] = __ldcg((whole ? l.row_ml : l.part_ml) + at);
-            const float *src = (whole ? l.row_part : l.part) + at * D;
+            const int64_t at = whole ? row + (mine ? own_rows : 0) : info.x + (int64_t)(2 * k + (k == 0)) * l.rows;
+            s[u] = __ldcg((whole ? p.row_ml : l.part_ml) + at);
+            const float *src = (whole ? p.row_part : l.part) + at * D;
             if constexpr (V == 2) {
                 const float2 a = __ldcg(reinterpret_cast<const float2 *>(src) + lane);
                 y[u][0] = a.x, y[u][1] = a.y;

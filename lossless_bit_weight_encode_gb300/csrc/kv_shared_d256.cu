@@ -5,17 +5,14 @@ namespace w12 {
 namespace launch {
 
 template <>
-int shared_dim<256>(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvPrefixParams *p, const CUtensorMap *tm_k,
-                    const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
-    return q8 ? attend_rows_variant<256, true>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err)
-              : attend_rows_variant<256, false>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err);
-}
-
-template <>
-int shared_dim<256>(const DeviceView &d, bool q8, int rows, int *resident, const dev::KvOwnParams *p, const CUtensorMap *tm_k,
-                    const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
-    return q8 ? attend_rows_variant<256, true>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err)
-              : attend_rows_variant<256, false>(d, rows, resident, p, tm_k, tm_v, ctas, stream, err);
+int shared_dim<256>(const DeviceView &d, bool q8, int rows, dev::KvSpans kind, int *resident,
+                    const dev::KvSharedParams *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream,
+                    std::string *err) {
+    const auto run = !q8                         ? &shared_kind<256, false, dev::kKvAllSpans>
+                     : kind == dev::kKvAllSpans ? &shared_kind<256, true, dev::kKvAllSpans>
+                     : kind == dev::kKvPrefixes ? &shared_kind<256, true, dev::kKvPrefixes>
+                                                : &shared_kind<256, true, dev::kKvOwnSpans>;
+    return run(d, rows, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
 }  // namespace launch

@@ -94,7 +94,8 @@ int kv_attend_workspace_size(const w12_kv_cache &c, const w12_kv_attend_args &a,
 int kv_attend(const w12_kv_cache &c, const w12_kv_attend_args &a, void *workspace, size_t ws_bytes, void *stream,
               std::string *err);
 
-int kv_fork(const w12_kv_fork_args &a, void *stream, std::string *err);
+int kv_fork_workspace_size(const w12_kv_fork_args &a, size_t *bytes);
+int kv_fork(const w12_kv_fork_args &a, void *workspace, size_t ws_bytes, void *stream, std::string *err);
 int kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, const int32_t *dst, const int32_t *rows,
             int32_t pairs, void *stream, std::string *err);
 int kv_attend_shared_workspace_size(const w12_kv_cache &c, const w12_kv_attend_args &a, const w12_kv_prefix &prefix,

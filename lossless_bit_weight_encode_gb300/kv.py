@@ -71,7 +71,7 @@ def _load_host():
     lib = w12.lib()
     host.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.w12_kv_plan, lib.w12_kv_store, lib.w12_kv_read, lib.w12_kv_attend_workspace_size, lib.w12_kv_attend,
-        lib.w12_kv_fork, lib.w12_kv_copy, lib.w12_kv_attend_shared_workspace_size, lib.w12_kv_attend_shared,
+        lib.w12_kv_fork_workspace_size, lib.w12_kv_fork, lib.w12_kv_copy, lib.w12_kv_attend_shared_workspace_size, lib.w12_kv_attend_shared,
         lib.w12_beam_workspace_size, lib.w12_beam_select)), w12._check)
     return host
 
@@ -233,7 +233,7 @@ class KVPages:
             _ints(shares, _I32, "shares", self._index)
             _need(ring.numel() >= shares.numel() >= 1, "ring must have as many entries as shares or more")
         self.tables, self.owned, self.ring, self.ring_state = tables, owned, ring, ring_state
-        self.page_size, self.shares = int(page_size), shares
+        self.page_size, self.shares, self._ws = int(page_size), shares, None
 
     @classmethod
     def create(cls, num_pages, page_size, requests, max_blocks, device=None, shared=False):
@@ -288,7 +288,14 @@ class KVPages:
                 return self.fork(parents, lens, copies, prefix, lens_out)
         if copies is None:
             copies = KVCopies.empty(self.tables.shape[0], self.tables.device)
-        return _host.fork(self, self._index, parents, lens, copies, prefix, lens_out, _current_stream(self._index))
+        return _host.fork(self, self._index, parents, lens, copies, prefix, lens_out, self._ws, self._grow,
+                          _current_stream(self._index))
+
+    def _grow(self, index, st, size):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("make one ordinary fork() of these pages before capturing one")
+        self._ws = torch.zeros(size, dtype=torch.uint8, device=self.tables.device)
+        return self._ws
 
 
 class KVCache:

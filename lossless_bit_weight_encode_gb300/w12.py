@@ -29,7 +29,7 @@ EXPORTED = (
     "w12_q8_encoded_size", "w12_q8_encode_host", "w12_q8_blob_info", "w12_q8_gemm_workspace_size", "w12_q8_gemm",
     "w12_q8_gemm_group_workspace_size", "w12_q8_gemm_group_launch_info", "w12_q8_gemm_group",
     "w12_kv_plan", "w12_kv_store", "w12_kv_read", "w12_kv_attend_workspace_size", "w12_kv_attend",
-    "w12_kv_fork", "w12_kv_copy", "w12_kv_attend_shared_workspace_size", "w12_kv_attend_shared",
+    "w12_kv_fork_workspace_size", "w12_kv_fork", "w12_kv_copy", "w12_kv_attend_shared_workspace_size", "w12_kv_attend_shared",
     "w12_beam_workspace_size", "w12_beam_select",
     "w12_read_stream", "w12_check_status", "w12_selftest_timeout", "w12_set_option", "w12_get_option",
 )
@@ -199,7 +199,8 @@ def lib() -> ctypes.CDLL:
     L.w12_kv_attend_workspace_size.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), ctypes.POINTER(sz)]
     L.w12_kv_attend.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), vp, sz, vp]
     prefix_p, beam_p = ctypes.POINTER(w12_kv_prefix), ctypes.POINTER(w12_beam_args)
-    L.w12_kv_fork.argtypes = [ctypes.POINTER(w12_kv_fork_args), vp]
+    L.w12_kv_fork_workspace_size.argtypes = [ctypes.POINTER(w12_kv_fork_args), ctypes.POINTER(sz)]
+    L.w12_kv_fork.argtypes = [ctypes.POINTER(w12_kv_fork_args), vp, sz, vp]
     L.w12_kv_copy.argtypes = [cache_p, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp]
     L.w12_kv_attend_shared_workspace_size.argtypes = [cache_p, ctypes.POINTER(w12_kv_attend_args), prefix_p,
                                                       ctypes.POINTER(sz)]
@@ -503,8 +504,14 @@ def w12_kv_attend(cache: w12_kv_cache, args: w12_kv_attend_args, workspace_ptr: 
     _check(lib().w12_kv_attend(cache, args, workspace_ptr, workspace_bytes, _stream_handle(stream)))
 
 
-def w12_kv_fork(args: w12_kv_fork_args, stream=None) -> None:
-    _check(lib().w12_kv_fork(args, _stream_handle(stream)))
+def w12_kv_fork_workspace_size(args: w12_kv_fork_args) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().w12_kv_fork_workspace_size(args, ctypes.byref(out)))
+    return out.value
+
+
+def w12_kv_fork(args: w12_kv_fork_args, workspace_ptr: int, workspace_bytes: int, stream=None) -> None:
+    _check(lib().w12_kv_fork(args, workspace_ptr, workspace_bytes, _stream_handle(stream)))
 
 
 def w12_kv_copy(caches, src_ptr: int, dst_ptr: int, rows_ptr: int | None, pairs: int, stream=None) -> None:

@@ -43,12 +43,18 @@ def beam(**kw):
     [({n: None}, INVALID) for n in ("parents", "lens", "owned", "tables", "ring", "ring_state", "shares", "src", "dst",
                                     "rows")])
 def test_fork_refused(kw, status):
-    assert w12.lib().w12_kv_fork(fork(**kw), None) == status
+    assert w12.lib().w12_kv_fork(fork(**kw), A, 1 << 30, None) == status
     assert w12.w12_last_error() != ""
 
 
 def test_fork_null():
-    assert w12.lib().w12_kv_fork(None, None) == INVALID
+    L, size = w12.lib(), ctypes.c_size_t()
+    assert L.w12_kv_fork(None, A, 1 << 30, None) == INVALID
+    assert L.w12_kv_fork(fork(), None, 1 << 30, None) == INVALID
+    assert L.w12_kv_fork(fork(), A + 64, 1 << 30, None) == ALIGN
+    assert L.w12_kv_fork_workspace_size(fork(), None) == INVALID
+    assert L.w12_kv_fork_workspace_size(None, ctypes.byref(size)) == INVALID
+    assert L.w12_kv_fork_workspace_size(fork(requests=4097), ctypes.byref(size)) == SHAPE
 
 
 @pytest.mark.parametrize("kw,status", BAD_CACHES)
