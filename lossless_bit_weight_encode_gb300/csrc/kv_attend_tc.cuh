@@ -49,7 +49,7 @@ struct TcPlace {
     KvPiece c;
 };
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool SHARED = false>
 struct AttendTcCfg {
     // Q is the scores' A operand: from TMEM, written there once per piece, where there
     // are columns for it beside O and the scores; else from shared memory, where every
@@ -62,7 +62,8 @@ struct AttendTcCfg {
     static constexpr bool kOne = D == 256 || (D == 128 && kQTmem);
     // Score buffers, and how many tiles the scores are made ahead of the products.
     static constexpr int kS = D == 128 && kQTmem ? 4 : 2, kAheadS = kS / 2;
-    // Softmax warps, then two loaders, the MMA warp (and one that idles), the converters
+    // Softmax warps, then two loaders, the MMA warp (and one that idles, or with shared
+    // prefixes finds the places), the converters
     // in groups of four.  Where one CTA has the SM, eight softmax warps (16 rows each)
     // shorten the way from scores to weights; where two share it, four (32 rows each, 16
     // at a time) fill it as well and leave the registers.  72 rows of 256 columns, two
@@ -72,7 +73,7 @@ struct AttendTcCfg {
     // buffer; 128: 376 against 365 with one, at 64000 tokens).
     static constexpr int kSoft = kOne ? 8 : 4;
     static constexpr int kGroups = !Q8 ? 0 : kOne ? 2 : 1;
-    static constexpr int kThreads = 32 * (kSoft + (Q8 ? 4 + 4 * kGroups : kOne ? 4 : 3));
+    static constexpr int kThreads = 32 * (kSoft + (Q8 ? 4 + 4 * kGroups : kOne || SHARED ? 4 : 3));
     // Registers per thread at launch, then of the softmax warps and of the others: the
     // softmax warps take what the others give up (0: no exchange).
     static constexpr int kRegs = !Q8 ? 0 : kOne ? 96 : 80;
@@ -98,7 +99,8 @@ struct AttendTcCfg {
     static constexpr int kInfoBytes = 528;  // 64 key scales, 64 value scales, the largest key scale
     static constexpr int kOffScale = kOffRawScale + kRaws * 512;  // [kTcInfo][kInfoBytes] (Q8)
     static constexpr int kOffBars = kOffScale + (Q8 ? kTcInfo * kInfoBytes : 0);
-    static constexpr int kBars = 4 * kOps + 4 * kRaws + 3 * kS + 3;
+    static constexpr int kPlaces = SHARED ? 4 : 0;  // ring of pieces that the place warp fills
+    static constexpr int kBars = 4 * kOps + 4 * kRaws + 3 * kS + 3 + 2 * kPlaces + SHARED;
     static constexpr int kOffInfo = kOffBars + 8 * kBars;
     static constexpr int kOffStats = kOffInfo + 4 * kTcInfo + 32;  // (max, sum) of the 128 rows
     static constexpr int kOffPlaces = kOffStats + 8 * kTcRows;
@@ -234,6 +236,23 @@ __device__ __forceinline__ void tmem_st16x32p(uint32_t taddr, const uint32_t (&v
                  : "memory");
 }
 
+// A row's four lanes t (as above) between 16 consecutive columns of 32 bits as four each, lane t
+// the ones at 8 (t & 1) + 4 (t >> 1), and as the two words each of two blocks of eight that
+// TMEM's form has (x[0], x[1], x[4], x[5]): neighbours exchange two words.  Four lanes then
+// reach 64 bytes of a row in global memory at once; with a row per lane every 16 bytes
+// were a line of their own (128 rows of 128 floats: 2 us more).
+__device__ __forceinline__ void tc_to_words(int t, const uint4 &v, uint32_t *x) {
+    const bool odd = t & 1;
+    const uint32_t a = __shfl_xor_sync(~0u, odd ? v.x : v.z, 1), b = __shfl_xor_sync(~0u, odd ? v.y : v.w, 1);
+    x[0] = odd ? a : v.x, x[1] = odd ? b : v.y;
+    x[4] = odd ? v.z : a, x[5] = odd ? v.w : b;
+}
+__device__ __forceinline__ uint4 tc_from_words(int t, const uint32_t *x) {
+    const bool odd = t & 1;
+    const uint32_t a = __shfl_xor_sync(~0u, odd ? x[0] : x[4], 1), b = __shfl_xor_sync(~0u, odd ? x[1] : x[5], 1);
+    return odd ? make_uint4(a, b, x[4], x[5]) : make_uint4(x[0], x[1], a, b);
+}
+
 // The softmax of 16 rows' 64 scores x, which become BF16 weights at ts, over them.
 // A thread has 16 keys of two rows (see tmem_ld16x64), so it needs the scales of 16
 // keys and not of 64: with a row per thread their broadcast reads from shared memory
@@ -335,6 +354,27 @@ __device__ __forceinline__ void tc_softmax(uint32_t ts, const uint32_t (&x)[32],
     tmem_st16x32p(ts, pk);
 }
 
+// What the values that are not finite give to column d of a row's sums: they count, as they
+// are, for the rows that see their keys.
+template <class P>
+__device__ __noinline__ float tc_not_finite(const P &p, const KvWalk &w, const KvRequest &r, const KvPiece &c, int row,
+                                            int d) {
+    const KvRowView view = kv_row_view<false>(p, r, (c.rb * kTcRows + row) / p.group);
+    float sum = 0.0f;
+    for (int j = c.ja; j < c.jb; ++j) {
+        const int32_t kb = (r.tile0 + j) * kAttendTile;
+        for (uint64_t seen = kv_seen64(p, r.kv, r.past, view, kb, 15u); seen; seen &= seen - 1) {
+            const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
+            const int32_t page = kv_table_row(p, w.b)[e];
+            if (page < 0 || page >= p.num_pages) continue;
+            const uint32_t v = p.v[page * p.v_page_stride + c.head * p.v_head_stride +
+                                   (int64_t)(key - e * p.page_size) * p.v_row_stride + d];
+            if ((v & 0x7F80u) == 0x7F80u) sum += __uint_as_float(v << 16);
+        }
+    }
+    return sum;
+}
+
 // Fills a ring with the keys or the values of the CTA's tiles, one tile per step().
 // Keys and values have a loader (and a warp) each: a ring's next tile is then asked
 // for as soon as its own slot is free, up to a ring (kOps or kRaws tiles) ahead of its use.
@@ -416,10 +456,11 @@ struct TcLoader {
 // time the tile loop's registers went another way (trees over an 8-bit cache 116 us, 144
 // with the positions looked up in the loop, 118 with nothing but their load there).
 template <int D, bool Q8, bool PLACED, class P = KvAttendParams>
-__global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q8>::kOne ? 1 : 2)
+__global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
+                                  AttendTcCfg<D, Q8, kKvShared<P>>::kOne ? 1 : 2)
     w12_kv_attend_tc_kernel(const P p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
-    using C = AttendTcCfg<D, Q8>;
+    using C = AttendTcCfg<D, Q8, kKvShared<P>>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + C::kOffBars), *kempty = kfull + C::kOps;
@@ -428,11 +469,15 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
     uint64_t *rvfull = rkempty + C::kRaws, *rvempty = rvfull + C::kRaws;
     uint64_t *sfull = rvempty + C::kRaws, *pfull = sfull + C::kS;
     uint64_t *pvdone = pfull + C::kS, *qfull = pvdone + C::kS, *ofree = qfull + 1, *drain = ofree + 1;
+    // with shared prefixes: the pieces' places, and the notes of values that are not finite
+    uint64_t *placed = drain + 1, *pfree = placed + C::kPlaces, *noted = pfree + C::kPlaces;
+    TcPlace *places = reinterpret_cast<TcPlace *>(smem + C::kOffPlaces);
     uint32_t *present = reinterpret_cast<uint32_t *>(smem + C::kOffInfo);
     volatile uint32_t *poison = present + kTcInfo;
     uint32_t *tmem_slot = present + kTcInfo + 3;
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
-    constexpr int kLoadK = C::kSoft, kMma = kLoadK + 1, kLoadV = kLoadK + 2, kConvert = kLoadK + 4;  // warps
+    constexpr int kLoadK = C::kSoft, kMma = kLoadK + 1, kLoadV = kLoadK + 2, kPlace = kLoadK + 3;  // warps
+    constexpr int kConvert = kLoadK + 4;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kOps; ++i) {
@@ -455,6 +500,11 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
         mbar_init(qfull, C::kSoft);
         mbar_init(ofree, C::kSoft);
         mbar_init(drain, 1);
+        for (int i = 0; i < C::kPlaces; ++i) {
+            mbar_init(&placed[i], 1);
+            mbar_init(&pfree[i], C::kSoft);
+        }
+        if (C::kPlaces > 0) mbar_init(noted, C::kSoft);
         fence_mbar_init();
         poison[0] = poison[1] = poison[2] = 0;
     }
@@ -466,7 +516,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
     const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
     KvWalk w;
     KvRequest r;
-    if (!kv_walk_start<kTcRows, kAttendTile>(p, w, r, 0)) {  // the same for the whole CTA
+    if (!kv_walk_start<C::kThreads / 32, kTcRows, kAttendTile>(p, w, r)) {  // the same for the whole CTA
         kv_end<P>();
         return;
     }
@@ -483,6 +533,14 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
     pdl_launch_dependents();
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
+    // The place of piece n (shared prefixes), for all but the loaders, which run ahead; none and no
+    // tiles when the CTA has no such piece.
+    const auto place_of = [&](uint32_t n) -> const TcPlace & { return places[n % (C::kPlaces > 0 ? C::kPlaces : 1)]; };
+    const auto piece_tiles = [&](uint32_t n) -> int {
+        constexpr uint32_t N = C::kPlaces > 0 ? C::kPlaces : 1;
+        ok = __all_sync(~0u, ok && tc_wait(&placed[n % N], n / N, deadline));
+        return ok ? __shfl_sync(~0u, places[n % N].c.jb - places[n % N].c.ja, 0) : 0;
+    };
 
     if (warp < C::kSoft) {
         if constexpr (C::kRegs > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
@@ -501,14 +559,62 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
         // of a BF16 cache the softmax scale's sign is in Q, so that the largest product
         // is the largest score
         const float scale = fabsf(p.scale_log2);
-        uint32_t it = 0, piece = 0;
-        TcPlace &place = reinterpret_cast<TcPlace *>(smem + C::kOffPlaces)[warp];
-        if (lane == 0) place = TcPlace{w, r, kv_piece<P>(w, r)};
+        uint32_t it = 0, piece = 0, notes = 0;
+        TcPlace &mine = places[warp];  // (without shared prefixes)
+        if (!kKvShared<P> && lane == 0) mine = TcPlace{w, r, kv_piece<P>(w, r)};
         __syncwarp();
         // Q rows of a piece to TMEM or shared memory, rows behind the last one zero; for a
         // Q8 cache in the column order of the converted keys
         auto load_q = [&](const KvRequest &rq, const KvPiece &pc) {
             constexpr int CH = D / 8, STEPS = HALVES * CH / 2, G = STEPS < 8 ? STEPS : 8;  // 16-byte chunks; 32 a step
+            if constexpr (C::kQTmem && kKvShared<P> && D == 256) {
+                // 16 rows at a time, four lanes on 64 bytes of each
+                const int rows = (int)min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    const uint16_t *src[2];
+                    bool there[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = tc_row<P>(base + 16 * h + 8 * e + g8, rows);
+                        const int32_t rr = pc.rb * kTcRows + row, tok = rr / p.group;
+                        there[e] = row < rows;
+                        src[e] = p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
+                                 (int64_t)(pc.head * p.group + rr - tok * p.group) * D + (t4 & 1) * 16 + (t4 >> 1) * 8;
+                    }
+                    constexpr int N = D >= 128 ? 2 : 1;  // 64 columns (as 32 words) a step
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 64 * N) {
+                        uint4 u[N][2][2];
+#pragma unroll
+                        for (int k = 0; k < 4 * N; ++k) {
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (there[k & 1]) v = *reinterpret_cast<const uint4 *>(src[k & 1] + c0 + 32 * (k >> 1));
+                            u[k >> 2][(k >> 1) & 1][k & 1] = v;
+                        }
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            uint32_t x[16];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint4 v = u[n][k >> 1][k & 1];
+                                if (!Q8 && p.scale_log2 < 0.0f)  // the softmax scale's sign
+                                    v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+                                if (Q8)
+                                    v = make_uint4(prmt(v.x, v.y, 0x5410u), prmt(v.x, v.y, 0x7632u),
+                                                   prmt(v.z, v.w, 0x5410u), prmt(v.z, v.w, 0x7632u));
+                                tc_to_words(t4, v, x + 8 * (k >> 1) + 2 * (k & 1));
+                            }
+                            tmem_st16x32(tl + ((uint32_t)(16 * (h + half)) << 16) + C::kQCol + c0 / 2 + 32 * n, x);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfull);
+                return;
+            }
             if constexpr (C::kQTmem) {
                 // the lane's row; where a quarter has two warps, half of its columns each
                 const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
@@ -579,8 +685,14 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
         };
-        load_q(place.r, place.c);
-        while (true) {
+        if constexpr (kKvShared<P>) {
+            if (piece_tiles(0) > 0) load_q(place_of(0).r, place_of(0).c);
+        } else {
+            load_q(mine.r, mine.c);
+        }
+        while (ok || !kKvShared<P>) {
+            const TcPlace &place = kKvShared<P> ? place_of(piece) : mine;
+            bool more = false, scanned = false;
             int32_t nrows, i, row0, kb, tiles, keys, past, lim, low;
             {
                 const KvRequest &r = place.r;
@@ -611,6 +723,16 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 // barrier below is reached
                 if (ok) ok = tc_wait(&sfull[it % C::kS], it / C::kS, deadline);
                 ok = __all_sync(~0u, ok);
+                if constexpr (kKvShared<P>) {
+                    if (!ok) break;
+                    // the next piece's Q as soon as all scores of this one are there, so that
+                    // its own are made during this one's last softmax and output (64 requests
+                    // of 225 tokens behind a prompt: a piece's 6.7 us were 1.3 of waiting for it)
+                    if (j + 1 == tiles && piece_tiles(piece + 1) > 0) {
+                        more = true;
+                        load_q(place_of(piece + 1).r, place_of(piece + 1).c);
+                    }
+                }
                 tc_fence_after();
                 const uint32_t here = present[it % kTcInfo];
                 // a tile whose keys not all rows see, or of which a slice is missing
@@ -660,8 +782,10 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                     if (ok) ok = tc_wait(&vfull[stage], it / C::kOps, deadline);
                     ok = __all_sync(~0u, ok);
                     constexpr int CH = D / 8;
+                    scanned = scanned || (keys > lim && kb + kAttendTile > lim);
                     for (int q = threadIdx.x; q < kAttendTile * CH; q += 32 * C::kSoft) {
                         const int key = q / CH, ch = q % CH;
+                        if (kKvShared<P> && kb + key < lim && ((here >> (key / 16)) & 1u)) continue;
                         uint4 *at = reinterpret_cast<uint4 *>(smem + C::kOffV + stage * C::kTileBytes +
                                                               (ch / 8) * (kAttendTile * 128) + key * 128 +
                                                               (((ch % 8) ^ (key & 7)) << 4));
@@ -678,7 +802,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                             }
                             if (hit) {
                                 *at = make_uint4(e[0], e[1], e[2], e[3]);
-                                poison[piece % 3] = 1;
+                                poison[(kKvShared<P> ? notes : piece) % 3] = 1;
                             }
                         }
                     }
@@ -688,126 +812,189 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[it % C::kS]);
             }
+            if (kKvShared<P> && !ok) break;
             // the next piece's Q while the last products of this one run (all
             // scores of this piece are there, so nothing reads Q any more)
             const KvWalk w1 = place.w;
             const KvRequest r1 = place.r;
             const KvPiece c1 = place.c;
-            bool more;
-            {
+            if constexpr (!kKvShared<P>) {
                 KvWalk w2 = w1;
                 KvRequest r2 = r1;
-                kv_advance<kTcRows, kAttendTile>(p, w2, r2, kKvShared<P> ? kv_piece_units<P>(w2, r2, c1) : tiles);
+                kv_advance<kTcRows, kAttendTile>(p, w2, r2, tiles);
                 more = w2.u < w2.end;
                 if (more) {
                     const KvPiece c2 = kv_piece<P>(w2, r2);
                     load_q(r2, c2);
-                    if (lane == 0) place = TcPlace{w2, r2, c2};
+                    if (lane == 0) mine = TcPlace{w2, r2, c2};
                     __syncwarp();
                 }
             }
             if (ok) ok = tc_wait(&pvdone[(it - 1) % C::kS], (it - 1) / C::kS, deadline);
             ok = __all_sync(~0u, ok);
             tc_fence_after();
-            // the rows' statistics, summed over a row's four threads, for who puts the
-            // rows out; and every thread's note of values that are not finite.  One sync
-            // covers both: the notes take turns, and the next piece's is cleared while
-            // no thread can be reading or setting it
-            float m = 0.0f, l = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 2 * HALVES; ++k) {
-                float s = sr[k / 2][k % 2];
-                s += __shfl_xor_sync(~0u, s, 1);
-                s += __shfl_xor_sync(~0u, s, 2);
-                if constexpr (HALVES == 1) {
-                    if (t4 == 0) stats[base + 8 * k + g8] = make_float2(mr[0][k], s);
-                } else {  // the warp has all of its rows: row 8 k + g from lane 4 g
-                    const float a = __shfl_sync(~0u, mr[k / 2][k % 2], (lane & 7) * 4);
-                    const float b = __shfl_sync(~0u, s, (lane & 7) * 4);
-                    if (lane >> 3 == k) m = a, l = b;
+            if constexpr (kKvShared<P>) {
+                bool bad = false;
+                if (!Q8 && scanned) {  // every thread's note, as below
+                    if (threadIdx.x == 0) poison[(notes + 1) % 3] = 0;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(noted);
+                    if (ok) ok = tc_wait(noted, notes, deadline);
+                    bad = poison[notes % 3] != 0;
+                    ++notes;
                 }
-            }
-            bool bad = false;
-            if constexpr (!Q8 || HALVES == 1) {
-                if (threadIdx.x == 0) poison[(piece + 1) % 3] = 0;
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoft) : "memory");
-                if (HALVES == 1) m = stats[lr].x, l = stats[lr].y;
-                bad = !Q8 && poison[piece % 3] != 0;
-            }
-            ++piece;
-            const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (c1.ja > 0 ? 0 : 1);
-            if (tc_row<P>(32 * quarter, nrows) < nrows) {
-                const int row = tc_row<P>(lr, nrows);  // of the block, in TMEM lane lr
-                const int32_t head = c1.head * p.group + c1.rb * kTcRows + row - i * p.group;
-                uint16_t *dst = p.out + (r1.q0 + i) * p.out_stride + (int64_t)head * D;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll 1
-                for (int d0 = half * (D / 2); d0 < (half + HALVES) * (D / 2); d0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tl + d0, o);
-                    tmem_wait_ld();
-                    if (bad && row < nrows) {
-                        // values that are not finite count, as they are, for the
-                        // rows that see their keys (a weight is positive; what went
-                        // through the product already stays what it is)
-                        for (int j = c1.ja; j < c1.jb; ++j) {
-                            const int32_t kb = (r1.tile0 + j) * kAttendTile;
-                            uint64_t seen =
-                                kv_seen64(p, r1.kv, r1.past, kv_row_view<PLACED>(p, r1, i), kb, 15u);
-                            for (; seen; seen &= seen - 1) {
-                                const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
-                                const int32_t page = kv_table_row(p, w1.b)[e];
-                                if (page < 0 || page >= p.num_pages) continue;
-                                const uint16_t *v = p.v + page * p.v_page_stride + c1.head * p.v_head_stride +
-                                                    (int64_t)(key - e * p.page_size) * p.v_row_stride + d0;
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (c1.ja > 0 ? 0 : 1);
+                // with 16 rows a quarter or less its two warps put out half of the columns each
+                const bool split = HALVES == 1 && nrows <= kTcRows / 2;
+                const int up = split ? 0 : half, d_end = split && half == 0 ? D / 2 : D;
+                int row[HALVES][2];
+                int64_t at[HALVES][2];
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if ((v[k] & 0x7F80u) == 0x7F80u)
-                                        o[k] = __float_as_uint(__uint_as_float(o[k]) +
-                                                               __uint_as_float((uint32_t)v[k] << 16));
+                for (int h = 0; h < HALVES; ++h) {
+                    const uint32_t to = tl + ((uint32_t)(16 * (h + up)) << 16);
+                    float *dst[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        row[h][e] = tc_row<P>(32 * quarter + 16 * (h + up) + 8 * e + g8, nrows);
+                        at[h][e] = whole ? kv_row_at<kTcRows>(p, w1, r1, c1, row[h][e]) : slot * kTcRows + row[h][e];
+                        dst[e] = (whole ? p.row_part : p.part) + at[h][e] * D + (t4 & 1) * 8 + (t4 >> 1) * 4;
+                    }
+                    if (tc_row<P>(32 * quarter + 16 * (h + up), nrows) >= nrows) continue;  // the same for the warp
+#pragma unroll 2
+                    for (int d0 = split ? half * (D / 2) : 0; d0 < d_end; d0 += 32) {
+                        uint32_t o[16];
+                        tmem_ld16x32(to + d0, o);
+                        tmem_wait_ld();
+                        if (!Q8 && bad) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                if (row[h][(k >> 1) & 1] < nrows)
+                                    o[k] = __float_as_uint(
+                                        __uint_as_float(o[k]) + tc_not_finite(p, w1, r1, c1, row[h][(k >> 1) & 1],
+                                                                              d0 + 8 * (k >> 2) + 2 * t4 + (k & 1)));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint4 y = tc_from_words(t4, o + 8 * (k >> 1) + 2 * (k & 1));
+                            if (Q8) y = make_uint4(y.x, y.z, y.y, y.w);  // columns (0, 2, 1, 3) of every four
+                            if (row[h][k & 1] < nrows)
+                                *reinterpret_cast<uint4 *>(dst[k & 1] + d0 + 16 * (k >> 1)) = y;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(ofree);
+                    mbar_arrive(&pfree[piece % (C::kPlaces > 0 ? C::kPlaces : 1)]);
+                }
+                ++piece;
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float s = sr[h][e];
+                        s += __shfl_xor_sync(~0u, s, 1);
+                        s += __shfl_xor_sync(~0u, s, 2);
+                        if (row[h][e] >= nrows || (split && half > 0)) continue;
+                        if (t4 == 0) (whole ? p.row_ml : p.part_ml)[at[h][e]] = make_float2(mr[h][e], s);
+                    }
+                }
+            } else {
+                // the rows' statistics, summed over a row's four threads, for who puts the
+                // rows out; and every thread's note of values that are not finite.  One sync
+                // covers both: the notes take turns, and the next piece's is cleared while
+                // no thread can be reading or setting it
+                float m = 0.0f, l = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 2 * HALVES; ++k) {
+                    float s = sr[k / 2][k % 2];
+                    s += __shfl_xor_sync(~0u, s, 1);
+                    s += __shfl_xor_sync(~0u, s, 2);
+                    if constexpr (HALVES == 1) {
+                        if (t4 == 0) stats[base + 8 * k + g8] = make_float2(mr[0][k], s);
+                    } else {  // the warp has all of its rows: row 8 k + g from lane 4 g
+                        const float a = __shfl_sync(~0u, mr[k / 2][k % 2], (lane & 7) * 4);
+                        const float b = __shfl_sync(~0u, s, (lane & 7) * 4);
+                        if (lane >> 3 == k) m = a, l = b;
+                    }
+                }
+                bool bad = false;
+                if constexpr (!Q8 || HALVES == 1) {
+                    if (threadIdx.x == 0) poison[(piece + 1) % 3] = 0;
+                    asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoft) : "memory");
+                    if (HALVES == 1) m = stats[lr].x, l = stats[lr].y;
+                    bad = !Q8 && poison[piece % 3] != 0;
+                }
+                ++piece;
+                const bool whole = c1.ja == 0 && c1.jb == r1.ntiles;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (c1.ja > 0 ? 0 : 1);
+                if (32 * quarter < nrows) {
+                    const int row = lr;
+                    const int32_t head = c1.head * p.group + c1.rb * kTcRows + row - i * p.group;
+                    uint16_t *dst = p.out + (r1.q0 + i) * p.out_stride + (int64_t)head * D;
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+                    for (int d0 = half * (D / 2); d0 < (half + HALVES) * (D / 2); d0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tl + d0, o);
+                        tmem_wait_ld();
+                        if (bad && row < nrows) {
+                            // values that are not finite count, as they are, for the
+                            // rows that see their keys (a weight is positive; what went
+                            // through the product already stays what it is)
+                            for (int j = c1.ja; j < c1.jb; ++j) {
+                                const int32_t kb = (r1.tile0 + j) * kAttendTile;
+                                uint64_t seen =
+                                    kv_seen64(p, r1.kv, r1.past, kv_row_view<PLACED>(p, r1, i), kb, 15u);
+                                for (; seen; seen &= seen - 1) {
+                                    const int32_t key = kb + __ffsll((long long)seen) - 1, e = key / p.page_size;
+                                    const int32_t page = kv_table_row(p, w1.b)[e];
+                                    if (page < 0 || page >= p.num_pages) continue;
+                                    const uint16_t *v = p.v + page * p.v_page_stride + c1.head * p.v_head_stride +
+                                                        (int64_t)(key - e * p.page_size) * p.v_row_stride + d0;
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        if ((v[k] & 0x7F80u) == 0x7F80u)
+                                            o[k] = __float_as_uint(__uint_as_float(o[k]) +
+                                                                   __uint_as_float((uint32_t)v[k] << 16));
+                                }
+                            }
+                        }
+                        if (row < nrows) {
+                            float y[32];  // Q8: columns (0, 2, 1, 3) of every four
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                y[k] = __uint_as_float(o[!Q8 || k % 4 == 0 || k % 4 == 3 ? k : k % 4 == 1 ? k + 1 : k - 1]);
+                            if (whole) {
+#pragma unroll
+                                for (int k = 0; k < 32; k += 8)
+                                    *reinterpret_cast<uint4 *>(dst + d0 + k) = make_uint4(
+                                        pack_bf16(y[k] * inv, y[k + 1] * inv), pack_bf16(y[k + 2] * inv, y[k + 3] * inv),
+                                        pack_bf16(y[k + 4] * inv, y[k + 5] * inv),
+                                        pack_bf16(y[k + 6] * inv, y[k + 7] * inv));
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; k += 4)
+                                    *reinterpret_cast<float4 *>(p.part + (slot * kTcRows + row) * D + d0 + k) =
+                                        make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
                             }
                         }
                     }
-                    if (row < nrows) {
-                        float y[32];  // Q8: columns (0, 2, 1, 3) of every four
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            y[k] = __uint_as_float(o[!Q8 || k % 4 == 0 || k % 4 == 3 ? k : k % 4 == 1 ? k + 1 : k - 1]);
-                        if constexpr (kKvShared<P>) {
-                            float *to = whole ? p.row_part + kv_row_at<kTcRows>(p, w1, r1, c1, row) * D : p.part + (slot * kTcRows + row) * D;
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                *reinterpret_cast<float4 *>(to + d0 + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                        } else if (whole) {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 8)
-                                *reinterpret_cast<uint4 *>(dst + d0 + k) = make_uint4(
-                                    pack_bf16(y[k] * inv, y[k + 1] * inv), pack_bf16(y[k + 2] * inv, y[k + 3] * inv),
-                                    pack_bf16(y[k + 4] * inv, y[k + 5] * inv),
-                                    pack_bf16(y[k + 6] * inv, y[k + 7] * inv));
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                *reinterpret_cast<float4 *>(p.part + (slot * kTcRows + row) * D + d0 + k) =
-                                    make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                        }
+                    if (half == 0 && row < nrows) {
+                        if (!whole) p.part_ml[slot * kTcRows + row] = make_float2(m, l);
+                        else if (p.lse)
+                            p.lse[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] =
+                                l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
                     }
                 }
-                if (half == 0 && row < nrows) {
-                    if constexpr (kKvShared<P>) {
-                        if (c1.ja == 0) kv_note<kTcRows>(p, w1, r1, c1, row, whole);
-                        if (whole) p.row_ml[kv_row_at<kTcRows>(p, w1, r1, c1, row)] = make_float2(m, l);
-                    }
-                    if (!whole) p.part_ml[slot * kTcRows + row] = make_float2(m, l);
-                    else if (!kKvShared<P> && p.lse)
-                        p.lse[(int64_t)(r1.q0 + i) * (p.group * p.kv_heads) + head] =
-                            l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ofree);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ofree);
             if (!more) break;
         }
         if (!ok && lane == 0) atomicOr(p.status, 8u);
@@ -876,13 +1063,9 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 return true;
             };
             while (ok) {
-                int n = 0, units = 0;  // tiles, and the units that they are
+                int n = 0;  // tiles
                 if constexpr (kKvShared<P>) {
-                    if (w.u < w.end) {
-                        const KvPiece c = kv_piece<P>(w, r);
-                        n = c.jb - c.ja;
-                        units = kv_piece_units<P>(w, r, c);
-                    }
+                    n = piece_tiles(piece);
                 } else {
                     n = w.u < w.end ? (int)min((int64_t)r.ntiles - (w.u - w.start) % r.ntiles, w.end - w.u) : 0;
                 }
@@ -913,7 +1096,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                     ++done;
                 }
                 ++piece;
-                if (ok) kv_advance<kTcRows, kAttendTile>(p, w, r, kKvShared<P> ? units : n);
+                if (!kKvShared<P> && ok) kv_advance<kTcRows, kAttendTile>(p, w, r, n);
             }
             if (leader) {
                 if (!ok) atomicOr(p.status, 8u);
@@ -921,6 +1104,37 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
                 tc_wait(drain, 0, globaltimer_ns() + p.timeout_ns);
             }
             __syncwarp();
+        } else if (kKvShared<P> && warp == kPlace) {
+            // ------------------------------------------------------------ places of the pieces
+            // What a piece costs besides its tiles, and the notes for the joining kernel, off the
+            // softmax warps' way; the last entry has no tiles.
+            constexpr uint32_t N = C::kPlaces > 0 ? C::kPlaces : 1;
+            for (uint32_t n = 0; ok; ++n) {
+                const bool some = w.u < w.end;
+                KvPiece c = {};
+                if (some) c = kv_piece<P>(w, r);
+                if (n >= N) ok = __all_sync(~0u, tc_wait(&pfree[n % N], n / N - 1, deadline));
+                if (!ok) break;
+                if (lane == 0) {
+                    places[n % N] = TcPlace{w, r, c};
+                    mbar_arrive(&placed[n % N]);
+                }
+                __syncwarp();
+                if (!some) break;
+                const int64_t left = (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows;
+                const bool whole = c.ja == 0 && c.jb == r.ntiles;
+                for (int row = lane; row < min((int64_t)kTcRows, left); row += 32) {
+                    const int32_t rr = c.rb * kTcRows + row, tok = rr / p.group;
+                    const uint16_t *q = p.q + (int64_t)(r.q0 + tok) * p.q_stride +
+                                        (int64_t)(c.head * p.group + rr - tok * p.group) * D;
+                    if (n > 0)
+                        for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+                    if constexpr (kKvShared<P>)
+                        if (c.ja == 0) kv_note<kTcRows>(p, w, r, c, row, whole);
+                }
+                kv_advance<kTcRows, kAttendTile>(p, w, r, kv_piece_units<P>(w, r, c));
+            }
+            if (!ok && lane == 0) atomicOr(p.status, 8u);
         } else if (Q8 && warp >= kConvert) {
             // ------------------------------------------------------------ converters of a Q8 cache
             const int cw = (warp - kConvert) & 3, ct = cw * 32 + lane;
@@ -934,17 +1148,18 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             const uint32_t base = (cc / 4) * (kAttendTile * 128) + ckey * 128;
             const uint32_t at0 = base + (((2 * (cc % 4) + (turn ? 1 : 0)) ^ (ckey & 7)) << 4);
             const uint32_t at1 = base + (((2 * (cc % 4) + (turn ? 0 : 1)) ^ (ckey & 7)) << 4);
-            uint32_t total = (uint32_t)(w.end - w.u);  // tiles of the CTA
-            if constexpr (kKvShared<P>) {
-                KvWalk w2 = w;
-                KvRequest r2 = r;
-                total = 0;
-                while (w2.u < w2.end) {
-                    const KvPiece c = kv_piece<P>(w2, r2);
-                    total += (uint32_t)(c.jb - c.ja);
-                    kv_advance<kTcRows, kAttendTile>(p, w2, r2, kv_piece_units<P>(w2, r2, c));
+            const uint32_t total = (uint32_t)(w.end - w.u);  // tiles of the CTA
+            uint32_t piece = 0, known = 0;                   // with shared prefixes: of its pieces so far
+            const auto exists = [&](uint32_t x) -> bool {
+                if constexpr (!kKvShared<P>) return x < total;
+                while (x >= known) {
+                    const int n = piece_tiles(piece);
+                    if (n == 0) return false;
+                    known += n;
+                    ++piece;
                 }
-            }
+                return true;
+            };
             // K or V of tile x to its operand buffer, which the tile before it there must have left
             auto convert = [&](bool values, uint32_t x) -> bool {
                 const uint32_t stage = x % N;
@@ -1004,13 +1219,13 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8>::kThreads, AttendTcCfg<D, Q
             };
             if constexpr (C::kGroups == 2) {
                 const bool values = warp >= kConvert + 4;
-                for (uint32_t x = 0; ok && x < total; ++x) ok = convert(values, x);
+                for (uint32_t x = 0; ok && exists(x); ++x) ok = convert(values, x);
             } else {
                 // the keys run one tile ahead: their buffer is free as soon as the scores
                 // are made, the values' only after the softmax
                 ok = convert(false, 0);
-                for (uint32_t x = 0; ok && x < total; ++x) {
-                    if (x + 1 < total) ok = convert(false, x + 1);
+                for (uint32_t x = 0; ok && exists(x); ++x) {
+                    if (exists(x + 1)) ok = convert(false, x + 1);
                     ok = ok && convert(true, x);
                 }
             }

@@ -175,7 +175,7 @@ int attend_variant(const DeviceView &d, int *resident, const P *p, const CUtenso
 template <int D, bool Q8, bool PLACED, class P>
 int attend_tc_variant(const DeviceView &d, int *resident, const P *p, const CUtensorMap *tm_k,
                       const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
-    using C = dev::AttendTcCfg<D, Q8>;
+    using C = dev::AttendTcCfg<D, Q8, dev::kKvShared<P>>;
     static std::mutex mu;
     static int per_sm[kKvMaxDevices] = {};
     return attend_kernel(d, &dev::w12_kv_attend_tc_kernel<D, Q8, PLACED, P>,
