@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
         auto load_q = [&](const KvRequest &rq, const KvPiece &pc) {
             constexpr int CH = D / 8, STEPS = HALVES * CH / 2, G = STEPS < 8 ? STEPS : 8;  // 16-byte chunks; 32 a step
             if constexpr (C::kQTmem && kKvShared<P> && D == 256) {
-                // 16 rows at a time, four lanes on 64 bytes of each
+                // 16 rows at a time, four lanes on 64 bytes of each (twenty trees of four tokens:
+                // 48.3 us, with a row per lane 52.4; of 128 columns no faster)
                 const int rows = (int)min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
                         src[e] = p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
                                  (int64_t)(pc.head * p.group + rr - tok * p.group) * D + (t4 & 1) * 16 + (t4 >> 1) * 8;
                     }
-                    constexpr int N = D >= 128 ? 2 : 1;  // 64 columns (as 32 words) a step
+                    constexpr int N = 2;  // 64 columns (as 32 words) a step
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 64 * N) {
                         uint4 u[N][2][2];
@@ -850,20 +851,24 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
                 // with 16 rows a quarter or less its two warps put out half of the columns each
                 const bool split = HALVES == 1 && nrows <= kTcRows / 2;
                 const int up = split ? 0 : half, d_end = split && half == 0 ? D / 2 : D;
-                int row[HALVES][2];
-                int64_t at[HALVES][2];
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
                     const uint32_t to = tl + ((uint32_t)(16 * (h + up)) << 16);
+                    int row[2];
                     float *dst[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        row[h][e] = tc_row<P>(32 * quarter + 16 * (h + up) + 8 * e + g8, nrows);
-                        at[h][e] = whole ? kv_row_at<kTcRows>(p, w1, r1, c1, row[h][e]) : slot * kTcRows + row[h][e];
-                        dst[e] = (whole ? p.row_part : p.part) + at[h][e] * D + (t4 & 1) * 8 + (t4 >> 1) * 4;
+                        row[e] = tc_row<P>(32 * quarter + 16 * (h + up) + 8 * e + g8, nrows);
+                        const int64_t at = whole ? kv_row_at<kTcRows>(p, w1, r1, c1, row[e]) : slot * kTcRows + row[e];
+                        dst[e] = (whole ? p.row_part : p.part) + at * D + (t4 & 1) * 8 + (t4 >> 1) * 4;
+                        float s = sr[h][e];
+                        s += __shfl_xor_sync(~0u, s, 1);
+                        s += __shfl_xor_sync(~0u, s, 2);
+                        if (t4 == 0 && row[e] < nrows && !(split && half > 0))
+                            (whole ? p.row_ml : p.part_ml)[at] = make_float2(mr[h][e], s);
                     }
                     if (tc_row<P>(32 * quarter + 16 * (h + up), nrows) >= nrows) continue;  // the same for the warp
-#pragma unroll 2
+#pragma unroll (HALVES == 1 ? 2 : 1)
                     for (int d0 = split ? half * (D / 2) : 0; d0 < d_end; d0 += 32) {
                         uint32_t o[16];
                         tmem_ld16x32(to + d0, o);
@@ -871,16 +876,16 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
                         if (!Q8 && bad) {
 #pragma unroll
                             for (int k = 0; k < 16; ++k)
-                                if (row[h][(k >> 1) & 1] < nrows)
+                                if (row[(k >> 1) & 1] < nrows)
                                     o[k] = __float_as_uint(
-                                        __uint_as_float(o[k]) + tc_not_finite(p, w1, r1, c1, row[h][(k >> 1) & 1],
+                                        __uint_as_float(o[k]) + tc_not_finite(p, w1, r1, c1, row[(k >> 1) & 1],
                                                                               d0 + 8 * (k >> 2) + 2 * t4 + (k & 1)));
                         }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint4 y = tc_from_words(t4, o + 8 * (k >> 1) + 2 * (k & 1));
                             if (Q8) y = make_uint4(y.x, y.z, y.y, y.w);  // columns (0, 2, 1, 3) of every four
-                            if (row[h][k & 1] < nrows)
+                            if (row[k & 1] < nrows)
                                 *reinterpret_cast<uint4 *>(dst[k & 1] + d0 + 16 * (k >> 1)) = y;
                         }
                     }
@@ -892,17 +897,6 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
                     mbar_arrive(&pfree[piece % (C::kPlaces > 0 ? C::kPlaces : 1)]);
                 }
                 ++piece;
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float s = sr[h][e];
-                        s += __shfl_xor_sync(~0u, s, 1);
-                        s += __shfl_xor_sync(~0u, s, 2);
-                        if (row[h][e] >= nrows || (split && half > 0)) continue;
-                        if (t4 == 0) (whole ? p.row_ml : p.part_ml)[at[h][e]] = make_float2(mr[h][e], s);
-                    }
-                }
             } else {
                 // the rows' statistics, summed over a row's four threads, for who puts the
                 // rows out; and every thread's note of values that are not finite.  One sync
