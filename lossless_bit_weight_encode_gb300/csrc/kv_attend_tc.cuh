@@ -57,7 +57,7 @@ struct AttendTcCfg {
     // memory, for the trees above) and where it takes the room of ring slots.  Only the
     // 8-bit cache of 128 columns has no columns left: its two CTAs per SM are worth more
     // (117 us; one CTA with Q in TMEM 116, but 404 against 365 at 64000 tokens).
-    static constexpr bool kQTmem = !Q8 || D != 128;
+    static constexpr bool kQTmem = !Q8 || D != 128 || SHARED;
     // One CTA per SM or two (with half of TMEM each).
     static constexpr bool kOne = D == 256 || (D == 128 && kQTmem);
     // Score buffers, and how many tiles the scores are made ahead of the products.
@@ -86,8 +86,8 @@ struct AttendTcCfg {
     static constexpr int kRawBytes = kAttendTile * D;       // K or V of a tile as bytes (Q8)
     static constexpr int kBlocks = D / 64;                  // 128-byte column blocks of an operand row
     // operand rings (filled by TMA, or by the converting warps) and byte rings
-    static constexpr int kOps = Q8 ? (D == 256 ? 2 : 1) : D == 64 ? 5 : D == 128 ? 6 : 3;
-    static constexpr int kRaws = Q8 ? (D == 64 ? 6 : 2) : 0;
+    static constexpr int kOps = Q8 ? (D == 256 ? 2 : D == 128 && SHARED ? 3 : 1) : D == 64 ? 5 : D == 128 ? 6 : 3;
+    static constexpr int kRaws = Q8 ? (D == 64 ? 6 : D == 128 && SHARED ? 4 : 2) : 0;
     // A slot of the ring of facts is written again after the softmax of its tile: the
     // loader is at most the byte ring, the operand ring and the score buffers ahead.
     static_assert(kRaws + kOps + kS <= kTcInfo, "the ring of facts");
@@ -378,9 +378,9 @@ __device__ __noinline__ float tc_not_finite(const P &p, const KvWalk &w, const K
 // Fills a ring with the keys or the values of the CTA's tiles, one tile per step().
 // Keys and values have a loader (and a warp) each: a ring's next tile is then asked
 // for as soon as its own slot is free, up to a ring (kOps or kRaws tiles) ahead of its use.
-template <int D, bool Q8>
+template <int D, bool Q8, bool SHARED>
 struct TcLoader {
-    using C = AttendTcCfg<D, Q8>;
+    using C = AttendTcCfg<D, Q8, SHARED>;
     static constexpr uint32_t N = Q8 ? C::kRaws : C::kOps;
     const void *map;
     uint8_t *ring;            // slot 0
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
         if constexpr (C::kRegs > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
         if (warp == kLoadK || warp == kLoadV) {
             // ------------------------------------------------------------ loaders
-            TcLoader<D, Q8> load;
+            TcLoader<D, Q8, kKvShared<P>> load;
             const bool keys = warp == kLoadK;
             load.map = keys ? &tm_k : &tm_v;
             load.ring = smem + (Q8 ? C::kOffRaw + (keys ? 0 : C::kRawBytes) : keys ? C::kOffK : C::kOffV);
