@@ -86,6 +86,8 @@ struct ForkPlan {
 ForkPlan fork_plan(const w12_kv_fork_args &a) {
     ForkPlan plan;
     if ((int64_t)a.requests * a.max_blocks <= dev::kForkOne) plan.cols = a.max_blocks;
+    else
+        while (plan.cols > 1 && a.max_blocks <= dev::kForkCtas * (plan.cols / 2)) plan.cols /= 2;
     plan.ctas = (a.max_blocks + plan.cols - 1) / plan.cols;
     plan.off_state = (size_t)dev::kForkRows * sizeof(int32_t);
     plan.bytes = plan.off_state + 16 + ((size_t)4 * a.requests + plan.ctas) * sizeof(int32_t);

@@ -30,6 +30,7 @@ namespace dev {
 
 constexpr int kForkRows = 4096, kForkCols = 8;
 constexpr int kForkOne = 8192;  // table entries that one CTA takes
+constexpr int kForkCtas = 152;  // with fewer columns per CTA than kForkCols: at most one per SM
 
 struct KvForkParams {
     const int32_t *parents, *lens;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
     if (STEP == 1 && blockIdx.x == 0 && tid == 0) p.old_state[0] = head, p.old_state[1] = tail;
     // the columns' old entries
     for (int i = tid; i < cols * R; i += T) {
-        const int r = STEP == 0 ? i / cols : i / kForkCols, k = i - r * cols;
+        const int r = STEP == 0 ? i / cols : i >> (__ffs(cols) - 1), k = i - r * cols;
         int32_t e = -1;
         if (c0 + k < s_owned[r]) e = __ldcg(p.tables + r * p.table_stride + c0 + k);
         s_e[k * pitch + r] = e >= 0 && e < p.num_pages ? e : -1;
