@@ -434,6 +434,7 @@ int kv_fork(const w12_kv_fork_args &a, void *workspace, size_t ws_bytes, void *s
     p.copies = p.parent + a.requests;
     p.counts = p.copies + a.requests;
     p.cols = plan.cols;
+    p.ctas = plan.ctas;
     static std::mutex mu;
     static bool set[kKvMaxDevices] = {};
     cudaError_t e = cudaSuccess;
@@ -450,7 +451,7 @@ int kv_fork(const w12_kv_fork_args &a, void *workspace, size_t ws_bytes, void *s
     }
     const int smem = dev::fork_smem(a.requests, plan.cols);
     const int64_t line = (int64_t)plan.cols * a.requests;
-    const int threads = (int)std::min<int64_t>(1024, (std::max<int64_t>(line / 2, a.requests) + 127) / 128 * 128);
+    const int threads = (int)std::min<int64_t>(1024, (std::max<int64_t>(line, a.requests) + 127) / 128 * 128);
     // held over both launches, as the locks of the attend calls
     const std::lock_guard<std::mutex> lock(workspace_lock(workspace));
     if (plan.ctas == 1) {
@@ -458,7 +459,8 @@ int kv_fork(const w12_kv_fork_args &a, void *workspace, size_t ws_bytes, void *s
     } else {
         e = kv_launch(d, &dev::w12_kv_fork_kernel<1>, dim3((unsigned)plan.ctas), threads, smem, 1, stream, p);
         if (e == cudaSuccess)
-            e = kv_launch(d, &dev::w12_kv_fork_kernel<2>, dim3((unsigned)plan.ctas), threads, smem, 1, stream, p);
+            e = kv_launch(d, &dev::w12_kv_fork_kernel<2>,
+                          dim3((unsigned)plan.ctas + (a.prefix_lens ? 1u : 0u)), threads, smem, 1, stream, p);
     }
     if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_fork launch", err);
     return W12_OK;

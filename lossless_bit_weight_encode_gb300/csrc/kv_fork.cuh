@@ -51,7 +51,7 @@ struct KvForkParams {
     int32_t *need, *held, *parent, *copies, *counts, *differ;
     int64_t *old_state;
     uint32_t rows_inv;  // ceil(2^32 / requests)
-    int32_t requests, max_blocks, page_size, ring_size, groups, cols;
+    int32_t requests, max_blocks, page_size, ring_size, groups, cols, ctas;
     uint32_t *status;
 };
 
@@ -88,8 +88,9 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
     uint8_t *s_copy = reinterpret_cast<uint8_t *>(s_start + R);
     constexpr int32_t kTwo = 1 << 30;
     const bool prefix = p.prefix_lens != nullptr;
-    // what CTA 0 of the second launch does of the prefixes needs the groups too
-    const bool groups = prefix && (STEP != 2 || blockIdx.x == 0);
+    // the second launch has one CTA more for the prefixes
+    const bool last = STEP == 2 && (int)blockIdx.x == p.ctas, groups = prefix && (STEP != 2 || last);
+    const int32_t *cu = s_differ;  // at first the groups' first rows, where every row looks for its own
     pdl_launch_dependents();
     pdl_wait();
     uint32_t flags = 0;
@@ -97,58 +98,64 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
     int64_t head, tail;
     if (STEP == 2) head = __ldcg(&p.old_state[0]), tail = __ldcg(&p.old_state[1]);
     else head = __ldcg(&p.state[0]), tail = __ldcg(&p.state[1]);
+    const int32_t cu_end = groups ? p.prefix_cu[p.groups] : 0;
+    // parents and lengths wait in the places of what comes of them
     for (int i = tid; i < R; i += T) {
         const int32_t o = STEP == 2 ? p.held[i] : p.owned[i];
+        const int32_t par = STEP == 2 ? p.parent[i] : p.parents[i], n = STEP == 2 ? p.need[i] : p.lens[i];
+        const int32_t copy = STEP == 2 ? p.copies[i] : 0, start = groups && i < p.groups ? p.prefix_cu[i] : 0;
         s_owned[i] = min(max(o, 0), p.max_blocks);
         s_lead[i] = kTwo - 1;
-        s_differ[i] = 0;
-        s_copy[i] = 0;
-        if (o != s_owned[i]) flags |= kStatusKvSizes;
-        if (STEP == 2) {
-            s_need[i] = p.need[i];
-            s_parent[i] = (int16_t)p.parent[i];
-        }
+        s_differ[i] = start;
+        s_copy[i] = copy != 0;
+        s_need[i] = n;
+        s_parent[i] = (int16_t)(par >= 0 && par < R ? par : -1);
+        if (o != s_owned[i] || (STEP != 2 && (par < -1 || par >= R))) flags |= kStatusKvSizes;
     }
     __syncthreads();
+    // the columns' old entries
+    if (!last)
+#pragma unroll 4
+        for (int i = tid; i < cols * R; i += T) {
+            const int r = STEP == 0 ? i / cols : i >> (__ffs(cols) - 1), k = i - r * cols;
+            int32_t e = -1;
+            if (c0 + k < s_owned[r]) e = __ldcg(p.tables + r * p.table_stride + c0 + k);
+            s_e[k * pitch + r] = e >= 0 && e < p.num_pages ? e : -1;
+        }
     for (int i = tid; i < R; i += T) {
         if (STEP != 2) {
-            const int32_t par = p.parents[i], l = p.lens[i];
-            const bool real = par >= 0 && par < R;
-            const int64_t most = real ? (int64_t)s_owned[par] * p.page_size : 0;
+            const int32_t par = s_parent[i], l = s_need[i];
+            const int64_t most = par >= 0 ? (int64_t)s_owned[par] * p.page_size : 0;
             const int32_t keep = clamp_i32(l, 0, most);
-            if ((real && keep != l) || par < -1 || par >= R) flags |= kStatusKvSizes;
+            if (par >= 0 && keep != l) flags |= kStatusKvSizes;
             const int32_t need = (int32_t)(((int64_t)keep + p.page_size - 1) / p.page_size);
             const bool part = need * (int64_t)p.page_size != keep;
-            s_parent[i] = real ? (int16_t)par : (int16_t)-1;
             s_need[i] = need | (part ? (int32_t)0x80000000 : 0);
             if (STEP == 1 && blockIdx.x == 0) {
                 p.need[i] = s_need[i];
                 p.held[i] = s_owned[i];
-                p.parent[i] = s_parent[i];
+                p.parent[i] = par;
             }
         }
         if (groups) {
             int lo = 0, hi = p.groups;  // the last group that starts at or before i
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (p.prefix_cu[mid] <= i) lo = mid;
+                if (cu[mid] <= i) lo = mid;
                 else hi = mid;
             }
-            const int32_t a = p.prefix_cu[lo], b = p.prefix_cu[lo + 1];
+            const int32_t a = cu[lo], b = lo + 1 < p.groups ? cu[lo + 1] : cu_end;
             const int start = i >= a && i < b ? max(a, 0) : i;  // in no group: one of its own
             s_start[i] = (uint16_t)start;
             if ((s_need[i] & 0x7FFFFFFF) > 0) atomicMin(&s_lead[start], i);
         }
     }
     if (STEP == 1 && blockIdx.x == 0 && tid == 0) p.old_state[0] = head, p.old_state[1] = tail;
-    // the columns' old entries
-    for (int i = tid; i < cols * R; i += T) {
-        const int r = STEP == 0 ? i / cols : i >> (__ffs(cols) - 1), k = i - r * cols;
-        int32_t e = -1;
-        if (c0 + k < s_owned[r]) e = __ldcg(p.tables + r * p.table_stride + c0 + k);
-        s_e[k * pitch + r] = e >= 0 && e < p.num_pages ? e : -1;
-    }
     __syncthreads();
+    if (STEP != 1 && groups) {
+        for (int i = tid; i < R; i += T) s_differ[i] = 0;
+        __syncthreads();
+    }
 
     // the page that row r wants at column k as a full one (-1: none)
     const auto wants = [&](int r, int k) {
@@ -171,6 +178,29 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
             f(x - k * R, k);
         }
     };
+
+    const auto prefixes = [&]() {
+        for (int r = tid; r < R; r += T) {
+            const int lead = s_lead[s_start[r]] & (kTwo - 1);
+            if ((s_need[r] & 0x7FFFFFFF) == 0) continue;
+            if (lead != r) atomicOr(&s_lead[s_start[r]], kTwo);
+            if (STEP == 2 && lead == r) s_differ[r] = __ldcg(&p.differ[r]), p.differ[r] = 0;
+        }
+        __syncthreads();
+        for (int r = tid; r < R; r += T) {
+            int32_t tokens = 0;
+            if ((s_need[r] & 0x7FFFFFFF) > 0) {
+                const int32_t l = s_lead[s_start[r]], lead = l & (kTwo - 1), m = s_need[lead];
+                const int32_t full = (m & 0x7FFFFFFF) - (m < 0 ? 1 : 0), d = s_differ[lead];
+                if (l & kTwo) tokens = min(full, d > 0 ? p.max_blocks - d : full) * p.page_size;
+            }
+            p.prefix_lens[r] = tokens;
+        }
+    };
+    if (last) {
+        prefixes();
+        return;
+    }
 
     // ------------------------------------------------------------ counting
     bool any = false;
@@ -222,11 +252,11 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
         __syncthreads();
     }
     // rows that end here and have to copy: those whose page has another one's mark
-    for (int r = tid; r < R; r += T) {
+    for (int r = tid; STEP != 2 && r < R; r += T) {
         int k;
         if (!ends(r, k)) continue;
         const int32_t b = s_need[r] < 0 ? s_e[k * pitch + s_parent[r]] : -1;
-        const bool copy = STEP == 2 ? p.copies[r] != 0 : b >= 0 && __ldcg(&p.shares[b]) != keep_mark(r);
+        const bool copy = b >= 0 && __ldcg(&p.shares[b]) != keep_mark(r);
         s_copy[r] = copy;
         if (STEP == 1) p.copies[r] = copy;
     }
@@ -255,7 +285,7 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
     int32_t before = 0, all = 0, here = 1;  // pages freed before these columns, in all, and here (0: none)
     if (STEP == 2) {
         int32_t a = 0, b = 0;
-        for (int i = tid; i < (int)gridDim.x; i += T) {
+        for (int i = tid; i < p.ctas; i += T) {
             const int32_t n = p.counts[i];
             a += i < (int)blockIdx.x ? n : 0;
             b += n;
@@ -324,7 +354,7 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
     int32_t given = 0;  // copies of the rows before
     for (int r0 = 0; r0 < R; r0 += T) {
         const int r = r0 + tid;
-        const bool want = mine && r < R && (STEP == 2 ? p.copies[r] != 0 : s_copy[r] != 0);
+        const bool want = mine && r < R && s_copy[r];
         const uint32_t hit = __ballot_sync(~0u, want);
         int32_t at = given;
         if (mine) {
@@ -362,25 +392,8 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
             p.state[0] = head + min(given, avail);
             p.state[1] = tail + min(all, room);
         }
-        if (prefix) {
-            for (int r = tid; r < R; r += T) {
-                const int lead = s_lead[s_start[r]] & (kTwo - 1);
-                if ((s_need[r] & 0x7FFFFFFF) == 0) continue;
-                if (lead != r) atomicOr(&s_lead[s_start[r]], kTwo);
-                if (STEP == 2 && lead == r) s_differ[r] = __ldcg(&p.differ[r]), p.differ[r] = 0;
-            }
-            __syncthreads();
-            for (int r = tid; r < R; r += T) {
-                int32_t tokens = 0;
-                if ((s_need[r] & 0x7FFFFFFF) > 0) {
-                    const int32_t l = s_lead[s_start[r]], lead = l & (kTwo - 1), m = s_need[lead];
-                    const int32_t full = (m & 0x7FFFFFFF) - (m < 0 ? 1 : 0), d = s_differ[lead];
-                    if (l & kTwo) tokens = min(full, d > 0 ? p.max_blocks - d : full) * p.page_size;
-                }
-                p.prefix_lens[r] = tokens;
-            }
-        }
     }
+    if (STEP == 0 && prefix) prefixes();
     if (flags && (STEP == 0 || first || (flags & kStatusKvPages))) atomicOr(p.status, flags);
 }
 
