@@ -575,6 +575,8 @@ int kv_attend_shared(const w12_kv_cache &c, const w12_kv_attend_args &a, const w
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     dev::KvSharedParams p = {};
     static_cast<dev::KvAttendParams &>(p) = attend_params(d, c, a);
+    p.by_group = dev::kv_divisor((uint32_t)p.group);
+    p.by_page = dev::kv_divisor((uint32_t)p.page_size);
     p.prefix_cu = prefix.cu;
     p.prefix_lens = prefix.lens;
     p.groups = prefix.groups;

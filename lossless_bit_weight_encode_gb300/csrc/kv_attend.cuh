@@ -190,7 +190,7 @@ __device__ __forceinline__ const int32_t *kv_table_row(const KvAttendParams &p, 
 // With shared prefixes: the tokens that request b shares with its group, whole pages.
 __device__ __forceinline__ int32_t kv_shared_tokens(const KvSharedParams &p, int b) {
     const int32_t n = min(max(p.prefix_lens[b], 0), min(max(p.lens[b], 0), p.max_keys));
-    return n / p.page_size * p.page_size;
+    return kv_over_page(p, n) * p.page_size;
 }
 
 // The group's first request that shares a prefix (-1: none does).
@@ -242,7 +242,7 @@ __device__ __forceinline__ const int32_t *kv_table_row(const KvSpanParams<KIND> 
         kv_group(p, s, b0, b1);
         b0 = max(kv_leader(p, b0, b1), 0);
     }
-    return p.tables + (int64_t)b0 * p.table_stride + (own ? kv_shared_tokens(p, b0) / p.page_size : 0);
+    return p.tables + (int64_t)b0 * p.table_stride + (own ? kv_over_page(p, kv_shared_tokens(p, b0)) : 0);
 }
 
 // What a launch's line has: requests, or groups and requests.
@@ -393,8 +393,9 @@ __device__ __forceinline__ bool kv_walk_start(const P &p, KvWalk &w, KvRequest &
 }
 
 // Table entries that the request's keys take.
-__device__ __forceinline__ int32_t kv_entries(const KvAttendParams &p, const KvRequest &r) {
-    return r.kv > 0 ? (r.kv - 1) / p.page_size + 1 : 0;
+template <class P>
+__device__ __forceinline__ int32_t kv_entries(const P &p, const KvRequest &r) {
+    return r.kv > 0 ? kv_over_page(p, r.kv - 1) + 1 : 0;
 }
 
 // The piece at w.u: its (key head, row block) and its tiles [ja, jb).
@@ -504,7 +505,7 @@ __device__ __forceinline__ void kv_emit(const KvAttendParams &p, const KvRequest
 template <int ROWS, class P>
 __device__ __forceinline__ int64_t kv_row_at(const P &p, const KvWalk &w, const KvRequest &r,
                                              const KvPiece &c, int lr) {
-    const int32_t rr = c.rb * ROWS + lr, i = rr / p.group, heads = p.group * p.kv_heads;
+    const int32_t rr = c.rb * ROWS + lr, i = kv_over_group(p, rr), heads = p.group * p.kv_heads;
     return (int64_t)(r.q0 + i + (w.b + p.first_span() >= p.groups ? p.tokens : 0)) * heads + c.head * p.group + rr - i * p.group;
 }
 template <int D>
@@ -708,14 +709,14 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
         while (ok && w.u < w.end) {
             const KvPiece c = kv_piece<P>(w, r);
             KvPageWindow pages;
-            pages.start(kv_table_row(p, w.b), (r.tile0 + c.ja) * TILE / p.page_size, kv_entries(p, r));
+            pages.start(kv_table_row(p, w.b), kv_over_page(p, (r.tile0 + c.ja) * TILE), kv_entries(p, r));
             for (int j = c.ja; ok && j < c.jb; ++j, ++it) {
                 const uint32_t stage = it % C::kStages, round = it / C::kStages;
                 // lane s deals with slice s
                 const int32_t t0 = (r.tile0 + j) * TILE, kb = t0 + (lane % C::kSlices) * kAttendSlice;
                 const bool want = lane < C::kSlices && kb < r.kv && kb + kAttendSlice > r.first;
-                const int32_t e = kb / p.page_size, off = kb - e * p.page_size;
-                const int32_t found = pages.get(t0 / p.page_size, e), page = want ? found : -1;
+                const int32_t e = kv_over_page(p, kb), off = kb - e * p.page_size;
+                const int32_t found = pages.get(kv_over_page(p, t0), e), page = want ? found : -1;
                 if (round > 0) ok = mbar_wait(&empty[stage], (round - 1) & 1, deadline);
                 ok = __shfl_sync(~0u, ok, 0);
                 if (!ok) break;
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
         for (int nt = 0; nt < NT; ++nt) {
             const int lr = (wr * NT + nt) * 8 + g;
             const int32_t rr = row0 + lr;
-            const int32_t i = rr / p.group;
+            const int32_t i = kv_over_group(p, rr);
             const uint32_t *src = reinterpret_cast<const uint32_t *>(
                 p.q + (int64_t)(r.q0 + (lr < nrows ? i : 0)) * p.q_stride +
                 (int64_t)(c.head * p.group + (lr < nrows ? rr - i * p.group : 0)) * D);
@@ -880,7 +881,7 @@ __global__ void __launch_bounds__(kAttendThreads, attend_ctas<D, Q8, NT>()) w12_
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int32_t lr = (wr * NT + nt) * 8 + 2 * t + e;
-                            const int32_t i = (row0 + min(lr, nrows - 1)) / p.group;
+                            const int32_t i = kv_over_group(p, row0 + min(lr, nrows - 1));
                             const KvRowView v = p.positions ? kv_row_view<true>(p, r, i) : kv_row_view<false>(p, r, i);
 #pragma unroll
                             for (int u = 0; u < PAIR; ++u) {

@@ -359,7 +359,7 @@ __device__ __forceinline__ void tc_softmax(uint32_t ts, const uint32_t (&x)[32],
 template <class P>
 __device__ __noinline__ float tc_not_finite(const P &p, const KvWalk &w, const KvRequest &r, const KvPiece &c, int row,
                                             int d) {
-    const KvRowView view = kv_row_view<false>(p, r, (c.rb * kTcRows + row) / p.group);
+    const KvRowView view = kv_row_view<false>(p, r, kv_over_group(p, c.rb * kTcRows + row));
     float sum = 0.0f;
     for (int j = c.ja; j < c.jb; ++j) {
         const int32_t kb = (r.tile0 + j) * kAttendTile;
@@ -399,7 +399,7 @@ struct TcLoader {
     __device__ __forceinline__ void open(const P &p) {
         c = kv_piece<P>(w, r);
         j = c.ja;
-        pages.start(kv_table_row(p, w.b), (r.tile0 + c.ja) * kAttendTile / p.page_size, kv_entries(p, r));
+        pages.start(kv_table_row(p, w.b), kv_over_page(p, (r.tile0 + c.ja) * kAttendTile), kv_entries(p, r));
     }
     template <class P>
     __device__ __forceinline__ void start(const P &p, const KvWalk &walk, const KvRequest &req) {
@@ -417,8 +417,8 @@ struct TcLoader {
         const int s = lane & 3, blk = lane >> 2;
         const int32_t t0 = (r.tile0 + j) * kAttendTile, kb = t0 + s * kAttendSlice;
         const bool want = lane < (Q8 ? 4 : 4 * C::kBlocks) && kb < r.kv && kb + kAttendSlice > r.first;
-        const int32_t e = kb / p.page_size, off = kb - e * p.page_size;
-        const int32_t found = pages.get(t0 / p.page_size, e), page = want ? found : -1;
+        const int32_t e = kv_over_page(p, kb), off = kb - e * p.page_size;
+        const int32_t found = pages.get(kv_over_page(p, t0), e), page = want ? found : -1;
         const bool here = page >= 0 && page < p.num_pages;
         const uint32_t mask = __ballot_sync(~0u, here) & 15u;
         constexpr uint32_t bytes = kAttendSlice * D * (Q8 ? 1 : 2);  // of a slice
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int row = tc_row<P>(base + 16 * h + 8 * e + g8, rows);
-                        const int32_t rr = pc.rb * kTcRows + row, tok = rr / p.group;
+                        const int32_t rr = pc.rb * kTcRows + row, tok = kv_over_group(p, rr);
                         there[e] = row < rows;
                         src[e] = p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
                                  (int64_t)(pc.head * p.group + rr - tok * p.group) * D + (t4 & 1) * 16 + (t4 >> 1) * 8;
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
                 // the lane's row; where a quarter has two warps, half of its columns each
                 const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
                 const int row = tc_row<P>(lr, (int)rows);
-                const int32_t rr = pc.rb * kTcRows + row, tok = rr / p.group;
+                const int32_t rr = pc.rb * kTcRows + row, tok = kv_over_group(p, rr);
                 const uint16_t *src = p.q + (int64_t)(rq.q0 + tok) * p.q_stride +
                                       (int64_t)(pc.head * p.group + rr - tok * p.group) * D;
 #pragma unroll
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
             // where each lane's row is (of 16 or 32); the steps then ask the lanes
             const int64_t rows = min((int64_t)kTcRows, (int64_t)rq.qlen * p.group - (int64_t)pc.rb * kTcRows);
             const int mine = tc_row<P>(HALVES == 2 ? lr : base + lane % 16, (int)rows);
-            const int32_t rr = pc.rb * kTcRows + mine, tok = rr / p.group;
+            const int32_t rr = pc.rb * kTcRows + mine, tok = kv_over_group(p, rr);
             const int64_t src = mine < rows ? (int64_t)(rq.q0 + tok) * p.q_stride +
                                                   (int64_t)(pc.head * p.group + rr - tok * p.group) * D
                                             : -1;
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
                 const KvPiece &c = place.c;
                 nrows = (int32_t)min((int64_t)kTcRows, (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows);
                 row0 = c.rb * kTcRows;
-                i = (row0 + min(tc_row<P>(lr, nrows), nrows - 1)) / p.group;  // new token of TMEM lane lr's row
+                i = kv_over_group(p, row0 + min(tc_row<P>(lr, nrows), nrows - 1));  // new token of TMEM lane lr's row
                 kb = (r.tile0 + c.ja) * kAttendTile;
                 tiles = c.jb - c.ja;
                 keys = r.kv;
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
             }
             // the keys of the tile at kb that row `row` of the block sees
             const auto seen_by = [&](int row, uint32_t here) -> uint64_t {
-                const int32_t tok = (row0 + min(tc_row<P>(row, nrows), nrows - 1)) / p.group;
+                const int32_t tok = kv_over_group(p, row0 + min(tc_row<P>(row, nrows), nrows - 1));
                 return kv_seen64(p, keys, past, kv_row_view<PLACED>(p, place.r, tok), kb, here) >> (2 * t4);
             };
             const bool busy = tc_row<P>(base, nrows) < nrows;  // a warp without rows only keeps step
@@ -1118,11 +1118,6 @@ __global__ void __launch_bounds__(AttendTcCfg<D, Q8, kKvShared<P>>::kThreads,
                 const int64_t left = (int64_t)r.qlen * p.group - (int64_t)c.rb * kTcRows;
                 const bool whole = c.ja == 0 && c.jb == r.ntiles;
                 for (int row = lane; row < min((int64_t)kTcRows, left); row += 32) {
-                    const int32_t rr = c.rb * kTcRows + row, tok = rr / p.group;
-                    const uint16_t *q = p.q + (int64_t)(r.q0 + tok) * p.q_stride +
-                                        (int64_t)(c.head * p.group + rr - tok * p.group) * D;
-                    if (n > 0)
-                        for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
                     if constexpr (kKvShared<P>)
                         if (c.ja == 0) kv_note<kTcRows>(p, w, r, c, row, whole);
                 }

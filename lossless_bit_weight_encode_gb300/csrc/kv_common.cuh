@@ -87,6 +87,20 @@ struct KvAttendParams {
     uint64_t timeout_ns;
 };
 
+// n / d of 0 <= n < 2^31 as a product: with 2^(s - 1) < d <= 2^s, mul = ceil(2^(31 + s) / d) is
+// less than d / 2^(31 + s) too large, which moves the quotient by less than n / 2^31 / d < 1 / d.
+struct KvDivisor {
+    uint32_t mul, shift;
+};
+inline KvDivisor kv_divisor(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < d) ++s;
+    return {(uint32_t)(((uint64_t(1) << (31 + s)) + d - 1) / d), 31 + s};
+}
+__device__ __forceinline__ int32_t kv_over(int32_t n, const KvDivisor &d) {
+    return (int32_t)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
+}
+
 // A call with shared prefixes (w12_kv_attend_shared): its spans are the groups' prefixes and
 // then what the requests have of their own.  Where one kernel suits both they are one line of
 // units and one launch, else two.  No row is finished there: what a CTA has whole goes to
@@ -96,10 +110,17 @@ struct KvAttendParams {
 struct KvSharedParams : KvAttendParams {
     const int32_t *prefix_cu, *prefix_lens;
     int32_t groups;
+    KvDivisor by_group, by_page;
     float *row_part;  // [2][tokens * heads][head_dim]
     float2 *row_ml;   // [2][tokens * heads]
     int2 *row_info;   // [2][tokens * heads]
 };
+// Row over query heads per key head, token over page size.
+__device__ __forceinline__ int32_t kv_over_group(const KvAttendParams &p, int32_t n) { return n / p.group; }
+__device__ __forceinline__ int32_t kv_over_group(const KvSharedParams &p, int32_t n) { return kv_over(n, p.by_group); }
+__device__ __forceinline__ int32_t kv_over_page(const KvAttendParams &p, int32_t n) { return n / p.page_size; }
+__device__ __forceinline__ int32_t kv_over_page(const KvSharedParams &p, int32_t n) { return kv_over(n, p.by_page); }
+
 // What a launch has of the spans: all, the prefixes, or the own tokens (then it is the second).
 enum KvSpans { kKvAllSpans, kKvPrefixes, kKvOwnSpans };
 template <KvSpans KIND>
