@@ -843,11 +843,11 @@ int check_status(void *stream, std::string *err) {
             return W12_ERR_BUFFER_TOO_SMALL;
         }
         if (v & dev::kStatusKvPages) {
-            *err = "w12_kv_plan: the ring of free pages ran out, or had no room for pages given back" + word;
+            *err = "w12_kv_plan or w12_kv_fork: the ring of free pages ran out, or had no room for pages given back" + word;
             return W12_ERR_BUFFER_TOO_SMALL;
         }
         if (v & dev::kStatusKvIndex) {
-            *err = "w12_kv_store or w12_kv_read: a slot or a position outside its table" + word;
+            *err = "w12_kv_store, w12_kv_read or w12_kv_copy: a slot, a position or a page outside its table" + word;
             return W12_ERR_INVALID_ARG;
         }
         if (v & dev::kStatusKvSizes) {

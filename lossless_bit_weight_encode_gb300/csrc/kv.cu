@@ -198,7 +198,7 @@ int shared_call(const DeviceView &d, const w12_kv_cache &c, int rows, dev::KvSpa
 
 int shared_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_args &a, const w12_kv_prefix &x,
                 SharedPlan *plan, std::string *err) {
-    const int group = a.heads / c.kv_heads, max_new = std::max(a.max_new, 1);
+    const int group = a.heads / c.kv_heads, max_new = std::max(std::min(a.max_new, a.tokens), 1);
     const bool q8 = c.dtype == W12_KV_Q8;
     const int64_t together = std::min<int64_t>((int64_t)std::max(x.max_requests, 1) * max_new, a.tokens);
     plan->line[0].rows = attend_rows((int)together, group, c.kv_heads, x.groups, q8, d.sm_count);
@@ -225,7 +225,7 @@ int shared_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_
     plan->off_row = at;
     plan->off_row_ml = plan->off_row + up(rows * c.head_dim * sizeof(float));
     plan->off_info = plan->off_row_ml + up(rows * sizeof(float2));
-    plan->bytes = plan->off_info + up(rows * sizeof(int2));
+    plan->bytes = plan->off_info + up(rows * sizeof(int4));
     return W12_OK;
 }
 
@@ -582,9 +582,9 @@ int kv_attend_shared(const w12_kv_cache &c, const w12_kv_attend_args &a, const w
     p.groups = prefix.groups;
     p.row_part = reinterpret_cast<float *>(ws + plan.off_row);
     p.row_ml = reinterpret_cast<float2 *>(ws + plan.off_row_ml);
-    p.row_info = reinterpret_cast<int2 *>(ws + plan.off_info);
-    dev::KvSharedJoin join = {a.out,      a.lse,    a.out_stride, a.cu_new, a.tokens, a.heads,
-                              a.requests, p.row_part, p.row_ml,   p.row_info, {}};
+    p.row_info = reinterpret_cast<int4 *>(ws + plan.off_info);
+    dev::KvSharedJoin join = {a.out,    a.lse,    a.out_stride, a.cu_new, a.tokens, a.heads, a.requests,
+                              p.row_part, p.row_ml, p.row_info,   d.status, {}};
     CUtensorMap tm[2][2];
     for (int i = 0; i < plan.lines; ++i) {
         const bool tc = plan.line[i].rows == dev::kTcRows;
@@ -597,7 +597,7 @@ int kv_attend_shared(const w12_kv_cache &c, const w12_kv_attend_args &a, const w
         const SharedPlan::Line &l = plan.line[i];
         p.part = reinterpret_cast<float *>(ws + l.off_part);
         p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
-        join.line[i] = {p.part, p.part_ml, l.rows};
+        join.line[i] = {p.part, p.part_ml, l.rows, l.ctas};
         if (i == plan.lines) break;
         int resident = 0;
         rc = shared_call(d, c, l.rows, l.kind, &resident, &p, &tm[i][0], &tm[i][1], l.ctas, stream, err);

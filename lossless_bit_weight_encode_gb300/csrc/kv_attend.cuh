@@ -540,18 +540,20 @@ __device__ __forceinline__ KvParts kv_parts(const KvAttendParams &p, const KvWal
 template <int ROWS, class P>
 __device__ __forceinline__ void kv_note(const P &p, const KvWalk &w, const KvRequest &r, const KvPiece &c,
                                         int lr, bool whole) {
-    int2 info = make_int2(0, 1);
+    int4 info = make_int4(0, 1, r.kv, 0);
     if (!whole) {
         // the CTAs that have the block's first and last tile
         const int64_t span = r.ntiles + kKvBlockUnits, s0 = w.u - (w.u - w.start) % span;
         const int32_t c0 = (int32_t)(((s0 + kKvBlockUnits + 1) * w.ctas - 1) / w.total);
         const int32_t c1 = (int32_t)(((s0 + span) * w.ctas - 1) / w.total);
-        info = make_int2(2 * c0 * ROWS + lr, c1 - c0 + 1);
+        info.x = 2 * c0 * ROWS + lr, info.y = c1 - c0 + 1;
     }
     const int b = w.b + p.first_span() - p.groups;
     if (b >= 0) {
         const int shared = kv_shared_tokens(p, b);
-        if (shared > 0) info.y |= kKvSharesPrefix;
+        info.z = shared;
+        // in no group: nothing was computed of the prefix
+        if (shared > 0 && (b < p.prefix_cu[0] || b >= p.prefix_cu[p.groups])) info.x = -1;
         if (lr == 0 && shared != max(p.prefix_lens[b], 0)) atomicOr(p.status, kStatusKvSizes);
     }
     p.row_info[kv_row_at<ROWS>(p, w, r, c, lr)] = info;

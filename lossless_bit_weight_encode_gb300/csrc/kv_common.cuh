@@ -87,8 +87,9 @@ struct KvAttendParams {
     uint64_t timeout_ns;
 };
 
-// n / d of 0 <= n < 2^31 as a product: with 2^(s - 1) < d <= 2^s, mul = ceil(2^(31 + s) / d) is
-// less than d / 2^(31 + s) too large, which moves the quotient by less than n / 2^31 / d < 1 / d.
+// n / d of 0 <= n < 2^31 as a product: with 2^(s - 1) < d <= 2^s and mul = ceil(2^(31 + s) / d),
+// mul d is less than d above 2^(31 + s), which moves the quotient by less than
+// n / 2^(31 + s) < 1 / d.
 struct KvDivisor {
     uint32_t mul, shift;
 };
@@ -102,18 +103,17 @@ __device__ __forceinline__ int32_t kv_over(int32_t n, const KvDivisor &d) {
 }
 
 // A call with shared prefixes (w12_kv_attend_shared): its spans are the groups' prefixes and
-// then what the requests have of their own.  Where one kernel suits both they are one line of
-// units and one launch, else two.  No row is finished there: what a CTA has whole goes to
-// row_part and row_ml, and row_info says where a row's parts are: {row of its first part,
-// parts (1: whole; bit 30, of the own tokens: their request shares a prefix)}.  All three
-// have the prefixes' rows first, then the own ones'.
+// then what each request has of its own; a row block in one range leaves its rows' sums in
+// row_part and row_ml, and row_info says of every row {row of its first part, parts (1: whole),
+// tokens of the prefix, of the own ones: that the request shares}.  All three have the prefixes'
+// rows first, then the own ones'.
 struct KvSharedParams : KvAttendParams {
     const int32_t *prefix_cu, *prefix_lens;
     int32_t groups;
     KvDivisor by_group, by_page;
     float *row_part;  // [2][tokens * heads][head_dim]
     float2 *row_ml;   // [2][tokens * heads]
-    int2 *row_info;   // [2][tokens * heads]
+    int4 *row_info;   // [2][tokens * heads]
 };
 // Row over query heads per key head, token over page size.
 __device__ __forceinline__ int32_t kv_over_group(const KvAttendParams &p, int32_t n) { return n / p.group; }
@@ -129,7 +129,6 @@ struct KvSpanParams : KvSharedParams {
     // the first of the launch's spans among all
     __device__ __forceinline__ int32_t first_span() const { return KIND == kKvOwnSpans ? groups : 0; }
 };
-constexpr int32_t kKvSharesPrefix = 1 << 30;
 // What a row block costs beside its tiles (its q, the pipeline's start and end), in tiles:
 // the line counts that many units more for each, so that CTAs with many short blocks have
 // fewer of them.

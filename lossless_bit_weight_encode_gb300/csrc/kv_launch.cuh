@@ -214,7 +214,16 @@ int shared_kind(const DeviceView &d, int rows, int *resident, const dev::KvShare
                 const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     dev::KvSpanParams<KIND> spans;
     if (p) static_cast<dev::KvSharedParams &>(spans) = *p;
-    return attend_rows_variant<D, Q8>(d, rows, resident, p ? &spans : nullptr, tm_k, tm_v, ctas, stream, err);
+    const auto *q = p ? &spans : nullptr;
+    // of two launches the prefixes' has the larger row tile
+    if constexpr (KIND == dev::kKvPrefixes)
+        if (rows != 16) return attend_tc_variant<D, Q8, false>(d, resident, q, tm_k, tm_v, ctas, stream, err);
+    if constexpr (KIND == dev::kKvOwnSpans)
+        if (rows != 16) return attend_variant<D, Q8, 4, 1, 1>(d, resident, q, tm_k, tm_v, ctas, stream, err);
+    if constexpr (KIND != dev::kKvAllSpans)
+        return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(d, resident, q, tm_k, tm_v,
+                                                                                          ctas, stream, err);
+    else return attend_rows_variant<D, Q8>(d, rows, resident, q, tm_k, tm_v, ctas, stream, err);
 }
 
 }  // namespace launch

@@ -25,11 +25,12 @@ struct KvSharedJoin {
     int32_t tokens, heads, requests;
     const float *row_part;
     const float2 *row_ml;
-    const int2 *row_info;
+    const int4 *row_info;
+    uint32_t *status;
     struct Line {
         const float *part;
         const float2 *part_ml;
-        int32_t rows;  // of a row block
+        int32_t rows, ctas;  // of a row block, of the launch
     } line[2];  // of the prefixes, of the own tokens
 };
 
@@ -46,9 +47,19 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const 
     pdl_wait();
     // rows of no request have no note
     if (tok >= min(p.tokens, p.cu_new[p.requests]) || tok < p.cu_new[0]) return;
-    int2 prefix = __ldcg(&p.row_info[row]), own = __ldcg(&p.row_info[own_rows + row]);
-    if (!(own.y & kKvSharesPrefix)) prefix.y = 0;
-    own.y &= ~kKvSharesPrefix;
+    int4 prefix = __ldcg(&p.row_info[row]), own = __ldcg(&p.row_info[own_rows + row]);
+    // a group whose requests share different numbers of tokens, or a row that no group or
+    // request has (a cu that is no prefix sum): what is there then may be anything
+    const auto fits = [&](const int4 &i, const KvSharedJoin::Line &l) {
+        return i.y == 1 || (i.x >= 0 && i.y > 1 && i.y <= l.ctas &&
+                            i.x + (int64_t)(2 * i.y - 1) * l.rows <= (int64_t)2 * l.ctas * l.rows);
+    };
+    if (own.z <= 0) prefix.y = 0;
+    else if (prefix.z != own.z || !fits(prefix, p.line[0])) own.x = -1;
+    if (own.x < 0 || !fits(own, p.line[1])) {
+        prefix.y = own.y = 0;
+        if (lane == 0) atomicOr(p.status, kStatusKvSizes);
+    }
     const int32_t n0 = prefix.y, n = n0 + own.y;
     float acc[V] = {}, mm = -INFINITY, sum = 0.0f;
     for (int32_t k0 = 0; k0 < n; k0 += U) {
@@ -59,7 +70,7 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const 
             const int32_t kk = min(k0 + u, n - 1);
             const bool mine = kk >= n0;
             const int32_t k = mine ? kk - n0 : kk;
-            const int2 info = mine ? own : prefix;
+            const int4 info = mine ? own : prefix;
             const KvSharedJoin::Line &l = p.line[mine];
             const bool whole = info.y == 1;
             // the first CTA's part is in its second slot, every other one's in its first

@@ -209,6 +209,34 @@ def test_many_groups():
     compare(shared_case(groups, 16, 1, 64, 16, True, 11))
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dim,heads,kv_heads,new", [(64, 24, 8, 1), (128, 24, 8, 1), (128, 40, 2, 2), (256, 24, 4, 3)])
+def test_many_short_requests(dim, heads, kv_heads, new, q8):
+    """Several row blocks in every range, most of them shorter than a tile."""
+    rng = random.Random(dim + new)
+    members = [(rng.choice([0, 1, 15, 16, 47, 48, 60, 63, 64, 65, 130]), rng.choice([0, new, new])) for _ in range(230)]
+    compare(shared_case([(5, members), (0, members[:40]), (1, members[40:80])], heads, kv_heads, dim, 16, q8, 21))
+
+
+@pytest.mark.parametrize("dim,heads", [(128, 6), (64, 3), (256, 4)])
+def test_values_that_are_not_finite_among_drafted_tokens(dim, heads):
+    """Infinities in keys' values that only some rows of a tile see, in pieces with and without
+    them by turns, for row blocks behind one another in a range."""
+    rng = random.Random(dim)
+    members = [(rng.randrange(0, 50), rng.choice([1, 3])) for _ in range(200)]
+    case = shared_case([(2, members)], heads * 4, 4, dim, 16, False, 22)
+    cache, tables, lens, cu, q, step = case
+    clean, _ = run(cache, q, step)
+    want = clean.double().view(-1, heads * 4, dim).clone()
+    for b in range(0, 200, 3):
+        at = lens[b] + cu[b + 1] - cu[b] - 1  # the last new token: the earlier ones do not see it
+        bad = float("inf") if b % 2 else float("-inf")
+        cache.v[int(tables[b, at // 16]), b % 4, at % 16, b % dim] = bad
+        want[cu[b + 1] - 1, b % 4 * heads:(b % 4 + 1) * heads, b % dim] = bad
+    out, _ = run(cache, q, step)
+    assert torch.equal(out.double().view(want.shape), want)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_shapes(seed):
     rng = random.Random(seed)
@@ -243,6 +271,30 @@ def test_prefixes_that_do_not_fit_are_cut_and_reported(what):
         assert e.value.status == 2
     want = attend_ref(q, cache, tables, total, cu, None, 0, 0.125, 2)
     check_attend(out, want[1], want)
+
+
+@pytest.mark.parametrize("heads,q8", [(4, False), (40, False), (40, True), (32, True)])
+@pytest.mark.parametrize("what", ["another length", "no group"])
+def test_requests_that_do_not_fit_their_group(what, heads, q8):
+    """They get zeros and are reported; the others are right."""
+    case = shared_case([(3, [(20, 1), (7, 1), (33, 1)]), (2, [(20, 1)] * 4)], heads, 2, 64, 16, q8, 23)
+    cache, tables, total, cu, q, step = case
+    if what == "another length":
+        step.prefix.lens = dev([48, 32, 48, 32, 32, 32, 32], torch.int32)
+        bad = [1]
+    else:
+        step.prefix.cu = dev([0, 3, 5], torch.int32)
+        bad = [5, 6]
+    lse = torch.zeros(7, heads, device="cuda")
+    out = cache.attend(q.view(7, -1), step, lse=lse)
+    torch.cuda.synchronize()
+    with pytest.raises(w12.W12Error) as e:
+        w12.w12_check_status()
+    assert e.value.status == 2
+    want = attend_ref(q, cache, tables, total, cu, None, 0, 0.125, heads // 2)
+    good = [b for b in range(7) if b not in bad]
+    assert (out[bad] == 0).all() and (lse[bad] == float("-inf")).all()
+    check_attend(out[good], lse[good], tuple(w[good] for w in want))
 
 
 def test_streams_graphs_and_workspaces():
