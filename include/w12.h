@@ -593,10 +593,11 @@ int w12_kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, c
  * w12_kv_attend where requests share a prefix: the keys and values of a group's prefix are
  * read once for the new tokens of all its requests, then each request's own.  The result
  * is that of w12_kv_attend (with other splits of the sums).  Group g has requests cu[g] ..
- * cu[g + 1] - 1 (cu[groups + 1], cu[0] = 0, cu[groups] = requests); lens[b] (int32
+ * cu[g + 1] - 1 (cu[groups + 1], cu[0] = 0, cu[groups] = requests, else w12_check_status returns
+ * SHAPE and a request in no group whose lens is not 0 has any result); lens[b] (int32
  * [requests]): the tokens that request b shares with its group, 0: none.  Within a group
  * the lens that are not 0 are the same (else a request that differs from the first has zeros
- * for results, and so has one in no group; w12_check_status returns SHAPE), a multiple of
+ * for results, and w12_check_status returns SHAPE), a multiple of
  * page_size (else rounded down) and at most args->lens[b] (else clamped, SHAPE); the leading
  * lens / page_size table entries of those requests are the same too: the first one's are
  * read.  max_requests: the most requests of a group, as far as the caller knows; it picks

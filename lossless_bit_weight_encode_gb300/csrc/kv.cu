@@ -583,8 +583,8 @@ int kv_attend_shared(const w12_kv_cache &c, const w12_kv_attend_args &a, const w
     p.row_part = reinterpret_cast<float *>(ws + plan.off_row);
     p.row_ml = reinterpret_cast<float2 *>(ws + plan.off_row_ml);
     p.row_info = reinterpret_cast<int4 *>(ws + plan.off_info);
-    dev::KvSharedJoin join = {a.out,    a.lse,    a.out_stride, a.cu_new, a.tokens, a.heads, a.requests,
-                              p.row_part, p.row_ml, p.row_info,   d.status, {}};
+    dev::KvSharedJoin join = {a.out,      a.lse,         a.out_stride, a.cu_new, prefix.cu,  a.tokens, a.heads,
+                              a.requests, prefix.groups, p.row_part,   p.row_ml, p.row_info, d.status, {}};
     CUtensorMap tm[2][2];
     for (int i = 0; i < plan.lines; ++i) {
         const bool tc = plan.line[i].rows == dev::kTcRows;

@@ -552,8 +552,6 @@ __device__ __forceinline__ void kv_note(const P &p, const KvWalk &w, const KvReq
     if (b >= 0) {
         const int shared = kv_shared_tokens(p, b);
         info.z = shared;
-        // in no group: nothing was computed of the prefix
-        if (shared > 0 && (b < p.prefix_cu[0] || b >= p.prefix_cu[p.groups])) info.x = -1;
         if (lr == 0 && shared != max(p.prefix_lens[b], 0)) atomicOr(p.status, kStatusKvSizes);
     }
     p.row_info[kv_row_at<ROWS>(p, w, r, c, lr)] = info;

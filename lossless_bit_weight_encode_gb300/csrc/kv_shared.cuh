@@ -22,7 +22,8 @@ struct KvSharedJoin {
     float *lse;
     int64_t out_stride;
     const int32_t *cu_new;
-    int32_t tokens, heads, requests;
+    const int32_t *prefix_cu;
+    int32_t tokens, heads, requests, groups;
     const float *row_part;
     const float2 *row_ml;
     const int4 *row_info;
@@ -39,20 +40,23 @@ struct KvSharedJoin {
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const __grid_constant__ KvSharedJoin p) {
     constexpr int W = kJoinThreads / 32, V = D / 32;  // columns of a lane
-    constexpr int U = V == 8 ? 4 : 8;                 // parts whose loads are in flight
+    constexpr int U = 8;                              // parts whose loads are in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * W + warp, own_rows = (int64_t)p.tokens * p.heads;
     const int32_t tok = (int32_t)(row / p.heads), h = (int32_t)(row - (int64_t)tok * p.heads);
     pdl_launch_dependents();
     pdl_wait();
-    // rows of no request have no note
-    if (tok >= min(p.tokens, p.cu_new[p.requests]) || tok < p.cu_new[0]) return;
+    if (row == 0 && lane == 0 && (p.prefix_cu[0] != 0 || p.prefix_cu[p.groups] != p.requests))
+        atomicOr(p.status, kStatusKvSizes);
+    if (row >= own_rows) return;
     int4 prefix = __ldcg(&p.row_info[row]), own = __ldcg(&p.row_info[own_rows + row]);
+    // rows of no request have no note
+    if (tok >= __ldcg(&p.cu_new[p.requests]) || tok < __ldcg(&p.cu_new[0])) return;
     // a group whose requests share different numbers of tokens, or a row that no group or
     // request has (a cu that is no prefix sum): what is there then may be anything
     const auto fits = [&](const int4 &i, const KvSharedJoin::Line &l) {
-        return i.y == 1 || (i.x >= 0 && i.y > 1 && i.y <= l.ctas &&
-                            i.x + (int64_t)(2 * i.y - 1) * l.rows <= (int64_t)2 * l.ctas * l.rows);
+        return i.y == 1 || ((uint32_t)(i.y - 1) < (uint32_t)l.ctas &&
+                            (uint32_t)i.x <= (uint32_t)((2 * (l.ctas - i.y) + 1) * l.rows));
     };
     if (own.z <= 0) prefix.y = 0;
     else if (prefix.z != own.z || !fits(prefix, p.line[0])) own.x = -1;
