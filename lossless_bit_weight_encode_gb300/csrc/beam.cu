@@ -85,7 +85,8 @@ int beam_select(const w12_beam_args &a, void *workspace, size_t ws_bytes, void *
     p.eos = a.eos;
     p.parts = plan.parts;
     p.part = plan.part;
-    p.per_row_inv = (uint32_t)(((uint64_t(1) << 32) + (uint64_t)plan.parts * plan.keep - 1) / ((uint64_t)plan.parts * plan.keep));
+    const uint64_t per_row = (uint64_t)plan.parts * plan.keep;
+    p.per_row_inv = (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row);
     const int smem = (int)sizeof(dev::BeamShared) + a.beams * plan.parts;
     const auto kernel = a.dtype == W12_BEAM_BF16 ? &dev::w12_beam_select_kernel<true, 32>
                                                  : &dev::w12_beam_select_kernel<false, 16>;

@@ -491,9 +491,13 @@ int kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, const
     p.heads_inv = ~uint64_t(0) / (uint64_t)c.kv_heads;
     p.pairs_inv = ~uint64_t(0) / (uint64_t)pairs;
     p.status = d.status;
-    const auto kernel = c.head_dim == 64    ? q8 ? &dev::w12_kv_copy_kernel<64, true> : &dev::w12_kv_copy_kernel<128, false>
-                        : c.head_dim == 128 ? q8 ? &dev::w12_kv_copy_kernel<128, true> : &dev::w12_kv_copy_kernel<256, false>
-                                            : q8 ? &dev::w12_kv_copy_kernel<256, true> : &dev::w12_kv_copy_kernel<512, false>;
+    const int row = c.head_dim * (q8 ? 1 : 2);  // bytes
+    const auto kernel = q8 ? row == 64    ? &dev::w12_kv_copy_kernel<64, true>
+                             : row == 128 ? &dev::w12_kv_copy_kernel<128, true>
+                                          : &dev::w12_kv_copy_kernel<256, true>
+                        : row == 128 ? &dev::w12_kv_copy_kernel<128, false>
+                        : row == 256 ? &dev::w12_kv_copy_kernel<256, false>
+                                     : &dev::w12_kv_copy_kernel<512, false>;
     for (int32_t i0 = 0; i0 < count; i0 += dev::kCopyCaches) {
         const int32_t n = std::min(count - i0, dev::kCopyCaches);
         for (int32_t i = 0; i < n; ++i) {
@@ -607,8 +611,8 @@ int kv_attend_shared(const w12_kv_cache &c, const w12_kv_attend_args &a, const w
     const auto kernel = c.head_dim == 64    ? &dev::w12_kv_join_shared_kernel<64>
                         : c.head_dim == 128 ? &dev::w12_kv_join_shared_kernel<128>
                                             : &dev::w12_kv_join_shared_kernel<256>;
-    const cudaError_t e = kv_launch(d, kernel, dim3((unsigned)((rows + per - 1) / per)), dev::kJoinThreads, 0, 1, stream,
-                                    join);
+    const cudaError_t e =
+        kv_launch(d, kernel, dim3((unsigned)((rows + per - 1) / per)), dev::kJoinThreads, 0, 1, stream, join);
     if (e != cudaSuccess) return kv_cuda_fail(e, "w12_kv_attend_shared join launch", err);
     return W12_OK;
 }

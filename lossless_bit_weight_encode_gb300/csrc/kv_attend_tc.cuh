@@ -31,6 +31,12 @@
 // scores, weights and product, of which two CTAs per SM overlap two.  30 rows of 64
 // requests of 8000: BF16 320 us, 6.6 TB/s, Q8 332.  72 rows of 256 columns, two of
 // 100001: BF16 128 us, Q8 107.
+//
+// Behind shared prefixes (w12_kv_attend_shared; kv_shared.cuh) pieces are many and short, and
+// what a piece costs beside its tiles counts: a warp of its own finds their places and writes
+// the joining kernel's notes, a piece's Q is loaded before the last softmax of the one before,
+// few rows are spread over all softmax warps, and parts go out four lanes to a row.  A piece of
+// four tiles took 6.7 us with none of this and takes 4.5; a tile takes 0.55 to 0.7.
 #pragma once
 
 #include "kv_attend.cuh"
@@ -56,17 +62,19 @@ struct AttendTcCfg {
     // tile's products read it again (128 columns, BF16: 96 us from TMEM, 102 from shared
     // memory, for the trees above) and where it takes the room of ring slots.  Only the
     // 8-bit cache of 128 columns has no columns left: its two CTAs per SM are worth more
-    // (117 us; one CTA with Q in TMEM 116, but 404 against 365 at 64000 tokens).
+    // (117 us; one CTA with Q in TMEM 116, but 404 against 365 at 64000 tokens).  Behind shared
+    // prefixes, where the rows of a block are spread over all softmax warps, one CTA with
+    // three operand buffers is (8 groups of 48 rows: 57.3 us against 61.4 at 6000 tokens, 217
+    // against 210 at 40000; 4 of 96 rows at 40000 133 against 144).
     static constexpr bool kQTmem = !Q8 || D != 128 || SHARED;
     // One CTA per SM or two (with half of TMEM each).
     static constexpr bool kOne = D == 256 || (D == 128 && kQTmem);
     // Score buffers, and how many tiles the scores are made ahead of the products.
     static constexpr int kS = D == 128 && kQTmem ? 4 : 2, kAheadS = kS / 2;
     // Softmax warps, then two loaders, the MMA warp (and one that idles, or with shared
-    // prefixes finds the places), the converters
-    // in groups of four.  Where one CTA has the SM, eight softmax warps (16 rows each)
-    // shorten the way from scores to weights; where two share it, four (32 rows each, 16
-    // at a time) fill it as well and leave the registers.  72 rows of 256 columns, two
+    // prefixes finds the pieces' places), the converters in groups of four.  Where one CTA
+    // has the SM, eight softmax warps (16 rows each) shorten the way from scores to weights;
+    // where two share it, four (32 rows each, 16 at a time) fill it as well and leave the registers.  72 rows of 256 columns, two
     // requests of 100001: 127 us with eight, 133 with four; 96 rows of 128, the 8-bit
     // trees: 122 and 116.  Keys and values have a group of converters each where there
     // are threads for it (256 columns, 8-bit: 107 us, 140 with one group and one operand

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(1024, 1) w12_kv_fork_kernel(const __grid_const
 
     // ------------------------------------------------------------ places in the ring
     const int32_t avail = clamp_i32(tail - head, 0, p.ring_size), room = p.ring_size - avail;
-    const int32_t head_at = ring_base(head, p.ring_size, p.ring_inv), tail_at = ring_base(tail, p.ring_size, p.ring_inv);
+    const int32_t head_at = ring_base(head, p.ring_size, p.ring_inv);
+    const int32_t tail_at = ring_base(tail, p.ring_size, p.ring_inv);
     if (tail - head != avail) flags |= kStatusKvPages;
     int32_t before = 0, all = 0, here = 1;  // pages freed before these columns, in all, and here (0: none)
     if (STEP == 2) {

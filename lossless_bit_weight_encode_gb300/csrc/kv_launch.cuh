@@ -126,8 +126,8 @@ int attend_dim(const DeviceView &d, bool q8, int rows, int *resident, const dev:
 // its launch.  regs > 0: the registers per thread it has to have been compiled to.
 template <class P>
 int attend_kernel(const DeviceView &d, void (*kernel)(P, CUtensorMap, CUtensorMap), int most, int threads, int regs,
-                  int smem, std::mutex &mu, int *per_sm, int *resident, const P *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas,
-                         void *stream, std::string *err) {
+                  int smem, std::mutex &mu, int *per_sm, int *resident, const P *p, const CUtensorMap *tm_k,
+                  const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     if (d.device < 0 || d.device >= kKvMaxDevices) {
         *err = "device ordinal out of range";
         return W12_ERR_CUDA;
@@ -187,7 +187,8 @@ int attend_tc_variant(const DeviceView &d, int *resident, const P *p, const CUte
 // do with 16, but for 256 columns, whose sums for 16 rows do not fit a warp: there
 // they split the rows too.
 template <int D, bool Q8, class P>
-int attend_rows_variant(const DeviceView &d, int rows, int *resident, const P *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
+int attend_rows_variant(const DeviceView &d, int rows, int *resident, const P *p, const CUtensorMap *tm_k,
+                        const CUtensorMap *tm_v, int ctas, void *stream, std::string *err) {
     switch (rows) {
     case 8: return attend_variant<D, Q8, 4, 1, 1>(d, resident, p, tm_k, tm_v, ctas, stream, err);
     case 16:

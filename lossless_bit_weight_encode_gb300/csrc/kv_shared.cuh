@@ -7,9 +7,18 @@
 // once (32 beams of six query heads: 192 rows, on the tensor cores), and over what each
 // request has of its own, and leave the sums of every row's parts; this kernel joins them.
 //
-// What bounds the call: a prefix's bytes are read once per group instead of once per
-// request, so with many requests the prefix is bound by the products and the softmax of its
-// rows, and the rest by HBM.
+// BF16 caches take groups and requests as one line of units and one launch: the tcgen05 kernel
+// takes a tile of 64 keys in 0.6 us on each SM, faster than HBM brings it, however few of its
+// 128 rows are used (64 requests of 225 tokens behind 4000 36.9 us; the own tokens in a second
+// launch of 8-row tiles 46).  Of an 8-bit cache the conversion would be paid for few rows too:
+// there the own tokens are a second launch with tiles of their own rows (8 x 8 beams of 130
+// tokens behind 6000: 57 us, in one launch 79), which takes the SMs as the first one's CTAs
+// end.
+//
+// What bounds the call: a prefix's bytes are read once per group instead of once per request,
+// so with a long prefix of few rows it is HBM (16 samples behind 100000 tokens 87.7 us, 5.2
+// TB/s), with many rows the softmax of a tile, and with short own contexts what a piece
+// costs beside its tiles (kv_attend_tc.cuh).
 #pragma once
 
 #include "kv_attend.cuh"
@@ -36,7 +45,8 @@ struct KvSharedJoin {
 };
 
 // A warp per output row (token and head, heads fastest) takes its parts, first the prefix's in
-// range order, then the own ones.
+// range order, then the own ones; eight loads in flight (four: twenty trees over 256 columns,
+// eight parts a row, 50.5 us in all against 47.7).  2 us behind the last part.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const __grid_constant__ KvSharedJoin p) {
     constexpr int W = kJoinThreads / 32, V = D / 32;  // columns of a lane
@@ -53,7 +63,7 @@ __global__ void __launch_bounds__(kJoinThreads) w12_kv_join_shared_kernel(const 
     // rows of no request have no note
     if (tok >= __ldcg(&p.cu_new[p.requests]) || tok < __ldcg(&p.cu_new[0])) return;
     // a group whose requests share different numbers of tokens, or a row that no group or
-    // request has (a cu that is no prefix sum): what is there then may be anything
+    // request has (a cu that is no prefix sum): its note may be anything
     const auto fits = [&](const int4 &i, const KvSharedJoin::Line &l) {
         return i.y == 1 || ((uint32_t)(i.y - 1) < (uint32_t)l.ctas &&
                             (uint32_t)i.x <= (uint32_t)((2 * (l.ctas - i.y) + 1) * l.rows));

@@ -29,7 +29,8 @@ EXPORTED = (
     "w12_q8_encoded_size", "w12_q8_encode_host", "w12_q8_blob_info", "w12_q8_gemm_workspace_size", "w12_q8_gemm",
     "w12_q8_gemm_group_workspace_size", "w12_q8_gemm_group_launch_info", "w12_q8_gemm_group",
     "w12_kv_plan", "w12_kv_store", "w12_kv_read", "w12_kv_attend_workspace_size", "w12_kv_attend",
-    "w12_kv_fork_workspace_size", "w12_kv_fork", "w12_kv_copy", "w12_kv_attend_shared_workspace_size", "w12_kv_attend_shared",
+    "w12_kv_fork_workspace_size", "w12_kv_fork", "w12_kv_copy", "w12_kv_attend_shared_workspace_size",
+    "w12_kv_attend_shared",
     "w12_beam_workspace_size", "w12_beam_select",
     "w12_read_stream", "w12_check_status", "w12_selftest_timeout", "w12_set_option", "w12_get_option",
 )
