@@ -379,11 +379,15 @@ struct BeamTiles {
         return fmaxf(__uint_as_float(BF16 ? raw << 16 : raw) + 0.0f, -INFINITY);  // no NaN, no -0
     }
     // f(tile, its place in the part) for the thread's elements of each tile, the next one's
-    // loads in flight while one is worked on.
+    // loads in flight while one is worked on; `next`: the first one's.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
         BeamElems<BF16, E> next;
         next.load(base, t0, t1, vocab);
+        each(next, f);
+    }
+    template <class F>
+    __device__ __forceinline__ void each(BeamElems<BF16, E> &next, F f) const {
         for (int32_t a = t0; a < t1; a += TILE) {
             BeamElems<BF16, E> x = next;
             if (a + TILE < t1) next.load(base, a + TILE, t1, vocab);
@@ -440,9 +444,16 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
     const BeamTiles<BF16, E> tiles = {static_cast<const uint8_t *>(p.logits) + row * p.stride * (BF16 ? 2 : 4),
                                       p.allowed ? p.allowed + row * p.allowed_stride : nullptr, t0,
                                       min(t0 + p.part, p.vocab), p.vocab};
+    BeamElems<BF16, E> first;
+    first.load(tiles.base, t0, tiles.t1, p.vocab);
+    if (!isfinite(p.scores_in[row])) {  // a beam that does not go on
+        if (tid < p.keep) p.entries[(row * p.parts + part) * p.keep + tid] = BeamEntry{-INFINITY, -1};
+        if (tid == 0) p.stats[row * p.parts + part] = BeamStat{-INFINITY, 0, 0};
+        return;
+    }
     // the warp's largest logit so far, the thread's sum relative to it, the thread's largest
     float top = -INFINITY, sum = 0.0f, mine = -INFINITY;
-    tiles.each([&](const BeamElems<BF16, E> &x, int32_t at) {
+    tiles.each(first, [&](const BeamElems<BF16, E> &x, int32_t at) {
         const float own = x.top();
         mine = fmaxf(mine, own);
         s.tops[at / E + tid] = own;
@@ -766,13 +777,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamCtas) w12_beam_select_kerne
     const int32_t part = (int32_t)(blockIdx.x - row * p.parts), request = (int32_t)(row / p.beams);
     pdl_launch_dependents();
     pdl_wait();
-    if (isfinite(p.scores_in[row])) {
-        beam_part<BF16, E>(p, s, row, part);
-    } else {  // a beam that does not go on
-        BeamEntry *to = p.entries + (row * p.parts + part) * p.keep;
-        if (tid < p.keep) to[tid] = BeamEntry{-INFINITY, -1};
-        if (tid == 0) p.stats[row * p.parts + part] = BeamStat{-INFINITY, 0, 0};
-    }
+    beam_part<BF16, E>(p, s, row, part);
     __syncthreads();
     if (tid == 0) {
         const uint32_t all = (uint32_t)p.beams * (uint32_t)p.parts;
