@@ -157,6 +157,28 @@ def test_orders_that_are_not_random(kind, vocab, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [9000, 20011, 70003])
+@pytest.mark.parametrize("kind", ["random", "equal", "rising", "one tile", "mask"])
+def test_many_rows_of_several_tiles(kind, vocab, dtype):
+    """More rows than the device has places for, so that a block takes several tiles."""
+    n, b = 80, 8
+    at = torch.arange(vocab, device="cuda", dtype=torch.float64)
+    logits, scores, g = draw(n, b, vocab, dtype, vocab)
+    allowed = None
+    if kind == "equal":
+        logits.zero_()
+    elif kind == "rising":
+        logits.copy_((at / vocab * 40).expand_as(logits))
+    elif kind == "one tile":
+        logits[:, vocab - 700:] += 30  # all that counts in the last one
+    elif kind == "mask":
+        allowed = torch.rand(logits.shape, device="cuda", generator=g) < 0.01
+        allowed[:, :8200] = False  # a first tile without tokens
+        logits[~allowed] = float("inf")
+    run(logits, scores, allowed, eos=vocab - 1, exact=kind in ("equal", "rising"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_values_that_are_not_finite(dtype):
     logits, scores, _ = draw(5, 2, 5000, dtype, 8)
     low = torch.finfo(dtype).min
