@@ -193,10 +193,17 @@ __device__ __forceinline__ int32_t kv_shared_tokens(const KvSharedParams &p, int
     return kv_over_page(p, n) * p.page_size;
 }
 
-// The group's first request that shares a prefix (-1: none does).
+// The group's first request that shares a prefix, a page or more (-1: none does): mostly its
+// first one; then eight requests' loads at a time, for in a large group none may.
 __device__ __forceinline__ int kv_leader(const KvSharedParams &p, int b0, int b1) {
-    for (int b = b0; b < b1; ++b)
-        if (kv_shared_tokens(p, b) > 0) return b;
+    const auto shares = [&](int b) { return min(p.prefix_lens[b], p.lens[b]) >= p.page_size; };
+    if (b0 < b1 && shares(b0)) return b0;
+    for (; b0 < b1; b0 += 8) {
+        uint32_t some = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) some |= (uint32_t)shares(min(b0 + i, b1 - 1)) << i;
+        if (some) return min(b0 + __ffs((int)some) - 1, b1 - 1);
+    }
     return -1;
 }
 __device__ __forceinline__ void kv_group(const KvSharedParams &p, int g, int &b0, int &b1) {

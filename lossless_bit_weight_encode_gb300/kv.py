@@ -170,8 +170,9 @@ class KVStep:
 
 class KVPrefix:
     """Groups of requests with a common prefix: group g has requests ``cu[g] : cu[g + 1]``
-    (int32), request b shares its first ``lens[b]`` (int32, whole pages, 0: nothing) tokens
-    with its group; ``max_requests``: the most requests of a group, as far as is known.
+    (int32; together all requests), request b shares its first ``lens[b]`` (int32, whole pages,
+    0: nothing, else the same in all of the group) tokens with its group; ``max_requests``: the
+    most requests of a group, as far as is known.
     ``KVPages.fork`` fills ``lens``; for a prompt that was put in every request's table
     the caller does."""
 
@@ -272,7 +273,6 @@ class KVPages:
         if step.tables is not self.tables:
             step.tables = self.tables
         return step
-
 
     def fork(self, parents, lens, copies=None, prefix=None, lens_out=None, stream=None):
         """Request i goes on from request ``parents[i]`` (int32, -1: from none, it is empty
