@@ -204,8 +204,7 @@ int attend_rows_variant(const DeviceView &d, int rows, int *resident, const P *p
     }
 }
 
-// The same for calls with shared prefixes (kv_shared_*.cu), over one kind of spans: BF16
-// caches take all in one launch.
+// The same for calls with shared prefixes (kv_shared_*.cu), over one kind of spans.
 template <int D>
 int shared_dim(const DeviceView &d, bool q8, int rows, dev::KvSpans kind, int *resident, const dev::KvSharedParams *p,
                const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas, void *stream, std::string *err);
@@ -219,12 +218,14 @@ int shared_kind(const DeviceView &d, int rows, int *resident, const dev::KvShare
     // of two launches the prefixes' has the larger row tile
     if constexpr (KIND == dev::kKvPrefixes)
         if (rows != 16) return attend_tc_variant<D, Q8, false>(d, resident, q, tm_k, tm_v, ctas, stream, err);
+    // (BF16: with 9 to 16 rows as many requests take the tcgen05 kernel, in one launch)
     if constexpr (KIND == dev::kKvOwnSpans)
-        if (rows != 16) return attend_variant<D, Q8, 4, 1, 1>(d, resident, q, tm_k, tm_v, ctas, stream, err);
-    if constexpr (KIND != dev::kKvAllSpans)
+        if (!Q8 || rows != 16) return attend_variant<D, Q8, 4, 1, 1>(d, resident, q, tm_k, tm_v, ctas, stream, err);
+    if constexpr (KIND == dev::kKvPrefixes || (KIND == dev::kKvOwnSpans && Q8))
         return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(d, resident, q, tm_k, tm_v,
                                                                                           ctas, stream, err);
-    else return attend_rows_variant<D, Q8>(d, rows, resident, q, tm_k, tm_v, ctas, stream, err);
+    else if constexpr (KIND == dev::kKvAllSpans)
+        return attend_rows_variant<D, Q8>(d, rows, resident, q, tm_k, tm_v, ctas, stream, err);
 }
 
 }  // namespace launch

@@ -7,13 +7,11 @@
 // once (32 beams of six query heads: 192 rows, on the tensor cores), and over what each
 // request has of its own, and leave the sums of every row's parts; this kernel joins them.
 //
-// BF16 caches take groups and requests as one line of units and one launch: the tcgen05 kernel
-// takes a tile of 64 keys in 0.6 us on each SM, faster than HBM brings it, however few of its
-// 128 rows are used (64 requests of 225 tokens behind 4000 36.9 us; the own tokens in a second
-// launch of 8-row tiles 46).  Of an 8-bit cache the conversion would be paid for few rows too:
-// there the own tokens are a second launch with tiles of their own rows (8 x 8 beams of 130
-// tokens behind 6000: 57 us, in one launch 79), which takes the SMs as the first one's CTAs
-// end.
+// Groups and requests are one line of units and one launch where that serves both: the
+// tcgen05 kernel takes a BF16 tile of 64 keys in 0.6 us on each SM, faster than HBM brings it,
+// however few of its 128 rows are used.  Else (8-bit caches, very many requests; the rule is
+// in kv.cu) the own tokens are a second launch with tiles of their own rows, which takes the
+// SMs as the first one's CTAs end.
 //
 // What bounds the call: a prefix's bytes are read once per group instead of once per request,
 // so with a long prefix of few rows it is HBM (16 samples behind 100000 tokens 87.7 us, 5.2

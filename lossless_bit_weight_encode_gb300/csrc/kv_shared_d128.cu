@@ -8,10 +8,12 @@ template <>
 int shared_dim<128>(const DeviceView &d, bool q8, int rows, dev::KvSpans kind, int *resident,
                     const dev::KvSharedParams *p, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int ctas,
                     void *stream, std::string *err) {
-    const auto run = !q8                         ? &shared_kind<128, false, dev::kKvAllSpans>
-                     : kind == dev::kKvAllSpans ? &shared_kind<128, true, dev::kKvAllSpans>
-                     : kind == dev::kKvPrefixes ? &shared_kind<128, true, dev::kKvPrefixes>
-                                                : &shared_kind<128, true, dev::kKvOwnSpans>;
+    const auto run = kind == dev::kKvAllSpans ? q8 ? &shared_kind<128, true, dev::kKvAllSpans>
+                                                   : &shared_kind<128, false, dev::kKvAllSpans>
+                     : kind == dev::kKvPrefixes ? q8 ? &shared_kind<128, true, dev::kKvPrefixes>
+                                                     : &shared_kind<128, false, dev::kKvPrefixes>
+                     : q8                       ? &shared_kind<128, true, dev::kKvOwnSpans>
+                                                : &shared_kind<128, false, dev::kKvOwnSpans>;
     return run(d, rows, resident, p, tm_k, tm_v, ctas, stream, err);
 }
 
