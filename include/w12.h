@@ -602,7 +602,9 @@ int w12_kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, c
  * lens / page_size table entries of those requests are the same too: the first one's are
  * read.  max_requests: the most requests of a group, as far as the caller knows; it picks
  * the row tile and any value is correct.  args as w12_kv_attend, window 0 (INVALID_ARG
- * otherwise; a layer with a window reads no long prefix).
+ * otherwise; a layer with a window reads no long prefix).  Where the requests' keys and values
+ * are together, shared ones counted for each, below some 150 MB, w12_kv_attend, which reads
+ * them from L2, is the shorter call.
  * workspace: w12_kv_attend_shared_workspace_size bytes, 256-byte aligned, no initial
  * contents; not one that w12_kv_attend uses, whose counters have to stay zero.  Calls that
  * share one are ordered on the GPU; host threads may make them at the same time on one
