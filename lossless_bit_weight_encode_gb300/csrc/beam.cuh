@@ -23,8 +23,8 @@
 //
 // What bounds it: few rows the chain load, maximum, sum, selection, join (4 beams of 151936
 // BF16 logits 9.8 us, where the bytes take 0.2); many rows the instructions, 15 per 32 logits
-// (128 rows 21.2 us, 1.8 TB/s, half of all issue slots; the bytes take 5.8).  35 rows of
-// 50257 fp32 logits under a mask 13.4 us: four CTAs per SM begin at once, and what follows
+// (128 rows 20.9 us, 1.9 TB/s, half of all issue slots; the bytes take 5.8).  35 rows of
+// 50257 fp32 logits under a mask 13.1 us: four CTAs per SM begin at once, and what follows
 // the loads is as long as they are.
 #pragma once
 

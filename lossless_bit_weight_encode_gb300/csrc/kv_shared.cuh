@@ -14,7 +14,7 @@
 // SMs as the first one's CTAs end.
 //
 // What bounds the call: a prefix's bytes are read once per group instead of once per request,
-// so with a long prefix of few rows it is HBM (16 samples behind 100000 tokens 87.7 us, 5.2
+// so with a long prefix of few rows it is HBM (16 samples behind 100000 tokens 88 us, 5.2
 // TB/s), with many rows the softmax of a tile, and with short own contexts what a piece
 // costs beside its tiles (kv_attend_tc.cuh).
 #pragma once
