@@ -64,7 +64,7 @@ struct AttendTcCfg {
     // 8-bit cache of 128 columns has no columns left: its two CTAs per SM are worth more
     // (117 us; one CTA with Q in TMEM 116, but 404 against 365 at 64000 tokens).  Behind shared
     // prefixes, where the rows of a block are spread over all softmax warps, one CTA with
-    // three operand buffers is (8 groups of 48 rows: 57.3 us against 61.4 at 6000 tokens, 217
+    // four operand buffers is (8 groups of 48 rows: 57.3 us against 61.4 at 6000 tokens, 215
     // against 210 at 40000; 4 of 96 rows at 40000 133 against 144).
     static constexpr bool kQTmem = !Q8 || D != 128 || SHARED;
     // One CTA per SM or two (with half of TMEM each).
@@ -94,7 +94,7 @@ struct AttendTcCfg {
     static constexpr int kRawBytes = kAttendTile * D;       // K or V of a tile as bytes (Q8)
     static constexpr int kBlocks = D / 64;                  // 128-byte column blocks of an operand row
     // operand rings (filled by TMA, or by the converting warps) and byte rings
-    static constexpr int kOps = Q8 ? (D == 256 ? 2 : D == 128 && SHARED ? 3 : 1) : D == 64 ? 5 : D == 128 ? 6 : 3;
+    static constexpr int kOps = Q8 ? (D == 256 ? 2 : D == 128 && SHARED ? 4 : 1) : D == 64 ? 5 : D == 128 ? 6 : 3;
     static constexpr int kRaws = Q8 ? (D == 64 ? 6 : D == 128 && SHARED ? 4 : 2) : 0;
     // A slot of the ring of facts is written again after the softmax of its tile: the
     // loader is at most the byte ring, the operand ring and the score buffers ahead.
