@@ -125,7 +125,6 @@ __device__ __forceinline__ int32_t kv_over_page(const KvSharedParams &p, int32_t
 enum KvSpans { kKvAllSpans, kKvPrefixes, kKvOwnSpans };
 template <KvSpans KIND>
 struct KvSpanParams : KvSharedParams {
-    static constexpr KvSpans kind = KIND;
     // the first of the launch's spans among all
     __device__ __forceinline__ int32_t first_span() const { return KIND == kKvOwnSpans ? groups : 0; }
 };
