@@ -198,25 +198,18 @@ int shared_call(const DeviceView &d, const w12_kv_cache &c, int rows, dev::KvSpa
 
 int shared_plan(const DeviceView &d, const w12_kv_cache &c, const w12_kv_attend_args &a, const w12_kv_prefix &x,
                 SharedPlan *plan, std::string *err) {
-    const int group = a.heads / c.kv_heads, max_new = std::max(std::min(a.max_new, a.tokens), 1);
-    const bool q8 = c.dtype == W12_KV_Q8;
-    const int64_t together = std::min<int64_t>((int64_t)std::max(x.max_requests, 1) * max_new, a.tokens);
-    plan->line[0].rows = attend_rows((int)together, group, c.kv_heads, x.groups, q8, d.sm_count);
-    // The own tokens in a launch of their own, with their own row tile, for 8-bit caches, whose
-    // conversion would be paid for few rows too (8 x 8 beams of 130 tokens behind 6000: 57 us, in
-    // one launch 79), and for so many row blocks that the start and end of each in the tcgen05
-    // kernel weigh more than a second launch (48 heads over 8: 64 requests of 225 tokens 38
-    // against 35, 128 54 against 55, 256 of 100 tokens 68 against 88, 512 118 against 170).
-    const bool apart = q8 || (int64_t)a.requests * c.kv_heads >= 6 * (int64_t)d.sm_count;
-    plan->line[1].rows =
-        apart ? attend_rows(max_new, group, c.kv_heads, a.requests, q8, d.sm_count) : plan->line[0].rows;
-    plan->lines = plan->line[0].rows == plan->line[1].rows ? 1 : 2;
+    const int group = a.heads / c.kv_heads;
+    const SharedTiles tiles_of = shared_tiles(a.tokens, a.max_new, a.requests, x.groups, x.max_requests, group,
+                                              c.kv_heads, c.dtype == W12_KV_Q8, d.sm_count);
+    plan->lines = tiles_of.lines();
+    plan->line[0].rows = tiles_of.prefix;
+    plan->line[1].rows = tiles_of.own;
     const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     size_t at = 0;
     for (int i = 0; i < plan->lines; ++i) {
         SharedPlan::Line &l = plan->line[i];
         int resident = 0;
-        if (plan->lines == 2) l.kind = i == 0 ? dev::kKvPrefixes : dev::kKvOwnSpans;
+        l.kind = tiles_of.kind(i);
         const int rc = shared_call(d, c, l.rows, l.kind, &resident, nullptr, nullptr, nullptr, 0, nullptr, err);
         if (rc != W12_OK) return rc;
         // no more CTAs than tiles can exist

@@ -44,7 +44,6 @@
 namespace w12 {
 namespace dev {
 
-constexpr int kTcRows = 128;
 constexpr int kTcInfo = 16;  // ring of per-tile facts (present slices, scales)
 
 // A softmax warp's place: kept in shared memory, so that the loop over a piece's

@@ -3,6 +3,8 @@
 
 #include <cstdint>
 
+#include "kv_tiles.hpp"
+
 namespace w12 {
 namespace dev {
 
@@ -121,8 +123,6 @@ __device__ __forceinline__ int32_t kv_over_group(const KvSharedParams &p, int32_
 __device__ __forceinline__ int32_t kv_over_page(const KvAttendParams &p, int32_t n) { return n / p.page_size; }
 __device__ __forceinline__ int32_t kv_over_page(const KvSharedParams &p, int32_t n) { return kv_over(n, p.by_page); }
 
-// What a launch has of the spans: all, the prefixes, or the own tokens (then it is the second).
-enum KvSpans { kKvAllSpans, kKvPrefixes, kKvOwnSpans };
 template <KvSpans KIND>
 struct KvSpanParams : KvSharedParams {
     // the first of the launch's spans among all

@@ -11,6 +11,7 @@
 
 #include "kv_attend.cuh"
 #include "kv_attend_tc.cuh"
+#include "kv_tiles.hpp"
 #include "w12.h"
 #include "w12_launch.hpp"
 
@@ -53,22 +54,6 @@ cudaError_t kv_launch(const DeviceView &d, void (*kernel)(KArgs...), dim3 grid, 
 }
 
 constexpr int kKvMaxDevices = 64;
-
-// Rows of the tile a launch uses: new tokens times query heads per key head.  Up to
-// 8 the warp-level kernel, above 16 the tcgen05 kernel with 128 (more rows take
-// several row blocks).  30 rows measured 326 us against 532 with 32-row warp-level
-// tiles (64 requests of 8000 tokens, BF16; 8-bit 337 against 547), 128 against 133
-// for two requests of 100001.  Between 9 and 16 rows the warp-level kernel is the
-// shorter way for few row blocks (12 rows, one request of 777 tokens: 9.1 against
-// 10.6 us) and for 8-bit caches (64 x 8000: 325 against 340), the tcgen05 kernel for
-// as many blocks as SMs (64 x 8000, BF16: 315 against 343; windows of 1024: 76
-// against 81).
-inline int attend_rows(int max_new, int group, int kv_heads, int requests, bool q8, int sm_count) {
-    const int64_t rows = (int64_t)(max_new < 1 ? 1 : max_new) * group;
-    if (rows <= 8) return 8;
-    if (rows > 16 || (!q8 && (int64_t)kv_heads * requests >= sm_count)) return dev::kTcRows;
-    return 16;
-}
 
 // Workspace: the partial outputs, their maxima and sums, the counters.  The
 // first two have the same size in every plan of a device (kPartElems bounds rows x
@@ -215,17 +200,24 @@ int shared_kind(const DeviceView &d, int rows, int *resident, const dev::KvShare
     dev::KvSpanParams<KIND> spans;
     if (p) static_cast<dev::KvSharedParams &>(spans) = *p;
     const auto *q = p ? &spans : nullptr;
-    // of two launches the prefixes' has the larger row tile
-    if constexpr (KIND == dev::kKvPrefixes)
-        if (rows != 16) return attend_tc_variant<D, Q8, false>(d, resident, q, tm_k, tm_v, ctas, stream, err);
-    // (BF16: with 9 to 16 rows as many requests take the tcgen05 kernel, in one launch)
-    if constexpr (KIND == dev::kKvOwnSpans)
-        if (!Q8 || rows != 16) return attend_variant<D, Q8, 4, 1, 1>(d, resident, q, tm_k, tm_v, ctas, stream, err);
-    if constexpr (KIND == dev::kKvPrefixes || (KIND == dev::kKvOwnSpans && Q8))
-        return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(d, resident, q, tm_k, tm_v,
-                                                                                          ctas, stream, err);
-    else if constexpr (KIND == dev::kKvAllSpans)
+    if (shared_kernel_rows(KIND, Q8, rows) != rows) {
+        *err = "w12_kv_attend_shared has no kernel for a launch of " + std::to_string(rows) + "-row tiles";
+        return W12_ERR_CUDA;
+    }
+    if constexpr (KIND == dev::kKvAllSpans) {
         return attend_rows_variant<D, Q8>(d, rows, resident, q, tm_k, tm_v, ctas, stream, err);
+    } else {
+        if constexpr (shared_kernel_rows(KIND, Q8, dev::kTcRows) != 0)
+            if (rows == dev::kTcRows)
+                return attend_tc_variant<D, Q8, false>(d, resident, q, tm_k, tm_v, ctas, stream, err);
+        if constexpr (shared_kernel_rows(KIND, Q8, 8) != 0)
+            if (rows == 8) return attend_variant<D, Q8, 4, 1, 1>(d, resident, q, tm_k, tm_v, ctas, stream, err);
+        if constexpr (shared_kernel_rows(KIND, Q8, 16) != 0)
+            if (rows == 16)
+                return attend_variant<D, Q8, D == 256 ? 2 : 4, D == 256 ? 2 : 1, D == 256 ? 1 : 2>(
+                    d, resident, q, tm_k, tm_v, ctas, stream, err);
+        return W12_ERR_CUDA;  // (not reached)
+    }
 }
 
 }  // namespace launch
