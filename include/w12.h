@@ -627,7 +627,11 @@ int w12_kv_attend_shared(const w12_kv_cache *cache, const w12_kv_attend_args *ar
  * (BF16 or fp32, row i at i * logits_stride elements, aligned to an element).  With
  * M = max_v x_v over the tokens that count, token v of the row has the score
  *   scores_in[row] + ((x_v - M) - ln sum_v exp(x_v - M)),
- * compared in 64 bits, ties to the lower beam, then token.  Tokens that do not count:
+ * compared in 64 bits, ties to the lower beam, then token.  The sum's terms below the
+ * largest one are rounded to 32 bits: a score is within 4e-6 of this (mostly 2e-7), and
+ * candidates of different beams that are closer than that may change places.  A token that
+ * counts alone has the score scores_in[row], and rows whose x_v - M are the same numbers have
+ * the same sum.  Tokens that do not count:
  * those whose bit (v % 32 of word v / 32 of the row's words at allowed + row *
  * allowed_stride; allowed NULL: all have theirs; allowed_stride 0: one line for all rows) is 0,
  * and logits of -infinity or NaN.  Where M is +infinity, the tokens that have it share

@@ -9,12 +9,14 @@
 //
 // One launch.  A CTA takes one part of a row, tile by tile into registers (16-byte loads, the
 // next tile's in flight), for the maximum and the sum; the selection reads the few threads'
-// elements that may be among the best once more.  The parts' sums are relative to a
-// power of two 2^r, r = ceil(max log2(e)), with the exponent x log2(e) - r from two fused
-// multiply-adds (the constant in two pieces), and are added in 64-bit fixed point: the
-// joined sum does not depend on the parts' order and only the exponentials themselves
-// (2^-22, independent from element to element) are rounded, so that scores of different
-// beams compare right down to about 1e-8.  The selection's threshold is the smallest of
+// elements that may be among the best once more.  The threads' sums are relative to the warp's
+// largest logit so far, are added in 64-bit fixed point relative to the part's and the row's
+// largest one and do not depend on the parts' order.  The largest logit's own term is exactly
+// 1, and what is summed depends on differences from it alone: a token that alone counts has
+// the beam's score, and rows that differ by a constant compare as equal.  Every other term
+// carries 2^-22 of the exponential, a thread's sum its fp32 roundings (2^-24 of it for each of
+// some 20 additions) and a new maximum 2^-23: a score is within 4e-6 of the definition's if all
+// went the same way, and mostly within 2e-7.  The selection's threshold is the smallest of
 // as many thread groups' maxima as elements are kept: at least that many elements reach
 // it and, in random order, a few times that many; they are sorted by counting.  Where too many reach
 // it (a mask that leaves whole groups empty, equal logits), the exact one is found by
@@ -45,24 +47,31 @@ constexpr int kBeamFixed = 40;     // bits of the sums' fraction
 struct BeamStat {
     float top;      // largest logit of the part (-infinity: none)
     uint32_t pad;
-    uint64_t sum;   // of 2^(x log2(e) - beam_ref(top)), times 2^kBeamFixed
+    uint64_t sum;   // of exp(x - top), times 2^kBeamFixed
 };
 struct BeamEntry {
     float x;
     int32_t token;  // -1: none
 };
 
-// log2 of a positive whole number, to 1e-9.  x = 2^k f with 1 <= f < 2; of f's first six bits
-// c is about 1 / f, in eight bits, so that t = f c - 1 is small (2^-6) and exact, and
+// log2 of a positive whole number, to 3e-9.  x = 2^k f with 1 <= f < 2; of f's first six bits
+// c is about 1 / f, in eight bits (1 for the first ones: a power of two's is exact), so that
+// t = f c - 1 is small (2^-6) and exact, and
 // log2(f) = log2(1 / c) + log2(1 + t), the first from a table and the second from its series,
 // in 32 bits (2^-24 of 2^-6).
+// exp(-d) for d > 0, to 1e-9 (in what beam_scaled does with it): -d log2(e) = n / 64 + t with n
+// whole and t within 1 / 128, 2^(n mod 64 / 64) from a table, 2^t - 1 from its series in 32 bits.
 struct BeamLog {
     double log[64];
+    uint32_t power[64];    // 2^(i / 64) times 2^31
     uint16_t inverse[64];  // c times 256
-    constexpr BeamLog() : log(), inverse() {
+    constexpr BeamLog() : log(), power(), inverse() {
         for (int i = 0; i < 64; ++i) {
+            double term = 1, whole = 0;  // exp(i ln(2) / 64)
+            for (int n = 1; n < 30; ++n) whole += term, term *= i / 64.0 * 0.69314718055994530942 / n;
+            power[i] = (uint32_t)(whole * 2147483648.0 + 0.5);
             // 256 / (1 + (i + 0.5) / 64)
-            inverse[i] = (uint16_t)((2 * 256 * 64 * 2 + (2 * i + 1 + 128)) / (2 * (2 * i + 1 + 128)));
+            inverse[i] = i == 0 ? 256 : (uint16_t)((2 * 256 * 64 * 2 + (2 * i + 1 + 128)) / (2 * (2 * i + 1 + 128)));
             // ln(256 / c) = 2 atanh(z)
             const double x = 256.0 / inverse[i], z = (x - 1) / (x + 1);
             double power = z, sum = 0;
@@ -91,13 +100,7 @@ struct BeamParams {
     BeamLog logs;         // (parameters are near; one lane's loads of a table in memory are not)
 };
 
-// Exponent that a part's sum is relative to, in powers of two.  Where the integer nearest
-// to the largest logit is no exact float any more, that logit itself.
-__device__ __forceinline__ bool beam_plain(float top) { return fabsf(top) <= 1048576.0f; }
 constexpr float kLog2E = 1.44269504f, kLog2ELow = 1.92596303e-8f;  // log2(e) - kLog2E
-__device__ __forceinline__ double beam_ref(float top) {
-    return beam_plain(top) ? (double)ceilf(top * kLog2E) : (double)top * 1.4426950408889634;
-}
 
 // Larger value, larger number (no NaN, no -0).
 __device__ __forceinline__ uint32_t beam_order(float x) {
@@ -313,40 +316,49 @@ __device__ __forceinline__ void beam_limit(BeamShared &s, int32_t keep, int widt
     }
 }
 
+// exp(from - to) = 2^(n / 64) (1 + p) for from < to; false where that is below 2^-62.
+__device__ __forceinline__ bool beam_power(float from, float to, int32_t &n, float &p) {
+    const float d = from - to;
+    if (!(d > -43.0f)) return false;
+    const float part = d - from, low = (from - (d - part)) - (to + part);  // d and low are the difference
+    const float whole = rintf(d * (64.0f * kLog2E));
+    float t = fmaf(d, kLog2E, whole * -0.015625f);
+    t = fmaf(low, kLog2E, fmaf(d, kLog2ELow, t));
+    p = t * (0.69314718f + t * (0.24022651f + t * 0.05550411f));
+    n = (int32_t)whole;
+    return true;
+}
+// A sum relative to the logit `from` as one relative to `to`, at least as large.
+__device__ __forceinline__ uint64_t beam_scaled(const BeamLog &table, uint64_t v, float from, float to) {
+    int32_t n;
+    float p;
+    if (from == to) return v;
+    if (!beam_power(from, to, n, p)) return 0;
+    const uint64_t y = __umul64hi(v, (uint64_t)table.power[n & 63] << 32);  // v 2^(n mod 64 / 64) / 2
+    return (y + (uint64_t)__float2ll_rn((float)y * p)) << 1 >> -(n >> 6);
+}
+__device__ __forceinline__ float beam_scaled(const BeamLog &table, float v, float from, float to) {
+    int32_t n;
+    float p;
+    if (!beam_power(from, to, n, p)) return 0.0f;
+    const float y = v * ((float)table.power[n & 63] * 4.656612873077393e-10f);  // 2^-31
+    return fmaf(y, p, y) * __int_as_float(((n >> 6) + 127) << 23);
+}
+
 // Adds a part's sum (largest logit t) to that of others (largest logit top).
-__device__ __forceinline__ void beam_add(float &top, uint64_t &sum, float t, uint64_t y) {
+__device__ __forceinline__ void beam_add(const BeamLog &table, float &top, uint64_t &sum, float t, uint64_t y) {
     const float m = fmaxf(top, t);
-    const auto scaled = [&](float from, uint64_t v) -> uint64_t {
-        if (from == m) return v;
-        if (v == 0 || m == INFINITY || from == -INFINITY) return 0;
-        if (beam_plain(from) && beam_plain(m)) {  // whole powers of two apart
-            const float d = ceilf(m * kLog2E) - ceilf(from * kLog2E);
-            return d >= 64.0f ? 0 : v >> (int)d;
-        }
-        const double d = beam_ref(m) - beam_ref(from);
-        return d >= 64.0 ? 0 : (uint64_t)((double)v * exp2(-d));
-    };
-    sum = scaled(top, sum) + scaled(t, y);
+    sum = beam_scaled(table, sum, top, m) + beam_scaled(table, y, t, m);
     top = m;
 }
 
 // The lanes' sums together, for all of them.
-__device__ __forceinline__ void beam_total(float &top, uint64_t &sum) {
+__device__ __forceinline__ void beam_total(const BeamLog &table, float &top, uint64_t &sum) {
     const float most = beam_value(__reduce_max_sync(~0u, beam_order(top)));
-    if (__all_sync(~0u, beam_plain(top) || top == -INFINITY) && most > -INFINITY) {  // whole powers of two apart
-        const int32_t r = top == -INFINITY ? -(1 << 24) : (int32_t)ceilf(top * kLog2E);
-        const int32_t d = __reduce_max_sync(~0u, r) - r;
-        sum = d >= 64 ? 0 : sum >> d;
+    sum = beam_scaled(table, sum, top, most);
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += beam_shfl(sum, x);
-        top = most;
-        return;
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
-        const float t = __shfl_xor_sync(~0u, top, x);
-        beam_add(top, sum, t, beam_shfl(sum, x));
-    }
+    for (int x = 16; x > 0; x >>= 1) sum += beam_shfl(sum, x);
+    top = most;
 }
 
 __device__ __forceinline__ double beam_log2(const BeamLog &table, uint64_t x) {
@@ -459,33 +471,24 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
         s.tops[at / E + tid] = own;
         const float most = fmaxf(top, beam_value(__reduce_max_sync(~0u, beam_order(own))));
         if (most != top) {  // the same for the warp
-            if (sum > 0.0f) {
-                if (most == INFINITY) sum = 0.0f;
-                else if (beam_plain(top) && beam_plain(most))
-                    sum *= beam_ex2(ceilf(top * kLog2E) - ceilf(most * kLog2E));
-                else sum *= (float)exp2(beam_ref(top) - beam_ref(most));
-            }
+            if (sum > 0.0f) sum = beam_scaled(p.logs, sum, top, most);
             top = most;
         }
         if (top == INFINITY) {
 #pragma unroll
             for (int e = 0; e < E; ++e) sum += x.get(e) == INFINITY ? 1.0f : 0.0f;
-        } else if (beam_plain(top)) {
-            const float r = -ceilf(top * kLog2E);
-            const f2 ref = make_f2(r, r), big = make_f2(kLog2E, kLog2E), low = make_f2(kLog2ELow, kLog2ELow);
+        } else if (top > -INFINITY) {
+            const f2 minus = make_f2(-top, -top), by = make_f2(kLog2E, kLog2E);
             f2 s0 = make_f2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
-                const f2 u = make_f2(x.get(e), x.get(e + 1)), v = make_f2(x.get(e + 2), x.get(e + 3));
-                const f2 c = fma2(u, low, fma2(u, big, ref)), d = fma2(v, low, fma2(v, big, ref));
+                const f2 c = (make_f2(x.get(e), x.get(e + 1)) + minus) * by;
+                const f2 d = (make_f2(x.get(e + 2), x.get(e + 3)) + minus) * by;
                 s0 = s0 + make_f2(beam_ex2(f2_lo(c)), beam_ex2(f2_hi(c)));
                 s1 = s1 + make_f2(beam_ex2(f2_lo(d)), beam_ex2(f2_hi(d)));
             }
             s0 = s0 + s1;
             sum += f2_lo(s0) + f2_hi(s0);
-        } else if (top > -INFINITY) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) sum += beam_ex2((x.get(e) - top) * kLog2E);
         }
     });
     // the selection's threshold, from the largest of groups of threads; meanwhile the part's sum
@@ -573,7 +576,7 @@ __device__ __forceinline__ void beam_part(const BeamParams &p, BeamShared &s, in
     if (warp == kBeamThreads / 32 - 1) {
         float most = lane < kBeamThreads / 32 ? __uint_as_float(s.high[lane]) : -INFINITY;
         uint64_t all = lane < kBeamThreads / 32 ? s.sum[lane] : 0;
-        beam_total(most, all);
+        beam_total(p.logs, most, all);
         if (lane == 0) p.stats[row * p.parts + part] = BeamStat{most, 0, all};
     }
 }
@@ -606,17 +609,14 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, BeamShared &s, in
             uint4 u = make_uint4(0xFF800000u, 0, 0, 0);
             if (c0 + lane < p.parts) u = __ldcg(reinterpret_cast<const uint4 *>(st + c0 + lane));
             if (c0 == 0) top = __uint_as_float(u.x), sum = (uint64_t)u.w << 32 | u.z;
-            else beam_add(top, sum, __uint_as_float(u.x), (uint64_t)u.w << 32 | u.z);
+            else beam_add(p.logs, top, sum, __uint_as_float(u.x), (uint64_t)u.w << 32 | u.z);
         }
-        beam_total(top, sum);
+        beam_total(p.logs, top, sum);
         if (lane == 0) {
             const float score = p.scores_in[row0 + b];
             double add = -INFINITY;
-            if (sum > 0 && isfinite(score)) {
-                // ln of the sum relative to the largest logit
-                const double shift = beam_plain(top) ? beam_ref(top) - (double)top * 1.4426950408889634 : 0.0;
-                add = (double)score - (beam_log2(p.logs, sum) + (shift - kBeamFixed)) * 0.69314718055994530942;
-            }
+            if (sum > 0 && isfinite(score))
+                add = (double)score - (beam_log2(p.logs, sum) - kBeamFixed) * 0.69314718055994530942;
             s.join.top[b] = top;
             s.join.add[b] = add;
             s.join.add32[b] = (float)add;
