@@ -364,6 +364,7 @@ class KVCache:
         if stream is not None or _current_device() != self._index:
             with _on(self._index, stream):
                 return self.copy(copies, others)
+        others = tuple(others)  # looked at twice: a generator has them once
         for c in others:
             _need(c._index == self._index, "the caches must be on one device")
         _host.copy(self._address, self._index, others, copies, _current_stream(self._index))
