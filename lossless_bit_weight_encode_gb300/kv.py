@@ -44,8 +44,11 @@ def _grow(index, st, size):
 
 
 def _grow_shared(index, st, size):
-    """The same for calls with shared prefixes, which leave other things in theirs."""
-    return _grow_for((index, st, "shared"), index, size)
+    """The same for calls with shared prefixes, which leave other things in theirs.  Its size
+    goes with the tokens: at least twice the last one, so that the smaller ones that are kept
+    do not add up to more than it where a batch grows by degrees."""
+    last = _workspaces.get((index, st, "shared"))
+    return _grow_for((index, st, "shared"), index, size if last is None else max(size, 2 * last.numel()))
 
 
 def _grow_for(key, index, size):
@@ -379,7 +382,9 @@ class KVCache:
         first use) takes its place, as a captured graph needs that is replayed
         beside other calls.  With ``step.prefix`` (no window then) the keys that a
         group of requests shares are read once for all of them; such calls have a workspace of
-        their own."""
+        their own, of 2 * tokens * heads * (4 * head_dim + 24) bytes (8192 tokens of 48 heads of
+        128: 420 MB) and up to 80 MB more; it is kept for the stream and grows to twice its size
+        or more."""
         if stream is not None or _current_device() != self._index:
             with _on(self._index, stream):
                 return self.attend(q, step, scale, window, out, lse, workspace)
