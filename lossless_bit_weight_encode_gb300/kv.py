@@ -238,7 +238,7 @@ class KVPages:
             _ints(shares, _I32, "shares", self._index)
             _need(ring.numel() >= shares.numel() >= 1, "ring must have as many entries as shares or more")
         self.tables, self.owned, self.ring, self.ring_state = tables, owned, ring, ring_state
-        self.page_size, self.shares, self._ws = int(page_size), shares, None
+        self.page_size, self.shares, self._ws, self._outgrown = int(page_size), shares, None, []
 
     @classmethod
     def create(cls, num_pages, page_size, requests, max_blocks, device=None, shared=False):
@@ -298,6 +298,8 @@ class KVPages:
     def _grow(self, index, st, size):
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("make one ordinary fork() of these pages before capturing one")
+        if self._ws is not None:
+            self._outgrown.append(self._ws)  # a captured graph may still use it
         self._ws = torch.zeros(size, dtype=torch.uint8, device=self.tables.device)
         return self._ws
 

@@ -43,3 +43,11 @@ def test_workspaces_of_other_streams_and_calls_are_their_own():
     assert (a.numel(), b.numel(), c.numel()) == (1 << 20, 1 << 20, 5 << 20)
     assert kv._grow(0, 7, 6 << 20).numel() == 6 << 20  # one size on a device but for its counters
     assert kv._outgrown == [c]
+
+
+def test_forked_pages_keep_the_workspace_that_a_graph_may_use():
+    """Tables that were replaced by larger ones need a larger workspace."""
+    pages = types.SimpleNamespace(_ws=None, _outgrown=[], tables=types.SimpleNamespace(device="cuda:0"))
+    first = kv.KVPages._grow(pages, 0, 7, 1000)
+    second = kv.KVPages._grow(pages, 0, 7, 2000)
+    assert pages._ws is second and pages._outgrown == [first] and second.numel() == 2000
