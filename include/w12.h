@@ -598,13 +598,14 @@ int w12_kv_copy(const w12_kv_cache *caches, int32_t count, const int32_t *src, c
  * [requests]): the tokens that request b shares with its group, 0: none.  Within a group
  * the lens that are not 0 are the same (else a request that differs from the first has zeros
  * for results, and w12_check_status returns SHAPE), a multiple of
- * page_size (else rounded down) and at most args->lens[b] (else clamped, SHAPE); the leading
+ * page_size (else rounded down, SHAPE) and at most args->lens[b] (else clamped, SHAPE); the leading
  * lens / page_size table entries of those requests are the same too: the first one's are
  * read.  max_requests: the most requests of a group, as far as the caller knows; it picks
  * the row tile and any value is correct.  args as w12_kv_attend, window 0 (INVALID_ARG
  * otherwise; a layer with a window reads no long prefix).  Where the requests' keys and values
  * are together, shared ones counted for each, below some 150 MB, w12_kv_attend, which reads
- * them from L2, is the shorter call.
+ * them from L2, is the shorter call, and so it is from some ten new tokens per request on (an
+ * 8-bit cache: some thirty).
  * workspace: w12_kv_attend_shared_workspace_size bytes, 256-byte aligned, no initial
  * contents; not one that w12_kv_attend uses, whose counters have to stay zero.  Calls that
  * share one are ordered on the GPU; host threads may make them at the same time on one

@@ -24,10 +24,12 @@
 // same way, in 64 bits.
 //
 // What bounds it: few rows the chain load, maximum, sum, selection, join (4 beams of 151936
-// BF16 logits 9.8 us, where the bytes take 0.2); many rows the instructions, 15 per 32 logits
-// (128 rows 20.9 us, 1.9 TB/s, half of all issue slots; the bytes take 5.8).  35 rows of
-// 50257 fp32 logits under a mask 13.1 us: four CTAs per SM begin at once, and what follows
-// the loads is as long as they are.
+// BF16 logits 10.0 us, where the bytes take 0.2); many rows, next to that chain, 15 instructions
+// per 32 logits on SMs with uneven work (128 rows 21.1 us, 1.8 TB/s, 56 % of all issue slots:
+// the instructions alone are 7.5 us, the bytes 5.8; parts are a whole number per row, here
+// four of 4.6 tiles, so that an SM has three or four CTAs, up to 18.6 tiles where 15.6 are its
+// share).  35 rows of 50257 fp32 logits under a mask 13.2 us: four CTAs per SM begin at once,
+// and what follows the loads is as long as they are.
 #pragma once
 
 #include <cstdint>

@@ -131,7 +131,10 @@ struct KvSpanParams : KvSharedParams {
 // What a row block costs beside its tiles (its q, the pipeline's start and end), in tiles:
 // the line counts that many units more for each, so that CTAs with many short blocks have
 // fewer of them.  64 requests of 225 tokens behind a prompt of 4000: 2 units 39.6 us, 3 36.6,
-// 4 38.3, 6 41.2; twenty trees behind four prompts of 10000: 49.5, 48.5, 47.1, 46.3.
+// 4 38.3, 6 41.2; twenty trees behind four prompts of 10000: 49.5, 48.5, 47.1, 46.3.  A full
+// block of a prompt's own tokens costs much more, 12 us with five tiles that all need masks, and
+// these blocks stand together at the line's end: with hundreds of new tokens per request the
+// CTAs that get them take twice as long as the others.
 constexpr int32_t kKvBlockUnits = 3;
 
 // Two fp32 to packed BF16, round to nearest even, `lo` in the low half.

@@ -35,7 +35,9 @@ constexpr int kForkRows = 4096, kForkCols = 8;
 // Table entries that one CTA takes: 512 are 8.0 us in one launch and 10.6 in two, 2048 13.4 and
 // 12.3, 8192 24 and 12.
 constexpr int kForkOne = 1024;
-constexpr int kForkCtas = 152;  // with fewer columns per CTA than kForkCols: at most one per SM
+// With fewer columns per CTA than kForkCols: at most one per SM (a constant, for the workspace's
+// size is asked for without a device).
+constexpr int kForkCtas = 152;
 
 struct KvForkParams {
     const int32_t *parents, *lens;

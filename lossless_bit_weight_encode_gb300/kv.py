@@ -178,7 +178,9 @@ class KVPrefix:
     most requests of a group, as far as is known.
     ``KVPages.fork`` fills ``lens``; for a prompt that was put in every request's table
     the caller does.  (With less than some 150 MB of keys and values, shared ones counted
-    for each request, a step without a prefix is the shorter call.)"""
+    for each request, a step without a prefix is the shorter call, and so it is from some
+    ten new tokens per request on, with an 8-bit cache some thirty.)
+    A layer with a window takes a step without a prefix: a second KVStep of the same arrays."""
 
     def __init__(self, cu, lens, max_requests=1):
         _need(cu.is_cuda, "cu must be on a CUDA device")
