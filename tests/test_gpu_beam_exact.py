@@ -4,7 +4,7 @@ import math
 
 import pytest
 import torch
-from test_gpu_beam import DTYPES, draw, pack, scores_ref
+from test_gpu_beam import DTYPES, draw, pack
 
 from lossless_bit_weight_encode_gb300 import Beams, w12
 
