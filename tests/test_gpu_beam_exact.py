@@ -1,5 +1,5 @@
-"""What beam search's selection gives exactly: the score of a token that alone counts, rows
-whose logits differ by a constant, and the beams that go on from behind the candidates."""
+"""What beam search's selection gives exactly: the score of a token that alone counts, and equal
+scores for rows whose logits differ by a constant."""
 import math
 
 import pytest
